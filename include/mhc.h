@@ -52,7 +52,8 @@ typedef enum {
     MHC_ERR_UNSUPPORTED = 2,  /* n != 4, D not a multiple of the vector width, iters > MHC_MAX_ITERS */
     MHC_ERR_MISALIGNED = 3,   /* a pointer is not 16-byte aligned */
     MHC_ERR_CUDA = 4,         /* a CUDA runtime call or kernel launch failed */
-    MHC_ERR_TIMEOUT = 5       /* a bounded device-side wait gave up (see mhc_get_last_device_error) */
+    MHC_ERR_TIMEOUT = 5,      /* a bounded device-side wait gave up (see mhc_get_last_device_error) */
+    MHC_ERR_RANGE = 6         /* a position, slot, length or page number in device memory is outside its tensor */
 } mhc_status;
 
 typedef enum { MHC_F32 = 0, MHC_BF16 = 1 } mhc_dtype;
@@ -69,8 +70,9 @@ const char* mhc_version(void);
 
 /* Synchronises `stream`, then reads and clears the library's device error
  * word on the current device.  Returns MHC_OK if no kernel latched an error,
- * MHC_ERR_TIMEOUT if a bounded wait ran out, MHC_ERR_CUDA if the
- * synchronisation itself failed. */
+ * MHC_ERR_TIMEOUT if a bounded wait ran out, MHC_ERR_RANGE if a kernel of the
+ * attention sublayer met a number in device memory that points outside its
+ * tensor, MHC_ERR_CUDA if the synchronisation itself failed. */
 mhc_status mhc_get_last_device_error(cudaStream_t stream);
 
 /*
@@ -394,6 +396,150 @@ mhc_status mhc_layer_bwd_recompute(mhc_dtype dt, const void* g_in, const void* g
                                    int64_t D, int iters, float eps, void* dx, void* dy,
                                    float* dphi, float* db, float* dalpha, void* workspace,
                                    size_t ws_bytes, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The attention sublayer, between mhc_pre (which writes its input x_in) and
+ * mhc_post (which takes its output y): per-head normalisation of queries and
+ * keys with the position rotation, in training and in serving, and attention
+ * of new tokens over a paged key/value cache.
+ *
+ * Heads: Hq query heads and Hk key/value heads of Dh values, Hq a multiple of
+ * Hk; query head h belongs to key head h / (Hq/Hk).  Dh is a multiple of 8, at
+ * most 256.  A tensor of heads [T, H, Dh] is given with the distance between
+ * its tokens in elements (>= H*Dh), so that q, k and v may be parts of one
+ * packed projection; the heads of a token lie one after the other.  Pointers
+ * and distances of activations, caches, weights, angles and workspaces are
+ * multiples of 16 bytes, those of integers and of lse of their own size.
+ *
+ * Numbers that only the device sees (positions, slots, lengths, page numbers)
+ * are checked by the kernels.  One that points outside its tensor is latched
+ * (MHC_ERR_RANGE from mhc_get_last_device_error) and nothing outside the
+ * tensors is read or written.
+ * ------------------------------------------------------------------------- */
+
+/* flags of the rotation: pairs (j, j + rot/2) by default, or (2j, 2j + 1) */
+#define MHC_ROPE_ADJACENT 1
+
+/*
+ * mhc_qk_norm_rope -- for every head x of q (weight w = w_q) and k (w_k):
+ *   z = x w / sqrt(mean_Dh(x^2) + eps)                 (RMSNorm of the head)
+ *   y = z with its first `rot` values turned by the token's position p: each
+ *       pair (a, b) with angle index j becomes
+ *       (a cos[p, j] - b sin[p, j], b cos[p, j] + a sin[p, j])
+ *   Sums in float32; y is rounded to dt once.
+ *
+ *   q [T, Hq, Dh], k [T, Hk, Dh]  dt       q_stride, k_stride between tokens
+ *   w_q, w_k [Dh]        float
+ *   positions [T]        int32            rows of cos_sin (0 <= p < max_pos)
+ *   cos_sin [max_pos, rot] float          rot/2 cosines, then rot/2 sines
+ *   rot                  int              multiple of 16, 0 <= rot <= Dh; with
+ *                                         rot = 0 positions and cos_sin may be null
+ *   flags                int              0 or MHC_ROPE_ADJACENT
+ * outputs: q_out, k_out  dt               as q and k (may be the same memory
+ *                                         with the same stride)
+ * A token whose position is out of range gets zeros.  T = 0 is a no-op.
+ */
+mhc_status mhc_qk_norm_rope(mhc_dtype dt, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                            const float* w_q, const float* w_k, const int32_t* positions,
+                            const float* cos_sin, int64_t max_pos, int64_t T, int Hq, int Hk, int Dh,
+                            int rot, int flags, float eps, void* q_out, int64_t q_out_stride, void* k_out,
+                            int64_t k_out_stride, cudaStream_t stream);
+
+/*
+ * mhc_qk_norm_rope_bwd -- gradients of <g_q, q_out> + <g_k, k_out>:
+ * with h = the gradient turned back, r = 1/sqrt(mean(x^2) + eps), u = h w,
+ *   dx = r u - x r^3 <u, x> / Dh,      dw = sum over tokens and heads of h x r
+ * Nothing is saved by the forward: r is computed again from x.
+ *
+ *   g_q, g_k             dt               as q_out and k_out of the forward
+ *   the rest as passed to mhc_qk_norm_rope
+ * outputs (written): dq, dk dt as q and k; dw_q, dw_k [Dh] float (sums in a
+ *   fixed order, so results repeat bit for bit; zeros for T = 0)
+ *   workspace  device scratch of mhc_qk_norm_rope_bwd_workspace_bytes() bytes
+ * A token whose position is out of range gets zero gradients.
+ */
+mhc_status mhc_qk_norm_rope_bwd(mhc_dtype dt, const void* g_q, int64_t gq_stride, const void* g_k,
+                                int64_t gk_stride, const void* q, int64_t q_stride, const void* k,
+                                int64_t k_stride, const float* w_q, const float* w_k,
+                                const int32_t* positions, const float* cos_sin, int64_t max_pos, int64_t T,
+                                int Hq, int Hk, int Dh, int rot, int flags, float eps, void* dq,
+                                int64_t dq_stride, void* dk, int64_t dk_stride, float* dw_q, float* dw_k,
+                                void* workspace, size_t ws_bytes, cudaStream_t stream);
+size_t mhc_qk_norm_rope_bwd_workspace_bytes(int64_t T, int Dh);
+
+/*
+ * mhc_qk_norm_rope_append -- the serving form of mhc_qk_norm_rope: q_out as
+ * there; the normalised, turned keys and the values as they are go to the
+ * paged cache.  Token t goes to slot slots[t] = page * page_size + place in
+ * the page; -1 writes no key and no value (a padding token).  Two tokens of a
+ * call must not share a slot.
+ *
+ *   v [T, Hk, Dh]        dt               v_stride between tokens
+ *   slots [T]            int64
+ *   k_cache, v_cache     dt               element (page, place, head, d) at
+ *     page*page_stride + place*slot_stride + head*head_stride + d: both
+ *     [pages, page_size, Hk, Dh] and [pages, Hk, page_size, Dh] are covered
+ */
+mhc_status mhc_qk_norm_rope_append(mhc_dtype dt, const void* q, int64_t q_stride, const void* k,
+                                   int64_t k_stride, const void* v, int64_t v_stride, const float* w_q,
+                                   const float* w_k, const int32_t* positions, const float* cos_sin,
+                                   int64_t max_pos, const int64_t* slots, int64_t T, int Hq, int Hk, int Dh,
+                                   int rot, int flags, float eps, void* q_out, int64_t q_out_stride,
+                                   void* k_cache, int64_t k_page_stride, int64_t k_slot_stride,
+                                   int64_t k_head_stride, void* v_cache, int64_t v_page_stride,
+                                   int64_t v_slot_stride, int64_t v_head_stride, int64_t num_pages,
+                                   int page_size, cudaStream_t stream);
+
+/*
+ * mhc_paged_attn -- causal attention of new tokens over a paged cache that
+ * holds their keys and values already.  Sequence b of B has the rows
+ * cu_q[b] .. cu_q[b+1] of q (its newest tokens, n of them; one in decoding, a
+ * chunk of a prompt otherwise) and kv_lens[b] = m cached tokens, the n new ones
+ * last.  Token j of the sequence is at place j % page_size of page
+ * page_table[b, j / page_size].  For query i of the n, with scores
+ *   z_ij = scale <q_i, k_j>,   z <- softcap tanh(z / softcap) if softcap > 0,
+ * over the keys 0 <= j <= m - n + i, and, if window > 0, j > m - n + i - window:
+ *   o_i = sum_j exp(z_ij) v_j / sum_j exp(z_ij),   lse_i = log sum_j exp(z_ij).
+ * A row that sees no key (m < n) gets o = 0 and lse = -inf.  Sums and softmax
+ * statistics are float32; on the tensor cores the exponentials of a block are
+ * rounded to bf16 for their product with the values (relative 2^-9 each).
+ *
+ *   q [T, Hq, Dh]        dt               q_stride between tokens
+ *   k_cache, v_cache     dt               as in mhc_qk_norm_rope_append
+ *   page_table [B, *]    int32            table_stride between rows, at least
+ *                                         ceil(max_kv / page_size); entries of
+ *                                         pages that no query of the sequence
+ *                                         sees are not used
+ *   cu_q [B+1], kv_lens [B] int32         or both null: the workspace holds
+ *                                         the plan of mhc_paged_attn_plan
+ *   max_q, max_kv                         no sequence has more new or cached tokens
+ *   scale > 0, softcap >= 0 (0: off), window >= 0 (0: unlimited)
+ * outputs: o [T, Hq, Dh] dt; lse [T, Hq] float (null: not wanted).  Rows of q
+ *   that belong to no sequence are left as they are, and so are the rows of a
+ *   sequence whose numbers do not fit the call (MHC_ERR_RANGE).
+ *   workspace  device scratch of mhc_paged_attn_workspace_bytes() bytes; calls
+ *              that may overlap need one each
+ * What the pages hold beyond the cached tokens, or outside what a tile of rows
+ * can see, is never used (it may be NaN).  Values that some row of a call sees
+ * must be finite for every row's result to be.
+ *
+ * mhc_paged_attn_plan -- splits the batch over the GPU (one small kernel) into
+ * `workspace`, for any number of mhc_paged_attn calls with the same sizes: the
+ * layers of one step.  It depends on cu_q, kv_lens, window and the sizes only.
+ */
+mhc_status mhc_paged_attn_plan(mhc_dtype dt, const int32_t* cu_q, const int32_t* kv_lens, int64_t T, int B,
+                               int Hq, int Hk, int Dh, int page_size, int64_t max_q, int64_t max_kv,
+                               int window, void* workspace, size_t ws_bytes, cudaStream_t stream);
+mhc_status mhc_paged_attn(mhc_dtype dt, const void* q, int64_t q_stride, const void* k_cache,
+                          int64_t k_page_stride, int64_t k_slot_stride, int64_t k_head_stride,
+                          const void* v_cache, int64_t v_page_stride, int64_t v_slot_stride,
+                          int64_t v_head_stride, int64_t num_pages, int page_size,
+                          const int32_t* page_table, int64_t table_stride, const int32_t* cu_q,
+                          const int32_t* kv_lens, int64_t T, int B, int Hq, int Hk, int Dh, int64_t max_q,
+                          int64_t max_kv, int window, float scale, float softcap, void* o, float* lse,
+                          void* workspace, size_t ws_bytes, cudaStream_t stream);
+size_t mhc_paged_attn_workspace_bytes(mhc_dtype dt, int64_t T, int B, int Hq, int Hk, int Dh, int page_size,
+                                      int64_t max_q);
 
 #ifdef __cplusplus
 }

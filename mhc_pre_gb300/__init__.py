@@ -8,12 +8,19 @@ first use, so importing the package never needs a GPU.
 
 from .binding import (  # noqa: F401
     MhcError,
+    mhc_paged_attn,
+    mhc_paged_attn_plan,
     mhc_post,
     mhc_post_bwd,
     mhc_pre,
     mhc_pre_bwd,
+    mhc_qk_norm_rope,
+    mhc_qk_norm_rope_append,
+    mhc_qk_norm_rope_bwd,
     pre_bwd_workspace_bytes,
 )
 
 __all__ = ["mhc_pre", "mhc_post", "mhc_post_bwd", "mhc_pre_bwd",
+           "mhc_qk_norm_rope", "mhc_qk_norm_rope_bwd", "mhc_qk_norm_rope_append",
+           "mhc_paged_attn", "mhc_paged_attn_plan",
            "pre_bwd_workspace_bytes", "MhcError"]

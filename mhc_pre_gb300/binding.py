@@ -21,6 +21,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)),
 
 MHC_OK, MHC_ERR_INVALID_ARG, MHC_ERR_UNSUPPORTED = 0, 1, 2
 MHC_ERR_MISALIGNED, MHC_ERR_CUDA, MHC_ERR_TIMEOUT = 3, 4, 5
+MHC_ERR_RANGE = 6
 MHC_F32, MHC_BF16 = 0, 1
 MAX_ITERS = 64
 
@@ -31,7 +32,10 @@ EXPORTS = ("mhc_status_string", "mhc_version", "mhc_get_last_device_error",
            "mhc_pre_bwd_workspace_bytes", "mhc_pre_bwd", "mhc_pre_bwd_noalloc",
            "mhc_pre_gates", "mhc_layer_bwd_recompute_workspace_bytes",
            "mhc_layer_bwd_recompute", "mhc_test_force_timeout", "mhc_pre_critical",
-           "mhc_post_res_gates")
+           "mhc_post_res_gates",
+           "mhc_qk_norm_rope", "mhc_qk_norm_rope_bwd", "mhc_qk_norm_rope_bwd_workspace_bytes",
+           "mhc_qk_norm_rope_append", "mhc_paged_attn_plan", "mhc_paged_attn",
+           "mhc_paged_attn_workspace_bytes")
 
 PreOut = namedtuple("PreOut", "x_in H_pre H_post H_res proj inv_rms")
 PostPreOut = namedtuple("PostPreOut", "x_next x_in H_pre H_post H_res proj inv_rms")
@@ -43,6 +47,11 @@ PreGatesOut = namedtuple("PreGatesOut", "H_pre H_post H_res proj inv_rms")
 PreCriticalOut = namedtuple("PreCriticalOut", "x_in H_pre proj inv_rms")
 PostResGatesOut = namedtuple("PostResGatesOut", "H_post H_res")
 LayerBwdOut = namedtuple("LayerBwdOut", "dx dy dphi db dalpha")
+QKOut = namedtuple("QKOut", "q k")
+QKBwdOut = namedtuple("QKBwdOut", "dq dk dw_q dw_k")
+PagedAttnOut = namedtuple("PagedAttnOut", "o lse")
+PagedAttnPlan = namedtuple("PagedAttnPlan", "workspace sizes")
+ROPE_ADJACENT = 1
 
 _P, _I64, _I, _F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
 _SIGS = {
@@ -74,6 +83,21 @@ _SIGS = {
     "mhc_post_res_gates": ([_P, _P, _P, _I64, _I, _I, _P, _P, _P], _I),
     "mhc_layer_bwd_recompute": ([_I, _P, _P, _P, _P, _P, _P, _P, _I64, _I, _I64, _I, _F,
                                  _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P], _I),
+    "mhc_qk_norm_rope": ([_I, _P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _I64, _I, _I, _I, _I, _I, _F,
+                          _P, _I64, _P, _I64, _P], _I),
+    "mhc_qk_norm_rope_bwd": ([_I, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _I64,
+                              _I, _I, _I, _I, _I, _F, _P, _I64, _P, _I64, _P, _P, _P, ctypes.c_size_t,
+                              _P], _I),
+    "mhc_qk_norm_rope_bwd_workspace_bytes": ([_I64, _I], ctypes.c_size_t),
+    "mhc_qk_norm_rope_append": ([_I, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _P, _I64,
+                                 _I, _I, _I, _I, _I, _F, _P, _I64, _P, _I64, _I64, _I64,
+                                 _P, _I64, _I64, _I64, _I64, _I, _P], _I),
+    "mhc_paged_attn_plan": ([_I, _P, _P, _I64, _I, _I, _I, _I, _I, _I64, _I64, _I, _P,
+                             ctypes.c_size_t, _P], _I),
+    "mhc_paged_attn": ([_I, _P, _I64, _P, _I64, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I,
+                        _P, _I64, _P, _P, _I64, _I, _I, _I, _I, _I64, _I64, _I, _F, _F, _P, _P,
+                        _P, ctypes.c_size_t, _P], _I),
+    "mhc_paged_attn_workspace_bytes": ([_I, _I64, _I, _I, _I, _I, _I, _I64], ctypes.c_size_t),
 }
 
 _lib = None
@@ -381,6 +405,204 @@ def mhc_pre_bwd_noalloc(g_in, dH_post, dH_res, x, phi, b, alpha, proj, inv_rms,
         _ptr(dphi), _ptr(db), _ptr(dalpha), _stream(x.device))
     _check(st, "mhc_pre_bwd_noalloc")
     return PreBwdOut(dx, dphi, db, dalpha)
+
+
+# ------------------------------------------------------ attention sublayer
+
+def _heads(t: torch.Tensor, name: str, like=None):
+    """Address and token distance of a tensor of heads [T, H, Dh]; the tokens
+    may be apart (a part of a packed projection), a token's heads are not."""
+    if like is not None and t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError("the mHC library takes CUDA tensors only")
+    T, H, Dh = t.shape
+    st, sh, sd = t.stride()
+    if (Dh > 1 and sd != 1) or (H > 1 and sh != Dh):
+        raise ValueError(f"{name}: the heads of a token must lie one after the other")
+    return t.data_ptr(), st if T > 1 else H * Dh
+
+
+def _ints(t: torch.Tensor, name: str, dtype, n=None):
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{name} must have {n} entries, got {t.numel()}")
+    return _ptr(t)
+
+
+def _rope(w_q, w_k, positions, cos_sin, T, Dh, interleaved):
+    """The arguments w_q, w_k, positions, cos_sin, max_pos and rot, flags."""
+    for w, name in ((w_q, "w_q"), (w_k, "w_k")):
+        if _f32(w, name).numel() != Dh:
+            raise ValueError(f"{name} must have {Dh} entries, got {w.numel()}")
+    if cos_sin is None:
+        return (_ptr(w_q), _ptr(w_k), None, None, 0), 0, 0
+    max_pos, rot = _f32(cos_sin, "cos_sin").shape
+    return ((_ptr(w_q), _ptr(w_k), _ints(positions, "positions", torch.int32, T), _ptr(cos_sin), max_pos),
+            rot, ROPE_ADJACENT if interleaved else 0)
+
+
+def _cache(t: torch.Tensor, name: str, like, Hk: int, Dh: int):
+    """Address and (page, slot, head) distances of a cache [pages, page_size, Hk, Dh]
+    in any memory order that keeps a head's values together."""
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError("the mHC library takes CUDA tensors only")
+    P, ps, H, D = t.shape
+    if H != Hk or D != Dh:
+        raise ValueError(f"{name} must be [pages, page_size, {Hk}, {Dh}], got {tuple(t.shape)}")
+    sp, ss, sh, sd = t.stride()
+    if D > 1 and sd != 1:
+        raise ValueError(f"{name}: the values of a head must lie one after the other")
+    return (t.data_ptr(), sp if P > 1 else ps * Hk * Dh, ss if ps > 1 else Hk * Dh, sh if Hk > 1 else Dh)
+
+
+def mhc_qk_norm_rope(q, k, w_q, w_k, positions=None, cos_sin=None, eps: float = 1e-6,
+                     interleaved: bool = False):
+    """Per-head RMSNorm of q [T, Hq, Dh] and k [T, Hk, Dh], then the rotation of
+    the first cos_sin.shape[1] values of each head by cos_sin[positions]
+    (cosines, then sines).  ``interleaved``: pairs (2j, 2j + 1)."""
+    T, Hq, Dh = q.shape
+    if k.shape[0] != T or k.shape[2] != Dh:
+        raise ValueError("q and k must have the same tokens and head size")
+    Hk = k.shape[1]
+    rope, rot, flags = _rope(w_q, w_k, positions, cos_sin, T, Dh, interleaved)
+    out = QKOut(_empty((T, Hq, Dh), dtype=q.dtype, device=q.device),
+                _empty((T, Hk, Dh), dtype=q.dtype, device=q.device))
+    st = lib().mhc_qk_norm_rope(_dtype_code(q), *_heads(q, "q"), *_heads(k, "k", q), *rope, T, Hq, Hk, Dh,
+                                rot, flags, eps, out.q.data_ptr(), Hq * Dh, out.k.data_ptr(), Hk * Dh,
+                                _stream(q.device))
+    _check(st, "mhc_qk_norm_rope")
+    return out
+
+
+def mhc_qk_norm_rope_bwd(g_q, g_k, q, k, w_q, w_k, positions=None, cos_sin=None, eps: float = 1e-6,
+                         interleaved: bool = False, dq=None, dk=None):
+    """Gradients of <g_q, q_out> + <g_k, k_out> for mhc_qk_norm_rope.  ``dq`` and
+    ``dk`` (parts of a packed gradient, say) are written when given."""
+    T, Hq, Dh = q.shape
+    if k.shape[0] != T or k.shape[2] != Dh or g_q.shape != q.shape or g_k.shape != k.shape:
+        raise ValueError("q, k and their gradients must have the same shapes")
+    Hk = k.shape[1]
+    rope, rot, flags = _rope(w_q, w_k, positions, cos_sin, T, Dh, interleaved)
+    if dq is None:
+        dq = _empty((T, Hq, Dh), dtype=q.dtype, device=q.device)
+    if dk is None:
+        dk = _empty((T, Hk, Dh), dtype=q.dtype, device=q.device)
+    if dq.shape != q.shape or dk.shape != k.shape:
+        raise ValueError("dq and dk must have the shapes of q and k")
+    dw_q = _empty((Dh,), dtype=torch.float32, device=q.device)
+    dw_k = _empty((Dh,), dtype=torch.float32, device=q.device)
+    need = int(lib().mhc_qk_norm_rope_bwd_workspace_bytes(T, Dh))
+    ws = _empty((max(need, 16),), dtype=torch.uint8, device=q.device)
+    st = lib().mhc_qk_norm_rope_bwd(_dtype_code(q), *_heads(g_q, "g_q", q), *_heads(g_k, "g_k", q),
+                                    *_heads(q, "q"), *_heads(k, "k", q), *rope, T, Hq, Hk, Dh, rot, flags,
+                                    eps, *_heads(dq, "dq", q), *_heads(dk, "dk", q), dw_q.data_ptr(),
+                                    dw_k.data_ptr(), ws.data_ptr(), need, _stream(q.device))
+    _check(st, "mhc_qk_norm_rope_bwd")
+    return QKBwdOut(dq, dk, dw_q, dw_k)
+
+
+def mhc_qk_norm_rope_append(q, k, v, w_q, w_k, k_cache, v_cache, slots, positions=None, cos_sin=None,
+                            eps: float = 1e-6, interleaved: bool = False):
+    """The serving form: returns the normalised, rotated q; the keys (likewise)
+    and the values go to slots[t] = page * page_size + place of the caches
+    [pages, page_size, Hk, Dh] (-1: nowhere), in place."""
+    T, Hq, Dh = q.shape
+    if k.shape[0] != T or k.shape[2] != Dh or v.shape != k.shape:
+        raise ValueError("q, k and v must have the same tokens and head size")
+    Hk = k.shape[1]
+    if k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same shape")
+    rope, rot, flags = _rope(w_q, w_k, positions, cos_sin, T, Dh, interleaved)
+    out = _empty((T, Hq, Dh), dtype=q.dtype, device=q.device)
+    st = lib().mhc_qk_norm_rope_append(
+        _dtype_code(q), *_heads(q, "q"), *_heads(k, "k", q), *_heads(v, "v", q), *rope,
+        _ints(slots, "slots", torch.int64, T), T, Hq, Hk, Dh, rot, flags, eps, out.data_ptr(), Hq * Dh,
+        *_cache(k_cache, "k_cache", q, Hk, Dh), *_cache(v_cache, "v_cache", q, Hk, Dh),
+        k_cache.shape[0], k_cache.shape[1], _stream(q.device))
+    _check(st, "mhc_qk_norm_rope_append")
+    return out
+
+
+def _attn_sizes(dtype, T, Hq, Hk, Dh, page_size, B, max_q, max_kv, window):
+    return (MHC_BF16 if dtype == torch.bfloat16 else MHC_F32, T, B, Hq, Hk, Dh, page_size, max_q, max_kv, window)
+
+
+def _attn_workspace(sizes, device):
+    code, T, B, Hq, Hk, Dh, page_size, max_q = sizes[:8]
+    need = int(lib().mhc_paged_attn_workspace_bytes(code, T, B, Hq, Hk, Dh, page_size, max_q))
+    return _empty((max(need, 16),), dtype=torch.uint8, device=device)
+
+
+def mhc_paged_attn_plan(cu_q, kv_lens, dtype, T: int, Hq: int, Hk: int, Dh: int, page_size: int,
+                        max_q: int, max_kv: int, window: int = 0):
+    """Splits a batch over the GPU once, for every mhc_paged_attn call of the
+    same sizes (the layers of one step).  Calls that share a plan share its
+    workspace: they must not overlap."""
+    B = kv_lens.numel()
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"activations must be bfloat16 or float32, got {dtype}")
+    sizes = _attn_sizes(dtype, T, Hq, Hk, Dh, page_size, B, max_q, max_kv, window)
+    ws = _attn_workspace(sizes, cu_q.device)
+    st = lib().mhc_paged_attn_plan(sizes[0], _ints(cu_q, "cu_q", torch.int32, B + 1),
+                                   _ints(kv_lens, "kv_lens", torch.int32), *sizes[1:], ws.data_ptr(),
+                                   ws.numel(), _stream(cu_q.device))
+    _check(st, "mhc_paged_attn_plan")
+    return PagedAttnPlan(ws, sizes)
+
+
+def mhc_paged_attn(q, k_cache, v_cache, page_table, cu_q=None, kv_lens=None, max_q: int = None,
+                   max_kv: int = None, scale: float = None, window: int = None, softcap: float = 0.0,
+                   plan=None, out=None):
+    """Causal attention of the new tokens q [T, Hq, Dh] over a paged cache
+    [pages, page_size, Hk, Dh]: sequence b has the rows cu_q[b]:cu_q[b+1] and
+    kv_lens[b] cached tokens, the new ones last.  ``max_q`` and ``max_kv`` bound
+    the new and the cached tokens of a sequence (default: all rows of q, the
+    page table's width); ``window`` 0 or None: unlimited.  ``plan`` (from
+    mhc_paged_attn_plan) takes the place of cu_q and kv_lens and brings its own
+    max_q, max_kv and window.  ``out``: a tensor for o; rows of no sequence stay as they
+    are.  Returns o and lse [T, Hq]."""
+    T, Hq, Dh = q.shape
+    P, page_size, Hk, _ = k_cache.shape
+    if k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same shape")
+    B, width = page_table.shape
+    if plan is None:
+        sizes = _attn_sizes(q.dtype, T, Hq, Hk, Dh, page_size, B, T if max_q is None else max_q,
+                            width * page_size if max_kv is None else max_kv, window or 0)
+        ws = _attn_workspace(sizes, q.device)
+        lens = (_ints(cu_q, "cu_q", torch.int32, B + 1), _ints(kv_lens, "kv_lens", torch.int32, B))
+    else:
+        ws, sizes = plan
+        lens = (None, None)
+        want = _attn_sizes(q.dtype, T, Hq, Hk, Dh, page_size, B,
+                           *(a if b is None else b for a, b in zip(sizes[7:], (max_q, max_kv, window))))
+        if want != sizes or cu_q is not None or kv_lens is not None:
+            raise ValueError(f"the plan has its own lengths and sizes: {sizes}, not {want}")
+    if page_table.dtype != torch.int32:
+        raise TypeError(f"page_table must be {torch.int32}, got {page_table.dtype}")
+    if not page_table.is_cuda:
+        raise ValueError("the mHC library takes CUDA tensors only")
+    if width * page_size < sizes[8]:
+        raise ValueError(f"page_table holds {width * page_size} tokens a sequence, max_kv is {sizes[8]}")
+    if width > 1 and page_table.stride(1) != 1:
+        raise ValueError("page_table: the pages of a sequence must lie one after the other")
+    if out is None:
+        out = _empty((T, Hq, Dh), dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must have the shape and type of q")
+    lse = _empty((T, Hq), dtype=torch.float32, device=q.device)
+    st = lib().mhc_paged_attn(
+        _dtype_code(q), *_heads(q, "q"), *_cache(k_cache, "k_cache", q, Hk, Dh),
+        *_cache(v_cache, "v_cache", q, Hk, Dh), P, page_size, page_table.data_ptr(),
+        page_table.stride(0) if B > 1 else width, *lens, T, B, Hq, Hk, Dh, sizes[7], sizes[8], sizes[9],
+        Dh ** -0.5 if scale is None else scale, softcap, _ptr(out), lse.data_ptr(), ws.data_ptr(), ws.numel(),
+        _stream(q.device))
+    _check(st, "mhc_paged_attn")
+    return PagedAttnOut(out, lse)
 
 
 def get_last_device_error(device=None) -> int:

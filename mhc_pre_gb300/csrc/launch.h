@@ -99,4 +99,53 @@ cudaError_t launch_pre_bwd_tc_main(const void* g_in, const void* x, const float*
                                    int64_t T, int64_t D, int64_t nb, void* dx, float* part,
                                    cudaStream_t s);
 
+// ---------------------------------------------------------------------------
+// The attention sublayer between mhc_pre and mhc_post (qk_norm_rope.cu,
+// paged_attn.cu, paged_attn_tc.cu).
+// ---------------------------------------------------------------------------
+
+// Per-head RMSNorm and rotation.  Strides are in elements; `v`, `slots` and
+// the cache strides belong to the form that writes the paged cache (k_out and
+// v_out are the caches then).
+struct QkParams {
+    const void *q, *k, *v;
+    const float *w_q, *w_k;
+    const int32_t* positions;
+    const float* cos_sin;       // [max_pos, rot]: cosines, then sines
+    const int64_t* slots;
+    int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
+    int64_t k_page_stride, k_slot_stride, k_head_stride;
+    int64_t v_page_stride, v_slot_stride, v_head_stride;
+    int64_t num_slots, T;
+    int page_size, Hq, Hk, Dh, rot, max_pos;
+    float eps;
+    void *q_out, *k_out, *v_out;
+};
+struct QkBwdParams {
+    const void *g_q, *g_k, *q, *k;
+    const float *w_q, *w_k;
+    const int32_t* positions;
+    const float* cos_sin;
+    int64_t gq_stride, gk_stride, q_stride, k_stride, dq_stride, dk_stride, T;
+    int Hq, Hk, Dh, rot, max_pos;
+    float eps;
+    void *dq, *dk;
+    float* partial;             // [qk_bwd_blocks(T)][2][Dh]
+};
+int64_t qk_bwd_blocks(int64_t T);
+cudaError_t launch_qk_norm_rope(bool bf16, bool adjacent, bool append, const QkParams& p, cudaStream_t s);
+cudaError_t launch_qk_norm_rope_bwd(bool bf16, bool adjacent, const QkBwdParams& p, float* dw_q, float* dw_k,
+                                    cudaStream_t s);
+
+struct AttnPlan;
+struct AttnParams;
+AttnPlan attn_plan_sizes(bool bf16, int64_t T, int B, int Hq, int Hk, int Dh, int page_size, int64_t max_q);
+cudaError_t launch_attn_plan(const AttnPlan& plan, const int32_t* cu_q, const int32_t* kv_lens, int64_t T, int B,
+                             int Hq, int Hk, int window, int64_t max_q, int64_t max_kv, void* ws, cudaStream_t s);
+cudaError_t launch_paged_attn(bool bf16, const AttnParams& p, cudaStream_t s);
+
+// Device error words of these kernels, read and cleared.
+cudaError_t read_and_clear_qk_error(unsigned* word);
+cudaError_t read_and_clear_attn_error(unsigned* word);
+
 }  // namespace mhc

@@ -92,6 +92,7 @@ const char* mhc_status_string(mhc_status s) {
         case MHC_ERR_MISALIGNED: return "MHC_ERR_MISALIGNED: a pointer is not 16-byte aligned";
         case MHC_ERR_CUDA: return "MHC_ERR_CUDA: a CUDA call or kernel launch failed";
         case MHC_ERR_TIMEOUT: return "MHC_ERR_TIMEOUT: a bounded device-side wait gave up";
+        case MHC_ERR_RANGE: return "MHC_ERR_RANGE: a position, slot, length or page number is outside its tensor";
     }
     return "MHC_ERR_UNKNOWN";
 }
@@ -101,7 +102,9 @@ const char* mhc_version(void) { return "mhc_gb300 0.1.0 sm_103a"; }
 mhc_status mhc_get_last_device_error(cudaStream_t stream) {
     unsigned word = 0;
     if (mhc::read_and_clear_device_error(&word, stream) != cudaSuccess) return MHC_ERR_CUDA;
-    return word == 0 ? MHC_OK : MHC_ERR_TIMEOUT;
+    // bit 0: a wait ran out; bit 1: a number outside its tensor
+    if (word & 1u) return MHC_ERR_TIMEOUT;
+    return word == 0 ? MHC_OK : MHC_ERR_RANGE;
 }
 
 mhc_status mhc_test_force_timeout(int on) {

@@ -1,0 +1,510 @@
+// paged_attn.cu -- attention of a chunk of new tokens over a paged cache: the
+// plan kernel, the CUDA-core kernel, and the choice of kernel.
+//
+//   z[i, j] = scale <q_i, k_j>,  z = softcap tanh(z / softcap) when capped,
+//   keys j <= kvlen - qlen + i, and j > kvlen - qlen + i - window,
+//   o_i = sum_j exp(z_ij - lse_i) v_j,  lse_i = log sum_j exp(z_ij);
+// a row that sees no key gives o = 0 and lse = -inf.
+//
+// bf16 heads of at most 128 over pages that divide (or are a multiple of) 128
+// keys run on the tensor cores (paged_attn_tc.cu).  Everything else (float32,
+// wider heads, other page sizes) runs in attn_cc_kernel below, which keeps a
+// tile's scores and sums in registers and walks the keys once.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "launch.h"
+#include "paged_attn.cuh"
+#include "tc_ptx.cuh"
+
+namespace mhc {
+
+__device__ unsigned g_attn_error;   // ATTN_ERR_* bits
+
+cudaError_t read_and_clear_attn_error(unsigned* word) {
+    cudaError_t e = cudaMemcpyFromSymbol(word, g_attn_error, sizeof(unsigned));
+    if (e != cudaSuccess) return e;
+    const unsigned zero = 0;
+    return cudaMemcpyToSymbol(g_attn_error, &zero, sizeof(unsigned));
+}
+
+namespace attn {
+
+constexpr int PLAN_THREADS = 512;
+constexpr int PLAN_TILES = 4096;    // tile starts kept in shared memory for the CTAs' search
+
+struct PlanParams {
+    const int32_t *cu_q, *kv_lens;
+    unsigned char* ws;
+    int64_t T;
+    int64_t max_kv;
+    int B, Hq, Hk, G, window, max_q;
+    AttnPlan plan;
+};
+
+// Exclusive sum over the block; `total` is the block's sum.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t& total) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    int64_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sums[w] = x;
+    __syncthreads();
+    int64_t before = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < PLAN_THREADS / 32; ++i) {
+        const int64_t s = warp_sums[i];
+        if (i < w) before += s;
+        all += s;
+    }
+    total = all;
+    return before + x - v;
+}
+
+// One block: tiles of every sequence, their first units, and each CTA's start.
+__global__ void __launch_bounds__(PLAN_THREADS)
+attn_plan_kernel(const PlanParams p) {
+    __shared__ int64_t sums[PLAN_THREADS / 32];
+    __shared__ int tile_base[PLAN_THREADS + 1];
+    __shared__ int s_q0[PLAN_THREADS], s_qlen[PLAN_THREADS], s_kvlen[PLAN_THREADS];
+    __shared__ int64_t s_start[PLAN_TILES];
+    ptx::griddep_launch_dependents();
+    const int tid = threadIdx.x;
+    AttnTile* tiles = reinterpret_cast<AttnTile*>(p.ws + p.plan.tile_off);
+    int* counts = reinterpret_cast<int*>(p.ws + p.plan.count_off);
+    const int TR = p.plan.tile_rows, BN = p.plan.block_keys;
+    int64_t units = 0;
+    int ntiles = 0;
+    for (int b0 = 0; b0 < p.B; b0 += PLAN_THREADS) {
+        const int b = b0 + tid;
+        int q0 = 0, qlen = 0, kvlen = 0;
+        if (b < p.B) {
+            q0 = p.cu_q[b];
+            qlen = p.cu_q[b + 1] - q0;
+            kvlen = p.kv_lens[b];
+            // a sequence whose numbers do not fit the call is left out
+            if (q0 < 0 || qlen < 0 || qlen > p.max_q || q0 + static_cast<int64_t>(qlen) > p.T || kvlen < 0 ||
+                kvlen > p.max_kv) {
+                atomicOr(&g_attn_error, ATTN_ERR_RANGE);
+                qlen = 0;
+                kvlen = 0;
+            }
+        }
+        const int nt = (qlen * p.G + TR - 1) / TR;
+        int64_t all = 0;
+        const int64_t base = block_scan(nt, sums, all);
+        tile_base[tid] = static_cast<int>(base);
+        if (tid == 0) tile_base[PLAN_THREADS] = static_cast<int>(all);
+        s_q0[tid] = q0;
+        s_qlen[tid] = qlen;
+        s_kvlen[tid] = kvlen;
+        __syncthreads();
+        for (int t0 = 0; t0 < all; t0 += PLAN_THREADS) {
+            const int i = t0 + tid;
+            const bool on = i < all && ntiles + i < p.plan.max_tiles;
+            if (i < all && !on) atomicOr(&g_attn_error, ATTN_ERR_RANGE);
+            AttnTile t = {};
+            if (on) {
+                // the sequence of tile i: the last one whose base is at most i
+                int lo = 0, hi = PLAN_THREADS - 1;
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (tile_base[mid] <= i) lo = mid;
+                    else hi = mid - 1;
+                }
+                t.seq = b0 + lo;
+                t.q0 = s_q0[lo];
+                t.qlen = s_qlen[lo];
+                t.kvlen = s_kvlen[lo];
+                t.row0 = (i - tile_base[lo]) * TR;
+                const int last = min(t.row0 + TR, t.qlen * p.G) - 1;
+                int lo_k, hi_k, unused;
+                attn_row_keys(t, t.row0, p.G, p.window, lo_k, unused);
+                attn_row_keys(t, last, p.G, p.window, unused, hi_k);
+                // rows that see nothing still get their zeros written: one masked block
+                t.blk0 = hi_k > lo_k ? lo_k / BN : 0;
+                t.nblk = hi_k > lo_k ? (hi_k + BN - 1) / BN - t.blk0 : 1;
+                t.cnt = (ntiles + i) * p.Hk;
+            }
+            int64_t sum = 0;
+            t.start = units + block_scan(static_cast<int64_t>(t.nblk) * p.Hk, sums, sum);
+            units += sum;
+            if (on) {
+                tiles[ntiles + i] = t;
+                if (ntiles + i < PLAN_TILES) s_start[ntiles + i] = t.start;
+                for (int h = 0; h < p.Hk; ++h) counts[t.cnt + h] = 0;
+            }
+        }
+        ntiles = static_cast<int>(min(static_cast<int64_t>(ntiles) + all, p.plan.max_tiles));
+        __syncthreads();
+    }
+    int64_t per = (units + p.plan.ncta - 1) / p.plan.ncta;
+    if (per < 1) per = 1;
+    if (tid == 0) {
+        AttnHead* h = reinterpret_cast<AttnHead*>(p.ws);
+        h->units = units;
+        h->per_cta = per;
+        h->T = p.T;
+        h->ntiles = ntiles;
+        h->ncta = p.plan.ncta;
+        h->Hq = p.Hq;
+        h->Hk = p.Hk;
+        h->B = p.B;
+        h->tile_rows = TR;
+        h->block_keys = BN;
+        h->window = p.window;
+    }
+    AttnStart* starts = reinterpret_cast<AttnStart*>(p.ws + p.plan.start_off);
+    for (int c = tid; c < p.plan.ncta; c += PLAN_THREADS) {
+        const int64_t u = c * per;
+        AttnStart s = {0, 0, 0, 0};
+        if (u < units) {
+            int lo = 0, hi = ntiles - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                const int64_t st = mid < PLAN_TILES ? s_start[mid] : tiles[mid].start;
+                if (st <= u) lo = mid;
+                else hi = mid - 1;
+            }
+            const int nblk = tiles[lo].nblk;
+            const int64_t in = u - (lo < PLAN_TILES ? s_start[lo] : tiles[lo].start);
+            s.tile = lo;
+            s.head = static_cast<int>(in / nblk);
+            s.blk = static_cast<int>(in - static_cast<int64_t>(s.head) * nblk);
+        }
+        starts[c] = s;
+    }
+}
+
+// ------------------------------------------------------------ CUDA cores ---
+//
+// 256 threads as 16 x 16: thread (ty, tx) has rows ty*RPT .. +RPT of the tile
+// and keys tx, tx + 16, ... of a block for the scores, and the columns
+// 4 tx + 64 c of the values for the sums.  Queries, keys, values and
+// exponentials are float32 in shared memory; a row's maximum and sum live in
+// the 16 lanes that share the row.
+constexpr int CC_THREADS = 256, CC_KEYS = 64, CC_KPT = CC_KEYS / 16;
+
+template <typename TA>
+__device__ __forceinline__ float4 ld4(const TA* p) {
+    if (sizeof(TA) == 2) {
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                           __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+    }
+    return *reinterpret_cast<const float4*>(p);
+}
+
+__host__ __device__ constexpr int cc_pitch(int dp) { return dp + 4; }   // floats: 16-byte rows, no bank conflicts
+constexpr size_t cc_smem(int dp, int rows) {
+    return sizeof(float) * (static_cast<size_t>(rows) * cc_pitch(dp) + 2u * CC_KEYS * cc_pitch(dp) +
+                            static_cast<size_t>(rows) * (CC_KEYS + 4));
+}
+
+template <typename TA, int DP, int RPT>
+__global__ void __launch_bounds__(CC_THREADS)
+attn_cc_kernel(const AttnParams p) {
+    constexpr int ROWS = 16 * RPT, PITCH = cc_pitch(DP), NC = DP / 64, PP = CC_KEYS + 4;
+    extern __shared__ __align__(16) float smem_f[];
+    float* Qs = smem_f;
+    float* Ks = Qs + ROWS * PITCH;
+    float* Vs = Ks + CC_KEYS * PITCH;
+    float* Ps = Vs + CC_KEYS * PITCH;
+    __shared__ int s_last;
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, cta = blockIdx.x;
+    ptx::griddep_wait();
+    if (!attn_plan_agrees(p)) {
+        if (tid == 0) atomicOr(&g_attn_error, ATTN_ERR_RANGE);
+        return;
+    }
+    AttnWalk walk;
+    if (!walk.begin(p, cta)) return;
+    const int64_t per = attn_head(p)->per_cta;
+    const float zscale = p.scale * LOG2E;
+    const float cap_in = p.softcap > 0.0f ? p.scale / p.softcap : 0.0f;
+    AttnPiece pc;
+    while (walk.next(p, cta, per, pc)) {
+        const int nrows = pc.t.qlen * p.G;
+        // the tile's queries
+        for (int i = tid; i < ROWS * (DP / 4); i += CC_THREADS) {
+            const int row = i / (DP / 4), d = (i - row * (DP / 4)) * 4, r = pc.t.row0 + row;
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (r < nrows && d < p.Dh)
+                v = ld4(static_cast<const TA*>(p.q) + (pc.t.q0 + r / p.G) * p.q_stride +
+                        static_cast<int64_t>(pc.head * p.G + r % p.G) * p.Dh + d);
+            *reinterpret_cast<float4*>(Qs + row * PITCH + d) = v;
+        }
+        int lo[RPT], hi[RPT];
+        float m[RPT], l[RPT], acc[RPT][NC][4];
+#pragma unroll
+        for (int a = 0; a < RPT; ++a) {
+            const int r = pc.t.row0 + ty * RPT + a;
+            lo[a] = hi[a] = 0;
+            if (r < nrows) attn_row_keys(pc.t, r, p.G, p.window, lo[a], hi[a]);
+            m[a] = -INFINITY;
+            l[a] = 0.0f;
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[a][c][e] = 0.0f;
+        }
+        int tlo, thi, unused;
+        attn_row_keys(pc.t, pc.t.row0, p.G, p.window, tlo, unused);
+        attn_row_keys(pc.t, min(pc.t.row0 + ROWS, nrows) - 1, p.G, p.window, unused, thi);
+        for (int b = pc.b0; b < pc.b1; ++b) {
+            const int k0 = (pc.t.blk0 + b) * CC_KEYS;
+            __syncthreads();
+            // keys outside what the tile sees are zeros, whatever the pages hold there
+            for (int i = tid; i < CC_KEYS * (DP / 4); i += CC_THREADS) {
+                const int row = i / (DP / 4), d = (i - row * (DP / 4)) * 4, key = k0 + row;
+                float4 kk = make_float4(0.0f, 0.0f, 0.0f, 0.0f), vv = kk;
+                if (key >= tlo && key < thi && d < p.Dh) {
+                    const int pg = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
+                    const int in = key - pg * p.page_size;
+                    const int64_t page = p.page_table[pc.t.seq * p.table_stride + pg];
+                    if (page >= 0 && page < p.num_pages) {
+                        kk = ld4(static_cast<const TA*>(p.k_cache) + page * p.k_page_stride + in * p.k_slot_stride +
+                                 pc.head * p.k_head_stride + d);
+                        vv = ld4(static_cast<const TA*>(p.v_cache) + page * p.v_page_stride + in * p.v_slot_stride +
+                                 pc.head * p.v_head_stride + d);
+                    } else if (d == 0) {
+                        atomicOr(&g_attn_error, ATTN_ERR_RANGE);
+                    }
+                }
+                *reinterpret_cast<float4*>(Ks + row * PITCH + d) = kk;
+                *reinterpret_cast<float4*>(Vs + row * PITCH + d) = vv;
+            }
+            __syncthreads();
+            float s[RPT][CC_KPT];
+#pragma unroll
+            for (int a = 0; a < RPT; ++a)
+#pragma unroll
+                for (int j = 0; j < CC_KPT; ++j) s[a][j] = 0.0f;
+#pragma unroll 4
+            for (int d = 0; d < DP; d += 4) {
+                float4 kv[CC_KPT];
+#pragma unroll
+                for (int j = 0; j < CC_KPT; ++j)
+                    kv[j] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * j) * PITCH + d);
+#pragma unroll
+                for (int a = 0; a < RPT; ++a) {
+                    const float4 qv = *reinterpret_cast<const float4*>(Qs + (ty * RPT + a) * PITCH + d);
+#pragma unroll
+                    for (int j = 0; j < CC_KPT; ++j)
+                        s[a][j] = fmaf(qv.x, kv[j].x, fmaf(qv.y, kv[j].y, fmaf(qv.z, kv[j].z, fmaf(qv.w, kv[j].w, s[a][j]))));
+                }
+            }
+#pragma unroll
+            for (int a = 0; a < RPT; ++a) {
+                float mx = m[a];
+#pragma unroll
+                for (int j = 0; j < CC_KPT; ++j) {
+                    const int key = k0 + tx + 16 * j;
+                    float z = p.softcap > 0.0f ? p.softcap * LOG2E * tanhf(s[a][j] * cap_in) : s[a][j] * zscale;
+                    z = key >= lo[a] && key < hi[a] ? z : -INFINITY;
+                    s[a][j] = z;
+                    mx = fmaxf(mx, z);
+                }
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o, 16));
+                const float base = mx > -INFINITY ? mx : 0.0f;
+                const float keep = exp2f(m[a] - base);
+                float sum = 0.0f;
+#pragma unroll
+                for (int j = 0; j < CC_KPT; ++j) {
+                    const float e = exp2f(s[a][j] - base);
+                    sum += e;
+                    Ps[(ty * RPT + a) * PP + tx + 16 * j] = e;
+                }
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o, 16);
+                l[a] = fmaf(l[a], keep, sum);
+                m[a] = mx;
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[a][c][e] *= keep;
+            }
+            __syncwarp();   // a row's 16 lanes are in one warp
+#pragma unroll 2
+            for (int k = 0; k < CC_KEYS; k += 4) {
+                float4 pr[RPT];
+#pragma unroll
+                for (int a = 0; a < RPT; ++a) pr[a] = *reinterpret_cast<const float4*>(Ps + (ty * RPT + a) * PP + k);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        const float4 v = *reinterpret_cast<const float4*>(Vs + (k + kk) * PITCH + tx * 4 + 64 * c);
+#pragma unroll
+                        for (int a = 0; a < RPT; ++a) {
+                            const float w = kk == 0 ? pr[a].x : kk == 1 ? pr[a].y : kk == 2 ? pr[a].z : pr[a].w;
+                            acc[a][c][0] = fmaf(w, v.x, acc[a][c][0]);
+                            acc[a][c][1] = fmaf(w, v.y, acc[a][c][1]);
+                            acc[a][c][2] = fmaf(w, v.z, acc[a][c][2]);
+                            acc[a][c][3] = fmaf(w, v.w, acc[a][c][3]);
+                        }
+                    }
+                }
+            }
+        }
+        if (pc.whole) {
+#pragma unroll
+            for (int a = 0; a < RPT; ++a) {
+                const int r = pc.t.row0 + ty * RPT + a;
+                if (r >= nrows) continue;
+                const float inv = l[a] != 0.0f ? 1.0f / l[a] : 0.0f;
+                const int64_t out = (pc.t.q0 + r / p.G) * p.Hq + pc.head * p.G + r % p.G;
+                TA* o = static_cast<TA*>(p.o) + out * p.Dh;
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    const int d = tx * 4 + 64 * c;
+                    if (d >= p.Dh) continue;
+                    if (sizeof(TA) == 2) {
+                        const __nv_bfloat162 x = __floats2bfloat162_rn(acc[a][c][0] * inv, acc[a][c][1] * inv);
+                        const __nv_bfloat162 y = __floats2bfloat162_rn(acc[a][c][2] * inv, acc[a][c][3] * inv);
+                        *reinterpret_cast<uint2*>(o + d) = make_uint2(*reinterpret_cast<const uint32_t*>(&x),
+                                                                      *reinterpret_cast<const uint32_t*>(&y));
+                    } else {
+                        *reinterpret_cast<float4*>(o + d) = make_float4(acc[a][c][0] * inv, acc[a][c][1] * inv,
+                                                                        acc[a][c][2] * inv, acc[a][c][3] * inv);
+                    }
+                }
+                if (tx == 0 && p.lse != nullptr) p.lse[out] = attn_lse(m[a], l[a]);
+            }
+        } else {
+            float* s = attn_slot(p, pc.slot);
+            const int sr = p.plan.slot_rows;
+#pragma unroll
+            for (int a = 0; a < RPT; ++a) {
+                const int row = ty * RPT + a;
+                if (pc.t.row0 + row >= nrows) continue;
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+                    *reinterpret_cast<float4*>(s + static_cast<int64_t>(row) * DP + tx * 4 + 64 * c) =
+                        make_float4(acc[a][c][0], acc[a][c][1], acc[a][c][2], acc[a][c][3]);
+                if (tx == 0) {
+                    s[static_cast<int64_t>(sr) * DP + row] = m[a];
+                    s[static_cast<int64_t>(sr) * (DP + 1) + row] = l[a];
+                }
+            }
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                const int n = atomicAdd(attn_counts(p) + pc.t.cnt + pc.head, 1);
+                s_last = n == pc.last_cta - pc.first_cta;
+                // the counter is back at zero for the next call with this plan
+                if (s_last) attn_counts(p)[pc.t.cnt + pc.head] = 0;
+                __threadfence();
+            }
+            __syncthreads();
+            if (s_last) attn_join<TA>(p, pc, DP, tid, CC_THREADS);
+        }
+        __syncthreads();
+    }
+}
+
+int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+        return 148;
+    return n;
+}
+
+// cudaFuncSetAttribute once per device and kernel (idempotent, so a race is harmless).
+cudaError_t allow_smem(const void* kernel, std::atomic<uint64_t>& done, size_t bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (bit != 0 && (done.load() & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e == cudaSuccess) done.fetch_or(bit);
+    return e;
+}
+
+template <typename TA, int DP, int RPT>
+cudaError_t launch_cc(const AttnParams& p, cudaStream_t s) {
+    static std::atomic<uint64_t> done{0};
+    constexpr size_t smem = cc_smem(DP, 16 * RPT);
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(attn_cc_kernel<TA, DP, RPT>), done, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.plan.ncta));
+    cfg.blockDim = dim3(CC_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_cc_kernel<TA, DP, RPT>, p);
+}
+
+template <typename TA>
+cudaError_t launch_cc_dp(const AttnParams& p, cudaStream_t s) {
+    const bool small = p.plan.tile_rows == 16;
+    if (p.Dh <= 64) return small ? launch_cc<TA, 64, 1>(p, s) : launch_cc<TA, 64, 4>(p, s);
+    if (p.Dh <= 128) return small ? launch_cc<TA, 128, 1>(p, s) : launch_cc<TA, 128, 4>(p, s);
+    return small ? launch_cc<TA, 256, 1>(p, s) : launch_cc<TA, 256, 4>(p, s);
+}
+
+size_t up(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
+
+}  // namespace attn
+
+AttnPlan attn_plan_sizes(bool bf16, int64_t T, int B, int Hq, int Hk, int Dh, int page_size, int64_t max_q) {
+    AttnPlan a = {};
+    const int64_t G = Hq / Hk;
+    const int dp = Dh <= 64 ? 64 : Dh <= 128 ? 128 : 256;
+    (void)bf16;
+    (void)page_size;
+    // up to 16 rows a sequence and key head: the 16-row tile, which wastes no
+    // arithmetic on rows that are not there
+    a.tile_rows = max_q * G <= 16 ? 16 : 64;
+    a.block_keys = attn::CC_KEYS;
+    a.ncta = (dp == 256 ? 1 : 2) * attn::sm_count();
+    const int64_t rows = max_q * G < a.tile_rows ? max_q * G : a.tile_rows;
+    a.slot_rows = static_cast<int>((rows + 3) & ~int64_t(3));
+    a.max_tiles = T * G / a.tile_rows + B;
+    a.start_off = 256;
+    a.tile_off = a.start_off + attn::up(static_cast<size_t>(a.ncta) * sizeof(AttnStart));
+    a.count_off = a.tile_off + attn::up(static_cast<size_t>(a.max_tiles) * sizeof(AttnTile));
+    a.part_off = a.count_off + attn::up(static_cast<size_t>(a.max_tiles) * Hk * sizeof(int));
+    a.part_slot_bytes = attn::up(static_cast<size_t>(a.slot_rows) * (dp + 2) * sizeof(float));
+    a.total = a.part_off + 2u * static_cast<size_t>(a.ncta) * a.part_slot_bytes;
+    return a;
+}
+
+cudaError_t launch_attn_plan(const AttnPlan& plan, const int32_t* cu_q, const int32_t* kv_lens, int64_t T, int B,
+                             int Hq, int Hk, int window, int64_t max_q, int64_t max_kv, void* ws, cudaStream_t s) {
+    attn::PlanParams p;
+    p.cu_q = cu_q;
+    p.kv_lens = kv_lens;
+    p.ws = static_cast<unsigned char*>(ws);
+    p.T = T;
+    p.max_kv = max_kv;
+    p.B = B;
+    p.Hq = Hq;
+    p.Hk = Hk;
+    p.G = Hq / Hk;
+    p.window = window;
+    p.max_q = static_cast<int>(max_q);
+    p.plan = plan;
+    attn::attn_plan_kernel<<<1, attn::PLAN_THREADS, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_paged_attn(bool bf16, const AttnParams& p, cudaStream_t s) {
+    return bf16 ? attn::launch_cc_dp<__nv_bfloat16>(p, s) : attn::launch_cc_dp<float>(p, s);
+}
+
+}  // namespace mhc

@@ -103,6 +103,14 @@ cudaError_t read_and_clear_device_error(unsigned* word, cudaStream_t s) {
     *word |= other;
     other = 0;
     e = read_and_clear_small_error(&other);
+    if (e != cudaSuccess) return e;
+    *word |= other;
+    other = 0;
+    e = read_and_clear_qk_error(&other);
+    if (e != cudaSuccess) return e;
+    *word |= other;
+    other = 0;
+    e = read_and_clear_attn_error(&other);
     *word |= other;
     return e;
 }
