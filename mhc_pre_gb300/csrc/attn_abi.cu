@@ -318,6 +318,7 @@ mhc_status mhc_paged_attn(mhc_dtype dt, const void* q, int64_t q_stride, const v
     p.window = window;
     p.scale = scale;
     p.softcap = softcap;
+    p.force_timeout = mhc::forced_timeout();
     p.plan = plan;
     return from_cuda(mhc::launch_paged_attn(dt == MHC_BF16, p, stream));
 }

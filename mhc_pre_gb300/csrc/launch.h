@@ -144,8 +144,17 @@ cudaError_t launch_attn_plan(const AttnPlan& plan, const int32_t* cu_q, const in
                              int Hq, int Hk, int window, int64_t max_q, int64_t max_kv, void* ws, cudaStream_t s);
 cudaError_t launch_paged_attn(bool bf16, const AttnParams& p, cudaStream_t s);
 
+// On the tensor cores (paged_attn_tc.cu), where the types and sizes allow it.
+bool attn_tc_supports(bool bf16, int Dh, int page_size);
+cudaError_t launch_paged_attn_tc(const AttnParams& p, cudaStream_t s);
+
 // Device error words of these kernels, read and cleared.
 cudaError_t read_and_clear_qk_error(unsigned* word);
 cudaError_t read_and_clear_attn_error(unsigned* word);
+cudaError_t read_and_clear_attn_tc_error(unsigned* word);
+
+// The test hook of the bounded waits (pre_tc.cu), for kernels that take it as
+// a launch parameter.
+unsigned forced_timeout();
 
 }  // namespace mhc

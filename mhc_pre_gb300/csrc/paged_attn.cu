@@ -465,13 +465,17 @@ AttnPlan attn_plan_sizes(bool bf16, int64_t T, int B, int Hq, int Hk, int Dh, in
     AttnPlan a = {};
     const int64_t G = Hq / Hk;
     const int dp = Dh <= 64 ? 64 : Dh <= 128 ? 128 : 256;
-    (void)bf16;
-    (void)page_size;
-    // up to 16 rows a sequence and key head: the 16-row tile, which wastes no
-    // arithmetic on rows that are not there
-    a.tile_rows = max_q * G <= 16 ? 16 : 64;
-    a.block_keys = attn::CC_KEYS;
-    a.ncta = (dp == 256 ? 1 : 2) * attn::sm_count();
+    if (attn_tc_supports(bf16, Dh, page_size)) {
+        a.tile_rows = max_q * G <= 128 ? 128 : 256;
+        a.block_keys = 128;
+        a.ncta = attn::sm_count();
+    } else {
+        // up to 16 rows a sequence and key head: the 16-row tile, which wastes
+        // no arithmetic on rows that are not there
+        a.tile_rows = max_q * G <= 16 ? 16 : 64;
+        a.block_keys = attn::CC_KEYS;
+        a.ncta = (dp == 256 ? 1 : 2) * attn::sm_count();
+    }
     const int64_t rows = max_q * G < a.tile_rows ? max_q * G : a.tile_rows;
     a.slot_rows = static_cast<int>((rows + 3) & ~int64_t(3));
     a.max_tiles = T * G / a.tile_rows + B;
@@ -504,6 +508,7 @@ cudaError_t launch_attn_plan(const AttnPlan& plan, const int32_t* cu_q, const in
 }
 
 cudaError_t launch_paged_attn(bool bf16, const AttnParams& p, cudaStream_t s) {
+    if (attn_tc_supports(bf16, p.Dh, p.page_size)) return launch_paged_attn_tc(p, s);
     return bf16 ? attn::launch_cc_dp<__nv_bfloat16>(p, s) : attn::launch_cc_dp<float>(p, s);
 }
 

@@ -1,0 +1,621 @@
+// paged_attn_tc.cu -- attention of new tokens over a paged cache on the
+// tensor cores (bf16, heads of at most 128, pages that divide 128 keys or are
+// a multiple of 128).
+//
+// One CTA per SM walks the pieces of the plan (paged_attn.cuh).  Roles:
+//   * warp 8 loads: key and value blocks of 128 keys go through a ring of
+//     shared-memory stages, one TMA box per page and 64 columns (128-byte
+//     swizzle); the page numbers are read one block ahead.
+//   * warp 9 issues the MMAs: S = Q K^T (128 rows x 128 keys, both operands in
+//     shared memory) and O += P V with P read from tensor memory and V as it
+//     lies in the cache (keys along K, so no transposition anywhere).
+//   * two groups of four warps run the softmax of one 128-row lane each, a
+//     thread per row: scores are read from tensor memory to registers, the
+//     row's maximum needs no exchange between threads, and the exponentials go
+//     back as bf16 over the scores they came from.  While one lane is in its
+//     softmax the tensor core works for the other.
+// A tile of more than 128 rows gives each lane its own 128 rows and both use
+// every key block.  A tile of at most 128 rows (decoding) gives both lanes the
+// same rows and every other key block; the lanes are joined at the end.
+//
+// The running maximum is only raised when a row's new maximum exceeds it by
+// more than 2^8 in the exponentials' scale: float32 sums and bf16 exponentials
+// lose nothing by a common factor of up to 2^8, and O in tensor memory is then
+// rescaled a few times per row instead of at every block.
+//
+// Keys outside what a tile's rows see (past the sequence's end, before the
+// window, in pages that are not there) are masked in the scores, and their
+// value rows are zeroed in shared memory before the MMA reads them, so that
+// what the pages hold there (NaN, say) cannot reach a sum.
+//
+// Every wait is bounded (about one second); on expiry the kernel latches its
+// error word and all roles leave.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "launch.h"
+#include "paged_attn.cuh"
+#include "tc_ptx.cuh"
+
+namespace mhc {
+
+__device__ unsigned g_attn_tc_error;   // ATTN_ERR_* bits
+
+cudaError_t read_and_clear_attn_tc_error(unsigned* word) {
+    cudaError_t e = cudaMemcpyFromSymbol(word, g_attn_tc_error, sizeof(unsigned));
+    if (e != cudaSuccess) return e;
+    const unsigned zero = 0;
+    return cudaMemcpyToSymbol(g_attn_tc_error, &zero, sizeof(unsigned));
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();   // pre_tc.cu
+
+namespace attn_tc {
+
+constexpr int NTHREADS = 320;
+constexpr int LOAD_WARP = 8, MMA_WARP = 9;
+constexpr int ROWS = 128, KEYS = 128;
+constexpr int SUB = KEYS * 128;              // 128 rows x 64 columns: 16 KB
+constexpr int RING_BYTES = 160 * 1024;
+constexpr int TMEM_COLS = 512;
+constexpr uint32_t S_COL = 0, O_COL = 256;   // two of each, 128 columns apart
+constexpr uint64_t WAIT_LIMIT_NS = 1000000000ull;
+constexpr float RAISE = 8.0f;                // see above
+constexpr uint32_t FULL = 0xffffffffu;
+
+template <int DP> struct Cfg {
+    static constexpr int TILE = (DP / 64) * SUB;           // a block of keys, or 128 rows of queries
+    static constexpr int STAGES = RING_BYTES / TILE;
+    static constexpr int Q = 0;
+    static constexpr int RING = 2 * TILE;
+    static constexpr int BARS = RING + STAGES * TILE;
+    static constexpr int B_FULL = 0, B_EMPTY = STAGES, B_S = 2 * STAGES, B_P = B_S + 2, B_Q = B_P + 2, B_O = B_Q + 2;
+    static constexpr int NBARS = B_O + 2;
+    static constexpr int MISC = BARS + ((8 * NBARS + 15) / 16) * 16;   // TMEM address, abort flag, last-CTA flag
+    static constexpr int ML = MISC + 32;                               // lane 1's maxima and sums
+    static constexpr int TOTAL = ML + 2 * ROWS * 4;
+    static constexpr int SMEM = TOTAL + 1024;                          // the base is rounded up to 1024
+    static_assert(SMEM <= 232448, "shared memory of one SM");
+};
+
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = ptx::globaltimer();
+    for (uint32_t it = 1;; ++it) {
+        if (ptx::mbar_try_wait(bar, parity)) return true;
+        if ((it & 63) == 0) {
+            if (*abort_flag) return false;
+            if (ptx::globaltimer() - t0 > WAIT_LIMIT_NS) {
+                atomicOr(&g_attn_tc_error, ATTN_ERR_TIMEOUT);
+                *abort_flag = 1;
+                return false;
+            }
+        }
+    }
+}
+// The same for a whole warp: all lanes go on, or none.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    return __all_sync(FULL, wait_bar(bar, parity, abort_flag));
+}
+
+// Keys that any row of the piece's tile sees.
+__device__ __forceinline__ void tile_keys(const AttnParams& p, const AttnPiece& pc, int& lo, int& hi) {
+    int unused;
+    attn_row_keys(pc.t, pc.t.row0, p.G, p.window, lo, unused);
+    attn_row_keys(pc.t, min(pc.t.row0 + p.plan.tile_rows, pc.t.qlen * p.G) - 1, p.G, p.window, unused, hi);
+}
+
+template <int DP, bool CAP>
+__global__ void __launch_bounds__(NTHREADS, 1)
+attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+               const AttnParams p) {
+    using C = Cfg<DP>;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = ptx::smem_u32(smem);
+    auto bar = [&](int i) { return sbase + C::BARS + 8u * static_cast<uint32_t>(i); };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC + 4);
+    volatile int* last_flag = reinterpret_cast<volatile int*>(smem + C::MISC + 8);
+    float* ml = reinterpret_cast<float*>(smem + C::ML);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
+
+    if (p.force_timeout != 0u) {
+        // test hook: one bounded wait that runs out before anything async starts
+        if (tid == 0 && ptx::forced_wait_runs_out(sbase, 100000ull)) atomicOr(&g_attn_tc_error, ATTN_ERR_TIMEOUT);
+        __syncthreads();
+        return;
+    }
+    if (tid == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            ptx::mbar_init(bar(C::B_FULL + s), 1);
+            ptx::mbar_init(bar(C::B_EMPTY + s), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(bar(C::B_S + i), 1);
+            ptx::mbar_init(bar(C::B_P + i), 4);
+            ptx::mbar_init(bar(C::B_Q + i), 4);
+            ptx::mbar_init(bar(C::B_O + i), 1);
+        }
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+        ptx::prefetch_tmap(&tmap_k);
+        ptx::prefetch_tmap(&tmap_v);
+    }
+    if (warp == MMA_WARP) {
+        ptx::tmem_alloc(ptx::smem_u32(tmem_slot), TMEM_COLS);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    ptx::griddep_wait();   // the plan, the queries and the cache are written
+
+    AttnWalk walk;
+    const bool agrees = attn_plan_agrees(p);
+    if (!agrees && tid == 0) atomicOr(&g_attn_tc_error, ATTN_ERR_RANGE);
+    if (agrees && walk.begin(p, cta)) {
+        const int64_t per = attn_head(p)->per_cta;
+        AttnPiece pc;
+        if (warp == LOAD_WARP) {
+            // ------------------------------------------------------ loads ---
+            const uint64_t policy = ptx::policy_evict_normal();
+            const int box = p.page_size < KEYS ? p.page_size : KEYS;      // keys of one TMA box
+            const int boxes = KEYS / box;                                 // of a block: at most 16
+            int stage = 0;
+            uint32_t round = 0;
+            bool ok = true;
+            while (ok && walk.next(p, cta, per, pc)) {
+                int tlo, thi;
+                tile_keys(p, pc, tlo, thi);
+                const bool pair = pc.t.qlen * p.G - pc.t.row0 > ROWS;
+                const int nb = pc.b1 - pc.b0;
+                const int32_t* row = p.page_table + pc.t.seq * p.table_stride;
+                // lane i: the page of box i of a block, -1 where no row sees its keys
+                auto page_of = [&](int j) {
+                    const int key = (pc.t.blk0 + pc.b0 + j) * KEYS + lane * box;
+                    if (j >= nb || lane >= boxes || key + box <= tlo || key >= thi) return -1;
+                    const int pg = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
+                    const int page = row[pg];
+                    if (page >= 0 && page < p.num_pages) return page;
+                    atomicOr(&g_attn_tc_error, ATTN_ERR_RANGE);
+                    return -1;
+                };
+                auto load = [&](const CUtensorMap* tm, int j, int page) {
+                    if (!wait_warp(bar(C::B_EMPTY + stage), (round & 1) ^ 1, abort_flag)) return false;
+                    const uint32_t full = bar(C::B_FULL + stage), dst = sbase + C::RING + stage * C::TILE;
+                    const int n = __popc(__ballot_sync(FULL, page >= 0));
+                    if (lane == 0) ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(n * box * DP * 2));
+                    __syncwarp();
+                    if (page >= 0) {
+                        const int key = (pc.t.blk0 + pc.b0 + j) * KEYS + lane * box;
+                        const int place = p.page_shift >= 0 ? key & (p.page_size - 1) : key % p.page_size;
+#pragma unroll
+                        for (int c = 0; c < DP / 64; ++c)
+                            ptx::tma_load_4d(dst + c * SUB + lane * box * 128, tm, c * 64, place, pc.head, page, full,
+                                             policy);
+                    }
+                    if (++stage == C::STAGES) {
+                        stage = 0;
+                        ++round;
+                    }
+                    return true;
+                };
+                // in the order of use: K0 V0 K1 V1 ... for a pair of lanes on
+                // one block, K0 K1 V0 K2 V1 ... for lanes on alternate blocks
+                int page = page_of(0), ahead = page_of(1);
+                ok = load(&tmap_k, 0, page);
+                for (int j = 0; ok && j < nb; ++j) {
+                    const int next = page_of(j + 2);
+                    if (!pair && j + 1 < nb) ok = load(&tmap_k, j + 1, ahead);
+                    ok = ok && load(&tmap_v, j, page);
+                    if (pair && j + 1 < nb) ok = ok && load(&tmap_k, j + 1, ahead);
+                    page = ahead;
+                    ahead = next;
+                }
+            }
+        } else if (warp == MMA_WARP) {
+            // -------------------------------------------------------- MMA ---
+            constexpr uint32_t IDESC_S = ptx::idesc_bf16_f32(ROWS, KEYS);
+            constexpr uint32_t IDESC_O = ptx::idesc_bf16_f32(ROWS, DP) | (1u << 16);   // B (V) MN-major
+            const uint64_t desc_q = ptx::sw128_kmajor_desc(sbase + C::Q);
+            const uint64_t desc_k = ptx::sw128_kmajor_desc(sbase + C::RING);
+            const uint64_t desc_v = ptx::sw128_mnmajor_desc(sbase + C::RING, SUB, 1024);
+            int stage = 0;
+            uint32_t round = 0, par_q = 0, par_p[2] = {0, 0};
+            bool ok = true;
+            auto take = [&]() {   // the ring's next stage, once it is full
+                const int s = stage;
+                ok = ok && wait_warp(bar(C::B_FULL + s), round & 1, abort_flag);
+                if (++stage == C::STAGES) {
+                    stage = 0;
+                    ++round;
+                }
+                return s;
+            };
+            auto scores = [&](int L, int s) {
+                if (lane == 0) {
+                    const uint64_t a = ptx::desc_add(desc_q, L * C::TILE), b = ptx::desc_add(desc_k, s * C::TILE);
+#pragma unroll
+                    for (int k = 0; k < DP / 16; ++k)
+                        ptx::tc_mma_f16(tmem + S_COL + L * 128, ptx::desc_add(a, (k / 4) * SUB + (k % 4) * 32),
+                                        ptx::desc_add(b, (k / 4) * SUB + (k % 4) * 32), IDESC_S, k > 0);
+                    ptx::tc_commit(bar(C::B_S + L));
+                }
+            };
+            auto values = [&](int L, int s, bool add) {
+                if (lane == 0) {
+                    const uint64_t b = ptx::desc_add(desc_v, s * C::TILE);
+#pragma unroll
+                    for (int k = 0; k < KEYS / 16; ++k)
+                        ptx::tc_mma_f16_ts(tmem + O_COL + L * 128, tmem + S_COL + L * 128 + k * 8,
+                                           ptx::desc_add(b, k * 2048), IDESC_O, add || k > 0);
+                }
+            };
+            auto commit = [&](int b) {
+                if (lane == 0) ptx::tc_commit(bar(b));
+            };
+            while (ok && walk.next(p, cta, per, pc)) {
+                int tlo, thi;
+                tile_keys(p, pc, tlo, thi);
+                const bool pair = pc.t.qlen * p.G - pc.t.row0 > ROWS;
+                const int nb = pc.b1 - pc.b0;
+                // value rows that no row of the tile sees become zeros
+                auto blank = [&](int s, int j) {
+                    const int k0 = (pc.t.blk0 + pc.b0 + j) * KEYS;
+                    if (k0 >= tlo && k0 + KEYS <= thi) return;
+                    for (int r = 0; r < KEYS; ++r) {
+                        if (k0 + r >= tlo && k0 + r < thi) continue;
+                        if (lane < DP / 8)
+                            *reinterpret_cast<uint4*>(smem + C::RING + s * C::TILE + (lane >> 3) * SUB + r * 128 +
+                                                      (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                };
+                ok = wait_warp(bar(C::B_Q + 0), par_q, abort_flag) && wait_warp(bar(C::B_Q + 1), par_q, abort_flag);
+                par_q ^= 1;
+                auto wait_p = [&](int L) {
+                    ok = ok && wait_warp(bar(C::B_P + L), par_p[L], abort_flag);
+                    par_p[L] ^= 1;
+                    ptx::tc_fence_after();
+                };
+                if (!ok) break;
+                ptx::tc_fence_after();
+                if (pair) {
+                    int sk = take();
+                    if (!ok) break;
+                    scores(0, sk);
+                    scores(1, sk);
+                    commit(C::B_EMPTY + sk);
+                    for (int j = 0; j < nb; ++j) {
+                        const bool more = j + 1 < nb;
+                        const int sv = take();
+                        if (!ok) break;
+                        blank(sv, j);
+                        wait_p(0);
+                        if (!ok) break;
+                        values(0, sv, j > 0);
+                        if (more) {
+                            sk = take();
+                            if (!ok) break;
+                            scores(0, sk);
+                        } else {
+                            commit(C::B_O + 0);
+                        }
+                        wait_p(1);
+                        if (!ok) break;
+                        values(1, sv, j > 0);
+                        commit(C::B_EMPTY + sv);
+                        if (more) {
+                            scores(1, sk);
+                            commit(C::B_EMPTY + sk);
+                        } else {
+                            commit(C::B_O + 1);
+                        }
+                    }
+                } else {
+                    for (int j = 0; j < 2 && j < nb; ++j) {
+                        const int sk = take();
+                        if (!ok) break;
+                        scores(j, sk);
+                        commit(C::B_EMPTY + sk);
+                    }
+                    for (int j = 0; ok && j < nb; ++j) {
+                        const int L = j & 1;
+                        const int sv = take();
+                        if (!ok) break;
+                        blank(sv, j);
+                        wait_p(L);
+                        if (!ok) break;
+                        values(L, sv, j > 1);
+                        commit(C::B_EMPTY + sv);
+                        if (j + 2 < nb) {
+                            const int sk = take();
+                            if (!ok) break;
+                            scores(L, sk);
+                            commit(C::B_EMPTY + sk);
+                        } else {
+                            commit(C::B_O + L);
+                        }
+                    }
+                }
+            }
+        } else {
+            // ---------------------------------------------------- softmax ---
+            const int L = warp >> 2, w4 = warp & 3, row_t = w4 * 32 + lane;
+            const uint32_t t_lane = tmem + (static_cast<uint32_t>(w4 * 32) << 16);
+            const uint32_t t_s = t_lane + S_COL + L * 128;
+            const float zscale = CAP ? 1.0f : p.scale * LOG2E;
+            const float cap2 = p.softcap * LOG2E, cap_in = CAP ? 2.0f * LOG2E * p.scale / p.softcap : 0.0f;
+            uint32_t par_s = 0, par_o = 0;
+            bool ok = true;
+            while (walk.next(p, cta, per, pc)) {
+                const int nrows = pc.t.qlen * p.G;
+                const bool pair = nrows - pc.t.row0 > ROWS;
+                const int nb = pc.b1 - pc.b0;
+                const int mine = pair ? nb : (nb + 1 - L) / 2;      // blocks of this lane
+                const int rbase = pc.t.row0 + (pair ? L * ROWS : 0);
+                const bool active = rbase + w4 * 32 < nrows;        // a warp without rows only keeps the protocol
+                // the lane's queries, 128-byte swizzle
+                if (active) {
+                    constexpr int LPR = DP / 8;
+                    for (int i = lane / LPR; i < 32; i += 32 / LPR) {
+                        const int rt = w4 * 32 + i, r = rbase + rt, c = lane % LPR;
+                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                        if (r < nrows && c * 8 < p.Dh)
+                            v = ld16(static_cast<const __nv_bfloat16*>(p.q) + (pc.t.q0 + r / p.G) * p.q_stride +
+                                     static_cast<int64_t>(pc.head * p.G + r % p.G) * p.Dh + c * 8);
+                        *reinterpret_cast<uint4*>(smem + C::Q + L * C::TILE + (c >> 3) * SUB + rt * 128 +
+                                                  (((c & 7) ^ (rt & 7)) << 4)) = v;
+                    }
+                }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(C::B_Q + L));
+
+                const int r = rbase + row_t;
+                int lo = 0, hi = 0x7fffffff;   // rows that are not there need no mask
+                if (r < nrows) attn_row_keys(pc.t, r, p.G, p.window, lo, hi);
+                float m = -INFINITY, l = 0.0f;
+                for (int i = 0; ok && i < mine; ++i) {
+                    const int k0 = (pc.t.blk0 + pc.b0 + (pair ? i : 2 * i + L)) * KEYS;
+                    ok = wait_warp(bar(C::B_S + L), par_s, abort_flag);
+                    par_s ^= 1;
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    if (active) {
+                        uint32_t u[128];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) ptx::tmem_ld32(t_s + c * 32, u + c * 32);
+                        ptx::tmem_wait_ld();
+                        if (CAP) {
+#pragma unroll
+                            for (int e = 0; e < 128; ++e)
+                                u[e] = __float_as_uint(
+                                    fmaf(-2.0f * cap2, fast_rcp(ex2(__uint_as_float(u[e]) * cap_in) + 1.0f), cap2));
+                        }
+                        if (__any_sync(FULL, k0 < lo || k0 + KEYS > hi)) {
+                            const int a = lo - k0, b = hi - k0;
+#pragma unroll
+                            for (int e = 0; e < 128; ++e)
+                                if (e < a || e >= b) u[e] = 0xff800000u;
+                        }
+                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int e = 0; e < 128; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(u[e]));
+                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * zscale;
+                        const bool raise = top > m + RAISE || (m == -INFINITY && top > -INFINITY);
+                        if (__any_sync(FULL, raise)) {
+                            // S of this block is complete, so every earlier MMA is: O stands still
+                            const float f = raise ? ex2(m - top) : 1.0f;
+                            if (raise) m = top;
+                            l *= f;
+                            if (i > 0) {
+#pragma unroll
+                                for (int c = 0; c < DP / 32; ++c) {
+                                    uint32_t o[32];
+                                    ptx::tmem_ld32(t_lane + O_COL + L * 128 + c * 32, o);
+                                    ptx::tmem_wait_ld();
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                    ptx::tmem_st32(t_lane + O_COL + L * 128 + c * 32, o);
+                                }
+                            }
+                        }
+                        const float base = m == -INFINITY ? 0.0f : m;
+                        const float2 z2 = make_float2(zscale, zscale), b2 = make_float2(-base, -base);
+                        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t pk[32];
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const float2 x = __ffma2_rn(make_float2(__uint_as_float(u[64 * h + 2 * e]),
+                                                                        __uint_as_float(u[64 * h + 2 * e + 1])),
+                                                            z2, b2);
+                                const float2 y = make_float2(ex2(x.x), ex2(x.y));
+                                sum[e & 1] = __fadd2_rn(sum[e & 1], y);
+                                const __nv_bfloat162 t = __floats2bfloat162_rn(y.x, y.y);
+                                pk[e] = *reinterpret_cast<const uint32_t*>(&t);
+                            }
+                            ptx::tmem_st32(t_s + h * 32, pk);
+                        }
+                        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                        ptx::tmem_wait_st();
+                    }
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(bar(C::B_P + L));
+                }
+                if (ok && mine > 0) {
+                    ok = wait_warp(bar(C::B_O + L), par_o, abort_flag);
+                    par_o ^= 1;
+                }
+                if (!pair && L == 1) {
+                    ml[row_t] = m;
+                    ml[ROWS + row_t] = l;
+                }
+                if (ptx::named_bar_or(1, 256, !ok)) break;   // both lanes are complete, or both leave
+                ptx::tc_fence_after();
+                // the rows' sums: to the output if this is the whole tile,
+                // else to the workspace
+                if (active && (pair || L == 0)) {
+                    float w0 = 1.0f, w1 = 0.0f;
+                    if (!pair) {
+                        const float m1 = ml[row_t], l1 = ml[ROWS + row_t];
+                        const float M = fmaxf(m, m1), base = M == -INFINITY ? 0.0f : M;
+                        w0 = ex2(m - base);
+                        w1 = ex2(m1 - base);
+                        m = M;
+                        l = l * w0 + l1 * w1;
+                    }
+                    const float inv = pc.whole ? (l != 0.0f ? 1.0f / l : 0.0f) : 1.0f;
+                    w0 *= inv;
+                    w1 *= inv;
+                    const bool valid = r < nrows;
+                    const int64_t out = valid ? (pc.t.q0 + r / p.G) * p.Hq + pc.head * p.G + r % p.G : 0;
+                    const int rt = r - pc.t.row0;
+                    float* part = attn_slot(p, pc.slot);
+#pragma unroll
+                    for (int c = 0; c < DP / 32; ++c) {
+                        uint32_t o[32];
+                        ptx::tmem_ld32(t_lane + O_COL + L * 128 + c * 32, o);
+                        ptx::tmem_wait_ld();
+                        float f[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * w0;
+                        if (!pair && nb > 1) {
+                            ptx::tmem_ld32(t_lane + O_COL + 128 + c * 32, o);
+                            ptx::tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) f[e] = fmaf(__uint_as_float(o[e]), w1, f[e]);
+                        }
+                        if (valid && pc.whole) {
+                            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + out * p.Dh + c * 32;
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) {
+                                float t[8];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) t[e] = f[8 * g + e];
+                                if (c * 32 + g * 8 < p.Dh)
+                                    *reinterpret_cast<uint4*>(dst + g * 8) = Vec<__nv_bfloat16>::pack(t);
+                            }
+                        } else if (valid) {
+#pragma unroll
+                            for (int g = 0; g < 8; ++g)
+                                *reinterpret_cast<float4*>(part + static_cast<int64_t>(rt) * DP + c * 32 + g * 4) =
+                                    make_float4(f[4 * g], f[4 * g + 1], f[4 * g + 2], f[4 * g + 3]);
+                        }
+                        __syncwarp();
+                    }
+                    if (valid) {
+                        if (pc.whole) {
+                            if (p.lse != nullptr) p.lse[out] = attn_lse(m, l);
+                        } else {
+                            part[static_cast<int64_t>(p.plan.slot_rows) * DP + rt] = m;
+                            part[static_cast<int64_t>(p.plan.slot_rows) * (DP + 1) + rt] = l;
+                        }
+                    }
+                    __syncwarp();
+                    ptx::tc_fence_before();
+                }
+                if (!pc.whole) __threadfence();
+                ptx::named_bar_sync(1, 256);   // O may be overwritten; partial rows are written
+                if (!pc.whole) {
+                    if (tid == 0) {
+                        int* count = attn_counts(p) + pc.t.cnt + pc.head;
+                        const int n = atomicAdd(count, 1);
+                        const bool last = n == pc.last_cta - pc.first_cta;
+                        if (last) *count = 0;   // back at zero for the next call with this plan
+                        *last_flag = last;
+                        __threadfence();
+                    }
+                    ptx::named_bar_sync(1, 256);
+                    if (*last_flag) attn_join<__nv_bfloat16>(p, pc, DP, tid, 256);
+                }
+            }
+        }
+    }
+    __syncthreads();
+    if (*abort_flag) {
+        // let copies already issued land before the shared memory goes away
+        const uint64_t t0 = ptx::globaltimer();
+        while (ptx::globaltimer() - t0 < 20000ull) {
+        }
+    }
+    if (warp == MMA_WARP) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+// ------------------------------------------------------------------ host ---
+
+cudaError_t encode(PFN_cuTensorMapEncodeTiled_v12000 fn, CUtensorMap* tm, const void* cache, const AttnParams& p,
+                   int64_t page_stride, int64_t slot_stride, int64_t head_stride) {
+    // (d, place, head, page); a box is 64 columns x (a page or 128 places)
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(p.Dh), static_cast<cuuint64_t>(p.page_size),
+                                static_cast<cuuint64_t>(p.Hk), static_cast<cuuint64_t>(p.num_pages)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(slot_stride * 2), static_cast<cuuint64_t>(head_stride * 2),
+                                   static_cast<cuuint64_t>(page_stride * 2)};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(p.page_size < KEYS ? p.page_size : KEYS), 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(cache), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+
+template <int DP, bool CAP>
+cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const AttnParams& p, cudaStream_t s) {
+    static std::atomic<uint64_t> done{0};   // devices whose kernel has its shared memory allowed
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (bit == 0 || !(done.load() & bit)) {
+        e = cudaFuncSetAttribute(attn_tc_kernel<DP, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<DP>::SMEM);
+        if (e != cudaSuccess) return e;
+        done.fetch_or(bit);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.plan.ncta));
+    cfg.blockDim = dim3(NTHREADS);
+    cfg.dynamicSmemBytes = Cfg<DP>::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_tc_kernel<DP, CAP>, tk, tv, p);
+}
+
+}  // namespace attn_tc
+
+// Boxes of 8 or more whole swizzle rows that tile a block of 128 keys.
+bool attn_tc_supports(bool bf16, int Dh, int page_size) {
+    return bf16 && Dh <= 128 && page_size >= 8 && (128 % page_size == 0 || page_size % 128 == 0);
+}
+
+cudaError_t launch_paged_attn_tc(const AttnParams& p, cudaStream_t s) {
+    auto fn = tensor_map_encoder();
+    if (fn == nullptr) return cudaErrorNotSupported;
+    CUtensorMap tk, tv;
+    cudaError_t e = attn_tc::encode(fn, &tk, p.k_cache, p, p.k_page_stride, p.k_slot_stride, p.k_head_stride);
+    if (e == cudaSuccess) e = attn_tc::encode(fn, &tv, p.v_cache, p, p.v_page_stride, p.v_slot_stride, p.v_head_stride);
+    if (e != cudaSuccess) return e;
+    if (p.Dh <= 64)
+        return p.softcap > 0.0f ? attn_tc::launch<64, true>(tk, tv, p, s) : attn_tc::launch<64, false>(tk, tv, p, s);
+    return p.softcap > 0.0f ? attn_tc::launch<128, true>(tk, tv, p, s) : attn_tc::launch<128, false>(tk, tv, p, s);
+}
+
+}  // namespace mhc

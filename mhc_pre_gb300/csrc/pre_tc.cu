@@ -67,6 +67,8 @@ cudaError_t set_force_timeout_pre(unsigned on) {
     return cudaSuccess;
 }
 
+unsigned forced_timeout() { return g_force_timeout_pre.load(); }
+
 cudaError_t read_and_clear_bwd_tc_error(unsigned* word);      // pre_bwd_tc.cu
 cudaError_t read_and_clear_bwd_fused_error(unsigned* word);   // pre_bwd_fused.cu
 cudaError_t read_and_clear_post_pre_error(unsigned* word);    // post_pre_tc.cu
@@ -111,6 +113,10 @@ cudaError_t read_and_clear_device_error(unsigned* word, cudaStream_t s) {
     *word |= other;
     other = 0;
     e = read_and_clear_attn_error(&other);
+    if (e != cudaSuccess) return e;
+    *word |= other;
+    other = 0;
+    e = read_and_clear_attn_tc_error(&other);
     *word |= other;
     return e;
 }
