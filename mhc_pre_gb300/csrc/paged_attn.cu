@@ -133,7 +133,7 @@ attn_plan_kernel(const PlanParams p) {
                 t.cnt = (ntiles + i) * p.Hk;
             }
             int64_t sum = 0;
-            t.start = units + block_scan(static_cast<int64_t>(t.nblk) * p.Hk, sums, sum);
+            t.start = units + block_scan(on ? static_cast<int64_t>(t.nblk + p.plan.lead) * p.Hk : 0, sums, sum);
             units += sum;
             if (on) {
                 tiles[ntiles + i] = t;
@@ -159,11 +159,12 @@ attn_plan_kernel(const PlanParams p) {
         h->tile_rows = TR;
         h->block_keys = BN;
         h->window = p.window;
+        h->lead = p.plan.lead;
     }
     AttnStart* starts = reinterpret_cast<AttnStart*>(p.ws + p.plan.start_off);
     for (int c = tid; c < p.plan.ncta; c += PLAN_THREADS) {
         const int64_t u = c * per;
-        AttnStart s = {0, 0, 0, 0};
+        AttnStart s = {};
         if (u < units) {
             int lo = 0, hi = ntiles - 1;
             while (lo < hi) {
@@ -172,11 +173,12 @@ attn_plan_kernel(const PlanParams p) {
                 if (st <= u) lo = mid;
                 else hi = mid - 1;
             }
-            const int nblk = tiles[lo].nblk;
-            const int64_t in = u - (lo < PLAN_TILES ? s_start[lo] : tiles[lo].start);
+            s.t = tiles[lo];
+            const int cost = s.t.nblk + p.plan.lead;
+            const int64_t in = u - s.t.start;
             s.tile = lo;
-            s.head = static_cast<int>(in / nblk);
-            s.blk = static_cast<int>(in - static_cast<int64_t>(s.head) * nblk);
+            s.head = static_cast<int>(in / cost);
+            s.unit = static_cast<int>(in - static_cast<int64_t>(s.head) * cost);
         }
         starts[c] = s;
     }
@@ -225,18 +227,17 @@ attn_cc_kernel(const AttnParams p) {
     }
     AttnWalk walk;
     if (!walk.begin(p, cta)) return;
-    const int64_t per = attn_head(p)->per_cta;
     const float zscale = p.scale * LOG2E;
     const float cap_in = p.softcap > 0.0f ? p.scale / p.softcap : 0.0f;
     AttnPiece pc;
-    while (walk.next(p, cta, per, pc)) {
-        const int nrows = pc.t.qlen * p.G;
+    while (walk.next(p, cta, pc)) {
+        const int nrows = pc.qlen * p.G;
         // the tile's queries
         for (int i = tid; i < ROWS * (DP / 4); i += CC_THREADS) {
-            const int row = i / (DP / 4), d = (i - row * (DP / 4)) * 4, r = pc.t.row0 + row;
+            const int row = i / (DP / 4), d = (i - row * (DP / 4)) * 4, r = pc.row0 + row;
             float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             if (r < nrows && d < p.Dh)
-                v = ld4(static_cast<const TA*>(p.q) + (pc.t.q0 + r / p.G) * p.q_stride +
+                v = ld4(static_cast<const TA*>(p.q) + (pc.q0 + r / p.G) * p.q_stride +
                         static_cast<int64_t>(pc.head * p.G + r % p.G) * p.Dh + d);
             *reinterpret_cast<float4*>(Qs + row * PITCH + d) = v;
         }
@@ -244,9 +245,9 @@ attn_cc_kernel(const AttnParams p) {
         float m[RPT], l[RPT], acc[RPT][NC][4];
 #pragma unroll
         for (int a = 0; a < RPT; ++a) {
-            const int r = pc.t.row0 + ty * RPT + a;
+            const int r = pc.row0 + ty * RPT + a;
             lo[a] = hi[a] = 0;
-            if (r < nrows) attn_row_keys(pc.t, r, p.G, p.window, lo[a], hi[a]);
+            if (r < nrows) attn_row_keys(pc, r, p.G, p.window, lo[a], hi[a]);
             m[a] = -INFINITY;
             l[a] = 0.0f;
 #pragma unroll
@@ -255,10 +256,10 @@ attn_cc_kernel(const AttnParams p) {
                 for (int e = 0; e < 4; ++e) acc[a][c][e] = 0.0f;
         }
         int tlo, thi, unused;
-        attn_row_keys(pc.t, pc.t.row0, p.G, p.window, tlo, unused);
-        attn_row_keys(pc.t, min(pc.t.row0 + ROWS, nrows) - 1, p.G, p.window, unused, thi);
-        for (int b = pc.b0; b < pc.b1; ++b) {
-            const int k0 = (pc.t.blk0 + b) * CC_KEYS;
+        attn_row_keys(pc, pc.row0, p.G, p.window, tlo, unused);
+        attn_row_keys(pc, min(pc.row0 + ROWS, nrows) - 1, p.G, p.window, unused, thi);
+        for (int b = 0; b < pc.nb; ++b) {
+            const int k0 = (pc.blk + b) * CC_KEYS;
             __syncthreads();
             // keys outside what the tile sees are zeros, whatever the pages hold there
             for (int i = tid; i < CC_KEYS * (DP / 4); i += CC_THREADS) {
@@ -267,7 +268,7 @@ attn_cc_kernel(const AttnParams p) {
                 if (key >= tlo && key < thi && d < p.Dh) {
                     const int pg = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
                     const int in = key - pg * p.page_size;
-                    const int64_t page = p.page_table[pc.t.seq * p.table_stride + pg];
+                    const int64_t page = p.page_table[pc.seq * p.table_stride + pg];
                     if (page >= 0 && page < p.num_pages) {
                         kk = ld4(static_cast<const TA*>(p.k_cache) + page * p.k_page_stride + in * p.k_slot_stride +
                                  pc.head * p.k_head_stride + d);
@@ -357,10 +358,10 @@ attn_cc_kernel(const AttnParams p) {
         if (pc.whole) {
 #pragma unroll
             for (int a = 0; a < RPT; ++a) {
-                const int r = pc.t.row0 + ty * RPT + a;
+                const int r = pc.row0 + ty * RPT + a;
                 if (r >= nrows) continue;
                 const float inv = l[a] != 0.0f ? 1.0f / l[a] : 0.0f;
-                const int64_t out = (pc.t.q0 + r / p.G) * p.Hq + pc.head * p.G + r % p.G;
+                const int64_t out = (pc.q0 + r / p.G) * p.Hq + pc.head * p.G + r % p.G;
                 TA* o = static_cast<TA*>(p.o) + out * p.Dh;
 #pragma unroll
                 for (int c = 0; c < NC; ++c) {
@@ -384,7 +385,7 @@ attn_cc_kernel(const AttnParams p) {
 #pragma unroll
             for (int a = 0; a < RPT; ++a) {
                 const int row = ty * RPT + a;
-                if (pc.t.row0 + row >= nrows) continue;
+                if (pc.row0 + row >= nrows) continue;
 #pragma unroll
                 for (int c = 0; c < NC; ++c)
                     *reinterpret_cast<float4*>(s + static_cast<int64_t>(row) * DP + tx * 4 + 64 * c) =
@@ -397,14 +398,14 @@ attn_cc_kernel(const AttnParams p) {
             __threadfence();
             __syncthreads();
             if (tid == 0) {
-                const int n = atomicAdd(attn_counts(p) + pc.t.cnt + pc.head, 1);
+                const int n = atomicAdd(attn_counts(p) + pc.cnt, 1);
                 s_last = n == pc.last_cta - pc.first_cta;
                 // the counter is back at zero for the next call with this plan
-                if (s_last) attn_counts(p)[pc.t.cnt + pc.head] = 0;
+                if (s_last) attn_counts(p)[pc.cnt] = 0;
                 __threadfence();
             }
             __syncthreads();
-            if (s_last) attn_join<TA>(p, pc, DP, tid, CC_THREADS);
+            if (s_last) attn_join<TA, DP, CC_THREADS / 32>(p, pc, tid);
         }
         __syncthreads();
     }
@@ -476,6 +477,7 @@ AttnPlan attn_plan_sizes(bool bf16, int64_t T, int B, int Hq, int Hk, int Dh, in
         a.block_keys = attn::CC_KEYS;
         a.ncta = (dp == 256 ? 1 : 2) * attn::sm_count();
     }
+    a.lead = 2;
     const int64_t rows = max_q * G < a.tile_rows ? max_q * G : a.tile_rows;
     a.slot_rows = static_cast<int>((rows + 3) & ~int64_t(3));
     a.max_tiles = T * G / a.tile_rows + B;

@@ -7,6 +7,8 @@
 // r / G, head r % G of the group, G = Hq/Hk); a tile is up to `tile_rows`
 // consecutive rows, and it reads the keys that any of its rows sees in blocks
 // of `block_keys`.  The unit of work is one block of one tile of one key head.
+// A tile of a key head begins with `lead` units that stand for its fixed costs
+// (queries in, sums out), so that many short tiles weigh what they take.
 // All units are laid end to end (tiles, then key heads, then blocks) and CTA c
 // takes the `per_cta` consecutive units from c * per_cta: every CTA has the
 // same share whatever the lengths are, a long sequence is split over as many
@@ -26,7 +28,7 @@ namespace mhc {
 constexpr unsigned ATTN_ERR_TIMEOUT = 1u, ATTN_ERR_RANGE = 2u;
 
 // One tile of rows of one sequence, for every key head.
-struct AttnTile {
+struct alignas(16) AttnTile {
     int64_t start;      // its first unit
     int64_t q0;         // the sequence's first row of q
     int seq;
@@ -44,14 +46,15 @@ struct AttnHead {       // start of the plan
     int64_t T;          // rows of q, for the check that plan and call agree
     int ntiles;
     int ncta;
-    int Hq, Hk, B, tile_rows, block_keys, window;
+    int Hq, Hk, B, tile_rows, block_keys, window, lead;
 };
-static_assert(sizeof(AttnHead) <= 64, "the header has 64 bytes");
+static_assert(sizeof(AttnHead) <= 256, "the header has 256 bytes");
 
 // Sizes both the host and the device need.
 struct AttnPlan {
     int ncta;           // CTAs of the launch
     int tile_rows, block_keys;
+    int lead;           // fixed cost of a tile, in blocks
     int slot_rows;      // rows a partial result can have
     int64_t max_tiles;
     size_t start_off, tile_off, count_off, part_off, part_slot_bytes, total;
@@ -73,10 +76,13 @@ struct AttnParams {
     AttnPlan plan;
 };
 
-// Where a CTA starts: tile, key head and block.
-struct AttnStart {
-    int tile, head, blk, pad;
+// Where a CTA starts: tile, key head and unit of the tile, and the tile itself
+// (one read instead of two on the way to the first queries and keys).
+struct alignas(16) AttnStart {
+    int tile, head, unit, pad;
+    AttnTile t;
 };
+static_assert(sizeof(AttnStart) == 64, "AttnStart is read as four 16-byte words");
 
 __device__ __forceinline__ const AttnHead* attn_head(const AttnParams& p) {
     return reinterpret_cast<const AttnHead*>(p.ws);
@@ -96,66 +102,76 @@ __device__ __forceinline__ bool attn_plan_agrees(const AttnParams& p) {
     const AttnHead* h = attn_head(p);
     return h->T == p.T && h->Hq == p.Hq && h->Hk == p.Hk && h->B == p.B && h->tile_rows == p.plan.tile_rows &&
            h->block_keys == p.plan.block_keys && h->window == p.window && h->ncta == p.plan.ncta &&
-           h->ntiles >= 0 && h->ntiles <= p.plan.max_tiles && h->per_cta > 0;
+           h->lead == p.plan.lead && h->ntiles >= 0 && h->ntiles <= p.plan.max_tiles && h->per_cta > 0;
 }
 
 // A CTA's pieces one after the other.
 struct AttnPiece {
-    AttnTile t;
-    int tile, head;
-    int b0, b1;          // blocks [b0, b1) of the tile, relative to its first
-    bool whole;          // the tile's only piece
-    int slot;            // where a partial result goes
+    int64_t q0;
+    int seq, qlen, kvlen, row0, head;
+    int blk, nb;                // first key block and number of blocks (0: there is no piece)
+    int whole;                  // the tile's only piece
+    int cnt, slot;              // join counter; where a partial result goes
     int first_cta, last_cta;
 };
+static_assert(sizeof(AttnPiece) == 56, "two pieces and the walk fit the softmax warps' state");
 struct AttnWalk {
-    int64_t at, end;
-    int tile, head, blk;
+    int64_t at, end, per;
+    int tile, head, unit;
+    AttnTile t;
     __device__ __forceinline__ bool begin(const AttnParams& p, int cta) {
         const AttnHead* h = attn_head(p);
-        const int64_t per = h->per_cta;
+        const AttnStart s = attn_starts(p)[cta];
+        per = h->per_cta;
         at = static_cast<int64_t>(cta) * per;
         end = min(at + per, h->units);
-        if (at >= end) return false;
-        const AttnStart s = attn_starts(p)[cta];
         tile = s.tile;
         head = s.head;
-        blk = s.blk;
-        return true;
+        unit = s.unit;
+        t = s.t;
+        return at < end;
     }
-    __device__ __forceinline__ bool next(const AttnParams& p, int cta, int64_t per, AttnPiece& out) {
-        if (at >= end) return false;
-        const int4* src = reinterpret_cast<const int4*>(attn_tiles(p) + tile);
-        int4* dst = reinterpret_cast<int4*>(&out.t);
-        dst[0] = src[0];
-        dst[1] = src[1];
-        dst[2] = src[2];
-        out.tile = tile;
-        out.head = head;
-        out.b0 = blk;
-        const int64_t left = end - at;
-        const int n = left < out.t.nblk - blk ? static_cast<int>(left) : out.t.nblk - blk;
-        out.b1 = blk + n;
-        out.whole = out.b0 == 0 && out.b1 == out.t.nblk;
-        out.slot = 2 * cta + (out.b0 > 0 ? 0 : 1);
-        const int64_t u0 = out.t.start + static_cast<int64_t>(head) * out.t.nblk;
-        out.first_cta = static_cast<int>(u0 / per);
-        out.last_cta = static_cast<int>((u0 + out.t.nblk - 1) / per);
-        at += n;
-        blk += n;
-        if (blk == out.t.nblk) {
-            blk = 0;
-            if (++head == p.Hk) {
-                head = 0;
-                ++tile;
+    // The next piece that has blocks; false when the CTA's share is done.
+    __device__ __forceinline__ bool next(const AttnParams& p, int cta, AttnPiece& out) {
+        while (at < end) {
+            const int lead = p.plan.lead, cost = t.nblk + lead;
+            const int64_t left = end - at;
+            const int n = left < cost - unit ? static_cast<int>(left) : cost - unit;
+            const int b0 = max(0, unit - lead), b1 = max(0, unit + n - lead);
+            out.q0 = t.q0;
+            out.seq = t.seq;
+            out.qlen = t.qlen;
+            out.kvlen = t.kvlen;
+            out.row0 = t.row0;
+            out.head = head;
+            out.blk = t.blk0 + b0;
+            out.nb = b1 - b0;
+            out.whole = b0 == 0 && b1 == t.nblk;
+            out.cnt = t.cnt + head;
+            out.slot = 2 * cta + (b0 > 0 ? 0 : 1);
+            const int64_t u0 = t.start + static_cast<int64_t>(head) * cost + lead;
+            out.first_cta = static_cast<int>(u0 / per);
+            out.last_cta = static_cast<int>((u0 + t.nblk - 1) / per);
+            at += n;
+            unit += n;
+            if (unit == cost) {
+                unit = 0;
+                if (++head == p.Hk) {
+                    head = 0;
+                    ++tile;
+                    if (at < end) t = attn_tiles(p)[tile];
+                }
             }
+            if (b1 > b0) return true;
         }
-        return true;
+        out.nb = 0;
+        return false;
     }
 };
 
-// Keys [lo, hi) that row r of a tile's sequence sees.
-__device__ __forceinline__ void attn_row_keys(const AttnTile& t, int r, int G, int window, int& lo, int& hi) {
+// Keys [lo, hi) that row r of the sequence sees.
+template <typename T>
+__device__ __forceinline__ void attn_row_keys(const T& t, int r, int G, int window, int& lo, int& hi) {
     const int pos = t.kvlen - t.qlen + r / G;
     hi = max(0, min(t.kvlen, pos + 1));
     lo = window > 0 ? max(0, pos - window + 1) : 0;
@@ -185,47 +201,80 @@ __device__ __forceinline__ float attn_lse(float m2, float l) {
     return l != 0.0f ? fmaf(m2, LN2, logf(l)) : -INFINITY;
 }
 
-// Joins the partial results of a tile (nthr threads, all of them after a
-// barrier that follows the last arrival): item i is 4 values of one row.
-template <typename TA>
-__device__ __forceinline__ void attn_join(const AttnParams& p, const AttnPiece& pc, int dp, int tid, int nthr) {
-    const int rows_left = pc.t.qlen * p.G - pc.t.row0;
-    const int rows = min(rows_left, p.plan.tile_rows);
-    const int d4 = p.Dh / 4, sr = p.plan.slot_rows;
-    for (int i = tid; i < rows * d4; i += nthr) {
-        const int row = i / d4, d = (i - row * d4) * 4;
-        float M = -INFINITY;
+// Joins the partial results of a tile (NW warps, all of them after a barrier
+// that follows the last arrival).  A warp takes R rows at a time, 4 values of a
+// row a lane, and walks the parts in order with a running maximum; the loads of
+// the rows and of two parts are in flight together.
+template <typename TA, int DP, int NW>
+__device__ __forceinline__ void attn_join(const AttnParams& p, const AttnPiece& pc, int tid) {
+    constexpr int LPR = DP < 128 ? DP / 4 : 32;   // lanes of a row
+    constexpr int NV = DP / 4 / LPR;              // pieces of 4 values a lane has of a row
+    constexpr int RW = 32 / LPR, R = 4;           // rows of a warp at once, times R
+    const int rows = min(pc.qlen * p.G - pc.row0, p.plan.tile_rows);
+    const int lane = tid & 31, sub = lane % LPR, sr = p.plan.slot_rows;
+    for (int r0 = (tid >> 5) * RW * R + lane / LPR; r0 - lane / LPR < rows; r0 += NW * RW * R) {
+        float M[R], l[R];
+        float4 a[R][NV];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            M[i] = -INFINITY;
+            l[i] = 0.0f;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) a[i][v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+#pragma unroll 2
         for (int c = pc.first_cta; c <= pc.last_cta; ++c) {
             const float* s = attn_slot(p, 2 * c + (c == pc.first_cta ? 1 : 0));
-            M = fmaxf(M, __ldcg(s + static_cast<int64_t>(sr) * dp + row));
-        }
-        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        float l = 0.0f;
-        if (M > -INFINITY) {
-            for (int c = pc.first_cta; c <= pc.last_cta; ++c) {
-                const float* s = attn_slot(p, 2 * c + (c == pc.first_cta ? 1 : 0));
-                const float w = ex2(__ldcg(s + static_cast<int64_t>(sr) * dp + row) - M);
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(s + static_cast<int64_t>(row) * dp + d));
-                l = fmaf(w, __ldcg(s + static_cast<int64_t>(sr) * (dp + 1) + row), l);
-                a.x = fmaf(w, v.x, a.x);
-                a.y = fmaf(w, v.y, a.y);
-                a.z = fmaf(w, v.z, a.z);
-                a.w = fmaf(w, v.w, a.w);
+            float pm[R], pl[R];
+            float4 pv[R][NV];
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int row = min(r0 + i * RW, rows - 1);
+                pm[i] = __ldcg(s + static_cast<int64_t>(sr) * DP + row);
+                pl[i] = __ldcg(s + static_cast<int64_t>(sr) * (DP + 1) + row);
+#pragma unroll
+                for (int v = 0; v < NV; ++v)
+                    pv[i][v] = __ldcg(reinterpret_cast<const float4*>(s + static_cast<int64_t>(row) * DP) + v * LPR + sub);
+            }
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const float top = fmaxf(M[i], pm[i]), base = top == -INFINITY ? 0.0f : top;
+                const float w0 = ex2(M[i] - base), w1 = ex2(pm[i] - base);
+                M[i] = top;
+                l[i] = fmaf(pl[i], w1, l[i] * w0);
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    a[i][v].x = fmaf(pv[i][v].x, w1, a[i][v].x * w0);
+                    a[i][v].y = fmaf(pv[i][v].y, w1, a[i][v].y * w0);
+                    a[i][v].z = fmaf(pv[i][v].z, w1, a[i][v].z * w0);
+                    a[i][v].w = fmaf(pv[i][v].w, w1, a[i][v].w * w0);
+                }
             }
         }
-        const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-        const int r = pc.t.row0 + row;
-        const int64_t out = (pc.t.q0 + r / p.G) * p.Hq + pc.head * p.G + r % p.G;
-        TA* o = static_cast<TA*>(p.o) + out * p.Dh + d;
-        if (sizeof(TA) == 2) {
-            const __nv_bfloat162 x = __floats2bfloat162_rn(a.x * inv, a.y * inv);
-            const __nv_bfloat162 y = __floats2bfloat162_rn(a.z * inv, a.w * inv);
-            *reinterpret_cast<uint2*>(o) = make_uint2(*reinterpret_cast<const uint32_t*>(&x),
-                                                      *reinterpret_cast<const uint32_t*>(&y));
-        } else {
-            *reinterpret_cast<float4*>(o) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int row = r0 + i * RW;
+            if (row >= rows) continue;
+            const float inv = l[i] != 0.0f ? 1.0f / l[i] : 0.0f;
+            const int r = pc.row0 + row;
+            const int64_t out = (pc.q0 + r / p.G) * p.Hq + pc.head * p.G + r % p.G;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const int d = (v * LPR + sub) * 4;
+                if (d >= p.Dh) continue;
+                TA* o = static_cast<TA*>(p.o) + out * p.Dh + d;
+                if (sizeof(TA) == 2) {
+                    const __nv_bfloat162 x = __floats2bfloat162_rn(a[i][v].x * inv, a[i][v].y * inv);
+                    const __nv_bfloat162 y = __floats2bfloat162_rn(a[i][v].z * inv, a[i][v].w * inv);
+                    *reinterpret_cast<uint2*>(o) = make_uint2(*reinterpret_cast<const uint32_t*>(&x),
+                                                              *reinterpret_cast<const uint32_t*>(&y));
+                } else {
+                    *reinterpret_cast<float4*>(o) = make_float4(a[i][v].x * inv, a[i][v].y * inv, a[i][v].z * inv,
+                                                                a[i][v].w * inv);
+                }
+            }
+            if (sub == 0 && p.lse != nullptr) p.lse[out] = attn_lse(M[i], l[i]);
         }
-        if (d == 0 && p.lse != nullptr) p.lse[out] = attn_lse(M, l);
     }
 }
 

@@ -56,8 +56,12 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();   // pre_tc.cu
 
 namespace attn_tc {
 
-constexpr int NTHREADS = 320;
-constexpr int LOAD_WARP = 8, MMA_WARP = 9;
+constexpr int NTHREADS = 384;
+constexpr int LOAD_WARP = 8, MMA_WARP = 9;   // warps 10 and 11 complete their warpgroup
+// A softmax thread holds a row's 128 scores: 208 registers, taken from the
+// third warpgroup.  256 * 208 + 128 * 88 = 384 * 168, the block's registers at
+// its launch.
+constexpr int SOFTMAX_REGS = 208, OTHER_REGS = 88;
 constexpr int ROWS = 128, KEYS = 128;
 constexpr int SUB = KEYS * 128;              // 128 rows x 64 columns: 16 KB
 constexpr int RING_BYTES = 160 * 1024;
@@ -67,19 +71,29 @@ constexpr uint64_t WAIT_LIMIT_NS = 1000000000ull;
 constexpr float RAISE = 8.0f;                // see above
 constexpr uint32_t FULL = 0xffffffffu;
 
+// A softmax warp's place in the work: in shared memory, so that the registers
+// are the scores'.
+struct State {
+    AttnWalk walk;
+    AttnPiece pc[2];
+};
+constexpr int STATE_BYTES = 224;
+static_assert(sizeof(State) <= STATE_BYTES, "see Cfg::TOTAL");
+
 template <int DP> struct Cfg {
     static constexpr int TILE = (DP / 64) * SUB;           // a block of keys, or 128 rows of queries
     static constexpr int STAGES = RING_BYTES / TILE;
     static constexpr int Q = 0;
     static constexpr int RING = 2 * TILE;
     static constexpr int BARS = RING + STAGES * TILE;
-    static constexpr int B_FULL = 0, B_EMPTY = STAGES, B_S = 2 * STAGES, B_P = B_S + 2, B_Q = B_P + 2, B_O = B_Q + 2;
+    static constexpr int B_FULL = 0, B_EMPTY = STAGES, B_S = 2 * STAGES, B_P = B_S + 2, B_Q = B_P + 4, B_O = B_Q + 2;
     static constexpr int NBARS = B_O + 2;
     static constexpr int MISC = BARS + ((8 * NBARS + 15) / 16) * 16;   // TMEM address, abort flag, last-CTA flag
     static constexpr int ML = MISC + 32;                               // lane 1's maxima and sums
-    static constexpr int TOTAL = ML + 2 * ROWS * 4;
-    static constexpr int SMEM = TOTAL + 1024;                          // the base is rounded up to 1024
-    static_assert(SMEM <= 232448, "shared memory of one SM");
+    static constexpr int STATE = ML + 2 * ROWS * 4;                    // the softmax warps' walks
+    static constexpr int TOTAL = STATE + 8 * STATE_BYTES;
+    static constexpr int SMEM = 232448;                                // all that a block may have
+    static_assert(TOTAL <= SMEM, "shared memory of one SM");
 };
 
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
@@ -102,11 +116,284 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatil
     return __all_sync(FULL, wait_bar(bar, parity, abort_flag));
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// 32 bytes in one store (32-byte aligned).
+__device__ __forceinline__ void st32(void* p, const uint4& a, const uint4& b) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z),
+                 "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+}
+
 // Keys that any row of the piece's tile sees.
 __device__ __forceinline__ void tile_keys(const AttnParams& p, const AttnPiece& pc, int& lo, int& hi) {
     int unused;
-    attn_row_keys(pc.t, pc.t.row0, p.G, p.window, lo, unused);
-    attn_row_keys(pc.t, min(pc.t.row0 + p.plan.tile_rows, pc.t.qlen * p.G) - 1, p.G, p.window, unused, hi);
+    attn_row_keys(pc, pc.row0, p.G, p.window, lo, unused);
+    attn_row_keys(pc, min(pc.row0 + p.plan.tile_rows, pc.qlen * p.G) - 1, p.G, p.window, unused, hi);
+}
+
+template <int DP, bool CAP>
+__device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char* smem, uint32_t sbase, uint32_t tmem) {
+    using C = Cfg<DP>;
+    auto bar = [&](int i) { return sbase + C::BARS + 8u * static_cast<uint32_t>(i); };
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC + 4);
+    volatile int* last_flag = reinterpret_cast<volatile int*>(smem + C::MISC + 8);
+    float* ml = reinterpret_cast<float*>(smem + C::ML);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
+    const int L = warp >> 2, w4 = warp & 3, row_t = w4 * 32 + lane;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(w4 * 32) << 16);
+    const uint32_t t_s = t_lane + S_COL + L * 128, t_o = t_lane + O_COL + L * 128;
+    const float zscale = CAP ? 1.0f : p.scale * LOG2E;
+    const float cap2 = p.softcap * LOG2E, cap_in = CAP ? 2.0f * LOG2E * p.scale / p.softcap : 0.0f;
+    // rows of 32-byte multiples at 32-byte addresses are stored 32 bytes at a time
+    const bool wide = p.Dh % 16 == 0 && (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0;
+    uint32_t par_s = 0, par_o = 0;
+    bool ok = true;
+
+    State* st = reinterpret_cast<State*>(smem + C::STATE + warp * STATE_BYTES);
+    auto is_pair = [&](const AttnPiece& pc) { return pc.qlen * p.G - pc.row0 > ROWS; };
+    auto first_row = [&](const AttnPiece& pc) { return pc.row0 + (is_pair(pc) ? L * ROWS : 0); };
+    auto has_rows = [&](const AttnPiece& pc) { return first_row(pc) + w4 * 32 < pc.qlen * p.G; };
+    // The lane's queries into its buffer (128-byte swizzle), asynchronously.
+    auto load_q = [&](const AttnPiece& pc) {
+        if (!has_rows(pc)) return;
+        constexpr int LPR = DP / 8, STEP = 32 / LPR;
+        const int c = lane % LPR, nrows = pc.qlen * p.G;
+        int r = first_row(pc) + w4 * 32 + lane / LPR;
+        int tok = r / p.G, g = r - tok * p.G;
+        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + pc.q0 * p.q_stride +
+                                 static_cast<int64_t>(pc.head) * p.G * p.Dh + c * 8;
+        for (int i = lane / LPR; i < 32; i += STEP, r += STEP) {
+            const int rt = w4 * 32 + i;
+            const bool there = r < nrows && c * 8 < p.Dh;
+            ptx::cp_async16(sbase + C::Q + L * C::TILE + (c >> 3) * SUB + rt * 128 + (((c & 7) ^ (rt & 7)) << 4),
+                            there ? q + tok * p.q_stride + g * p.Dh : static_cast<const __nv_bfloat16*>(p.q),
+                            there ? 16u : 0u);
+            g += STEP;
+            while (g >= p.G) {
+                g -= p.G;
+                ++tok;
+            }
+        }
+    };
+    auto q_ready = [&]() {
+        ptx::cp_async_wait_all();
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(C::B_Q + L));
+    };
+
+    // lane 0 walks, the warp reads
+    auto advance = [&](int which) {
+        if (lane == 0) st->walk.next(p, cta, st->pc[which]);
+        __syncwarp();
+        return st->pc[which].nb > 0;
+    };
+    if (lane == 0) st->walk.begin(p, cta);
+    int now = 0;
+    bool have = advance(0);
+    if (have) {
+        load_q(st->pc[0]);
+        q_ready();
+    }
+    while (have) {
+        const AttnPiece& pc = st->pc[now];
+        const bool pair = is_pair(pc), active = has_rows(pc);   // a warp without rows only keeps the protocol
+        const int mine = pair ? pc.nb : (pc.nb + 1 - L) / 2;    // blocks of this lane
+        const int r = first_row(pc) + row_t, blk = pc.blk;
+        const bool valid = r < pc.qlen * p.G;
+        int lo = 0, hi = 0x7fffffff;   // rows that are not there need no mask
+        if (valid) attn_row_keys(pc, r, p.G, p.window, lo, hi);
+        float m = -INFINITY, l = 0.0f;
+        for (int i = 0; ok && i < mine; ++i) {
+            const int k0 = (blk + (pair ? i : 2 * i + L)) * KEYS;
+            ok = wait_warp(bar(C::B_S + L), par_s, abort_flag);
+            par_s ^= 1;
+            if (!ok) break;
+            ptx::tc_fence_after();
+            if (active) {
+                uint32_t u[128];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) ptx::tmem_ld32(t_s + c * 32, u + c * 32);
+                ptx::tmem_wait_ld();
+                if (CAP) {
+                    // cap tanh(x) = cap - 2 cap / (e^2x + 1), in base 2
+#pragma unroll
+                    for (int e = 0; e < 128; ++e)
+                        u[e] = __float_as_uint(
+                            fmaf(-2.0f * cap2, fast_rcp(ex2(__uint_as_float(u[e]) * cap_in) + 1.0f), cap2));
+                }
+                if (__any_sync(FULL, k0 < lo || k0 + KEYS > hi)) {
+                    const int from = lo - k0, to = hi - k0;
+#pragma unroll
+                    for (int e = 0; e < 128; ++e)
+                        if (e < from || e >= to) u[e] = 0xff800000u;
+                }
+                float mx[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mx[e] = fmaxf(__uint_as_float(u[e]), __uint_as_float(u[4 + e]));
+#pragma unroll
+                for (int e = 8; e < 128; e += 8)
+#pragma unroll
+                    for (int f = 0; f < 4; ++f)
+                        mx[f] = max3(mx[f], __uint_as_float(u[e + f]), __uint_as_float(u[e + 4 + f]));
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * zscale;
+                const bool raise = top > m + RAISE || (m == -INFINITY && top > -INFINITY);
+                if (__any_sync(FULL, raise)) {
+                    // S of this block is complete, so every earlier MMA is: O stands still
+                    const float f = raise ? ex2(m - top) : 1.0f;
+                    if (raise) m = top;
+                    l *= f;
+                    if (i > 0) {
+#pragma unroll
+                        for (int c = 0; c < DP / 32; ++c) {
+                            uint32_t o[32];
+                            ptx::tmem_ld32(t_o + c * 32, o);
+                            ptx::tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            ptx::tmem_st32(t_o + c * 32, o);
+                        }
+                    }
+                }
+                const float base = m == -INFINITY ? 0.0f : m;
+                const float2 z2 = make_float2(zscale, zscale), b2 = make_float2(-base, -base);
+                float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const float2 x = __ffma2_rn(
+                            make_float2(__uint_as_float(u[64 * h + 2 * e]), __uint_as_float(u[64 * h + 2 * e + 1])), z2, b2);
+                        const float2 y = make_float2(ex2(x.x), ex2(x.y));
+                        sum[e & 1] = __fadd2_rn(sum[e & 1], y);
+                        const __nv_bfloat162 t = __floats2bfloat162_rn(y.x, y.y);
+                        pk[e] = *reinterpret_cast<const uint32_t*>(&t);
+                    }
+                    ptx::tmem_st32(t_s + h * 32, pk);
+                    ptx::tmem_wait_st();
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(bar(C::B_P + 2 * L + h));
+                }
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            } else {
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    ptx::mbar_arrive(bar(C::B_P + 2 * L));
+                    ptx::mbar_arrive(bar(C::B_P + 2 * L + 1));
+                }
+            }
+        }
+        // the lane's last scores are complete, so its query buffer is free: the
+        // next piece's queries come in under this one's last product
+        const bool more = advance(now ^ 1);
+        if (ok && more) load_q(st->pc[now ^ 1]);
+        if (ok && mine > 0) {
+            ok = wait_warp(bar(C::B_O + L), par_o, abort_flag);
+            par_o ^= 1;
+        }
+        if (!pair && L == 1) {
+            ml[row_t] = m;
+            ml[ROWS + row_t] = l;
+        }
+        if (ptx::named_bar_or(1, 256, !ok)) break;   // both lanes are complete, or both leave
+        ptx::tc_fence_after();
+        if (more) q_ready();   // the next scores overlap what follows
+        // the rows' sums: to the output if this is the whole tile, else to the
+        // workspace
+        if (active && (pair || L == 0)) {
+            float w0 = 1.0f, w1 = 0.0f;
+            if (!pair) {
+                const float m1 = ml[row_t], l1 = ml[ROWS + row_t];
+                const float M = fmaxf(m, m1), base = M == -INFINITY ? 0.0f : M;
+                w0 = ex2(m - base);
+                w1 = ex2(m1 - base);
+                m = M;
+                l = l * w0 + l1 * w1;
+            }
+            const float inv = pc.whole ? (l != 0.0f ? 1.0f / l : 0.0f) : 1.0f;
+            w0 *= inv;
+            w1 *= inv;
+            const int tok = r / p.G;
+            const int64_t out = valid ? (pc.q0 + tok) * p.Hq + pc.head * p.G + (r - tok * p.G) : 0;
+            const int rt = r - pc.row0;
+            float* part = attn_slot(p, pc.slot);
+#pragma unroll
+            for (int c = 0; c < DP / 32; ++c) {
+                uint32_t o[32];
+                ptx::tmem_ld32(t_o + c * 32, o);
+                ptx::tmem_wait_ld();
+                float f[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * w0;
+                if (!pair && pc.nb > 1) {
+                    ptx::tmem_ld32(t_o + 128 + c * 32, o);   // lane 1's
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) f[e] = fmaf(__uint_as_float(o[e]), w1, f[e]);
+                }
+                if (valid && pc.whole) {
+                    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + out * p.Dh + c * 32;
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        float t[2][8];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) t[e >> 3][e & 7] = f[16 * g + e];
+                        const uint4 x = Vec<__nv_bfloat16>::pack(t[0]), y = Vec<__nv_bfloat16>::pack(t[1]);
+                        if (wide) {
+                            if (c * 32 + g * 16 < p.Dh) st32(dst + g * 16, x, y);
+                        } else {
+                            if (c * 32 + g * 16 < p.Dh) *reinterpret_cast<uint4*>(dst + g * 16) = x;
+                            if (c * 32 + g * 16 + 8 < p.Dh) *reinterpret_cast<uint4*>(dst + g * 16 + 8) = y;
+                        }
+                    }
+                } else if (valid) {
+                    float* dst = part + static_cast<int64_t>(rt) * DP + c * 32;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+                        st32(dst + g * 8,
+                             make_uint4(__float_as_uint(f[8 * g]), __float_as_uint(f[8 * g + 1]),
+                                        __float_as_uint(f[8 * g + 2]), __float_as_uint(f[8 * g + 3])),
+                             make_uint4(__float_as_uint(f[8 * g + 4]), __float_as_uint(f[8 * g + 5]),
+                                        __float_as_uint(f[8 * g + 6]), __float_as_uint(f[8 * g + 7])));
+                }
+                __syncwarp();
+            }
+            if (valid) {
+                if (pc.whole) {
+                    if (p.lse != nullptr) p.lse[out] = attn_lse(m, l);
+                } else {
+                    part[static_cast<int64_t>(p.plan.slot_rows) * DP + rt] = m;
+                    part[static_cast<int64_t>(p.plan.slot_rows) * (DP + 1) + rt] = l;
+                }
+            }
+            __syncwarp();
+            ptx::tc_fence_before();
+        }
+        if (!pc.whole) __threadfence();
+        ptx::named_bar_sync(1, 256);   // O may be overwritten; partial rows are written
+        if (!pc.whole) {
+            if (tid == 0) {
+                int* count = attn_counts(p) + pc.cnt;
+                const int n = atomicAdd(count, 1);
+                const bool last = n == pc.last_cta - pc.first_cta;
+                if (last) *count = 0;   // back at zero for the next call with this plan
+                *last_flag = last;
+                __threadfence();
+            }
+            ptx::named_bar_sync(1, 256);
+            if (*last_flag) attn_join<__nv_bfloat16, DP, 8>(p, pc, tid);
+        }
+        have = more;
+        now ^= 1;
+    }
+    ptx::cp_async_wait_all();
 }
 
 template <int DP, bool CAP>
@@ -115,20 +402,21 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
                const AttnParams p) {
     using C = Cfg<DP>;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    unsigned char* smem = reinterpret_cast<unsigned char*>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    unsigned char* smem = smem_raw;
     const uint32_t sbase = ptx::smem_u32(smem);
     auto bar = [&](int i) { return sbase + C::BARS + 8u * static_cast<uint32_t>(i); };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC + 4);
-    volatile int* last_flag = reinterpret_cast<volatile int*>(smem + C::MISC + 8);
-    float* ml = reinterpret_cast<float*>(smem + C::ML);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
 
     if (p.force_timeout != 0u) {
         // test hook: one bounded wait that runs out before anything async starts
         if (tid == 0 && ptx::forced_wait_runs_out(sbase, 100000ull)) atomicOr(&g_attn_tc_error, ATTN_ERR_TIMEOUT);
         __syncthreads();
+        return;
+    }
+    if ((sbase & 1023u) != 0) {   // the swizzle needs it; dynamic shared memory starts there without static arrays
+        if (tid == 0) atomicOr(&g_attn_tc_error, ATTN_ERR_TIMEOUT);
         return;
     }
     if (tid == 0) {
@@ -138,7 +426,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(bar(C::B_S + i), 1);
-            ptx::mbar_init(bar(C::B_P + i), 4);
+            ptx::mbar_init(bar(C::B_P + 2 * i), 4);       // exponentials of the block's first 64 keys
+            ptx::mbar_init(bar(C::B_P + 2 * i + 1), 4);   // and of the other 64
             ptx::mbar_init(bar(C::B_Q + i), 4);
             ptx::mbar_init(bar(C::B_O + i), 1);
         }
@@ -160,10 +449,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
     AttnWalk walk;
     const bool agrees = attn_plan_agrees(p);
     if (!agrees && tid == 0) atomicOr(&g_attn_tc_error, ATTN_ERR_RANGE);
-    if (agrees && walk.begin(p, cta)) {
-        const int64_t per = attn_head(p)->per_cta;
+    const bool work = agrees && walk.begin(p, cta);
+    if (warp >= LOAD_WARP) {
+        ptx::regs_dec<OTHER_REGS>();
         AttnPiece pc;
-        if (warp == LOAD_WARP) {
+        if (work && warp == LOAD_WARP) {
             // ------------------------------------------------------ loads ---
             const uint64_t policy = ptx::policy_evict_normal();
             const int box = p.page_size < KEYS ? p.page_size : KEYS;      // keys of one TMA box
@@ -171,15 +461,15 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
             int stage = 0;
             uint32_t round = 0;
             bool ok = true;
-            while (ok && walk.next(p, cta, per, pc)) {
+            while (ok && walk.next(p, cta, pc)) {
                 int tlo, thi;
                 tile_keys(p, pc, tlo, thi);
-                const bool pair = pc.t.qlen * p.G - pc.t.row0 > ROWS;
-                const int nb = pc.b1 - pc.b0;
-                const int32_t* row = p.page_table + pc.t.seq * p.table_stride;
+                const bool pair = pc.qlen * p.G - pc.row0 > ROWS;
+                const int nb = pc.nb;
+                const int32_t* row = p.page_table + pc.seq * p.table_stride;
                 // lane i: the page of box i of a block, -1 where no row sees its keys
                 auto page_of = [&](int j) {
-                    const int key = (pc.t.blk0 + pc.b0 + j) * KEYS + lane * box;
+                    const int key = (pc.blk + j) * KEYS + lane * box;
                     if (j >= nb || lane >= boxes || key + box <= tlo || key >= thi) return -1;
                     const int pg = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
                     const int page = row[pg];
@@ -194,7 +484,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
                     if (lane == 0) ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(n * box * DP * 2));
                     __syncwarp();
                     if (page >= 0) {
-                        const int key = (pc.t.blk0 + pc.b0 + j) * KEYS + lane * box;
+                        const int key = (pc.blk + j) * KEYS + lane * box;
                         const int place = p.page_shift >= 0 ? key & (p.page_size - 1) : key % p.page_size;
 #pragma unroll
                         for (int c = 0; c < DP / 64; ++c)
@@ -220,7 +510,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
                     ahead = next;
                 }
             }
-        } else if (warp == MMA_WARP) {
+        } else if (work && warp == MMA_WARP) {
             // -------------------------------------------------------- MMA ---
             constexpr uint32_t IDESC_S = ptx::idesc_bf16_f32(ROWS, KEYS);
             constexpr uint32_t IDESC_O = ptx::idesc_bf16_f32(ROWS, DP) | (1u << 16);   // B (V) MN-major
@@ -249,43 +539,48 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
                     ptx::tc_commit(bar(C::B_S + L));
                 }
             };
+            // the exponentials come in two halves: the first 64 keys' product
+            // starts while the softmax still works on the others
             auto values = [&](int L, int s, bool add) {
-                if (lane == 0) {
-                    const uint64_t b = ptx::desc_add(desc_v, s * C::TILE);
+                const uint64_t b = ptx::desc_add(desc_v, s * C::TILE);
 #pragma unroll
-                    for (int k = 0; k < KEYS / 16; ++k)
-                        ptx::tc_mma_f16_ts(tmem + O_COL + L * 128, tmem + S_COL + L * 128 + k * 8,
-                                           ptx::desc_add(b, k * 2048), IDESC_O, add || k > 0);
+                for (int h = 0; h < 2; ++h) {
+                    ok = ok && wait_warp(bar(C::B_P + 2 * L + h), par_p[L], abort_flag);
+                    ptx::tc_fence_after();
+                    if (ok && lane == 0) {
+#pragma unroll
+                        for (int k = 4 * h; k < 4 * h + 4; ++k)
+                            ptx::tc_mma_f16_ts(tmem + O_COL + L * 128, tmem + S_COL + L * 128 + k * 8,
+                                               ptx::desc_add(b, k * 2048), IDESC_O, add || k > 0);
+                    }
                 }
+                par_p[L] ^= 1;
+                return ok;
             };
             auto commit = [&](int b) {
                 if (lane == 0) ptx::tc_commit(bar(b));
             };
-            while (ok && walk.next(p, cta, per, pc)) {
+            while (ok && walk.next(p, cta, pc)) {
                 int tlo, thi;
                 tile_keys(p, pc, tlo, thi);
-                const bool pair = pc.t.qlen * p.G - pc.t.row0 > ROWS;
-                const int nb = pc.b1 - pc.b0;
+                const bool pair = pc.qlen * p.G - pc.row0 > ROWS;
+                const int nb = pc.nb;
                 // value rows that no row of the tile sees become zeros
                 auto blank = [&](int s, int j) {
-                    const int k0 = (pc.t.blk0 + pc.b0 + j) * KEYS;
-                    if (k0 >= tlo && k0 + KEYS <= thi) return;
-                    for (int r = 0; r < KEYS; ++r) {
-                        if (k0 + r >= tlo && k0 + r < thi) continue;
-                        if (lane < DP / 8)
-                            *reinterpret_cast<uint4*>(smem + C::RING + s * C::TILE + (lane >> 3) * SUB + r * 128 +
-                                                      (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    const int k0 = (pc.blk + j) * KEYS;
+                    const int before = min(KEYS, max(0, tlo - k0)), from = max(before, min(KEYS, thi - k0));
+                    const int n = before + KEYS - from;   // rows [0, before) and [from, KEYS)
+                    if (n == 0) return;
+                    for (int e = lane; e < n * (DP / 8); e += 32) {
+                        const int i = e / (DP / 8), c = e % (DP / 8), r = i < before ? i : from + i - before;
+                        *reinterpret_cast<uint4*>(smem + C::RING + s * C::TILE + (c >> 3) * SUB + r * 128 +
+                                                  (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
                     }
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
                 };
                 ok = wait_warp(bar(C::B_Q + 0), par_q, abort_flag) && wait_warp(bar(C::B_Q + 1), par_q, abort_flag);
                 par_q ^= 1;
-                auto wait_p = [&](int L) {
-                    ok = ok && wait_warp(bar(C::B_P + L), par_p[L], abort_flag);
-                    par_p[L] ^= 1;
-                    ptx::tc_fence_after();
-                };
                 if (!ok) break;
                 ptx::tc_fence_after();
                 if (pair) {
@@ -299,9 +594,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
                         const int sv = take();
                         if (!ok) break;
                         blank(sv, j);
-                        wait_p(0);
-                        if (!ok) break;
-                        values(0, sv, j > 0);
+                        if (!values(0, sv, j > 0)) break;
                         if (more) {
                             sk = take();
                             if (!ok) break;
@@ -309,9 +602,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
                         } else {
                             commit(C::B_O + 0);
                         }
-                        wait_p(1);
-                        if (!ok) break;
-                        values(1, sv, j > 0);
+                        if (!values(1, sv, j > 0)) break;
                         commit(C::B_EMPTY + sv);
                         if (more) {
                             scores(1, sk);
@@ -332,9 +623,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
                         const int sv = take();
                         if (!ok) break;
                         blank(sv, j);
-                        wait_p(L);
-                        if (!ok) break;
-                        values(L, sv, j > 1);
+                        if (!values(L, sv, j > 1)) break;
                         commit(C::B_EMPTY + sv);
                         if (j + 2 < nb) {
                             const int sk = take();
@@ -347,201 +636,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
                     }
                 }
             }
-        } else {
-            // ---------------------------------------------------- softmax ---
-            const int L = warp >> 2, w4 = warp & 3, row_t = w4 * 32 + lane;
-            const uint32_t t_lane = tmem + (static_cast<uint32_t>(w4 * 32) << 16);
-            const uint32_t t_s = t_lane + S_COL + L * 128;
-            const float zscale = CAP ? 1.0f : p.scale * LOG2E;
-            const float cap2 = p.softcap * LOG2E, cap_in = CAP ? 2.0f * LOG2E * p.scale / p.softcap : 0.0f;
-            uint32_t par_s = 0, par_o = 0;
-            bool ok = true;
-            while (walk.next(p, cta, per, pc)) {
-                const int nrows = pc.t.qlen * p.G;
-                const bool pair = nrows - pc.t.row0 > ROWS;
-                const int nb = pc.b1 - pc.b0;
-                const int mine = pair ? nb : (nb + 1 - L) / 2;      // blocks of this lane
-                const int rbase = pc.t.row0 + (pair ? L * ROWS : 0);
-                const bool active = rbase + w4 * 32 < nrows;        // a warp without rows only keeps the protocol
-                // the lane's queries, 128-byte swizzle
-                if (active) {
-                    constexpr int LPR = DP / 8;
-                    for (int i = lane / LPR; i < 32; i += 32 / LPR) {
-                        const int rt = w4 * 32 + i, r = rbase + rt, c = lane % LPR;
-                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                        if (r < nrows && c * 8 < p.Dh)
-                            v = ld16(static_cast<const __nv_bfloat16*>(p.q) + (pc.t.q0 + r / p.G) * p.q_stride +
-                                     static_cast<int64_t>(pc.head * p.G + r % p.G) * p.Dh + c * 8);
-                        *reinterpret_cast<uint4*>(smem + C::Q + L * C::TILE + (c >> 3) * SUB + rt * 128 +
-                                                  (((c & 7) ^ (rt & 7)) << 4)) = v;
-                    }
-                }
-                ptx::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bar(C::B_Q + L));
-
-                const int r = rbase + row_t;
-                int lo = 0, hi = 0x7fffffff;   // rows that are not there need no mask
-                if (r < nrows) attn_row_keys(pc.t, r, p.G, p.window, lo, hi);
-                float m = -INFINITY, l = 0.0f;
-                for (int i = 0; ok && i < mine; ++i) {
-                    const int k0 = (pc.t.blk0 + pc.b0 + (pair ? i : 2 * i + L)) * KEYS;
-                    ok = wait_warp(bar(C::B_S + L), par_s, abort_flag);
-                    par_s ^= 1;
-                    if (!ok) break;
-                    ptx::tc_fence_after();
-                    if (active) {
-                        uint32_t u[128];
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) ptx::tmem_ld32(t_s + c * 32, u + c * 32);
-                        ptx::tmem_wait_ld();
-                        if (CAP) {
-#pragma unroll
-                            for (int e = 0; e < 128; ++e)
-                                u[e] = __float_as_uint(
-                                    fmaf(-2.0f * cap2, fast_rcp(ex2(__uint_as_float(u[e]) * cap_in) + 1.0f), cap2));
-                        }
-                        if (__any_sync(FULL, k0 < lo || k0 + KEYS > hi)) {
-                            const int a = lo - k0, b = hi - k0;
-#pragma unroll
-                            for (int e = 0; e < 128; ++e)
-                                if (e < a || e >= b) u[e] = 0xff800000u;
-                        }
-                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                        for (int e = 0; e < 128; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(u[e]));
-                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * zscale;
-                        const bool raise = top > m + RAISE || (m == -INFINITY && top > -INFINITY);
-                        if (__any_sync(FULL, raise)) {
-                            // S of this block is complete, so every earlier MMA is: O stands still
-                            const float f = raise ? ex2(m - top) : 1.0f;
-                            if (raise) m = top;
-                            l *= f;
-                            if (i > 0) {
-#pragma unroll
-                                for (int c = 0; c < DP / 32; ++c) {
-                                    uint32_t o[32];
-                                    ptx::tmem_ld32(t_lane + O_COL + L * 128 + c * 32, o);
-                                    ptx::tmem_wait_ld();
-#pragma unroll
-                                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                    ptx::tmem_st32(t_lane + O_COL + L * 128 + c * 32, o);
-                                }
-                            }
-                        }
-                        const float base = m == -INFINITY ? 0.0f : m;
-                        const float2 z2 = make_float2(zscale, zscale), b2 = make_float2(-base, -base);
-                        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t pk[32];
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const float2 x = __ffma2_rn(make_float2(__uint_as_float(u[64 * h + 2 * e]),
-                                                                        __uint_as_float(u[64 * h + 2 * e + 1])),
-                                                            z2, b2);
-                                const float2 y = make_float2(ex2(x.x), ex2(x.y));
-                                sum[e & 1] = __fadd2_rn(sum[e & 1], y);
-                                const __nv_bfloat162 t = __floats2bfloat162_rn(y.x, y.y);
-                                pk[e] = *reinterpret_cast<const uint32_t*>(&t);
-                            }
-                            ptx::tmem_st32(t_s + h * 32, pk);
-                        }
-                        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                        ptx::tmem_wait_st();
-                    }
-                    ptx::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(bar(C::B_P + L));
-                }
-                if (ok && mine > 0) {
-                    ok = wait_warp(bar(C::B_O + L), par_o, abort_flag);
-                    par_o ^= 1;
-                }
-                if (!pair && L == 1) {
-                    ml[row_t] = m;
-                    ml[ROWS + row_t] = l;
-                }
-                if (ptx::named_bar_or(1, 256, !ok)) break;   // both lanes are complete, or both leave
-                ptx::tc_fence_after();
-                // the rows' sums: to the output if this is the whole tile,
-                // else to the workspace
-                if (active && (pair || L == 0)) {
-                    float w0 = 1.0f, w1 = 0.0f;
-                    if (!pair) {
-                        const float m1 = ml[row_t], l1 = ml[ROWS + row_t];
-                        const float M = fmaxf(m, m1), base = M == -INFINITY ? 0.0f : M;
-                        w0 = ex2(m - base);
-                        w1 = ex2(m1 - base);
-                        m = M;
-                        l = l * w0 + l1 * w1;
-                    }
-                    const float inv = pc.whole ? (l != 0.0f ? 1.0f / l : 0.0f) : 1.0f;
-                    w0 *= inv;
-                    w1 *= inv;
-                    const bool valid = r < nrows;
-                    const int64_t out = valid ? (pc.t.q0 + r / p.G) * p.Hq + pc.head * p.G + r % p.G : 0;
-                    const int rt = r - pc.t.row0;
-                    float* part = attn_slot(p, pc.slot);
-#pragma unroll
-                    for (int c = 0; c < DP / 32; ++c) {
-                        uint32_t o[32];
-                        ptx::tmem_ld32(t_lane + O_COL + L * 128 + c * 32, o);
-                        ptx::tmem_wait_ld();
-                        float f[32];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * w0;
-                        if (!pair && nb > 1) {
-                            ptx::tmem_ld32(t_lane + O_COL + 128 + c * 32, o);
-                            ptx::tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) f[e] = fmaf(__uint_as_float(o[e]), w1, f[e]);
-                        }
-                        if (valid && pc.whole) {
-                            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + out * p.Dh + c * 32;
-#pragma unroll
-                            for (int g = 0; g < 4; ++g) {
-                                float t[8];
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) t[e] = f[8 * g + e];
-                                if (c * 32 + g * 8 < p.Dh)
-                                    *reinterpret_cast<uint4*>(dst + g * 8) = Vec<__nv_bfloat16>::pack(t);
-                            }
-                        } else if (valid) {
-#pragma unroll
-                            for (int g = 0; g < 8; ++g)
-                                *reinterpret_cast<float4*>(part + static_cast<int64_t>(rt) * DP + c * 32 + g * 4) =
-                                    make_float4(f[4 * g], f[4 * g + 1], f[4 * g + 2], f[4 * g + 3]);
-                        }
-                        __syncwarp();
-                    }
-                    if (valid) {
-                        if (pc.whole) {
-                            if (p.lse != nullptr) p.lse[out] = attn_lse(m, l);
-                        } else {
-                            part[static_cast<int64_t>(p.plan.slot_rows) * DP + rt] = m;
-                            part[static_cast<int64_t>(p.plan.slot_rows) * (DP + 1) + rt] = l;
-                        }
-                    }
-                    __syncwarp();
-                    ptx::tc_fence_before();
-                }
-                if (!pc.whole) __threadfence();
-                ptx::named_bar_sync(1, 256);   // O may be overwritten; partial rows are written
-                if (!pc.whole) {
-                    if (tid == 0) {
-                        int* count = attn_counts(p) + pc.t.cnt + pc.head;
-                        const int n = atomicAdd(count, 1);
-                        const bool last = n == pc.last_cta - pc.first_cta;
-                        if (last) *count = 0;   // back at zero for the next call with this plan
-                        *last_flag = last;
-                        __threadfence();
-                    }
-                    ptx::named_bar_sync(1, 256);
-                    if (*last_flag) attn_join<__nv_bfloat16>(p, pc, DP, tid, 256);
-                }
-            }
         }
+    } else {
+        ptx::regs_inc<SOFTMAX_REGS>();
+        if (work) softmax_lanes<DP, CAP>(p, smem, sbase, tmem);
     }
     __syncthreads();
     if (*abort_flag) {
