@@ -6,6 +6,7 @@
 //   * warp 8 loads: key and value blocks of 128 keys go through a ring of
 //     shared-memory stages, one TMA box per page and 64 columns (128-byte
 //     swizzle); the page numbers are read one block ahead.
+//   * warp 10 zeroes the value rows that no row of a tile sees (below).
 //   * warp 9 issues the MMAs: S = Q K^T (128 rows x 128 keys, both operands in
 //     shared memory) and O += P V with P read from tensor memory and V as it
 //     lies in the cache (keys along K, so no transposition anywhere).
@@ -57,7 +58,7 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();   // pre_tc.cu
 namespace attn_tc {
 
 constexpr int NTHREADS = 384;
-constexpr int LOAD_WARP = 8, MMA_WARP = 9;   // warps 10 and 11 complete their warpgroup
+constexpr int LOAD_WARP = 8, MMA_WARP = 9, BLANK_WARP = 10;   // warp 11 completes the warpgroup
 // A softmax thread holds a row's 128 scores: 208 registers, taken from the
 // third warpgroup.  256 * 208 + 128 * 88 = 384 * 168, the block's registers at
 // its launch.
@@ -87,7 +88,7 @@ template <int DP> struct Cfg {
     static constexpr int RING = 2 * TILE;
     static constexpr int BARS = RING + STAGES * TILE;
     static constexpr int B_FULL = 0, B_EMPTY = STAGES, B_S = 2 * STAGES, B_P = B_S + 2, B_Q = B_P + 4, B_O = B_Q + 2;
-    static constexpr int NBARS = B_O + 2;
+    static constexpr int B_ASK = B_O + 2, B_Z = B_ASK + 1, NBARS = B_Z + 1;
     static constexpr int MISC = BARS + ((8 * NBARS + 15) / 16) * 16;   // TMEM address, abort flag, last-CTA flag
     static constexpr int ML = MISC + 32;                               // lane 1's maxima and sums
     static constexpr int STATE = ML + 2 * ROWS * 4;                    // the softmax warps' walks
@@ -127,6 +128,9 @@ __device__ __forceinline__ void st32(void* p, const uint4& a, const uint4& b) {
                  "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
                  : "memory");
 }
+
+// Whether some of a block's keys lie outside [lo, hi).
+__device__ __forceinline__ bool partly_seen(int k0, int lo, int hi) { return k0 < lo || k0 + KEYS > hi; }
 
 // Keys that any row of the piece's tile sees.
 __device__ __forceinline__ void tile_keys(const AttnParams& p, const AttnPiece& pc, int& lo, int& hi) {
@@ -431,6 +435,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
             ptx::mbar_init(bar(C::B_Q + i), 4);
             ptx::mbar_init(bar(C::B_O + i), 1);
         }
+        ptx::mbar_init(bar(C::B_ASK), 1);
+        ptx::mbar_init(bar(C::B_Z), 1);
         *abort_flag = 0;
         ptx::fence_mbar_init();
         ptx::prefetch_tmap(&tmap_k);
@@ -510,34 +516,68 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
                     ahead = next;
                 }
             }
-        } else if (work && warp == MMA_WARP) {
+        } else if (work && warp == BLANK_WARP) {
+            // ---------------------------------------------------- blanks ---
+            // Value rows that no row of the tile sees become zeros before
+            // their product.  Only a tile's first and last block can have some.
+            uint32_t n = 0, par_a = 0;   // ring stages used by earlier pieces
+            bool ok = true;
+            while (ok && walk.next(p, cta, pc)) {
+                int tlo, thi;
+                tile_keys(p, pc, tlo, thi);
+                const bool pair = pc.qlen * p.G - pc.row0 > ROWS;
+                for (int j = 0; ok && j < pc.nb; j = j == 0 && pc.nb > 1 ? pc.nb - 1 : pc.nb) {
+                    const int k0 = (pc.blk + j) * KEYS;
+                    if (!partly_seen(k0, tlo, thi)) continue;
+                    // the loads' order: K0 V0 K1 V1 ... or K0 K1 V0 K2 V1 ...
+                    const uint32_t at = n + (pair || j == pc.nb - 1 ? 2 * j + 1 : 2 * j + 2);
+                    const int s = static_cast<int>(at % C::STAGES);
+                    // the MMA thread saw the stage full and asks: this warp meets
+                    // too few of the ring's stages to follow their parities itself
+                    ok = wait_warp(bar(C::B_ASK), par_a, abort_flag);
+                    par_a ^= 1;
+                    if (!ok) break;
+                    const int before = min(KEYS, max(0, tlo - k0)), from = max(before, min(KEYS, thi - k0));
+                    for (int e = lane; e < (before + KEYS - from) * (DP / 8); e += 32) {
+                        const int i = e / (DP / 8), c = e % (DP / 8), r = i < before ? i : from + i - before;
+                        *reinterpret_cast<uint4*>(smem + C::RING + s * C::TILE + (c >> 3) * SUB + r * 128 +
+                                                  (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(bar(C::B_Z));
+                }
+                n += 2u * static_cast<uint32_t>(pc.nb);
+            }
+        } else if (work && warp == MMA_WARP && lane == 0) {
             // -------------------------------------------------------- MMA ---
+            // One thread runs this loop alone: with votes and warp barriers in
+            // it the tensor core waited for its instructions (a 128x128x16 MMA
+            // lasts 64 cycles).
             constexpr uint32_t IDESC_S = ptx::idesc_bf16_f32(ROWS, KEYS);
             constexpr uint32_t IDESC_O = ptx::idesc_bf16_f32(ROWS, DP) | (1u << 16);   // B (V) MN-major
             const uint64_t desc_q = ptx::sw128_kmajor_desc(sbase + C::Q);
             const uint64_t desc_k = ptx::sw128_kmajor_desc(sbase + C::RING);
             const uint64_t desc_v = ptx::sw128_mnmajor_desc(sbase + C::RING, SUB, 1024);
             int stage = 0;
-            uint32_t round = 0, par_q = 0, par_p[2] = {0, 0};
+            uint32_t par_f = 0, par_q = 0, par_z = 0, par_p[2] = {0, 0};
             bool ok = true;
             auto take = [&]() {   // the ring's next stage, once it is full
                 const int s = stage;
-                ok = ok && wait_warp(bar(C::B_FULL + s), round & 1, abort_flag);
+                ok = ok && wait_bar(bar(C::B_FULL + s), par_f, abort_flag);
                 if (++stage == C::STAGES) {
                     stage = 0;
-                    ++round;
+                    par_f ^= 1;
                 }
                 return s;
             };
             auto scores = [&](int L, int s) {
-                if (lane == 0) {
-                    const uint64_t a = ptx::desc_add(desc_q, L * C::TILE), b = ptx::desc_add(desc_k, s * C::TILE);
+                const uint64_t a = ptx::desc_add(desc_q, L * C::TILE), b = ptx::desc_add(desc_k, s * C::TILE);
 #pragma unroll
-                    for (int k = 0; k < DP / 16; ++k)
-                        ptx::tc_mma_f16(tmem + S_COL + L * 128, ptx::desc_add(a, (k / 4) * SUB + (k % 4) * 32),
-                                        ptx::desc_add(b, (k / 4) * SUB + (k % 4) * 32), IDESC_S, k > 0);
-                    ptx::tc_commit(bar(C::B_S + L));
-                }
+                for (int k = 0; k < DP / 16; ++k)
+                    ptx::tc_mma_f16(tmem + S_COL + L * 128, ptx::desc_add(a, (k / 4) * SUB + (k % 4) * 32),
+                                    ptx::desc_add(b, (k / 4) * SUB + (k % 4) * 32), IDESC_S, k > 0);
+                ptx::tc_commit(bar(C::B_S + L));
             };
             // the exponentials come in two halves: the first 64 keys' product
             // starts while the softmax still works on the others
@@ -545,41 +585,33 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
                 const uint64_t b = ptx::desc_add(desc_v, s * C::TILE);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    ok = ok && wait_warp(bar(C::B_P + 2 * L + h), par_p[L], abort_flag);
+                    ok = ok && wait_bar(bar(C::B_P + 2 * L + h), par_p[L], abort_flag);
+                    if (!ok) return false;
                     ptx::tc_fence_after();
-                    if (ok && lane == 0) {
 #pragma unroll
-                        for (int k = 4 * h; k < 4 * h + 4; ++k)
-                            ptx::tc_mma_f16_ts(tmem + O_COL + L * 128, tmem + S_COL + L * 128 + k * 8,
-                                               ptx::desc_add(b, k * 2048), IDESC_O, add || k > 0);
-                    }
+                    for (int k = 4 * h; k < 4 * h + 4; ++k)
+                        ptx::tc_mma_f16_ts(tmem + O_COL + L * 128, tmem + S_COL + L * 128 + k * 8,
+                                           ptx::desc_add(b, k * 2048), IDESC_O, add || k > 0);
                 }
                 par_p[L] ^= 1;
-                return ok;
+                return true;
             };
-            auto commit = [&](int b) {
-                if (lane == 0) ptx::tc_commit(bar(b));
-            };
+            auto free_stage = [&](int s) { ptx::tc_commit(bar(C::B_EMPTY + s)); };
             while (ok && walk.next(p, cta, pc)) {
                 int tlo, thi;
                 tile_keys(p, pc, tlo, thi);
                 const bool pair = pc.qlen * p.G - pc.row0 > ROWS;
                 const int nb = pc.nb;
-                // value rows that no row of the tile sees become zeros
-                auto blank = [&](int s, int j) {
-                    const int k0 = (pc.blk + j) * KEYS;
-                    const int before = min(KEYS, max(0, tlo - k0)), from = max(before, min(KEYS, thi - k0));
-                    const int n = before + KEYS - from;   // rows [0, before) and [from, KEYS)
-                    if (n == 0) return;
-                    for (int e = lane; e < n * (DP / 8); e += 32) {
-                        const int i = e / (DP / 8), c = e % (DP / 8), r = i < before ? i : from + i - before;
-                        *reinterpret_cast<uint4*>(smem + C::RING + s * C::TILE + (c >> 3) * SUB + r * 128 +
-                                                  (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                const bool z0 = partly_seen(pc.blk * KEYS, tlo, thi);
+                const bool z1 = partly_seen((pc.blk + nb - 1) * KEYS, tlo, thi);
+                auto blanked = [&](int j) {
+                    if (ok && ((j == 0 && z0) || (j > 0 && j == nb - 1 && z1))) {
+                        ptx::mbar_arrive(bar(C::B_ASK));
+                        ok = wait_bar(bar(C::B_Z), par_z, abort_flag);
+                        par_z ^= 1;
                     }
-                    ptx::fence_proxy_async_smem();
-                    __syncwarp();
                 };
-                ok = wait_warp(bar(C::B_Q + 0), par_q, abort_flag) && wait_warp(bar(C::B_Q + 1), par_q, abort_flag);
+                ok = wait_bar(bar(C::B_Q + 0), par_q, abort_flag) && wait_bar(bar(C::B_Q + 1), par_q, abort_flag);
                 par_q ^= 1;
                 if (!ok) break;
                 ptx::tc_fence_after();
@@ -588,27 +620,26 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
                     if (!ok) break;
                     scores(0, sk);
                     scores(1, sk);
-                    commit(C::B_EMPTY + sk);
+                    free_stage(sk);
                     for (int j = 0; j < nb; ++j) {
                         const bool more = j + 1 < nb;
                         const int sv = take();
-                        if (!ok) break;
-                        blank(sv, j);
+                        blanked(j);
                         if (!values(0, sv, j > 0)) break;
                         if (more) {
                             sk = take();
                             if (!ok) break;
                             scores(0, sk);
                         } else {
-                            commit(C::B_O + 0);
+                            ptx::tc_commit(bar(C::B_O + 0));
                         }
                         if (!values(1, sv, j > 0)) break;
-                        commit(C::B_EMPTY + sv);
+                        free_stage(sv);
                         if (more) {
                             scores(1, sk);
-                            commit(C::B_EMPTY + sk);
+                            free_stage(sk);
                         } else {
-                            commit(C::B_O + 1);
+                            ptx::tc_commit(bar(C::B_O + 1));
                         }
                     }
                 } else {
@@ -616,22 +647,21 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
                         const int sk = take();
                         if (!ok) break;
                         scores(j, sk);
-                        commit(C::B_EMPTY + sk);
+                        free_stage(sk);
                     }
                     for (int j = 0; ok && j < nb; ++j) {
                         const int L = j & 1;
                         const int sv = take();
-                        if (!ok) break;
-                        blank(sv, j);
+                        blanked(j);
                         if (!values(L, sv, j > 1)) break;
-                        commit(C::B_EMPTY + sv);
+                        free_stage(sv);
                         if (j + 2 < nb) {
                             const int sk = take();
                             if (!ok) break;
                             scores(L, sk);
-                            commit(C::B_EMPTY + sk);
+                            free_stage(sk);
                         } else {
-                            commit(C::B_O + L);
+                            ptx::tc_commit(bar(C::B_O + L));
                         }
                     }
                 }
