@@ -549,13 +549,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
                 }
                 n += 2u * static_cast<uint32_t>(pc.nb);
             }
-        } else if (work && warp == MMA_WARP && lane == 0) {
+        } else if (work && warp == MMA_WARP) {
             // -------------------------------------------------------- MMA ---
-            // One thread runs this loop alone: with votes and warp barriers in
-            // it the tensor core waited for its instructions (a 128x128x16 MMA
-            // lasts 64 cycles).
+            // The warp runs this loop converged, on values that it knows to be
+            // the same in every lane, and one lane's instructions take effect.
             constexpr uint32_t IDESC_S = ptx::idesc_bf16_f32(ROWS, KEYS);
             constexpr uint32_t IDESC_O = ptx::idesc_bf16_f32(ROWS, DP) | (1u << 16);   // B (V) MN-major
+            const uint32_t on = ptx::elect_one();
+            const uint32_t tm = __shfl_sync(FULL, tmem, 0);
             const uint64_t desc_q = ptx::sw128_kmajor_desc(sbase + C::Q);
             const uint64_t desc_k = ptx::sw128_kmajor_desc(sbase + C::RING);
             const uint64_t desc_v = ptx::sw128_mnmajor_desc(sbase + C::RING, SUB, 1024);
@@ -564,7 +565,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
             bool ok = true;
             auto take = [&]() {   // the ring's next stage, once it is full
                 const int s = stage;
-                ok = ok && wait_bar(bar(C::B_FULL + s), par_f, abort_flag);
+                ok = ok && wait_warp(bar(C::B_FULL + s), par_f, abort_flag);
                 if (++stage == C::STAGES) {
                     stage = 0;
                     par_f ^= 1;
@@ -575,9 +576,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
                 const uint64_t a = ptx::desc_add(desc_q, L * C::TILE), b = ptx::desc_add(desc_k, s * C::TILE);
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k)
-                    ptx::tc_mma_f16(tmem + S_COL + L * 128, ptx::desc_add(a, (k / 4) * SUB + (k % 4) * 32),
+                    ptx::tc_mma_f16_if(on, tm + S_COL + L * 128, ptx::desc_add(a, (k / 4) * SUB + (k % 4) * 32),
                                     ptx::desc_add(b, (k / 4) * SUB + (k % 4) * 32), IDESC_S, k > 0);
-                ptx::tc_commit(bar(C::B_S + L));
+                ptx::tc_commit_if(on, bar(C::B_S + L));
             };
             // the exponentials come in two halves: the first 64 keys' product
             // starts while the softmax still works on the others
@@ -585,33 +586,33 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
                 const uint64_t b = ptx::desc_add(desc_v, s * C::TILE);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    ok = ok && wait_bar(bar(C::B_P + 2 * L + h), par_p[L], abort_flag);
+                    ok = ok && wait_warp(bar(C::B_P + 2 * L + h), par_p[L], abort_flag);
                     if (!ok) return false;
                     ptx::tc_fence_after();
 #pragma unroll
                     for (int k = 4 * h; k < 4 * h + 4; ++k)
-                        ptx::tc_mma_f16_ts(tmem + O_COL + L * 128, tmem + S_COL + L * 128 + k * 8,
+                        ptx::tc_mma_f16_ts_if(on, tm + O_COL + L * 128, tm + S_COL + L * 128 + k * 8,
                                            ptx::desc_add(b, k * 2048), IDESC_O, add || k > 0);
                 }
                 par_p[L] ^= 1;
                 return true;
             };
-            auto free_stage = [&](int s) { ptx::tc_commit(bar(C::B_EMPTY + s)); };
+            auto free_stage = [&](int s) { ptx::tc_commit_if(on, bar(C::B_EMPTY + s)); };
             while (ok && walk.next(p, cta, pc)) {
                 int tlo, thi;
                 tile_keys(p, pc, tlo, thi);
-                const bool pair = pc.qlen * p.G - pc.row0 > ROWS;
-                const int nb = pc.nb;
-                const bool z0 = partly_seen(pc.blk * KEYS, tlo, thi);
-                const bool z1 = partly_seen((pc.blk + nb - 1) * KEYS, tlo, thi);
+                const bool pair = __shfl_sync(FULL, pc.qlen * p.G - pc.row0, 0) > ROWS;
+                const int nb = __shfl_sync(FULL, pc.nb, 0);
+                const bool z0 = __all_sync(FULL, partly_seen(pc.blk * KEYS, tlo, thi));
+                const bool z1 = __all_sync(FULL, partly_seen((pc.blk + nb - 1) * KEYS, tlo, thi));
                 auto blanked = [&](int j) {
                     if (ok && ((j == 0 && z0) || (j > 0 && j == nb - 1 && z1))) {
-                        ptx::mbar_arrive(bar(C::B_ASK));
-                        ok = wait_bar(bar(C::B_Z), par_z, abort_flag);
+                        if (lane == 0) ptx::mbar_arrive(bar(C::B_ASK));
+                        ok = wait_warp(bar(C::B_Z), par_z, abort_flag);
                         par_z ^= 1;
                     }
                 };
-                ok = wait_bar(bar(C::B_Q + 0), par_q, abort_flag) && wait_bar(bar(C::B_Q + 1), par_q, abort_flag);
+                ok = wait_warp(bar(C::B_Q + 0), par_q, abort_flag) && wait_warp(bar(C::B_Q + 1), par_q, abort_flag);
                 par_q ^= 1;
                 if (!ok) break;
                 ptx::tc_fence_after();
@@ -631,7 +632,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
                             if (!ok) break;
                             scores(0, sk);
                         } else {
-                            ptx::tc_commit(bar(C::B_O + 0));
+                            ptx::tc_commit_if(on, bar(C::B_O + 0));
                         }
                         if (!values(1, sv, j > 0)) break;
                         free_stage(sv);
@@ -639,7 +640,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
                             scores(1, sk);
                             free_stage(sk);
                         } else {
-                            ptx::tc_commit(bar(C::B_O + 1));
+                            ptx::tc_commit_if(on, bar(C::B_O + 1));
                         }
                     }
                 } else {
@@ -661,7 +662,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
                             scores(L, sk);
                             free_stage(sk);
                         } else {
-                            ptx::tc_commit(bar(C::B_O + L));
+                            ptx::tc_commit_if(on, bar(C::B_O + L));
                         }
                     }
                 }
