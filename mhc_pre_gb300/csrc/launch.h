@@ -145,7 +145,7 @@ cudaError_t launch_attn_plan(const AttnPlan& plan, const int32_t* cu_q, const in
 cudaError_t launch_paged_attn(bool bf16, const AttnParams& p, cudaStream_t s);
 
 // On the tensor cores (paged_attn_tc.cu), where the types and sizes allow it.
-bool attn_tc_supports(bool bf16, int Dh, int page_size);
+bool attn_tc_supports(bool bf16, int Hq, int Hk, int Dh, int page_size);
 cudaError_t launch_paged_attn_tc(const AttnParams& p, cudaStream_t s);
 
 // Device error words of these kernels, read and cleared.

@@ -138,12 +138,13 @@ attn_plan_kernel(const PlanParams p) {
             if (on) {
                 tiles[ntiles + i] = t;
                 if (ntiles + i < PLAN_TILES) s_start[ntiles + i] = t.start;
-                for (int h = 0; h < p.Hk; ++h) counts[t.cnt + h] = 0;
             }
         }
         ntiles = static_cast<int>(min(static_cast<int64_t>(ntiles) + all, p.plan.max_tiles));
         __syncthreads();
     }
+    for (int64_t i = tid; i < static_cast<int64_t>(ntiles) * p.Hk * (JOINS / 4); i += PLAN_THREADS)
+        reinterpret_cast<int4*>(counts)[i] = make_int4(0, 0, 0, 0);
     int64_t per = (units + p.plan.ncta - 1) / p.plan.ncta;
     if (per < 1) per = 1;
     if (tid == 0) {
@@ -405,7 +406,10 @@ attn_cc_kernel(const AttnParams p) {
                 __threadfence();
             }
             __syncthreads();
-            if (s_last) attn_join<TA, DP, CC_THREADS / 32>(p, pc, tid);
+            if (s_last) {
+                const int rows = min(ROWS, nrows - pc.row0), each = (rows + 7) / 8, begin = (tid >> 5) * each;
+                attn_join<TA, DP, 4>(p, pc, begin, min(rows, begin + each), tid & 31);
+            }
         }
         __syncthreads();
     }
@@ -466,8 +470,9 @@ AttnPlan attn_plan_sizes(bool bf16, int64_t T, int B, int Hq, int Hk, int Dh, in
     AttnPlan a = {};
     const int64_t G = Hq / Hk;
     const int dp = Dh <= 64 ? 64 : Dh <= 128 ? 128 : 256;
-    if (attn_tc_supports(bf16, Dh, page_size)) {
-        a.tile_rows = max_q * G <= 128 ? 128 : 256;
+    if (attn_tc_supports(bf16, Hq, Hk, Dh, page_size)) {
+        a.lane_rows = static_cast<int>(128 / G * G);
+        a.tile_rows = (max_q * G <= a.lane_rows ? 1 : 2) * a.lane_rows;
         a.block_keys = 128;
         a.ncta = attn::sm_count();
     } else {
@@ -484,7 +489,7 @@ AttnPlan attn_plan_sizes(bool bf16, int64_t T, int B, int Hq, int Hk, int Dh, in
     a.start_off = 256;
     a.tile_off = a.start_off + attn::up(static_cast<size_t>(a.ncta) * sizeof(AttnStart));
     a.count_off = a.tile_off + attn::up(static_cast<size_t>(a.max_tiles) * sizeof(AttnTile));
-    a.part_off = a.count_off + attn::up(static_cast<size_t>(a.max_tiles) * Hk * sizeof(int));
+    a.part_off = a.count_off + attn::up(static_cast<size_t>(a.max_tiles) * Hk * JOINS * sizeof(int));
     a.part_slot_bytes = attn::up(static_cast<size_t>(a.slot_rows) * (dp + 2) * sizeof(float));
     a.total = a.part_off + 2u * static_cast<size_t>(a.ncta) * a.part_slot_bytes;
     return a;
@@ -510,7 +515,7 @@ cudaError_t launch_attn_plan(const AttnPlan& plan, const int32_t* cu_q, const in
 }
 
 cudaError_t launch_paged_attn(bool bf16, const AttnParams& p, cudaStream_t s) {
-    if (attn_tc_supports(bf16, p.Dh, p.page_size)) return launch_paged_attn_tc(p, s);
+    if (attn_tc_supports(bf16, p.Hq, p.Hk, p.Dh, p.page_size)) return launch_paged_attn_tc(p, s);
     return bf16 ? attn::launch_cc_dp<__nv_bfloat16>(p, s) : attn::launch_cc_dp<float>(p, s);
 }
 

@@ -27,6 +27,10 @@ namespace mhc {
 
 constexpr unsigned ATTN_ERR_TIMEOUT = 1u, ATTN_ERR_RANGE = 2u;
 
+// Join counters of a tile and key head: each warp's rows are joined by
+// themselves.
+constexpr int JOINS = 8;
+
 // One tile of rows of one sequence, for every key head.
 struct alignas(16) AttnTile {
     int64_t start;      // its first unit
@@ -35,7 +39,7 @@ struct alignas(16) AttnTile {
     int qlen, kvlen;    // new tokens; cached tokens including them
     int row0;           // first row of the tile in the sequence's list
     int blk0, nblk;     // key blocks that any of its rows sees
-    int cnt;            // index of its join counters (one per key head)
+    int cnt;            // index of its join counters (JOINS per key head)
     int pad;
 };
 static_assert(sizeof(AttnTile) == 48, "AttnTile is read as three 16-byte words");
@@ -54,6 +58,7 @@ static_assert(sizeof(AttnHead) <= 256, "the header has 256 bytes");
 struct AttnPlan {
     int ncta;           // CTAs of the launch
     int tile_rows, block_keys;
+    int lane_rows;      // rows of one softmax lane (tensor cores): whole tokens
     int lead;           // fixed cost of a tile, in blocks
     int slot_rows;      // rows a partial result can have
     int64_t max_tiles;
@@ -111,8 +116,8 @@ struct AttnPiece {
     int seq, qlen, kvlen, row0, head;
     int blk, nb;                // first key block and number of blocks (0: there is no piece)
     int whole;                  // the tile's only piece
-    int cnt, slot;              // join counter; where a partial result goes
-    int first_cta, last_cta;
+    int cnt, slot;              // join counters; where a partial result goes
+    int first_cta, last_cta;    // the CTAs with a part of the tile (unless whole)
 };
 static_assert(sizeof(AttnPiece) == 56, "two pieces and the walk fit the softmax warps' state");
 struct AttnWalk {
@@ -147,11 +152,13 @@ struct AttnWalk {
             out.blk = t.blk0 + b0;
             out.nb = b1 - b0;
             out.whole = b0 == 0 && b1 == t.nblk;
-            out.cnt = t.cnt + head;
+            out.cnt = (t.cnt + head) * JOINS;
             out.slot = 2 * cta + (b0 > 0 ? 0 : 1);
-            const int64_t u0 = t.start + static_cast<int64_t>(head) * cost + lead;
-            out.first_cta = static_cast<int>(u0 / per);
-            out.last_cta = static_cast<int>((u0 + t.nblk - 1) / per);
+            if (!out.whole) {
+                const int64_t u0 = t.start + static_cast<int64_t>(head) * cost + lead;
+                out.first_cta = static_cast<int>(u0 / per);
+                out.last_cta = static_cast<int>((u0 + t.nblk - 1) / per);
+            }
             at += n;
             unit += n;
             if (unit == cost) {
@@ -201,18 +208,17 @@ __device__ __forceinline__ float attn_lse(float m2, float l) {
     return l != 0.0f ? fmaf(m2, LN2, logf(l)) : -INFINITY;
 }
 
-// Joins the partial results of a tile (NW warps, all of them after a barrier
-// that follows the last arrival).  A warp takes R rows at a time, 4 values of a
-// row a lane, and walks the parts in order with a running maximum; the loads of
-// the rows and of two parts are in flight together.
-template <typename TA, int DP, int NW>
-__device__ __forceinline__ void attn_join(const AttnParams& p, const AttnPiece& pc, int tid) {
+// Joins the partial results of rows [begin, end) of a tile (one warp, after the
+// last part has arrived).  R rows at a time, 4 values of a row a lane, walking
+// the parts in order with a running maximum; the loads of the rows and of two
+// parts are in flight together.
+template <typename TA, int DP, int R>
+__device__ __forceinline__ void attn_join(const AttnParams& p, const AttnPiece& pc, int begin, int end, int lane) {
     constexpr int LPR = DP < 128 ? DP / 4 : 32;   // lanes of a row
     constexpr int NV = DP / 4 / LPR;              // pieces of 4 values a lane has of a row
-    constexpr int RW = 32 / LPR, R = 4;           // rows of a warp at once, times R
-    const int rows = min(pc.qlen * p.G - pc.row0, p.plan.tile_rows);
-    const int lane = tid & 31, sub = lane % LPR, sr = p.plan.slot_rows;
-    for (int r0 = (tid >> 5) * RW * R + lane / LPR; r0 - lane / LPR < rows; r0 += NW * RW * R) {
+    constexpr int RW = 32 / LPR;                  // rows side by side
+    const int sub = lane % LPR, sr = p.plan.slot_rows;
+    for (int r0 = begin; r0 < end; r0 += RW * R) {
         float M[R], l[R];
         float4 a[R][NV];
 #pragma unroll
@@ -229,7 +235,7 @@ __device__ __forceinline__ void attn_join(const AttnParams& p, const AttnPiece& 
             float4 pv[R][NV];
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                const int row = min(r0 + i * RW, rows - 1);
+                const int row = min(r0 + i * RW + lane / LPR, end - 1);
                 pm[i] = __ldcg(s + static_cast<int64_t>(sr) * DP + row);
                 pl[i] = __ldcg(s + static_cast<int64_t>(sr) * (DP + 1) + row);
 #pragma unroll
@@ -253,8 +259,8 @@ __device__ __forceinline__ void attn_join(const AttnParams& p, const AttnPiece& 
         }
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const int row = r0 + i * RW;
-            if (row >= rows) continue;
+            const int row = r0 + i * RW + lane / LPR;
+            if (row >= end) continue;
             const float inv = l[i] != 0.0f ? 1.0f / l[i] : 0.0f;
             const int r = pc.row0 + row;
             const int64_t out = (pc.q0 + r / p.G) * p.Hq + pc.head * p.G + r % p.G;

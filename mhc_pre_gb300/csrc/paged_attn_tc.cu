@@ -5,19 +5,22 @@
 // One CTA per SM walks the pieces of the plan (paged_attn.cuh).  Roles:
 //   * warp 8 loads: key and value blocks of 128 keys go through a ring of
 //     shared-memory stages, one TMA box per page and 64 columns (128-byte
-//     swizzle); the page numbers are read one block ahead.
-//   * warp 10 zeroes the value rows that no row of a tile sees (below).
+//     swizzle); the page numbers are read one block ahead.  Queries come by TMA
+//     too: a box of G heads x (128/G) tokens lies in shared memory in the order
+//     of the rows.
 //   * warp 9 issues the MMAs: S = Q K^T (128 rows x 128 keys, both operands in
 //     shared memory) and O += P V with P read from tensor memory and V as it
 //     lies in the cache (keys along K, so no transposition anywhere).
-//   * two groups of four warps run the softmax of one 128-row lane each, a
-//     thread per row: scores are read from tensor memory to registers, the
-//     row's maximum needs no exchange between threads, and the exponentials go
-//     back as bf16 over the scores they came from.  While one lane is in its
-//     softmax the tensor core works for the other.
-// A tile of more than 128 rows gives each lane its own 128 rows and both use
-// every key block.  A tile of at most 128 rows (decoding) gives both lanes the
-// same rows and every other key block; the lanes are joined at the end.
+//   * warp 10 zeroes the value rows that no row of a tile sees (below).
+//   * two lanes of four warps run the softmax of up to 128 rows each, a thread
+//     per row: scores are read from tensor memory to registers, the row's
+//     maximum needs no exchange between threads, and the exponentials go back
+//     as bf16 over the scores they came from.  While one lane is in its softmax
+//     the tensor core works for the other.
+// A tile of more rows than a lane has gives each lane its own rows and both
+// use every key block; the lanes never wait for each other.  A smaller tile
+// (decoding) gives both lanes the same rows and every other key block; lane 0
+// adds lane 1's sums to its own at the end.
 //
 // The running maximum is only raised when a row's new maximum exceeds it by
 // more than 2^8 in the exponentials' scale: float32 sums and bf16 exponentials
@@ -78,7 +81,7 @@ struct State {
     AttnWalk walk;
     AttnPiece pc[2];
 };
-constexpr int STATE_BYTES = 224;
+constexpr int STATE_BYTES = 208;
 static_assert(sizeof(State) <= STATE_BYTES, "see Cfg::TOTAL");
 
 template <int DP> struct Cfg {
@@ -87,10 +90,11 @@ template <int DP> struct Cfg {
     static constexpr int Q = 0;
     static constexpr int RING = 2 * TILE;
     static constexpr int BARS = RING + STAGES * TILE;
-    static constexpr int B_FULL = 0, B_EMPTY = STAGES, B_S = 2 * STAGES, B_P = B_S + 2, B_Q = B_P + 4, B_O = B_Q + 2;
-    static constexpr int B_ASK = B_O + 2, B_Z = B_ASK + 1, NBARS = B_Z + 1;
-    static constexpr int MISC = BARS + ((8 * NBARS + 15) / 16) * 16;   // TMEM address, abort flag, last-CTA flag
-    static constexpr int ML = MISC + 32;                               // lane 1's maxima and sums
+    static constexpr int B_FULL = 0, B_EMPTY = STAGES, B_S = 2 * STAGES, B_P = B_S + 2;
+    static constexpr int B_Q = B_P + 4, B_QE = B_Q + 2, B_O = B_QE + 2, B_ASK = B_O + 2, B_Z = B_ASK + 1;
+    static constexpr int B_X = B_Z + 1, B_XE = B_X + 4, NBARS = B_XE + 4;
+    static constexpr int MISC = BARS + ((8 * NBARS + 15) / 16) * 16;   // TMEM address, abort flag
+    static constexpr int ML = MISC + 16;                               // lane 1's maxima and sums
     static constexpr int STATE = ML + 2 * ROWS * 4;                    // the softmax warps' walks
     static constexpr int TOTAL = STATE + 8 * STATE_BYTES;
     static constexpr int SMEM = 232448;                                // all that a block may have
@@ -117,9 +121,24 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatil
     return __all_sync(FULL, wait_bar(bar, parity, abort_flag));
 }
 
+// Maxima; with NAN_TOO a NaN among the values is the result.
+template <bool NAN_TOO>
+__device__ __forceinline__ float max2(float a, float b) {
+    float r;
+    if (NAN_TOO) asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    else asm("max.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+template <bool NAN_TOO>
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    if (NAN_TOO) asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    else asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float rcp_ftz(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 // 32 bytes in one store (32-byte aligned).
@@ -139,14 +158,44 @@ __device__ __forceinline__ void tile_keys(const AttnParams& p, const AttnPiece& 
     attn_row_keys(pc, min(pc.row0 + p.plan.tile_rows, pc.qlen * p.G) - 1, p.G, p.window, unused, hi);
 }
 
+// Scores z = cap tanh(scale s / cap) of four values, in base 2:
+// tanh(x) = 1 - 2 / (e^2x + 1), the four quotients from one reciprocal of the
+// denominators' product.  Past 2^30 a denominator changes nothing in float32.
+__device__ __forceinline__ void cap4(uint32_t* u, float in, float cap2) {
+    float t[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) t[e] = ex2(fminf(__uint_as_float(u[e]) * in, 30.0f)) + 1.0f;
+    const float a = t[0] * t[1], b = t[2] * t[3];
+    const float r = rcp_ftz(a * b) * (-2.0f * cap2);
+    const float ra = r * b, rb = r * a;
+    u[0] = __float_as_uint(fmaf(ra, t[1], cap2));
+    u[1] = __float_as_uint(fmaf(ra, t[0], cap2));
+    u[2] = __float_as_uint(fmaf(rb, t[3], cap2));
+    u[3] = __float_as_uint(fmaf(rb, t[2], cap2));
+}
+
+// Scores of keys outside [from, to) of the block become -inf.  Most blocks
+// with a mask have it at one end only.
+__device__ __forceinline__ void mask_scores(uint32_t (&u)[128], bool head, bool tail, int from, int to) {
+    if (tail) {
+#pragma unroll
+        for (int e = 0; e < 128; ++e)
+            if (e >= to) u[e] = 0xff800000u;
+    }
+    if (head) {
+#pragma unroll
+        for (int e = 0; e < 128; ++e)
+            if (e < from) u[e] = 0xff800000u;
+    }
+}
+
 template <int DP, bool CAP>
 __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char* smem, uint32_t sbase, uint32_t tmem) {
     using C = Cfg<DP>;
     auto bar = [&](int i) { return sbase + C::BARS + 8u * static_cast<uint32_t>(i); };
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC + 4);
-    volatile int* last_flag = reinterpret_cast<volatile int*>(smem + C::MISC + 8);
     float* ml = reinterpret_cast<float*>(smem + C::ML);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
     const int L = warp >> 2, w4 = warp & 3, row_t = w4 * 32 + lane;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(w4 * 32) << 16);
     const uint32_t t_s = t_lane + S_COL + L * 128, t_o = t_lane + O_COL + L * 128;
@@ -154,42 +203,10 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
     const float cap2 = p.softcap * LOG2E, cap_in = CAP ? 2.0f * LOG2E * p.scale / p.softcap : 0.0f;
     // rows of 32-byte multiples at 32-byte addresses are stored 32 bytes at a time
     const bool wide = p.Dh % 16 == 0 && (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0;
-    uint32_t par_s = 0, par_o = 0;
-    bool ok = true;
+    uint32_t par_s = 0, par_o = 0, par_x = 0;
+    bool ok = true, lent = false;   // lane 1's sums are with lane 0
 
     State* st = reinterpret_cast<State*>(smem + C::STATE + warp * STATE_BYTES);
-    auto is_pair = [&](const AttnPiece& pc) { return pc.qlen * p.G - pc.row0 > ROWS; };
-    auto first_row = [&](const AttnPiece& pc) { return pc.row0 + (is_pair(pc) ? L * ROWS : 0); };
-    auto has_rows = [&](const AttnPiece& pc) { return first_row(pc) + w4 * 32 < pc.qlen * p.G; };
-    // The lane's queries into its buffer (128-byte swizzle), asynchronously.
-    auto load_q = [&](const AttnPiece& pc) {
-        if (!has_rows(pc)) return;
-        constexpr int LPR = DP / 8, STEP = 32 / LPR;
-        const int c = lane % LPR, nrows = pc.qlen * p.G;
-        int r = first_row(pc) + w4 * 32 + lane / LPR;
-        int tok = r / p.G, g = r - tok * p.G;
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + pc.q0 * p.q_stride +
-                                 static_cast<int64_t>(pc.head) * p.G * p.Dh + c * 8;
-        for (int i = lane / LPR; i < 32; i += STEP, r += STEP) {
-            const int rt = w4 * 32 + i;
-            const bool there = r < nrows && c * 8 < p.Dh;
-            ptx::cp_async16(sbase + C::Q + L * C::TILE + (c >> 3) * SUB + rt * 128 + (((c & 7) ^ (rt & 7)) << 4),
-                            there ? q + tok * p.q_stride + g * p.Dh : static_cast<const __nv_bfloat16*>(p.q),
-                            there ? 16u : 0u);
-            g += STEP;
-            while (g >= p.G) {
-                g -= p.G;
-                ++tok;
-            }
-        }
-    };
-    auto q_ready = [&]() {
-        ptx::cp_async_wait_all();
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(C::B_Q + L));
-    };
-
     // lane 0 walks, the warp reads
     auto advance = [&](int which) {
         if (lane == 0) st->walk.next(p, cta, st->pc[which]);
@@ -199,19 +216,24 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
     if (lane == 0) st->walk.begin(p, cta);
     int now = 0;
     bool have = advance(0);
-    if (have) {
-        load_q(st->pc[0]);
-        q_ready();
-    }
-    while (have) {
+    while (ok && have) {
         const AttnPiece& pc = st->pc[now];
-        const bool pair = is_pair(pc), active = has_rows(pc);   // a warp without rows only keeps the protocol
+        const int lane_rows = p.plan.lane_rows, nrows = pc.qlen * p.G;
+        const bool pair = nrows - pc.row0 > lane_rows;
         const int mine = pair ? pc.nb : (pc.nb + 1 - L) / 2;    // blocks of this lane
-        const int r = first_row(pc) + row_t, blk = pc.blk;
-        const bool valid = r < pc.qlen * p.G;
-        int lo = 0, hi = 0x7fffffff;   // rows that are not there need no mask
+        const int rt = (pair ? L * lane_rows : 0) + row_t;      // row of the tile
+        const int r = pc.row0 + rt, blk = pc.blk;
+        const bool valid = row_t < lane_rows && r < nrows;
+        const bool active = __any_sync(FULL, valid);            // a warp without rows only keeps the protocol
+        int lo = 0, hi = 0x7fffffff;                            // rows that are not there need no mask
         if (valid) attn_row_keys(pc, r, p.G, p.window, lo, hi);
         float m = -INFINITY, l = 0.0f;
+        if (lent) {
+            ok = wait_warp(bar(C::B_XE + w4), par_x, abort_flag);
+            par_x ^= 1;
+            lent = false;
+            ptx::tc_fence_after();
+        }
         for (int i = 0; ok && i < mine; ++i) {
             const int k0 = (blk + (pair ? i : 2 * i + L)) * KEYS;
             ok = wait_warp(bar(C::B_S + L), par_s, abort_flag);
@@ -223,29 +245,30 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
 #pragma unroll
                 for (int c = 0; c < 4; ++c) ptx::tmem_ld32(t_s + c * 32, u + c * 32);
                 ptx::tmem_wait_ld();
-                if (CAP) {
-                    // cap tanh(x) = cap - 2 cap / (e^2x + 1), in base 2
-#pragma unroll
-                    for (int e = 0; e < 128; ++e)
-                        u[e] = __float_as_uint(
-                            fmaf(-2.0f * cap2, fast_rcp(ex2(__uint_as_float(u[e]) * cap_in) + 1.0f), cap2));
-                }
-                if (__any_sync(FULL, k0 < lo || k0 + KEYS > hi)) {
-                    const int from = lo - k0, to = hi - k0;
-#pragma unroll
-                    for (int e = 0; e < 128; ++e)
-                        if (e < from || e >= to) u[e] = 0xff800000u;
-                }
+                const bool head = __any_sync(FULL, k0 < lo), tail = __any_sync(FULL, k0 + KEYS > hi);
+                if (head || tail) mask_scores(u, head, tail, lo - k0, hi - k0);
                 float mx[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) mx[e] = fmaxf(__uint_as_float(u[e]), __uint_as_float(u[4 + e]));
+                for (int e = 0; e < 4; ++e) mx[e] = max2<CAP>(__uint_as_float(u[e]), __uint_as_float(u[4 + e]));
 #pragma unroll
                 for (int e = 8; e < 128; e += 8)
 #pragma unroll
                     for (int f = 0; f < 4; ++f)
-                        mx[f] = max3(mx[f], __uint_as_float(u[e + f]), __uint_as_float(u[e + 4 + f]));
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * zscale;
-                const bool raise = top > m + RAISE || (m == -INFINITY && top > -INFINITY);
+                        mx[f] = max3<CAP>(mx[f], __uint_as_float(u[e + f]), __uint_as_float(u[e + 4 + f]));
+                float top = max2<CAP>(max2<CAP>(mx[0], mx[1]), max2<CAP>(mx[2], mx[3])) * zscale;
+                bool raise = top > m + RAISE || (m == -INFINITY && top > -INFINITY);
+                if (CAP) {
+                    // tanh keeps the order: the capped maximum is the maximum's.  A
+                    // score that is no number does not survive cap4; the maximum
+                    // has it, and the row's sums take it from there.
+                    uint32_t t[4] = {__float_as_uint(top), 0u, 0u, 0u};
+                    cap4(t, cap_in, cap2);
+                    if (top == top && top > -INFINITY) top = __uint_as_float(t[0]);
+                    raise = !(top <= m + RAISE) || (m == -INFINITY && top > -INFINITY);
+#pragma unroll
+                    for (int e = 0; e < 128; e += 4) cap4(u + e, cap_in, cap2);
+                    if (head || tail) mask_scores(u, head, tail, lo - k0, hi - k0);
+                }
                 if (__any_sync(FULL, raise)) {
                     // S of this block is complete, so every earlier MMA is: O stands still
                     const float f = raise ? ex2(m - top) : 1.0f;
@@ -294,26 +317,30 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
                 }
             }
         }
-        // the lane's last scores are complete, so its query buffer is free: the
-        // next piece's queries come in under this one's last product
-        const bool more = advance(now ^ 1);
-        if (ok && more) load_q(st->pc[now ^ 1]);
+        const bool more = advance(now ^ 1);   // under the last product
         if (ok && mine > 0) {
             ok = wait_warp(bar(C::B_O + L), par_o, abort_flag);
             par_o ^= 1;
         }
-        if (!pair && L == 1) {
+        if (!ok) break;
+        ptx::tc_fence_after();
+        if (active && !pair && L == 1) {
+            // warp w4 of lane 0 adds this warp's rows to its own
             ml[row_t] = m;
             ml[ROWS + row_t] = l;
-        }
-        if (ptx::named_bar_or(1, 256, !ok)) break;   // both lanes are complete, or both leave
-        ptx::tc_fence_after();
-        if (more) q_ready();   // the next scores overlap what follows
-        // the rows' sums: to the output if this is the whole tile, else to the
-        // workspace
-        if (active && (pair || L == 0)) {
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(C::B_X + w4));
+            lent = true;
+        } else if (active) {
+            // the rows' sums: to the output if this is the whole tile, else to
+            // the workspace
             float w0 = 1.0f, w1 = 0.0f;
             if (!pair) {
+                ok = wait_warp(bar(C::B_X + w4), par_x, abort_flag);
+                par_x ^= 1;
+                if (!ok) break;
+                ptx::tc_fence_after();
                 const float m1 = ml[row_t], l1 = ml[ROWS + row_t];
                 const float M = fmaxf(m, m1), base = M == -INFINITY ? 0.0f : M;
                 w0 = ex2(m - base);
@@ -321,13 +348,14 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
                 m = M;
                 l = l * w0 + l1 * w1;
             }
-            const float inv = pc.whole ? (l != 0.0f ? 1.0f / l : 0.0f) : 1.0f;
+            const bool whole = pc.whole != 0;
+            const float inv = whole ? (l != 0.0f ? 1.0f / l : 0.0f) : 1.0f;
             w0 *= inv;
             w1 *= inv;
             const int tok = r / p.G;
             const int64_t out = valid ? (pc.q0 + tok) * p.Hq + pc.head * p.G + (r - tok * p.G) : 0;
-            const int rt = r - pc.row0;
             float* part = attn_slot(p, pc.slot);
+            const bool both = !pair && pc.nb > 1;
 #pragma unroll
             for (int c = 0; c < DP / 32; ++c) {
                 uint32_t o[32];
@@ -336,13 +364,13 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
                 float f[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * w0;
-                if (!pair && pc.nb > 1) {
+                if (both) {
                     ptx::tmem_ld32(t_o + 128 + c * 32, o);   // lane 1's
                     ptx::tmem_wait_ld();
 #pragma unroll
                     for (int e = 0; e < 32; ++e) f[e] = fmaf(__uint_as_float(o[e]), w1, f[e]);
                 }
-                if (valid && pc.whole) {
+                if (valid && whole) {
                     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + out * p.Dh + c * 32;
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
@@ -369,41 +397,44 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
                 }
                 __syncwarp();
             }
-            if (valid) {
-                if (pc.whole) {
-                    if (p.lse != nullptr) p.lse[out] = attn_lse(m, l);
-                } else {
+            ptx::tc_fence_before();
+            if (!pair) {
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(C::B_XE + w4));
+            }
+            if (whole) {
+                if (valid && p.lse != nullptr) p.lse[out] = attn_lse(m, l);
+            } else {
+                if (valid) {
                     part[static_cast<int64_t>(p.plan.slot_rows) * DP + rt] = m;
                     part[static_cast<int64_t>(p.plan.slot_rows) * (DP + 1) + rt] = l;
                 }
-            }
-            __syncwarp();
-            ptx::tc_fence_before();
-        }
-        if (!pc.whole) __threadfence();
-        ptx::named_bar_sync(1, 256);   // O may be overwritten; partial rows are written
-        if (!pc.whole) {
-            if (tid == 0) {
-                int* count = attn_counts(p) + pc.cnt;
-                const int n = atomicAdd(count, 1);
-                const bool last = n == pc.last_cta - pc.first_cta;
-                if (last) *count = 0;   // back at zero for the next call with this plan
-                *last_flag = last;
+                // the same warp of the CTA that comes last joins these rows
                 __threadfence();
+                __syncwarp();
+                int last = 0;
+                if (lane == 0) {
+                    int* count = attn_counts(p) + pc.cnt + (pair ? L * 4 : 0) + w4;
+                    last = atomicAdd(count, 1) == pc.last_cta - pc.first_cta;
+                    if (last) *count = 0;   // back at zero for the next call with this plan
+                    __threadfence();
+                }
+                if (__shfl_sync(FULL, last, 0)) {
+                    const int begin = __shfl_sync(FULL, rt, 0), n = __popc(__ballot_sync(FULL, valid));
+                    attn_join<__nv_bfloat16, DP, 8>(p, pc, begin, begin + n, lane);
+                }
+                __syncwarp();
             }
-            ptx::named_bar_sync(1, 256);
-            if (*last_flag) attn_join<__nv_bfloat16, DP, 8>(p, pc, tid);
         }
         have = more;
         now ^= 1;
     }
-    ptx::cp_async_wait_all();
 }
 
 template <int DP, bool CAP>
 __global__ void __launch_bounds__(NTHREADS, 1)
-attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
-               const AttnParams p) {
+attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+               const __grid_constant__ CUtensorMap tmap_v, const AttnParams p) {
     using C = Cfg<DP>;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = smem_raw;
@@ -432,13 +463,19 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
             ptx::mbar_init(bar(C::B_S + i), 1);
             ptx::mbar_init(bar(C::B_P + 2 * i), 4);       // exponentials of the block's first 64 keys
             ptx::mbar_init(bar(C::B_P + 2 * i + 1), 4);   // and of the other 64
-            ptx::mbar_init(bar(C::B_Q + i), 4);
+            ptx::mbar_init(bar(C::B_Q + i), 1);
+            ptx::mbar_init(bar(C::B_QE + i), 1);
             ptx::mbar_init(bar(C::B_O + i), 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            ptx::mbar_init(bar(C::B_X + i), 1);    // lane 1's rows of warp i are final
+            ptx::mbar_init(bar(C::B_XE + i), 1);   // and have been taken
         }
         ptx::mbar_init(bar(C::B_ASK), 1);
         ptx::mbar_init(bar(C::B_Z), 1);
         *abort_flag = 0;
         ptx::fence_mbar_init();
+        ptx::prefetch_tmap(&tmap_q);
         ptx::prefetch_tmap(&tmap_k);
         ptx::prefetch_tmap(&tmap_v);
     }
@@ -465,12 +502,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
             const int box = p.page_size < KEYS ? p.page_size : KEYS;      // keys of one TMA box
             const int boxes = KEYS / box;                                 // of a block: at most 16
             int stage = 0;
-            uint32_t round = 0;
+            uint32_t round = 0, par_q = 1;
             bool ok = true;
             while (ok && walk.next(p, cta, pc)) {
                 int tlo, thi;
                 tile_keys(p, pc, tlo, thi);
-                const bool pair = pc.qlen * p.G - pc.row0 > ROWS;
+                const bool pair = pc.qlen * p.G - pc.row0 > p.plan.lane_rows;
                 const int nb = pc.nb;
                 const int32_t* row = p.page_table + pc.seq * p.table_stride;
                 // lane i: the page of box i of a block, -1 where no row sees its keys
@@ -506,7 +543,22 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
                 // in the order of use: K0 V0 K1 V1 ... for a pair of lanes on
                 // one block, K0 K1 V0 K2 V1 ... for lanes on alternate blocks
                 int page = page_of(0), ahead = page_of(1);
-                ok = load(&tmap_k, 0, page);
+                // each lane's queries, once its last scores have been formed
+                for (int L = 0; ok && L < 2; ++L) {
+                    ok = wait_warp(bar(C::B_QE + L), par_q, abort_flag);
+                    if (ok && lane == 0) {
+                        const uint32_t full = bar(C::B_Q + L);
+                        ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(p.plan.lane_rows * DP * 2));
+                        const int64_t tok = pc.q0 + (pc.row0 + (pair ? L * p.plan.lane_rows : 0)) / p.G;
+#pragma unroll
+                        for (int c = 0; c < DP / 64; ++c)
+                            ptx::tma_load_3d(sbase + C::Q + L * C::TILE + c * SUB, &tmap_q, c * 64, pc.head * p.G,
+                                             static_cast<int32_t>(tok), full, policy);
+                    }
+                    __syncwarp();
+                }
+                par_q ^= 1;
+                ok = ok && load(&tmap_k, 0, page);
                 for (int j = 0; ok && j < nb; ++j) {
                     const int next = page_of(j + 2);
                     if (!pair && j + 1 < nb) ok = load(&tmap_k, j + 1, ahead);
@@ -525,7 +577,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
             while (ok && walk.next(p, cta, pc)) {
                 int tlo, thi;
                 tile_keys(p, pc, tlo, thi);
-                const bool pair = pc.qlen * p.G - pc.row0 > ROWS;
+                const bool pair = pc.qlen * p.G - pc.row0 > p.plan.lane_rows;
                 for (int j = 0; ok && j < pc.nb; j = j == 0 && pc.nb > 1 ? pc.nb - 1 : pc.nb) {
                     const int k0 = (pc.blk + j) * KEYS;
                     if (!partly_seen(k0, tlo, thi)) continue;
@@ -601,7 +653,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
             while (ok && walk.next(p, cta, pc)) {
                 int tlo, thi;
                 tile_keys(p, pc, tlo, thi);
-                const bool pair = __shfl_sync(FULL, pc.qlen * p.G - pc.row0, 0) > ROWS;
+                const bool pair = __shfl_sync(FULL, pc.qlen * p.G - pc.row0, 0) > p.plan.lane_rows;
                 const int nb = __shfl_sync(FULL, pc.nb, 0);
                 const bool z0 = __all_sync(FULL, partly_seen(pc.blk * KEYS, tlo, thi));
                 const bool z1 = __all_sync(FULL, partly_seen((pc.blk + nb - 1) * KEYS, tlo, thi));
@@ -612,16 +664,21 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
                         par_z ^= 1;
                     }
                 };
-                ok = wait_warp(bar(C::B_Q + 0), par_q, abort_flag) && wait_warp(bar(C::B_Q + 1), par_q, abort_flag);
-                par_q ^= 1;
-                if (!ok) break;
-                ptx::tc_fence_after();
+                auto queries = [&](int L) { ok = ok && wait_warp(bar(C::B_Q + L), par_q, abort_flag); };
+                auto free_queries = [&](int L) { ptx::tc_commit_if(on, bar(C::B_QE + L)); };
                 if (pair) {
                     int sk = take();
+                    queries(0);
                     if (!ok) break;
                     scores(0, sk);
+                    queries(1);
+                    if (!ok) break;
                     scores(1, sk);
                     free_stage(sk);
+                    if (nb == 1) {
+                        free_queries(0);
+                        free_queries(1);
+                    }
                     for (int j = 0; j < nb; ++j) {
                         const bool more = j + 1 < nb;
                         const int sv = take();
@@ -631,6 +688,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
                             sk = take();
                             if (!ok) break;
                             scores(0, sk);
+                            if (j + 2 == nb) free_queries(0);
                         } else {
                             ptx::tc_commit_if(on, bar(C::B_O + 0));
                         }
@@ -639,16 +697,21 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
                         if (more) {
                             scores(1, sk);
                             free_stage(sk);
+                            if (j + 2 == nb) free_queries(1);
                         } else {
                             ptx::tc_commit_if(on, bar(C::B_O + 1));
                         }
                     }
                 } else {
-                    for (int j = 0; j < 2 && j < nb; ++j) {
-                        const int sk = take();
-                        if (!ok) break;
-                        scores(j, sk);
-                        free_stage(sk);
+                    for (int j = 0; ok && j < 2; ++j) {
+                        queries(j);
+                        if (j < nb) {
+                            const int sk = take();
+                            if (!ok) break;
+                            scores(j, sk);
+                            free_stage(sk);
+                        }
+                        if (j + 2 >= nb) free_queries(j);
                     }
                     for (int j = 0; ok && j < nb; ++j) {
                         const int L = j & 1;
@@ -661,11 +724,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
                             if (!ok) break;
                             scores(L, sk);
                             free_stage(sk);
+                            if (j + 4 >= nb) free_queries(L);
                         } else {
                             ptx::tc_commit_if(on, bar(C::B_O + L));
                         }
                     }
                 }
+                par_q ^= 1;
             }
         }
     } else {
@@ -687,6 +752,20 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
 
 // ------------------------------------------------------------------ host ---
 
+cudaError_t encode_q(PFN_cuTensorMapEncodeTiled_v12000 fn, CUtensorMap* tm, const AttnParams& p) {
+    // (d, head, token); a box is 64 columns x G heads x as many whole tokens as a lane has rows for
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.Dh), static_cast<cuuint64_t>(p.Hq),
+                                static_cast<cuuint64_t>(p.T)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(p.Dh) * 2, static_cast<cuuint64_t>(p.q_stride) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(p.G), static_cast<cuuint32_t>(p.plan.lane_rows / p.G)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p.q), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+
 cudaError_t encode(PFN_cuTensorMapEncodeTiled_v12000 fn, CUtensorMap* tm, const void* cache, const AttnParams& p,
                    int64_t page_stride, int64_t slot_stride, int64_t head_stride) {
     // (d, place, head, page); a box is 64 columns x (a page or 128 places)
@@ -704,7 +783,7 @@ cudaError_t encode(PFN_cuTensorMapEncodeTiled_v12000 fn, CUtensorMap* tm, const 
 }
 
 template <int DP, bool CAP>
-cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const AttnParams& p, cudaStream_t s) {
+cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const AttnParams& p, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};   // devices whose kernel has its shared memory allowed
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -725,26 +804,28 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const AttnParam
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_tc_kernel<DP, CAP>, tk, tv, p);
+    return cudaLaunchKernelEx(&cfg, attn_tc_kernel<DP, CAP>, tq, tk, tv, p);
 }
 
 }  // namespace attn_tc
 
-// Boxes of 8 or more whole swizzle rows that tile a block of 128 keys.
-bool attn_tc_supports(bool bf16, int Dh, int page_size) {
-    return bf16 && Dh <= 128 && page_size >= 8 && (128 % page_size == 0 || page_size % 128 == 0);
+// Boxes of 8 or more whole swizzle rows that tile a block of 128 keys, and a
+// token's query heads of one key head within a lane's rows.
+bool attn_tc_supports(bool bf16, int Hq, int Hk, int Dh, int page_size) {
+    return bf16 && Hq / Hk <= 128 && Dh <= 128 && page_size >= 8 && (128 % page_size == 0 || page_size % 128 == 0);
 }
 
 cudaError_t launch_paged_attn_tc(const AttnParams& p, cudaStream_t s) {
     auto fn = tensor_map_encoder();
     if (fn == nullptr) return cudaErrorNotSupported;
-    CUtensorMap tk, tv;
-    cudaError_t e = attn_tc::encode(fn, &tk, p.k_cache, p, p.k_page_stride, p.k_slot_stride, p.k_head_stride);
+    CUtensorMap tq, tk, tv;
+    cudaError_t e = attn_tc::encode_q(fn, &tq, p);
+    if (e == cudaSuccess) e = attn_tc::encode(fn, &tk, p.k_cache, p, p.k_page_stride, p.k_slot_stride, p.k_head_stride);
     if (e == cudaSuccess) e = attn_tc::encode(fn, &tv, p.v_cache, p, p.v_page_stride, p.v_slot_stride, p.v_head_stride);
     if (e != cudaSuccess) return e;
     if (p.Dh <= 64)
-        return p.softcap > 0.0f ? attn_tc::launch<64, true>(tk, tv, p, s) : attn_tc::launch<64, false>(tk, tv, p, s);
-    return p.softcap > 0.0f ? attn_tc::launch<128, true>(tk, tv, p, s) : attn_tc::launch<128, false>(tk, tv, p, s);
+        return p.softcap > 0.0f ? attn_tc::launch<64, true>(tq, tk, tv, p, s) : attn_tc::launch<64, false>(tq, tk, tv, p, s);
+    return p.softcap > 0.0f ? attn_tc::launch<128, true>(tq, tk, tv, p, s) : attn_tc::launch<128, false>(tq, tk, tv, p, s);
 }
 
 }  // namespace mhc
