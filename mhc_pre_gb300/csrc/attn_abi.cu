@@ -316,6 +316,12 @@ mhc_status mhc_paged_attn(mhc_dtype dt, const void* q, int64_t q_stride, const v
     for (int i = 0; i < 21; ++i)
         if (page_size == (1 << i)) p.page_shift = i;
     p.window = window;
+    if (p.G > 1) {   // M = floor(2^(31+s) / G) + 1, 2^s >= G: exact below 2^31
+        unsigned sh = 1;
+        while ((1 << sh) < p.G) ++sh;
+        p.g_mul = static_cast<unsigned>((uint64_t(1) << (31 + sh)) / static_cast<unsigned>(p.G)) + 1u;
+        p.g_shift = sh - 1;
+    }
     p.scale = scale;
     p.softcap = softcap;
     p.force_timeout = mhc::forced_timeout();

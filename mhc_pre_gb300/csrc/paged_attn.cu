@@ -125,8 +125,8 @@ attn_plan_kernel(const PlanParams p) {
                 t.row0 = (i - tile_base[lo]) * TR;
                 const int last = min(t.row0 + TR, t.qlen * p.G) - 1;
                 int lo_k, hi_k, unused;
-                attn_row_keys(t, t.row0, p.G, p.window, lo_k, unused);
-                attn_row_keys(t, last, p.G, p.window, unused, hi_k);
+                attn_token_keys(t, t.row0 / p.G, p.window, lo_k, unused);
+                attn_token_keys(t, last / p.G, p.window, unused, hi_k);
                 // rows that see nothing still get their zeros written: one masked block
                 t.blk0 = hi_k > lo_k ? lo_k / BN : 0;
                 t.nblk = hi_k > lo_k ? (hi_k + BN - 1) / BN - t.blk0 : 1;
@@ -237,9 +237,11 @@ attn_cc_kernel(const AttnParams p) {
         for (int i = tid; i < ROWS * (DP / 4); i += CC_THREADS) {
             const int row = i / (DP / 4), d = (i - row * (DP / 4)) * 4, r = pc.row0 + row;
             float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (r < nrows && d < p.Dh)
-                v = ld4(static_cast<const TA*>(p.q) + (pc.q0 + r / p.G) * p.q_stride +
-                        static_cast<int64_t>(pc.head * p.G + r % p.G) * p.Dh + d);
+            if (r < nrows && d < p.Dh) {
+                const int tok = attn_token(p, r);
+                v = ld4(static_cast<const TA*>(p.q) + (pc.q0 + tok) * p.q_stride +
+                        static_cast<int64_t>(pc.head * p.G + r - tok * p.G) * p.Dh + d);
+            }
             *reinterpret_cast<float4*>(Qs + row * PITCH + d) = v;
         }
         int lo[RPT], hi[RPT];
@@ -248,7 +250,7 @@ attn_cc_kernel(const AttnParams p) {
         for (int a = 0; a < RPT; ++a) {
             const int r = pc.row0 + ty * RPT + a;
             lo[a] = hi[a] = 0;
-            if (r < nrows) attn_row_keys(pc, r, p.G, p.window, lo[a], hi[a]);
+            if (r < nrows) attn_token_keys(pc, attn_token(p, r), p.window, lo[a], hi[a]);
             m[a] = -INFINITY;
             l[a] = 0.0f;
 #pragma unroll
@@ -256,9 +258,7 @@ attn_cc_kernel(const AttnParams p) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[a][c][e] = 0.0f;
         }
-        int tlo, thi, unused;
-        attn_row_keys(pc, pc.row0, p.G, p.window, tlo, unused);
-        attn_row_keys(pc, min(pc.row0 + ROWS, nrows) - 1, p.G, p.window, unused, thi);
+        const int tlo = pc.lo, thi = pc.hi;
         for (int b = 0; b < pc.nb; ++b) {
             const int k0 = (pc.blk + b) * CC_KEYS;
             __syncthreads();
@@ -362,7 +362,8 @@ attn_cc_kernel(const AttnParams p) {
                 const int r = pc.row0 + ty * RPT + a;
                 if (r >= nrows) continue;
                 const float inv = l[a] != 0.0f ? 1.0f / l[a] : 0.0f;
-                const int64_t out = (pc.q0 + r / p.G) * p.Hq + pc.head * p.G + r % p.G;
+                const int tok = attn_token(p, r);
+                const int64_t out = (pc.q0 + tok) * p.Hq + pc.head * p.G + (r - tok * p.G);
                 TA* o = static_cast<TA*>(p.o) + out * p.Dh;
 #pragma unroll
                 for (int c = 0; c < NC; ++c) {

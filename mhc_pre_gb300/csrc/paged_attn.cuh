@@ -76,6 +76,7 @@ struct AttnParams {
     int64_t v_page_stride, v_slot_stride, v_head_stride;
     int64_t T;
     int B, Hq, Hk, G, Dh, page_size, page_shift, window;
+    unsigned g_mul, g_shift;       // r / G = umulhi(r, g_mul) >> g_shift for 0 <= r < 2^31
     float scale, softcap;
     unsigned force_timeout;
     AttnPlan plan;
@@ -110,6 +111,19 @@ __device__ __forceinline__ bool attn_plan_agrees(const AttnParams& p) {
            h->lead == p.plan.lead && h->ntiles >= 0 && h->ntiles <= p.plan.max_tiles && h->per_cta > 0;
 }
 
+// The token of row r.
+__device__ __forceinline__ int attn_token(const AttnParams& p, int r) {
+    return p.G == 1 ? r : static_cast<int>(__umulhi(static_cast<unsigned>(r), p.g_mul) >> p.g_shift);
+}
+
+// Keys [lo, hi) that token i of the sequence's new ones sees.
+template <typename T>
+__device__ __forceinline__ void attn_token_keys(const T& t, int i, int window, int& lo, int& hi) {
+    const int pos = t.kvlen - t.qlen + i;
+    hi = max(0, min(t.kvlen, pos + 1));
+    lo = window > 0 ? max(0, pos - window + 1) : 0;
+}
+
 // A CTA's pieces one after the other.
 struct AttnPiece {
     int64_t q0;
@@ -118,8 +132,8 @@ struct AttnPiece {
     int whole;                  // the tile's only piece
     int cnt, slot;              // join counters; where a partial result goes
     int first_cta, last_cta;    // the CTAs with a part of the tile (unless whole)
+    int lo, hi;                 // keys [lo, hi) that any row of the tile sees
 };
-static_assert(sizeof(AttnPiece) == 56, "two pieces and the walk fit the softmax warps' state");
 struct AttnWalk {
     int64_t at, end, per;
     int tile, head, unit;
@@ -152,6 +166,9 @@ struct AttnWalk {
             out.blk = t.blk0 + b0;
             out.nb = b1 - b0;
             out.whole = b0 == 0 && b1 == t.nblk;
+            int unused;
+            attn_token_keys(t, attn_token(p, t.row0), p.window, out.lo, unused);
+            attn_token_keys(t, attn_token(p, min(t.row0 + p.plan.tile_rows, t.qlen * p.G) - 1), p.window, unused, out.hi);
             out.cnt = (t.cnt + head) * JOINS;
             out.slot = 2 * cta + (b0 > 0 ? 0 : 1);
             if (!out.whole) {
@@ -175,14 +192,6 @@ struct AttnWalk {
         return false;
     }
 };
-
-// Keys [lo, hi) that row r of the sequence sees.
-template <typename T>
-__device__ __forceinline__ void attn_row_keys(const T& t, int r, int G, int window, int& lo, int& hi) {
-    const int pos = t.kvlen - t.qlen + r / G;
-    hi = max(0, min(t.kvlen, pos + 1));
-    lo = window > 0 ? max(0, pos - window + 1) : 0;
-}
 
 // Partial result of one piece: rows of `dp` sums, then the maxima (in the
 // scores' own unit times log2 e), then the sums of the exponentials.
@@ -262,8 +271,8 @@ __device__ __forceinline__ void attn_join(const AttnParams& p, const AttnPiece& 
             const int row = r0 + i * RW + lane / LPR;
             if (row >= end) continue;
             const float inv = l[i] != 0.0f ? 1.0f / l[i] : 0.0f;
-            const int r = pc.row0 + row;
-            const int64_t out = (pc.q0 + r / p.G) * p.Hq + pc.head * p.G + r % p.G;
+            const int r = pc.row0 + row, tok = attn_token(p, r);
+            const int64_t out = (pc.q0 + tok) * p.Hq + pc.head * p.G + (r - tok * p.G);
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
                 const int d = (v * LPR + sub) * 4;

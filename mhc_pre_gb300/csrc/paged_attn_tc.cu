@@ -12,6 +12,7 @@
 //     shared memory) and O += P V with P read from tensor memory and V as it
 //     lies in the cache (keys along K, so no transposition anywhere).
 //   * warp 10 zeroes the value rows that no row of a tile sees (below).
+//   * warp 11 walks the plan and hands the pieces to the others, a few ahead.
 //   * two lanes of four warps run the softmax of up to 128 rows each, a thread
 //     per row: scores are read from tensor memory to registers, the row's
 //     maximum needs no exchange between threads, and the exponentials go back
@@ -61,7 +62,7 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();   // pre_tc.cu
 namespace attn_tc {
 
 constexpr int NTHREADS = 384;
-constexpr int LOAD_WARP = 8, MMA_WARP = 9, BLANK_WARP = 10;   // warp 11 completes the warpgroup
+constexpr int LOAD_WARP = 8, MMA_WARP = 9, BLANK_WARP = 10, WALK_WARP = 11;
 // A softmax thread holds a row's 128 scores: 208 registers, taken from the
 // third warpgroup.  256 * 208 + 128 * 88 = 384 * 168, the block's registers at
 // its launch.
@@ -75,14 +76,9 @@ constexpr uint64_t WAIT_LIMIT_NS = 1000000000ull;
 constexpr float RAISE = 8.0f;                // see above
 constexpr uint32_t FULL = 0xffffffffu;
 
-// A softmax warp's place in the work: in shared memory, so that the registers
-// are the scores'.
-struct State {
-    AttnWalk walk;
-    AttnPiece pc[2];
-};
-constexpr int STATE_BYTES = 208;
-static_assert(sizeof(State) <= STATE_BYTES, "see Cfg::TOTAL");
+constexpr int PIECES = 4;                    // pieces handed out and not done with
+constexpr int PIECE_BYTES = 64;
+static_assert(sizeof(AttnPiece) <= PIECE_BYTES, "see Cfg::TOTAL");
 
 template <int DP> struct Cfg {
     static constexpr int TILE = (DP / 64) * SUB;           // a block of keys, or 128 rows of queries
@@ -92,11 +88,11 @@ template <int DP> struct Cfg {
     static constexpr int BARS = RING + STAGES * TILE;
     static constexpr int B_FULL = 0, B_EMPTY = STAGES, B_S = 2 * STAGES, B_P = B_S + 2;
     static constexpr int B_Q = B_P + 4, B_QE = B_Q + 2, B_O = B_QE + 2, B_ASK = B_O + 2, B_Z = B_ASK + 1;
-    static constexpr int B_X = B_Z + 1, B_XE = B_X + 4, NBARS = B_XE + 4;
+    static constexpr int B_X = B_Z + 1, B_XE = B_X + 4, B_PF = B_XE + 4, B_PE = B_PF + PIECES, NBARS = B_PE + PIECES;
     static constexpr int MISC = BARS + ((8 * NBARS + 15) / 16) * 16;   // TMEM address, abort flag
     static constexpr int ML = MISC + 16;                               // lane 1's maxima and sums
-    static constexpr int STATE = ML + 2 * ROWS * 4;                    // the softmax warps' walks
-    static constexpr int TOTAL = STATE + 8 * STATE_BYTES;
+    static constexpr int PIECE = ML + 2 * ROWS * 4;
+    static constexpr int TOTAL = PIECE + PIECES * PIECE_BYTES;
     static constexpr int SMEM = 232448;                                // all that a block may have
     static_assert(TOTAL <= SMEM, "shared memory of one SM");
 };
@@ -121,19 +117,9 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatil
     return __all_sync(FULL, wait_bar(bar, parity, abort_flag));
 }
 
-// Maxima; with NAN_TOO a NaN among the values is the result.
-template <bool NAN_TOO>
-__device__ __forceinline__ float max2(float a, float b) {
-    float r;
-    if (NAN_TOO) asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    else asm("max.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-template <bool NAN_TOO>
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
-    if (NAN_TOO) asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    else asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 __device__ __forceinline__ float rcp_ftz(float x) {
@@ -151,27 +137,48 @@ __device__ __forceinline__ void st32(void* p, const uint4& a, const uint4& b) {
 // Whether some of a block's keys lie outside [lo, hi).
 __device__ __forceinline__ bool partly_seen(int k0, int lo, int hi) { return k0 < lo || k0 + KEYS > hi; }
 
-// Keys that any row of the piece's tile sees.
-__device__ __forceinline__ void tile_keys(const AttnParams& p, const AttnPiece& pc, int& lo, int& hi) {
-    int unused;
-    attn_row_keys(pc, pc.row0, p.G, p.window, lo, unused);
-    attn_row_keys(pc, min(pc.row0 + p.plan.tile_rows, pc.qlen * p.G) - 1, p.G, p.window, unused, hi);
-}
+// A warp's view of the pieces that the walking warp hands out.
+template <int DP> struct Pieces {
+    unsigned char* smem;
+    uint32_t sbase;
+    volatile int* abort_flag;
+    uint32_t n;
+    __device__ __forceinline__ Pieces(unsigned char* s, uint32_t b, volatile int* a)
+        : smem(s), sbase(b), abort_flag(a), n(0) {}
+    __device__ __forceinline__ uint32_t bar(int i) const {
+        return sbase + Cfg<DP>::BARS + 8u * (static_cast<uint32_t>(i) + n % PIECES);
+    }
+    // The next piece; nb is 0 after the last one and when a role gave up.
+    __device__ __forceinline__ const AttnPiece& get(bool& ok) const {
+        ok = wait_warp(bar(Cfg<DP>::B_PF), (n / PIECES) & 1, abort_flag);
+        return *reinterpret_cast<const AttnPiece*>(smem + Cfg<DP>::PIECE + (n % PIECES) * PIECE_BYTES);
+    }
+    // The warp is done with it.
+    __device__ __forceinline__ void done(int lane) {
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(Cfg<DP>::B_PE));
+        ++n;
+    }
+};
 
-// Scores z = cap tanh(scale s / cap) of four values, in base 2:
-// tanh(x) = 1 - 2 / (e^2x + 1), the four quotients from one reciprocal of the
-// denominators' product.  Past 2^30 a denominator changes nothing in float32.
+// Scores z = cap tanh(scale s / cap) in base 2: tanh(x) = 1 - 2 / (e^2x + 1),
+// four quotients from one reciprocal of their denominators' product (so e^2x
+// stays below 2^30: past it a denominator changes nothing in float32).  Packed
+// pairs: (0, 2) and (1, 3).
 __device__ __forceinline__ void cap4(uint32_t* u, float in, float cap2) {
-    float t[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) t[e] = ex2(fminf(__uint_as_float(u[e]) * in, 30.0f)) + 1.0f;
-    const float a = t[0] * t[1], b = t[2] * t[3];
-    const float r = rcp_ftz(a * b) * (-2.0f * cap2);
-    const float ra = r * b, rb = r * a;
-    u[0] = __float_as_uint(fmaf(ra, t[1], cap2));
-    u[1] = __float_as_uint(fmaf(ra, t[0], cap2));
-    u[2] = __float_as_uint(fmaf(rb, t[3], cap2));
-    u[3] = __float_as_uint(fmaf(rb, t[2], cap2));
+    const float2 in2 = make_float2(in, in), one = make_float2(1.0f, 1.0f), c2 = make_float2(cap2, cap2);
+    const float2 x = __fmul2_rn(make_float2(__uint_as_float(u[0]), __uint_as_float(u[2])), in2);
+    const float2 y = __fmul2_rn(make_float2(__uint_as_float(u[1]), __uint_as_float(u[3])), in2);
+    const float2 s = __fadd2_rn(make_float2(ex2(x.x), ex2(x.y)), one);
+    const float2 t = __fadd2_rn(make_float2(ex2(y.x), ex2(y.y)), one);
+    const float2 ab = __fmul2_rn(s, t);
+    const float r = rcp_ftz(ab.x * ab.y) * (-2.0f * cap2);
+    const float2 q = make_float2(r * ab.y, r * ab.x);   // 1 / (s t) of each pair
+    const float2 z = __ffma2_rn(q, t, c2), w = __ffma2_rn(q, s, c2);
+    u[0] = __float_as_uint(z.x);
+    u[2] = __float_as_uint(z.y);
+    u[1] = __float_as_uint(w.x);
+    u[3] = __float_as_uint(w.y);
 }
 
 // Scores of keys outside [from, to) of the block become -inf.  Most blocks
@@ -195,7 +202,7 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
     auto bar = [&](int i) { return sbase + C::BARS + 8u * static_cast<uint32_t>(i); };
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC + 4);
     float* ml = reinterpret_cast<float*>(smem + C::ML);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int L = warp >> 2, w4 = warp & 3, row_t = w4 * 32 + lane;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(w4 * 32) << 16);
     const uint32_t t_s = t_lane + S_COL + L * 128, t_o = t_lane + O_COL + L * 128;
@@ -206,18 +213,10 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
     uint32_t par_s = 0, par_o = 0, par_x = 0;
     bool ok = true, lent = false;   // lane 1's sums are with lane 0
 
-    State* st = reinterpret_cast<State*>(smem + C::STATE + warp * STATE_BYTES);
-    // lane 0 walks, the warp reads
-    auto advance = [&](int which) {
-        if (lane == 0) st->walk.next(p, cta, st->pc[which]);
-        __syncwarp();
-        return st->pc[which].nb > 0;
-    };
-    if (lane == 0) st->walk.begin(p, cta);
-    int now = 0;
-    bool have = advance(0);
-    while (ok && have) {
-        const AttnPiece& pc = st->pc[now];
+    Pieces<DP> pieces(smem, sbase, abort_flag);
+    while (ok) {
+        const AttnPiece& pc = pieces.get(ok);
+        if (!ok || pc.nb == 0) break;
         const int lane_rows = p.plan.lane_rows, nrows = pc.qlen * p.G;
         const bool pair = nrows - pc.row0 > lane_rows;
         const int mine = pair ? pc.nb : (pc.nb + 1 - L) / 2;    // blocks of this lane
@@ -226,7 +225,8 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
         const bool valid = row_t < lane_rows && r < nrows;
         const bool active = __any_sync(FULL, valid);            // a warp without rows only keeps the protocol
         int lo = 0, hi = 0x7fffffff;                            // rows that are not there need no mask
-        if (valid) attn_row_keys(pc, r, p.G, p.window, lo, hi);
+        const int tok = attn_token(p, valid ? r : 0);
+        if (valid) attn_token_keys(pc, tok, p.window, lo, hi);
         float m = -INFINITY, l = 0.0f;
         if (lent) {
             ok = wait_warp(bar(C::B_XE + w4), par_x, abort_flag);
@@ -249,26 +249,30 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
                 if (head || tail) mask_scores(u, head, tail, lo - k0, hi - k0);
                 float mx[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) mx[e] = max2<CAP>(__uint_as_float(u[e]), __uint_as_float(u[4 + e]));
+                for (int e = 0; e < 4; ++e) mx[e] = fmaxf(__uint_as_float(u[e]), __uint_as_float(u[4 + e]));
 #pragma unroll
                 for (int e = 8; e < 128; e += 8)
 #pragma unroll
                     for (int f = 0; f < 4; ++f)
-                        mx[f] = max3<CAP>(mx[f], __uint_as_float(u[e + f]), __uint_as_float(u[e + 4 + f]));
-                float top = max2<CAP>(max2<CAP>(mx[0], mx[1]), max2<CAP>(mx[2], mx[3])) * zscale;
-                bool raise = top > m + RAISE || (m == -INFINITY && top > -INFINITY);
+                        mx[f] = max3(mx[f], __uint_as_float(u[e + f]), __uint_as_float(u[e + 4 + f]));
+                float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * zscale;
                 if (CAP) {
-                    // tanh keeps the order: the capped maximum is the maximum's.  A
-                    // score that is no number does not survive cap4; the maximum
-                    // has it, and the row's sums take it from there.
+                    // tanh keeps the order, so the capped maximum is the maximum's
+                    if (__any_sync(FULL, top * cap_in > 30.0f)) {
+                        const float most = 30.0f / cap_in;
+#pragma unroll
+                        for (int e = 0; e < 128; ++e)
+                            if (__uint_as_float(u[e]) > most) u[e] = __float_as_uint(most);
+                        top = fminf(top, most);
+                    }
                     uint32_t t[4] = {__float_as_uint(top), 0u, 0u, 0u};
                     cap4(t, cap_in, cap2);
-                    if (top == top && top > -INFINITY) top = __uint_as_float(t[0]);
-                    raise = !(top <= m + RAISE) || (m == -INFINITY && top > -INFINITY);
+                    if (top > -INFINITY) top = __uint_as_float(t[0]);
 #pragma unroll
                     for (int e = 0; e < 128; e += 4) cap4(u + e, cap_in, cap2);
                     if (head || tail) mask_scores(u, head, tail, lo - k0, hi - k0);
                 }
+                const bool raise = top > m + RAISE || (m == -INFINITY && top > -INFINITY);
                 if (__any_sync(FULL, raise)) {
                     // S of this block is complete, so every earlier MMA is: O stands still
                     const float f = raise ? ex2(m - top) : 1.0f;
@@ -317,7 +321,6 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
                 }
             }
         }
-        const bool more = advance(now ^ 1);   // under the last product
         if (ok && mine > 0) {
             ok = wait_warp(bar(C::B_O + L), par_o, abort_flag);
             par_o ^= 1;
@@ -352,7 +355,6 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
             const float inv = whole ? (l != 0.0f ? 1.0f / l : 0.0f) : 1.0f;
             w0 *= inv;
             w1 *= inv;
-            const int tok = r / p.G;
             const int64_t out = valid ? (pc.q0 + tok) * p.Hq + pc.head * p.G + (r - tok * p.G) : 0;
             float* part = attn_slot(p, pc.slot);
             const bool both = !pair && pc.nb > 1;
@@ -426,8 +428,7 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
                 __syncwarp();
             }
         }
-        have = more;
-        now ^= 1;
+        pieces.done(lane);
     }
 }
 
@@ -471,6 +472,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
             ptx::mbar_init(bar(C::B_X + i), 1);    // lane 1's rows of warp i are final
             ptx::mbar_init(bar(C::B_XE + i), 1);   // and have been taken
         }
+        for (int i = 0; i < PIECES; ++i) {
+            ptx::mbar_init(bar(C::B_PF + i), 1);
+            ptx::mbar_init(bar(C::B_PE + i), 11);   // every other warp
+        }
         ptx::mbar_init(bar(C::B_ASK), 1);
         ptx::mbar_init(bar(C::B_Z), 1);
         *abort_flag = 0;
@@ -495,18 +500,34 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
     const bool work = agrees && walk.begin(p, cta);
     if (warp >= LOAD_WARP) {
         ptx::regs_dec<OTHER_REGS>();
-        AttnPiece pc;
-        if (work && warp == LOAD_WARP) {
+        Pieces<DP> pieces(smem, sbase, abort_flag);
+        bool ok = true;
+        if (work && warp == WALK_WARP) {
+            // ------------------------------------------------------ walk ---
+            for (uint32_t n = 0; ok; ++n) {
+                ok = wait_warp(bar(C::B_PE + n % PIECES), ((n / PIECES) & 1) ^ 1, abort_flag);
+                if (!ok) break;
+                AttnPiece pc;
+                const bool more = walk.next(p, cta, pc);
+                if (lane == 0) {
+                    *reinterpret_cast<AttnPiece*>(smem + C::PIECE + (n % PIECES) * PIECE_BYTES) = pc;
+                    ptx::mbar_arrive(bar(C::B_PF + n % PIECES));
+                }
+                __syncwarp();
+                if (!more) break;   // the piece without blocks ends every role
+            }
+        } else if (work && warp == LOAD_WARP) {
             // ------------------------------------------------------ loads ---
             const uint64_t policy = ptx::policy_evict_normal();
             const int box = p.page_size < KEYS ? p.page_size : KEYS;      // keys of one TMA box
             const int boxes = KEYS / box;                                 // of a block: at most 16
             int stage = 0;
             uint32_t round = 0, par_q = 1;
-            bool ok = true;
-            while (ok && walk.next(p, cta, pc)) {
-                int tlo, thi;
-                tile_keys(p, pc, tlo, thi);
+            while (ok) {
+                const AttnPiece pc = pieces.get(ok);
+                if (!ok || pc.nb == 0) break;
+                pieces.done(lane);
+                const int tlo = pc.lo, thi = pc.hi;
                 const bool pair = pc.qlen * p.G - pc.row0 > p.plan.lane_rows;
                 const int nb = pc.nb;
                 const int32_t* row = p.page_table + pc.seq * p.table_stride;
@@ -549,7 +570,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
                     if (ok && lane == 0) {
                         const uint32_t full = bar(C::B_Q + L);
                         ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(p.plan.lane_rows * DP * 2));
-                        const int64_t tok = pc.q0 + (pc.row0 + (pair ? L * p.plan.lane_rows : 0)) / p.G;
+                        const int64_t tok = pc.q0 + attn_token(p, pc.row0 + (pair ? L * p.plan.lane_rows : 0));
 #pragma unroll
                         for (int c = 0; c < DP / 64; ++c)
                             ptx::tma_load_3d(sbase + C::Q + L * C::TILE + c * SUB, &tmap_q, c * 64, pc.head * p.G,
@@ -573,10 +594,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
             // Value rows that no row of the tile sees become zeros before
             // their product.  Only a tile's first and last block can have some.
             uint32_t n = 0, par_a = 0;   // ring stages used by earlier pieces
-            bool ok = true;
-            while (ok && walk.next(p, cta, pc)) {
-                int tlo, thi;
-                tile_keys(p, pc, tlo, thi);
+            while (ok) {
+                const AttnPiece pc = pieces.get(ok);
+                if (!ok || pc.nb == 0) break;
+                pieces.done(lane);
+                const int tlo = pc.lo, thi = pc.hi;
                 const bool pair = pc.qlen * p.G - pc.row0 > p.plan.lane_rows;
                 for (int j = 0; ok && j < pc.nb; j = j == 0 && pc.nb > 1 ? pc.nb - 1 : pc.nb) {
                     const int k0 = (pc.blk + j) * KEYS;
@@ -614,7 +636,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
             const uint64_t desc_v = ptx::sw128_mnmajor_desc(sbase + C::RING, SUB, 1024);
             int stage = 0;
             uint32_t par_f = 0, par_q = 0, par_z = 0, par_p[2] = {0, 0};
-            bool ok = true;
             auto take = [&]() {   // the ring's next stage, once it is full
                 const int s = stage;
                 ok = ok && wait_warp(bar(C::B_FULL + s), par_f, abort_flag);
@@ -650,13 +671,15 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
                 return true;
             };
             auto free_stage = [&](int s) { ptx::tc_commit_if(on, bar(C::B_EMPTY + s)); };
-            while (ok && walk.next(p, cta, pc)) {
-                int tlo, thi;
-                tile_keys(p, pc, tlo, thi);
+            while (ok) {
+                const AttnPiece& pc = pieces.get(ok);
+                if (!ok || pc.nb == 0) break;
+                const int tlo = pc.lo, thi = pc.hi;
                 const bool pair = __shfl_sync(FULL, pc.qlen * p.G - pc.row0, 0) > p.plan.lane_rows;
                 const int nb = __shfl_sync(FULL, pc.nb, 0);
                 const bool z0 = __all_sync(FULL, partly_seen(pc.blk * KEYS, tlo, thi));
                 const bool z1 = __all_sync(FULL, partly_seen((pc.blk + nb - 1) * KEYS, tlo, thi));
+                pieces.done(lane);
                 auto blanked = [&](int j) {
                     if (ok && ((j == 0 && z0) || (j > 0 && j == nb - 1 && z1))) {
                         if (lane == 0) ptx::mbar_arrive(bar(C::B_ASK));
