@@ -408,55 +408,88 @@ def mhc_pre_bwd_noalloc(g_in, dH_post, dH_res, x, phi, b, alpha, proj, inv_rms,
 
 
 # ------------------------------------------------------ attention sublayer
+#
+# These calls are made once per layer in a decoding step, where the host's time
+# is the call's time: each tensor's attributes are read once, and the checks
+# are plain comparisons.
 
-def _heads(t: torch.Tensor, name: str, like=None):
+_I32, _I64T, _F32, _BF16 = torch.int32, torch.int64, torch.float32, torch.bfloat16
+_CODES = {_BF16: MHC_BF16, _F32: MHC_F32}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(t: torch.Tensor) -> int:
+    return _raw_stream(t.get_device()) if _raw_stream is not None else _stream(t.device)
+
+
+def _code(dtype) -> int:
+    c = _CODES.get(dtype)
+    if c is None:
+        raise TypeError(f"activations must be bfloat16 or float32, got {dtype}")
+    return c
+
+
+def _refuse_host():
+    raise ValueError("the mHC library takes CUDA tensors only")
+
+
+def _heads(t: torch.Tensor, name: str, dtype, T: int, H: int, Dh: int):
     """Address and token distance of a tensor of heads [T, H, Dh]; the tokens
     may be apart (a part of a packed projection), a token's heads are not."""
-    if like is not None and t.dtype != like.dtype:
-        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
-        raise ValueError("the mHC library takes CUDA tensors only")
-    T, H, Dh = t.shape
+        _refuse_host()
     st, sh, sd = t.stride()
-    if (Dh > 1 and sd != 1) or (H > 1 and sh != Dh):
+    if (sd != 1 and Dh > 1) or (sh != Dh and H > 1):
         raise ValueError(f"{name}: the heads of a token must lie one after the other")
     return t.data_ptr(), st if T > 1 else H * Dh
 
 
-def _ints(t: torch.Tensor, name: str, dtype, n=None):
-    if t.dtype != dtype:
+def _flat(t: torch.Tensor, name: str, dtype, n: int) -> int:
+    """Address of a dense tensor of n entries."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if n is not None and t.numel() != n:
+    if t.numel() != n:
         raise ValueError(f"{name} must have {n} entries, got {t.numel()}")
-    return _ptr(t)
+    if not t.is_cuda:
+        _refuse_host()
+    if not t.is_contiguous():
+        raise ValueError("the mHC library takes contiguous tensors only")
+    return t.data_ptr()
 
 
-def _rope(w_q, w_k, positions, cos_sin, T, Dh, interleaved):
-    """The arguments w_q, w_k, positions, cos_sin, max_pos and rot, flags."""
-    for w, name in ((w_q, "w_q"), (w_k, "w_k")):
-        if _f32(w, name).numel() != Dh:
-            raise ValueError(f"{name} must have {Dh} entries, got {w.numel()}")
+def _rope(positions, cos_sin, T):
+    """The arguments positions, cos_sin, max_pos, and rot."""
     if cos_sin is None:
-        return (_ptr(w_q), _ptr(w_k), None, None, 0), 0, 0
-    max_pos, rot = _f32(cos_sin, "cos_sin").shape
-    return ((_ptr(w_q), _ptr(w_k), _ints(positions, "positions", torch.int32, T), _ptr(cos_sin), max_pos),
-            rot, ROPE_ADJACENT if interleaved else 0)
+        return None, None, 0, 0
+    max_pos, rot = cos_sin.shape
+    return _flat(positions, "positions", _I32, T), _flat(cos_sin, "cos_sin", _F32, max_pos * rot), max_pos, rot
 
 
-def _cache(t: torch.Tensor, name: str, like, Hk: int, Dh: int):
+def _cache(t: torch.Tensor, name: str, dtype, shape):
     """Address and (page, slot, head) distances of a cache [pages, page_size, Hk, Dh]
     in any memory order that keeps a head's values together."""
-    if t.dtype != like.dtype:
-        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
-        raise ValueError("the mHC library takes CUDA tensors only")
-    P, ps, H, D = t.shape
-    if H != Hk or D != Dh:
-        raise ValueError(f"{name} must be [pages, page_size, {Hk}, {Dh}], got {tuple(t.shape)}")
+        _refuse_host()
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    P, ps, H, D = shape
     sp, ss, sh, sd = t.stride()
-    if D > 1 and sd != 1:
+    if sd != 1 and D > 1:
         raise ValueError(f"{name}: the values of a head must lie one after the other")
-    return (t.data_ptr(), sp if P > 1 else ps * Hk * Dh, ss if ps > 1 else Hk * Dh, sh if Hk > 1 else Dh)
+    return t.data_ptr(), sp if P > 1 else ps * H * D, ss if ps > 1 else H * D, sh if H > 1 else D
+
+
+def _same_tokens(q, k):
+    """T, Hq, Hk, Dh of q and k."""
+    T, Hq, Dh = q.shape
+    Tk, Hk, Dk = k.shape
+    if Tk != T or Dk != Dh:
+        raise ValueError("q and k must have the same tokens and head size")
+    return T, Hq, Hk, Dh
 
 
 def mhc_qk_norm_rope(q, k, w_q, w_k, positions=None, cos_sin=None, eps: float = 1e-6,
@@ -464,16 +497,16 @@ def mhc_qk_norm_rope(q, k, w_q, w_k, positions=None, cos_sin=None, eps: float = 
     """Per-head RMSNorm of q [T, Hq, Dh] and k [T, Hk, Dh], then the rotation of
     the first cos_sin.shape[1] values of each head by cos_sin[positions]
     (cosines, then sines).  ``interleaved``: pairs (2j, 2j + 1)."""
-    T, Hq, Dh = q.shape
-    if k.shape[0] != T or k.shape[2] != Dh:
-        raise ValueError("q and k must have the same tokens and head size")
-    Hk = k.shape[1]
-    rope, rot, flags = _rope(w_q, w_k, positions, cos_sin, T, Dh, interleaved)
-    out = QKOut(_empty((T, Hq, Dh), dtype=q.dtype, device=q.device),
-                _empty((T, Hk, Dh), dtype=q.dtype, device=q.device))
-    st = lib().mhc_qk_norm_rope(_dtype_code(q), *_heads(q, "q"), *_heads(k, "k", q), *rope, T, Hq, Hk, Dh,
-                                rot, flags, eps, out.q.data_ptr(), Hq * Dh, out.k.data_ptr(), Hk * Dh,
-                                _stream(q.device))
+    T, Hq, Hk, Dh = _same_tokens(q, k)
+    dt, dev = q.dtype, q.device
+    wq, wk = _flat(w_q, "w_q", _F32, Dh), _flat(w_k, "w_k", _F32, Dh)
+    qp, qs = _heads(q, "q", dt, T, Hq, Dh)
+    kp, ks = _heads(k, "k", dt, T, Hk, Dh)
+    pos, cs, max_pos, rot = _rope(positions, cos_sin, T)
+    out = QKOut(_empty((T, Hq, Dh), dtype=dt, device=dev), _empty((T, Hk, Dh), dtype=dt, device=dev))
+    st = (_lib or lib()).mhc_qk_norm_rope(
+        _code(dt), qp, qs, kp, ks, wq, wk, pos, cs, max_pos, T, Hq, Hk, Dh, rot,
+        ROPE_ADJACENT if interleaved else 0, eps, out.q.data_ptr(), Hq * Dh, out.k.data_ptr(), Hk * Dh, _stream_of(q))
     _check(st, "mhc_qk_norm_rope")
     return out
 
@@ -482,25 +515,32 @@ def mhc_qk_norm_rope_bwd(g_q, g_k, q, k, w_q, w_k, positions=None, cos_sin=None,
                          interleaved: bool = False, dq=None, dk=None):
     """Gradients of <g_q, q_out> + <g_k, k_out> for mhc_qk_norm_rope.  ``dq`` and
     ``dk`` (parts of a packed gradient, say) are written when given."""
-    T, Hq, Dh = q.shape
-    if k.shape[0] != T or k.shape[2] != Dh or g_q.shape != q.shape or g_k.shape != k.shape:
+    T, Hq, Hk, Dh = _same_tokens(q, k)
+    dt, dev = q.dtype, q.device
+    if g_q.shape != q.shape or g_k.shape != k.shape:
         raise ValueError("q, k and their gradients must have the same shapes")
-    Hk = k.shape[1]
-    rope, rot, flags = _rope(w_q, w_k, positions, cos_sin, T, Dh, interleaved)
     if dq is None:
-        dq = _empty((T, Hq, Dh), dtype=q.dtype, device=q.device)
+        dq = _empty((T, Hq, Dh), dtype=dt, device=dev)
     if dk is None:
-        dk = _empty((T, Hk, Dh), dtype=q.dtype, device=q.device)
+        dk = _empty((T, Hk, Dh), dtype=dt, device=dev)
     if dq.shape != q.shape or dk.shape != k.shape:
         raise ValueError("dq and dk must have the shapes of q and k")
-    dw_q = _empty((Dh,), dtype=torch.float32, device=q.device)
-    dw_k = _empty((Dh,), dtype=torch.float32, device=q.device)
-    need = int(lib().mhc_qk_norm_rope_bwd_workspace_bytes(T, Dh))
-    ws = _empty((max(need, 16),), dtype=torch.uint8, device=q.device)
-    st = lib().mhc_qk_norm_rope_bwd(_dtype_code(q), *_heads(g_q, "g_q", q), *_heads(g_k, "g_k", q),
-                                    *_heads(q, "q"), *_heads(k, "k", q), *rope, T, Hq, Hk, Dh, rot, flags,
-                                    eps, *_heads(dq, "dq", q), *_heads(dk, "dk", q), dw_q.data_ptr(),
-                                    dw_k.data_ptr(), ws.data_ptr(), need, _stream(q.device))
+    wq, wk = _flat(w_q, "w_q", _F32, Dh), _flat(w_k, "w_k", _F32, Dh)
+    L = _lib or lib()
+    gqp, gqs = _heads(g_q, "g_q", dt, T, Hq, Dh)
+    gkp, gks = _heads(g_k, "g_k", dt, T, Hk, Dh)
+    qp, qs = _heads(q, "q", dt, T, Hq, Dh)
+    kp, ks = _heads(k, "k", dt, T, Hk, Dh)
+    dqp, dqs = _heads(dq, "dq", dt, T, Hq, Dh)
+    dkp, dks = _heads(dk, "dk", dt, T, Hk, Dh)
+    pos, cs, max_pos, rot = _rope(positions, cos_sin, T)
+    dw_q, dw_k = _empty((Dh,), dtype=_F32, device=dev), _empty((Dh,), dtype=_F32, device=dev)
+    need = L.mhc_qk_norm_rope_bwd_workspace_bytes(T, Dh)
+    ws = _empty((need or 16,), dtype=torch.uint8, device=dev)
+    st = L.mhc_qk_norm_rope_bwd(
+        _code(dt), gqp, gqs, gkp, gks, qp, qs, kp, ks, wq, wk, pos, cs, max_pos, T, Hq, Hk, Dh, rot,
+        ROPE_ADJACENT if interleaved else 0, eps, dqp, dqs, dkp, dks, dw_q.data_ptr(), dw_k.data_ptr(),
+        ws.data_ptr(), need, _stream_of(q))
     _check(st, "mhc_qk_norm_rope_bwd")
     return QKBwdOut(dq, dk, dw_q, dw_k)
 
@@ -510,31 +550,26 @@ def mhc_qk_norm_rope_append(q, k, v, w_q, w_k, k_cache, v_cache, slots, position
     """The serving form: returns the normalised, rotated q; the keys (likewise)
     and the values go to slots[t] = page * page_size + place of the caches
     [pages, page_size, Hk, Dh] (-1: nowhere), in place."""
-    T, Hq, Dh = q.shape
-    if k.shape[0] != T or k.shape[2] != Dh or v.shape != k.shape:
-        raise ValueError("q, k and v must have the same tokens and head size")
-    Hk = k.shape[1]
-    if k_cache.shape != v_cache.shape:
-        raise ValueError("k_cache and v_cache must have the same shape")
-    rope, rot, flags = _rope(w_q, w_k, positions, cos_sin, T, Dh, interleaved)
-    out = _empty((T, Hq, Dh), dtype=q.dtype, device=q.device)
-    st = lib().mhc_qk_norm_rope_append(
-        _dtype_code(q), *_heads(q, "q"), *_heads(k, "k", q), *_heads(v, "v", q), *rope,
-        _ints(slots, "slots", torch.int64, T), T, Hq, Hk, Dh, rot, flags, eps, out.data_ptr(), Hq * Dh,
-        *_cache(k_cache, "k_cache", q, Hk, Dh), *_cache(v_cache, "v_cache", q, Hk, Dh),
-        k_cache.shape[0], k_cache.shape[1], _stream(q.device))
+    T, Hq, Hk, Dh = _same_tokens(q, k)
+    dt = q.dtype
+    if v.shape != k.shape:
+        raise ValueError("k and v must have the same shape")
+    shape = k_cache.shape
+    if len(shape) != 4 or shape[2] != Hk or shape[3] != Dh:
+        raise ValueError(f"k_cache must be [pages, page_size, {Hk}, {Dh}], got {tuple(shape)}")
+    wq, wk = _flat(w_q, "w_q", _F32, Dh), _flat(w_k, "w_k", _F32, Dh)
+    qp, qs = _heads(q, "q", dt, T, Hq, Dh)
+    kp, ks = _heads(k, "k", dt, T, Hk, Dh)
+    vp, vs = _heads(v, "v", dt, T, Hk, Dh)
+    pos, cs, max_pos, rot = _rope(positions, cos_sin, T)
+    kc, kpg, ksl, kh = _cache(k_cache, "k_cache", dt, shape)
+    vc, vpg, vsl, vh = _cache(v_cache, "v_cache", dt, shape)
+    out = _empty((T, Hq, Dh), dtype=dt, device=q.device)
+    st = (_lib or lib()).mhc_qk_norm_rope_append(
+        _code(dt), qp, qs, kp, ks, vp, vs, wq, wk, pos, cs, max_pos, _flat(slots, "slots", _I64T, T), T, Hq, Hk, Dh, rot, ROPE_ADJACENT if interleaved else 0,
+        eps, out.data_ptr(), Hq * Dh, kc, kpg, ksl, kh, vc, vpg, vsl, vh, shape[0], shape[1], _stream_of(q))
     _check(st, "mhc_qk_norm_rope_append")
     return out
-
-
-def _attn_sizes(dtype, T, Hq, Hk, Dh, page_size, B, max_q, max_kv, window):
-    return (MHC_BF16 if dtype == torch.bfloat16 else MHC_F32, T, B, Hq, Hk, Dh, page_size, max_q, max_kv, window)
-
-
-def _attn_workspace(sizes, device):
-    code, T, B, Hq, Hk, Dh, page_size, max_q = sizes[:8]
-    need = int(lib().mhc_paged_attn_workspace_bytes(code, T, B, Hq, Hk, Dh, page_size, max_q))
-    return _empty((max(need, 16),), dtype=torch.uint8, device=device)
 
 
 def mhc_paged_attn_plan(cu_q, kv_lens, dtype, T: int, Hq: int, Hk: int, Dh: int, page_size: int,
@@ -543,15 +578,15 @@ def mhc_paged_attn_plan(cu_q, kv_lens, dtype, T: int, Hq: int, Hk: int, Dh: int,
     same sizes (the layers of one step).  Calls that share a plan share its
     workspace: they must not overlap."""
     B = kv_lens.numel()
-    if dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"activations must be bfloat16 or float32, got {dtype}")
-    sizes = _attn_sizes(dtype, T, Hq, Hk, Dh, page_size, B, max_q, max_kv, window)
-    ws = _attn_workspace(sizes, cu_q.device)
-    st = lib().mhc_paged_attn_plan(sizes[0], _ints(cu_q, "cu_q", torch.int32, B + 1),
-                                   _ints(kv_lens, "kv_lens", torch.int32), *sizes[1:], ws.data_ptr(),
-                                   ws.numel(), _stream(cu_q.device))
+    L = _lib or lib()
+    code = _code(dtype)
+    need = L.mhc_paged_attn_workspace_bytes(code, T, B, Hq, Hk, Dh, page_size, max_q)
+    ws = _empty((need or 16,), dtype=torch.uint8, device=cu_q.device)
+    st = L.mhc_paged_attn_plan(code, _flat(cu_q, "cu_q", _I32, B + 1), _flat(kv_lens, "kv_lens", _I32, B), T, B,
+                               Hq, Hk, Dh, page_size, max_q, max_kv, window, ws.data_ptr(), need,
+                               _stream_of(cu_q))
     _check(st, "mhc_paged_attn_plan")
-    return PagedAttnPlan(ws, sizes)
+    return PagedAttnPlan(ws, (code, T, B, Hq, Hk, Dh, page_size, max_q, max_kv, window))
 
 
 def mhc_paged_attn(q, k_cache, v_cache, page_table, cu_q=None, kv_lens=None, max_q: int = None,
@@ -563,44 +598,58 @@ def mhc_paged_attn(q, k_cache, v_cache, page_table, cu_q=None, kv_lens=None, max
     the new and the cached tokens of a sequence (default: all rows of q, the
     page table's width); ``window`` 0 or None: unlimited.  ``plan`` (from
     mhc_paged_attn_plan) takes the place of cu_q and kv_lens and brings its own
-    max_q, max_kv and window.  ``out``: a tensor for o; rows of no sequence stay as they
-    are.  Returns o and lse [T, Hq]."""
+    max_q, max_kv and window.  ``out``: a tensor for o; rows of no sequence stay
+    as they are.  Returns o and lse [T, Hq]."""
     T, Hq, Dh = q.shape
-    P, page_size, Hk, _ = k_cache.shape
-    if k_cache.shape != v_cache.shape:
-        raise ValueError("k_cache and v_cache must have the same shape")
+    dt, dev = q.dtype, q.device
+    code = _code(dt)
+    shape = k_cache.shape
+    if len(shape) != 4 or shape[3] != Dh:
+        raise ValueError(f"k_cache must be [pages, page_size, heads, {Dh}], got {tuple(shape)}")
+    P, page_size, Hk, _ = shape
     B, width = page_table.shape
+    L = _lib or lib()
     if plan is None:
-        sizes = _attn_sizes(q.dtype, T, Hq, Hk, Dh, page_size, B, T if max_q is None else max_q,
-                            width * page_size if max_kv is None else max_kv, window or 0)
-        ws = _attn_workspace(sizes, q.device)
-        lens = (_ints(cu_q, "cu_q", torch.int32, B + 1), _ints(kv_lens, "kv_lens", torch.int32, B))
+        max_q = T if max_q is None else max_q
+        max_kv = width * page_size if max_kv is None else max_kv
+        window = window or 0
+        need = L.mhc_paged_attn_workspace_bytes(code, T, B, Hq, Hk, Dh, page_size, max_q)
+        ws = _empty((need or 16,), dtype=torch.uint8, device=dev)
+        cu, kv = _flat(cu_q, "cu_q", _I32, B + 1), _flat(kv_lens, "kv_lens", _I32, B)
     else:
         ws, sizes = plan
-        lens = (None, None)
-        want = _attn_sizes(q.dtype, T, Hq, Hk, Dh, page_size, B,
-                           *(a if b is None else b for a, b in zip(sizes[7:], (max_q, max_kv, window))))
+        mine = tuple(a if b is None else b for a, b in zip(sizes[7:], (max_q, max_kv, window)))
+        want = (code, T, B, Hq, Hk, Dh, page_size) + mine
         if want != sizes or cu_q is not None or kv_lens is not None:
             raise ValueError(f"the plan has its own lengths and sizes: {sizes}, not {want}")
-    if page_table.dtype != torch.int32:
-        raise TypeError(f"page_table must be {torch.int32}, got {page_table.dtype}")
+        max_q, max_kv, window = mine
+        need = ws.numel()
+        cu = kv = None
+    if page_table.dtype is not _I32:
+        raise TypeError(f"page_table must be {_I32}, got {page_table.dtype}")
     if not page_table.is_cuda:
-        raise ValueError("the mHC library takes CUDA tensors only")
-    if width * page_size < sizes[8]:
-        raise ValueError(f"page_table holds {width * page_size} tokens a sequence, max_kv is {sizes[8]}")
-    if width > 1 and page_table.stride(1) != 1:
+        _refuse_host()
+    if width * page_size < max_kv:
+        raise ValueError(f"page_table holds {width * page_size} tokens a sequence, max_kv is {max_kv}")
+    row, col = page_table.stride()
+    if col != 1 and width > 1:
         raise ValueError("page_table: the pages of a sequence must lie one after the other")
+    qp, qs = _heads(q, "q", dt, T, Hq, Dh)
+    kc, kpg, ksl, kh = _cache(k_cache, "k_cache", dt, shape)
+    vc, vpg, vsl, vh = _cache(v_cache, "v_cache", dt, shape)
     if out is None:
-        out = _empty((T, Hq, Dh), dtype=q.dtype, device=q.device)
-    elif out.shape != q.shape or out.dtype != q.dtype:
-        raise ValueError("out must have the shape and type of q")
-    lse = _empty((T, Hq), dtype=torch.float32, device=q.device)
-    st = lib().mhc_paged_attn(
-        _dtype_code(q), *_heads(q, "q"), *_cache(k_cache, "k_cache", q, Hk, Dh),
-        *_cache(v_cache, "v_cache", q, Hk, Dh), P, page_size, page_table.data_ptr(),
-        page_table.stride(0) if B > 1 else width, *lens, T, B, Hq, Hk, Dh, sizes[7], sizes[8], sizes[9],
-        Dh ** -0.5 if scale is None else scale, softcap, _ptr(out), lse.data_ptr(), ws.data_ptr(), ws.numel(),
-        _stream(q.device))
+        out = _empty((T, Hq, Dh), dtype=dt, device=dev)
+        op = out.data_ptr()
+    else:
+        op = _flat(out, "out", dt, T * Hq * Dh)
+        if out.shape != q.shape:
+            raise ValueError("out must have the shape of q")
+    lse = _empty((T, Hq), dtype=_F32, device=dev)
+    st = L.mhc_paged_attn(
+        code, qp, qs, kc, kpg, ksl, kh, vc, vpg, vsl, vh, P, page_size, page_table.data_ptr(),
+        row if B > 1 else width, cu, kv, T, B, Hq, Hk, Dh, max_q, max_kv, window,
+        Dh ** -0.5 if scale is None else scale, softcap, op, lse.data_ptr(), ws.data_ptr(), need,
+        _stream_of(q))
     _check(st, "mhc_paged_attn")
     return PagedAttnOut(out, lse)
 

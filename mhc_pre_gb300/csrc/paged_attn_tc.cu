@@ -181,17 +181,16 @@ __device__ __forceinline__ void cap4(uint32_t* u, float in, float cap2) {
     u[3] = __float_as_uint(w.y);
 }
 
-// Scores of keys outside [from, to) of the block become -inf.  Most blocks
-// with a mask have it at one end only.
-__device__ __forceinline__ void mask_scores(uint32_t (&u)[128], bool head, bool tail, int from, int to) {
+// Scores of keys outside [from, to) become -inf, of 32 keys from the first.
+__device__ __forceinline__ void mask32(uint32_t* u, bool head, bool tail, int from, int to) {
     if (tail) {
 #pragma unroll
-        for (int e = 0; e < 128; ++e)
+        for (int e = 0; e < 32; ++e)
             if (e >= to) u[e] = 0xff800000u;
     }
     if (head) {
 #pragma unroll
-        for (int e = 0; e < 128; ++e)
+        for (int e = 0; e < 32; ++e)
             if (e < from) u[e] = 0xff800000u;
     }
 }
@@ -241,36 +240,56 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
             if (!ok) break;
             ptx::tc_fence_after();
             if (active) {
-                uint32_t u[128];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) ptx::tmem_ld32(t_s + c * 32, u + c * 32);
-                ptx::tmem_wait_ld();
+                // Without a cap the scores stay in registers (128 of them) from
+                // the maximum to the exponentials.  With one they are read twice,
+                // 32 at a time with the next 32 on their way: the capping's code
+                // over all 128 is so long that the warps wait for instructions.
+                // Exponentials overwrite scores already read.
                 const bool head = __any_sync(FULL, k0 < lo), tail = __any_sync(FULL, k0 + KEYS > hi);
-                if (head || tail) mask_scores(u, head, tail, lo - k0, hi - k0);
-                float mx[4];
+                const int from = lo - k0, to = hi - k0;
+                constexpr int HELD = CAP ? 64 : 128;
+                uint32_t u[HELD];
+                float top, most = INFINITY;
+                if constexpr (!CAP) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) mx[e] = fmaxf(__uint_as_float(u[e]), __uint_as_float(u[4 + e]));
+                    for (int c = 0; c < 4; ++c) ptx::tmem_ld32(t_s + c * 32, u + c * 32);
+                    ptx::tmem_wait_ld();
+                    if (head || tail) {
 #pragma unroll
-                for (int e = 8; e < 128; e += 8)
-#pragma unroll
-                    for (int f = 0; f < 4; ++f)
-                        mx[f] = max3(mx[f], __uint_as_float(u[e + f]), __uint_as_float(u[e + 4 + f]));
-                float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * zscale;
-                if (CAP) {
-                    // tanh keeps the order, so the capped maximum is the maximum's
-                    if (__any_sync(FULL, top * cap_in > 30.0f)) {
-                        const float most = 30.0f / cap_in;
-#pragma unroll
-                        for (int e = 0; e < 128; ++e)
-                            if (__uint_as_float(u[e]) > most) u[e] = __float_as_uint(most);
-                        top = fminf(top, most);
+                        for (int c = 0; c < 4; ++c) mask32(u + 32 * c, head, tail, from - 32 * c, to - 32 * c);
                     }
-                    uint32_t t[4] = {__float_as_uint(top), 0u, 0u, 0u};
+                    float mx[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mx[e] = fmaxf(__uint_as_float(u[e]), __uint_as_float(u[4 + e]));
+#pragma unroll
+                    for (int e = 8; e < 128; e += 8)
+#pragma unroll
+                        for (int f = 0; f < 4; ++f)
+                            mx[f] = max3(mx[f], __uint_as_float(u[e + f]), __uint_as_float(u[e + 4 + f]));
+                    top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * zscale;
+                } else {
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    ptx::tmem_ld32(t_s, u);
+#pragma unroll 1
+                    for (int c = 0; c < 4; c += 2) {
+#pragma unroll
+                        for (int d = 0; d < 2; ++d) {
+                            ptx::tmem_wait_ld();
+                            if (d == 0 || c == 0) ptx::tmem_ld32(t_s + (c + d + 1) * 32, u + 32 * (d ^ 1));
+                            if (head || tail) mask32(u + 32 * d, head, tail, from - 32 * (c + d), to - 32 * (c + d));
+#pragma unroll
+                            for (int e = 0; e < 32; e += 8)
+#pragma unroll
+                                for (int f = 0; f < 4; ++f)
+                                    mx[f] = max3(mx[f], __uint_as_float(u[32 * d + e + f]), __uint_as_float(u[32 * d + e + 4 + f]));
+                        }
+                    }
+                    top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * zscale;
+                    // tanh keeps the order, so the capped maximum is the maximum's
+                    if (__any_sync(FULL, top * cap_in > 30.0f)) most = 30.0f / cap_in;
+                    uint32_t t[4] = {__float_as_uint(fminf(top, most)), 0u, 0u, 0u};
                     cap4(t, cap_in, cap2);
                     if (top > -INFINITY) top = __uint_as_float(t[0]);
-#pragma unroll
-                    for (int e = 0; e < 128; e += 4) cap4(u + e, cap_in, cap2);
-                    if (head || tail) mask_scores(u, head, tail, lo - k0, hi - k0);
                 }
                 const bool raise = top > m + RAISE || (m == -INFINITY && top > -INFINITY);
                 if (__any_sync(FULL, raise)) {
@@ -279,7 +298,7 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
                     if (raise) m = top;
                     l *= f;
                     if (i > 0) {
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < DP / 32; ++c) {
                             uint32_t o[32];
                             ptx::tmem_ld32(t_o + c * 32, o);
@@ -293,23 +312,63 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
                 const float base = m == -INFINITY ? 0.0f : m;
                 const float2 z2 = make_float2(zscale, zscale), b2 = make_float2(-base, -base);
                 float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                if constexpr (!CAP) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t pk[32];
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t pk[32];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const float2 x = __ffma2_rn(
-                            make_float2(__uint_as_float(u[64 * h + 2 * e]), __uint_as_float(u[64 * h + 2 * e + 1])), z2, b2);
-                        const float2 y = make_float2(ex2(x.x), ex2(x.y));
-                        sum[e & 1] = __fadd2_rn(sum[e & 1], y);
-                        const __nv_bfloat162 t = __floats2bfloat162_rn(y.x, y.y);
-                        pk[e] = *reinterpret_cast<const uint32_t*>(&t);
+                        for (int e = 0; e < 32; ++e) {
+                            const float2 x = __ffma2_rn(
+                                make_float2(__uint_as_float(u[64 * h + 2 * e]), __uint_as_float(u[64 * h + 2 * e + 1])), z2, b2);
+                            const float2 y = make_float2(ex2(x.x), ex2(x.y));
+                            sum[e & 1] = __fadd2_rn(sum[e & 1], y);
+                            const __nv_bfloat162 t = __floats2bfloat162_rn(y.x, y.y);
+                            pk[e] = *reinterpret_cast<const uint32_t*>(&t);
+                        }
+                        ptx::tmem_st32(t_s + h * 32, pk);
+                        ptx::tmem_wait_st();
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(bar(C::B_P + 2 * L + h));
                     }
-                    ptx::tmem_st32(t_s + h * 32, pk);
-                    ptx::tmem_wait_st();
-                    ptx::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(bar(C::B_P + 2 * L + h));
+                } else {
+                    ptx::tmem_ld32(t_s, u);
+#pragma unroll 1
+                    for (int c = 0; c < 4; c += 2) {
+#pragma unroll
+                        for (int d = 0; d < 2; ++d) {
+                            ptx::tmem_wait_ld();
+                            if (d == 0 || c == 0) ptx::tmem_ld32(t_s + (c + d + 1) * 32, u + 32 * (d ^ 1));
+                            uint32_t* v = u + 32 * d;
+                            const int f = from - 32 * (c + d), t = to - 32 * (c + d);
+                            // an unseen key's NaN must not reach the other three of its cap4
+                            if (head || tail) mask32(v, head, tail, f, t);
+                            if (most < INFINITY) {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (__uint_as_float(v[e]) > most) v[e] = __float_as_uint(most);
+                            }
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) cap4(v + e, cap_in, cap2);
+                            if (head || tail) mask32(v, head, tail, f, t);
+                            uint32_t pk[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const float2 x = __ffma2_rn(
+                                    make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), z2, b2);
+                                const float2 y = make_float2(ex2(x.x), ex2(x.y));
+                                sum[e & 1] = __fadd2_rn(sum[e & 1], y);
+                                const __nv_bfloat162 h = __floats2bfloat162_rn(y.x, y.y);
+                                pk[e] = *reinterpret_cast<const uint32_t*>(&h);
+                            }
+                            ptx::tmem_st16(t_s + (c + d) * 16, pk);
+                        }
+                        // 64 keys' exponentials are there: their product may start
+                        ptx::tmem_wait_st();
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(bar(C::B_P + 2 * L + (c >> 1)));
+                    }
                 }
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             } else {
@@ -358,7 +417,7 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
             const int64_t out = valid ? (pc.q0 + tok) * p.Hq + pc.head * p.G + (r - tok * p.G) : 0;
             float* part = attn_slot(p, pc.slot);
             const bool both = !pair && pc.nb > 1;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < DP / 32; ++c) {
                 uint32_t o[32];
                 ptx::tmem_ld32(t_o + c * 32, o);
