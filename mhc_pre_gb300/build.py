@@ -22,8 +22,8 @@ SOURCES = ["mhc_abi.cu", "kernels_fwd.cu", "kernels_bwd.cu", "pre_tc.cu", "pre_b
            "pre_bwd_fused.cu",
            "pre_bwd_noalloc.cu", "post_pre_tc.cu",
            "post_norm.cu", "pre_small.cu",
-           "qk_norm_rope.cu", "paged_attn.cu", "paged_attn_tc.cu",
-           "attn_abi.cu"]
+           "qk_norm_rope.cu", "qk_norm_rope_bwd.cu", "paged_attn.cu",
+           "paged_attn_tc.cu", "attn_abi.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
          "--expt-relaxed-constexpr", "-Xptxas", "-warn-spills"]

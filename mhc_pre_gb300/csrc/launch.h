@@ -150,6 +150,7 @@ cudaError_t launch_paged_attn_tc(const AttnParams& p, cudaStream_t s);
 
 // Device error words of these kernels, read and cleared.
 cudaError_t read_and_clear_qk_error(unsigned* word);
+cudaError_t read_and_clear_qk_bwd_error(unsigned* word);
 cudaError_t read_and_clear_attn_error(unsigned* word);
 cudaError_t read_and_clear_attn_tc_error(unsigned* word);
 

@@ -112,6 +112,10 @@ cudaError_t read_and_clear_device_error(unsigned* word, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     *word |= other;
     other = 0;
+    e = read_and_clear_qk_bwd_error(&other);
+    if (e != cudaSuccess) return e;
+    *word |= other;
+    other = 0;
     e = read_and_clear_attn_error(&other);
     if (e != cudaSuccess) return e;
     *word |= other;
