@@ -189,9 +189,12 @@ attn_plan_kernel(const PlanParams p) {
 //
 // 256 threads as 16 x 16: thread (ty, tx) has rows ty*RPT .. +RPT of the tile
 // and keys tx, tx + 16, ... of a block for the scores, and the columns
-// 4 tx + 64 c of the values for the sums.  Queries, keys, values and
-// exponentials are float32 in shared memory; a row's maximum and sum live in
-// the 16 lanes that share the row.
+// 4 tx + 64 c of the values for the sums; a row's maximum and sum live in the
+// 16 lanes that share the row.  Products go through packed pairs of float32
+// (pairs along d for the scores, of columns for the sums): a register tile of
+// 4 x 4 then has more arithmetic than shared-memory reads.  Keys and values
+// come by asynchronous copies, each while the other is being multiplied.
+// Bound by float32 arithmetic where rows fill the tile.
 constexpr int CC_THREADS = 256, CC_KEYS = 64, CC_KPT = CC_KEYS / 16;
 
 template <typename TA>
@@ -204,21 +207,57 @@ __device__ __forceinline__ float4 ld4(const TA* p) {
     return *reinterpret_cast<const float4*>(p);
 }
 
-__host__ __device__ constexpr int cc_pitch(int dp) { return dp + 4; }   // floats: 16-byte rows, no bank conflicts
+// Elements of a row of keys or values: 16 bytes more than its values, so that
+// the rows of 8 neighbouring threads lie in different banks.
+template <typename TA> __host__ __device__ constexpr int cc_pitch(int dp) { return dp + 16 / static_cast<int>(sizeof(TA)); }
+constexpr int CC_PP = CC_KEYS + 4;   // floats of a row of exponentials
+template <typename TA>
 constexpr size_t cc_smem(int dp, int rows) {
-    return sizeof(float) * (static_cast<size_t>(rows) * cc_pitch(dp) + 2u * CC_KEYS * cc_pitch(dp) +
-                            static_cast<size_t>(rows) * (CC_KEYS + 4));
+    return sizeof(float) * static_cast<size_t>(rows) * (dp + 4 + CC_PP) + sizeof(TA) * 2u * CC_KEYS * cc_pitch<TA>(dp);
+}
+
+// Starts the copy of one block of keys or values; what lies outside [lo, hi)
+// becomes zeros, whatever the pages hold there.
+template <typename TA, int DP>
+__device__ __forceinline__ void cc_copy(const AttnParams& p, const AttnPiece& pc, TA* dst, const void* cache,
+                                        int64_t page_stride, int64_t slot_stride, int64_t head_stride, int k0, int tid) {
+    constexpr int PER = 16 / static_cast<int>(sizeof(TA)), CPR = DP / PER;   // values of a copy, copies of a row
+    constexpr int ROWS = CC_THREADS / CPR, PASSES = CC_KEYS / ROWS;
+    const int d = (tid % CPR) * PER;
+    int page[PASSES];
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+        const int key = k0 + i * ROWS + tid / CPR;
+        page[i] = -1;
+        if (key >= pc.lo && key < pc.hi && d < p.Dh) {
+            const int pg = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
+            page[i] = p.page_table[pc.seq * p.table_stride + pg];
+            if (page[i] < 0 || page[i] >= p.num_pages) {
+                atomicOr(&g_attn_error, ATTN_ERR_RANGE);
+                page[i] = -1;
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+        const int row = i * ROWS + tid / CPR, key = k0 + row;
+        const int in = p.page_shift >= 0 ? key & (p.page_size - 1) : key % p.page_size;
+        const TA* src = static_cast<const TA*>(cache);
+        if (page[i] >= 0) src += page[i] * page_stride + in * slot_stride + pc.head * head_stride + d;
+        ptx::cp_async16(ptx::smem_u32(dst + row * cc_pitch<TA>(DP) + d), src, page[i] >= 0 ? 16u : 0u);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
 template <typename TA, int DP, int RPT>
 __global__ void __launch_bounds__(CC_THREADS)
 attn_cc_kernel(const AttnParams p) {
-    constexpr int ROWS = 16 * RPT, PITCH = cc_pitch(DP), NC = DP / 64, PP = CC_KEYS + 4;
+    constexpr int ROWS = 16 * RPT, QP = DP + 4, PITCH = cc_pitch<TA>(DP), NC = DP / 64, PP = CC_PP;
     extern __shared__ __align__(16) float smem_f[];
     float* Qs = smem_f;
-    float* Ks = Qs + ROWS * PITCH;
-    float* Vs = Ks + CC_KEYS * PITCH;
-    float* Ps = Vs + CC_KEYS * PITCH;
+    float* Ps = Qs + ROWS * QP;
+    TA* Ks = reinterpret_cast<TA*>(Ps + ROWS * PP);
+    TA* Vs = Ks + CC_KEYS * PITCH;
     __shared__ int s_last;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, cta = blockIdx.x;
     ptx::griddep_wait();
@@ -233,6 +272,16 @@ attn_cc_kernel(const AttnParams p) {
     AttnPiece pc;
     while (walk.next(p, cta, pc)) {
         const int nrows = pc.qlen * p.G;
+        auto copy_k = [&](int b) {
+            cc_copy<TA, DP>(p, pc, Ks, p.k_cache, p.k_page_stride, p.k_slot_stride, p.k_head_stride,
+                            (pc.blk + b) * CC_KEYS, tid);
+        };
+        auto copy_v = [&](int b) {
+            cc_copy<TA, DP>(p, pc, Vs, p.v_cache, p.v_page_stride, p.v_slot_stride, p.v_head_stride,
+                            (pc.blk + b) * CC_KEYS, tid);
+        };
+        copy_k(0);
+        copy_v(0);
         // the tile's queries
         for (int i = tid; i < ROWS * (DP / 4); i += CC_THREADS) {
             const int row = i / (DP / 4), d = (i - row * (DP / 4)) * 4, r = pc.row0 + row;
@@ -242,10 +291,11 @@ attn_cc_kernel(const AttnParams p) {
                 v = ld4(static_cast<const TA*>(p.q) + (pc.q0 + tok) * p.q_stride +
                         static_cast<int64_t>(pc.head * p.G + r - tok * p.G) * p.Dh + d);
             }
-            *reinterpret_cast<float4*>(Qs + row * PITCH + d) = v;
+            *reinterpret_cast<float4*>(Qs + row * QP + d) = v;
         }
         int lo[RPT], hi[RPT];
-        float m[RPT], l[RPT], acc[RPT][NC][4];
+        float m[RPT], l[RPT];
+        float2 acc[RPT][NC][2];
 #pragma unroll
         for (int a = 0; a < RPT; ++a) {
             const int r = pc.row0 + ty * RPT + a;
@@ -254,64 +304,45 @@ attn_cc_kernel(const AttnParams p) {
             m[a] = -INFINITY;
             l[a] = 0.0f;
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[a][c][e] = 0.0f;
+            for (int c = 0; c < NC; ++c) acc[a][c][0] = acc[a][c][1] = make_float2(0.0f, 0.0f);
         }
-        const int tlo = pc.lo, thi = pc.hi;
         for (int b = 0; b < pc.nb; ++b) {
             const int k0 = (pc.blk + b) * CC_KEYS;
+            const bool more = b + 1 < pc.nb;
+            asm volatile("cp.async.wait_group 1;" ::: "memory");   // the keys; the values may still come
             __syncthreads();
-            // keys outside what the tile sees are zeros, whatever the pages hold there
-            for (int i = tid; i < CC_KEYS * (DP / 4); i += CC_THREADS) {
-                const int row = i / (DP / 4), d = (i - row * (DP / 4)) * 4, key = k0 + row;
-                float4 kk = make_float4(0.0f, 0.0f, 0.0f, 0.0f), vv = kk;
-                if (key >= tlo && key < thi && d < p.Dh) {
-                    const int pg = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
-                    const int in = key - pg * p.page_size;
-                    const int64_t page = p.page_table[pc.seq * p.table_stride + pg];
-                    if (page >= 0 && page < p.num_pages) {
-                        kk = ld4(static_cast<const TA*>(p.k_cache) + page * p.k_page_stride + in * p.k_slot_stride +
-                                 pc.head * p.k_head_stride + d);
-                        vv = ld4(static_cast<const TA*>(p.v_cache) + page * p.v_page_stride + in * p.v_slot_stride +
-                                 pc.head * p.v_head_stride + d);
-                    } else if (d == 0) {
-                        atomicOr(&g_attn_error, ATTN_ERR_RANGE);
-                    }
-                }
-                *reinterpret_cast<float4*>(Ks + row * PITCH + d) = kk;
-                *reinterpret_cast<float4*>(Vs + row * PITCH + d) = vv;
-            }
-            __syncthreads();
-            float s[RPT][CC_KPT];
+            float2 s2[RPT][CC_KPT];
 #pragma unroll
             for (int a = 0; a < RPT; ++a)
 #pragma unroll
-                for (int j = 0; j < CC_KPT; ++j) s[a][j] = 0.0f;
+                for (int j = 0; j < CC_KPT; ++j) s2[a][j] = make_float2(0.0f, 0.0f);
 #pragma unroll 4
             for (int d = 0; d < DP; d += 4) {
                 float4 kv[CC_KPT];
 #pragma unroll
-                for (int j = 0; j < CC_KPT; ++j)
-                    kv[j] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * j) * PITCH + d);
+                for (int j = 0; j < CC_KPT; ++j) kv[j] = ld4(Ks + (tx + 16 * j) * PITCH + d);
 #pragma unroll
                 for (int a = 0; a < RPT; ++a) {
-                    const float4 qv = *reinterpret_cast<const float4*>(Qs + (ty * RPT + a) * PITCH + d);
+                    const float4 qv = *reinterpret_cast<const float4*>(Qs + (ty * RPT + a) * QP + d);
 #pragma unroll
-                    for (int j = 0; j < CC_KPT; ++j)
-                        s[a][j] = fmaf(qv.x, kv[j].x, fmaf(qv.y, kv[j].y, fmaf(qv.z, kv[j].z, fmaf(qv.w, kv[j].w, s[a][j]))));
+                    for (int j = 0; j < CC_KPT; ++j) {
+                        s2[a][j] = __ffma2_rn(make_float2(qv.x, qv.y), make_float2(kv[j].x, kv[j].y), s2[a][j]);
+                        s2[a][j] = __ffma2_rn(make_float2(qv.z, qv.w), make_float2(kv[j].z, kv[j].w), s2[a][j]);
+                    }
                 }
             }
+            __syncthreads();
+            if (more) copy_k(b + 1);
 #pragma unroll
             for (int a = 0; a < RPT; ++a) {
-                float mx = m[a];
+                float s[CC_KPT], mx = m[a];
 #pragma unroll
                 for (int j = 0; j < CC_KPT; ++j) {
                     const int key = k0 + tx + 16 * j;
-                    float z = p.softcap > 0.0f ? p.softcap * LOG2E * tanhf(s[a][j] * cap_in) : s[a][j] * zscale;
-                    z = key >= lo[a] && key < hi[a] ? z : -INFINITY;
-                    s[a][j] = z;
-                    mx = fmaxf(mx, z);
+                    const float x = s2[a][j].x + s2[a][j].y;
+                    const float z = p.softcap > 0.0f ? p.softcap * LOG2E * tanhf(x * cap_in) : x * zscale;
+                    s[j] = key >= lo[a] && key < hi[a] ? z : -INFINITY;
+                    mx = fmaxf(mx, s[j]);
                 }
 #pragma unroll
                 for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o, 16));
@@ -320,7 +351,7 @@ attn_cc_kernel(const AttnParams p) {
                 float sum = 0.0f;
 #pragma unroll
                 for (int j = 0; j < CC_KPT; ++j) {
-                    const float e = exp2f(s[a][j] - base);
+                    const float e = exp2f(s[j] - base);
                     sum += e;
                     Ps[(ty * RPT + a) * PP + tx + 16 * j] = e;
                 }
@@ -328,12 +359,16 @@ attn_cc_kernel(const AttnParams p) {
                 for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o, 16);
                 l[a] = fmaf(l[a], keep, sum);
                 m[a] = mx;
+                const float2 keep2 = make_float2(keep, keep);
 #pragma unroll
-                for (int c = 0; c < NC; ++c)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[a][c][e] *= keep;
+                for (int c = 0; c < NC; ++c) {
+                    acc[a][c][0] = __fmul2_rn(acc[a][c][0], keep2);
+                    acc[a][c][1] = __fmul2_rn(acc[a][c][1], keep2);
+                }
             }
-            __syncwarp();   // a row's 16 lanes are in one warp
+            if (more) asm volatile("cp.async.wait_group 1;" ::: "memory");   // the values; the next keys may still come
+            else asm volatile("cp.async.wait_group 0;" ::: "memory");
+            __syncthreads();
 #pragma unroll 2
             for (int k = 0; k < CC_KEYS; k += 4) {
                 float4 pr[RPT];
@@ -343,18 +378,18 @@ attn_cc_kernel(const AttnParams p) {
                 for (int kk = 0; kk < 4; ++kk) {
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
-                        const float4 v = *reinterpret_cast<const float4*>(Vs + (k + kk) * PITCH + tx * 4 + 64 * c);
+                        const float4 v = ld4(Vs + (k + kk) * PITCH + tx * 4 + 64 * c);
 #pragma unroll
                         for (int a = 0; a < RPT; ++a) {
                             const float w = kk == 0 ? pr[a].x : kk == 1 ? pr[a].y : kk == 2 ? pr[a].z : pr[a].w;
-                            acc[a][c][0] = fmaf(w, v.x, acc[a][c][0]);
-                            acc[a][c][1] = fmaf(w, v.y, acc[a][c][1]);
-                            acc[a][c][2] = fmaf(w, v.z, acc[a][c][2]);
-                            acc[a][c][3] = fmaf(w, v.w, acc[a][c][3]);
+                            acc[a][c][0] = __ffma2_rn(make_float2(w, w), make_float2(v.x, v.y), acc[a][c][0]);
+                            acc[a][c][1] = __ffma2_rn(make_float2(w, w), make_float2(v.z, v.w), acc[a][c][1]);
                         }
                     }
                 }
             }
+            __syncthreads();
+            if (more) copy_v(b + 1);
         }
         if (pc.whole) {
 #pragma unroll
@@ -370,13 +405,13 @@ attn_cc_kernel(const AttnParams p) {
                     const int d = tx * 4 + 64 * c;
                     if (d >= p.Dh) continue;
                     if (sizeof(TA) == 2) {
-                        const __nv_bfloat162 x = __floats2bfloat162_rn(acc[a][c][0] * inv, acc[a][c][1] * inv);
-                        const __nv_bfloat162 y = __floats2bfloat162_rn(acc[a][c][2] * inv, acc[a][c][3] * inv);
+                        const __nv_bfloat162 x = __floats2bfloat162_rn(acc[a][c][0].x * inv, acc[a][c][0].y * inv);
+                        const __nv_bfloat162 y = __floats2bfloat162_rn(acc[a][c][1].x * inv, acc[a][c][1].y * inv);
                         *reinterpret_cast<uint2*>(o + d) = make_uint2(*reinterpret_cast<const uint32_t*>(&x),
                                                                       *reinterpret_cast<const uint32_t*>(&y));
                     } else {
-                        *reinterpret_cast<float4*>(o + d) = make_float4(acc[a][c][0] * inv, acc[a][c][1] * inv,
-                                                                        acc[a][c][2] * inv, acc[a][c][3] * inv);
+                        *reinterpret_cast<float4*>(o + d) = make_float4(acc[a][c][0].x * inv, acc[a][c][0].y * inv,
+                                                                        acc[a][c][1].x * inv, acc[a][c][1].y * inv);
                     }
                 }
                 if (tx == 0 && p.lse != nullptr) p.lse[out] = attn_lse(m[a], l[a]);
@@ -391,7 +426,7 @@ attn_cc_kernel(const AttnParams p) {
 #pragma unroll
                 for (int c = 0; c < NC; ++c)
                     *reinterpret_cast<float4*>(s + static_cast<int64_t>(row) * DP + tx * 4 + 64 * c) =
-                        make_float4(acc[a][c][0], acc[a][c][1], acc[a][c][2], acc[a][c][3]);
+                        make_float4(acc[a][c][0].x, acc[a][c][0].y, acc[a][c][1].x, acc[a][c][1].y);
                 if (tx == 0) {
                     s[static_cast<int64_t>(sr) * DP + row] = m[a];
                     s[static_cast<int64_t>(sr) * (DP + 1) + row] = l[a];
@@ -439,7 +474,7 @@ cudaError_t allow_smem(const void* kernel, std::atomic<uint64_t>& done, size_t b
 template <typename TA, int DP, int RPT>
 cudaError_t launch_cc(const AttnParams& p, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
-    constexpr size_t smem = cc_smem(DP, 16 * RPT);
+    constexpr size_t smem = cc_smem<TA>(DP, 16 * RPT);
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(attn_cc_kernel<TA, DP, RPT>), done, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};

@@ -115,7 +115,7 @@ qk_direct_kernel(const QkParams p) {
 
 // ------------------------------------------------------------- many tokens ---
 template <typename TA, int LPH, bool ADJ, bool APPEND>
-__global__ void __launch_bounds__(THREADS, 4)
+__global__ void __launch_bounds__(THREADS, FWD_BLOCKS)
 qk_staged_kernel(const QkParams p, const Ring ring) {
     const int W = ring.team_warps, NGRP = W * 32 / LPH;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -206,7 +206,7 @@ template <typename TA, int LPH, bool ADJ, bool APPEND>
 cudaError_t launch_fwd_lph(const QkParams& p, cudaStream_t s) {
     const int e = static_cast<int>(sizeof(TA));
     const int sizes[4] = {p.Hq * p.Dh * e, p.Hk * p.Dh * e, p.Hk * p.Dh * e, 0};
-    const RingPlan r = plan_ring(sizes, APPEND ? 3 : 2, p.rot, p.T);
+    const RingPlan r = plan_ring(sizes, APPEND ? 3 : 2, p.rot, p.T, FWD_BLOCKS);
     if (r.ring.stages > 0) {
         static std::atomic<uint64_t> done{0};
         auto kernel = qk_staged_kernel<TA, LPH, ADJ, APPEND>;

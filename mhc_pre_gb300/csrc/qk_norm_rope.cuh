@@ -42,6 +42,9 @@ static __device__ unsigned g_qk_error;
 namespace qk {
 
 constexpr int THREADS = 128;
+// Staged blocks of an SM (the kernels are compiled for that many).  Forward, at
+// T = 32768 and 48 heads of 128: 4, 5 and 6 take 149, 145 and 150 us.
+constexpr int FWD_BLOCKS = 5, BWD_BLOCKS = 4;
 constexpr uint64_t WAIT_LIMIT_NS = 1000000000ull;
 
 // ------------------------------------------------------------- four pairs ---
@@ -360,7 +363,8 @@ struct RingPlan {
 constexpr int SM_SMEM = 224 * 1024;
 constexpr int TEAM_BYTES = 6 * 1024;   // larger rows: a team of four warps (see below)
 
-inline RingPlan plan_ring(const int (&sizes)[4], int nrows, int rot, int64_t T) {
+// `most`: blocks of an SM that the kernel's registers allow.
+inline RingPlan plan_ring(const int (&sizes)[4], int nrows, int rot, int64_t T, int most) {
     RingPlan r = {};
     int at = 0;
     for (int i = 0; i < nrows; ++i) {
@@ -375,10 +379,9 @@ inline RingPlan plan_ring(const int (&sizes)[4], int nrows, int rot, int64_t T) 
     r.ring.stage_bytes = at + 128;
     r.ring.team_warps = bytes >= TEAM_BYTES ? 4 : 1;
     const int teams = THREADS / 32 / r.ring.team_warps, sms = sm_count();
-    // Four blocks of an SM (their registers allow no more) with two stages or
-    // more each, fewer where two stages do not fit: all of an SM's stages
-    // together are what is in flight.
-    for (int per_sm = 4; per_sm >= 1; --per_sm) {
+    // The most blocks of an SM that have two stages or more each: all of an
+    // SM's stages together are what is in flight.
+    for (int per_sm = most; per_sm >= 1; --per_sm) {
         const int each = SM_SMEM / per_sm - 1024 - teams * 8 * 16;
         const int stages = each / (teams * r.ring.stage_bytes);
         if (stages >= 2) {

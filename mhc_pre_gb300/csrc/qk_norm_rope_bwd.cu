@@ -138,7 +138,7 @@ qk_direct_bwd_kernel(const QkBwdParams p) {
 }
 
 template <typename TA, int LPH, bool ADJ>
-__global__ void __launch_bounds__(THREADS, 4)
+__global__ void __launch_bounds__(THREADS, BWD_BLOCKS)
 qk_staged_bwd_kernel(const QkBwdParams p, const Ring ring) {
     const int W = ring.team_warps, NGRP = W * 32 / LPH;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -244,7 +244,7 @@ template <typename TA>
 RingPlan plan_bwd(const QkBwdParams& p) {
     const int e = static_cast<int>(sizeof(TA));
     const int sizes[4] = {p.Hq * p.Dh * e, p.Hk * p.Dh * e, p.Hq * p.Dh * e, p.Hk * p.Dh * e};
-    RingPlan r = plan_ring(sizes, 4, p.rot, p.T);
+    RingPlan r = plan_ring(sizes, 4, p.rot, p.T, BWD_BLOCKS);
     // the ring also holds the groups' sums at the end
     if (r.ring.stages > 0 && r.smem < THREADS * 8 * sizeof(float)) r.smem = THREADS * 8 * sizeof(float);
     return r;
