@@ -187,15 +187,15 @@ attn_plan_kernel(const PlanParams p) {
 
 // ------------------------------------------------------------ CUDA cores ---
 //
-// 256 threads as 16 x 16: thread (ty, tx) has rows ty*RPT .. +RPT of the tile
-// and keys tx, tx + 16, ... of a block for the scores, and the columns
+// TY x 16 threads: thread (ty, tx) has the rows ty, ty + TY, ... of the tile and
+// keys tx, tx + 16, ... of a block for the scores, and the columns
 // 4 tx + 64 c of the values for the sums; a row's maximum and sum live in the
 // 16 lanes that share the row.  Products go through packed pairs of float32
 // (pairs along d for the scores, of columns for the sums): a register tile of
 // 4 x 4 then has more arithmetic than shared-memory reads.  Keys and values
 // come by asynchronous copies, each while the other is being multiplied.
 // Bound by float32 arithmetic where rows fill the tile.
-constexpr int CC_THREADS = 256, CC_KEYS = 64, CC_KPT = CC_KEYS / 16;
+constexpr int CC_KEYS = 64, CC_KPT = CC_KEYS / 16;
 
 template <typename TA>
 __device__ __forceinline__ float4 ld4(const TA* p) {
@@ -218,11 +218,12 @@ constexpr size_t cc_smem(int dp, int rows) {
 
 // Starts the copy of one block of keys or values; what lies outside [lo, hi)
 // becomes zeros, whatever the pages hold there.
-template <typename TA, int DP>
+template <typename TA, int DP, int TY>
 __device__ __forceinline__ void cc_copy(const AttnParams& p, const AttnPiece& pc, TA* dst, const void* cache,
                                         int64_t page_stride, int64_t slot_stride, int64_t head_stride, int k0, int tid) {
     constexpr int PER = 16 / static_cast<int>(sizeof(TA)), CPR = DP / PER;   // values of a copy, copies of a row
-    constexpr int ROWS = CC_THREADS / CPR, PASSES = CC_KEYS / ROWS;
+    constexpr int ROWS = TY * 16 / CPR, PASSES = CC_KEYS / ROWS;
+    static_assert(ROWS * PASSES == CC_KEYS, "the threads copy whole rows");
     const int d = (tid % CPR) * PER;
     int page[PASSES];
 #pragma unroll
@@ -249,204 +250,215 @@ __device__ __forceinline__ void cc_copy(const AttnParams& p, const AttnPiece& pc
     asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
-template <typename TA, int DP, int RPT>
-__global__ void __launch_bounds__(CC_THREADS)
+// One piece of a tile of at most TY RPT rows.
+template <typename TA, int DP, int TY, int RPT>
+__device__ __forceinline__ void cc_piece(const AttnParams& p, const AttnPiece& pc, float* Qs, float* Ps, TA* Ks, TA* Vs,
+                                         int* s_last) {
+    constexpr int QP = DP + 4, PITCH = cc_pitch<TA>(DP), NC = DP / 64, PP = CC_PP;
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const float zscale = p.scale * LOG2E;
+    const float cap_in = p.softcap > 0.0f ? p.scale / p.softcap : 0.0f;
+    const int nrows = pc.qlen * p.G;
+    auto copy_k = [&](int b) {
+        cc_copy<TA, DP, TY>(p, pc, Ks, p.k_cache, p.k_page_stride, p.k_slot_stride, p.k_head_stride,
+                        (pc.blk + b) * CC_KEYS, tid);
+    };
+    auto copy_v = [&](int b) {
+        cc_copy<TA, DP, TY>(p, pc, Vs, p.v_cache, p.v_page_stride, p.v_slot_stride, p.v_head_stride,
+                        (pc.blk + b) * CC_KEYS, tid);
+    };
+    copy_k(0);
+    copy_v(0);
+    // the tile's queries
+    for (int i = tid; i < TY * RPT * (DP / 4); i += TY * 16) {
+        const int row = i / (DP / 4), d = (i - row * (DP / 4)) * 4, r = pc.row0 + row;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (r < nrows && d < p.Dh) {
+            const int tok = attn_token(p, r);
+            v = ld4(static_cast<const TA*>(p.q) + (pc.q0 + tok) * p.q_stride +
+                    static_cast<int64_t>(pc.head * p.G + r - tok * p.G) * p.Dh + d);
+        }
+        *reinterpret_cast<float4*>(Qs + row * QP + d) = v;
+    }
+    int lo[RPT], hi[RPT];
+    float m[RPT], l[RPT];
+    float2 acc[RPT][NC][2];
+#pragma unroll
+    for (int a = 0; a < RPT; ++a) {
+        const int r = pc.row0 + ty + TY * a;
+        lo[a] = hi[a] = 0;
+        if (r < nrows) attn_token_keys(pc, attn_token(p, r), p.window, lo[a], hi[a]);
+        m[a] = -INFINITY;
+        l[a] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) acc[a][c][0] = acc[a][c][1] = make_float2(0.0f, 0.0f);
+    }
+    for (int b = 0; b < pc.nb; ++b) {
+        const int k0 = (pc.blk + b) * CC_KEYS;
+        const bool more = b + 1 < pc.nb;
+        asm volatile("cp.async.wait_group 1;" ::: "memory");   // the keys; the values may still come
+        __syncthreads();
+        float2 s2[RPT][CC_KPT];
+#pragma unroll
+        for (int a = 0; a < RPT; ++a)
+#pragma unroll
+            for (int j = 0; j < CC_KPT; ++j) s2[a][j] = make_float2(0.0f, 0.0f);
+#pragma unroll 4
+        for (int d = 0; d < DP; d += 4) {
+            float4 kv[CC_KPT];
+#pragma unroll
+            for (int j = 0; j < CC_KPT; ++j) kv[j] = ld4(Ks + (tx + 16 * j) * PITCH + d);
+#pragma unroll
+            for (int a = 0; a < RPT; ++a) {
+                const float4 qv = *reinterpret_cast<const float4*>(Qs + (ty + TY * a) * QP + d);
+#pragma unroll
+                for (int j = 0; j < CC_KPT; ++j) {
+                    s2[a][j] = __ffma2_rn(make_float2(qv.x, qv.y), make_float2(kv[j].x, kv[j].y), s2[a][j]);
+                    s2[a][j] = __ffma2_rn(make_float2(qv.z, qv.w), make_float2(kv[j].z, kv[j].w), s2[a][j]);
+                }
+            }
+        }
+        __syncthreads();
+        if (more) copy_k(b + 1);
+#pragma unroll
+        for (int a = 0; a < RPT; ++a) {
+            float s[CC_KPT], mx = m[a];
+#pragma unroll
+            for (int j = 0; j < CC_KPT; ++j) {
+                const int key = k0 + tx + 16 * j;
+                const float x = s2[a][j].x + s2[a][j].y;
+                const float z = p.softcap > 0.0f ? p.softcap * LOG2E * tanhf(x * cap_in) : x * zscale;
+                s[j] = key >= lo[a] && key < hi[a] ? z : -INFINITY;
+                mx = fmaxf(mx, s[j]);
+            }
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o, 16));
+            const float base = mx > -INFINITY ? mx : 0.0f;
+            const float keep = exp2f(m[a] - base);
+            float sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < CC_KPT; ++j) {
+                const float e = exp2f(s[j] - base);
+                sum += e;
+                Ps[(ty + TY * a) * PP + tx + 16 * j] = e;
+            }
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o, 16);
+            l[a] = fmaf(l[a], keep, sum);
+            m[a] = mx;
+            const float2 keep2 = make_float2(keep, keep);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                acc[a][c][0] = __fmul2_rn(acc[a][c][0], keep2);
+                acc[a][c][1] = __fmul2_rn(acc[a][c][1], keep2);
+            }
+        }
+        if (more) asm volatile("cp.async.wait_group 1;" ::: "memory");   // the values; the next keys may still come
+        else asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
+#pragma unroll 2
+        for (int k = 0; k < CC_KEYS; k += 4) {
+            float4 pr[RPT];
+#pragma unroll
+            for (int a = 0; a < RPT; ++a) pr[a] = *reinterpret_cast<const float4*>(Ps + (ty + TY * a) * PP + k);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    const float4 v = ld4(Vs + (k + kk) * PITCH + tx * 4 + 64 * c);
+#pragma unroll
+                    for (int a = 0; a < RPT; ++a) {
+                        const float w = kk == 0 ? pr[a].x : kk == 1 ? pr[a].y : kk == 2 ? pr[a].z : pr[a].w;
+                        acc[a][c][0] = __ffma2_rn(make_float2(w, w), make_float2(v.x, v.y), acc[a][c][0]);
+                        acc[a][c][1] = __ffma2_rn(make_float2(w, w), make_float2(v.z, v.w), acc[a][c][1]);
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        if (more) copy_v(b + 1);
+    }
+    if (pc.whole) {
+#pragma unroll
+        for (int a = 0; a < RPT; ++a) {
+            const int r = pc.row0 + ty + TY * a;
+            if (r >= nrows) continue;
+            const float inv = l[a] != 0.0f ? 1.0f / l[a] : 0.0f;
+            const int tok = attn_token(p, r);
+            const int64_t out = (pc.q0 + tok) * p.Hq + pc.head * p.G + (r - tok * p.G);
+            TA* o = static_cast<TA*>(p.o) + out * p.Dh;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const int d = tx * 4 + 64 * c;
+                if (d >= p.Dh) continue;
+                if (sizeof(TA) == 2) {
+                    const __nv_bfloat162 x = __floats2bfloat162_rn(acc[a][c][0].x * inv, acc[a][c][0].y * inv);
+                    const __nv_bfloat162 y = __floats2bfloat162_rn(acc[a][c][1].x * inv, acc[a][c][1].y * inv);
+                    *reinterpret_cast<uint2*>(o + d) = make_uint2(*reinterpret_cast<const uint32_t*>(&x),
+                                                                  *reinterpret_cast<const uint32_t*>(&y));
+                } else {
+                    *reinterpret_cast<float4*>(o + d) = make_float4(acc[a][c][0].x * inv, acc[a][c][0].y * inv,
+                                                                    acc[a][c][1].x * inv, acc[a][c][1].y * inv);
+                }
+            }
+            if (tx == 0 && p.lse != nullptr) p.lse[out] = attn_lse(m[a], l[a]);
+        }
+    } else {
+        float* s = attn_slot(p, pc.slot);
+        const int sr = p.plan.slot_rows;
+#pragma unroll
+        for (int a = 0; a < RPT; ++a) {
+            const int row = ty + TY * a;
+            if (pc.row0 + row >= nrows) continue;
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                *reinterpret_cast<float4*>(s + static_cast<int64_t>(row) * DP + tx * 4 + 64 * c) =
+                    make_float4(acc[a][c][0].x, acc[a][c][0].y, acc[a][c][1].x, acc[a][c][1].y);
+            if (tx == 0) {
+                s[static_cast<int64_t>(sr) * DP + row] = m[a];
+                s[static_cast<int64_t>(sr) * (DP + 1) + row] = l[a];
+            }
+        }
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) {
+            const int n = atomicAdd(attn_counts(p) + pc.cnt, 1);
+            *s_last = n == pc.last_cta - pc.first_cta;
+            // the counter is back at zero for the next call with this plan
+            if (*s_last) attn_counts(p)[pc.cnt] = 0;
+            __threadfence();
+        }
+        __syncthreads();
+        if (*s_last) {
+            const int rows = min(p.plan.tile_rows, nrows - pc.row0), each = (rows + TY / 2 - 1) / (TY / 2), begin = (tid >> 5) * each;
+            attn_join<TA, DP, 4>(p, pc, begin, min(rows, begin + each), tid & 31);
+        }
+    }
+}
+
+// Tiles of up to TY RPT rows; one of at most TY (a sequence that decodes, in a
+// batch with chunks) takes the code that has no other rows.
+template <typename TA, int DP, int TY, int RPT>
+__global__ void __launch_bounds__(TY * 16)
 attn_cc_kernel(const AttnParams p) {
-    constexpr int ROWS = 16 * RPT, QP = DP + 4, PITCH = cc_pitch<TA>(DP), NC = DP / 64, PP = CC_PP;
     extern __shared__ __align__(16) float smem_f[];
     float* Qs = smem_f;
-    float* Ps = Qs + ROWS * QP;
-    TA* Ks = reinterpret_cast<TA*>(Ps + ROWS * PP);
-    TA* Vs = Ks + CC_KEYS * PITCH;
+    float* Ps = Qs + TY * RPT * (DP + 4);
+    TA* Ks = reinterpret_cast<TA*>(Ps + TY * RPT * CC_PP);
+    TA* Vs = Ks + CC_KEYS * cc_pitch<TA>(DP);
     __shared__ int s_last;
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, cta = blockIdx.x;
+    const int cta = blockIdx.x;
     ptx::griddep_wait();
     if (!attn_plan_agrees(p)) {
-        if (tid == 0) atomicOr(&g_attn_error, ATTN_ERR_RANGE);
+        if (threadIdx.x == 0) atomicOr(&g_attn_error, ATTN_ERR_RANGE);
         return;
     }
     AttnWalk walk;
     if (!walk.begin(p, cta)) return;
-    const float zscale = p.scale * LOG2E;
-    const float cap_in = p.softcap > 0.0f ? p.scale / p.softcap : 0.0f;
     AttnPiece pc;
     while (walk.next(p, cta, pc)) {
-        const int nrows = pc.qlen * p.G;
-        auto copy_k = [&](int b) {
-            cc_copy<TA, DP>(p, pc, Ks, p.k_cache, p.k_page_stride, p.k_slot_stride, p.k_head_stride,
-                            (pc.blk + b) * CC_KEYS, tid);
-        };
-        auto copy_v = [&](int b) {
-            cc_copy<TA, DP>(p, pc, Vs, p.v_cache, p.v_page_stride, p.v_slot_stride, p.v_head_stride,
-                            (pc.blk + b) * CC_KEYS, tid);
-        };
-        copy_k(0);
-        copy_v(0);
-        // the tile's queries
-        for (int i = tid; i < ROWS * (DP / 4); i += CC_THREADS) {
-            const int row = i / (DP / 4), d = (i - row * (DP / 4)) * 4, r = pc.row0 + row;
-            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (r < nrows && d < p.Dh) {
-                const int tok = attn_token(p, r);
-                v = ld4(static_cast<const TA*>(p.q) + (pc.q0 + tok) * p.q_stride +
-                        static_cast<int64_t>(pc.head * p.G + r - tok * p.G) * p.Dh + d);
-            }
-            *reinterpret_cast<float4*>(Qs + row * QP + d) = v;
-        }
-        int lo[RPT], hi[RPT];
-        float m[RPT], l[RPT];
-        float2 acc[RPT][NC][2];
-#pragma unroll
-        for (int a = 0; a < RPT; ++a) {
-            const int r = pc.row0 + ty * RPT + a;
-            lo[a] = hi[a] = 0;
-            if (r < nrows) attn_token_keys(pc, attn_token(p, r), p.window, lo[a], hi[a]);
-            m[a] = -INFINITY;
-            l[a] = 0.0f;
-#pragma unroll
-            for (int c = 0; c < NC; ++c) acc[a][c][0] = acc[a][c][1] = make_float2(0.0f, 0.0f);
-        }
-        for (int b = 0; b < pc.nb; ++b) {
-            const int k0 = (pc.blk + b) * CC_KEYS;
-            const bool more = b + 1 < pc.nb;
-            asm volatile("cp.async.wait_group 1;" ::: "memory");   // the keys; the values may still come
-            __syncthreads();
-            float2 s2[RPT][CC_KPT];
-#pragma unroll
-            for (int a = 0; a < RPT; ++a)
-#pragma unroll
-                for (int j = 0; j < CC_KPT; ++j) s2[a][j] = make_float2(0.0f, 0.0f);
-#pragma unroll 4
-            for (int d = 0; d < DP; d += 4) {
-                float4 kv[CC_KPT];
-#pragma unroll
-                for (int j = 0; j < CC_KPT; ++j) kv[j] = ld4(Ks + (tx + 16 * j) * PITCH + d);
-#pragma unroll
-                for (int a = 0; a < RPT; ++a) {
-                    const float4 qv = *reinterpret_cast<const float4*>(Qs + (ty * RPT + a) * QP + d);
-#pragma unroll
-                    for (int j = 0; j < CC_KPT; ++j) {
-                        s2[a][j] = __ffma2_rn(make_float2(qv.x, qv.y), make_float2(kv[j].x, kv[j].y), s2[a][j]);
-                        s2[a][j] = __ffma2_rn(make_float2(qv.z, qv.w), make_float2(kv[j].z, kv[j].w), s2[a][j]);
-                    }
-                }
-            }
-            __syncthreads();
-            if (more) copy_k(b + 1);
-#pragma unroll
-            for (int a = 0; a < RPT; ++a) {
-                float s[CC_KPT], mx = m[a];
-#pragma unroll
-                for (int j = 0; j < CC_KPT; ++j) {
-                    const int key = k0 + tx + 16 * j;
-                    const float x = s2[a][j].x + s2[a][j].y;
-                    const float z = p.softcap > 0.0f ? p.softcap * LOG2E * tanhf(x * cap_in) : x * zscale;
-                    s[j] = key >= lo[a] && key < hi[a] ? z : -INFINITY;
-                    mx = fmaxf(mx, s[j]);
-                }
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o, 16));
-                const float base = mx > -INFINITY ? mx : 0.0f;
-                const float keep = exp2f(m[a] - base);
-                float sum = 0.0f;
-#pragma unroll
-                for (int j = 0; j < CC_KPT; ++j) {
-                    const float e = exp2f(s[j] - base);
-                    sum += e;
-                    Ps[(ty * RPT + a) * PP + tx + 16 * j] = e;
-                }
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o, 16);
-                l[a] = fmaf(l[a], keep, sum);
-                m[a] = mx;
-                const float2 keep2 = make_float2(keep, keep);
-#pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    acc[a][c][0] = __fmul2_rn(acc[a][c][0], keep2);
-                    acc[a][c][1] = __fmul2_rn(acc[a][c][1], keep2);
-                }
-            }
-            if (more) asm volatile("cp.async.wait_group 1;" ::: "memory");   // the values; the next keys may still come
-            else asm volatile("cp.async.wait_group 0;" ::: "memory");
-            __syncthreads();
-#pragma unroll 2
-            for (int k = 0; k < CC_KEYS; k += 4) {
-                float4 pr[RPT];
-#pragma unroll
-                for (int a = 0; a < RPT; ++a) pr[a] = *reinterpret_cast<const float4*>(Ps + (ty * RPT + a) * PP + k);
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-#pragma unroll
-                    for (int c = 0; c < NC; ++c) {
-                        const float4 v = ld4(Vs + (k + kk) * PITCH + tx * 4 + 64 * c);
-#pragma unroll
-                        for (int a = 0; a < RPT; ++a) {
-                            const float w = kk == 0 ? pr[a].x : kk == 1 ? pr[a].y : kk == 2 ? pr[a].z : pr[a].w;
-                            acc[a][c][0] = __ffma2_rn(make_float2(w, w), make_float2(v.x, v.y), acc[a][c][0]);
-                            acc[a][c][1] = __ffma2_rn(make_float2(w, w), make_float2(v.z, v.w), acc[a][c][1]);
-                        }
-                    }
-                }
-            }
-            __syncthreads();
-            if (more) copy_v(b + 1);
-        }
-        if (pc.whole) {
-#pragma unroll
-            for (int a = 0; a < RPT; ++a) {
-                const int r = pc.row0 + ty * RPT + a;
-                if (r >= nrows) continue;
-                const float inv = l[a] != 0.0f ? 1.0f / l[a] : 0.0f;
-                const int tok = attn_token(p, r);
-                const int64_t out = (pc.q0 + tok) * p.Hq + pc.head * p.G + (r - tok * p.G);
-                TA* o = static_cast<TA*>(p.o) + out * p.Dh;
-#pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    const int d = tx * 4 + 64 * c;
-                    if (d >= p.Dh) continue;
-                    if (sizeof(TA) == 2) {
-                        const __nv_bfloat162 x = __floats2bfloat162_rn(acc[a][c][0].x * inv, acc[a][c][0].y * inv);
-                        const __nv_bfloat162 y = __floats2bfloat162_rn(acc[a][c][1].x * inv, acc[a][c][1].y * inv);
-                        *reinterpret_cast<uint2*>(o + d) = make_uint2(*reinterpret_cast<const uint32_t*>(&x),
-                                                                      *reinterpret_cast<const uint32_t*>(&y));
-                    } else {
-                        *reinterpret_cast<float4*>(o + d) = make_float4(acc[a][c][0].x * inv, acc[a][c][0].y * inv,
-                                                                        acc[a][c][1].x * inv, acc[a][c][1].y * inv);
-                    }
-                }
-                if (tx == 0 && p.lse != nullptr) p.lse[out] = attn_lse(m[a], l[a]);
-            }
-        } else {
-            float* s = attn_slot(p, pc.slot);
-            const int sr = p.plan.slot_rows;
-#pragma unroll
-            for (int a = 0; a < RPT; ++a) {
-                const int row = ty * RPT + a;
-                if (pc.row0 + row >= nrows) continue;
-#pragma unroll
-                for (int c = 0; c < NC; ++c)
-                    *reinterpret_cast<float4*>(s + static_cast<int64_t>(row) * DP + tx * 4 + 64 * c) =
-                        make_float4(acc[a][c][0].x, acc[a][c][0].y, acc[a][c][1].x, acc[a][c][1].y);
-                if (tx == 0) {
-                    s[static_cast<int64_t>(sr) * DP + row] = m[a];
-                    s[static_cast<int64_t>(sr) * (DP + 1) + row] = l[a];
-                }
-            }
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                const int n = atomicAdd(attn_counts(p) + pc.cnt, 1);
-                s_last = n == pc.last_cta - pc.first_cta;
-                // the counter is back at zero for the next call with this plan
-                if (s_last) attn_counts(p)[pc.cnt] = 0;
-                __threadfence();
-            }
-            __syncthreads();
-            if (s_last) {
-                const int rows = min(ROWS, nrows - pc.row0), each = (rows + 7) / 8, begin = (tid >> 5) * each;
-                attn_join<TA, DP, 4>(p, pc, begin, min(rows, begin + each), tid & 31);
-            }
-        }
+        if (RPT > 1 && pc.qlen * p.G - pc.row0 <= TY) cc_piece<TA, DP, TY, 1>(p, pc, Qs, Ps, Ks, Vs, &s_last);
+        else cc_piece<TA, DP, TY, RPT>(p, pc, Qs, Ps, Ks, Vs, &s_last);
         __syncthreads();
     }
 }
@@ -471,15 +483,15 @@ cudaError_t allow_smem(const void* kernel, std::atomic<uint64_t>& done, size_t b
     return e;
 }
 
-template <typename TA, int DP, int RPT>
+template <typename TA, int DP, int TY, int RPT>
 cudaError_t launch_cc(const AttnParams& p, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
-    constexpr size_t smem = cc_smem<TA>(DP, 16 * RPT);
-    cudaError_t e = allow_smem(reinterpret_cast<const void*>(attn_cc_kernel<TA, DP, RPT>), done, smem);
+    constexpr size_t smem = cc_smem<TA>(DP, TY * RPT);
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(attn_cc_kernel<TA, DP, TY, RPT>), done, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.plan.ncta));
-    cfg.blockDim = dim3(CC_THREADS);
+    cfg.blockDim = dim3(TY * 16);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -487,15 +499,15 @@ cudaError_t launch_cc(const AttnParams& p, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_cc_kernel<TA, DP, RPT>, p);
+    return cudaLaunchKernelEx(&cfg, attn_cc_kernel<TA, DP, TY, RPT>, p);
 }
 
 template <typename TA>
 cudaError_t launch_cc_dp(const AttnParams& p, cudaStream_t s) {
     const bool small = p.plan.tile_rows == 16;
-    if (p.Dh <= 64) return small ? launch_cc<TA, 64, 1>(p, s) : launch_cc<TA, 64, 4>(p, s);
-    if (p.Dh <= 128) return small ? launch_cc<TA, 128, 1>(p, s) : launch_cc<TA, 128, 4>(p, s);
-    return small ? launch_cc<TA, 256, 1>(p, s) : launch_cc<TA, 256, 4>(p, s);
+    if (p.Dh <= 64) return small ? launch_cc<TA, 64, 16, 1>(p, s) : launch_cc<TA, 64, 32, 4>(p, s);
+    if (p.Dh <= 128) return small ? launch_cc<TA, 128, 16, 1>(p, s) : launch_cc<TA, 128, 32, 4>(p, s);
+    return small ? launch_cc<TA, 256, 16, 1>(p, s) : launch_cc<TA, 256, 32, 2>(p, s);
 }
 
 size_t up(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
@@ -514,9 +526,10 @@ AttnPlan attn_plan_sizes(bool bf16, int64_t T, int B, int Hq, int Hk, int Dh, in
     } else {
         // up to 16 rows a sequence and key head: the 16-row tile, which wastes
         // no arithmetic on rows that are not there
-        a.tile_rows = max_q * G <= 16 ? 16 : 64;
+        a.tile_rows = max_q * G <= 16 ? 16 : dp == 256 ? 64 : 128;
         a.block_keys = attn::CC_KEYS;
-        a.ncta = (dp == 256 ? 1 : 2) * attn::sm_count();
+        // CTAs of an SM by their shared memory: two of the 16-row tile
+        a.ncta = (a.tile_rows == 16 && dp < 256 ? 2 : 1) * attn::sm_count();
     }
     a.lead = 2;
     const int64_t rows = max_q * G < a.tile_rows ? max_q * G : a.tile_rows;
