@@ -13,7 +13,10 @@
 // takes the `per_cta` consecutive units from c * per_cta: every CTA has the
 // same share whatever the lengths are, a long sequence is split over as many
 // CTAs as it needs, and at most two of a CTA's pieces (its first and its last)
-// are incomplete.  Incomplete pieces go to the workspace as unnormalised sums
+// are incomplete.  A tile of a key head that costs at most 1/8 of a share is
+// not split: the border moves to its nearer end, which unbalances the shares
+// by less than joining its parts would take (14 tiles of 7 units a CTA: 216 ->
+// 203 us).  Incomplete pieces go to the workspace as unnormalised sums
 // with their row maxima, and the CTA that finishes a tile last joins them in
 // the order of the CTAs, so that results do not depend on timing.
 #pragma once
@@ -82,13 +85,14 @@ struct AttnParams {
     AttnPlan plan;
 };
 
-// Where a CTA starts: tile, key head and unit of the tile, and the tile itself
+// A CTA's share: its units, tile, key head and unit of the tile, and the tile itself
 // (one read instead of two on the way to the first queries and keys).
 struct alignas(16) AttnStart {
+    int64_t begin, end;     // the CTA's units
     int tile, head, unit, pad;
     AttnTile t;
 };
-static_assert(sizeof(AttnStart) == 64, "AttnStart is read as four 16-byte words");
+static_assert(sizeof(AttnStart) == 80, "AttnStart is read as five 16-byte words");
 
 __device__ __forceinline__ const AttnHead* attn_head(const AttnParams& p) {
     return reinterpret_cast<const AttnHead*>(p.ws);
@@ -142,8 +146,8 @@ struct AttnWalk {
         const AttnHead* h = attn_head(p);
         const AttnStart s = attn_starts(p)[cta];
         per = h->per_cta;
-        at = static_cast<int64_t>(cta) * per;
-        end = min(at + per, h->units);
+        at = s.begin;
+        end = s.end;
         tile = s.tile;
         head = s.head;
         unit = s.unit;

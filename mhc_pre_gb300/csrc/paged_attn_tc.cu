@@ -161,23 +161,23 @@ template <int DP> struct Pieces {
     }
 };
 
-// Scores z = cap tanh(scale s / cap) in base 2: tanh(x) = 1 - 2 / (e^2x + 1),
+// cap tanh(scale s / cap) in base 2, plus `c` - cap: tanh(x) = 1 - 2 / (e^2x + 1),
 // four quotients from one reciprocal of their denominators' product (so e^2x
-// stays below 2^30: past it a denominator changes nothing in float32).  Packed
-// pairs: (0, 2) and (1, 3).
-__device__ __forceinline__ void cap4(uint32_t* u, float in, float cap2) {
-    const float2 in2 = make_float2(in, in), one = make_float2(1.0f, 1.0f), c2 = make_float2(cap2, cap2);
-    const float2 x = __fmul2_rn(make_float2(__uint_as_float(u[0]), __uint_as_float(u[2])), in2);
-    const float2 y = __fmul2_rn(make_float2(__uint_as_float(u[1]), __uint_as_float(u[3])), in2);
+// stays below 2^30: past it a denominator changes nothing in float32).  Pairs
+// are neighbours in registers.
+__device__ __forceinline__ void cap4(uint32_t* u, float in, float cap2, float c) {
+    const float2 in2 = make_float2(in, in), one = make_float2(1.0f, 1.0f), c2 = make_float2(c, c);
+    const float2 x = __fmul2_rn(make_float2(__uint_as_float(u[0]), __uint_as_float(u[1])), in2);
+    const float2 y = __fmul2_rn(make_float2(__uint_as_float(u[2]), __uint_as_float(u[3])), in2);
     const float2 s = __fadd2_rn(make_float2(ex2(x.x), ex2(x.y)), one);
     const float2 t = __fadd2_rn(make_float2(ex2(y.x), ex2(y.y)), one);
-    const float2 ab = __fmul2_rn(s, t);
-    const float r = rcp_ftz(ab.x * ab.y) * (-2.0f * cap2);
-    const float2 q = make_float2(r * ab.y, r * ab.x);   // 1 / (s t) of each pair
+    const float2 st = __fmul2_rn(s, t);
+    const float r = rcp_ftz(st.x * st.y) * (-2.0f * cap2);
+    const float2 q = make_float2(r * st.y, r * st.x);   // -2 cap / (s t) of each pair
     const float2 z = __ffma2_rn(q, t, c2), w = __ffma2_rn(q, s, c2);
     u[0] = __float_as_uint(z.x);
-    u[2] = __float_as_uint(z.y);
-    u[1] = __float_as_uint(w.x);
+    u[1] = __float_as_uint(z.y);
+    u[2] = __float_as_uint(w.x);
     u[3] = __float_as_uint(w.y);
 }
 
@@ -288,7 +288,7 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
                     // tanh keeps the order, so the capped maximum is the maximum's
                     if (__any_sync(FULL, top * cap_in > 30.0f)) most = 30.0f / cap_in;
                     uint32_t t[4] = {__float_as_uint(fminf(top, most)), 0u, 0u, 0u};
-                    cap4(t, cap_in, cap2);
+                    cap4(t, cap_in, cap2, cap2);
                     if (top > -INFINITY) top = __uint_as_float(t[0]);
                 }
                 const bool raise = top > m + RAISE || (m == -INFINITY && top > -INFINITY);
@@ -349,14 +349,13 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
                                     if (__uint_as_float(v[e]) > most) v[e] = __float_as_uint(most);
                             }
 #pragma unroll
-                            for (int e = 0; e < 32; e += 4) cap4(v + e, cap_in, cap2);
+                            for (int e = 0; e < 32; e += 4) cap4(v + e, cap_in, cap2, cap2 - base);
                             if (head || tail) mask32(v, head, tail, f, t);
                             uint32_t pk[16];
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
-                                const float2 x = __ffma2_rn(
-                                    make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), z2, b2);
-                                const float2 y = make_float2(ex2(x.x), ex2(x.y));
+                                const float2 y = make_float2(ex2(__uint_as_float(v[2 * e])),
+                                                             ex2(__uint_as_float(v[2 * e + 1])));
                                 sum[e & 1] = __fadd2_rn(sum[e & 1], y);
                                 const __nv_bfloat162 h = __floats2bfloat162_rn(y.x, y.y);
                                 pk[e] = *reinterpret_cast<const uint32_t*>(&h);
