@@ -410,86 +410,26 @@ def mhc_pre_bwd_noalloc(g_in, dH_post, dH_res, x, phi, b, alpha, proj, inv_rms,
 # ------------------------------------------------------ attention sublayer
 #
 # These calls are made once per layer in a decoding step, where the host's time
-# is the call's time: each tensor's attributes are read once, and the checks
-# are plain comparisons.
+# is the call's time: their checks and marshalling are in a CPython module
+# (csrc/py_attn.cpp) linked to the library.
 
-_I32, _I64T, _F32, _BF16 = torch.int32, torch.int64, torch.float32, torch.bfloat16
-_CODES = {_BF16: MHC_BF16, _F32: MHC_F32}
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _stream_of(t: torch.Tensor) -> int:
-    return _raw_stream(t.get_device()) if _raw_stream is not None else _stream(t.device)
+CALLS_PATH = os.path.join(os.path.dirname(LIB_PATH), "_attn_calls.so")
+_calls_module = None
 
 
-def _code(dtype) -> int:
-    c = _CODES.get(dtype)
-    if c is None:
-        raise TypeError(f"activations must be bfloat16 or float32, got {dtype}")
-    return c
-
-
-def _refuse_host():
-    raise ValueError("the mHC library takes CUDA tensors only")
-
-
-def _heads(t: torch.Tensor, name: str, dtype, T: int, H: int, Dh: int):
-    """Address and token distance of a tensor of heads [T, H, Dh]; the tokens
-    may be apart (a part of a packed projection), a token's heads are not."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_cuda:
-        _refuse_host()
-    st, sh, sd = t.stride()
-    if (sd != 1 and Dh > 1) or (sh != Dh and H > 1):
-        raise ValueError(f"{name}: the heads of a token must lie one after the other")
-    return t.data_ptr(), st if T > 1 else H * Dh
-
-
-def _flat(t: torch.Tensor, name: str, dtype, n: int) -> int:
-    """Address of a dense tensor of n entries."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.numel() != n:
-        raise ValueError(f"{name} must have {n} entries, got {t.numel()}")
-    if not t.is_cuda:
-        _refuse_host()
-    if not t.is_contiguous():
-        raise ValueError("the mHC library takes contiguous tensors only")
-    return t.data_ptr()
-
-
-def _rope(positions, cos_sin, T):
-    """The arguments positions, cos_sin, max_pos, and rot."""
-    if cos_sin is None:
-        return None, None, 0, 0
-    max_pos, rot = cos_sin.shape
-    return _flat(positions, "positions", _I32, T), _flat(cos_sin, "cos_sin", _F32, max_pos * rot), max_pos, rot
-
-
-def _cache(t: torch.Tensor, name: str, dtype, shape):
-    """Address and (page, slot, head) distances of a cache [pages, page_size, Hk, Dh]
-    in any memory order that keeps a head's values together."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_cuda:
-        _refuse_host()
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    P, ps, H, D = shape
-    sp, ss, sh, sd = t.stride()
-    if sd != 1 and D > 1:
-        raise ValueError(f"{name}: the values of a head must lie one after the other")
-    return t.data_ptr(), sp if P > 1 else ps * H * D, ss if ps > 1 else H * D, sh if H > 1 else D
-
-
-def _same_tokens(q, k):
-    """T, Hq, Hk, Dh of q and k."""
-    T, Hq, Dh = q.shape
-    Tk, Hk, Dk = k.shape
-    if Tk != T or Dk != Dh:
-        raise ValueError("q and k must have the same tokens and head size")
-    return T, Hq, Hk, Dh
+def _calls():
+    """The module, loaded once."""
+    global _calls_module
+    if _calls_module is None:
+        lib()
+        if not os.path.exists(CALLS_PATH):
+            raise RuntimeError(f"{CALLS_PATH} is missing: build it with `python -m mhc_pre_gb300.build`")
+        from . import _attn_calls
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _attn_calls.setup(torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8,
+                          raw or (lambda i: torch.cuda.current_stream(i).cuda_stream))
+        _calls_module = _attn_calls
+    return _calls_module
 
 
 def mhc_qk_norm_rope(q, k, w_q, w_k, positions=None, cos_sin=None, eps: float = 1e-6,
@@ -497,51 +437,21 @@ def mhc_qk_norm_rope(q, k, w_q, w_k, positions=None, cos_sin=None, eps: float = 
     """Per-head RMSNorm of q [T, Hq, Dh] and k [T, Hk, Dh], then the rotation of
     the first cos_sin.shape[1] values of each head by cos_sin[positions]
     (cosines, then sines).  ``interleaved``: pairs (2j, 2j + 1)."""
-    T, Hq, Hk, Dh = _same_tokens(q, k)
-    dt, dev = q.dtype, q.device
-    wq, wk = _flat(w_q, "w_q", _F32, Dh), _flat(w_k, "w_k", _F32, Dh)
-    qp, qs = _heads(q, "q", dt, T, Hq, Dh)
-    kp, ks = _heads(k, "k", dt, T, Hk, Dh)
-    pos, cs, max_pos, rot = _rope(positions, cos_sin, T)
-    out = QKOut(_empty((T, Hq, Dh), dtype=dt, device=dev), _empty((T, Hk, Dh), dtype=dt, device=dev))
-    st = (_lib or lib()).mhc_qk_norm_rope(
-        _code(dt), qp, qs, kp, ks, wq, wk, pos, cs, max_pos, T, Hq, Hk, Dh, rot,
-        ROPE_ADJACENT if interleaved else 0, eps, out.q.data_ptr(), Hq * Dh, out.k.data_ptr(), Hk * Dh, _stream_of(q))
-    _check(st, "mhc_qk_norm_rope")
-    return out
+    st, qo, ko = (_calls_module or _calls()).qk_norm_rope(_empty, q, k, w_q, w_k, positions, cos_sin, eps,
+                                                          ROPE_ADJACENT if interleaved else 0)
+    if st:
+        _check(st, "mhc_qk_norm_rope")
+    return QKOut(qo, ko)
 
 
 def mhc_qk_norm_rope_bwd(g_q, g_k, q, k, w_q, w_k, positions=None, cos_sin=None, eps: float = 1e-6,
                          interleaved: bool = False, dq=None, dk=None):
     """Gradients of <g_q, q_out> + <g_k, k_out> for mhc_qk_norm_rope.  ``dq`` and
     ``dk`` (parts of a packed gradient, say) are written when given."""
-    T, Hq, Hk, Dh = _same_tokens(q, k)
-    dt, dev = q.dtype, q.device
-    if g_q.shape != q.shape or g_k.shape != k.shape:
-        raise ValueError("q, k and their gradients must have the same shapes")
-    if dq is None:
-        dq = _empty((T, Hq, Dh), dtype=dt, device=dev)
-    if dk is None:
-        dk = _empty((T, Hk, Dh), dtype=dt, device=dev)
-    if dq.shape != q.shape or dk.shape != k.shape:
-        raise ValueError("dq and dk must have the shapes of q and k")
-    wq, wk = _flat(w_q, "w_q", _F32, Dh), _flat(w_k, "w_k", _F32, Dh)
-    L = _lib or lib()
-    gqp, gqs = _heads(g_q, "g_q", dt, T, Hq, Dh)
-    gkp, gks = _heads(g_k, "g_k", dt, T, Hk, Dh)
-    qp, qs = _heads(q, "q", dt, T, Hq, Dh)
-    kp, ks = _heads(k, "k", dt, T, Hk, Dh)
-    dqp, dqs = _heads(dq, "dq", dt, T, Hq, Dh)
-    dkp, dks = _heads(dk, "dk", dt, T, Hk, Dh)
-    pos, cs, max_pos, rot = _rope(positions, cos_sin, T)
-    dw_q, dw_k = _empty((Dh,), dtype=_F32, device=dev), _empty((Dh,), dtype=_F32, device=dev)
-    need = L.mhc_qk_norm_rope_bwd_workspace_bytes(T, Dh)
-    ws = _empty((need or 16,), dtype=torch.uint8, device=dev)
-    st = L.mhc_qk_norm_rope_bwd(
-        _code(dt), gqp, gqs, gkp, gks, qp, qs, kp, ks, wq, wk, pos, cs, max_pos, T, Hq, Hk, Dh, rot,
-        ROPE_ADJACENT if interleaved else 0, eps, dqp, dqs, dkp, dks, dw_q.data_ptr(), dw_k.data_ptr(),
-        ws.data_ptr(), need, _stream_of(q))
-    _check(st, "mhc_qk_norm_rope_bwd")
+    st, dq, dk, dw_q, dw_k = (_calls_module or _calls()).qk_norm_rope_bwd(
+        _empty, g_q, g_k, q, k, w_q, w_k, positions, cos_sin, eps, ROPE_ADJACENT if interleaved else 0, dq, dk)
+    if st:
+        _check(st, "mhc_qk_norm_rope_bwd")
     return QKBwdOut(dq, dk, dw_q, dw_k)
 
 
@@ -550,25 +460,11 @@ def mhc_qk_norm_rope_append(q, k, v, w_q, w_k, k_cache, v_cache, slots, position
     """The serving form: returns the normalised, rotated q; the keys (likewise)
     and the values go to slots[t] = page * page_size + place of the caches
     [pages, page_size, Hk, Dh] (-1: nowhere), in place."""
-    T, Hq, Hk, Dh = _same_tokens(q, k)
-    dt = q.dtype
-    if v.shape != k.shape:
-        raise ValueError("k and v must have the same shape")
-    shape = k_cache.shape
-    if len(shape) != 4 or shape[2] != Hk or shape[3] != Dh:
-        raise ValueError(f"k_cache must be [pages, page_size, {Hk}, {Dh}], got {tuple(shape)}")
-    wq, wk = _flat(w_q, "w_q", _F32, Dh), _flat(w_k, "w_k", _F32, Dh)
-    qp, qs = _heads(q, "q", dt, T, Hq, Dh)
-    kp, ks = _heads(k, "k", dt, T, Hk, Dh)
-    vp, vs = _heads(v, "v", dt, T, Hk, Dh)
-    pos, cs, max_pos, rot = _rope(positions, cos_sin, T)
-    kc, kpg, ksl, kh = _cache(k_cache, "k_cache", dt, shape)
-    vc, vpg, vsl, vh = _cache(v_cache, "v_cache", dt, shape)
-    out = _empty((T, Hq, Dh), dtype=dt, device=q.device)
-    st = (_lib or lib()).mhc_qk_norm_rope_append(
-        _code(dt), qp, qs, kp, ks, vp, vs, wq, wk, pos, cs, max_pos, _flat(slots, "slots", _I64T, T), T, Hq, Hk, Dh, rot, ROPE_ADJACENT if interleaved else 0,
-        eps, out.data_ptr(), Hq * Dh, kc, kpg, ksl, kh, vc, vpg, vsl, vh, shape[0], shape[1], _stream_of(q))
-    _check(st, "mhc_qk_norm_rope_append")
+    st, out = (_calls_module or _calls()).qk_norm_rope_append(
+        _empty, q, k, v, w_q, w_k, k_cache, v_cache, slots, positions, cos_sin, eps,
+        ROPE_ADJACENT if interleaved else 0)
+    if st:
+        _check(st, "mhc_qk_norm_rope_append")
     return out
 
 
@@ -578,13 +474,18 @@ def mhc_paged_attn_plan(cu_q, kv_lens, dtype, T: int, Hq: int, Hk: int, Dh: int,
     same sizes (the layers of one step).  Calls that share a plan share its
     workspace: they must not overlap."""
     B = kv_lens.numel()
-    L = _lib or lib()
-    code = _code(dtype)
-    need = L.mhc_paged_attn_workspace_bytes(code, T, B, Hq, Hk, Dh, page_size, max_q)
-    ws = _empty((need or 16,), dtype=torch.uint8, device=cu_q.device)
-    st = L.mhc_paged_attn_plan(code, _flat(cu_q, "cu_q", _I32, B + 1), _flat(kv_lens, "kv_lens", _I32, B), T, B,
-                               Hq, Hk, Dh, page_size, max_q, max_kv, window, ws.data_ptr(), need,
-                               _stream_of(cu_q))
+    for t, name, n in ((cu_q, "cu_q", B + 1), (kv_lens, "kv_lens", B)):
+        if t.dtype != torch.int32:
+            raise TypeError(f"{name} must be {torch.int32}, got {t.dtype}")
+        if t.numel() != n:
+            raise ValueError(f"{name} must have {n} entries, got {t.numel()}")
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"activations must be bfloat16 or float32, got {dtype}")
+    code = MHC_BF16 if dtype == torch.bfloat16 else MHC_F32
+    need = int(lib().mhc_paged_attn_workspace_bytes(code, T, B, Hq, Hk, Dh, page_size, max_q))
+    ws = _empty((max(need, 16),), dtype=torch.uint8, device=cu_q.device)
+    st = lib().mhc_paged_attn_plan(code, _ptr(cu_q), _ptr(kv_lens), T, B, Hq, Hk, Dh, page_size, max_q, max_kv,
+                                   window, _ptr(ws), need, _stream(cu_q.device))
     _check(st, "mhc_paged_attn_plan")
     return PagedAttnPlan(ws, (code, T, B, Hq, Hk, Dh, page_size, max_q, max_kv, window))
 
@@ -600,58 +501,20 @@ def mhc_paged_attn(q, k_cache, v_cache, page_table, cu_q=None, kv_lens=None, max
     mhc_paged_attn_plan) takes the place of cu_q and kv_lens and brings its own
     max_q, max_kv and window.  ``out``: a tensor for o; rows of no sequence stay
     as they are.  Returns o and lse [T, Hq]."""
-    T, Hq, Dh = q.shape
-    dt, dev = q.dtype, q.device
-    code = _code(dt)
-    shape = k_cache.shape
-    if len(shape) != 4 or shape[3] != Dh:
-        raise ValueError(f"k_cache must be [pages, page_size, heads, {Dh}], got {tuple(shape)}")
-    P, page_size, Hk, _ = shape
-    B, width = page_table.shape
-    L = _lib or lib()
-    if plan is None:
-        max_q = T if max_q is None else max_q
-        max_kv = width * page_size if max_kv is None else max_kv
-        window = window or 0
-        need = L.mhc_paged_attn_workspace_bytes(code, T, B, Hq, Hk, Dh, page_size, max_q)
-        ws = _empty((need or 16,), dtype=torch.uint8, device=dev)
-        cu, kv = _flat(cu_q, "cu_q", _I32, B + 1), _flat(kv_lens, "kv_lens", _I32, B)
-    else:
+    ws = None
+    if plan is not None:
         ws, sizes = plan
-        mine = tuple(a if b is None else b for a, b in zip(sizes[7:], (max_q, max_kv, window)))
-        want = (code, T, B, Hq, Hk, Dh, page_size) + mine
+        max_q, max_kv, window = (a if b is None else b for a, b in zip(sizes[7:], (max_q, max_kv, window)))
+        code = MHC_BF16 if q.dtype == torch.bfloat16 else MHC_F32
+        want = (code, q.shape[0], page_table.shape[0], q.shape[1], k_cache.shape[2], q.shape[2], k_cache.shape[1],
+                max_q, max_kv, window)
         if want != sizes or cu_q is not None or kv_lens is not None:
             raise ValueError(f"the plan has its own lengths and sizes: {sizes}, not {want}")
-        max_q, max_kv, window = mine
-        need = ws.numel()
-        cu = kv = None
-    if page_table.dtype is not _I32:
-        raise TypeError(f"page_table must be {_I32}, got {page_table.dtype}")
-    if not page_table.is_cuda:
-        _refuse_host()
-    if width * page_size < max_kv:
-        raise ValueError(f"page_table holds {width * page_size} tokens a sequence, max_kv is {max_kv}")
-    row, col = page_table.stride()
-    if col != 1 and width > 1:
-        raise ValueError("page_table: the pages of a sequence must lie one after the other")
-    qp, qs = _heads(q, "q", dt, T, Hq, Dh)
-    kc, kpg, ksl, kh = _cache(k_cache, "k_cache", dt, shape)
-    vc, vpg, vsl, vh = _cache(v_cache, "v_cache", dt, shape)
-    if out is None:
-        out = _empty((T, Hq, Dh), dtype=dt, device=dev)
-        op = out.data_ptr()
-    else:
-        op = _flat(out, "out", dt, T * Hq * Dh)
-        if out.shape != q.shape:
-            raise ValueError("out must have the shape of q")
-    lse = _empty((T, Hq), dtype=_F32, device=dev)
-    st = L.mhc_paged_attn(
-        code, qp, qs, kc, kpg, ksl, kh, vc, vpg, vsl, vh, P, page_size, page_table.data_ptr(),
-        row if B > 1 else width, cu, kv, T, B, Hq, Hk, Dh, max_q, max_kv, window,
-        Dh ** -0.5 if scale is None else scale, softcap, op, lse.data_ptr(), ws.data_ptr(), need,
-        _stream_of(q))
-    _check(st, "mhc_paged_attn")
-    return PagedAttnOut(out, lse)
+    st, o, lse = (_calls_module or _calls()).paged_attn(
+        _empty, q, k_cache, v_cache, page_table, cu_q, kv_lens, max_q, max_kv, scale, window or 0, softcap, ws, out)
+    if st:
+        _check(st, "mhc_paged_attn")
+    return PagedAttnOut(o, lse)
 
 
 def get_last_device_error(device=None) -> int:

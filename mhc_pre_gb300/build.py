@@ -11,12 +11,14 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmhc_gb300.so")
+CALLS = os.path.join(HERE, "_attn_calls.so")     # CPython module that calls the library
 
 SOURCES = ["mhc_abi.cu", "kernels_fwd.cu", "kernels_bwd.cu", "pre_tc.cu", "pre_bwd_tc.cu",
            "pre_bwd_fused.cu",
@@ -56,14 +58,27 @@ def _compile(nvcc: str, src: str, extra) -> str:
     return obj
 
 
+def _build_calls(nvcc: str) -> None:
+    """The Python module of the attention sublayer's calls, linked to the library."""
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+    tmp = CALLS + ".tmp"
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-Wall", "-I", sysconfig.get_paths()["include"], "-I",
+           os.path.join(cuda, "include"), os.path.join(CSRC, "py_attn.cpp"), "-o", tmp, LIB, "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on py_attn.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+
+
 def build(verbose: bool = False, extra_flags=()) -> str:
-    """Builds the library if any source is newer than it; returns its path."""
+    """Builds the library and its Python module if any source is newer than
+    they are; returns the library's path."""
     os.makedirs(BUILD, exist_ok=True)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     deps.append(os.path.join(INCLUDE, "mhc.h"))
     deps.append(os.path.abspath(__file__))
-    if os.path.exists(LIB) and not extra_flags:
-        lib_mtime = os.path.getmtime(LIB)
+    if os.path.exists(LIB) and os.path.exists(CALLS) and not extra_flags:
+        lib_mtime = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
         if all(os.path.getmtime(d) <= lib_mtime for d in deps):
             return LIB
     nvcc = _nvcc()
@@ -77,6 +92,7 @@ def build(verbose: bool = False, extra_flags=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _build_calls(nvcc)
     if verbose:
         print(f"built {LIB}")
     return LIB

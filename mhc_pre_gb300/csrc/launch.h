@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace mhc {
 
 // Record per token written by the pre backward's per-token kernel (floats).
@@ -98,6 +100,17 @@ bool pre_bwd_tc_supports(int64_t T, int64_t D);
 cudaError_t launch_pre_bwd_tc_main(const void* g_in, const void* x, const float* phi, const float* rec,
                                    int64_t T, int64_t D, int64_t nb, void* dx, float* part,
                                    cudaStream_t s);
+
+// SMs of the current device (asked once per device).
+inline int sm_count() {
+    static std::atomic<int> known[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+    if (dev >= 0 && dev < 64 && (n = known[dev].load()) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
+    if (dev >= 0 && dev < 64) known[dev].store(n);
+    return n;
+}
 
 // ---------------------------------------------------------------------------
 // The attention sublayer between mhc_pre and mhc_post (qk_norm_rope.cu,

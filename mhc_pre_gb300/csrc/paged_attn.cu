@@ -485,14 +485,6 @@ attn_cc_kernel(const AttnParams p) {
     }
 }
 
-int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-        return 148;
-    return n;
-}
-
 // cudaFuncSetAttribute once per device and kernel (idempotent, so a race is harmless).
 cudaError_t allow_smem(const void* kernel, std::atomic<uint64_t>& done, size_t bytes) {
     int dev = 0;
@@ -544,14 +536,14 @@ AttnPlan attn_plan_sizes(bool bf16, int64_t T, int B, int Hq, int Hk, int Dh, in
         a.lane_rows = static_cast<int>(128 / G * G);
         a.tile_rows = (max_q * G <= a.lane_rows ? 1 : 2) * a.lane_rows;
         a.block_keys = 128;
-        a.ncta = attn::sm_count();
+        a.ncta = sm_count();
     } else {
         // up to 16 rows a sequence and key head: the 16-row tile, which wastes
         // no arithmetic on rows that are not there
         a.tile_rows = max_q * G <= 16 ? 16 : dp == 256 ? 64 : 128;
         a.block_keys = attn::CC_KEYS;
         // CTAs of an SM by their shared memory: two of the 16-row tile
-        a.ncta = (a.tile_rows == 16 && dp < 256 ? 2 : 1) * attn::sm_count();
+        a.ncta = (a.tile_rows == 16 && dp < 256 ? 2 : 1) * sm_count();
     }
     if (a.ncta > attn::PLAN_CTAS) a.ncta = attn::PLAN_CTAS;
     a.lead = 2;   // 1, 2 and 3 take 191, 157 and 163 us for 4096 new tokens, 132, 131 and 132 us for 64 sequences decoding

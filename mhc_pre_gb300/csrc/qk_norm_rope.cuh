@@ -339,14 +339,6 @@ __device__ __forceinline__ bool start_token(const P& p, const int64_t* slots, in
 
 // ------------------------------------------------------------------ host ---
 
-inline int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-        return 148;
-    return n;
-}
-
 inline int lanes_per_head(int Dh) {
     int l = 8;
     while (l * 8 < Dh) l *= 2;

@@ -282,7 +282,7 @@ cudaError_t launch_bwd(const QkBwdParams& p, int64_t* nblk, cudaStream_t s) {
 
 // Most blocks a backward launch has, each with one partial of dw.
 int64_t qk_bwd_blocks(int64_t T) {
-    const int64_t most = 6ll * qk::sm_count();
+    const int64_t most = 6ll * sm_count();
     return T < most ? T : most;
 }
 
