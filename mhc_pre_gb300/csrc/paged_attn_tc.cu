@@ -201,9 +201,12 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
     auto bar = [&](int i) { return sbase + C::BARS + 8u * static_cast<uint32_t>(i); };
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC + 4);
     float* ml = reinterpret_cast<float*>(smem + C::ML);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // what is the same in every lane of the warp is said to be: it then lives
+    // in uniform registers
+    auto same = [](int v) { return __shfl_sync(FULL, v, 0); };
+    const int warp = same(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int L = warp >> 2, w4 = warp & 3, row_t = w4 * 32 + lane;
-    const uint32_t t_lane = tmem + (static_cast<uint32_t>(w4 * 32) << 16);
+    const uint32_t t_lane = same(tmem) + (static_cast<uint32_t>(w4 * 32) << 16);
     const uint32_t t_s = t_lane + S_COL + L * 128, t_o = t_lane + O_COL + L * 128;
     const float zscale = CAP ? 1.0f : p.scale * LOG2E;
     const float cap2 = p.softcap * LOG2E, cap_in = CAP ? 2.0f * LOG2E * p.scale / p.softcap : 0.0f;
@@ -216,16 +219,18 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
     while (ok) {
         const AttnPiece& pc = pieces.get(ok);
         if (!ok || pc.nb == 0) break;
-        const int lane_rows = p.plan.lane_rows, nrows = pc.qlen * p.G;
-        const bool pair = nrows - pc.row0 > lane_rows;
-        const int mine = pair ? pc.nb : (pc.nb + 1 - L) / 2;    // blocks of this lane
+        const int lane_rows = p.plan.lane_rows, left = same(pc.qlen * p.G - pc.row0);
+        const bool pair = left > lane_rows;
+        const int nb = same(pc.nb), blk = same(pc.blk);
+        const int mine = pair ? nb : (nb + 1 - L) / 2;          // blocks of this lane
         const int rt = (pair ? L * lane_rows : 0) + row_t;      // row of the tile
-        const int r = pc.row0 + rt, blk = pc.blk;
-        const bool valid = row_t < lane_rows && r < nrows;
+        const int r = pc.row0 + rt;
+        const bool valid = row_t < lane_rows && rt < left;
         const bool active = __any_sync(FULL, valid);            // a warp without rows only keeps the protocol
         int lo = 0, hi = 0x7fffffff;                            // rows that are not there need no mask
         const int tok = attn_token(p, valid ? r : 0);
         if (valid) attn_token_keys(pc, tok, p.window, lo, hi);
+        const int lo_most = __reduce_max_sync(FULL, lo), hi_least = __reduce_min_sync(FULL, hi);
         float m = -INFINITY, l = 0.0f;
         if (lent) {
             ok = wait_warp(bar(C::B_XE + w4), par_x, abort_flag);
@@ -245,7 +250,7 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
                 // 32 at a time with the next 32 on their way: the capping's code
                 // over all 128 is so long that the warps wait for instructions.
                 // Exponentials overwrite scores already read.
-                const bool head = __any_sync(FULL, k0 < lo), tail = __any_sync(FULL, k0 + KEYS > hi);
+                const bool head = k0 < lo_most, tail = k0 + KEYS > hi_least;
                 const int from = lo - k0, to = hi - k0;
                 constexpr int HELD = CAP ? 64 : 128;
                 uint32_t u[HELD];
@@ -415,7 +420,7 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
             w1 *= inv;
             const int64_t out = valid ? (pc.q0 + tok) * p.Hq + pc.head * p.G + (r - tok * p.G) : 0;
             float* part = attn_slot(p, pc.slot);
-            const bool both = !pair && pc.nb > 1;
+            const bool both = !pair && nb > 1;
 #pragma unroll 1
             for (int c = 0; c < DP / 32; ++c) {
                 uint32_t o[32];
