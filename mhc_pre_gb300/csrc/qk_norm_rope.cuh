@@ -246,7 +246,7 @@ struct Ring {
     int sizes[4];         // their bytes, 0: no such row
     int angles, note;     // byte offsets
     int stage_bytes, stages;
-    int team_warps;       // 1 or 4
+    int team_warps;       // 1, 2 or 4
 };
 
 __device__ __forceinline__ bool wait_full(uint32_t bar, uint32_t parity) {
@@ -353,10 +353,19 @@ struct RingPlan {
     size_t smem;
 };
 constexpr int SM_SMEM = 224 * 1024;
-constexpr int TEAM_BYTES = 6 * 1024;   // larger rows: a team of four warps (see below)
 
-// `most`: blocks of an SM that the kernel's registers allow.
-inline RingPlan plan_ring(const int (&sizes)[4], int nrows, int rot, int64_t T, int most) {
+// `values`: elements of a token's rows; `most`: blocks of an SM that the
+// kernel's registers allow.
+//
+// A team's warps share the fixed work of a token (its barrier, angles and
+// coefficients), so a team is as small as a token's rows allow: one warp up to
+// 3072 values, two up to 6144, four above; but each team wants several tokens,
+// or the last round leaves teams idle.  Forward, 32768 tokens of 48 heads of
+// 128 (6144 values): 189, 138 and 145 us with one, two and four warps; 24 heads
+// of 128: 74, 76 and 109; 9 heads of 128: 38, 51 and 77.  4096 tokens of 24
+// heads: 17.9, 12.4 and 15.1.  Backward, 48 heads (12288 values): 378, 247 and
+// 194; 24 heads: 131, 103 and 141.
+inline RingPlan plan_ring(const int (&sizes)[4], int nrows, int rot, int64_t T, int values, int most) {
     RingPlan r = {};
     int at = 0;
     for (int i = 0; i < nrows; ++i) {
@@ -364,25 +373,31 @@ inline RingPlan plan_ring(const int (&sizes)[4], int nrows, int rot, int64_t T, 
         r.ring.sizes[i] = sizes[i];
         at += (sizes[i] + 127) & ~127;
     }
-    const int bytes = at;
     r.ring.angles = at;
     at += (rot * 4 + 127) & ~127;
     r.ring.note = at;
     r.ring.stage_bytes = at + 128;
-    r.ring.team_warps = bytes >= TEAM_BYTES ? 4 : 1;
-    const int teams = THREADS / 32 / r.ring.team_warps, sms = sm_count();
-    // The most blocks of an SM that have two stages or more each: all of an
-    // SM's stages together are what is in flight.
-    for (int per_sm = most; per_sm >= 1; --per_sm) {
-        const int each = SM_SMEM / per_sm - 1024 - teams * 8 * 16;
-        const int stages = each / (teams * r.ring.stage_bytes);
-        if (stages >= 2) {
-            r.ring.stages = stages < 8 ? stages : 8;
-            r.blocks = per_sm * sms;
-            break;
+    const int sms = sm_count();
+    int teams = 1;
+    for (int warps = values <= 3072 ? 1 : values <= 6144 ? 2 : 4; warps <= 4; warps *= 2) {
+        teams = THREADS / 32 / warps;
+        r.ring.team_warps = warps;
+        r.ring.stages = 0;
+        // The most blocks of an SM that have two stages or more each: all of an
+        // SM's stages together are what is in flight.
+        for (int per_sm = most; per_sm >= 1; --per_sm) {
+            const int each = SM_SMEM / per_sm - 1024 - teams * 8 * 16;
+            const int stages = each / (teams * r.ring.stage_bytes);
+            if (stages >= 2) {
+                r.ring.stages = stages < 8 ? stages : 8;
+                r.blocks = per_sm * sms;
+                break;
+            }
         }
+        const int64_t tokens = warps == 1 ? 8 : 2;   // of a team, at least
+        if (r.ring.stages > 0 && T >= tokens * r.blocks * teams) break;
     }
-    // fewer than two tokens for every team: the direct kernels
+    // fewer than two tokens even for every team of four: the direct kernels
     if (r.ring.stages == 0 || T < 2ll * r.blocks * teams) {
         r.ring.stages = 0;
         return r;

@@ -65,8 +65,9 @@ def test_attention_stays_inside(lens, Hq, Hk, dh, page, dtype, monkeypatch):
     (1700, 40, 8, 128, 128, "bf16", False),    # four warps a token
     (1650, 10, 2, 128, 64, "f32", True),
     (400, 64, 8, 256, 256, "f32", False),      # stages of 72 KB, one block an SM
-    (6200, 2, 1, 64, 64, "bf16", True),        # a warp a token
+    (6200, 2, 1, 64, 64, "bf16", True),        # two warps a token
     (6300, 4, 4, 40, 32, "f32", False),
+    (24500, 2, 1, 64, 32, "bf16", False),      # a warp a token
 ])
 def test_many_tokens(T, Hq, Hk, dh, rot, dtype, adjacent):
     """Batches that the staged kernels take: every 37th token and the last ones
