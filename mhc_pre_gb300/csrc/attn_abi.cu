@@ -306,6 +306,8 @@ mhc_status mhc_paged_attn(mhc_dtype dt, const void* q, int64_t q_stride, const v
     p.v_slot_stride = v_slot_stride;
     p.v_head_stride = v_head_stride;
     p.T = T;
+    p.max_q = max_q;
+    p.max_kv = max_kv;
     p.B = B;
     p.Hq = Hq;
     p.Hk = Hk;

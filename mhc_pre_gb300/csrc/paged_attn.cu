@@ -33,9 +33,10 @@ cudaError_t read_and_clear_attn_error(unsigned* word) {
 namespace attn {
 
 constexpr int PLAN_THREADS = 512;   // also at least PLAN_CTAS
+constexpr int PLAN_NEAR = 256;
 constexpr int SMALL_TILE = 8;       // tiles below 1/8 of a CTA's share are not split
 constexpr int PLAN_CTAS = 512;      // most CTAs of a launch
-constexpr int PLAN_TILES = 4096;    // tile starts kept in shared memory for the CTAs' search
+constexpr int PLAN_TILES = 2048;    // tile starts kept in shared memory for the CTAs' search
 
 struct PlanParams {
     const int32_t *cu_q, *kv_lens;
@@ -76,6 +77,7 @@ attn_plan_kernel(const PlanParams p) {
     __shared__ int tile_base[PLAN_THREADS + 1];
     __shared__ int s_q0[PLAN_THREADS], s_qlen[PLAN_THREADS], s_kvlen[PLAN_THREADS];
     __shared__ int64_t s_start[PLAN_TILES];
+    __shared__ AttnTile s_tile[PLAN_NEAR];   // the first tiles again, for the borders
     ptx::griddep_launch_dependents();
     const int tid = threadIdx.x;
     AttnTile* tiles = reinterpret_cast<AttnTile*>(p.ws + p.plan.tile_off);
@@ -140,6 +142,7 @@ attn_plan_kernel(const PlanParams p) {
             if (on) {
                 tiles[ntiles + i] = t;
                 if (ntiles + i < PLAN_TILES) s_start[ntiles + i] = t.start;
+                if (ntiles + i < PLAN_NEAR) s_tile[ntiles + i] = t;
             }
         }
         ntiles = static_cast<int>(min(static_cast<int64_t>(ntiles) + all, p.plan.max_tiles));
@@ -154,6 +157,8 @@ attn_plan_kernel(const PlanParams p) {
         h->units = units;
         h->per_cta = per;
         h->T = p.T;
+        h->max_q = p.max_q;
+        h->max_kv = p.max_kv;
         h->ntiles = ntiles;
         h->ncta = p.plan.ncta;
         h->Hq = p.Hq;
@@ -176,7 +181,7 @@ attn_plan_kernel(const PlanParams p) {
             if (st <= u) lo = mid;
             else hi = mid - 1;
         }
-        s.t = tiles[lo];
+        s.t = lo < PLAN_NEAR ? s_tile[lo] : tiles[lo];
         const int cost = s.t.nblk + p.plan.lead;
         const int64_t in = u - s.t.start;
         s.tile = lo;
@@ -189,7 +194,8 @@ attn_plan_kernel(const PlanParams p) {
                 u += cost - s.unit;
                 if (++s.head == p.Hk && u < units) {
                     s.head = 0;
-                    s.t = tiles[++s.tile];
+                    ++s.tile;
+                    s.t = s.tile < PLAN_NEAR ? s_tile[s.tile] : tiles[s.tile];
                 }
             }
             s.unit = 0;
@@ -453,7 +459,7 @@ __device__ __forceinline__ void cc_piece(const AttnParams& p, const AttnPiece& p
         __syncthreads();
         if (*s_last) {
             const int rows = min(p.plan.tile_rows, nrows - pc.row0), each = (rows + TY / 2 - 1) / (TY / 2), begin = (tid >> 5) * each;
-            attn_join<TA, DP, 4>(p, pc, begin, min(rows, begin + each), tid & 31);
+            attn_join<TA, DP, 4, 2>(p, pc, begin, min(rows, begin + each), tid & 31);
         }
     }
 }

@@ -50,7 +50,8 @@ static_assert(sizeof(AttnTile) == 48, "AttnTile is read as three 16-byte words")
 struct AttnHead {       // start of the plan
     int64_t units;      // all units
     int64_t per_cta;    // units of a CTA
-    int64_t T;          // rows of q, for the check that plan and call agree
+    int64_t T;          // this and the sizes below: for the check that plan and call agree
+    int64_t max_q, max_kv;
     int ntiles;
     int ncta;
     int Hq, Hk, B, tile_rows, block_keys, window, lead;
@@ -77,7 +78,7 @@ struct AttnParams {
     int64_t q_stride, table_stride, num_pages;
     int64_t k_page_stride, k_slot_stride, k_head_stride;
     int64_t v_page_stride, v_slot_stride, v_head_stride;
-    int64_t T;
+    int64_t T, max_q, max_kv;
     int B, Hq, Hk, G, Dh, page_size, page_shift, window;
     unsigned g_mul, g_shift;       // r / G = umulhi(r, g_mul) >> g_shift for 0 <= r < 2^31
     float scale, softcap;
@@ -107,12 +108,13 @@ __device__ __forceinline__ int* attn_counts(const AttnParams& p) {
     return reinterpret_cast<int*>(p.ws + p.plan.count_off);
 }
 
-// Whether the plan in the workspace is the one that this call's sizes ask for.
+// Whether the plan in the workspace is the one that this call's sizes ask for: a
+// larger max_q would overrun the parts, a larger max_kv the page table.
 __device__ __forceinline__ bool attn_plan_agrees(const AttnParams& p) {
     const AttnHead* h = attn_head(p);
-    return h->T == p.T && h->Hq == p.Hq && h->Hk == p.Hk && h->B == p.B && h->tile_rows == p.plan.tile_rows &&
-           h->block_keys == p.plan.block_keys && h->window == p.window && h->ncta == p.plan.ncta &&
-           h->lead == p.plan.lead && h->ntiles >= 0 && h->ntiles <= p.plan.max_tiles && h->per_cta > 0;
+    return h->T == p.T && h->max_q == p.max_q && h->max_kv == p.max_kv && h->Hq == p.Hq && h->Hk == p.Hk &&
+           h->B == p.B && h->tile_rows == p.plan.tile_rows && h->block_keys == p.plan.block_keys &&
+           h->window == p.window && h->ncta == p.plan.ncta && h->lead == p.plan.lead && h->ntiles >= 0 && h->ntiles <= p.plan.max_tiles && h->per_cta > 0;
 }
 
 // The token of row r.
@@ -176,9 +178,14 @@ struct AttnWalk {
             out.cnt = (t.cnt + head) * JOINS;
             out.slot = 2 * cta + (b0 > 0 ? 0 : 1);
             if (!out.whole) {
-                const int64_t u0 = t.start + static_cast<int64_t>(head) * cost + lead;
-                out.first_cta = static_cast<int>(u0 / per);
-                out.last_cta = static_cast<int>((u0 + t.nblk - 1) / per);
+                const int64_t u0 = t.start + static_cast<int64_t>(head) * cost + lead, u1 = u0 + t.nblk - 1;
+                if (u1 >> 31 == 0) {   // the 64-bit division is a long subroutine
+                    out.first_cta = static_cast<int>(static_cast<uint32_t>(u0) / static_cast<uint32_t>(per));
+                    out.last_cta = static_cast<int>(static_cast<uint32_t>(u1) / static_cast<uint32_t>(per));
+                } else {
+                    out.first_cta = static_cast<int>(u0 / per);
+                    out.last_cta = static_cast<int>(u1 / per);
+                }
             }
             at += n;
             unit += n;
@@ -222,59 +229,105 @@ __device__ __forceinline__ float attn_lse(float m2, float l) {
 }
 
 // Joins the partial results of rows [begin, end) of a tile (one warp, after the
-// last part has arrived).  R rows at a time, 4 values of a row a lane, walking
-// the parts in order with a running maximum; the loads of the rows and of two
-// parts are in flight together.
-template <typename TA, int DP, int R>
+// last part has arrived), R rows at a time.  Lane c first takes the maximum and
+// the sum of part c for each row, so that the parts' weights come from one round
+// of loads; then the lanes take 4 values of a row each and add the parts in
+// order, the loads of U parts in flight together.  More than 32 parts go in
+// rounds of 32 with a running maximum.
+template <typename TA, int DP, int R, int U>
 __device__ __forceinline__ void attn_join(const AttnParams& p, const AttnPiece& pc, int begin, int end, int lane) {
     constexpr int LPR = DP < 128 ? DP / 4 : 32;   // lanes of a row
     constexpr int NV = DP / 4 / LPR;              // pieces of 4 values a lane has of a row
     constexpr int RW = 32 / LPR;                  // rows side by side
-    const int sub = lane % LPR, sr = p.plan.slot_rows;
+    const int sub = lane % LPR, side = lane / LPR, sr = p.plan.slot_rows;
+    auto part = [&](int c) { return attn_slot(p, 2 * c + (c == pc.first_cta ? 1 : 0)); };
     for (int r0 = begin; r0 < end; r0 += RW * R) {
-        float M[R], l[R];
+        float M[RW * R], l[RW * R];
         float4 a[R][NV];
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
+        for (int i = 0; i < RW * R; ++i) {
             M[i] = -INFINITY;
             l[i] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i)
 #pragma unroll
             for (int v = 0; v < NV; ++v) a[i][v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        }
-#pragma unroll 2
-        for (int c = pc.first_cta; c <= pc.last_cta; ++c) {
-            const float* s = attn_slot(p, 2 * c + (c == pc.first_cta ? 1 : 0));
-            float pm[R], pl[R];
-            float4 pv[R][NV];
+        for (int c0 = pc.first_cta; c0 <= pc.last_cta; c0 += 32) {
+            const int n = min(32, pc.last_cta - c0 + 1);
+            float w[RW * R], pl[RW * R];
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-                const int row = min(r0 + i * RW + lane / LPR, end - 1);
-                pm[i] = __ldcg(s + static_cast<int64_t>(sr) * DP + row);
-                pl[i] = __ldcg(s + static_cast<int64_t>(sr) * (DP + 1) + row);
-#pragma unroll
-                for (int v = 0; v < NV; ++v)
-                    pv[i][v] = __ldcg(reinterpret_cast<const float4*>(s + static_cast<int64_t>(row) * DP) + v * LPR + sub);
+            for (int i = 0; i < RW * R; ++i) {
+                const float* s = part(c0 + min(lane, n - 1)) + static_cast<int64_t>(sr) * DP + min(r0 + i, end - 1);
+                w[i] = lane < n ? __ldcg(s) : -INFINITY;
+                pl[i] = lane < n ? __ldcg(s + sr) : 0.0f;
             }
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-                const float top = fmaxf(M[i], pm[i]), base = top == -INFINITY ? 0.0f : top;
-                const float w0 = ex2(M[i] - base), w1 = ex2(pm[i] - base);
-                M[i] = top;
-                l[i] = fmaf(pl[i], w1, l[i] * w0);
+            for (int i = 0; i < RW * R; ++i) {
+                float top = w[i];
 #pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                    a[i][v].x = fmaf(pv[i][v].x, w1, a[i][v].x * w0);
-                    a[i][v].y = fmaf(pv[i][v].y, w1, a[i][v].y * w0);
-                    a[i][v].z = fmaf(pv[i][v].z, w1, a[i][v].z * w0);
-                    a[i][v].w = fmaf(pv[i][v].w, w1, a[i][v].w * w0);
+                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                top = fmaxf(top, M[i]);
+                const float base = top == -INFINITY ? 0.0f : top, keep = ex2(M[i] - base);
+                w[i] = ex2(w[i] - base);
+                l[i] = fmaf(l[i], keep, warp_sum(pl[i] * w[i]));
+                if (c0 > pc.first_cta) {
+#pragma unroll
+                    for (int v = 0; v < NV; ++v)
+                        if (i % RW == side) {
+                            float4& x = a[i / RW][v];
+                            x = make_float4(x.x * keep, x.y * keep, x.z * keep, x.w * keep);
+                        }
                 }
+                M[i] = top;
+            }
+            for (int c = 0; c < n; c += U) {
+                float4 pv[U][R][NV];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int i = 0; i < R; ++i) {
+                        const float* s = part(c0 + min(c + u, n - 1));
+                        const int row = min(r0 + i * RW + side, end - 1);
+#pragma unroll
+                        for (int v = 0; v < NV; ++v)
+                            pv[u][i][v] = __ldcg(reinterpret_cast<const float4*>(s + static_cast<int64_t>(row) * DP) +
+                                                 v * LPR + sub);
+                    }
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int i = 0; i < R; ++i) {
+                        float f = 0.0f;
+#pragma unroll
+                        for (int q = 0; q < RW; ++q) {
+                            const float x = __shfl_sync(0xffffffffu, w[i * RW + q], min(c + u, 31));
+                            if (q == side) f = x;
+                        }
+                        if (c + u < n) {
+#pragma unroll
+                            for (int v = 0; v < NV; ++v) {
+                                a[i][v].x = fmaf(pv[u][i][v].x, f, a[i][v].x);
+                                a[i][v].y = fmaf(pv[u][i][v].y, f, a[i][v].y);
+                                a[i][v].z = fmaf(pv[u][i][v].z, f, a[i][v].z);
+                                a[i][v].w = fmaf(pv[u][i][v].w, f, a[i][v].w);
+                            }
+                        }
+                    }
             }
         }
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const int row = r0 + i * RW + lane / LPR;
+            const int row = r0 + i * RW + side;
             if (row >= end) continue;
-            const float inv = l[i] != 0.0f ? 1.0f / l[i] : 0.0f;
+            float ml = M[i * RW], ll = l[i * RW];
+#pragma unroll
+            for (int q = 1; q < RW; ++q)
+                if (q == side) {
+                    ml = M[i * RW + q];
+                    ll = l[i * RW + q];
+                }
+            const float inv = ll != 0.0f ? 1.0f / ll : 0.0f;
             const int r = pc.row0 + row, tok = attn_token(p, r);
             const int64_t out = (pc.q0 + tok) * p.Hq + pc.head * p.G + (r - tok * p.G);
 #pragma unroll
@@ -292,7 +345,7 @@ __device__ __forceinline__ void attn_join(const AttnParams& p, const AttnPiece& 
                                                                 a[i][v].w * inv);
                 }
             }
-            if (sub == 0 && p.lse != nullptr) p.lse[out] = attn_lse(M[i], l[i]);
+            if (sub == 0 && p.lse != nullptr) p.lse[out] = attn_lse(ml, ll);
         }
     }
 }

@@ -486,7 +486,7 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
                 }
                 if (__shfl_sync(FULL, last, 0)) {
                     const int begin = __shfl_sync(FULL, rt, 0), n = __popc(__ballot_sync(FULL, valid));
-                    attn_join<__nv_bfloat16, DP, 8>(p, pc, begin, begin + n, lane);
+                    attn_join<__nv_bfloat16, DP, DP == 128 ? 8 : 4, 3>(p, pc, begin, begin + n, lane);
                 }
                 __syncwarp();
             }
@@ -558,9 +558,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
     ptx::griddep_wait();   // the plan, the queries and the cache are written
 
     AttnWalk walk;
-    const bool agrees = attn_plan_agrees(p);
+    const bool begun = walk.begin(p, cta), agrees = attn_plan_agrees(p);   // one round of loads
     if (!agrees && tid == 0) atomicOr(&g_attn_tc_error, ATTN_ERR_RANGE);
-    const bool work = agrees && walk.begin(p, cta);
+    const bool work = agrees && begun;
     if (warp >= LOAD_WARP) {
         ptx::regs_dec<OTHER_REGS>();
         Pieces<DP> pieces(smem, sbase, abort_flag);
@@ -586,6 +586,16 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
             const int boxes = KEYS / box;                                 // of a block: at most 16
             int stage = 0;
             uint32_t round = 0, par_q = 1;
+            {   // The first pieces' page numbers into the cache, before the walk has handed out the piece
+                AttnPiece first;
+                if (walk.next(p, cta, first)) {
+                    const int key = first.blk * KEYS + lane * box;
+                    if (lane < 2 * boxes && key < first.hi && key + box > first.lo) {
+                        const int pg = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
+                        asm volatile("prefetch.global.L1 [%0];" ::"l"(p.page_table + first.seq * p.table_stride + pg));
+                    }
+                }
+            }
             while (ok) {
                 const AttnPiece pc = pieces.get(ok);
                 if (!ok || pc.nb == 0) break;

@@ -150,3 +150,32 @@ def test_forced_timeout_of_the_attention_is_reported():
     got = c.run()
     assert B.get_last_device_error() == B.MHC_OK
     assert torch.equal(got.o, want.o)
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "f32"))
+def test_a_plan_of_other_sizes_is_reported(dtype):
+    """The C entry point, for which the workspace's plan is the only witness."""
+    c = Case([(8, 300), (2, 40)], 4, 2, 64, 64, dtype)
+    want = c.run(max_q=8, max_kv=300)
+    L, code = B.lib(), B.MHC_BF16 if dtype == "bf16" else B.MHC_F32
+    s = torch.cuda.current_stream().cuda_stream
+    sizes = (10, 2, 4, 2, 64)                         # T, B, Hq, Hk, Dh
+    n = L.mhc_paged_attn_workspace_bytes(code, *sizes, 64, 8)
+    ws = torch.empty(n, dtype=torch.uint8, device=c.q.device)
+    o = torch.full(c.q.shape, 7.0, dtype=c.q.dtype, device=c.q.device)
+
+    def call(max_q, max_kv, window):
+        assert L.mhc_paged_attn(code, c.q.data_ptr(), c.q.stride(0), c.k.data_ptr(), *c.k.stride()[:3],
+                                c.v.data_ptr(), *c.v.stride()[:3], c.k.shape[0], 64, c.table.data_ptr(),
+                                c.table.stride(0), None, None, *sizes, max_q, max_kv, window, 0.125, 0.0,
+                                o.data_ptr(), None, ws.data_ptr(), n, s) == B.MHC_OK
+        return B.get_last_device_error()
+
+    assert L.mhc_paged_attn_plan(code, c.cu.data_ptr(), c.kv.data_ptr(), *sizes, 64, 8, 300, 0, ws.data_ptr(), n,
+                                 s) == B.MHC_OK
+    assert B.get_last_device_error() == B.MHC_OK
+    for other in ((1, 300, 0), (7, 300, 0), (8, 64, 0), (8, 300, 100)):
+        assert call(*other) == B.MHC_ERR_RANGE, other
+        assert bool((o == 7.0).all()), other
+    assert call(8, 300, 0) == B.MHC_OK
+    assert torch.equal(o, want.o)
