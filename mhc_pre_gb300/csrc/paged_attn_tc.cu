@@ -181,19 +181,26 @@ __device__ __forceinline__ void cap4(uint32_t* u, float in, float cap2, float c)
     u[3] = __float_as_uint(w.y);
 }
 
-// Scores of keys outside [from, to) become -inf, of 32 keys from the first.
-__device__ __forceinline__ void mask32(uint32_t* u, bool head, bool tail, int from, int to) {
-    if (tail) {
+// Scores of 32 keys become -inf where `seen` has no bit.
+__device__ __forceinline__ void mask32(uint32_t* u, uint32_t seen) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-            if (e >= to) u[e] = 0xff800000u;
-    }
-    if (head) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-            if (e < from) u[e] = 0xff800000u;
-    }
+    for (int e = 0; e < 32; ++e)
+        if (!(seen & (1u << e))) u[e] = 0xff800000u;
 }
+
+// The keys [lo, hi) that a row sees, and the bounds of its warp's rows.
+struct Seen {
+    int lo, hi, lo_least, lo_most, hi_least, hi_most;
+    // Of the 32 keys from g: no row of the warp sees any, all rows see all, and
+    // which of them this row sees.
+    __device__ __forceinline__ bool none(int g) const { return g >= hi_most || g + 32 <= lo_least; }
+    __device__ __forceinline__ bool all(int g) const { return g >= lo_most && g + 32 <= hi_least; }
+    __device__ __forceinline__ uint32_t bits(int g) const {
+        const int from = max(lo - g, 0), to = min(hi - g, 32);
+        return from < to ? (FULL << from) & (FULL >> (32 - to)) : 0u;
+    }
+};
+template <bool V> struct Flag { static constexpr bool value = V; };
 
 template <int DP, bool CAP>
 __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char* smem, uint32_t sbase, uint32_t tmem) {
@@ -210,6 +217,7 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
     const uint32_t t_s = t_lane + S_COL + L * 128, t_o = t_lane + O_COL + L * 128;
     const float zscale = CAP ? 1.0f : p.scale * LOG2E;
     const float cap2 = p.softcap * LOG2E, cap_in = CAP ? 2.0f * LOG2E * p.scale / p.softcap : 0.0f;
+    const float most = CAP ? 30.0f / cap_in : 0.0f;   // larger scores are capped as this one
     // rows of 32-byte multiples at 32-byte addresses are stored 32 bytes at a time
     const bool wide = p.Dh % 16 == 0 && (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0;
     uint32_t par_s = 0, par_o = 0, par_x = 0;
@@ -230,7 +238,9 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
         int lo = 0, hi = 0x7fffffff;                            // rows that are not there need no mask
         const int tok = attn_token(p, valid ? r : 0);
         if (valid) attn_token_keys(pc, tok, p.window, lo, hi);
-        const int lo_most = __reduce_max_sync(FULL, lo), hi_least = __reduce_min_sync(FULL, hi);
+        const int lo_most = same(__reduce_max_sync(FULL, lo)), hi_least = same(__reduce_min_sync(FULL, hi));
+        const int lo_least = same(__reduce_min_sync(FULL, valid ? lo : 0x7fffffff));
+        const int hi_most = same(__reduce_max_sync(FULL, valid ? hi : 0));
         float m = -INFINITY, l = 0.0f;
         if (lent) {
             ok = wait_warp(bar(C::B_XE + w4), par_x, abort_flag);
@@ -246,52 +256,61 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
             ptx::tc_fence_after();
             if (active) {
                 // Without a cap the scores stay in registers (128 of them) from
-                // the maximum to the exponentials.  With one they are read twice,
-                // 32 at a time with the next 32 on their way: the capping's code
-                // over all 128 is so long that the warps wait for instructions.
-                // Exponentials overwrite scores already read.
-                const bool head = k0 < lo_most, tail = k0 + KEYS > hi_least;
-                const int from = lo - k0, to = hi - k0;
-                constexpr int HELD = CAP ? 64 : 128;
+                // the maximum to the exponentials.  With one they are read twice
+                // and 32 at a time, by loops that are not unrolled: the capping
+                // is long enough for the other warp's to cover the loads, and
+                // two loops' code of all 128 scores makes the warps wait for
+                // instructions (5 prompts with a window of 512 keys took 331 us
+                // and a chunk of 2048 tokens on 32768 keys 1550 us, these 231
+                // and 1338).  Of a block that not all rows see whole, 32 keys
+                // that no row of the warp sees cost nothing, and only the 32 at
+                // a border are masked.  Exponentials overwrite scores already read.
+                const bool partial = k0 < lo_most || k0 + KEYS > hi_least;
+                const Seen see = {lo, hi, lo_least, lo_most, hi_least, hi_most};
+                constexpr int HELD = CAP ? 32 : 128;
                 uint32_t u[HELD];
-                float top, most = INFINITY;
+                float top;
+                bool big = false;   // a score too large for cap4
                 if constexpr (!CAP) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) ptx::tmem_ld32(t_s + c * 32, u + c * 32);
+                    for (int c = 0; c < HELD / 32; ++c) ptx::tmem_ld32(t_s + c * 32, u + c * 32);
                     ptx::tmem_wait_ld();
-                    if (head || tail) {
+                    if (partial) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) mask32(u + 32 * c, head, tail, from - 32 * c, to - 32 * c);
+                        for (int c = 0; c < HELD / 32; ++c)
+                            if (!see.all(k0 + 32 * c)) mask32(u + 32 * c, see.bits(k0 + 32 * c));
                     }
                     float mx[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) mx[e] = fmaxf(__uint_as_float(u[e]), __uint_as_float(u[4 + e]));
 #pragma unroll
-                    for (int e = 8; e < 128; e += 8)
+                    for (int e = 8; e < HELD; e += 8)
 #pragma unroll
                         for (int f = 0; f < 4; ++f)
                             mx[f] = max3(mx[f], __uint_as_float(u[e + f]), __uint_as_float(u[e + 4 + f]));
                     top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * zscale;
                 } else {
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    ptx::tmem_ld32(t_s, u);
+                    auto sweep = [&](auto borders) {
 #pragma unroll 1
-                    for (int c = 0; c < 4; c += 2) {
-#pragma unroll
-                        for (int d = 0; d < 2; ++d) {
+                        for (int c = 0; c < 4; ++c) {
+                            const int g = k0 + 32 * c;
+                            if (borders.value && see.none(g)) continue;
+                            ptx::tmem_ld32(t_s + c * 32, u);
                             ptx::tmem_wait_ld();
-                            if (d == 0 || c == 0) ptx::tmem_ld32(t_s + (c + d + 1) * 32, u + 32 * (d ^ 1));
-                            if (head || tail) mask32(u + 32 * d, head, tail, from - 32 * (c + d), to - 32 * (c + d));
+                            if (borders.value && !see.all(g)) mask32(u, see.bits(g));
 #pragma unroll
                             for (int e = 0; e < 32; e += 8)
 #pragma unroll
                                 for (int f = 0; f < 4; ++f)
-                                    mx[f] = max3(mx[f], __uint_as_float(u[32 * d + e + f]), __uint_as_float(u[32 * d + e + 4 + f]));
+                                    mx[f] = max3(mx[f], __uint_as_float(u[e + f]), __uint_as_float(u[e + 4 + f]));
                         }
-                    }
-                    top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * zscale;
+                    };
+                    if (partial) sweep(Flag<true>{});
+                    else sweep(Flag<false>{});
+                    top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    big = __any_sync(FULL, top > most);
                     // tanh keeps the order, so the capped maximum is the maximum's
-                    if (__any_sync(FULL, top * cap_in > 30.0f)) most = 30.0f / cap_in;
                     uint32_t t[4] = {__float_as_uint(fminf(top, most)), 0u, 0u, 0u};
                     cap4(t, cap_in, cap2, cap2);
                     if (top > -INFINITY) top = __uint_as_float(t[0]);
@@ -319,7 +338,7 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
                 float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
                 if constexpr (!CAP) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
+                    for (int h = 0; h < HELD / 64; ++h) {
                         uint32_t pk[32];
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
@@ -337,42 +356,48 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
                         if (lane == 0) ptx::mbar_arrive(bar(C::B_P + 2 * L + h));
                     }
                 } else {
-                    ptx::tmem_ld32(t_s, u);
+                    auto sweep = [&](auto borders) {
 #pragma unroll 1
-                    for (int c = 0; c < 4; c += 2) {
-#pragma unroll
-                        for (int d = 0; d < 2; ++d) {
-                            ptx::tmem_wait_ld();
-                            if (d == 0 || c == 0) ptx::tmem_ld32(t_s + (c + d + 1) * 32, u + 32 * (d ^ 1));
-                            uint32_t* v = u + 32 * d;
-                            const int f = from - 32 * (c + d), t = to - 32 * (c + d);
-                            // an unseen key's NaN must not reach the other three of its cap4
-                            if (head || tail) mask32(v, head, tail, f, t);
-                            if (most < INFINITY) {
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (__uint_as_float(v[e]) > most) v[e] = __float_as_uint(most);
-                            }
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4) cap4(v + e, cap_in, cap2, cap2 - base);
-                            if (head || tail) mask32(v, head, tail, f, t);
+                        for (int c = 0; c < 4; ++c) {
+                            const int g = k0 + 32 * c;
                             uint32_t pk[16];
+                            if (borders.value && see.none(g)) {
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const float2 y = make_float2(ex2(__uint_as_float(v[2 * e])),
-                                                             ex2(__uint_as_float(v[2 * e + 1])));
-                                sum[e & 1] = __fadd2_rn(sum[e & 1], y);
-                                const __nv_bfloat162 h = __floats2bfloat162_rn(y.x, y.y);
-                                pk[e] = *reinterpret_cast<const uint32_t*>(&h);
+                                for (int e = 0; e < 16; ++e) pk[e] = 0u;
+                            } else {
+                                ptx::tmem_ld32(t_s + c * 32, u);
+                                ptx::tmem_wait_ld();
+                                const bool border = borders.value && !see.all(g);
+                                // (an unseen key's NaN becomes `most` here: it must not reach its cap4's other three)
+                                if (border || big) {
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e)
+                                        u[e] = __float_as_uint(fminf(__uint_as_float(u[e]), most));
+                                }
+#pragma unroll
+                                for (int e = 0; e < 32; e += 4) cap4(u + e, cap_in, cap2, cap2 - base);
+                                if (border) mask32(u, see.bits(g));
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) {
+                                    const float2 y = make_float2(ex2(__uint_as_float(u[2 * e])),
+                                                                 ex2(__uint_as_float(u[2 * e + 1])));
+                                    sum[e & 1] = __fadd2_rn(sum[e & 1], y);
+                                    const __nv_bfloat162 h = __floats2bfloat162_rn(y.x, y.y);
+                                    pk[e] = *reinterpret_cast<const uint32_t*>(&h);
+                                }
                             }
-                            ptx::tmem_st16(t_s + (c + d) * 16, pk);
+                            ptx::tmem_st16(t_s + c * 16, pk);
+                            if (c & 1) {
+                                // 64 keys' exponentials are there: their product may start
+                                ptx::tmem_wait_st();
+                                ptx::tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) ptx::mbar_arrive(bar(C::B_P + 2 * L + (c >> 1)));
+                            }
                         }
-                        // 64 keys' exponentials are there: their product may start
-                        ptx::tmem_wait_st();
-                        ptx::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(bar(C::B_P + 2 * L + (c >> 1)));
-                    }
+                    };
+                    if (partial) sweep(Flag<true>{});
+                    else sweep(Flag<false>{});
                 }
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             } else {
@@ -484,6 +509,7 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
                     if (last) *count = 0;   // back at zero for the next call with this plan
                     __threadfence();
                 }
+                __syncwarp();   // the others' reads come after lane 0's
                 if (__shfl_sync(FULL, last, 0)) {
                     const int begin = __shfl_sync(FULL, rt, 0), n = __popc(__ballot_sync(FULL, valid));
                     attn_join<__nv_bfloat16, DP, DP == 128 ? 8 : 4, 3>(p, pc, begin, begin + n, lane);
