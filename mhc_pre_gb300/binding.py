@@ -110,6 +110,9 @@ def _empty(shape, dtype=None, device=None):
     return torch.empty(shape, dtype=dtype, device=device)
 
 
+_torch_empty = _empty
+
+
 class MhcError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -425,11 +428,13 @@ def _calls():
         if not os.path.exists(CALLS_PATH):
             raise RuntimeError(f"{CALLS_PATH} is missing: build it with `python -m mhc_pre_gb300.build`")
         from . import _attn_calls
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        _attn_calls.setup(torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8,
-                          raw or (lambda i: torch.cuda.current_stream(i).cuda_stream))
         _calls_module = _attn_calls
     return _calls_module
+
+
+def _allocator():
+    """What _calls() allocates with: None (torch's empty) unless _empty has been replaced."""
+    return None if _empty is _torch_empty else _empty
 
 
 def mhc_qk_norm_rope(q, k, w_q, w_k, positions=None, cos_sin=None, eps: float = 1e-6,
@@ -437,7 +442,7 @@ def mhc_qk_norm_rope(q, k, w_q, w_k, positions=None, cos_sin=None, eps: float = 
     """Per-head RMSNorm of q [T, Hq, Dh] and k [T, Hk, Dh], then the rotation of
     the first cos_sin.shape[1] values of each head by cos_sin[positions]
     (cosines, then sines).  ``interleaved``: pairs (2j, 2j + 1)."""
-    st, qo, ko = (_calls_module or _calls()).qk_norm_rope(_empty, q, k, w_q, w_k, positions, cos_sin, eps,
+    st, qo, ko = (_calls_module or _calls()).qk_norm_rope(_allocator(), q, k, w_q, w_k, positions, cos_sin, eps,
                                                           ROPE_ADJACENT if interleaved else 0)
     if st:
         _check(st, "mhc_qk_norm_rope")
@@ -449,7 +454,7 @@ def mhc_qk_norm_rope_bwd(g_q, g_k, q, k, w_q, w_k, positions=None, cos_sin=None,
     """Gradients of <g_q, q_out> + <g_k, k_out> for mhc_qk_norm_rope.  ``dq`` and
     ``dk`` (parts of a packed gradient, say) are written when given."""
     st, dq, dk, dw_q, dw_k = (_calls_module or _calls()).qk_norm_rope_bwd(
-        _empty, g_q, g_k, q, k, w_q, w_k, positions, cos_sin, eps, ROPE_ADJACENT if interleaved else 0, dq, dk)
+        _allocator(), g_q, g_k, q, k, w_q, w_k, positions, cos_sin, eps, ROPE_ADJACENT if interleaved else 0, dq, dk)
     if st:
         _check(st, "mhc_qk_norm_rope_bwd")
     return QKBwdOut(dq, dk, dw_q, dw_k)
@@ -461,7 +466,7 @@ def mhc_qk_norm_rope_append(q, k, v, w_q, w_k, k_cache, v_cache, slots, position
     and the values go to slots[t] = page * page_size + place of the caches
     [pages, page_size, Hk, Dh] (-1: nowhere), in place."""
     st, out = (_calls_module or _calls()).qk_norm_rope_append(
-        _empty, q, k, v, w_q, w_k, k_cache, v_cache, slots, positions, cos_sin, eps,
+        _allocator(), q, k, v, w_q, w_k, k_cache, v_cache, slots, positions, cos_sin, eps,
         ROPE_ADJACENT if interleaved else 0)
     if st:
         _check(st, "mhc_qk_norm_rope_append")
@@ -511,7 +516,7 @@ def mhc_paged_attn(q, k_cache, v_cache, page_table, cu_q=None, kv_lens=None, max
         if want != sizes or cu_q is not None or kv_lens is not None:
             raise ValueError(f"the plan has its own lengths and sizes: {sizes}, not {want}")
     st, o, lse = (_calls_module or _calls()).paged_attn(
-        _empty, q, k_cache, v_cache, page_table, cu_q, kv_lens, max_q, max_kv, scale, window or 0, softcap, ws, out)
+        _allocator(), q, k_cache, v_cache, page_table, cu_q, kv_lens, max_q, max_kv, scale, window or 0, softcap, ws, out)
     if st:
         _check(st, "mhc_paged_attn")
     return PagedAttnOut(o, lse)

@@ -58,15 +58,32 @@ def _compile(nvcc: str, src: str, extra) -> str:
     return obj
 
 
-def _build_calls(nvcc: str) -> None:
-    """The Python module of the attention sublayer's calls, linked to the library."""
-    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
-    tmp = CALLS + ".tmp"
-    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-Wall", "-I", sysconfig.get_paths()["include"], "-I",
-           os.path.join(cuda, "include"), os.path.join(CSRC, "py_attn.cpp"), "-o", tmp, LIB, "-Wl,-rpath,$ORIGIN"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+def _gxx(cmd, what: str) -> None:
+    r = subprocess.run(["g++", *cmd], capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed on py_attn.cpp:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"g++ failed on {what}:\n{r.stdout}\n{r.stderr}")
+
+
+def _compile_calls(nvcc: str) -> str:
+    """The object of the Python module of the attention sublayer's calls."""
+    import torch
+    src, obj = os.path.join(CSRC, "py_attn.cpp"), os.path.join(BUILD, "py_attn.o")
+    if os.path.exists(obj) and all(os.path.getmtime(d) <= os.path.getmtime(obj)
+                                   for d in (src, os.path.join(INCLUDE, "mhc.h"), os.path.abspath(__file__))):
+        return obj
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+    headers = os.path.join(os.path.dirname(torch.__file__), "include")
+    _gxx(["-std=c++17", "-O2", "-fPIC", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+          "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"), "-isystem", headers,
+          "-isystem", os.path.join(headers, "torch", "csrc", "api", "include"), "-c", src, "-o", obj], src)
+    return obj
+
+
+def _link_calls(obj: str) -> None:
+    import torch
+    tmp = CALLS + ".tmp"
+    _gxx(["-shared", "-o", tmp, obj, LIB, "-Wl,-rpath,$ORIGIN", "-L", os.path.join(os.path.dirname(torch.__file__), "lib"),
+          "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"], "the Python module's link")
     os.replace(tmp, CALLS)
 
 
@@ -82,7 +99,8 @@ def build(verbose: bool = False, extra_flags=()) -> str:
         if all(os.path.getmtime(d) <= lib_mtime for d in deps):
             return LIB
     nvcc = _nvcc()
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        calls = ex.submit(_compile_calls, nvcc)
         objs = list(ex.map(lambda s: _compile(nvcc, s, list(extra_flags)), SOURCES))
     libdir = _cuda_lib_dir(nvcc)
     tmp = LIB + ".tmp"
@@ -92,7 +110,7 @@ def build(verbose: bool = False, extra_flags=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _build_calls(nvcc)
+    _link_calls(calls.result())
     if verbose:
         print(f"built {LIB}")
     return LIB
