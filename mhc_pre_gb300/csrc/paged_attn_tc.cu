@@ -26,7 +26,8 @@
 // The running maximum is only raised when a row's new maximum exceeds it by
 // more than 2^8 in the exponentials' scale: float32 sums and bf16 exponentials
 // lose nothing by a common factor of up to 2^8, and O in tensor memory is then
-// rescaled a few times per row instead of at every block.
+// rescaled a few times per row instead of at every block.  A cap of up to 52
+// bounds the scores so well that no maximum is needed at all (LOW_CAP).
 //
 // Keys outside what a tile's rows see (past the sequence's end, before the
 // window, in pages that are not there) are masked in the scores, and their
@@ -74,6 +75,15 @@ constexpr int TMEM_COLS = 512;
 constexpr uint32_t S_COL = 0, O_COL = 256;   // two of each, 128 columns apart
 constexpr uint64_t WAIT_LIMIT_NS = 1000000000ull;
 constexpr float RAISE = 8.0f;                // see above
+// Kinds of capping: none; a cap that bounds the scores so well that no maximum
+// is needed (below); any cap.
+constexpr int NO_CAP = 0, LOW_CAP = 1, HIGH_CAP = 2;
+// With |z| <= cap (in base 2, cap <= LOW_MOST) every row takes the base
+// min(cap, LOW_SPAN - cap): its exponentials then lie between 2^-90 and 2^60,
+// where bf16 and float32 round as everywhere, sums of 2^31 of them times values
+// of 2^30 stay finite, and a value below 2^-36 is the first that a row of
+// lowest scores could lose.  A softcap of 52 is the largest such.
+constexpr float LOW_MOST = 75.0f, LOW_SPAN = 90.0f;
 constexpr uint32_t FULL = 0xffffffffu;
 
 constexpr int PIECES = 4;                    // pieces handed out and not done with
@@ -120,6 +130,12 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatil
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// The lesser, or NaN if one is.
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
 __device__ __forceinline__ float rcp_ftz(float x) {
@@ -202,7 +218,7 @@ struct Seen {
 };
 template <bool V> struct Flag { static constexpr bool value = V; };
 
-template <int DP, bool CAP>
+template <int DP, int CAP>
 __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char* smem, uint32_t sbase, uint32_t tmem) {
     using C = Cfg<DP>;
     auto bar = [&](int i) { return sbase + C::BARS + 8u * static_cast<uint32_t>(i); };
@@ -217,6 +233,7 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
     const uint32_t t_s = t_lane + S_COL + L * 128, t_o = t_lane + O_COL + L * 128;
     const float zscale = CAP ? 1.0f : p.scale * LOG2E;
     const float cap2 = p.softcap * LOG2E, cap_in = CAP ? 2.0f * LOG2E * p.scale / p.softcap : 0.0f;
+    const float low_base = fminf(cap2, LOW_SPAN - cap2);
     const float most = CAP ? 30.0f / cap_in : 0.0f;   // larger scores are capped as this one
     // rows of 32-byte multiples at 32-byte addresses are stored 32 bytes at a time
     const bool wide = p.Dh % 16 == 0 && (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0;
@@ -256,22 +273,22 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
             ptx::tc_fence_after();
             if (active) {
                 // Without a cap the scores stay in registers (128 of them) from
-                // the maximum to the exponentials.  With one they are read twice
-                // and 32 at a time, by loops that are not unrolled: the capping
-                // is long enough for the other warp's to cover the loads, and
-                // two loops' code of all 128 scores makes the warps wait for
-                // instructions (5 prompts with a window of 512 keys took 331 us
-                // and a chunk of 2048 tokens on 32768 keys 1550 us, these 231
-                // and 1338).  Of a block that not all rows see whole, 32 keys
-                // that no row of the warp sees cost nothing, and only the 32 at
-                // a border are masked.  Exponentials overwrite scores already read.
+                // the maximum to the exponentials.  With one they are taken 32
+                // at a time, by loops that are not unrolled: the capping is long
+                // enough for the other warp's to cover the loads, and the code
+                // of all 128 scores makes the warps wait for instructions (5
+                // prompts with a window of 512 keys took 331 us, a chunk of 2048
+                // tokens on 32768 keys 1550; with these loops 231 and 1338, and
+                // 203 and 1135 without a maximum).  Of a block that not all rows
+                // see whole, 32 keys that no row of the warp sees cost nothing,
+                // and only the 32 at a border are masked.  Exponentials
+                // overwrite scores already read.
                 const bool partial = k0 < lo_most || k0 + KEYS > hi_least;
                 const Seen see = {lo, hi, lo_least, lo_most, hi_least, hi_most};
                 constexpr int HELD = CAP ? 32 : 128;
                 uint32_t u[HELD];
                 float top;
-                bool big = false;   // a score too large for cap4
-                if constexpr (!CAP) {
+                if constexpr (CAP == NO_CAP) {
 #pragma unroll
                     for (int c = 0; c < HELD / 32; ++c) ptx::tmem_ld32(t_s + c * 32, u + c * 32);
                     ptx::tmem_wait_ld();
@@ -289,7 +306,7 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
                         for (int f = 0; f < 4; ++f)
                             mx[f] = max3(mx[f], __uint_as_float(u[e + f]), __uint_as_float(u[e + 4 + f]));
                     top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * zscale;
-                } else {
+                } else if constexpr (CAP == HIGH_CAP) {
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                     auto sweep = [&](auto borders) {
 #pragma unroll 1
@@ -309,14 +326,14 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
                     if (partial) sweep(Flag<true>{});
                     else sweep(Flag<false>{});
                     top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                    big = __any_sync(FULL, top > most);
                     // tanh keeps the order, so the capped maximum is the maximum's
                     uint32_t t[4] = {__float_as_uint(fminf(top, most)), 0u, 0u, 0u};
                     cap4(t, cap_in, cap2, cap2);
                     if (top > -INFINITY) top = __uint_as_float(t[0]);
                 }
+                if constexpr (CAP == LOW_CAP) top = m;
                 const bool raise = top > m + RAISE || (m == -INFINITY && top > -INFINITY);
-                if (__any_sync(FULL, raise)) {
+                if (CAP != LOW_CAP && __any_sync(FULL, raise)) {
                     // S of this block is complete, so every earlier MMA is: O stands still
                     const float f = raise ? ex2(m - top) : 1.0f;
                     if (raise) m = top;
@@ -333,10 +350,10 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
                         }
                     }
                 }
-                const float base = m == -INFINITY ? 0.0f : m;
+                const float base = CAP == LOW_CAP ? low_base : m == -INFINITY ? 0.0f : m;
                 const float2 z2 = make_float2(zscale, zscale), b2 = make_float2(-base, -base);
                 float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-                if constexpr (!CAP) {
+                if constexpr (CAP == NO_CAP) {
 #pragma unroll
                     for (int h = 0; h < HELD / 64; ++h) {
                         uint32_t pk[32];
@@ -368,12 +385,11 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
                                 ptx::tmem_ld32(t_s + c * 32, u);
                                 ptx::tmem_wait_ld();
                                 const bool border = borders.value && !see.all(g);
-                                // (an unseen key's NaN becomes `most` here: it must not reach its cap4's other three)
-                                if (border || big) {
+                                // before the cap too: an unseen key's NaN must not reach its cap4's other three
+                                if (border) mask32(u, see.bits(g));
 #pragma unroll
-                                    for (int e = 0; e < 32; ++e)
-                                        u[e] = __float_as_uint(fminf(__uint_as_float(u[e]), most));
-                                }
+                                for (int e = 0; e < 32; ++e)
+                                    u[e] = __float_as_uint(min_nan(__uint_as_float(u[e]), most));
 #pragma unroll
                                 for (int e = 0; e < 32; e += 4) cap4(u + e, cap_in, cap2, cap2 - base);
                                 if (border) mask32(u, see.bits(g));
@@ -409,6 +425,7 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
                 }
             }
         }
+        if (CAP == LOW_CAP) m = l != 0.0f ? low_base : -INFINITY;   // (NaN: as a row that saw something)
         if (ok && mine > 0) {
             ok = wait_warp(bar(C::B_O + L), par_o, abort_flag);
             par_o ^= 1;
@@ -521,7 +538,7 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
     }
 }
 
-template <int DP, bool CAP>
+template <int DP, int CAP>
 __global__ void __launch_bounds__(NTHREADS, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                const __grid_constant__ CUtensorMap tmap_v, const AttnParams p) {
@@ -904,7 +921,7 @@ cudaError_t encode(PFN_cuTensorMapEncodeTiled_v12000 fn, CUtensorMap* tm, const 
                : cudaErrorInvalidValue;
 }
 
-template <int DP, bool CAP>
+template <int DP, int CAP>
 cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const AttnParams& p, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};   // devices whose kernel has its shared memory allowed
     int dev = 0;
@@ -929,6 +946,16 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
     return cudaLaunchKernelEx(&cfg, attn_tc_kernel<DP, CAP>, tq, tk, tv, p);
 }
 
+template <int DP>
+cudaError_t launch_cap(int cap, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const AttnParams& p,
+                       cudaStream_t s) {
+    switch (cap) {
+        case NO_CAP: return launch<DP, NO_CAP>(tq, tk, tv, p, s);
+        case LOW_CAP: return launch<DP, LOW_CAP>(tq, tk, tv, p, s);
+        default: return launch<DP, HIGH_CAP>(tq, tk, tv, p, s);
+    }
+}
+
 }  // namespace attn_tc
 
 // Boxes of 8 or more whole swizzle rows that tile a block of 128 keys, and a
@@ -945,9 +972,9 @@ cudaError_t launch_paged_attn_tc(const AttnParams& p, cudaStream_t s) {
     if (e == cudaSuccess) e = attn_tc::encode(fn, &tk, p.k_cache, p, p.k_page_stride, p.k_slot_stride, p.k_head_stride);
     if (e == cudaSuccess) e = attn_tc::encode(fn, &tv, p.v_cache, p, p.v_page_stride, p.v_slot_stride, p.v_head_stride);
     if (e != cudaSuccess) return e;
-    if (p.Dh <= 64)
-        return p.softcap > 0.0f ? attn_tc::launch<64, true>(tq, tk, tv, p, s) : attn_tc::launch<64, false>(tq, tk, tv, p, s);
-    return p.softcap > 0.0f ? attn_tc::launch<128, true>(tq, tk, tv, p, s) : attn_tc::launch<128, false>(tq, tk, tv, p, s);
+    const int cap = p.softcap > 0.0f ? (p.softcap * LOG2E <= attn_tc::LOW_MOST ? attn_tc::LOW_CAP : attn_tc::HIGH_CAP)
+                                     : attn_tc::NO_CAP;
+    return p.Dh <= 64 ? attn_tc::launch_cap<64>(cap, tq, tk, tv, p, s) : attn_tc::launch_cap<128>(cap, tq, tk, tv, p, s);
 }
 
 }  // namespace mhc

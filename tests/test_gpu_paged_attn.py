@@ -158,6 +158,38 @@ def test_capped_scores(softcap, std, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("softcap", [0.25, 51.9, 52.1, 400.0])
+def test_caps_of_any_size(softcap, dtype):
+    """Scores on both sides of the cap, which they reach where it is small."""
+    for dh, window in ((128, 0), (64, 60)):
+        c = Case(LENS["chunks"], 10, 2, dh, 64, dtype, std=4.0, window=window)
+        c.check(c.run(softcap=softcap), softcap=softcap)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("softcap", [30.0, 52.0, 60.0])
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+def test_every_score_at_the_cap(sign, softcap, dtype):
+    """tanh is +-1 for every key: o is the mean of the values, lse +-cap + log m."""
+    c = Case([(3, 300), (1, 70)], 4, 2, 64, 64, dtype)
+    c.q.fill_(16.0)
+    c.k = torch.where(c.k.isnan(), c.k, torch.full_like(c.k, 16.0 * sign))
+    c.kd = [torch.full_like(k, 16.0 * sign) for k in c.kd]
+    c.check(c.run(softcap=softcap), softcap=softcap)
+
+
+def test_a_capped_rows_own_nan_is_seen():
+    """A key that a row sees is not hidden by the cap."""
+    c = Case([(70, 200)], 4, 2, 64, 64, "bf16")
+    c.k[int(c.table[0, 3]), 2] = float("nan")     # token 194: the last 6 rows see it
+    r = c.run(softcap=30.0)
+    bad = r.o.isnan().flatten(1).all(1)
+    assert bad[-6:].all()
+    B.get_last_device_error()
+
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_peaked_and_flat_scores(dtype):
     """Scores of hundreds (one key takes the row) and of almost zero."""
     for std, scale in ((6.0, 1.0), (0.01, None)):
