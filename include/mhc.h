@@ -200,8 +200,9 @@ mhc_status mhc_post_bwd(mhc_dtype dt, const void* g_next, const void* x,
  * While on (nonzero), every launch of the bf16 forward kernels (the
  * tensor-core kernel and the small-batch cluster kernel of mhc_pre,
  * mhc_pre_gates and mhc_pre_critical), of mhc_paged_attn's tensor-core kernel
- * and of the pre backward's one-pass cluster kernel (mhc_pre_bwd) makes thread 0 of each CTA wait on an mbarrier
- * that nothing arrives on; the wait gives up after about 100 us, the kernel
+ * and of the pre backward's one-pass cluster kernel (mhc_pre_bwd) makes
+ * thread 0 of each CTA wait on an mbarrier that nothing arrives on; the wait
+ * gives up after about 100 us, the kernel
  * latches its device error word and returns before starting any copy or
  * tensor-memory allocation, leaving its outputs unwritten.  The next
  * mhc_get_last_device_error() then reports MHC_ERR_TIMEOUT, and the context

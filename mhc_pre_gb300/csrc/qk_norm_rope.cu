@@ -2,8 +2,9 @@
 // rotation: the training forward, and the serving form that writes keys and
 // values into a paged cache.  The mathematics and the shared parts are in
 // qk_norm_rope.cuh.
-// At T = 32768, 40 + 8 heads of 128, bf16: 138 us, 5.85 TB/s, 0.87 of the
-// measured copy rate; 4096 tokens into the cache 25 us.
+// Bound by memory traffic: at T = 32768, 40 + 8 heads of 128, bf16, 138 us,
+// 5.85 TB/s, 0.87 of the measured copy rate; 4096 tokens into the cache 25 us;
+// one token 3.5 us, a round of loads and its reduction.
 #include "qk_norm_rope.cuh"
 
 namespace mhc {

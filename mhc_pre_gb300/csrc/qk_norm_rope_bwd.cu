@@ -1,6 +1,6 @@
 // qk_norm_rope_bwd.cu -- backward of the per-head RMSNorm with rotation.  The
 // mathematics and the shared parts are in qk_norm_rope.cuh.
-// At T = 32768, 40 + 8 heads of 128, bf16: 194 us,
+// Bound by memory traffic: at T = 32768, 40 + 8 heads of 128, bf16, 194 us,
 // 6.2 TB/s, 0.93 of the measured copy rate.
 #include "qk_norm_rope.cuh"
 
