@@ -221,13 +221,18 @@ attn_plan_kernel(const PlanParams p) {
 // TY x 16 threads: thread (ty, tx) has the rows ty, ty + TY, ... of the tile and
 // keys tx, tx + 16, ... of a block for the scores, and the columns
 // 4 tx + 64 c of the values for the sums; a row's maximum and sum live in the
-// 16 lanes that share the row.  Products go through packed pairs of float32
+// 16 lanes that share the row.  Those are every other lane of a warp, which has
+// two rows at a time: 16-byte reads of shared memory take 2 cycles a warp where
+// neighbouring lanes share an address, and 4 where only lanes 16 apart do (a
+// chunk of 1024 tokens on 4096 keys in float32: 896 us, 960 with rows in half
+// warps).  Products go through packed pairs of float32
 // (pairs along d for the scores, of columns for the sums): a register tile of
 // 4 x 4 then has more arithmetic than shared-memory reads.  Keys and values
 // come by asynchronous copies, each while the other is being multiplied.
 // Bound by float32 arithmetic and the reads of the register tile from shared
-// memory: 6 sequences of up to 300 new tokens and 2000 keys, 20 + 4 heads of
-// 128, take 229 us, 30 TFLOP/s of the products that the mask leaves.
+// memory, which take about as long as each other: that chunk, of 20 + 4 heads of
+// 128, takes 878 us, 42.5 TFLOP/s of the products that the mask leaves; 6
+// sequences of up to 300 new tokens and 2000 keys 211 us.
 constexpr int CC_KEYS = 64, CC_KPT = CC_KEYS / 16;
 
 template <typename TA>
@@ -288,7 +293,7 @@ template <typename TA, int DP, int TY, int RPT>
 __device__ __forceinline__ void cc_piece(const AttnParams& p, const AttnPiece& pc, float* Qs, float* Ps, TA* Ks, TA* Vs,
                                          int* s_last) {
     constexpr int QP = DP + 4, PITCH = cc_pitch<TA>(DP), NC = DP / 64, PP = CC_PP;
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int tid = threadIdx.x, tx = (tid >> 1) & 15, ty = (tid >> 5) * 2 + (tid & 1);
     const float zscale = p.scale * LOG2E;
     const float cap_in = p.softcap > 0.0f ? p.scale / p.softcap : 0.0f;
     const int nrows = pc.qlen * p.G;
@@ -365,7 +370,7 @@ __device__ __forceinline__ void cc_piece(const AttnParams& p, const AttnPiece& p
                 mx = fmaxf(mx, s[j]);
             }
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o, 16));
+            for (int o = 16; o > 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             const float base = mx > -INFINITY ? mx : 0.0f;
             const float keep = exp2f(m[a] - base);
             float sum = 0.0f;
@@ -376,7 +381,7 @@ __device__ __forceinline__ void cc_piece(const AttnParams& p, const AttnPiece& p
                 Ps[(ty + TY * a) * PP + tx + 16 * j] = e;
             }
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o, 16);
+            for (int o = 16; o > 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             l[a] = fmaf(l[a], keep, sum);
             m[a] = mx;
             const float2 keep2 = make_float2(keep, keep);
@@ -389,7 +394,7 @@ __device__ __forceinline__ void cc_piece(const AttnParams& p, const AttnPiece& p
         if (more) asm volatile("cp.async.wait_group 1;" ::: "memory");   // the values; the next keys may still come
         else asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();
-#pragma unroll 2
+#pragma unroll 8
         for (int k = 0; k < CC_KEYS; k += 4) {
             float4 pr[RPT];
 #pragma unroll
