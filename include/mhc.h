@@ -504,6 +504,8 @@ mhc_status mhc_qk_norm_rope_append(mhc_dtype dt, const void* q, int64_t q_stride
  * A row that sees no key (m < n) gets o = 0 and lse = -inf.  Sums and softmax
  * statistics are float32; on the tensor cores the exponentials of a block are
  * rounded to bf16 for their product with the values (relative 2^-9 each).
+ * There a capped score is right to 2^-20 of a softcap of up to 256, and to a
+ * relative 2^-18 of the score with a larger one.
  *
  *   q [T, Hq, Dh]        dt               q_stride between tokens
  *   k_cache, v_cache     dt               as in mhc_qk_norm_rope_append

@@ -26,8 +26,8 @@
 // The running maximum is only raised when a row's new maximum exceeds it by
 // more than 2^8 in the exponentials' scale: float32 sums and bf16 exponentials
 // lose nothing by a common factor of up to 2^8, and O in tensor memory is then
-// rescaled a few times per row instead of at every block.  A cap of up to 52
-// bounds the scores so well that no maximum is needed at all (LOW_CAP).
+// rescaled a few times per row instead of at every block.  A cap below 52 bounds
+// the scores so well that no maximum is needed at all (LOW_CAP).
 //
 // Keys outside what a tile's rows see (past the sequence's end, before the
 // window, in pages that are not there) are masked in the scores, and their
@@ -84,13 +84,14 @@ constexpr uint32_t S_COL = 0, O_COL = 256;   // two of each, 128 columns apart
 constexpr uint64_t WAIT_LIMIT_NS = 1000000000ull;
 constexpr float RAISE = 8.0f;                // see above
 // Kinds of capping: none; a cap that bounds the scores so well that no maximum
-// is needed (below); any cap.
-constexpr int NO_CAP = 0, LOW_CAP = 1, HIGH_CAP = 2;
+// is needed (below); a higher one; one above HIGH_MOST, beside which ordinary
+// scores are so small that their tanh needs more care (near4).
+constexpr int NO_CAP = 0, LOW_CAP = 1, HIGH_CAP = 2, FAR_CAP = 3;
 // With |z| <= cap (in base 2, cap <= LOW_MOST) every row takes the base
 // min(cap, LOW_SPAN - cap): its exponentials then lie between 2^-90 and 2^60,
 // where bf16 and float32 round as everywhere, sums of 2^31 of them times values
 // of 2^30 stay finite, and a value below 2^-36 is the first that a row of
-// lowest scores could lose.  A softcap of 52 is the largest such.
+// lowest scores could lose.  The largest such softcap is 75 / log2 e = 51.98.
 constexpr float LOW_MOST = 75.0f, LOW_SPAN = 90.0f;
 constexpr uint32_t FULL = 0xffffffffu;
 
@@ -188,7 +189,10 @@ template <int DP> struct Pieces {
 // cap tanh(scale s / cap) in base 2, plus `c` - cap: tanh(x) = 1 - 2 / (e^2x + 1),
 // four quotients from one reciprocal of their denominators' product (so e^2x
 // stays below 2^30: past it a denominator changes nothing in float32).  Pairs
-// are neighbours in registers.
+// are neighbours in registers.  The difference leaves an error of about 2^-21
+// of the cap, whatever the score is: up to HIGH_MOST at most 1.2e-4, a
+// sixteenth of the exponentials' rounding to bf16.
+constexpr float HIGH_MOST = 256.0f;
 __device__ __forceinline__ void cap4(uint32_t* u, float in, float cap2, float c) {
     const float2 in2 = make_float2(in, in), one = make_float2(1.0f, 1.0f), c2 = make_float2(c, c);
     const float2 x = __fmul2_rn(make_float2(__uint_as_float(u[0]), __uint_as_float(u[1])), in2);
@@ -205,11 +209,37 @@ __device__ __forceinline__ void cap4(uint32_t* u, float in, float cap2, float c)
     u[3] = __float_as_uint(w.y);
 }
 
-// Scores of 32 keys become -inf where `seen` has no bit.
-__device__ __forceinline__ void mask32(uint32_t* u, uint32_t seen) {
+// The same for x = scale s / cap of at most NEAR, with `c` in place of `c` - cap:
+// scale s (tanh x) / x by the series of tanh to x^11, whose error is relative
+// (2^-27 at NEAR, where the quotients' is 2^-19 of the score).  18 packed
+// operations for four scores where the quotients have 7 and twice the MUFU's:
+// 2048 tokens on 32768 keys with a cap of 1e5 take 2130 us, 1315 with one of 60.
+constexpr float NEAR = 0.3f;
+__device__ __forceinline__ float2 near2(float2 s, float in, float zscale, float c) {
+    const float2 x = __fmul2_rn(s, make_float2(in, in)), w = __fmul2_rn(x, x);
+    auto both = [](float v) { return make_float2(v, v); };
+    float2 t = __ffma2_rn(w, both(-1382.0f / 155925.0f), both(62.0f / 2835.0f));
+    t = __ffma2_rn(w, t, both(-17.0f / 315.0f));
+    t = __ffma2_rn(w, t, both(2.0f / 15.0f));
+    t = __ffma2_rn(w, t, both(-1.0f / 3.0f));
+    t = __ffma2_rn(w, t, both(1.0f));
+    return __ffma2_rn(__fmul2_rn(s, both(zscale)), t, both(c));
+}
+__device__ __forceinline__ void near4(uint32_t* u, float in, float zscale, float c) {
+    const float2 a = near2(make_float2(__uint_as_float(u[0]), __uint_as_float(u[1])), in, zscale, c);
+    const float2 b = near2(make_float2(__uint_as_float(u[2]), __uint_as_float(u[3])), in, zscale, c);
+    u[0] = __float_as_uint(a.x);
+    u[1] = __float_as_uint(a.y);
+    u[2] = __float_as_uint(b.x);
+    u[3] = __float_as_uint(b.y);
+}
+
+// Scores of 32 keys become `with` where `seen` has no bit.
+constexpr uint32_t LOWEST = 0xff800000u;   // -inf
+__device__ __forceinline__ void mask32(uint32_t* u, uint32_t seen, uint32_t with = LOWEST) {
 #pragma unroll
     for (int e = 0; e < 32; ++e)
-        if (!(seen & (1u << e))) u[e] = 0xff800000u;
+        if (!(seen & (1u << e))) u[e] = with;
 }
 
 // The keys [lo, hi) that a row sees, and the bounds of its warp's rows.
@@ -243,6 +273,8 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
     const float cap2 = p.softcap * LOG2E, cap_in = CAP ? 2.0f * LOG2E * p.scale / p.softcap : 0.0f;
     const float low_base = fminf(cap2, LOW_SPAN - cap2);
     const float most = CAP ? 30.0f / cap_in : 0.0f;   // larger scores are capped as this one
+    // scale / cap, scale in base 2, the largest score that is near zero beside the cap (FAR_CAP)
+    const float near_in = p.scale / p.softcap, near_z = p.scale * LOG2E, near_most = NEAR * (p.softcap / p.scale);
     // rows of 32-byte multiples at 32-byte addresses are stored 32 bytes at a time
     const bool wide = p.Dh % 16 == 0 && (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0;
     uint32_t par_s = 0, par_o = 0, par_x = 0;
@@ -314,7 +346,7 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
                         for (int f = 0; f < 4; ++f)
                             mx[f] = max3(mx[f], __uint_as_float(u[e + f]), __uint_as_float(u[e + 4 + f]));
                     top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * zscale;
-                } else if constexpr (CAP == HIGH_CAP) {
+                } else if constexpr (CAP == HIGH_CAP || CAP == FAR_CAP) {
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                     auto sweep = [&](auto borders) {
 #pragma unroll 1
@@ -336,7 +368,8 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
                     top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     // tanh keeps the order, so the capped maximum is the maximum's
                     uint32_t t[4] = {__float_as_uint(fminf(top, most)), 0u, 0u, 0u};
-                    cap4(t, cap_in, cap2, cap2);
+                    if (CAP == FAR_CAP && fabsf(top) <= near_most) near4(t, near_in, near_z, 0.0f);
+                    else cap4(t, cap_in, cap2, cap2);
                     if (top > -INFINITY) top = __uint_as_float(t[0]);
                 }
                 if constexpr (CAP == LOW_CAP) top = m;
@@ -394,12 +427,41 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
                                 ptx::tmem_wait_ld();
                                 const bool border = borders.value && !see.all(g);
                                 // before the cap too: an unseen key's NaN must not reach its cap4's other three
-                                if (border) mask32(u, see.bits(g));
+                                if (border) mask32(u, see.bits(g), CAP == FAR_CAP ? 0u : LOWEST);
+                                bool near = false;   // every score of the warp's is near zero beside the cap
+                                if constexpr (CAP == FAR_CAP) {
+                                    float mx[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    u[e] = __float_as_uint(min_nan(__uint_as_float(u[e]), most));
+                                    for (int e = 0; e < 32; e += 8)
 #pragma unroll
-                                for (int e = 0; e < 32; e += 4) cap4(u + e, cap_in, cap2, cap2 - base);
+                                        for (int f = 0; f < 4; ++f)
+                                            mx[f] = max3(mx[f], fabsf(__uint_as_float(u[e + f])),
+                                                         fabsf(__uint_as_float(u[e + 4 + f])));
+                                    near = !__any_sync(FULL, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) > near_most);
+                                }
+                                if (near) {
+#pragma unroll
+                                    for (int e = 0; e < 32; e += 4) near4(u + e, near_in, near_z, -base);
+                                } else if (CAP == FAR_CAP) {
+#pragma unroll
+                                    for (int e = 0; e < 32; e += 4) {
+                                        uint32_t t[4] = {u[e], u[e + 1], u[e + 2], u[e + 3]}, q[4];
+#pragma unroll
+                                        for (int f = 0; f < 4; ++f)
+                                            q[f] = __float_as_uint(min_nan(__uint_as_float(t[f]), most));
+                                        cap4(q, cap_in, cap2, cap2 - base);
+                                        near4(t, near_in, near_z, -base);
+#pragma unroll
+                                        for (int f = 0; f < 4; ++f)
+                                            u[e + f] = fabsf(__uint_as_float(u[e + f])) <= near_most ? t[f] : q[f];
+                                    }
+                                } else {
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e)
+                                        u[e] = __float_as_uint(min_nan(__uint_as_float(u[e]), most));
+#pragma unroll
+                                    for (int e = 0; e < 32; e += 4) cap4(u + e, cap_in, cap2, cap2 - base);
+                                }
                                 if (border) mask32(u, see.bits(g));
 #pragma unroll
                                 for (int e = 0; e < 16; ++e) {
@@ -960,7 +1022,8 @@ cudaError_t launch_cap(int cap, const CUtensorMap& tq, const CUtensorMap& tk, co
     switch (cap) {
         case NO_CAP: return launch<DP, NO_CAP>(tq, tk, tv, p, s);
         case LOW_CAP: return launch<DP, LOW_CAP>(tq, tk, tv, p, s);
-        default: return launch<DP, HIGH_CAP>(tq, tk, tv, p, s);
+        case HIGH_CAP: return launch<DP, HIGH_CAP>(tq, tk, tv, p, s);
+        default: return launch<DP, FAR_CAP>(tq, tk, tv, p, s);
     }
 }
 
@@ -980,8 +1043,10 @@ cudaError_t launch_paged_attn_tc(const AttnParams& p, cudaStream_t s) {
     if (e == cudaSuccess) e = attn_tc::encode(fn, &tk, p.k_cache, p, p.k_page_stride, p.k_slot_stride, p.k_head_stride);
     if (e == cudaSuccess) e = attn_tc::encode(fn, &tv, p.v_cache, p, p.v_page_stride, p.v_slot_stride, p.v_head_stride);
     if (e != cudaSuccess) return e;
-    const int cap = p.softcap > 0.0f ? (p.softcap * LOG2E <= attn_tc::LOW_MOST ? attn_tc::LOW_CAP : attn_tc::HIGH_CAP)
-                                     : attn_tc::NO_CAP;
+    const int cap = !(p.softcap > 0.0f)                       ? attn_tc::NO_CAP
+                    : p.softcap * LOG2E <= attn_tc::LOW_MOST ? attn_tc::LOW_CAP
+                    : p.softcap <= attn_tc::HIGH_MOST        ? attn_tc::HIGH_CAP
+                                                             : attn_tc::FAR_CAP;
     return p.Dh <= 64 ? attn_tc::launch_cap<64>(cap, tq, tk, tv, p, s) : attn_tc::launch_cap<128>(cap, tq, tk, tv, p, s);
 }
 

@@ -1,0 +1,76 @@
+"""Attention over a paged cache where its numbers are at their limits: caps far
+above the scores, against the float64 oracle.
+
+Tolerances.  u = 2^-24; a score's products and sums are held to 32 sqrt(dh) u
+times the row's largest scale * sum |q k| ("size").  The cap: a relative 2^-18
+of the score, whatever the cap is (where the tanh is formed from a quotient, two
+approximations and five roundings come to 2^-20.5 of the cap, of which the
+score is then at least 0.3).  The rest is as in test_gpu_paged_attn.py: 2 e sum
+p |v| of an error e of the scores, 8 sqrt(n) u of the sums, 2^-20 of the
+exponentials, and for bf16 2^-8 of sum p |v| and of |o|.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from mhc_pre_gb300 import binding as B
+from oracle import attn_oracle as A
+from tests.test_gpu_paged_attn import LENS, U, Case, f64
+
+pytestmark = pytest.mark.gpu
+
+
+def check(c, r, softcap):
+    q, at = f64(c.q), 0
+    dh = q.shape[-1]
+    o, lse = f64(r.o), f64(r.lse)
+    for b, (n, m) in enumerate(c.lens):
+        assert np.all(np.isfinite(o[at:at + n]))
+        ro, rl, pabs, size = A.attention(q[at:at + n], f64(c.kd[b]), f64(c.vd[b]), dh ** -0.5, c.window, softcap)
+        e = (32 * np.sqrt(dh) * U + 2.0 ** -18) * size
+        tol = (2 * e + 8 * np.sqrt(max(m, 1)) * U + 2.0 ** -20)[..., None] * pabs
+        if c.dtype == "bf16":
+            tol = tol + 2.0 ** -8 * (pabs + np.abs(ro))
+        assert np.all(np.abs(o[at:at + n] - ro) <= tol), b
+        empty = ~np.isfinite(rl)
+        assert np.array_equal(empty, lse[at:at + n] == -np.inf)
+        ref = np.where(empty, 0, rl)
+        d = np.abs(np.where(empty, 0, lse[at:at + n]) - ref)
+        assert np.all(d <= e + 8 * np.sqrt(max(m, 1)) * U + 2.0 ** -20 * (1 + np.abs(ref))), (b, d.max())
+        at += n
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("softcap", [60.0, 400.0, 1e3, 1e4, 1e5, 1e6, 1e7, 1e30])
+@pytest.mark.parametrize("std", [1.5, 4.0])
+def test_a_caps_error_does_not_grow_with_it(std, softcap, dtype):
+    for dh, window in ((128, 0), (64, 60)):
+        c = Case(LENS["chunks"], 10, 2, dh, 64, dtype, std=std, window=window)
+        check(c, c.run(softcap=softcap), softcap)
+        assert B.get_last_device_error() == B.MHC_OK
+
+
+@pytest.mark.parametrize("softcap", [60.0, 1e5])
+def test_scores_on_both_sides_of_a_high_cap(softcap):
+    """Keys whose scores lie far below, near and above the cap, in every 32 of them."""
+    c = Case([(130, 300), (1, 200)], 4, 2, 64, 64, "bf16")
+    for b, (_, m) in enumerate(c.lens):
+        grow = (softcap ** (torch.arange(m) % 7 / 5.0 - 0.2))[:, None, None]
+        c.kd[b] = (c.kd[b].float() * grow).bfloat16()
+        for j in range(-(-m // 64)):
+            n = min(64, m - j * 64)
+            c.k[int(c.table[b, j]), :n] = c.kd[b][j * 64:j * 64 + n].to(c.k.device)
+    check(c, c.run(softcap=softcap), softcap)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("softcap", [51.9, 51.97, 52.1])
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+def test_every_score_at_a_cap_near_52(sign, softcap, dtype):
+    """tanh is +-1 for every key on both sides of the cap from which a maximum is kept."""
+    c = Case([(3, 300), (1, 70)], 4, 2, 64, 64, dtype)
+    c.q.fill_(16.0)
+    c.k = torch.where(c.k.isnan(), c.k, torch.full_like(c.k, 16.0 * sign))
+    c.kd = [torch.full_like(k, 16.0 * sign) for k in c.kd]
+    check(c, c.run(softcap=softcap), softcap)
