@@ -522,6 +522,9 @@ mhc_status mhc_qk_norm_rope_append(mhc_dtype dt, const void* q, int64_t q_stride
  *   sequence whose numbers do not fit the call (MHC_ERR_RANGE).
  *   workspace  device scratch of mhc_paged_attn_workspace_bytes() bytes; calls
  *              that may overlap need one each
+ * The tokens of a page number outside the cache count as zeros, keys and values
+ * (MHC_ERR_RANGE): their sequence's rows are computed with them, the other
+ * sequences' as ever.
  * What the pages hold beyond the cached tokens, or outside what a tile of rows
  * can see, is never used (it may be NaN).  Values that some row of a call sees
  * must be finite for every row's result to be.

@@ -30,9 +30,10 @@
 // the scores so well that no maximum is needed at all (LOW_CAP).
 //
 // Keys outside what a tile's rows see (past the sequence's end, before the
-// window, in pages that are not there) are masked in the scores, and their
-// value rows are zeroed in shared memory before the MMA reads them, so that
-// what the pages hold there (NaN, say) cannot reach a sum.
+// window) are masked in the scores, and their value rows are zeroed in shared
+// memory before the MMA reads them, so that what the pages hold there (NaN,
+// say) cannot reach a sum.  The keys and values of a page number outside the
+// cache are zeros.
 //
 // Bounds and figures, 40 query and 8 key heads of 128 on one GB300: 2048 new
 // tokens of 32768 keys take 0.83 to 0.85 ms, 1.58 PFLOP/s (0.81 of the library's
@@ -717,7 +718,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
                 const bool pair = pc.qlen * p.G - pc.row0 > p.plan.lane_rows;
                 const int nb = pc.nb;
                 const int32_t* row = p.page_table + pc.seq * p.table_stride;
-                // lane i: the page of box i of a block, -1 where no row sees its keys
+                // lane i: the page of box i of a block, -1 where no row sees its keys.  In
+                // place of a number outside the cache the page after the last one, of which
+                // the copy makes zeros.
                 auto page_of = [&](int j) {
                     const int key = (pc.blk + j) * KEYS + lane * box;
                     if (j >= nb || lane >= boxes || key + box <= tlo || key >= thi) return -1;
@@ -725,7 +728,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
                     const int page = row[pg];
                     if (page >= 0 && page < p.num_pages) return page;
                     atomicOr(&g_attn_tc_error, ATTN_ERR_RANGE);
-                    return -1;
+                    return static_cast<int>(p.num_pages);
                 };
                 auto load = [&](const CUtensorMap* tm, int j, int page) {
                     if (!wait_warp(bar(C::B_EMPTY + stage), (round & 1) ^ 1, abort_flag)) return false;

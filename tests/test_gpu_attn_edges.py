@@ -1,5 +1,5 @@
-"""Attention over a paged cache where its numbers are at their limits: caps far
-above the scores, against the float64 oracle.
+"""Attention over a paged cache where its numbers are at their limits, against
+the float64 oracle: caps far above the scores, page numbers outside the cache.
 
 Tolerances.  u = 2^-24; a score's products and sums are held to 32 sqrt(dh) u
 times the row's largest scale * sum |q k| ("size").  The cap: a relative 2^-18
@@ -74,3 +74,27 @@ def test_every_score_at_a_cap_near_52(sign, softcap, dtype):
     c.k = torch.where(c.k.isnan(), c.k, torch.full_like(c.k, 16.0 * sign))
     c.kd = [torch.full_like(k, 16.0 * sign) for k in c.kd]
     check(c, c.run(softcap=softcap), softcap)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("number", [10 ** 6, -5])
+@pytest.mark.parametrize("dh,lens", [(64, [(2, 200), (3, 90), (1, 300)]), (128, [(130, 700), (40, 200), (1, 64)])])
+def test_a_page_outside_the_cache_counts_as_zeros(dh, lens, number, dtype):
+    """Its keys score 0 and its values are 0, whatever ran on the GPU before."""
+    c = Case(lens, 4, 2, dh, 64, dtype)
+    want = c.run()
+    table = c.table.clone()
+    table[1, 1] = number
+    c.kd[1][64:128], c.vd[1][64:128] = 0.0, 0.0
+    results = []
+    for fill in (3.0, float("nan")):
+        other = Case([(5, 2000)] * 40, 4, 2, dh, 64, dtype)      # leaves its keys in every SM's shared memory
+        other.k.fill_(fill)
+        other.v.fill_(fill)
+        other.run()
+        r = B.mhc_paged_attn(c.q, c.k, c.v, table, c.cu, c.kv)
+        c.check(r, error=B.MHC_ERR_RANGE)
+        results.append(r)
+    n, m = lens[0][0], lens[0][0] + lens[1][0]
+    assert torch.equal(results[0].o, results[1].o) and torch.equal(results[0].lse, results[1].lse)
+    assert torch.equal(r.o[:n], want.o[:n]) and torch.equal(r.o[m:], want.o[m:])
