@@ -277,7 +277,9 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
     // scale / cap, scale in base 2, the largest score that is near zero beside the cap (FAR_CAP)
     const float near_in = p.scale / p.softcap, near_z = p.scale * LOG2E, near_most = NEAR * (p.softcap / p.scale);
     // rows of 32-byte multiples at 32-byte addresses are stored 32 bytes at a time
+    // (the workspace's offsets are multiples of 256 bytes, its own address of 16)
     const bool wide = p.Dh % 16 == 0 && (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0;
+    const bool wide_part = (reinterpret_cast<uintptr_t>(p.ws) & 31u) == 0;
     uint32_t par_s = 0, par_o = 0, par_x = 0;
     bool ok = true, lent = false;   // lane 1's sums are with lane 0
 
@@ -566,12 +568,18 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
                 } else if (valid) {
                     float* dst = part + static_cast<int64_t>(rt) * DP + c * 32;
 #pragma unroll
-                    for (int g = 0; g < 4; ++g)
-                        st32(dst + g * 8,
-                             make_uint4(__float_as_uint(f[8 * g]), __float_as_uint(f[8 * g + 1]),
-                                        __float_as_uint(f[8 * g + 2]), __float_as_uint(f[8 * g + 3])),
-                             make_uint4(__float_as_uint(f[8 * g + 4]), __float_as_uint(f[8 * g + 5]),
-                                        __float_as_uint(f[8 * g + 6]), __float_as_uint(f[8 * g + 7])));
+                    for (int g = 0; g < 4; ++g) {
+                        const uint4 x = make_uint4(__float_as_uint(f[8 * g]), __float_as_uint(f[8 * g + 1]),
+                                                   __float_as_uint(f[8 * g + 2]), __float_as_uint(f[8 * g + 3]));
+                        const uint4 y = make_uint4(__float_as_uint(f[8 * g + 4]), __float_as_uint(f[8 * g + 5]),
+                                                   __float_as_uint(f[8 * g + 6]), __float_as_uint(f[8 * g + 7]));
+                        if (wide_part) {
+                            st32(dst + g * 8, x, y);
+                        } else {
+                            *reinterpret_cast<uint4*>(dst + g * 8) = x;
+                            *reinterpret_cast<uint4*>(dst + g * 8 + 4) = y;
+                        }
+                    }
                 }
                 __syncwarp();
             }

@@ -98,3 +98,25 @@ def test_a_page_outside_the_cache_counts_as_zeros(dh, lens, number, dtype):
     n, m = lens[0][0], lens[0][0] + lens[1][0]
     assert torch.equal(results[0].o, results[1].o) and torch.equal(results[0].lse, results[1].lse)
     assert torch.equal(r.o[:n], want.o[:n]) and torch.equal(r.o[m:], want.o[m:])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dh", [64, 128])
+def test_buffers_at_16_bytes(dh, dtype, monkeypatch):
+    """Workspace and outputs at odd multiples of 16 bytes, which is all that the
+    library asks for; the long sequence's parts go through the workspace."""
+    c = Case([(1, 5000), (40, 900), (3, 3)], 10, 2, dh, 64, dtype)
+    want = c.run()
+
+    def empty(shape, dtype=None, device=None):
+        n = int(np.prod(shape)) * torch.empty((), dtype=dtype).element_size()
+        t = torch.empty(n + 32, dtype=torch.uint8, device=device)
+        at = (16 - t.data_ptr()) % 32
+        t = t[at:at + n].view(dtype).view(tuple(shape))
+        assert t.data_ptr() % 32 == 16
+        return t
+
+    monkeypatch.setattr(B, "_empty", empty)
+    got = c.run()
+    assert torch.equal(got.o, want.o) and torch.equal(got.lse, want.lse)
+    assert B.get_last_device_error() == B.MHC_OK
