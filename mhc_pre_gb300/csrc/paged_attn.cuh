@@ -122,12 +122,13 @@ __device__ __forceinline__ int attn_token(const AttnParams& p, int r) {
     return p.G == 1 ? r : static_cast<int>(__umulhi(static_cast<unsigned>(r), p.g_mul) >> p.g_shift);
 }
 
-// Keys [lo, hi) that token i of the sequence's new ones sees.
+// Keys [lo, hi) that token i of the sequence's new ones sees.  A token before the
+// cached ones has end = 0: end - window stays in 32 bits for every window.
 template <typename T>
 __device__ __forceinline__ void attn_token_keys(const T& t, int i, int window, int& lo, int& hi) {
-    const int pos = t.kvlen - t.qlen + i;
-    hi = max(0, min(t.kvlen, pos + 1));
-    lo = window > 0 ? max(0, pos - window + 1) : 0;
+    const int end = max(0, t.kvlen - t.qlen + i + 1);
+    hi = min(t.kvlen, end);
+    lo = window > 0 ? max(0, end - window) : 0;
 }
 
 // A CTA's pieces one after the other.

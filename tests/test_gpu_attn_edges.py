@@ -120,3 +120,13 @@ def test_buffers_at_16_bytes(dh, dtype, monkeypatch):
     got = c.run()
     assert torch.equal(got.o, want.o) and torch.equal(got.lse, want.lse)
     assert B.get_last_device_error() == B.MHC_OK
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 7, 2 ** 30])
+@pytest.mark.parametrize("dh", [64, 128])
+def test_a_window_of_any_size(dh, window, dtype):
+    """Also where a tile's first rows see nothing: their bounds stay in 32 bits."""
+    for lens in (LENS["empty"], [(40, 30), (1010, 1000), (1, 0), (3, 500)]):
+        c = Case(lens, 4, 2, dh, 16, dtype, window=window)
+        c.check(c.run())
