@@ -533,7 +533,8 @@ mhc_status mhc_qk_norm_rope_append(mhc_dtype dt, const void* q, int64_t q_stride
  * `workspace`, for any number of mhc_paged_attn calls with the same sizes: the
  * layers of one step.  It depends on cu_q, kv_lens, window and the sizes only.
  * A call whose sizes (max_q and max_kv among them) are not its plan's computes
- * nothing and sets MHC_ERR_RANGE.
+ * nothing and sets MHC_ERR_RANGE, and so does every later call with the plan of a
+ * call that ended with MHC_ERR_TIMEOUT: the batch has to be planned again.
  */
 mhc_status mhc_paged_attn_plan(mhc_dtype dt, const int32_t* cu_q, const int32_t* kv_lens, int64_t T, int B,
                                int Hq, int Hk, int Dh, int page_size, int64_t max_q, int64_t max_kv,

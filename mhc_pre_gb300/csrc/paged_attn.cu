@@ -171,6 +171,7 @@ attn_plan_kernel(const PlanParams p) {
         h->block_keys = BN;
         h->window = p.window;
         h->lead = p.plan.lead;
+        h->spent = 0;
     }
     AttnStart* starts = reinterpret_cast<AttnStart*>(p.ws + p.plan.start_off);
     // The border at unit u: moved to the nearer end of a small tile (of one key

@@ -55,6 +55,9 @@ struct AttnHead {       // start of the plan
     int ntiles;
     int ncta;
     int Hq, Hk, B, tile_rows, block_keys, window, lead;
+    int spent;          // a wait ran out in a call with this plan: parts of its tiles never
+                        // came, and their join counters stand where the next call would
+                        // take them for its own
 };
 static_assert(sizeof(AttnHead) <= 256, "the header has 256 bytes");
 
@@ -108,14 +111,17 @@ __device__ __forceinline__ int* attn_counts(const AttnParams& p) {
     return reinterpret_cast<int*>(p.ws + p.plan.count_off);
 }
 
-// Whether the plan in the workspace is the one that this call's sizes ask for: a
-// larger max_q would overrun the parts, a larger max_kv the page table.
+// Whether the plan in the workspace is the one that this call's sizes ask for (a
+// larger max_q would overrun the parts, a larger max_kv the page table) and its
+// counters are at zero.
 __device__ __forceinline__ bool attn_plan_agrees(const AttnParams& p) {
     const AttnHead* h = attn_head(p);
     return h->T == p.T && h->max_q == p.max_q && h->max_kv == p.max_kv && h->Hq == p.Hq && h->Hk == p.Hk &&
            h->B == p.B && h->tile_rows == p.plan.tile_rows && h->block_keys == p.plan.block_keys &&
-           h->window == p.window && h->ncta == p.plan.ncta && h->lead == p.plan.lead && h->ntiles >= 0 && h->ntiles <= p.plan.max_tiles && h->per_cta > 0;
+           h->window == p.window && h->ncta == p.plan.ncta && h->lead == p.plan.lead && h->ntiles >= 0 &&
+           h->ntiles <= p.plan.max_tiles && h->per_cta > 0 && h->spent == 0;
 }
+__device__ __forceinline__ void attn_plan_spent(const AttnParams& p) { reinterpret_cast<AttnHead*>(p.ws)->spent = 1; }
 
 // The token of row r.
 __device__ __forceinline__ int attn_token(const AttnParams& p, int r) {

@@ -44,7 +44,7 @@
 // from memory are the bound.
 //
 // Every wait is bounded (about one second); on expiry the kernel latches its
-// error word and all roles leave.
+// error word, marks the plan as spent and all roles leave.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -632,7 +632,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
 
     if (p.force_timeout != 0u) {
         // test hook: one bounded wait that runs out before anything async starts
-        if (tid == 0 && ptx::forced_wait_runs_out(sbase, 100000ull)) atomicOr(&g_attn_tc_error, ATTN_ERR_TIMEOUT);
+        if (tid == 0 && ptx::forced_wait_runs_out(sbase, 100000ull)) {
+            atomicOr(&g_attn_tc_error, ATTN_ERR_TIMEOUT);
+            ptx::griddep_wait();   // the plan is written
+            attn_plan_spent(p);
+        }
         __syncthreads();
         return;
     }
@@ -959,6 +963,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
     }
     __syncthreads();
     if (*abort_flag) {
+        if (tid == 0) attn_plan_spent(p);
         // let copies already issued land before the shared memory goes away
         const uint64_t t0 = ptx::globaltimer();
         while (ptx::globaltimer() - t0 < 20000ull) {

@@ -130,3 +130,29 @@ def test_a_window_of_any_size(dh, window, dtype):
     for lens in (LENS["empty"], [(40, 30), (1010, 1000), (1, 0), (3, 500)]):
         c = Case(lens, 4, 2, dh, 16, dtype, window=window)
         c.check(c.run())
+
+
+def test_a_plan_is_spent_by_a_timeout():
+    """Parts that never came would leave a plan's counters in mid-join: after a
+    timeout calls with it compute nothing and say so, and a new plan works."""
+    c = Case([(1, 3000), (20, 40)], 4, 2, 64, 64, "bf16")
+    sizes = (torch.bfloat16, c.T, 4, 2, 64, 64, c.T, c.table.shape[1] * 64)
+    plan = B.mhc_paged_attn_plan(c.cu, c.kv, *sizes)
+    want = B.mhc_paged_attn(c.q, c.k, c.v, c.table, plan=plan)
+    assert B.get_last_device_error() == B.MHC_OK
+    L = B.lib()
+    try:
+        assert L.mhc_test_force_timeout(1) == B.MHC_OK
+        B.mhc_paged_attn(c.q, c.k, c.v, c.table, plan=plan)
+        assert B.get_last_device_error() == B.MHC_ERR_TIMEOUT
+    finally:
+        assert L.mhc_test_force_timeout(0) == B.MHC_OK
+    out = torch.full_like(want.o, 7.0)
+    for _ in range(2):
+        B.mhc_paged_attn(c.q, c.k, c.v, c.table, plan=plan, out=out)
+        assert B.get_last_device_error() == B.MHC_ERR_RANGE
+        assert bool((out == 7.0).all())
+    plan = B.mhc_paged_attn_plan(c.cu, c.kv, *sizes)
+    got = B.mhc_paged_attn(c.q, c.k, c.v, c.table, plan=plan, out=out)
+    assert B.get_last_device_error() == B.MHC_OK
+    assert torch.equal(got.o, want.o) and torch.equal(got.lse, want.lse)
