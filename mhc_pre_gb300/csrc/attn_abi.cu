@@ -12,7 +12,7 @@ namespace {
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 mhc_status from_cuda(cudaError_t e) { return e == cudaSuccess ? MHC_OK : MHC_ERR_CUDA; }
 
-// Largest sizes taken: far inside what the kernels' index arithmetic holds.
+// Largest sizes taken: inside what the kernels' index arithmetic holds.
 constexpr int64_t MAX_T = int64_t(1) << 30, MAX_STRIDE = int64_t(1) << 36, MAX_KV = (int64_t(1) << 31) - 256;
 constexpr int MAX_HEADS = 1024;
 
@@ -78,6 +78,11 @@ mhc_status check_attn(mhc_dtype dt, int64_t T, int B, int Hq, int Hk, int Dh, in
     // tile's key range plus one block must not pass them
     if (B > (1 << 24) || max_q > MAX_T / Hq || max_kv > MAX_KV || T > MAX_T / Hq) return MHC_ERR_UNSUPPORTED;
     return MHC_OK;
+}
+
+// A tile's join counters are numbered in 32 bits.
+bool counters_fit(const mhc::AttnPlan& plan, int Hk) {
+    return plan.max_tiles * Hk < (int64_t(1) << 31) / mhc::JOINS;
 }
 
 }  // namespace
@@ -242,7 +247,8 @@ mhc_status mhc_qk_norm_rope_append(mhc_dtype dt, const void* q, int64_t q_stride
 size_t mhc_paged_attn_workspace_bytes(mhc_dtype dt, int64_t T, int B, int Hq, int Hk, int Dh, int page_size,
                                       int64_t max_q) {
     if (check_attn(dt, T, B, Hq, Hk, Dh, page_size, max_q, 0, 0) != MHC_OK || T == 0 || B == 0) return 0;
-    return mhc::attn_plan_sizes(dt == MHC_BF16, T, B, Hq, Hk, Dh, page_size, max_q).total;
+    const mhc::AttnPlan plan = mhc::attn_plan_sizes(dt == MHC_BF16, T, B, Hq, Hk, Dh, page_size, max_q);
+    return counters_fit(plan, Hk) ? plan.total : 0;
 }
 
 mhc_status mhc_paged_attn_plan(mhc_dtype dt, const int32_t* cu_q, const int32_t* kv_lens, int64_t T, int B, int Hq,
@@ -255,6 +261,7 @@ mhc_status mhc_paged_attn_plan(mhc_dtype dt, const int32_t* cu_q, const int32_t*
     if ((st = check_ptrs(ptrs, 1)) != MHC_OK) return st;
     if ((st = check_plain(cu_q, 4)) != MHC_OK || (st = check_plain(kv_lens, 4)) != MHC_OK) return st;
     const mhc::AttnPlan plan = mhc::attn_plan_sizes(dt == MHC_BF16, T, B, Hq, Hk, Dh, page_size, max_q);
+    if (!counters_fit(plan, Hk)) return MHC_ERR_UNSUPPORTED;
     if (ws_bytes < plan.total) return MHC_ERR_INVALID_ARG;
     return from_cuda(mhc::launch_attn_plan(plan, cu_q, kv_lens, T, B, Hq, Hk, window, max_q, max_kv, workspace, stream));
 }
@@ -282,6 +289,7 @@ mhc_status mhc_paged_attn(mhc_dtype dt, const void* q, int64_t q_stride, const v
         return st;
     if (table_stride < (max_kv + page_size - 1) / page_size) return MHC_ERR_INVALID_ARG;
     const mhc::AttnPlan plan = mhc::attn_plan_sizes(dt == MHC_BF16, T, B, Hq, Hk, Dh, page_size, max_q);
+    if (!counters_fit(plan, Hk)) return MHC_ERR_UNSUPPORTED;
     if (ws_bytes < plan.total) return MHC_ERR_INVALID_ARG;
     if (cu_q != nullptr) {
         st = mhc_paged_attn_plan(dt, cu_q, kv_lens, T, B, Hq, Hk, Dh, page_size, max_q, max_kv, window, workspace,

@@ -77,7 +77,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums, int
 __global__ void __launch_bounds__(PLAN_THREADS)
 attn_plan_kernel(const PlanParams p) {
     __shared__ int64_t sums[PLAN_THREADS / 32];
-    __shared__ int tile_base[PLAN_THREADS + 1];
+    __shared__ int tile_base[PLAN_THREADS];
     __shared__ int s_q0[PLAN_THREADS], s_qlen[PLAN_THREADS], s_kvlen[PLAN_THREADS];
     __shared__ int64_t s_start[PLAN_TILES];
     __shared__ AttnTile s_tile[PLAN_NEAR];   // the first tiles again, for the borders
@@ -106,16 +106,20 @@ attn_plan_kernel(const PlanParams p) {
         const int nt = (qlen * p.G + TR - 1) / TR;
         int64_t all = 0;
         const int64_t base = block_scan(nt, sums, all);
-        tile_base[tid] = static_cast<int>(base);
-        if (tid == 0) tile_base[PLAN_THREADS] = static_cast<int>(all);
+        // sequences of a call have at most max_tiles tiles unless their rows overlap
+        const int64_t room = p.plan.max_tiles - ntiles;
+        if (all > room) {
+            if (tid == 0) atomicOr(&g_attn_error, ATTN_ERR_RANGE);
+            all = room;
+        }
+        tile_base[tid] = static_cast<int>(min(base, room));
         s_q0[tid] = q0;
         s_qlen[tid] = qlen;
         s_kvlen[tid] = kvlen;
         __syncthreads();
         for (int t0 = 0; t0 < all; t0 += PLAN_THREADS) {
             const int i = t0 + tid;
-            const bool on = i < all && ntiles + i < p.plan.max_tiles;
-            if (i < all && !on) atomicOr(&g_attn_error, ATTN_ERR_RANGE);
+            const bool on = i < all;
             AttnTile t = {};
             if (on) {
                 // the sequence of tile i: the last one whose base is at most i
@@ -148,7 +152,7 @@ attn_plan_kernel(const PlanParams p) {
                 if (ntiles + i < PLAN_NEAR) s_tile[ntiles + i] = t;
             }
         }
-        ntiles = static_cast<int>(min(static_cast<int64_t>(ntiles) + all, p.plan.max_tiles));
+        ntiles += static_cast<int>(all);
         __syncthreads();
     }
     for (int64_t i = tid; i < static_cast<int64_t>(ntiles) * p.Hk * (JOINS / 4); i += PLAN_THREADS)

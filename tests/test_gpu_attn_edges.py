@@ -156,3 +156,14 @@ def test_a_plan_is_spent_by_a_timeout():
     got = B.mhc_paged_attn(c.q, c.k, c.v, c.table, plan=plan, out=out)
     assert B.get_last_device_error() == B.MHC_OK
     assert torch.equal(got.o, want.o) and torch.equal(got.lse, want.lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_sequences_that_overlap_have_no_more_tiles_than_fit(dtype):
+    """cu_q that goes back and forth: more tiles than any batch of these rows has."""
+    c = Case([(1024, 1100)], 4, 2, 64, 64, dtype)
+    n = 1400
+    cu = torch.tensor([0, 1024] * (n // 2) + [0], dtype=torch.int32, device=c.q.device)
+    kv = torch.full((n,), 1100, dtype=torch.int32, device=c.q.device)
+    r = B.mhc_paged_attn(c.q, c.k, c.v, c.table.expand(n, -1).contiguous(), cu, kv)
+    c.check(r, error=B.MHC_ERR_RANGE)
