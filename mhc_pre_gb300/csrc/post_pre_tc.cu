@@ -641,7 +641,7 @@ post_pre_mix_kernel(const __nv_bfloat16* __restrict__ x_next, const float* H_pre
             const uint64_t w0 = ptx::globaltimer();
             while (ld_acquire(tile_done + j) < need) {
                 if (ptx::globaltimer() - w0 > WAIT_LIMIT_NS) {
-                    atomicOr(&g_post_pre_error, 2u);
+                    atomicOr(&g_post_pre_error, 1u);
                     stop = 1;
                     break;
                 }
