@@ -190,8 +190,7 @@ qk_staged_kernel(const QkParams p, const Ring ring) {
                 x.store(vo + h * p.v_head_stride, L);
             }
         }
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(m.empty + 8 * s);
+        release_stage(m, s, lane);
         if (++s == ring.stages) {
             s = 0;
             parity ^= 1;

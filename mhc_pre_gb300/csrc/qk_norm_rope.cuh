@@ -337,6 +337,14 @@ __device__ __forceinline__ bool start_token(const P& p, const int64_t* slots, in
     return true;
 }
 
+// The warp has read stage s.  The bulk copies that refill it are of the
+// asynchronous proxy, which an arrive alone does not order behind these reads.
+__device__ __forceinline__ void release_stage(const Team& m, int s, int lane) {
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(m.empty + 8 * s);
+}
+
 // ------------------------------------------------------------------ host ---
 
 inline int lanes_per_head(int Dh) {

@@ -204,8 +204,7 @@ qk_staged_bwd_kernel(const QkBwdParams p, const Ring ring) {
             }
             head_backward<TA, LPH, ADJ>(x, g, ang, wk, dwk, good, inv_d, p.eps, dk + h * p.Dh, L, there);
         }
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(m.empty + 8 * s);
+        release_stage(m, s, lane);
         if (++s == ring.stages) {
             s = 0;
             parity ^= 1;
