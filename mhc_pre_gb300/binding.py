@@ -414,9 +414,12 @@ def mhc_pre_bwd_noalloc(g_in, dH_post, dH_res, x, phi, b, alpha, proj, inv_rms,
 #
 # These calls are made once per layer in a decoding step, where the host's time
 # is the call's time: their checks and marshalling are in a CPython module
-# (csrc/py_attn.cpp) linked to the library.
+# (csrc/py_attn.cpp), which is given the addresses of the library's entry points.
 
 CALLS_PATH = os.path.join(os.path.dirname(LIB_PATH), "_attn_calls.so")
+# the entry points that it calls, in its order
+CALLS_ENTRIES = ("mhc_qk_norm_rope", "mhc_qk_norm_rope_bwd", "mhc_qk_norm_rope_bwd_workspace_bytes",
+                 "mhc_qk_norm_rope_append", "mhc_paged_attn", "mhc_paged_attn_workspace_bytes")
 _calls_module = None
 
 
@@ -424,10 +427,11 @@ def _calls():
     """The module, loaded once."""
     global _calls_module
     if _calls_module is None:
-        lib()
+        handle = lib()
         if not os.path.exists(CALLS_PATH):
             raise RuntimeError(f"{CALLS_PATH} is missing: build it with `python -m mhc_pre_gb300.build`")
         from . import _attn_calls
+        _attn_calls.bind(*(ctypes.cast(getattr(handle, n), _P).value for n in CALLS_ENTRIES))
         _calls_module = _attn_calls
     return _calls_module
 

@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmhc_gb300.so")
-CALLS = os.path.join(HERE, "_attn_calls.so")     # CPython module that calls the library
+CALLS = os.path.join(HERE, "_attn_calls.so")     # CPython module that calls it (given the addresses)
 
 SOURCES = ["mhc_abi.cu", "kernels_fwd.cu", "kernels_bwd.cu", "pre_tc.cu", "pre_bwd_tc.cu",
            "pre_bwd_fused.cu",
@@ -82,7 +82,7 @@ def _compile_calls(nvcc: str) -> str:
 def _link_calls(obj: str) -> None:
     import torch
     tmp = CALLS + ".tmp"
-    _gxx(["-shared", "-o", tmp, obj, LIB, "-Wl,-rpath,$ORIGIN", "-L", os.path.join(os.path.dirname(torch.__file__), "lib"),
+    _gxx(["-shared", "-o", tmp, obj, "-L", os.path.join(os.path.dirname(torch.__file__), "lib"),
           "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"], "the Python module's link")
     os.replace(tmp, CALLS)
 

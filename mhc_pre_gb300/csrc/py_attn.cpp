@@ -18,6 +18,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <math.h>
 #include <stdint.h>
+#include <string.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -26,6 +27,20 @@
 namespace {
 
 using at::ScalarType;
+
+// The library's entry points, handed over by bind().  The module is not linked
+// to the library: whichever one the package has loaded is the one that both its
+// ctypes calls and these calls run, wherever the package lies.
+struct Library {
+    decltype(&mhc_qk_norm_rope) qk_norm_rope;
+    decltype(&mhc_qk_norm_rope_bwd) qk_norm_rope_bwd;
+    decltype(&mhc_qk_norm_rope_bwd_workspace_bytes) qk_norm_rope_bwd_workspace_bytes;
+    decltype(&mhc_qk_norm_rope_append) qk_norm_rope_append;
+    decltype(&mhc_paged_attn) paged_attn;
+    decltype(&mhc_paged_attn_workspace_bytes) paged_attn_workspace_bytes;
+};
+Library lib = {};
+constexpr int ENTRIES = sizeof(Library) / sizeof(void*);
 
 // One owned reference.
 class Ref {
@@ -260,6 +275,10 @@ PyObject* make_bytes(PyObject* empty, PyObject* like, size_t bytes, void** p) {
 }
 
 bool arguments(Py_ssize_t have, Py_ssize_t want) {
+    if (lib.qk_norm_rope == nullptr) {
+        PyErr_SetString(PyExc_RuntimeError, "bind() has not been called");
+        return false;
+    }
     if (have == want) return true;
     PyErr_SetString(PyExc_TypeError, "wrong number of arguments");
     return false;
@@ -267,6 +286,24 @@ bool arguments(Py_ssize_t have, Py_ssize_t want) {
 int clip(int64_t v) { return v > INT32_MAX ? INT32_MAX : static_cast<int>(v); }
 
 // --------------------------------------------------------------- functions ---
+
+// (addresses of the entry points, in the order of Library) -> None
+PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (n != ENTRIES) {
+        PyErr_SetString(PyExc_TypeError, "wrong number of entry points");
+        return nullptr;
+    }
+    void* at[ENTRIES];
+    for (int i = 0; i < ENTRIES; ++i) {
+        at[i] = PyLong_AsVoidPtr(a[i]);
+        if (at[i] == nullptr) {
+            if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "an entry point is missing");
+            return nullptr;
+        }
+    }
+    memcpy(&lib, at, sizeof(lib));
+    Py_RETURN_NONE;
+}
 
 // (empty, q, k, w_q, w_k, positions, cos_sin, eps, flags) -> (status, q_out, k_out)
 PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -289,7 +326,7 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!to) return nullptr;
     Ref tk(make(a[0], dt, a[1], 3, sk, &ko));
     if (!tk) return nullptr;
-    const int st = mhc_qk_norm_rope(code, q.p, q.stride, k.p, k.stride, static_cast<float*>(wq), static_cast<float*>(wk),
+    const int st = lib.qk_norm_rope(code, q.p, q.stride, k.p, k.stride, static_cast<float*>(wq), static_cast<float*>(wk),
                                     static_cast<int32_t*>(rope.positions), static_cast<float*>(rope.cos_sin),
                                     rope.max_pos, sq[0], clip(sq[1]), clip(sk[1]), clip(sq[2]), rope.rot, flags, eps, qo,
                                     sq[1] * sq[2], ko, sk[1] * sk[2], stream_of(a[1]));
@@ -341,10 +378,10 @@ PyObject* qk_norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!twq) return nullptr;
     Ref twk(make(a[0], ScalarType::Float, a[3], 1, sq + 2, &dwk));
     if (!twk) return nullptr;
-    const size_t need = mhc_qk_norm_rope_bwd_workspace_bytes(sq[0], clip(sq[2]));
+    const size_t need = lib.qk_norm_rope_bwd_workspace_bytes(sq[0], clip(sq[2]));
     Ref tws(make_bytes(a[0], a[3], need, &ws));
     if (!tws) return nullptr;
-    const int st = mhc_qk_norm_rope_bwd(
+    const int st = lib.qk_norm_rope_bwd(
         code, gq.p, gq.stride, gk.p, gk.stride, q.p, q.stride, k.p, k.stride, static_cast<float*>(wq),
         static_cast<float*>(wk), static_cast<int32_t*>(rope.positions), static_cast<float*>(rope.cos_sin), rope.max_pos,
         sq[0], clip(sq[1]), clip(sk[1]), clip(sq[2]), rope.rot, flags, eps, dq.p, dq.stride, dk.p, dk.stride,
@@ -382,7 +419,7 @@ PyObject* qk_norm_rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         return nullptr;
     Ref to(make(a[0], dt, a[1], 3, sq, &qo));
     if (!to) return nullptr;
-    const int st = mhc_qk_norm_rope_append(
+    const int st = lib.qk_norm_rope_append(
         code, q.p, q.stride, k.p, k.stride, v.p, v.stride, static_cast<float*>(wq), static_cast<float*>(wk),
         static_cast<int32_t*>(rope.positions), static_cast<float*>(rope.cos_sin), rope.max_pos,
         static_cast<int64_t*>(slots), sq[0], clip(sq[1]), clip(sk[1]), clip(sq[2]), rope.rot, flags, eps, qo,
@@ -441,7 +478,7 @@ PyObject* paged_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Ref tw;
     int64_t ws_bytes;
     if (a[12] == Py_None) {
-        ws_bytes = static_cast<int64_t>(mhc_paged_attn_workspace_bytes(code, T, clip(B), clip(sq[1]), clip(sc[2]),
+        ws_bytes = static_cast<int64_t>(lib.paged_attn_workspace_bytes(code, T, clip(B), clip(sq[1]), clip(sc[2]),
                                                                        clip(sq[2]), clip(page), max_q));
         tw.reset(make_bytes(a[0], a[1], static_cast<size_t>(ws_bytes), &ws));
         if (!tw) return nullptr;
@@ -463,7 +500,7 @@ PyObject* paged_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     Ref tl(make(a[0], ScalarType::Float, a[1], 2, sq, &lse));
     if (!tl) return nullptr;
-    const int st = mhc_paged_attn(code, q.p, q.stride, kc.p, kc.page, kc.slot, kc.head, vc.p, vc.page, vc.slot, vc.head,
+    const int st = lib.paged_attn(code, q.p, q.stride, kc.p, kc.page, kc.slot, kc.head, vc.p, vc.page, vc.slot, vc.head,
                                   sc[0], clip(page), static_cast<int32_t*>(table), B > 1 ? t->stride(0) : width,
                                   static_cast<int32_t*>(cu), static_cast<int32_t*>(kv), T, clip(B), clip(sq[1]),
                                   clip(sc[2]), clip(sq[2]), max_q, max_kv, window, scale, softcap, o,
@@ -473,7 +510,7 @@ PyObject* paged_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {FAST(qk_norm_rope), FAST(qk_norm_rope_bwd), FAST(qk_norm_rope_append), FAST(paged_attn),
+PyMethodDef methods[] = {FAST(bind), FAST(qk_norm_rope), FAST(qk_norm_rope_bwd), FAST(qk_norm_rope_append), FAST(paged_attn),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_attn_calls", "Marshalling of the attention sublayer's calls.", -1,
                       methods, nullptr, nullptr, nullptr, nullptr};
