@@ -430,7 +430,11 @@ def _calls():
         handle = lib()
         if not os.path.exists(CALLS_PATH):
             raise RuntimeError(f"{CALLS_PATH} is missing: build it with `python -m mhc_pre_gb300.build`")
-        from . import _attn_calls
+        from . import _attn_calls, build
+        made_for, here = _attn_calls.made_for, build.calls_made_for()
+        if made_for != here:
+            raise RuntimeError(f"{CALLS_PATH} was built for {made_for}, this is {here}: build it again with "
+                               "`python -m mhc_pre_gb300.build`")
         _attn_calls.bind(*(ctypes.cast(getattr(handle, n), _P).value for n in CALLS_ENTRIES))
         _calls_module = _attn_calls
     return _calls_module

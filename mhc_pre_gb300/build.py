@@ -11,6 +11,7 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +20,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmhc_gb300.so")
 CALLS = os.path.join(HERE, "_attn_calls.so")     # CPython module that calls it (given the addresses)
+CALLS_FOR = os.path.join(BUILD, "py_attn.for")       # the torch and Python that it was compiled for
 
 SOURCES = ["mhc_abi.cu", "kernels_fwd.cu", "kernels_bwd.cu", "pre_tc.cu", "pre_bwd_tc.cu",
            "pre_bwd_fused.cu",
@@ -64,44 +66,62 @@ def _gxx(cmd, what: str) -> None:
         raise RuntimeError(f"g++ failed on {what}:\n{r.stdout}\n{r.stderr}")
 
 
-def _compile_calls(nvcc: str) -> str:
-    """The object of the Python module of the attention sublayer's calls."""
+def calls_made_for() -> str:
+    """What the Python module is compiled against: it uses torch's C++ classes,
+    which no other torch or Python can be trusted to share."""
     import torch
-    src, obj = os.path.join(CSRC, "py_attn.cpp"), os.path.join(BUILD, "py_attn.o")
-    if os.path.exists(obj) and all(os.path.getmtime(d) <= os.path.getmtime(obj)
-                                   for d in (src, os.path.join(INCLUDE, "mhc.h"), os.path.abspath(__file__))):
-        return obj
+    return f"torch {torch.__version__}, {sys.implementation.cache_tag}"
+
+
+def _calls_missing() -> str | None:
+    """What this machine lacks to compile the Python module, if anything.  The
+    library needs none of it."""
+    try:
+        import torch
+    except ImportError:
+        return "torch"
+    root = os.path.dirname(torch.__file__)
+    for path in (os.path.join(root, "include", "torch", "csrc", "autograd", "python_variable.h"),
+                 os.path.join(root, "lib", "libc10_cuda.so"),
+                 os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        if not os.path.exists(path):
+            return path
+    return None if shutil.which("g++") else "g++"
+
+
+def _build_calls(nvcc: str, made_for: str) -> None:
+    """The Python module of the attention sublayer's calls."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    headers = os.path.join(root, "include")
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
-    headers = os.path.join(os.path.dirname(torch.__file__), "include")
+    src, obj, tmp = os.path.join(CSRC, "py_attn.cpp"), os.path.join(BUILD, "py_attn.o"), CALLS + ".tmp"
     _gxx(["-std=c++17", "-O2", "-fPIC", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
-          "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"), "-isystem", headers,
-          "-isystem", os.path.join(headers, "torch", "csrc", "api", "include"), "-c", src, "-o", obj], src)
-    return obj
-
-
-def _link_calls(obj: str) -> None:
-    import torch
-    tmp = CALLS + ".tmp"
-    _gxx(["-shared", "-o", tmp, obj, "-L", os.path.join(os.path.dirname(torch.__file__), "lib"),
-          "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"], "the Python module's link")
+          f'-DMHC_CALLS_MADE_FOR="{made_for}"', "-I", sysconfig.get_paths()["include"],
+          "-I", os.path.join(cuda, "include"), "-isystem", headers,
+          "-isystem", os.path.join(headers, "torch", "csrc", "api", "include"),
+          "-c", src, "-o", obj], src)
+    _gxx(["-shared", "-o", tmp, obj, "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda",
+          "-lc10"], "the Python module's link")
     os.replace(tmp, CALLS)
+    with open(CALLS_FOR, "w") as f:
+        f.write(made_for)
 
 
-def build(verbose: bool = False, extra_flags=()) -> str:
-    """Builds the library and its Python module if any source is newer than
-    they are; returns the library's path."""
-    os.makedirs(BUILD, exist_ok=True)
-    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    deps.append(os.path.join(INCLUDE, "mhc.h"))
-    deps.append(os.path.abspath(__file__))
-    if os.path.exists(LIB) and os.path.exists(CALLS) and not extra_flags:
-        lib_mtime = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
-        if all(os.path.getmtime(d) <= lib_mtime for d in deps):
-            return LIB
-    nvcc = _nvcc()
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        calls = ex.submit(_compile_calls, nvcc)
-        objs = list(ex.map(lambda s: _compile(nvcc, s, list(extra_flags)), SOURCES))
+def _fresh(target: str, deps) -> bool:
+    return os.path.exists(target) and all(os.path.getmtime(d) <= os.path.getmtime(target) for d in deps)
+
+
+def _calls_fresh(made_for: str, deps) -> bool:
+    if not _fresh(CALLS, deps) or not os.path.exists(CALLS_FOR):
+        return False
+    with open(CALLS_FOR) as f:
+        return f.read() == made_for
+
+
+def _build_library(nvcc: str, extra) -> None:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+        objs = list(ex.map(lambda s: _compile(nvcc, s, extra), SOURCES))
     libdir = _cuda_lib_dir(nvcc)
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs,
@@ -110,9 +130,33 @@ def build(verbose: bool = False, extra_flags=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_calls(calls.result())
-    if verbose:
-        print(f"built {LIB}")
+
+
+def build(verbose: bool = False, extra_flags=()) -> str:
+    """Builds the library and its Python module where a source is newer than
+    they are, and the module also for another torch or Python; returns the
+    library's path.  Without torch's headers, Python's or g++ the library is
+    built alone, and the binding says that its module is missing."""
+    os.makedirs(BUILD, exist_ok=True)
+    module = os.path.join(CSRC, "py_attn.cpp")
+    shared = [os.path.join(INCLUDE, "mhc.h"), os.path.abspath(__file__)]
+    sources = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
+    sources.remove(module)
+    missing = _calls_missing()
+    lib_due = bool(extra_flags) or not _fresh(LIB, sources + shared)
+    made_for = None if missing else calls_made_for()
+    calls_due = made_for is not None and not _calls_fresh(made_for, [module, *shared])
+    if lib_due or calls_due:
+        nvcc = _nvcc()
+        with cf.ThreadPoolExecutor(max_workers=2) as ex:
+            jobs = [ex.submit(_build_library, nvcc, list(extra_flags))] if lib_due else []
+            jobs += [ex.submit(_build_calls, nvcc, made_for)] if calls_due else []
+        for job in jobs:
+            job.result()
+        if verbose:
+            print(f"built {LIB}")
+    if missing:
+        print(f"the attention sublayer's Python calls are not built: {missing} is missing", file=sys.stderr)
     return LIB
 
 

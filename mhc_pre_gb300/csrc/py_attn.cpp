@@ -517,4 +517,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_attn_calls", "Marshalling of the 
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__attn_calls() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__attn_calls() {
+    Ref m(PyModule_Create(&module));
+    // the torch and Python that this was compiled for
+    if (!m || PyModule_AddStringConstant(m.get(), "made_for", MHC_CALLS_MADE_FOR) < 0) return nullptr;
+    return m.release();
+}
