@@ -161,6 +161,24 @@ cudaError_t launch_paged_attn(bool bf16, const AttnParams& p, cudaStream_t s);
 bool attn_tc_supports(bool bf16, int Hq, int Hk, int Dh, int page_size);
 cudaError_t launch_paged_attn_tc(const AttnParams& p, cudaStream_t s);
 
+// The host's side of a device error word.  Reading one is a blocking copy, so
+// words of kernels that no call has launched (or captured) are not asked for,
+// and a word is cleared only if it says something.
+class ErrorWord {
+  public:
+    void may_be_set() { used_.store(true, std::memory_order_relaxed); }
+    cudaError_t read_and_clear(unsigned& symbol, unsigned* word) const {
+        *word = 0;
+        if (!used_.load(std::memory_order_relaxed)) return cudaSuccess;
+        const unsigned zero = 0;
+        const cudaError_t e = cudaMemcpyFromSymbol(word, symbol, sizeof(unsigned));
+        if (e != cudaSuccess || *word == 0) return e;
+        return cudaMemcpyToSymbol(symbol, &zero, sizeof(unsigned));
+    }
+
+  private:
+    std::atomic<bool> used_{false};
+};
 // Device error words of these kernels, read and cleared.
 cudaError_t read_and_clear_qk_error(unsigned* word);
 cudaError_t read_and_clear_qk_bwd_error(unsigned* word);

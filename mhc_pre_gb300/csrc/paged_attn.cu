@@ -23,12 +23,9 @@ namespace mhc {
 
 __device__ unsigned g_attn_error;   // ATTN_ERR_* bits
 
-cudaError_t read_and_clear_attn_error(unsigned* word) {
-    cudaError_t e = cudaMemcpyFromSymbol(word, g_attn_error, sizeof(unsigned));
-    if (e != cudaSuccess) return e;
-    const unsigned zero = 0;
-    return cudaMemcpyToSymbol(g_attn_error, &zero, sizeof(unsigned));
-}
+static ErrorWord g_error_word;
+
+cudaError_t read_and_clear_attn_error(unsigned* word) { return g_error_word.read_and_clear(g_attn_error, word); }
 
 namespace attn {
 
@@ -582,6 +579,7 @@ AttnPlan attn_plan_sizes(bool bf16, int64_t T, int B, int Hq, int Hk, int Dh, in
 
 cudaError_t launch_attn_plan(const AttnPlan& plan, const int32_t* cu_q, const int32_t* kv_lens, int64_t T, int B,
                              int Hq, int Hk, int window, int64_t max_q, int64_t max_kv, void* ws, cudaStream_t s) {
+    g_error_word.may_be_set();
     attn::PlanParams p;
     p.cu_q = cu_q;
     p.kv_lens = kv_lens;
@@ -600,6 +598,7 @@ cudaError_t launch_attn_plan(const AttnPlan& plan, const int32_t* cu_q, const in
 }
 
 cudaError_t launch_paged_attn(bool bf16, const AttnParams& p, cudaStream_t s) {
+    g_error_word.may_be_set();
     if (attn_tc_supports(bf16, p.Hq, p.Hk, p.Dh, p.page_size)) return launch_paged_attn_tc(p, s);
     return bf16 ? attn::launch_cc_dp<__nv_bfloat16>(p, s) : attn::launch_cc_dp<float>(p, s);
 }

@@ -60,12 +60,9 @@ namespace mhc {
 
 __device__ unsigned g_attn_tc_error;   // ATTN_ERR_* bits
 
-cudaError_t read_and_clear_attn_tc_error(unsigned* word) {
-    cudaError_t e = cudaMemcpyFromSymbol(word, g_attn_tc_error, sizeof(unsigned));
-    if (e != cudaSuccess) return e;
-    const unsigned zero = 0;
-    return cudaMemcpyToSymbol(g_attn_tc_error, &zero, sizeof(unsigned));
-}
+static ErrorWord g_error_word;
+
+cudaError_t read_and_clear_attn_tc_error(unsigned* word) { return g_error_word.read_and_clear(g_attn_tc_error, word); }
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();   // pre_tc.cu
 
@@ -1052,6 +1049,7 @@ bool attn_tc_supports(bool bf16, int Hq, int Hk, int Dh, int page_size) {
 }
 
 cudaError_t launch_paged_attn_tc(const AttnParams& p, cudaStream_t s) {
+    g_error_word.may_be_set();
     auto fn = tensor_map_encoder();
     if (fn == nullptr) return cudaErrorNotSupported;
     CUtensorMap tq, tk, tv;

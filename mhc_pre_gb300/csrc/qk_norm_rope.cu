@@ -9,12 +9,9 @@
 
 namespace mhc {
 
-cudaError_t read_and_clear_qk_error(unsigned* word) {
-    cudaError_t e = cudaMemcpyFromSymbol(word, g_qk_error, sizeof(unsigned));
-    if (e != cudaSuccess) return e;
-    const unsigned zero = 0;
-    return cudaMemcpyToSymbol(g_qk_error, &zero, sizeof(unsigned));
-}
+static ErrorWord g_error_word;
+
+cudaError_t read_and_clear_qk_error(unsigned* word) { return g_error_word.read_and_clear(g_qk_error, word); }
 
 namespace qk {
 
@@ -240,6 +237,7 @@ cudaError_t launch_fwd(const QkParams& p, cudaStream_t s) {
 }  // namespace qk
 
 cudaError_t launch_qk_norm_rope(bool bf16, bool adjacent, bool append, const QkParams& p, cudaStream_t s) {
+    g_error_word.may_be_set();
     using B = __nv_bfloat16;
     if (bf16) {
         if (append) return adjacent ? qk::launch_fwd<B, true, true>(p, s) : qk::launch_fwd<B, false, true>(p, s);

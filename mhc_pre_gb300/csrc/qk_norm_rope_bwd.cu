@@ -6,12 +6,9 @@
 
 namespace mhc {
 
-cudaError_t read_and_clear_qk_bwd_error(unsigned* word) {
-    cudaError_t e = cudaMemcpyFromSymbol(word, g_qk_error, sizeof(unsigned));
-    if (e != cudaSuccess) return e;
-    const unsigned zero = 0;
-    return cudaMemcpyToSymbol(g_qk_error, &zero, sizeof(unsigned));
-}
+static ErrorWord g_error_word;
+
+cudaError_t read_and_clear_qk_bwd_error(unsigned* word) { return g_error_word.read_and_clear(g_qk_error, word); }
 
 namespace qk {
 
@@ -288,6 +285,7 @@ int64_t qk_bwd_blocks(int64_t T) {
 
 cudaError_t launch_qk_norm_rope_bwd(bool bf16, bool adjacent, const QkBwdParams& p, float* dw_q, float* dw_k,
                                     cudaStream_t s) {
+    g_error_word.may_be_set();
     using B = __nv_bfloat16;
     int64_t nblk = 0;
     cudaError_t e;
