@@ -167,3 +167,23 @@ def test_sequences_that_overlap_have_no_more_tiles_than_fit(dtype):
     kv = torch.full((n,), 1100, dtype=torch.int32, device=c.q.device)
     r = B.mhc_paged_attn(c.q, c.k, c.v, c.table.expand(n, -1).contiguous(), cu, kv)
     c.check(r, error=B.MHC_ERR_RANGE)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dh", [136, 256])
+def test_wide_heads(dh, dtype):
+    """Heads above 128: windows, caps, both, and contexts that are split and joined."""
+    for lens in (LENS["chunks"], [(1, 6000), (2, 1500)]):
+        for window, softcap in ((100, 0.0), (0, 30.0), (100, 60.0), (0, 0.0)):
+            c = Case(lens, 4, 2, dh, 16, dtype, window=window)
+            check(c, c.run(softcap=softcap), softcap)
+    assert B.get_last_device_error() == B.MHC_OK
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("page", [24, 64])
+def test_long_contexts_with_the_heads_outside(page, dtype):
+    for softcap in (0.0, 30.0, 60.0, 1e4):
+        c = Case([(1, 7000), (2, 3001), (1, 5)], 10, 2, 128, page, dtype, order="head")
+        check(c, c.run(softcap=softcap), softcap)
+    assert B.get_last_device_error() == B.MHC_OK
