@@ -158,7 +158,6 @@ attn_plan_kernel(const PlanParams p) {
     if (per < 1) per = 1;
     if (tid == 0) {
         AttnHead* h = reinterpret_cast<AttnHead*>(p.ws);
-        h->units = units;
         h->per_cta = per;
         h->T = p.T;
         h->max_q = p.max_q;

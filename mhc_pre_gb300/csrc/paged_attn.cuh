@@ -48,7 +48,6 @@ struct alignas(16) AttnTile {
 static_assert(sizeof(AttnTile) == 48, "AttnTile is read as three 16-byte words");
 
 struct AttnHead {       // start of the plan
-    int64_t units;      // all units
     int64_t per_cta;    // units of a CTA
     int64_t T;          // this and the sizes below: for the check that plan and call agree
     int64_t max_q, max_kv;
@@ -220,11 +219,6 @@ __device__ __forceinline__ float* attn_slot(const AttnParams& p, int slot) {
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ float lg2(float x) {
-    float r;
-    asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 
