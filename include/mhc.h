@@ -72,7 +72,7 @@ const char* mhc_version(void);
  * word on the current device.  Returns MHC_OK if no kernel latched an error,
  * MHC_ERR_TIMEOUT if a bounded wait ran out, MHC_ERR_RANGE if a kernel of the
  * attention sublayer met a number in device memory that points outside its
- * tensor, MHC_ERR_CUDA if the synchronisation itself failed. */
+ * tensor (and none ran out), MHC_ERR_CUDA if the synchronisation itself failed. */
 mhc_status mhc_get_last_device_error(cudaStream_t stream);
 
 /*
@@ -527,7 +527,8 @@ mhc_status mhc_qk_norm_rope_append(mhc_dtype dt, const void* q, int64_t q_stride
  * sequences' as ever.
  * What the pages hold beyond the cached tokens, or outside what a tile of rows
  * can see, is never used (it may be NaN).  Values that some row of a call sees
- * must be finite for every row's result to be.
+ * must be finite for every row's result to be, and with a softcap between 31 and
+ * 52 below 2^30: no running maximum is kept there on the tensor cores.
  *
  * mhc_paged_attn_plan -- splits the batch over the GPU (one small kernel) into
  * `workspace`, for any number of mhc_paged_attn calls with the same sizes: the

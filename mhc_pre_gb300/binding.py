@@ -485,7 +485,8 @@ def mhc_paged_attn_plan(cu_q, kv_lens, dtype, T: int, Hq: int, Hk: int, Dh: int,
                         max_q: int, max_kv: int, window: int = 0):
     """Splits a batch over the GPU once, for every mhc_paged_attn call of the
     same sizes (the layers of one step).  Calls that share a plan share its
-    workspace: they must not overlap."""
+    workspace: they must not overlap.  After a call that timed out the batch has
+    to be planned again."""
     B = kv_lens.numel()
     for t, name, n in ((cu_q, "cu_q", B + 1), (kv_lens, "kv_lens", B)):
         if t.dtype != torch.int32:

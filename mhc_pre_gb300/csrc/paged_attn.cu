@@ -232,8 +232,9 @@ attn_plan_kernel(const PlanParams p) {
 // come by asynchronous copies, each while the other is being multiplied.
 // Bound by float32 arithmetic and the reads of the register tile from shared
 // memory, which take about as long as each other: that chunk, of 20 + 4 heads of
-// 128, takes 878 us, 42.5 TFLOP/s of the products that the mask leaves; 6
-// sequences of up to 300 new tokens and 2000 keys 211 us.
+// 128, takes 883 us, 42.6 TFLOP/s of the products that the mask leaves; 6
+// sequences of up to 300 new tokens and 2000 keys 216 us; one new token for each
+// of 64 sequences of up to 8192 keys (20 + 4 heads) 320 us, 2.4 TB/s.
 constexpr int CC_KEYS = 64, CC_KPT = CC_KEYS / 16;
 
 template <typename TA>

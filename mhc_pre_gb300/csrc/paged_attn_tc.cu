@@ -36,12 +36,15 @@
 // cache are zeros.
 //
 // Bounds and figures, 40 query and 8 key heads of 128 on one GB300: 2048 new
-// tokens of 32768 keys take 0.83 to 0.85 ms, 1.58 PFLOP/s (0.81 of the library's
-// burst rate for a plain product; the lanes' softmax and the products share the
-// time, the tensor pipe is active for 62 % of it).  One new token for each of 64
-// sequences of up to 8192 keys takes 124 us, 6.1 TB/s, and two for each of 4
-// sequences of 131072 keys 320 us, 6.7 TB/s: there the keys and values coming
-// from memory are the bound.
+// tokens of 32768 keys take 0.80 to 0.85 ms in short runs, 1.6 PFLOP/s (0.81 of
+// the library's burst rate for a plain product; the lanes' softmax and the
+// products share the time, the tensor pipe is active for 62 % of it), and 0.93 to
+// 0.97 ms as calls in a row, under the power cap.  One new token for each of 64
+// sequences of up to 8192 keys takes 128 to 131 us with the plan, 5.9 TB/s, and
+// two for each of 4 sequences of 131072 keys 325 us, 6.6 TB/s: there the keys and
+// values coming from memory are the bound.  Tiles of few blocks (prompts with a
+// window, heads of 64) take 6.8 us each and 1.03 a block without a cap, 3.0 and
+// 2.2 with one of 30.
 //
 // Every wait is bounded (about one second); on expiry the kernel latches its
 // error word, marks the plan as spent and all roles leave.

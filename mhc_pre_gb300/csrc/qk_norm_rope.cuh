@@ -353,7 +353,7 @@ inline int lanes_per_head(int Dh) {
     return l;
 }
 
-// The ring for rows of these sizes: teams of 1 or 4 warps, blocks per SM, or
+// The ring for rows of these sizes: teams of 1, 2 or 4 warps, blocks per SM, or
 // stages = 0 where two stages do not fit or there are too few tokens.
 struct RingPlan {
     Ring ring;
