@@ -492,6 +492,57 @@ mhc_status mhc_qk_norm_rope_append(mhc_dtype dt, const void* q, int64_t q_stride
                                    int page_size, cudaStream_t stream);
 
 /*
+ * mhc_rope_table -- the angles that the rotations take, for positions
+ * 0 .. n - 1: row p holds amplitude cos(p f_j), then amplitude sin(p f_j), for
+ * the rot/2 frequencies
+ *   f_j = e_j (g_j + (1 - g_j) / factor),     e_j = base^(-2j / rot),
+ *   g_j = (original e_j / 2 pi - low) / (high - low), held to [0, 1].
+ * With factor = 1 that is the plain rotation.  For contexts `factor` times as
+ * long as the trained one, original = 0 slows every pair down alike (positions
+ * are interpolated linearly); with the trained length as `original`, pairs that
+ * make more than `high` turns over it keep their frequency, those that make
+ * fewer than `low` are slowed down, and the ones between are blended.  Scaling
+ * the base is the caller's: base factor^(rot / (rot - 2)).
+ * Angles are right to p f_j 2^-51 for every position (frequencies are computed in
+ * double and multiplied by positions in 64-bit integers), values to 3 2^-24 times
+ * the amplitude.
+ *
+ *   base >= 1, factor > 0, original >= 0, low < high, all finite
+ *   rot  int             multiple of 16, 16 <= rot <= 256
+ * output: cos_sin [n, rot] float, 16-byte aligned.  n = 0 is a no-op.
+ */
+mhc_status mhc_rope_table(int64_t n, int rot, double base, double factor, double original, double low, double high,
+                          float amplitude, float* cos_sin, cudaStream_t stream);
+
+/*
+ * mhc_rope -- mhc_qk_norm_rope without the normalisation: every head of q and k
+ * has its first `rot` values turned by the token's position, the others are
+ * copied.  Each value is rounded to dt once.  A table with an amplitude scales
+ * the turned values.
+ * mhc_rope_bwd -- gradients of <g_q, q_out> + <g_k, k_out>: the turned values
+ * turned back (times the amplitude).  It needs neither q nor k.
+ * mhc_rope_append -- the serving form, as mhc_qk_norm_rope_append.
+ * Arguments as there; rot > 0.  Outputs may be the same memory as q and k with
+ * the same strides.  A token whose position is out of range gets zeros
+ * (gradients too) and is not appended.  T = 0 is a no-op.
+ */
+mhc_status mhc_rope(mhc_dtype dt, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                    const int32_t* positions, const float* cos_sin, int64_t max_pos, int64_t T, int Hq, int Hk,
+                    int Dh, int rot, int flags, void* q_out, int64_t q_out_stride, void* k_out,
+                    int64_t k_out_stride, cudaStream_t stream);
+mhc_status mhc_rope_bwd(mhc_dtype dt, const void* g_q, int64_t gq_stride, const void* g_k, int64_t gk_stride,
+                        const int32_t* positions, const float* cos_sin, int64_t max_pos, int64_t T, int Hq, int Hk,
+                        int Dh, int rot, int flags, void* dq, int64_t dq_stride, void* dk, int64_t dk_stride,
+                        cudaStream_t stream);
+mhc_status mhc_rope_append(mhc_dtype dt, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                           const void* v, int64_t v_stride, const int32_t* positions, const float* cos_sin,
+                           int64_t max_pos, const int64_t* slots, int64_t T, int Hq, int Hk, int Dh, int rot,
+                           int flags, void* q_out, int64_t q_out_stride, void* k_cache, int64_t k_page_stride,
+                           int64_t k_slot_stride, int64_t k_head_stride, void* v_cache, int64_t v_page_stride,
+                           int64_t v_slot_stride, int64_t v_head_stride, int64_t num_pages, int page_size,
+                           cudaStream_t stream);
+
+/*
  * mhc_paged_attn -- causal attention of new tokens over a paged cache that
  * holds their keys and values already.  Sequence b of B has the rows
  * cu_q[b] .. cu_q[b+1] of q (its newest tokens, n of them; one in decoding, a

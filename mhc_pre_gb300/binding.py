@@ -35,7 +35,8 @@ EXPORTS = ("mhc_status_string", "mhc_version", "mhc_get_last_device_error",
            "mhc_post_res_gates",
            "mhc_qk_norm_rope", "mhc_qk_norm_rope_bwd", "mhc_qk_norm_rope_bwd_workspace_bytes",
            "mhc_qk_norm_rope_append", "mhc_paged_attn_plan", "mhc_paged_attn",
-           "mhc_paged_attn_workspace_bytes")
+           "mhc_paged_attn_workspace_bytes",
+           "mhc_rope_table", "mhc_rope", "mhc_rope_bwd", "mhc_rope_append")
 
 PreOut = namedtuple("PreOut", "x_in H_pre H_post H_res proj inv_rms")
 PostPreOut = namedtuple("PostPreOut", "x_next x_in H_pre H_post H_res proj inv_rms")
@@ -54,6 +55,7 @@ PagedAttnPlan = namedtuple("PagedAttnPlan", "workspace sizes")
 ROPE_ADJACENT = 1
 
 _P, _I64, _I, _F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
+_D = ctypes.c_double
 _SIGS = {
     "mhc_status_string": ([_I], ctypes.c_char_p),
     "mhc_version": ([], ctypes.c_char_p),
@@ -98,6 +100,11 @@ _SIGS = {
                         _P, _I64, _P, _P, _I64, _I, _I, _I, _I, _I64, _I64, _I, _F, _F, _P, _P,
                         _P, ctypes.c_size_t, _P], _I),
     "mhc_paged_attn_workspace_bytes": ([_I, _I64, _I, _I, _I, _I, _I, _I64], ctypes.c_size_t),
+    "mhc_rope_table": ([_I64, _I, _D, _D, _D, _D, _D, _F, _P, _P], _I),
+    "mhc_rope": ([_I, _P, _I64, _P, _I64, _P, _P, _I64, _I64, _I, _I, _I, _I, _I, _P, _I64, _P, _I64, _P], _I),
+    "mhc_rope_bwd": ([_I, _P, _I64, _P, _I64, _P, _P, _I64, _I64, _I, _I, _I, _I, _I, _P, _I64, _P, _I64, _P], _I),
+    "mhc_rope_append": ([_I, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _P, _I64, _I, _I, _I, _I, _I, _P, _I64,
+                         _P, _I64, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I, _P], _I),
 }
 
 _lib = None
@@ -419,7 +426,8 @@ def mhc_pre_bwd_noalloc(g_in, dH_post, dH_res, x, phi, b, alpha, proj, inv_rms,
 CALLS_PATH = os.path.join(os.path.dirname(LIB_PATH), "_attn_calls.so")
 # the entry points that it calls, in its order
 CALLS_ENTRIES = ("mhc_qk_norm_rope", "mhc_qk_norm_rope_bwd", "mhc_qk_norm_rope_bwd_workspace_bytes",
-                 "mhc_qk_norm_rope_append", "mhc_paged_attn", "mhc_paged_attn_workspace_bytes")
+                 "mhc_qk_norm_rope_append", "mhc_paged_attn", "mhc_paged_attn_workspace_bytes",
+                 "mhc_rope", "mhc_rope_bwd", "mhc_rope_append")
 _calls_module = None
 
 
@@ -478,6 +486,58 @@ def mhc_qk_norm_rope_append(q, k, v, w_q, w_k, k_cache, v_cache, slots, position
         ROPE_ADJACENT if interleaved else 0)
     if st:
         _check(st, "mhc_qk_norm_rope_append")
+    return out
+
+
+def mhc_rope_table(n: int, rot: int, base: float = 10000.0, factor: float = 1.0, original: float = 0.0,
+                   low: float = 1.0, high: float = 32.0, amplitude: float = 1.0, device=None):
+    """[n, rot] float32: cosines, then sines, of the positions 0 .. n - 1 for the
+    rotations' ``cos_sin``.  ``factor``: contexts that many times as long as the
+    trained one; ``original`` 0 slows every pair down by it, a trained length
+    only the pairs that make fewer than ``high`` turns over it (all of it below
+    ``low`` turns).  ``device``: a CUDA device (default: the current one)."""
+    dev = torch.device("cuda" if device is None else device)
+    if dev.type != "cuda":
+        raise ValueError("the mHC library takes CUDA tensors only")
+    if n < 0 or rot < 0:
+        raise ValueError(f"a table of {n} positions and {rot} values")
+    out = _empty((n, rot), dtype=torch.float32, device=dev)
+    with torch.cuda.device(out.device):
+        st = lib().mhc_rope_table(n, rot, base, factor, original, low, high, amplitude, _ptr(out), _stream(out.device))
+    _check(st, "mhc_rope_table")
+    return out
+
+
+def mhc_rope(q, k, positions, cos_sin, interleaved: bool = False):
+    """The rotation alone: the first cos_sin.shape[1] values of each head of
+    q [T, Hq, Dh] and k [T, Hk, Dh] turned by cos_sin[positions], the others
+    copied.  ``interleaved``: pairs (2j, 2j + 1)."""
+    st, qo, ko = (_calls_module or _calls()).rope(_allocator(), q, k, positions, cos_sin,
+                                                  ROPE_ADJACENT if interleaved else 0, 0, None, None)
+    if st:
+        _check(st, "mhc_rope")
+    return QKOut(qo, ko)
+
+
+def mhc_rope_bwd(g_q, g_k, positions, cos_sin, interleaved: bool = False, dq=None, dk=None):
+    """Gradients of <g_q, q_out> + <g_k, k_out> for mhc_rope, as (q, k).  ``dq``
+    and ``dk`` (parts of a packed gradient, say) are written when given; they may
+    be g_q and g_k."""
+    st, dq, dk = (_calls_module or _calls()).rope(_allocator(), g_q, g_k, positions, cos_sin,
+                                                  ROPE_ADJACENT if interleaved else 0, 1, dq, dk)
+    if st:
+        _check(st, "mhc_rope_bwd")
+    return QKOut(dq, dk)
+
+
+def mhc_rope_append(q, k, v, k_cache, v_cache, slots, positions, cos_sin, interleaved: bool = False):
+    """The serving form of mhc_rope: returns the rotated q; the rotated keys and
+    the values go to slots[t] = page * page_size + place of the caches
+    [pages, page_size, Hk, Dh] (-1: nowhere), in place."""
+    st, out = (_calls_module or _calls()).rope_append(
+        _allocator(), q, k, v, k_cache, v_cache, slots, positions, cos_sin, ROPE_ADJACENT if interleaved else 0)
+    if st:
+        _check(st, "mhc_rope_append")
     return out
 
 

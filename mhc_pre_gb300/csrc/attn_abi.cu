@@ -244,6 +244,128 @@ mhc_status mhc_qk_norm_rope_append(mhc_dtype dt, const void* q, int64_t q_stride
     return from_cuda(mhc::launch_qk_norm_rope(dt == MHC_BF16, (flags & MHC_ROPE_ADJACENT) != 0, true, p, stream));
 }
 
+static mhc_status rope_call(mhc_dtype dt, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                            const int32_t* positions, const float* cos_sin, int64_t max_pos, int64_t T, int Hq, int Hk,
+                            int Dh, int rot, int flags, bool back, void* q_out, int64_t q_out_stride, void* k_out,
+                            int64_t k_out_stride, cudaStream_t stream) {
+    mhc_status st = check_heads(dt, T, Hq, Hk, Dh);
+    if (st != MHC_OK) return st;
+    if (T == 0) return MHC_OK;
+    const void* ptrs[] = {q, k, q_out, k_out};
+    if ((st = check_ptrs(ptrs, 4)) != MHC_OK) return st;
+    if (rot == 0) return MHC_ERR_INVALID_ARG;   // nothing to turn
+    if ((st = check_rope(Dh, rot, flags, 0.0f, max_pos, positions, cos_sin)) != MHC_OK) return st;
+    if ((st = check_stride(dt, q_stride, Hq, Dh)) != MHC_OK) return st;
+    if ((st = check_stride(dt, k_stride, Hk, Dh)) != MHC_OK) return st;
+    if ((st = check_stride(dt, q_out_stride, Hq, Dh)) != MHC_OK) return st;
+    if ((st = check_stride(dt, k_out_stride, Hk, Dh)) != MHC_OK) return st;
+    mhc::QkParams p = {};
+    p.q = q;
+    p.k = k;
+    p.positions = positions;
+    p.cos_sin = cos_sin;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.q_out_stride = q_out_stride;
+    p.k_out_stride = k_out_stride;
+    p.T = T;
+    p.page_size = 1;
+    p.Hq = Hq;
+    p.Hk = Hk;
+    p.Dh = Dh;
+    p.rot = rot;
+    p.max_pos = static_cast<int>(max_pos);
+    p.sine_sign = back ? -1.0f : 1.0f;
+    p.q_out = q_out;
+    p.k_out = k_out;
+    return from_cuda(mhc::launch_rope(dt == MHC_BF16, (flags & MHC_ROPE_ADJACENT) != 0, false, p, stream));
+}
+
+mhc_status mhc_rope(mhc_dtype dt, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                    const int32_t* positions, const float* cos_sin, int64_t max_pos, int64_t T, int Hq, int Hk, int Dh,
+                    int rot, int flags, void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                    cudaStream_t stream) {
+    return rope_call(dt, q, q_stride, k, k_stride, positions, cos_sin, max_pos, T, Hq, Hk, Dh, rot, flags, false, q_out,
+                     q_out_stride, k_out, k_out_stride, stream);
+}
+
+mhc_status mhc_rope_bwd(mhc_dtype dt, const void* g_q, int64_t gq_stride, const void* g_k, int64_t gk_stride,
+                        const int32_t* positions, const float* cos_sin, int64_t max_pos, int64_t T, int Hq, int Hk,
+                        int Dh, int rot, int flags, void* dq, int64_t dq_stride, void* dk, int64_t dk_stride,
+                        cudaStream_t stream) {
+    return rope_call(dt, g_q, gq_stride, g_k, gk_stride, positions, cos_sin, max_pos, T, Hq, Hk, Dh, rot, flags, true, dq,
+                     dq_stride, dk, dk_stride, stream);
+}
+
+mhc_status mhc_rope_append(mhc_dtype dt, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                           const void* v, int64_t v_stride, const int32_t* positions, const float* cos_sin,
+                           int64_t max_pos, const int64_t* slots, int64_t T, int Hq, int Hk, int Dh, int rot, int flags,
+                           void* q_out, int64_t q_out_stride, void* k_cache, int64_t k_page_stride,
+                           int64_t k_slot_stride, int64_t k_head_stride, void* v_cache, int64_t v_page_stride,
+                           int64_t v_slot_stride, int64_t v_head_stride, int64_t num_pages, int page_size,
+                           cudaStream_t stream) {
+    mhc_status st = check_heads(dt, T, Hq, Hk, Dh);
+    if (st != MHC_OK) return st;
+    if (T == 0) return MHC_OK;
+    const void* ptrs[] = {q, k, v, q_out, k_cache, v_cache};
+    if ((st = check_ptrs(ptrs, 6)) != MHC_OK) return st;
+    if ((st = check_plain(slots, 8)) != MHC_OK) return st;
+    if (rot == 0) return MHC_ERR_INVALID_ARG;
+    if ((st = check_rope(Dh, rot, flags, 0.0f, max_pos, positions, cos_sin)) != MHC_OK) return st;
+    if ((st = check_stride(dt, q_stride, Hq, Dh)) != MHC_OK) return st;
+    if ((st = check_stride(dt, k_stride, Hk, Dh)) != MHC_OK) return st;
+    if ((st = check_stride(dt, v_stride, Hk, Dh)) != MHC_OK) return st;
+    if ((st = check_stride(dt, q_out_stride, Hq, Dh)) != MHC_OK) return st;
+    if ((st = check_cache(dt, num_pages, page_size, Hk, Dh, k_page_stride, k_slot_stride, k_head_stride)) != MHC_OK)
+        return st;
+    if ((st = check_cache(dt, num_pages, page_size, Hk, Dh, v_page_stride, v_slot_stride, v_head_stride)) != MHC_OK)
+        return st;
+    mhc::QkParams p = {};
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.positions = positions;
+    p.cos_sin = cos_sin;
+    p.slots = slots;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.q_out_stride = q_out_stride;
+    p.k_page_stride = k_page_stride;
+    p.k_slot_stride = k_slot_stride;
+    p.k_head_stride = k_head_stride;
+    p.v_page_stride = v_page_stride;
+    p.v_slot_stride = v_slot_stride;
+    p.v_head_stride = v_head_stride;
+    p.num_slots = num_pages * page_size;
+    p.T = T;
+    p.page_size = page_size;
+    p.Hq = Hq;
+    p.Hk = Hk;
+    p.Dh = Dh;
+    p.rot = rot;
+    p.max_pos = static_cast<int>(max_pos);
+    p.sine_sign = 1.0f;
+    p.q_out = q_out;
+    p.k_out = k_cache;
+    p.v_out = v_cache;
+    return from_cuda(mhc::launch_rope(dt == MHC_BF16, (flags & MHC_ROPE_ADJACENT) != 0, true, p, stream));
+}
+
+mhc_status mhc_rope_table(int64_t n, int rot, double base, double factor, double original, double low, double high,
+                          float amplitude, float* cos_sin, cudaStream_t stream) {
+    if (n < 0 || rot <= 0 || !(base >= 1.0) || !isfinite(base) || !(factor > 0.0) || !isfinite(factor) ||
+        !isfinite(1.0 / factor) || !(original >= 0.0) || !isfinite(original) || !isfinite(low) || !isfinite(high) ||
+        !(low < high) || !isfinite(amplitude))
+        return MHC_ERR_INVALID_ARG;
+    if (rot % 16 != 0 || rot > 256 || n > MAX_T) return MHC_ERR_UNSUPPORTED;
+    if (n == 0) return MHC_OK;
+    const void* ptrs[] = {cos_sin};
+    mhc_status st = check_ptrs(ptrs, 1);
+    if (st != MHC_OK) return st;
+    return from_cuda(mhc::launch_rope_table(n, rot, base, factor, original, low, high, amplitude, cos_sin, stream));
+}
+
 size_t mhc_paged_attn_workspace_bytes(mhc_dtype dt, int64_t T, int B, int Hq, int Hk, int Dh, int page_size,
                                       int64_t max_q) {
     if (check_attn(dt, T, B, Hq, Hk, Dh, page_size, max_q, 0, 0) != MHC_OK || T == 0 || B == 0) return 0;

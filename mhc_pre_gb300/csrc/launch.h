@@ -132,6 +132,7 @@ struct QkParams {
     int64_t num_slots, T;
     int page_size, Hq, Hk, Dh, rot, max_pos;
     float eps;
+    float sine_sign;            // the rotation alone: -1 turns back
     void *q_out, *k_out, *v_out;
 };
 struct QkBwdParams {
@@ -149,6 +150,11 @@ int64_t qk_bwd_blocks(int64_t T);
 cudaError_t launch_qk_norm_rope(bool bf16, bool adjacent, bool append, const QkParams& p, cudaStream_t s);
 cudaError_t launch_qk_norm_rope_bwd(bool bf16, bool adjacent, const QkBwdParams& p, float* dw_q, float* dw_k,
                                     cudaStream_t s);
+
+// The rotation without the normalisation (weights and eps are not used), and its table.
+cudaError_t launch_rope(bool bf16, bool adjacent, bool append, const QkParams& p, cudaStream_t s);
+cudaError_t launch_rope_table(int64_t n, int rot, double base, double factor, double original, double low, double high,
+                              float amplitude, float* cos_sin, cudaStream_t s);
 
 struct AttnPlan;
 struct AttnParams;
@@ -182,6 +188,7 @@ class ErrorWord {
 // Device error words of these kernels, read and cleared.
 cudaError_t read_and_clear_qk_error(unsigned* word);
 cudaError_t read_and_clear_qk_bwd_error(unsigned* word);
+cudaError_t read_and_clear_rope_error(unsigned* word);
 cudaError_t read_and_clear_attn_error(unsigned* word);
 cudaError_t read_and_clear_attn_tc_error(unsigned* word);
 

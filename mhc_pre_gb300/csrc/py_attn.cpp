@@ -15,7 +15,9 @@
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <initializer_list>
 #include <math.h>
 #include <stdint.h>
 #include <string.h>
@@ -38,6 +40,9 @@ struct Library {
     decltype(&mhc_qk_norm_rope_append) qk_norm_rope_append;
     decltype(&mhc_paged_attn) paged_attn;
     decltype(&mhc_paged_attn_workspace_bytes) paged_attn_workspace_bytes;
+    decltype(&mhc_rope) rope;
+    decltype(&mhc_rope_bwd) rope_bwd;
+    decltype(&mhc_rope_append) rope_append;
 };
 Library lib = {};
 constexpr int ENTRIES = sizeof(Library) / sizeof(void*);
@@ -242,6 +247,24 @@ bool same_shape(PyObject* t, const int64_t (&want)[3], const char* message) {
     return false;
 }
 
+// Tensors of one call (or None), all on one device; the call is made with it as
+// the current one.
+bool one_device(std::initializer_list<PyObject*> tensors, c10::cuda::OptionalCUDAGuard* guard) {
+    int device = -1;
+    for (PyObject* o : tensors) {
+        const at::Tensor* t;
+        if (o == Py_None) continue;
+        if (!tensor_of(o, "an argument", &t) || !check_cuda(*t)) return false;
+        if (device >= 0 && t->get_device() != device) {
+            PyErr_SetString(PyExc_ValueError, "the tensors of a call must be on one device");
+            return false;
+        }
+        device = t->get_device();
+    }
+    if (device >= 0) guard->set_index(static_cast<c10::DeviceIndex>(device));
+    return true;
+}
+
 cudaStream_t stream_of(PyObject* o) { return c10::cuda::getCurrentCUDAStream(THPVariable_Unpack(o).get_device()).stream(); }
 
 // A new tensor on the device of `like`, and its address.  `empty`: a callable
@@ -428,6 +451,84 @@ PyObject* qk_norm_rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// (empty, q, k, positions, cos_sin, flags, back, q_out | None, k_out | None) -> (status, q_out, k_out)
+PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!arguments(n, 9)) return nullptr;
+    int64_t sq[3], sk[3];
+    ScalarType dt;
+    mhc_dtype code;
+    Heads q, k, qo, ko;
+    Rope r;
+    int flags, back;
+    c10::cuda::OptionalCUDAGuard guard;
+    if (!same_tokens(a[1], a[2], sq, sk) || !activations(a[1], &dt, &code) || !heads_of(a[1], "q", dt, sq, &q) ||
+        !heads_of(a[2], "k", dt, sk, &k) || !rope_of(a[3], a[4], sq[0], &r) || !to_int(a[5], &flags) ||
+        !to_int(a[6], &back) || !one_device({a[1], a[2], a[3], a[4], a[7], a[8]}, &guard))
+        return nullptr;
+    Ref tq, tk;
+    if (a[7] == Py_None) {
+        tq.reset(make(a[0], dt, a[1], 3, sq, &qo.p));
+        if (!tq) return nullptr;
+        qo.stride = sq[1] * sq[2];
+    } else {
+        if (!same_shape(a[7], sq, "outputs must have the shapes of q and k") || !heads_of(a[7], "the output", dt, sq, &qo))
+            return nullptr;
+        tq.reset(Py_NewRef(a[7]));
+    }
+    if (a[8] == Py_None) {
+        tk.reset(make(a[0], dt, a[1], 3, sk, &ko.p));
+        if (!tk) return nullptr;
+        ko.stride = sk[1] * sk[2];
+    } else {
+        if (!same_shape(a[8], sk, "outputs must have the shapes of q and k") || !heads_of(a[8], "the output", dt, sk, &ko))
+            return nullptr;
+        tk.reset(Py_NewRef(a[8]));
+    }
+    const int st = (back ? lib.rope_bwd : lib.rope)(
+        code, q.p, q.stride, k.p, k.stride, static_cast<int32_t*>(r.positions), static_cast<float*>(r.cos_sin), r.max_pos,
+        sq[0], clip(sq[1]), clip(sk[1]), clip(sq[2]), r.rot, flags, qo.p, qo.stride, ko.p, ko.stride, stream_of(a[1]));
+    return Py_BuildValue("iOO", st, tq.get(), tk.get());
+    END_HANDLE_TH_ERRORS
+}
+
+// (empty, q, k, v, k_cache, v_cache, slots, positions, cos_sin, flags) -> (status, q_out)
+PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!arguments(n, 10)) return nullptr;
+    int64_t sq[3], sk[3], sc[4];
+    ScalarType dt;
+    mhc_dtype code;
+    void *slots, *qo;
+    Heads q, k, v;
+    Cache kc, vc;
+    Rope r;
+    int flags;
+    c10::cuda::OptionalCUDAGuard guard;
+    if (!same_tokens(a[1], a[2], sq, sk) || !activations(a[1], &dt, &code) ||
+        !same_shape(a[3], sk, "k and v must have the same shape") || !shape_of(a[4], 4, sc, "k_cache"))
+        return nullptr;
+    if (sc[2] != sk[1] || sc[3] != sk[2]) {
+        PyErr_Format(PyExc_ValueError, "k_cache must be [pages, page_size, %lld, %lld]", static_cast<long long>(sk[1]),
+                     static_cast<long long>(sk[2]));
+        return nullptr;
+    }
+    if (!heads_of(a[1], "q", dt, sq, &q) || !heads_of(a[2], "k", dt, sk, &k) || !heads_of(a[3], "v", dt, sk, &v) ||
+        !cache_of(a[4], "k_cache", dt, sc, &kc) || !cache_of(a[5], "v_cache", dt, sc, &vc) ||
+        !flat_of(a[6], "slots", ScalarType::Long, sq[0], &slots) || !rope_of(a[7], a[8], sq[0], &r) ||
+        !to_int(a[9], &flags) || !one_device({a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8]}, &guard))
+        return nullptr;
+    Ref to(make(a[0], dt, a[1], 3, sq, &qo));
+    if (!to) return nullptr;
+    const int st = lib.rope_append(
+        code, q.p, q.stride, k.p, k.stride, v.p, v.stride, static_cast<int32_t*>(r.positions),
+        static_cast<float*>(r.cos_sin), r.max_pos, static_cast<int64_t*>(slots), sq[0], clip(sq[1]), clip(sk[1]),
+        clip(sq[2]), r.rot, flags, qo, sq[1] * sq[2], kc.p, kc.page, kc.slot, kc.head, vc.p, vc.page, vc.slot, vc.head,
+        sc[0], clip(sc[1]), stream_of(a[1]));
+    return Py_BuildValue("iO", st, to.get());
+    END_HANDLE_TH_ERRORS
+}
+
 // (empty, q, k_cache, v_cache, page_table, cu_q, kv_lens, max_q, max_kv, scale, window, softcap, workspace, out)
 //   -> (status, o, lse); None: the lengths where there is a planned workspace, bounds and scale from the shapes, a
 //   new workspace, a new output
@@ -511,6 +612,7 @@ PyObject* paged_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(bind), FAST(qk_norm_rope), FAST(qk_norm_rope_bwd), FAST(qk_norm_rope_append), FAST(paged_attn),
+                         FAST(rope), FAST(rope_append),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_attn_calls", "Marshalling of the attention sublayer's calls.", -1,
                       methods, nullptr, nullptr, nullptr, nullptr};

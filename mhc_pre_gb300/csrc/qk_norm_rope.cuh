@@ -206,6 +206,18 @@ __device__ __forceinline__ Coef make_coef(const Pairs& w, const Angles& g) {
     return k;
 }
 
+// The rotation alone; `sign` -1 turns back.
+__device__ __forceinline__ Coef make_coef(const Angles& g, float sign) {
+    Coef k;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        k.ac[i] = k.bc[i] = g.c[i];
+        k.as[i] = make_float2(sign * g.s[i].x, sign * g.s[i].y);
+        k.bs[i] = make_float2(-k.as[i].x, -k.as[i].y);
+    }
+    return k;
+}
+
 template <int LPH>
 __device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
@@ -227,6 +239,16 @@ __device__ __forceinline__ Pairs turn(const Pairs& x, const Coef& k, float r) {
     for (int i = 0; i < 2; ++i) {
         y.a[i] = __fmul2_rn(rr, __ffma2_rn(x.a[i], k.ac[i], __fmul2_rn(x.b[i], k.bs[i])));
         y.b[i] = __fmul2_rn(rr, __ffma2_rn(x.b[i], k.bc[i], __fmul2_rn(x.a[i], k.as[i])));
+    }
+    return y;
+}
+
+__device__ __forceinline__ Pairs turn(const Pairs& x, const Coef& k) {
+    Pairs y;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        y.a[i] = __ffma2_rn(x.a[i], k.ac[i], __fmul2_rn(x.b[i], k.bs[i]));
+        y.b[i] = __ffma2_rn(x.b[i], k.bc[i], __fmul2_rn(x.a[i], k.as[i]));
     }
     return y;
 }

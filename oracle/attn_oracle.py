@@ -24,6 +24,18 @@ def rotation(cos_sin, positions, rot, dh, adjacent):
     return R
 
 
+def rope_table(n, rot, base=10000.0, factor=1.0, original=0.0, low=1.0, high=32.0, amplitude=1.0, first=0):
+    """[n, rot]: cosines, then sines, of the positions first .. first + n - 1
+    with scaled frequencies, and the angles [n, rot/2]."""
+    f = np.empty(rot // 2)
+    for j in range(rot // 2):
+        e = float(base) ** (-2.0 * j / rot)
+        g = min(1.0, max(0.0, (original * e / (2.0 * np.pi) - low) / (high - low)))
+        f[j] = e * (g + (1.0 - g) / factor)
+    a = (first + np.arange(n))[:, None] * f
+    return amplitude * np.concatenate([np.cos(a), np.sin(a)], 1), a
+
+
 def norm_rope(x, w, R, eps):
     """x [T, H, dh] -> R (x w / sqrt(mean(x^2) + eps))."""
     x = np.asarray(x, np.float64)
