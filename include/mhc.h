@@ -602,6 +602,43 @@ mhc_status mhc_paged_attn(mhc_dtype dt, const void* q, int64_t q_stride, const v
 size_t mhc_paged_attn_workspace_bytes(mhc_dtype dt, int64_t T, int B, int Hq, int Hk, int Dh, int page_size,
                                       int64_t max_q);
 
+/*
+ * mhc_tree_attn -- attention of trees of drafted tokens over a paged cache that
+ * holds their keys and values already: the verification of speculative decoding.
+ * As mhc_paged_attn, but the n new tokens of a sequence (the rows cu_q[b] ..
+ * cu_q[b+1] of q, and the last n of its m cached tokens) are the nodes of a tree
+ * in any order.  Row t of `tree` says which of the sequence's new tokens node t
+ * sees: bit i % 32 of word i / 32 for the i-th one (itself and its ancestors,
+ * usually; any mask is taken).  Node t sees the m - n cached tokens before the
+ * new ones (its context) and those.  With a window, it sees its nodes and the
+ * last window - max(1, how many these are) tokens of the context.
+ * A row that sees no key gets o = 0 and lse = -inf; so does every row of a
+ * sequence with m < n, whose drafted tokens are not all cached.
+ *
+ *   tree [T, *]          int32            tree_stride words between rows, at
+ *                                         least ceil(max_q / 32); bits past a
+ *                                         sequence's new tokens are ignored
+ *   max_q                                 at most 1024
+ * The rest, the workspace (mhc_paged_attn_workspace_bytes) and the errors are as
+ * for mhc_paged_attn.  What the pages hold for a drafted token that no row of a
+ * tile sees (padding, say) is never used; with a window the last window - 1
+ * tokens of the context count as seen.
+ *
+ * mhc_tree_attn_plan -- as mhc_paged_attn_plan, for mhc_tree_attn only.  It does
+ * not depend on `tree`.
+ */
+mhc_status mhc_tree_attn_plan(mhc_dtype dt, const int32_t* cu_q, const int32_t* kv_lens, int64_t T, int B,
+                              int Hq, int Hk, int Dh, int page_size, int64_t max_q, int64_t max_kv,
+                              int window, void* workspace, size_t ws_bytes, cudaStream_t stream);
+mhc_status mhc_tree_attn(mhc_dtype dt, const void* q, int64_t q_stride, const void* k_cache,
+                         int64_t k_page_stride, int64_t k_slot_stride, int64_t k_head_stride,
+                         const void* v_cache, int64_t v_page_stride, int64_t v_slot_stride,
+                         int64_t v_head_stride, int64_t num_pages, int page_size, const int32_t* page_table,
+                         int64_t table_stride, const int32_t* tree, int64_t tree_stride, const int32_t* cu_q,
+                         const int32_t* kv_lens, int64_t T, int B, int Hq, int Hk, int Dh, int64_t max_q,
+                         int64_t max_kv, int window, float scale, float softcap, void* o, float* lse,
+                         void* workspace, size_t ws_bytes, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -27,7 +27,8 @@ SOURCES = ["mhc_abi.cu", "kernels_fwd.cu", "kernels_bwd.cu", "pre_tc.cu", "pre_b
            "pre_bwd_noalloc.cu", "post_pre_tc.cu",
            "post_norm.cu", "pre_small.cu",
            "qk_norm_rope.cu", "qk_norm_rope_bwd.cu", "qk_norm_rope_bare.cu", "paged_attn.cu",
-           "paged_attn_tc.cu", "attn_abi.cu"]
+           "paged_attn_tc.cu", "paged_attn_tree.cu", "paged_attn_tree_tc.cu",
+           "attn_abi.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
          "--expt-relaxed-constexpr", "-Xptxas", "-warn-spills"]

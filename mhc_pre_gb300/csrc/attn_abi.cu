@@ -373,11 +373,20 @@ size_t mhc_paged_attn_workspace_bytes(mhc_dtype dt, int64_t T, int B, int Hq, in
     return counters_fit(plan, Hk) ? plan.total : 0;
 }
 
-mhc_status mhc_paged_attn_plan(mhc_dtype dt, const int32_t* cu_q, const int32_t* kv_lens, int64_t T, int B, int Hq,
-                               int Hk, int Dh, int page_size, int64_t max_q, int64_t max_kv, int window,
-                               void* workspace, size_t ws_bytes, cudaStream_t stream) {
+// What trees of drafted tokens ask for beside the causal call's checks.
+static mhc_status check_tree(int64_t max_q, const int32_t* tree, int64_t tree_stride) {
+    if (max_q > mhc::TREE_MOST) return MHC_ERR_UNSUPPORTED;
+    if (tree_stride < (max_q + 31) / 32) return MHC_ERR_INVALID_ARG;
+    if (tree_stride > MAX_STRIDE) return MHC_ERR_UNSUPPORTED;
+    return check_plain(tree, 4);
+}
+
+static mhc_status plan_call(mhc_dtype dt, const int32_t* cu_q, const int32_t* kv_lens, int64_t T, int B, int Hq, int Hk,
+                            int Dh, int page_size, int64_t max_q, int64_t max_kv, int window, bool tree,
+                            void* workspace, size_t ws_bytes, cudaStream_t stream) {
     mhc_status st = check_attn(dt, T, B, Hq, Hk, Dh, page_size, max_q, max_kv, window);
     if (st != MHC_OK) return st;
+    if (tree && max_q > mhc::TREE_MOST) return MHC_ERR_UNSUPPORTED;
     if (T == 0 || B == 0) return MHC_OK;
     const void* ptrs[] = {workspace};
     if ((st = check_ptrs(ptrs, 1)) != MHC_OK) return st;
@@ -385,16 +394,31 @@ mhc_status mhc_paged_attn_plan(mhc_dtype dt, const int32_t* cu_q, const int32_t*
     const mhc::AttnPlan plan = mhc::attn_plan_sizes(dt == MHC_BF16, T, B, Hq, Hk, Dh, page_size, max_q);
     if (!counters_fit(plan, Hk)) return MHC_ERR_UNSUPPORTED;
     if (ws_bytes < plan.total) return MHC_ERR_INVALID_ARG;
-    return from_cuda(mhc::launch_attn_plan(plan, cu_q, kv_lens, T, B, Hq, Hk, window, max_q, max_kv, workspace, stream));
+    return from_cuda(mhc::launch_attn_plan(plan, cu_q, kv_lens, T, B, Hq, Hk, window, max_q, max_kv, tree, workspace,
+                                           stream));
 }
 
-mhc_status mhc_paged_attn(mhc_dtype dt, const void* q, int64_t q_stride, const void* k_cache, int64_t k_page_stride,
-                          int64_t k_slot_stride, int64_t k_head_stride, const void* v_cache, int64_t v_page_stride,
-                          int64_t v_slot_stride, int64_t v_head_stride, int64_t num_pages, int page_size,
-                          const int32_t* page_table, int64_t table_stride, const int32_t* cu_q,
-                          const int32_t* kv_lens, int64_t T, int B, int Hq, int Hk, int Dh, int64_t max_q,
-                          int64_t max_kv, int window, float scale, float softcap, void* o, float* lse,
-                          void* workspace, size_t ws_bytes, cudaStream_t stream) {
+mhc_status mhc_paged_attn_plan(mhc_dtype dt, const int32_t* cu_q, const int32_t* kv_lens, int64_t T, int B, int Hq,
+                               int Hk, int Dh, int page_size, int64_t max_q, int64_t max_kv, int window,
+                               void* workspace, size_t ws_bytes, cudaStream_t stream) {
+    return plan_call(dt, cu_q, kv_lens, T, B, Hq, Hk, Dh, page_size, max_q, max_kv, window, false, workspace, ws_bytes,
+                     stream);
+}
+
+mhc_status mhc_tree_attn_plan(mhc_dtype dt, const int32_t* cu_q, const int32_t* kv_lens, int64_t T, int B, int Hq,
+                              int Hk, int Dh, int page_size, int64_t max_q, int64_t max_kv, int window,
+                              void* workspace, size_t ws_bytes, cudaStream_t stream) {
+    return plan_call(dt, cu_q, kv_lens, T, B, Hq, Hk, Dh, page_size, max_q, max_kv, window, true, workspace, ws_bytes,
+                     stream);
+}
+
+static mhc_status attn_call(mhc_dtype dt, const void* q, int64_t q_stride, const void* k_cache, int64_t k_page_stride,
+                            int64_t k_slot_stride, int64_t k_head_stride, const void* v_cache, int64_t v_page_stride,
+                            int64_t v_slot_stride, int64_t v_head_stride, int64_t num_pages, int page_size,
+                            const int32_t* page_table, int64_t table_stride, bool trees, const int32_t* tree,
+                            int64_t tree_stride, const int32_t* cu_q, const int32_t* kv_lens, int64_t T, int B, int Hq,
+                            int Hk, int Dh, int64_t max_q, int64_t max_kv, int window, float scale, float softcap,
+                            void* o, float* lse, void* workspace, size_t ws_bytes, cudaStream_t stream) {
     mhc_status st = check_attn(dt, T, B, Hq, Hk, Dh, page_size, max_q, max_kv, window);
     if (st != MHC_OK) return st;
     if (!(scale > 0.0f) || !isfinite(scale) || !(softcap >= 0.0f) || !isfinite(softcap)) return MHC_ERR_INVALID_ARG;
@@ -410,12 +434,13 @@ mhc_status mhc_paged_attn(mhc_dtype dt, const void* q, int64_t q_stride, const v
     if ((st = check_cache(dt, num_pages, page_size, Hk, Dh, v_page_stride, v_slot_stride, v_head_stride)) != MHC_OK)
         return st;
     if (table_stride < (max_kv + page_size - 1) / page_size) return MHC_ERR_INVALID_ARG;
+    if (trees && (st = check_tree(max_q, tree, tree_stride)) != MHC_OK) return st;
     const mhc::AttnPlan plan = mhc::attn_plan_sizes(dt == MHC_BF16, T, B, Hq, Hk, Dh, page_size, max_q);
     if (!counters_fit(plan, Hk)) return MHC_ERR_UNSUPPORTED;
     if (ws_bytes < plan.total) return MHC_ERR_INVALID_ARG;
     if (cu_q != nullptr) {
-        st = mhc_paged_attn_plan(dt, cu_q, kv_lens, T, B, Hq, Hk, Dh, page_size, max_q, max_kv, window, workspace,
-                                 ws_bytes, stream);
+        st = plan_call(dt, cu_q, kv_lens, T, B, Hq, Hk, Dh, page_size, max_q, max_kv, window, trees, workspace, ws_bytes,
+                       stream);
         if (st != MHC_OK) return st;
     }
     mhc::AttnParams p = {};
@@ -425,6 +450,8 @@ mhc_status mhc_paged_attn(mhc_dtype dt, const void* q, int64_t q_stride, const v
     p.o = o;
     p.lse = lse;
     p.page_table = page_table;
+    p.tree = reinterpret_cast<const uint32_t*>(tree);
+    p.tree_stride = tree_stride;
     p.ws = static_cast<unsigned char*>(workspace);
     p.q_stride = q_stride;
     p.table_stride = table_stride;
@@ -458,7 +485,33 @@ mhc_status mhc_paged_attn(mhc_dtype dt, const void* q, int64_t q_stride, const v
     p.softcap = softcap;
     p.force_timeout = mhc::forced_timeout();
     p.plan = plan;
-    return from_cuda(mhc::launch_paged_attn(dt == MHC_BF16, p, stream));
+    return from_cuda(trees ? mhc::launch_tree_attn(dt == MHC_BF16, p, stream)
+                           : mhc::launch_paged_attn(dt == MHC_BF16, p, stream));
+}
+
+mhc_status mhc_paged_attn(mhc_dtype dt, const void* q, int64_t q_stride, const void* k_cache, int64_t k_page_stride,
+                          int64_t k_slot_stride, int64_t k_head_stride, const void* v_cache, int64_t v_page_stride,
+                          int64_t v_slot_stride, int64_t v_head_stride, int64_t num_pages, int page_size,
+                          const int32_t* page_table, int64_t table_stride, const int32_t* cu_q,
+                          const int32_t* kv_lens, int64_t T, int B, int Hq, int Hk, int Dh, int64_t max_q,
+                          int64_t max_kv, int window, float scale, float softcap, void* o, float* lse,
+                          void* workspace, size_t ws_bytes, cudaStream_t stream) {
+    return attn_call(dt, q, q_stride, k_cache, k_page_stride, k_slot_stride, k_head_stride, v_cache, v_page_stride,
+                     v_slot_stride, v_head_stride, num_pages, page_size, page_table, table_stride, false, nullptr, 0, cu_q,
+                     kv_lens, T, B, Hq, Hk, Dh, max_q, max_kv, window, scale, softcap, o, lse, workspace, ws_bytes, stream);
+}
+
+mhc_status mhc_tree_attn(mhc_dtype dt, const void* q, int64_t q_stride, const void* k_cache, int64_t k_page_stride,
+                         int64_t k_slot_stride, int64_t k_head_stride, const void* v_cache, int64_t v_page_stride,
+                         int64_t v_slot_stride, int64_t v_head_stride, int64_t num_pages, int page_size,
+                         const int32_t* page_table, int64_t table_stride, const int32_t* tree, int64_t tree_stride,
+                         const int32_t* cu_q, const int32_t* kv_lens, int64_t T, int B, int Hq, int Hk, int Dh,
+                         int64_t max_q, int64_t max_kv, int window, float scale, float softcap, void* o, float* lse,
+                         void* workspace, size_t ws_bytes, cudaStream_t stream) {
+    return attn_call(dt, q, q_stride, k_cache, k_page_stride, k_slot_stride, k_head_stride, v_cache, v_page_stride,
+                     v_slot_stride, v_head_stride, num_pages, page_size, page_table, table_stride, true, tree, tree_stride,
+                     cu_q, kv_lens, T, B, Hq, Hk, Dh, max_q, max_kv, window, scale, softcap, o, lse, workspace, ws_bytes,
+                     stream);
 }
 
 }  // extern "C"

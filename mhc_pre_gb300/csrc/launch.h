@@ -160,12 +160,15 @@ struct AttnPlan;
 struct AttnParams;
 AttnPlan attn_plan_sizes(bool bf16, int64_t T, int B, int Hq, int Hk, int Dh, int page_size, int64_t max_q);
 cudaError_t launch_attn_plan(const AttnPlan& plan, const int32_t* cu_q, const int32_t* kv_lens, int64_t T, int B,
-                             int Hq, int Hk, int window, int64_t max_q, int64_t max_kv, void* ws, cudaStream_t s);
+                             int Hq, int Hk, int window, int64_t max_q, int64_t max_kv, bool tree, void* ws,
+                             cudaStream_t s);
 cudaError_t launch_paged_attn(bool bf16, const AttnParams& p, cudaStream_t s);
+cudaError_t launch_tree_attn(bool bf16, const AttnParams& p, cudaStream_t s);   // p.tree: trees of drafted tokens
 
 // On the tensor cores (paged_attn_tc.cu), where the types and sizes allow it.
 bool attn_tc_supports(bool bf16, int Hq, int Hk, int Dh, int page_size);
 cudaError_t launch_paged_attn_tc(const AttnParams& p, cudaStream_t s);
+cudaError_t launch_tree_attn_tc(const AttnParams& p, cudaStream_t s);
 
 // The host's side of a device error word.  Reading one is a blocking copy, so
 // words of kernels that no call has launched (or captured) are not asked for,
@@ -191,6 +194,8 @@ cudaError_t read_and_clear_qk_bwd_error(unsigned* word);
 cudaError_t read_and_clear_rope_error(unsigned* word);
 cudaError_t read_and_clear_attn_error(unsigned* word);
 cudaError_t read_and_clear_attn_tc_error(unsigned* word);
+cudaError_t read_and_clear_attn_tree_error(unsigned* word);
+cudaError_t read_and_clear_attn_tree_tc_error(unsigned* word);
 
 // The test hook of the bounded waits (pre_tc.cu), for kernels that take it as
 // a launch parameter.

@@ -30,6 +30,9 @@ namespace mhc {
 
 constexpr unsigned ATTN_ERR_TIMEOUT = 1u, ATTN_ERR_RANGE = 2u;
 
+// Most new tokens of a sequence that is a tree.
+constexpr int TREE_MOST = 1024;
+
 // Join counters of a tile and key head: each warp's rows are joined by
 // themselves.
 constexpr int JOINS = 8;
@@ -54,6 +57,7 @@ struct AttnHead {       // start of the plan
     int ntiles;
     int ncta;
     int Hq, Hk, B, tile_rows, block_keys, window, lead;
+    int tree;           // of trees of drafted tokens: its tiles see other keys
     int spent;          // a wait ran out in a call with this plan: parts of its tiles never
                         // came, and their join counters stand where the next call would
                         // take them for its own
@@ -76,8 +80,9 @@ struct AttnParams {
     void* o;
     float* lse;                    // may be null
     const int32_t* page_table;     // [B, table_stride]
+    const uint32_t* tree;          // [T, tree_stride]: bit i of a row, the sequence's i-th new token is seen
     unsigned char* ws;
-    int64_t q_stride, table_stride, num_pages;
+    int64_t q_stride, table_stride, num_pages, tree_stride;
     int64_t k_page_stride, k_slot_stride, k_head_stride;
     int64_t v_page_stride, v_slot_stride, v_head_stride;
     int64_t T, max_q, max_kv;
@@ -113,12 +118,13 @@ __device__ __forceinline__ int* attn_counts(const AttnParams& p) {
 // Whether the plan in the workspace is the one that this call's sizes ask for (a
 // larger max_q would overrun the parts, a larger max_kv the page table) and its
 // counters are at zero.
+template <bool TREE>
 __device__ __forceinline__ bool attn_plan_agrees(const AttnParams& p) {
     const AttnHead* h = attn_head(p);
     return h->T == p.T && h->max_q == p.max_q && h->max_kv == p.max_kv && h->Hq == p.Hq && h->Hk == p.Hk &&
            h->B == p.B && h->tile_rows == p.plan.tile_rows && h->block_keys == p.plan.block_keys &&
            h->window == p.window && h->ncta == p.plan.ncta && h->lead == p.plan.lead && h->ntiles >= 0 &&
-           h->ntiles <= p.plan.max_tiles && h->per_cta > 0 && h->spent == 0;
+           h->ntiles <= p.plan.max_tiles && h->per_cta > 0 && h->spent == 0 && h->tree == (TREE ? 1 : 0);
 }
 __device__ __forceinline__ void attn_plan_spent(const AttnParams& p) { reinterpret_cast<AttnHead*>(p.ws)->spent = 1; }
 
@@ -135,6 +141,61 @@ __device__ __forceinline__ void attn_token_keys(const T& t, int i, int window, i
     hi = min(t.kvlen, end);
     lo = window > 0 ? max(0, end - window) : 0;
 }
+
+// A tree's new tokens see the cached ones before them (with a window the last
+// ones of these) and, of each other, those whose bits they have.  Keys [lo, hi)
+// of which any of the sequence's tokens may see some: a path has at least one
+// token, which a window counts.
+template <typename T>
+__device__ __forceinline__ void attn_tree_keys(const T& t, int window, int& lo, int& hi) {
+    const int ctx = t.kvlen - t.qlen;   // a sequence of fewer cached than new tokens sees nothing
+    hi = ctx >= 0 ? t.kvlen : 0;
+    lo = window > 0 && ctx >= window ? ctx - window + 1 : 0;
+}
+// Keys that some row of a tile, from `first` to `last`, may see.
+template <bool TREE, typename T>
+__device__ __forceinline__ void attn_tile_keys(const T& t, int first, int last, int window, int& lo, int& hi) {
+    if (TREE) {
+        attn_tree_keys(t, window, lo, hi);
+    } else {
+        int unused;
+        attn_token_keys(t, first, window, lo, unused);
+        attn_token_keys(t, last, window, unused, hi);
+    }
+}
+
+// What one token of a tree sees: keys [lo, ctx), and of those from ctx on the
+// ones whose bits it has.  `words` are the bits of the sequence's new tokens;
+// those past them count for nothing.
+struct AttnNode {
+    const uint32_t* words;
+    int lo, ctx, nodes;
+    __device__ __forceinline__ uint32_t word(int i) const {
+        const int left = nodes - 32 * i;   // of the sequence's tokens from this word on
+        if (i < 0 || left <= 0) return 0u;
+        const uint32_t w = __ldg(words + i);
+        return left < 32 ? w & ((1u << left) - 1u) : w;
+    }
+    template <typename T>
+    __device__ __forceinline__ void init(const AttnParams& p, const T& t, int token) {
+        words = p.tree + (t.q0 + token) * p.tree_stride;
+        ctx = t.kvlen - t.qlen;
+        nodes = ctx >= 0 ? t.qlen : 0;
+        lo = 0;
+        if (p.window > 0 && t.kvlen > p.window && ctx >= 0) {
+            int path = 0;
+            for (int i = 0; 32 * i < nodes; ++i) path += __popc(word(i));
+            lo = max(0, min(ctx, ctx - p.window + max(path, 1)));
+        }
+    }
+    // Which of the 32 keys from g that lie at ctx or later it sees (bits of keys before ctx are 0).
+    __device__ __forceinline__ uint32_t drafted(int g) const {
+        const int from = g - ctx;
+        if (from <= -32) return 0u;
+        if (from < 0) return word(0) << -from;
+        return __funnelshift_r(word(from >> 5), word((from >> 5) + 1), from & 31);
+    }
+};
 
 // A CTA's pieces one after the other.
 struct AttnPiece {
@@ -163,6 +224,7 @@ struct AttnWalk {
         return at < end;
     }
     // The next piece that has blocks; false when the CTA's share is done.
+    template <bool TREE>
     __device__ __forceinline__ bool next(const AttnParams& p, int cta, AttnPiece& out) {
         while (at < end) {
             const int lead = p.plan.lead, cost = t.nblk + lead;
@@ -178,9 +240,8 @@ struct AttnWalk {
             out.blk = t.blk0 + b0;
             out.nb = b1 - b0;
             out.whole = b0 == 0 && b1 == t.nblk;
-            int unused;
-            attn_token_keys(t, attn_token(p, t.row0), p.window, out.lo, unused);
-            attn_token_keys(t, attn_token(p, min(t.row0 + p.plan.tile_rows, t.qlen * p.G) - 1), p.window, unused, out.hi);
+            attn_tile_keys<TREE>(t, attn_token(p, t.row0), attn_token(p, min(t.row0 + p.plan.tile_rows, t.qlen * p.G) - 1),
+                                 p.window, out.lo, out.hi);
             out.cnt = (t.cnt + head) * JOINS;
             out.slot = 2 * cta + (b0 > 0 ? 0 : 1);
             if (!out.whole) {

@@ -43,6 +43,7 @@ struct Library {
     decltype(&mhc_rope) rope;
     decltype(&mhc_rope_bwd) rope_bwd;
     decltype(&mhc_rope_append) rope_append;
+    decltype(&mhc_tree_attn) tree_attn;
 };
 Library lib = {};
 constexpr int ENTRIES = sizeof(Library) / sizeof(void*);
@@ -532,9 +533,8 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // (empty, q, k_cache, v_cache, page_table, cu_q, kv_lens, max_q, max_kv, scale, window, softcap, workspace, out)
 //   -> (status, o, lse); None: the lengths where there is a planned workspace, bounds and scale from the shapes, a
 //   new workspace, a new output
-PyObject* paged_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    HANDLE_TH_ERRORS
-    if (!arguments(n, 14)) return nullptr;
+// `tree`: the drafted tokens' mask [T, words], or null for causal rows
+PyObject* attn(PyObject* const* a, PyObject* mask) {
     int64_t sq[3], sc[4], stab[2], max_q, max_kv;
     const at::Tensor* t;
     ScalarType dt;
@@ -553,8 +553,33 @@ PyObject* paged_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
         return nullptr;
     }
     const int64_t T = sq[0], B = stab[0], width = stab[1], page = sc[1];
+    int64_t stree[2] = {0, 0}, tree_stride = 0;
+    int32_t* tree = nullptr;
+    c10::cuda::OptionalCUDAGuard guard;
+    if (mask != nullptr) {
+        const at::Tensor* m;
+        if (!shape_of(mask, 2, stree, "tree") || !tensor_of(mask, "tree", &m) ||
+            !check_dtype(mask, *m, ScalarType::Int, "tree") ||
+            !one_device({a[1], a[2], a[3], a[4], a[5], a[6], a[12], a[13], mask}, &guard))
+            return nullptr;
+        if (stree[0] != T) {
+            PyErr_Format(PyExc_ValueError, "tree must have a row for each of the %lld tokens", static_cast<long long>(T));
+            return nullptr;
+        }
+        if (m->stride(1) != 1 && stree[1] > 1) {
+            PyErr_SetString(PyExc_ValueError, "tree: the words of a row must lie one after the other");
+            return nullptr;
+        }
+        tree = static_cast<int32_t*>(m->data_ptr());
+        tree_stride = T > 1 ? m->stride(0) : stree[1];
+    }
     if (a[7] == Py_None) max_q = T;
     else if (!to_i64(a[7], &max_q)) return nullptr;
+    if (mask != nullptr && 32 * stree[1] < max_q) {
+        PyErr_Format(PyExc_ValueError, "tree has bits for %lld tokens a sequence, max_q is %lld",
+                     static_cast<long long>(32 * stree[1]), static_cast<long long>(max_q));
+        return nullptr;
+    }
     if (a[8] == Py_None) max_kv = width * page;
     else if (!to_i64(a[8], &max_kv)) return nullptr;
     if (a[9] == Py_None) scale = 1.0f / sqrtf(static_cast<float>(sq[2]));
@@ -601,18 +626,36 @@ PyObject* paged_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     Ref tl(make(a[0], ScalarType::Float, a[1], 2, sq, &lse));
     if (!tl) return nullptr;
-    const int st = lib.paged_attn(code, q.p, q.stride, kc.p, kc.page, kc.slot, kc.head, vc.p, vc.page, vc.slot, vc.head,
-                                  sc[0], clip(page), static_cast<int32_t*>(table), B > 1 ? t->stride(0) : width,
-                                  static_cast<int32_t*>(cu), static_cast<int32_t*>(kv), T, clip(B), clip(sq[1]),
-                                  clip(sc[2]), clip(sq[2]), max_q, max_kv, window, scale, softcap, o,
-                                  static_cast<float*>(lse), ws, static_cast<size_t>(ws_bytes), stream_of(a[1]));
+    const int64_t table_stride = B > 1 ? t->stride(0) : width;
+    const int32_t *tab = static_cast<int32_t*>(table), *cuq = static_cast<int32_t*>(cu), *kvl = static_cast<int32_t*>(kv);
+    const cudaStream_t stream = stream_of(a[1]);
+    const int st =
+        mask != nullptr
+            ? lib.tree_attn(code, q.p, q.stride, kc.p, kc.page, kc.slot, kc.head, vc.p, vc.page, vc.slot, vc.head, sc[0],
+                            clip(page), tab, table_stride, tree, tree_stride, cuq, kvl, T, clip(B), clip(sq[1]),
+                            clip(sc[2]), clip(sq[2]), max_q, max_kv, window, scale, softcap, o, static_cast<float*>(lse),
+                            ws, static_cast<size_t>(ws_bytes), stream)
+            : lib.paged_attn(code, q.p, q.stride, kc.p, kc.page, kc.slot, kc.head, vc.p, vc.page, vc.slot, vc.head, sc[0],
+                             clip(page), tab, table_stride, cuq, kvl, T, clip(B), clip(sq[1]), clip(sc[2]), clip(sq[2]),
+                             max_q, max_kv, window, scale, softcap, o, static_cast<float*>(lse), ws,
+                             static_cast<size_t>(ws_bytes), stream);
     return Py_BuildValue("iOO", st, to.get(), tl.get());
+}
+PyObject* paged_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    return arguments(n, 14) ? attn(a, nullptr) : nullptr;
+    END_HANDLE_TH_ERRORS
+}
+// The same, and the mask as the last argument.
+PyObject* tree_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    return arguments(n, 15) ? attn(a, a[14]) : nullptr;
     END_HANDLE_TH_ERRORS
 }
 
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(bind), FAST(qk_norm_rope), FAST(qk_norm_rope_bwd), FAST(qk_norm_rope_append), FAST(paged_attn),
-                         FAST(rope), FAST(rope_append),
+                         FAST(rope), FAST(rope_append), FAST(tree_attn),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_attn_calls", "Marshalling of the attention sublayer's calls.", -1,
                       methods, nullptr, nullptr, nullptr, nullptr};

@@ -82,3 +82,39 @@ def attention(q, k, v, scale, window=0, softcap=0.0):
             pabs[i, h] = p @ np.abs(vv)
             size[i, h] = (np.abs(kk) @ np.abs(q[i, h])).max() * scale
     return o, lse, pabs, size
+
+
+def tree_attention(q, k, v, scale, mask, window=0, softcap=0.0):
+    """Attention of n drafted tokens q [n, Hq, dh], the last n of the m cached
+    tokens k, v [m, Hk, dh]: row i sees the context (with a window the last
+    window - max(1, nodes it sees) of it) and the drafted tokens j with mask[i, j].
+    Returns what attention() does."""
+    q, k, v = (np.asarray(a, np.float64) for a in (q, k, v))
+    n, hq, dh = q.shape
+    m, hk, _ = k.shape
+    o, pabs = np.zeros((n, hq, dh)), np.zeros((n, hq, dh))
+    lse, size = np.full((n, hq), -np.inf), np.zeros((n, hq))
+    for i in range(n):
+        if m < n:
+            continue
+        nodes = [m - n + j for j in range(n) if mask[i][j]]
+        context = list(range(m - n))
+        if window:
+            left = max(0, window - max(1, len(nodes)))
+            context = context[len(context) - min(left, len(context)):]
+        keys = context + nodes
+        if not keys:
+            continue
+        for h in range(hq):
+            kk, vv = k[keys, h // (hq // hk)], v[keys, h // (hq // hk)]
+            z = kk @ q[i, h] * scale
+            if softcap > 0:
+                z = softcap * np.tanh(z / softcap)
+            top = z.max()
+            e = np.exp(z - top)
+            lse[i, h] = top + np.log(e.sum())
+            p = e / e.sum()
+            o[i, h] = p @ vv
+            pabs[i, h] = p @ np.abs(vv)
+            size[i, h] = (np.abs(kk) @ np.abs(q[i, h])).max() * scale
+    return o, lse, pabs, size
