@@ -639,6 +639,86 @@ mhc_status mhc_tree_attn(mhc_dtype dt, const void* q, int64_t q_stride, const vo
                          int64_t max_kv, int window, float scale, float softcap, void* o, float* lse,
                          void* workspace, size_t ws_bytes, cudaStream_t stream);
 
+/*
+ * mhc_paged_step -- the integer tensors of a step's new tokens, made on the GPU
+ * from the lengths of its sequences (no host copy, so a captured step serves any
+ * lengths): row starts, slots, positions, pages of the free list for those that
+ * run out of room, and what each node of a drafted tree sees.
+ *
+ * Sequence b has lens[b] cached tokens and gets new_lens[b] new ones (0: none
+ * this step), or ends (-1).  It holds held[b] pages, the first entries of its row
+ * of page_table, which cover its cached tokens; tokens that were drafted and
+ * dropped may have left it with more.  In order:
+ *   1. the pages of sequences that end go back on the free list, sequence after
+ *      sequence, each row's last page on top;
+ *   2. each sequence needs max(0, ceil((lens + new) / page_size) - held) pages; in
+ *      the order of the sequences they come from the top of the list, the page
+ *      on top first.  A sequence gets all of them or none: from the first one
+ *      for which too few are left on, only sequences that need none get room;
+ *   3. new token i of sequence b is row cu_q[b] + i, and its place in the sequence
+ *      lens[b] + i; slots holds page * page_size + place in the page, -1 where the
+ *      sequence got no room.
+ * kv_lens[b] is lens[b] + new_lens[b], lens[b] for a sequence without room (what
+ * attention gives its rows means nothing; it can be given its tokens again once
+ * others have ended), 0 for one that ends.
+ * Positions are the places in the sequence, or with trees lens[b] + the number of
+ * the node's ancestors.  Parent parents[t] of row t is a number among its
+ * sequence's new tokens, below its own, or -1 (it follows the context); row t of
+ * `tree` gets the bits of the node and its ancestors, as mhc_tree_attn takes them.
+ *
+ *   new_lens, lens [B]   int32
+ *   page_table [B, *]    int32   in/out   table_width entries a row, table_stride apart
+ *   held [B]             int32   in/out
+ *   free_pages           int32   in/out   a stack of free_capacity entries, free_count
+ *   free_count [1]       int32   in/out   of them in use, the last one on top
+ *   T                                     rows of the outputs; those past the new
+ *                                         tokens get slot -1, position 0, no bits
+ *   parents [T]          int32            or null: no trees
+ *   tree_words                            words of a row of `tree`, 1 to 32
+ * outputs: cu_q [B+1], kv_lens [B], positions [T] int32, slots [T] int64,
+ *   tree [T, tree_words] int32 (null without parents).  No output may be an input.
+ * MHC_ERR_RANGE: sequences whose rows would pass T (they and all later ones get
+ * none: cu_q stays), whose numbers do not fit (lengths below 0, or past held pages
+ * or the table; they get slots -1, positions 0 and kv_lens 0), parents that are not
+ * below their node (as -1), nodes past tree_words * 32 (without a bit), a list's
+ * length outside its tensor, more pages coming back than it has room for (those
+ * are lost).  At most 8192 sequences, 2^30 entries of the table.
+ */
+mhc_status mhc_paged_step(const int32_t* new_lens, const int32_t* lens, int B, int32_t* page_table,
+                          int64_t table_stride, int64_t table_width, int32_t* held, int32_t* free_pages,
+                          int64_t free_capacity, int32_t* free_count, int page_size, int64_t T,
+                          const int32_t* parents, int tree_words, int32_t* cu_q, int32_t* kv_lens,
+                          int32_t* positions, int64_t* slots, int32_t* tree, cudaStream_t stream);
+
+/*
+ * mhc_cache_keep -- after a drafted tree has been verified: the keys and values
+ * of the accepted path move to the places behind the context, in the caches of
+ * `layers` layers.  Sequence b has n = cu_q[b+1] - cu_q[b] drafted tokens, the
+ * last of its m = kv_lens[b] cached ones, and keeps keep[b] of them: nodes
+ * path[b, 0] < path[b, 1] < ... of 0 .. n - 1 go to the places m - n, m - n + 1,
+ * ...; then lens[b] = m - n + keep[b].  keep[b] = 0 moves nothing and leaves
+ * lens[b] as it is.  Places behind the kept tokens hold what is left there.
+ *
+ *   k_caches, v_caches   host arrays of `layers` device pointers, each a cache as
+ *                        in mhc_qk_norm_rope_append, all keys (and all values)
+ *                        with the same strides; no two overlap
+ *   page_table [B, *]    int32            table_stride between rows, at least
+ *                                         ceil(max_kv / page_size)
+ *   cu_q [B+1], kv_lens [B], keep [B] int32
+ *   path [B, *]          int32            path_stride between rows, >= max_keep
+ *   lens [B]             int32   out      or null
+ * MHC_ERR_RANGE: a sequence whose numbers do not fit (a path that does not rise
+ * or leaves the drafted tokens, keep past max_keep or n, m outside n .. max_kv) is
+ * left as it is; a row on a page outside the cache is not moved.
+ */
+mhc_status mhc_cache_keep(mhc_dtype dt, void* const* k_caches, int64_t k_page_stride, int64_t k_slot_stride,
+                          int64_t k_head_stride, void* const* v_caches, int64_t v_page_stride,
+                          int64_t v_slot_stride, int64_t v_head_stride, int layers, int64_t num_pages,
+                          int page_size, const int32_t* page_table, int64_t table_stride, const int32_t* cu_q,
+                          const int32_t* kv_lens, int64_t max_kv, int B, int Hk, int Dh, const int32_t* path,
+                          int64_t path_stride, int max_keep, const int32_t* keep, int32_t* lens,
+                          cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

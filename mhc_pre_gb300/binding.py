@@ -37,7 +37,7 @@ EXPORTS = ("mhc_status_string", "mhc_version", "mhc_get_last_device_error",
            "mhc_qk_norm_rope_append", "mhc_paged_attn_plan", "mhc_paged_attn",
            "mhc_paged_attn_workspace_bytes",
            "mhc_rope_table", "mhc_rope", "mhc_rope_bwd", "mhc_rope_append",
-           "mhc_tree_attn_plan", "mhc_tree_attn")
+           "mhc_tree_attn_plan", "mhc_tree_attn", "mhc_paged_step", "mhc_cache_keep")
 
 PreOut = namedtuple("PreOut", "x_in H_pre H_post H_res proj inv_rms")
 PostPreOut = namedtuple("PostPreOut", "x_next x_in H_pre H_post H_res proj inv_rms")
@@ -53,6 +53,7 @@ QKOut = namedtuple("QKOut", "q k")
 QKBwdOut = namedtuple("QKBwdOut", "dq dk dw_q dw_k")
 PagedAttnOut = namedtuple("PagedAttnOut", "o lse")
 PagedAttnPlan = namedtuple("PagedAttnPlan", "workspace sizes")
+PagedStep = namedtuple("PagedStep", "cu_q kv_lens positions slots tree")
 TreeAttnPlan = namedtuple("TreeAttnPlan", "workspace sizes")
 ROPE_ADJACENT = 1
 
@@ -106,6 +107,9 @@ _SIGS = {
     "mhc_tree_attn": ([_I, _P, _I64, _P, _I64, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I,
                        _P, _I64, _P, _I64, _P, _P, _I64, _I, _I, _I, _I, _I64, _I64, _I, _F, _F, _P, _P,
                        _P, ctypes.c_size_t, _P], _I),
+    "mhc_paged_step": ([_P, _P, _I, _P, _I64, _I64, _P, _P, _I64, _P, _I, _I64, _P, _I, _P, _P, _P, _P, _P, _P], _I),
+    "mhc_cache_keep": ([_I, _P, _I64, _I64, _I64, _P, _I64, _I64, _I64, _I, _I64, _I, _P, _I64, _P, _P, _I64, _I, _I,
+                        _I, _P, _I64, _I, _P, _P, _P], _I),
     "mhc_rope_table": ([_I64, _I, _D, _D, _D, _D, _D, _F, _P, _P], _I),
     "mhc_rope": ([_I, _P, _I64, _P, _I64, _P, _P, _I64, _I64, _I, _I, _I, _I, _I, _P, _I64, _P, _I64, _P], _I),
     "mhc_rope_bwd": ([_I, _P, _I64, _P, _I64, _P, _P, _I64, _I64, _I, _I, _I, _I, _I, _P, _I64, _P, _I64, _P], _I),
@@ -433,7 +437,8 @@ CALLS_PATH = os.path.join(os.path.dirname(LIB_PATH), "_attn_calls.so")
 # the entry points that it calls, in its order
 CALLS_ENTRIES = ("mhc_qk_norm_rope", "mhc_qk_norm_rope_bwd", "mhc_qk_norm_rope_bwd_workspace_bytes",
                  "mhc_qk_norm_rope_append", "mhc_paged_attn", "mhc_paged_attn_workspace_bytes",
-                 "mhc_rope", "mhc_rope_bwd", "mhc_rope_append", "mhc_tree_attn")
+                 "mhc_rope", "mhc_rope_bwd", "mhc_rope_append", "mhc_tree_attn",
+                 "mhc_paged_step", "mhc_cache_keep")
 _calls_module = None
 
 
@@ -636,6 +641,37 @@ def mhc_tree_attn(q, k_cache, v_cache, page_table, tree, cu_q=None, kv_lens=None
     if st:
         _check(st, "mhc_tree_attn")
     return PagedAttnOut(o, lse)
+
+
+def mhc_paged_step(new_lens, lens, page_table, held, free_pages, free_count, page_size: int, T: int, parents=None,
+                   width: int = None):
+    """The integer tensors of a step, made on the GPU from lengths: ``new_lens`` [B]
+    new tokens (-1: the sequence ends, its pages go back) after ``lens`` [B] cached
+    ones.  ``page_table`` [B, *], ``held`` [B] (pages of each sequence),
+    ``free_pages`` (a stack) and ``free_count`` [1] are brought up to date in
+    place.  A sequence for which too few pages are free gets slots -1 and
+    kv_lens = lens.  ``T``: rows of the outputs.  ``parents`` [T]: the drafted
+    trees (-1 or a number below the token's own); ``width``: words of a row of
+    ``tree`` (default: for T tokens, at most 1024).  All int32 but slots.  Returns
+    cu_q, kv_lens, positions, slots and tree (None without parents)."""
+    if width is None:
+        width = min(32, max(1, -(-T // 32)))
+    st, *out = (_calls_module or _calls()).paged_step(_allocator(), new_lens, lens, page_table, held, free_pages,
+                                                      free_count, page_size, T, parents, width)
+    if st:
+        _check(st, "mhc_paged_step")
+    return PagedStep(*out)
+
+
+def mhc_cache_keep(k_caches, v_caches, page_table, cu_q, kv_lens, path, keep, lens=None, max_kv: int = None):
+    """After a step of drafted trees: in every cache (a tensor [pages, page_size,
+    Hk, Dh], or a sequence of one for each layer) the accepted path path[b, :keep[b]]
+    of each sequence's new tokens, rising numbers, moves behind its context, in
+    place.  ``lens`` [B], when given, becomes the context and the kept tokens (as
+    it was where keep[b] is 0)."""
+    st = (_calls_module or _calls()).cache_keep(k_caches, v_caches, page_table, cu_q, kv_lens, path, keep, lens, max_kv)
+    if st:
+        _check(st, "mhc_cache_keep")
 
 
 def get_last_device_error(device=None) -> int:

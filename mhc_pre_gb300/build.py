@@ -28,6 +28,7 @@ SOURCES = ["mhc_abi.cu", "kernels_fwd.cu", "kernels_bwd.cu", "pre_tc.cu", "pre_b
            "post_norm.cu", "pre_small.cu",
            "qk_norm_rope.cu", "qk_norm_rope_bwd.cu", "qk_norm_rope_bare.cu", "paged_attn.cu",
            "paged_attn_tc.cu", "paged_attn_tree.cu", "paged_attn_tree_tc.cu",
+           "paged_attn_step.cu", "paged_attn_keep.cu",
            "attn_abi.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",

@@ -29,6 +29,11 @@ mhc_status check_plain(const void* p, unsigned bytes) {
     return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0 ? MHC_OK : MHC_ERR_MISALIGNED;
 }
 
+// Numbers that may be null where there are none.
+mhc_status check_counted(const void* p, unsigned bytes, int64_t entries) {
+    return entries == 0 && p == nullptr ? MHC_OK : check_plain(p, bytes);
+}
+
 mhc_status check_ptrs(const void* const* ptrs, int n) {
     for (int i = 0; i < n; ++i) {
         if (ptrs[i] == nullptr) return MHC_ERR_INVALID_ARG;
@@ -78,6 +83,13 @@ mhc_status check_attn(mhc_dtype dt, int64_t T, int B, int Hq, int Hk, int Dh, in
     // tile's key range plus one block must not pass them
     if (B > (1 << 24) || max_q > MAX_T / Hq || max_kv > MAX_KV || T > MAX_T / Hq) return MHC_ERR_UNSUPPORTED;
     return MHC_OK;
+}
+
+// The page size as a shift, -1 where it is none.
+int shift_of(int page_size) {
+    for (int i = 0; i < 21; ++i)
+        if (page_size == (1 << i)) return i;
+    return -1;
 }
 
 // A tile's join counters are numbered in 32 bits.
@@ -471,9 +483,7 @@ static mhc_status attn_call(mhc_dtype dt, const void* q, int64_t q_stride, const
     p.G = Hq / Hk;
     p.Dh = Dh;
     p.page_size = page_size;
-    p.page_shift = -1;
-    for (int i = 0; i < 21; ++i)
-        if (page_size == (1 << i)) p.page_shift = i;
+    p.page_shift = shift_of(page_size);
     p.window = window;
     if (p.G > 1) {   // M = floor(2^(31+s) / G) + 1, 2^s >= G: exact below 2^31
         unsigned sh = 1;
@@ -512,6 +522,114 @@ mhc_status mhc_tree_attn(mhc_dtype dt, const void* q, int64_t q_stride, const vo
                      v_slot_stride, v_head_stride, num_pages, page_size, page_table, table_stride, true, tree, tree_stride,
                      cu_q, kv_lens, T, B, Hq, Hk, Dh, max_q, max_kv, window, scale, softcap, o, lse, workspace, ws_bytes,
                      stream);
+}
+
+mhc_status mhc_paged_step(const int32_t* new_lens, const int32_t* lens, int B, int32_t* page_table,
+                          int64_t table_stride, int64_t table_width, int32_t* held, int32_t* free_pages,
+                          int64_t free_capacity, int32_t* free_count, int page_size, int64_t T,
+                          const int32_t* parents, int tree_words, int32_t* cu_q, int32_t* kv_lens,
+                          int32_t* positions, int64_t* slots, int32_t* tree, cudaStream_t stream) {
+    if (B < 0 || T < 0 || table_width < 0 || free_capacity < 0 || page_size <= 0) return MHC_ERR_INVALID_ARG;
+    const int64_t most = int64_t(1) << 30;
+    if (B > mhc::STEP_SEQUENCES || T > MAX_T || free_capacity > most || page_size > (1 << 20) || table_width > most ||
+        B * table_width > most || table_stride > MAX_STRIDE)
+        return MHC_ERR_UNSUPPORTED;
+    if (B > 1 && table_stride < table_width) return MHC_ERR_INVALID_ARG;
+    mhc_status st;
+    if ((st = check_counted(new_lens, 4, B)) != MHC_OK || (st = check_counted(lens, 4, B)) != MHC_OK ||
+        (st = check_counted(held, 4, B)) != MHC_OK || (st = check_counted(kv_lens, 4, B)) != MHC_OK ||
+        (st = check_counted(page_table, 4, B * table_width)) != MHC_OK ||
+        (st = check_counted(free_pages, 4, free_capacity)) != MHC_OK || (st = check_plain(free_count, 4)) != MHC_OK ||
+        (st = check_plain(cu_q, 4)) != MHC_OK || (st = check_counted(positions, 4, T)) != MHC_OK ||
+        (st = check_counted(slots, 8, T)) != MHC_OK)
+        return st;
+    if (T > 0 && (parents == nullptr) != (tree == nullptr)) return MHC_ERR_INVALID_ARG;
+    if (T > 0 && parents != nullptr) {
+        if (tree_words <= 0) return MHC_ERR_INVALID_ARG;
+        if (tree_words > mhc::TREE_MOST / 32) return MHC_ERR_UNSUPPORTED;
+        if ((st = check_plain(parents, 4)) != MHC_OK || (st = check_plain(tree, 4)) != MHC_OK) return st;
+    }
+    mhc::StepParams p = {};
+    p.new_lens = new_lens;
+    p.lens = lens;
+    p.parents = parents;
+    p.table = page_table;
+    p.held = held;
+    p.free_pages = free_pages;
+    p.free_count = free_count;
+    p.cu_q = cu_q;
+    p.kv_lens = kv_lens;
+    p.positions = positions;
+    p.tree = T > 0 ? tree : nullptr;
+    p.slots = slots;
+    p.table_stride = table_stride;
+    p.width = table_width;
+    p.T = T;
+    p.max_len = MAX_KV;
+    p.B = B;
+    p.page = page_size;
+    p.page_shift = shift_of(page_size);
+    p.cap = static_cast<int>(free_capacity);
+    p.words = tree_words;
+    return from_cuda(mhc::launch_paged_step(p, stream));
+}
+
+mhc_status mhc_cache_keep(mhc_dtype dt, void* const* k_caches, int64_t k_page_stride, int64_t k_slot_stride,
+                          int64_t k_head_stride, void* const* v_caches, int64_t v_page_stride, int64_t v_slot_stride,
+                          int64_t v_head_stride, int layers, int64_t num_pages, int page_size,
+                          const int32_t* page_table, int64_t table_stride, const int32_t* cu_q,
+                          const int32_t* kv_lens, int64_t max_kv, int B, int Hk, int Dh, const int32_t* path,
+                          int64_t path_stride, int max_keep, const int32_t* keep, int32_t* lens, cudaStream_t stream) {
+    mhc_status st = check_heads(dt, 0, Hk, Hk, Dh);
+    if (st != MHC_OK) return st;
+    if (B < 0 || layers < 0 || max_keep < 0 || max_kv < 0) return MHC_ERR_INVALID_ARG;
+    if (B > (1 << 24) || max_kv > MAX_KV || path_stride > MAX_STRIDE || table_stride > MAX_STRIDE)
+        return MHC_ERR_UNSUPPORTED;
+    if (B == 0 || layers == 0 || max_keep == 0) return MHC_OK;
+    if (k_caches == nullptr || v_caches == nullptr || path_stride < max_keep) return MHC_ERR_INVALID_ARG;
+    if ((st = check_ptrs(k_caches, layers)) != MHC_OK || (st = check_ptrs(v_caches, layers)) != MHC_OK) return st;
+    if ((st = check_cache(dt, num_pages, page_size, Hk, Dh, k_page_stride, k_slot_stride, k_head_stride)) != MHC_OK)
+        return st;
+    if ((st = check_cache(dt, num_pages, page_size, Hk, Dh, v_page_stride, v_slot_stride, v_head_stride)) != MHC_OK)
+        return st;
+    if (table_stride < (max_kv + page_size - 1) / page_size) return MHC_ERR_INVALID_ARG;
+    const void* numbers[] = {page_table, cu_q, kv_lens, path, keep};
+    for (const void* n : numbers)
+        if ((st = check_plain(n, 4)) != MHC_OK) return st;
+    if (lens != nullptr && (st = check_plain(lens, 4)) != MHC_OK) return st;
+    const int64_t e = dt == MHC_BF16 ? 2 : 4;
+    mhc::KeepParams p = {};
+    p.table = page_table;
+    p.cu_q = cu_q;
+    p.kv_lens = kv_lens;
+    p.path = path;
+    p.keep = keep;
+    p.k_page = k_page_stride * e;
+    p.k_slot = k_slot_stride * e;
+    p.k_head = k_head_stride * e;
+    p.v_page = v_page_stride * e;
+    p.v_slot = v_slot_stride * e;
+    p.v_head = v_head_stride * e;
+    p.table_stride = table_stride;
+    p.path_stride = path_stride;
+    p.num_pages = num_pages;
+    p.max_kv = max_kv;
+    p.page = page_size;
+    p.page_shift = shift_of(page_size);
+    p.max_keep = max_keep;
+    p.head_pieces = static_cast<int>(Dh * e / 16);
+    p.row_pieces = Hk * p.head_pieces;
+    for (int l0 = 0; l0 < layers; l0 += mhc::KEEP_LAYERS) {
+        p.layers = layers - l0 < mhc::KEEP_LAYERS ? layers - l0 : mhc::KEEP_LAYERS;
+        for (int i = 0; i < p.layers; ++i) {
+            p.k[i] = k_caches[l0 + i];
+            p.v[i] = v_caches[l0 + i];
+        }
+        p.lens = l0 == 0 ? lens : nullptr;
+        const cudaError_t err = mhc::launch_cache_keep(p, B, stream);
+        if (err != cudaSuccess) return from_cuda(err);
+    }
+    return MHC_OK;
 }
 
 }  // extern "C"

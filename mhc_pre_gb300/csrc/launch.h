@@ -170,6 +170,29 @@ bool attn_tc_supports(bool bf16, int Hq, int Hk, int Dh, int page_size);
 cudaError_t launch_paged_attn_tc(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_tree_attn_tc(const AttnParams& p, cudaStream_t s);
 
+// The tables of a step's new tokens (paged_attn_step.cu).
+constexpr int STEP_SEQUENCES = 8192;   // at most: three numbers of each are in shared memory
+struct StepParams {
+    const int32_t *new_lens, *lens, *parents;   // parents may be null (no trees)
+    int32_t *table, *held, *free_pages, *free_count;
+    int32_t *cu_q, *kv_lens, *positions, *tree;
+    int64_t* slots;
+    int64_t table_stride, width, T, max_len;    // max_len: of a sequence
+    int B, page, page_shift, cap, words;
+};
+cudaError_t launch_paged_step(const StepParams& p, cudaStream_t s);
+
+// The accepted path's keys and values (paged_attn_keep.cu); strides in bytes.
+constexpr int KEEP_LAYERS = 64;        // of a launch
+struct KeepParams {
+    void *k[KEEP_LAYERS], *v[KEEP_LAYERS];
+    const int32_t *table, *cu_q, *kv_lens, *path, *keep;
+    int32_t* lens;                     // may be null
+    int64_t k_page, k_slot, k_head, v_page, v_slot, v_head, table_stride, path_stride, num_pages, max_kv;
+    int layers, page, page_shift, max_keep, row_pieces, head_pieces;   // 16-byte pieces
+};
+cudaError_t launch_cache_keep(const KeepParams& p, int B, cudaStream_t s);
+
 // The host's side of a device error word.  Reading one is a blocking copy, so
 // words of kernels that no call has launched (or captured) are not asked for,
 // and a word is cleared only if it says something.
@@ -196,6 +219,8 @@ cudaError_t read_and_clear_attn_error(unsigned* word);
 cudaError_t read_and_clear_attn_tc_error(unsigned* word);
 cudaError_t read_and_clear_attn_tree_error(unsigned* word);
 cudaError_t read_and_clear_attn_tree_tc_error(unsigned* word);
+cudaError_t read_and_clear_step_error(unsigned* word);
+cudaError_t read_and_clear_keep_error(unsigned* word);
 
 // The test hook of the bounded waits (pre_tc.cu), for kernels that take it as
 // a launch parameter.

@@ -24,6 +24,8 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <vector>
+
 #include "../../include/mhc.h"
 
 namespace {
@@ -44,6 +46,8 @@ struct Library {
     decltype(&mhc_rope_bwd) rope_bwd;
     decltype(&mhc_rope_append) rope_append;
     decltype(&mhc_tree_attn) tree_attn;
+    decltype(&mhc_paged_step) paged_step;
+    decltype(&mhc_cache_keep) cache_keep;
 };
 Library lib = {};
 constexpr int ENTRIES = sizeof(Library) / sizeof(void*);
@@ -653,9 +657,153 @@ PyObject* tree_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// A page table [B, width], its rows apart.
+struct Table {
+    int32_t* p;
+    int64_t rows, width, stride;
+};
+bool table_of(PyObject* o, const char* name, Table* out) {
+    int64_t s[2];
+    const at::Tensor* t;
+    if (!shape_of(o, 2, s, name) || !tensor_of(o, name, &t) || !check_dtype(o, *t, ScalarType::Int, name) || !check_cuda(*t))
+        return false;
+    if (t->stride(1) != 1 && s[1] > 1) {
+        PyErr_Format(PyExc_ValueError, "%s: the numbers of a row must lie one after the other", name);
+        return false;
+    }
+    *out = {static_cast<int32_t*>(t->data_ptr()), s[0], s[1], s[0] > 1 ? t->stride(0) : s[1]};
+    return true;
+}
+
+// (empty, new_lens, lens, page_table, held, free_pages, free_count, page_size, T, parents | None, words)
+//   -> (status, cu_q, kv_lens, positions, slots, tree | None)
+PyObject* paged_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!arguments(n, 11)) return nullptr;
+    Table table;
+    const at::Tensor* list;
+    void *fresh, *lens, *held, *pages, *count, *parents = nullptr, *cu, *kv, *pos, *slots, *tree = nullptr;
+    int64_t T;
+    int page, words;
+    c10::cuda::OptionalCUDAGuard guard;
+    if (!table_of(a[3], "page_table", &table) || !flat_of(a[1], "new_lens", ScalarType::Int, table.rows, &fresh) ||
+        !flat_of(a[2], "lens", ScalarType::Int, table.rows, &lens) ||
+        !flat_of(a[4], "held", ScalarType::Int, table.rows, &held) || !tensor_of(a[5], "free_pages", &list) ||
+        !flat_of(a[5], "free_pages", ScalarType::Int, list->numel(), &pages) ||
+        !flat_of(a[6], "free_count", ScalarType::Int, 1, &count) || !to_int(a[7], &page) || !to_i64(a[8], &T) ||
+        !to_int(a[10], &words))
+        return nullptr;
+    if (T < 0 || words < 0) {
+        PyErr_SetString(PyExc_ValueError, "T and the words of a mask are numbers of rows and columns");
+        return nullptr;
+    }
+    if (a[9] != Py_None && !flat_of(a[9], "parents", ScalarType::Int, T, &parents)) return nullptr;
+    if (!one_device({a[1], a[2], a[3], a[4], a[5], a[6], a[9]}, &guard)) return nullptr;
+    const int64_t ends = table.rows + 1, shape[2] = {T, words};
+    Ref tcu(make(a[0], ScalarType::Int, a[1], 1, &ends, &cu));
+    if (!tcu) return nullptr;
+    Ref tkv(make(a[0], ScalarType::Int, a[1], 1, &table.rows, &kv));
+    if (!tkv) return nullptr;
+    Ref tpos(make(a[0], ScalarType::Int, a[1], 1, &T, &pos));
+    if (!tpos) return nullptr;
+    Ref tslots(make(a[0], ScalarType::Long, a[1], 1, &T, &slots));
+    if (!tslots) return nullptr;
+    Ref ttree(a[9] == Py_None ? Py_NewRef(Py_None) : make(a[0], ScalarType::Int, a[1], 2, shape, &tree));
+    if (!ttree) return nullptr;
+    const int st = lib.paged_step(
+        static_cast<int32_t*>(fresh), static_cast<int32_t*>(lens), clip(table.rows), table.p, table.stride, table.width,
+        static_cast<int32_t*>(held), static_cast<int32_t*>(pages), list->numel(), static_cast<int32_t*>(count), page, T,
+        static_cast<int32_t*>(parents), words, static_cast<int32_t*>(cu), static_cast<int32_t*>(kv),
+        static_cast<int32_t*>(pos), static_cast<int64_t*>(slots), static_cast<int32_t*>(tree), stream_of(a[1]));
+    return Py_BuildValue("iOOOOO", st, tcu.get(), tkv.get(), tpos.get(), tslots.get(), ttree.get());
+    END_HANDLE_TH_ERRORS
+}
+
+// The caches of all layers: a tensor or a sequence of them, alike in shape and strides.
+bool caches_of(PyObject* o, const char* name, ScalarType dtype, const int64_t (&shape)[4], int device,
+               std::vector<void*>* at, Cache* like) {
+    Ref list;
+    PyObject* one[1] = {o};
+    PyObject** items = one;
+    Py_ssize_t n = 1;
+    if (!THPVariable_Check(o)) {
+        list.reset(PySequence_Fast(o, "caches must be a tensor or a sequence of tensors"));
+        if (!list) return false;
+        n = PySequence_Fast_GET_SIZE(list.get());
+        items = PySequence_Fast_ITEMS(list.get());
+    }
+    at->reserve(static_cast<size_t>(n));
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        Cache c;
+        if (!cache_of(items[i], name, dtype, shape, &c)) return false;
+        if (i == 0) *like = c;
+        if (c.page != like->page || c.slot != like->slot || c.head != like->head) {
+            PyErr_Format(PyExc_ValueError, "%s: the layers' caches must have the same strides", name);
+            return false;
+        }
+        if (THPVariable_Unpack(items[i]).get_device() != device) {
+            PyErr_SetString(PyExc_ValueError, "the tensors of a call must be on one device");
+            return false;
+        }
+        at->push_back(c.p);
+    }
+    return true;
+}
+
+// (k_caches, v_caches, page_table, cu_q, kv_lens, path, keep, lens | None, max_kv | None) -> status
+PyObject* cache_keep(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!arguments(n, 9)) return nullptr;
+    Table table, path;
+    void *cu, *kv, *keep, *lens = nullptr;
+    Ref first(THPVariable_Check(a[0]) ? Py_NewRef(a[0]) : PySequence_GetItem(a[0], 0));
+    if (!first) return nullptr;
+    int64_t shape[4], max_kv;
+    ScalarType dt;
+    mhc_dtype code;
+    c10::cuda::OptionalCUDAGuard guard;
+    if (!shape_of(first.get(), 4, shape, "a cache") || !activations(first.get(), &dt, &code) ||
+        !table_of(a[2], "page_table", &table) || !flat_of(a[3], "cu_q", ScalarType::Int, table.rows + 1, &cu) ||
+        !flat_of(a[4], "kv_lens", ScalarType::Int, table.rows, &kv) || !table_of(a[5], "path", &path) ||
+        !flat_of(a[6], "keep", ScalarType::Int, table.rows, &keep) ||
+        (a[7] != Py_None && !flat_of(a[7], "lens", ScalarType::Int, table.rows, &lens)) ||
+        !one_device({first.get(), a[2], a[3], a[4], a[5], a[6], a[7]}, &guard))
+        return nullptr;
+    if (path.rows != table.rows) {
+        PyErr_Format(PyExc_ValueError, "path must have a row for each of the %lld sequences",
+                     static_cast<long long>(table.rows));
+        return nullptr;
+    }
+    if (a[8] == Py_None) max_kv = table.width * shape[1];
+    else if (!to_i64(a[8], &max_kv)) return nullptr;
+    if (table.width * shape[1] < max_kv) {
+        PyErr_Format(PyExc_ValueError, "page_table holds %lld tokens a sequence, max_kv is %lld",
+                     static_cast<long long>(table.width * shape[1]), static_cast<long long>(max_kv));
+        return nullptr;
+    }
+    constexpr int64_t MOST = (int64_t(1) << 31) - 256;   // a wide table may hold more than a sequence can have
+    if (a[8] == Py_None && max_kv > MOST) max_kv = MOST;
+    const int device = THPVariable_Unpack(first.get()).get_device();
+    std::vector<void*> ks, vs;
+    Cache k = {}, v = {};
+    if (!caches_of(a[0], "k_caches", dt, shape, device, &ks, &k) || !caches_of(a[1], "v_caches", dt, shape, device, &vs, &v))
+        return nullptr;
+    if (ks.size() != vs.size()) {
+        PyErr_SetString(PyExc_ValueError, "there must be as many caches of keys as of values");
+        return nullptr;
+    }
+    const int st = lib.cache_keep(
+        code, ks.data(), k.page, k.slot, k.head, vs.data(), v.page, v.slot, v.head, clip(static_cast<int64_t>(ks.size())),
+        shape[0], clip(shape[1]), table.p, table.stride, static_cast<int32_t*>(cu), static_cast<int32_t*>(kv), max_kv,
+        clip(table.rows), clip(shape[2]), clip(shape[3]), path.p, path.stride, clip(path.width),
+        static_cast<int32_t*>(keep), static_cast<int32_t*>(lens), stream_of(first.get()));
+    return PyLong_FromLong(st);
+    END_HANDLE_TH_ERRORS
+}
+
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(bind), FAST(qk_norm_rope), FAST(qk_norm_rope_bwd), FAST(qk_norm_rope_append), FAST(paged_attn),
-                         FAST(rope), FAST(rope_append), FAST(tree_attn),
+                         FAST(rope), FAST(rope_append), FAST(tree_attn), FAST(paged_step), FAST(cache_keep),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_attn_calls", "Marshalling of the attention sublayer's calls.", -1,
                       methods, nullptr, nullptr, nullptr, nullptr};
