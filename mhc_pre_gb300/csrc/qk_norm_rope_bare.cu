@@ -43,17 +43,39 @@ struct TableParams {
     float amplitude;
 };
 
-// Cosine and sine of a / 2^64 turns: the nearest quarter turn is taken off in
-// integers, so that what is rounded to float32 is at most an eighth.
-__device__ __forceinline__ void turned(uint64_t a, float amplitude, float& c, float& s) {
-    const uint32_t top = static_cast<uint32_t>((a + 0x80000000ull) >> 32);
-    const uint32_t quarter = (top + 0x20000000u) >> 30;
-    const int32_t rest = static_cast<int32_t>(top - (quarter << 30));
-    float y, x;
-    sincospif(static_cast<float>(rest) * 4.656612873077393e-10f, &y, &x);   // 2^-31: in half turns
-    const float u = (quarter & 1u) ? y : x, v = (quarter & 1u) ? x : y;
-    c = amplitude * (((quarter + 1u) & 2u) ? -u : u);
-    s = amplitude * ((quarter & 2u) ? -v : v);
+// a / 2^64 turns as the nearest quarter turn, in the top two bits, and what is left
+// of it in the others: `a` has an eighth of a turn (and the rounding of its lower
+// half) added, so that the rest is between -1/8 and 1/8.
+constexpr uint64_t EIGHTH = (uint64_t(1) << 61) + (uint64_t(1) << 31);
+
+// Cosines and sines of two angles, from the Taylor series of cos(pi x / 4) and
+// sin(pi x / 4) for -1 <= x <= 1: their truncation is below 2^-29, the sine's
+// first coefficient comes in two parts, and so both are right to 2^-24.
+__device__ __forceinline__ void turned2(uint32_t a, uint32_t b, float2 amplitude, float2& c, float2& s) {
+    auto both = [](float v) { return make_float2(v, v); };
+    const float2 rest = make_float2(static_cast<float>(static_cast<int32_t>((a << 2) ^ 0x80000000u)),
+                                    static_cast<float>(static_cast<int32_t>((b << 2) ^ 0x80000000u)));
+    const float2 x = __fmul2_rn(rest, both(4.656612873077393e-10f)), w = __fmul2_rn(x, x);   // 2^-31
+    float2 y = __ffma2_rn(w, both(3.13361689037812e-07f), both(-3.657620418217724e-05f));
+    y = __ffma2_rn(w, y, both(0.00249039457019272f));
+    y = __ffma2_rn(w, y, both(-0.08074551218828077f));
+    y = __ffma2_rn(w, y, both(-2.1855695031547384e-08f));   // pi / 4 less the float below
+    y = __ffma2_rn(x, both(0.78539818525314331f), __fmul2_rn(x, y));
+    float2 z = __ffma2_rn(w, both(-2.461136950494199e-08f), both(3.590860448591509e-06f));
+    z = __ffma2_rn(w, z, both(-0.00032599188692738996f));
+    z = __ffma2_rn(w, z, both(0.0158543442438155f));
+    z = __ffma2_rn(w, z, both(-0.30842513753404244f));
+    z = __ffma2_rn(w, z, both(1.0f));
+    y = __fmul2_rn(y, amplitude);
+    z = __fmul2_rn(z, amplitude);
+    // quarter turns 1 and 3 swap the two; the cosine is negative in 1 and 2, the sine in 2 and 3
+    auto put = [](uint32_t q, float cos, float sin, float& oc, float& os) {
+        const bool odd = q & 0x40000000u;
+        oc = __uint_as_float(__float_as_uint(odd ? sin : cos) ^ ((q ^ (q << 1)) & 0x80000000u));
+        os = __uint_as_float(__float_as_uint(odd ? cos : sin) ^ (q & 0x80000000u));
+    };
+    put(a, z.x, y.x, c.x, s.x);
+    put(b, z.y, y.y, c.y, s.y);
 }
 
 __global__ void __launch_bounds__(256)
@@ -66,19 +88,21 @@ rope_table_kernel(const __grid_constant__ TableParams p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint64_t f = p.turn[4 * q + i];
-        at[i] = f * static_cast<uint64_t>(row);
+        at[i] = f * static_cast<uint64_t>(row) + EIGHTH;
         by[i] = f * static_cast<uint64_t>(step);
     }
-    for (; row < p.n; row += step) {
-        float c[4], s[4];
+    const float2 amplitude = make_float2(p.amplitude, p.amplitude);
+    float* out = p.out + row * (2 * p.half) + 4 * q;
+    for (; row < p.n; row += step, out += step * (2 * p.half)) {
+        float2 c[2], s[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            turned(at[i], p.amplitude, c[i], s[i]);
-            at[i] += by[i];
-        }
-        float* out = p.out + row * (2 * p.half) + 4 * q;
-        *reinterpret_cast<float4*>(out) = make_float4(c[0], c[1], c[2], c[3]);
-        *reinterpret_cast<float4*>(out + p.half) = make_float4(s[0], s[1], s[2], s[3]);
+        for (int i = 0; i < 2; ++i)
+            turned2(static_cast<uint32_t>(at[2 * i] >> 32), static_cast<uint32_t>(at[2 * i + 1] >> 32), amplitude, c[i],
+                    s[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) at[i] += by[i];
+        *reinterpret_cast<float4*>(out) = make_float4(c[0].x, c[0].y, c[1].x, c[1].y);
+        *reinterpret_cast<float4*>(out + p.half) = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
     }
 }
 
