@@ -301,6 +301,7 @@ __device__ __forceinline__ void cc_piece(const AttnParams& p, const AttnPiece& p
                 s[static_cast<int64_t>(sr) * (DP + 1) + row] = l[a];
             }
         }
+        if constexpr (TREE) return;   // joined by a kernel of their own (paged_attn_tree.cu)
         __threadfence();
         __syncthreads();
         if (tid == 0) {
@@ -331,6 +332,7 @@ attn_cc_kernel(const AttnParams p) {
     __shared__ int s_last;
     __shared__ uint32_t s_drafted[TREE ? TREE_MOST / 32 : 1];
     const int cta = blockIdx.x;
+    if (TREE) ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     if (!attn_plan_agrees<TREE>(p)) {
         if (threadIdx.x == 0) atomicOr(&g_attn_error, ATTN_ERR_RANGE);

@@ -98,6 +98,13 @@ constexpr uint32_t FULL = 0xffffffffu;
 constexpr int PIECES = 4;                    // pieces handed out and not done with
 constexpr int PIECE_BYTES = 64;
 static_assert(sizeof(AttnPiece) <= PIECE_BYTES, "see Cfg::TOTAL");
+// Of a piece of a tree's tile: for each of its blocks with drafted tokens (9 at
+// most, the first may hold context too) which keys some row sees, and which of
+// these blocks have keys that none does.
+struct TreeSeen {
+    uint32_t keys[TREE_MOST / KEYS + 1][4];
+    uint32_t blank, pad[3];
+};
 
 template <int DP> struct Cfg {
     static constexpr int TILE = (DP / 64) * SUB;           // a block of keys, or 128 rows of queries
@@ -107,11 +114,12 @@ template <int DP> struct Cfg {
     static constexpr int BARS = RING + STAGES * TILE;
     static constexpr int B_FULL = 0, B_EMPTY = STAGES, B_S = 2 * STAGES, B_P = B_S + 2;
     static constexpr int B_Q = B_P + 4, B_QE = B_Q + 2, B_O = B_QE + 2, B_ASK = B_O + 2, B_Z = B_ASK + 1;
-    static constexpr int B_X = B_Z + 1, B_XE = B_X + 4, B_PF = B_XE + 4, B_PE = B_PF + PIECES, NBARS = B_PE + PIECES;
+    static constexpr int B_X = B_Z + 1, B_XE = B_X + 4, B_PF = B_XE + 4, B_PE = B_PF + PIECES, B_SN = B_PE + PIECES, NBARS = B_SN + PIECES;
     static constexpr int MISC = BARS + ((8 * NBARS + 15) / 16) * 16;   // TMEM address, abort flag
     static constexpr int ML = MISC + 16;                               // lane 1's maxima and sums
     static constexpr int PIECE = ML + 2 * ROWS * 4;
-    static constexpr int TOTAL = PIECE + PIECES * PIECE_BYTES;
+    static constexpr int SEEN = PIECE + PIECES * PIECE_BYTES;
+    static constexpr int TOTAL = SEEN + PIECES * static_cast<int>(sizeof(TreeSeen));
     static constexpr int SMEM = 232448;                                // all that a block may have
     static_assert(TOTAL <= SMEM, "shared memory of one SM");
 };
@@ -177,6 +185,11 @@ template <int DP> struct Pieces {
     __device__ __forceinline__ const AttnPiece& get(bool& ok) const {
         ok = wait_warp(bar(Cfg<DP>::B_PF), (n / PIECES) & 1, abort_flag);
         return *reinterpret_cast<const AttnPiece*>(smem + Cfg<DP>::PIECE + (n % PIECES) * PIECE_BYTES);
+    }
+    // A tree's list, which comes a little later than the piece; the piece must not be done with.
+    __device__ __forceinline__ const TreeSeen& seen(bool& ok) const {
+        ok = ok && wait_warp(bar(Cfg<DP>::B_SN), (n / PIECES) & 1, abort_flag);
+        return reinterpret_cast<const TreeSeen*>(smem + Cfg<DP>::SEEN)[n % PIECES];
     }
     // The warp is done with it.
     __device__ __forceinline__ void done(int lane) {
@@ -325,6 +338,18 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
         }
         for (int i = 0; ok && i < mine; ++i) {
             const int k0 = (blk + (pair ? i : 2 * i + L)) * KEYS;
+            const bool partial = k0 < lo_most || k0 + KEYS > hi_least;
+            const Seen<TREE> see = {lo, hi, lo_least, lo_most, hi_least, hi_most, node};
+            // a tree's bits are on their way while the scores are being formed
+            uint32_t tree_bits[4] = {FULL, FULL, FULL, FULL};
+            if (TREE && active && partial) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tree_bits[c] = see.bits(k0 + 32 * c);
+            }
+            auto bits = [&](int c) {
+                if (!TREE) return see.bits(k0 + 32 * c);
+                return c < 2 ? (c == 0 ? tree_bits[0] : tree_bits[1]) : (c == 2 ? tree_bits[2] : tree_bits[3]);
+            };
             ok = wait_warp(bar(C::B_S + L), par_s, abort_flag);
             par_s ^= 1;
             if (!ok) break;
@@ -341,8 +366,6 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
                 // see whole, 32 keys that no row of the warp sees cost nothing,
                 // and only the 32 at a border are masked.  Exponentials
                 // overwrite scores already read.
-                const bool partial = k0 < lo_most || k0 + KEYS > hi_least;
-                const Seen<TREE> see = {lo, hi, lo_least, lo_most, hi_least, hi_most, node};
                 constexpr int HELD = CAP ? 32 : 128;
                 uint32_t u[HELD];
                 float top;
@@ -353,7 +376,7 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
                     if (partial) {
 #pragma unroll
                         for (int c = 0; c < HELD / 32; ++c)
-                            if (!see.all(k0 + 32 * c)) mask32(u + 32 * c, see.bits(k0 + 32 * c));
+                            if (!see.all(k0 + 32 * c)) mask32(u + 32 * c, bits(c));
                     }
                     float mx[4];
 #pragma unroll
@@ -373,7 +396,7 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
                             if (borders.value && see.none(g)) continue;
                             ptx::tmem_ld32(t_s + c * 32, u);
                             ptx::tmem_wait_ld();
-                            if (borders.value && !see.all(g)) mask32(u, see.bits(g));
+                            if (borders.value && !see.all(g)) mask32(u, bits(c));
 #pragma unroll
                             for (int e = 0; e < 32; e += 8)
 #pragma unroll
@@ -445,7 +468,7 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
                                 ptx::tmem_wait_ld();
                                 const bool border = borders.value && !see.all(g);
                                 // before the cap too: an unseen key's NaN must not reach its cap4's other three
-                                if (border) mask32(u, see.bits(g), CAP == FAR_CAP ? 0u : LOWEST);
+                                if (border) mask32(u, bits(c), CAP == FAR_CAP ? 0u : LOWEST);
                                 bool near = false;   // every score of the warp's is near zero beside the cap
                                 if constexpr (CAP == FAR_CAP) {
                                     float mx[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -480,7 +503,7 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
 #pragma unroll
                                     for (int e = 0; e < 32; e += 4) cap4(u + e, cap_in, cap2, cap2 - base);
                                 }
-                                if (border) mask32(u, see.bits(g));
+                                if (border) mask32(u, bits(c));
 #pragma unroll
                                 for (int e = 0; e < 16; ++e) {
                                     const float2 y = make_float2(ex2(__uint_as_float(u[2 * e])),
@@ -610,6 +633,11 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
                     part[static_cast<int64_t>(p.plan.slot_rows) * DP + rt] = m;
                     part[static_cast<int64_t>(p.plan.slot_rows) * (DP + 1) + rt] = l;
                 }
+                if constexpr (TREE) {
+                    // joined by a kernel of their own (paged_attn_tree.cu)
+                    pieces.done(lane);
+                    continue;
+                }
                 // the same warp of the CTA that comes last joins these rows
                 __threadfence();
                 __syncwarp();
@@ -632,28 +660,39 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
     }
 }
 
-// Which of a block's keys from k0 some row of the tile sees as drafted tokens;
-// all before the drafted ones (one warp).
-__device__ __forceinline__ void tree_seen(const AttnParams& p, const AttnPiece& pc, int k0, int lane, uint32_t (&seen)[4]) {
-    const int ctx = pc.kvlen - pc.qlen;
+// The first of a piece's blocks that has drafted tokens (or is past them); the
+// number of blocks or more where none has.
+__device__ __forceinline__ int tree_tail(const AttnPiece& pc) { return max(0, ((pc.kvlen - pc.qlen) >> 7) - pc.blk); }
+
+// Which keys of a piece's last blocks some row of the tile sees (one warp): all of
+// the context from the tile's first key on, and the drafted tokens that any row has.
+__device__ __forceinline__ void tree_seen(const AttnParams& p, const AttnPiece& pc, int lane, TreeSeen& out) {
+    const int ctx = pc.kvlen - pc.qlen, first = tree_tail(pc);
     const int tok0 = attn_token(p, pc.row0);
     const int tok1 = attn_token(p, min(pc.row0 + p.plan.tile_rows, pc.qlen * p.G) - 1);
+    uint32_t blank = 0u;
+    for (int j = first; j < pc.nb; ++j) {
+        const int k0 = (pc.blk + j) * KEYS;
+        uint32_t seen[4] = {0u, 0u, 0u, 0u};
+        for (int t = tok0 + lane; t <= tok1; t += 32) {
+            AttnNode n;
+            n.words = p.tree + (pc.q0 + t) * p.tree_stride;
+            n.ctx = ctx;
+            n.nodes = ctx >= 0 ? pc.qlen : 0;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) seen[w] = 0u;
-    for (int t = tok0 + lane; t <= tok1; t += 32) {
-        AttnNode n;
-        n.words = p.tree + (pc.q0 + t) * p.tree_stride;
-        n.ctx = ctx;
-        n.nodes = ctx >= 0 ? pc.qlen : 0;
+            for (int w = 0; w < 4; ++w) seen[w] |= n.drafted(k0 + 32 * w);
+        }
 #pragma unroll
-        for (int w = 0; w < 4; ++w) seen[w] |= n.drafted(k0 + 32 * w);
+        for (int w = 0; w < 4; ++w) {
+            seen[w] = __reduce_or_sync(FULL, seen[w]);
+            const int g = k0 + 32 * w, later = ctx - g, hidden = pc.lo - g;   // keys of the word before the drafted ones, the tile's
+            if (later > 0) seen[w] |= later < 32 ? ~(FULL << later) : FULL;
+            if (hidden > 0) seen[w] &= hidden < 32 ? FULL << hidden : 0u;
+        }
+        if ((seen[0] & seen[1] & seen[2] & seen[3]) != FULL) blank |= 1u << (j - first);
+        if (lane == 0) *reinterpret_cast<uint4*>(out.keys[j - first]) = make_uint4(seen[0], seen[1], seen[2], seen[3]);
     }
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        seen[w] = __reduce_or_sync(FULL, seen[w]);
-        const int later = ctx - (k0 + 32 * w);   // keys of the word before the drafted ones
-        if (later > 0) seen[w] |= later < 32 ? ~(FULL << later) : FULL;
-    }
+    if (lane == 0) out.blank = blank;
 }
 
 template <int DP, int CAP, bool TREE>
@@ -669,6 +708,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC + 4);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
 
+    if (TREE) ptx::griddep_launch_dependents();   // the joins wait for all of this kernel, but are on the GPU by then
     if (p.force_timeout != 0u) {
         // test hook: one bounded wait that runs out before anything async starts
         if (tid == 0 && ptx::forced_wait_runs_out(sbase, 100000ull)) {
@@ -703,6 +743,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
         for (int i = 0; i < PIECES; ++i) {
             ptx::mbar_init(bar(C::B_PF + i), 1);
             ptx::mbar_init(bar(C::B_PE + i), 11);   // every other warp
+            ptx::mbar_init(bar(C::B_SN + i), 1);    // a tree: the piece's list of keys is there
         }
         ptx::mbar_init(bar(C::B_ASK), 1);
         ptx::mbar_init(bar(C::B_Z), 1);
@@ -742,6 +783,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
                     ptx::mbar_arrive(bar(C::B_PF + n % PIECES));
                 }
                 __syncwarp();
+                if (TREE && more) {   // needed by its last blocks only
+                    tree_seen(p, pc, lane, reinterpret_cast<TreeSeen*>(smem + C::SEEN)[n % PIECES]);
+                    if (lane == 0) ptx::mbar_arrive(bar(C::B_SN + n % PIECES));
+                    __syncwarp();
+                }
                 if (!more) break;   // the piece without blocks ends every role
             }
         } else if (work && warp == LOAD_WARP) {
@@ -837,18 +883,23 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
             while (ok) {
                 const AttnPiece pc = pieces.get(ok);
                 if (!ok || pc.nb == 0) break;
-                pieces.done(lane);
+                if (!TREE) pieces.done(lane);
                 const int tlo = pc.lo, thi = pc.hi;
                 const bool pair = pc.qlen * p.G - pc.row0 > p.plan.lane_rows;
-                const int ctx = pc.kvlen - pc.qlen;
-                // a tree's blocks from the first with drafted tokens on: any of these may be unseen
-                const int tail = TREE ? max(1, min(pc.nb - 1, (ctx >> 7) - pc.blk)) : 0;
-                for (int j = 0; ok && j < pc.nb;
-                     j = TREE ? (j == 0 ? tail : j + 1) : j == 0 && pc.nb > 1 ? pc.nb - 1 : pc.nb) {
+                // a tree's blocks from this one on have their own list of keys
+                const int tail = TREE ? tree_tail(pc) : pc.nb;
+                for (int j = 0; ok && j < pc.nb; j = TREE && j + 1 >= tail ? j + 1
+                                                     : j == 0 && pc.nb > 1  ? min(pc.nb - 1, TREE ? tail : pc.nb)
+                                                                            : pc.nb) {
                     const int k0 = (pc.blk + j) * KEYS;
-                    if (!partly_seen(k0, tlo, thi) && !(TREE && k0 + KEYS > ctx)) continue;
-                    uint32_t seen[4] = {FULL, FULL, FULL, FULL};   // a tree: keys that some row sees
-                    if (TREE && k0 + KEYS > ctx) tree_seen(p, pc, k0, lane, seen);
+                    const bool listed = TREE && j >= tail;
+                    if (listed) {
+                        const uint32_t blank = pieces.seen(ok).blank;
+                        if (!ok) break;
+                        if (!(blank >> (j - tail) & 1u)) continue;
+                    } else if (!partly_seen(k0, tlo, thi)) {
+                        continue;
+                    }
                     // the loads' order: K0 V0 K1 V1 ... or K0 K1 V0 K2 V1 ...
                     const uint32_t at = n + (pair || j == pc.nb - 1 ? 2 * j + 1 : 2 * j + 2);
                     const int s = static_cast<int>(at % C::STAGES);
@@ -857,30 +908,34 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
                     ok = wait_warp(bar(C::B_ASK), par_a, abort_flag);
                     par_a ^= 1;
                     if (!ok) break;
-                    if (TREE && k0 + KEYS > ctx) {
-                        for (int e = lane; e < KEYS * (DP / 8); e += 32) {
-                            const int r = e / (DP / 8), c = e % (DP / 8), w = r >> 5;
-                            const uint32_t bits = w == 0 ? seen[0] : w == 1 ? seen[1] : w == 2 ? seen[2] : seen[3];
-                            if (bits >> (r & 31) & 1u && k0 + r >= tlo) continue;
-                            *reinterpret_cast<uint4*>(smem + C::RING + s * C::TILE + (c >> 3) * SUB + r * 128 +
-                                                      (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    unsigned char* rows = smem + C::RING + s * C::TILE;
+                    if (listed) {
+                        constexpr int LPR = DP / 8;   // lanes of a row
+                        const int c = lane % LPR;
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            const uint32_t seen = pieces.seen(ok).keys[j - tail][w];
+                            if (seen == FULL) continue;
+#pragma unroll
+                            for (int r = lane / LPR; r < 32; r += 32 / LPR)
+                                if (!(seen >> r & 1u))
+                                    *reinterpret_cast<uint4*>(rows + (c >> 3) * SUB + (32 * w + r) * 128 + (c & 7) * 16) =
+                                        make_uint4(0u, 0u, 0u, 0u);
                         }
-                        ptx::fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(bar(C::B_Z));
-                        continue;
-                    }
-                    const int before = min(KEYS, max(0, tlo - k0)), from = max(before, min(KEYS, thi - k0));
-                    for (int e = lane; e < (before + KEYS - from) * (DP / 8); e += 32) {
-                        const int i = e / (DP / 8), c = e % (DP / 8), r = i < before ? i : from + i - before;
-                        *reinterpret_cast<uint4*>(smem + C::RING + s * C::TILE + (c >> 3) * SUB + r * 128 +
-                                                  (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    } else {
+                        const int before = min(KEYS, max(0, tlo - k0)), from = max(before, min(KEYS, thi - k0));
+                        for (int e = lane; e < (before + KEYS - from) * (DP / 8); e += 32) {
+                            const int i = e / (DP / 8), c = e % (DP / 8), r = i < before ? i : from + i - before;
+                            *reinterpret_cast<uint4*>(rows + (c >> 3) * SUB + r * 128 + (c & 7) * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                        }
                     }
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(bar(C::B_Z));
                 }
                 n += 2u * static_cast<uint32_t>(pc.nb);
+                if (TREE) pieces.done(lane);   // only now: its list has been read
             }
         } else if (work && warp == MMA_WARP) {
             // -------------------------------------------------------- MMA ---
@@ -938,11 +993,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
                 const int nb = __shfl_sync(FULL, pc.nb, 0);
                 const bool z0 = __all_sync(FULL, partly_seen(pc.blk * KEYS, tlo, thi));
                 const bool z1 = __all_sync(FULL, partly_seen((pc.blk + nb - 1) * KEYS, tlo, thi));
-                // blocks of a tree from this one on have drafted tokens
-                const int tail = TREE ? __shfl_sync(FULL, ((pc.kvlen - pc.qlen) >> 7) - pc.blk, 0) : 0;
-                pieces.done(lane);
+                // a tree's blocks from this one on have their own list
+                const int tail = TREE ? __shfl_sync(FULL, tree_tail(pc), 0) : 0;
+                if (!TREE) pieces.done(lane);
                 auto blanked = [&](int j) {
-                    if (ok && ((j == 0 && z0) || (j > 0 && j == nb - 1 && z1) || (TREE && j >= tail))) {
+                    bool ask = (j == 0 && z0) || (j > 0 && j == nb - 1 && z1);
+                    if (TREE && j >= tail) ask = __shfl_sync(FULL, pieces.seen(ok).blank >> (j - tail) & 1u, 0);
+                    if (ok && ask) {
                         if (lane == 0) ptx::mbar_arrive(bar(C::B_ASK));
                         ok = wait_warp(bar(C::B_Z), par_z, abort_flag);
                         par_z ^= 1;
@@ -1014,6 +1071,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
                         }
                     }
                 }
+                if (TREE) pieces.done(lane);
                 par_q ^= 1;
             }
         }

@@ -9,6 +9,12 @@
 // those of a causal chunk; only the blocks with drafted tokens differ: there a
 // row's bits take the place of the diagonal, 32 keys to a word, and values that no
 // row of a tile sees are zeroed like those past a sequence's end.
+//
+// Tiles of trees have many rows, and a tile that is split over CTAs leaves a part
+// of every row with each of them. The last CTA joining them by itself, a warp for
+// 32 rows, takes longer than all of the rest when contexts are short (one sequence
+// of 13 tokens and 777 keys: 22 of 35 us), so the joins are a kernel of their own,
+// a warp for each row.
 #include "paged_attn_cc.cuh"
 
 namespace mhc {
@@ -17,10 +23,148 @@ static ErrorWord g_error_word;
 
 cudaError_t read_and_clear_attn_tree_error(unsigned* word) { return g_error_word.read_and_clear(g_attn_error, word); }
 
+namespace attn {
+
+constexpr int JOIN_THREADS = 128, JOIN_WARPS = JOIN_THREADS / 32, JOIN_SPLIT = 16, JOIN_AHEAD = 8;
+
+// N consecutive floats of a part.
+template <int N> struct Floats {
+    float v[N];
+    __device__ __forceinline__ void load(const float* p) {
+        if constexpr (N == 2) {
+            const float2 x = __ldcg(reinterpret_cast<const float2*>(p));
+            v[0] = x.x;
+            v[1] = x.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; i += 4) {
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(p + i));
+                v[i] = x.x;
+                v[i + 1] = x.y;
+                v[i + 2] = x.z;
+                v[i + 3] = x.w;
+            }
+        }
+    }
+    __device__ __forceinline__ void store(float* p) const {
+        if constexpr (N == 2) *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+        else
+#pragma unroll
+            for (int i = 0; i < N; i += 4)
+                *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    }
+    __device__ __forceinline__ void store(__nv_bfloat16* p) const {
+        uint32_t u[N / 2];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const __nv_bfloat162 x = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t*>(&x);
+        }
+        if constexpr (N == 2) *reinterpret_cast<uint32_t*>(p) = u[0];
+        else if constexpr (N == 4) *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
+        else *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+};
+
+// Block (c, y): of the tile and head whose first part is CTA c's (a CTA has at
+// most one such, its last piece), a share of the rows, a warp for each.  Lane j
+// takes the maximum and the sum of the j-th part, so that all weights come from
+// one round of loads; then the lanes have DP/32 values of the row each and the
+// parts are added in their order, JOIN_AHEAD of them on their way together.
+template <typename TA, int DP>
+__global__ void __launch_bounds__(JOIN_THREADS)
+tree_join_kernel(const AttnParams p) {
+    constexpr int N = DP / 32;
+    ptx::griddep_wait();
+    if (!attn_plan_agrees<true>(p)) return;   // the kernel before has said so
+    const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (c + 1 >= p.plan.ncta) return;
+    const AttnStart s = attn_starts(p)[c + 1];   // where this CTA's share ends
+    const int cost = s.t.nblk + p.plan.lead;
+    if (s.begin >= s.end || s.unit <= p.plan.lead) return;   // no tile goes on there
+    const int64_t per = attn_head(p)->per_cta;
+    const int64_t u0 = s.t.start + static_cast<int64_t>(s.head) * cost + p.plan.lead;
+    const int first = static_cast<int>(u0 / per), last = static_cast<int>((u0 + s.t.nblk - 1) / per);
+    if (first != c || last == first) return;
+    const int rows = min(p.plan.tile_rows, s.t.qlen * p.G - s.t.row0), sr = p.plan.slot_rows;
+    auto part = [&](int j) { return attn_slot(p, 2 * j + (j == first ? 1 : 0)); };
+    for (int row = blockIdx.y * JOIN_WARPS + warp; row < rows; row += gridDim.y * JOIN_WARPS) {
+        float M = -INFINITY, l = 0.0f;
+        Floats<N> a;
+#pragma unroll
+        for (int i = 0; i < N; ++i) a.v[i] = 0.0f;
+        for (int c0 = first; c0 <= last; c0 += 32) {
+            const int n = min(32, last - c0 + 1);
+            const float* stat = part(c0 + min(lane, n - 1)) + static_cast<int64_t>(sr) * DP + row;
+            float w = lane < n ? __ldcg(stat) : -INFINITY;
+            const float pl = lane < n ? __ldcg(stat + sr) : 0.0f;
+            Floats<N> x[JOIN_AHEAD];
+            auto fetch = [&](int j0) {
+#pragma unroll
+                for (int u = 0; u < JOIN_AHEAD; ++u)
+                    x[u].load(part(c0 + min(j0 + u, n - 1)) + static_cast<int64_t>(row) * DP + lane * N);
+            };
+            fetch(0);   // on their way with the weights
+            float top = w;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            top = fmaxf(top, M);
+            const float base = top == -INFINITY ? 0.0f : top, keep = ex2(M - base);
+            w = ex2(w - base);
+            l = fmaf(l, keep, warp_sum(pl * w));
+            M = top;
+#pragma unroll
+            for (int i = 0; i < N; ++i) a.v[i] *= keep;
+            for (int j0 = 0; j0 < n; j0 += JOIN_AHEAD) {
+                if (j0 > 0) fetch(j0);
+#pragma unroll
+                for (int u = 0; u < JOIN_AHEAD; ++u) {
+                    const float f = __shfl_sync(0xffffffffu, w, min(j0 + u, 31));
+                    if (j0 + u < n)
+#pragma unroll
+                        for (int i = 0; i < N; ++i) a.v[i] = fmaf(x[u].v[i], f, a.v[i]);
+                }
+            }
+        }
+        const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+        const int r = s.t.row0 + row, tok = attn_token(p, r);
+        const int64_t out = (s.t.q0 + tok) * p.Hq + s.head * p.G + (r - tok * p.G);
+#pragma unroll
+        for (int i = 0; i < N; ++i) a.v[i] *= inv;
+        if (lane * N < p.Dh) a.store(static_cast<TA*>(p.o) + out * p.Dh + lane * N);   // heads are multiples of 8
+        if (lane == 0 && p.lse != nullptr) p.lse[out] = attn_lse(M, l);
+    }
+}
+
+template <typename TA>
+cudaError_t launch_tree_join(const AttnParams& p, cudaStream_t s) {
+    const int most = (p.plan.slot_rows + JOIN_WARPS - 1) / JOIN_WARPS;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.plan.ncta), static_cast<unsigned>(most < JOIN_SPLIT ? most : JOIN_SPLIT));
+    cfg.blockDim = dim3(JOIN_THREADS);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (p.Dh <= 64) return cudaLaunchKernelEx(&cfg, tree_join_kernel<TA, 64>, p);
+    if (p.Dh <= 128) return cudaLaunchKernelEx(&cfg, tree_join_kernel<TA, 128>, p);
+    return cudaLaunchKernelEx(&cfg, tree_join_kernel<TA, 256>, p);
+}
+
+}  // namespace attn
+
 cudaError_t launch_tree_attn(bool bf16, const AttnParams& p, cudaStream_t s) {
-    if (attn_tc_supports(bf16, p.Hq, p.Hk, p.Dh, p.page_size)) return launch_tree_attn_tc(p, s);
-    g_error_word.may_be_set();
-    return bf16 ? attn::launch_cc_dp<__nv_bfloat16, true>(p, s) : attn::launch_cc_dp<float, true>(p, s);
+    cudaError_t e;
+    if (attn_tc_supports(bf16, p.Hq, p.Hk, p.Dh, p.page_size)) {
+        e = launch_tree_attn_tc(p, s);
+    } else {
+        g_error_word.may_be_set();
+        e = bf16 ? attn::launch_cc_dp<__nv_bfloat16, true>(p, s) : attn::launch_cc_dp<float, true>(p, s);
+    }
+    if (e != cudaSuccess) return e;
+    return bf16 ? attn::launch_tree_join<__nv_bfloat16>(p, s) : attn::launch_tree_join<float>(p, s);
 }
 
 }  // namespace mhc
