@@ -56,11 +56,12 @@ class DraftServer:
         i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)       # noqa: E731
         s = B.mhc_paged_step(i32(counts), self.lens, self.table, self.held, self.free, self.count, self.page, T,
                              parents=None if parents is None else i32(parents), width=-(-n // 32))
-        lay = self.layers[0]
-        plan = (B.mhc_paged_attn_plan if parents is None else B.mhc_tree_attn_plan)(
-            s.cu_q, s.kv_lens, torch.bfloat16, T, lay.Hq, lay.Hk, lay.Dh, self.page, n, self.max_kv, lay.window)
+        plan, lay = None, self.layers[0]
+        if parents is None:
+            plan = B.mhc_paged_attn_plan(s.cu_q, s.kv_lens, torch.bfloat16, T, lay.Hq, lay.Hk, lay.Dh, self.page, n,
+                                         self.max_kv, lay.window)
         for layer, k, v in zip(self.layers, self.k, self.v):
-            x = self.layer(layer, x, k, v, s, plan)
+            x = self.layer(layer, x, k, v, s, n, plan)
         if paths is None:
             self.lens = s.kv_lens
         else:
@@ -69,16 +70,17 @@ class DraftServer:
             B.mhc_cache_keep(self.k, self.v, self.table, s.cu_q, s.kv_lens, path, i32(keep), lens=self.lens)
         return x
 
-    def layer(self, layer, x, k_cache, v_cache, s, plan):
+    def layer(self, layer, x, k_cache, v_cache, s, most, plan):
         T, h, k = x.shape[0], layer.Hq * layer.Dh, layer.Hk * layer.Dh
         f = B.mhc_pre(x, layer.phi, layer.b, layer.alpha)
         q, kk, v = (t.view(T, -1, layer.Dh) for t in (f.x_in @ layer.w_qkv).split([h, k, k], 1))
         q = B.mhc_qk_norm_rope_append(q, kk, v, layer.w_q, layer.w_k, k_cache, v_cache, s.slots,
                                       positions=s.positions, cos_sin=layer.cos_sin)
-        if s.tree is None:
+        if plan is not None:
             o = B.mhc_paged_attn(q, k_cache, v_cache, self.table, plan=plan).o
         else:
-            o = B.mhc_tree_attn(q, k_cache, v_cache, self.table, s.tree, plan=plan).o
+            o = B.mhc_tree_attn(q, k_cache, v_cache, self.table, s.tree, s.cu_q, s.kv_lens, max_q=most,
+                                max_kv=self.max_kv, window=layer.window).o
         return B.mhc_post(x, o.view(T, h) @ layer.w_out, f.H_post, f.H_res)
 
 

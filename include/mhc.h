@@ -619,17 +619,13 @@ size_t mhc_paged_attn_workspace_bytes(mhc_dtype dt, int64_t T, int B, int Hq, in
  *                                         least ceil(max_q / 32); bits past a
  *                                         sequence's new tokens are ignored
  *   max_q                                 at most 1024
+ *   cu_q, kv_lens                         there is no plan: every call splits the
+ *                                         batch by itself, from these
  * The rest, the workspace (mhc_paged_attn_workspace_bytes) and the errors are as
  * for mhc_paged_attn.  What the pages hold for a drafted token that no row of a
  * tile sees (padding, say) is never used; with a window the last window - 1
  * tokens of the context count as seen.
- *
- * mhc_tree_attn_plan -- as mhc_paged_attn_plan, for mhc_tree_attn only.  It does
- * not depend on `tree`.
  */
-mhc_status mhc_tree_attn_plan(mhc_dtype dt, const int32_t* cu_q, const int32_t* kv_lens, int64_t T, int B,
-                              int Hq, int Hk, int Dh, int page_size, int64_t max_q, int64_t max_kv,
-                              int window, void* workspace, size_t ws_bytes, cudaStream_t stream);
 mhc_status mhc_tree_attn(mhc_dtype dt, const void* q, int64_t q_stride, const void* k_cache,
                          int64_t k_page_stride, int64_t k_slot_stride, int64_t k_head_stride,
                          const void* v_cache, int64_t v_page_stride, int64_t v_slot_stride,

@@ -37,7 +37,7 @@ EXPORTS = ("mhc_status_string", "mhc_version", "mhc_get_last_device_error",
            "mhc_qk_norm_rope_append", "mhc_paged_attn_plan", "mhc_paged_attn",
            "mhc_paged_attn_workspace_bytes",
            "mhc_rope_table", "mhc_rope", "mhc_rope_bwd", "mhc_rope_append",
-           "mhc_tree_attn_plan", "mhc_tree_attn", "mhc_paged_step", "mhc_cache_keep")
+           "mhc_tree_attn", "mhc_paged_step", "mhc_cache_keep")
 
 PreOut = namedtuple("PreOut", "x_in H_pre H_post H_res proj inv_rms")
 PostPreOut = namedtuple("PostPreOut", "x_next x_in H_pre H_post H_res proj inv_rms")
@@ -54,7 +54,6 @@ QKBwdOut = namedtuple("QKBwdOut", "dq dk dw_q dw_k")
 PagedAttnOut = namedtuple("PagedAttnOut", "o lse")
 PagedAttnPlan = namedtuple("PagedAttnPlan", "workspace sizes")
 PagedStep = namedtuple("PagedStep", "cu_q kv_lens positions slots tree")
-TreeAttnPlan = namedtuple("TreeAttnPlan", "workspace sizes")
 ROPE_ADJACENT = 1
 
 _P, _I64, _I, _F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
@@ -103,7 +102,6 @@ _SIGS = {
                         _P, _I64, _P, _P, _I64, _I, _I, _I, _I, _I64, _I64, _I, _F, _F, _P, _P,
                         _P, ctypes.c_size_t, _P], _I),
     "mhc_paged_attn_workspace_bytes": ([_I, _I64, _I, _I, _I, _I, _I, _I64], ctypes.c_size_t),
-    "mhc_tree_attn_plan": ([_I, _P, _P, _I64, _I, _I, _I, _I, _I, _I64, _I64, _I, _P, ctypes.c_size_t, _P], _I),
     "mhc_tree_attn": ([_I, _P, _I64, _P, _I64, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I,
                        _P, _I64, _P, _I64, _P, _P, _I64, _I, _I, _I, _I, _I64, _I64, _I, _F, _F, _P, _P,
                        _P, ctypes.c_size_t, _P], _I),
@@ -552,51 +550,27 @@ def mhc_rope_append(q, k, v, k_cache, v_cache, slots, positions, cos_sin, interl
     return out
 
 
-def _attn_plan(name, cu_q, kv_lens, dtype, T, Hq, Hk, Dh, page_size, max_q, max_kv, window):
-    B = kv_lens.numel()
-    for t, what, n in ((cu_q, "cu_q", B + 1), (kv_lens, "kv_lens", B)):
-        if t.dtype != torch.int32:
-            raise TypeError(f"{what} must be {torch.int32}, got {t.dtype}")
-        if t.numel() != n:
-            raise ValueError(f"{what} must have {n} entries, got {t.numel()}")
-    if dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"activations must be bfloat16 or float32, got {dtype}")
-    code = MHC_BF16 if dtype == torch.bfloat16 else MHC_F32
-    need = int(lib().mhc_paged_attn_workspace_bytes(code, T, B, Hq, Hk, Dh, page_size, max_q))
-    ws = _empty((max(need, 16),), dtype=torch.uint8, device=cu_q.device)
-    st = getattr(lib(), name)(code, _ptr(cu_q), _ptr(kv_lens), T, B, Hq, Hk, Dh, page_size, max_q, max_kv,
-                              window, _ptr(ws), need, _stream(cu_q.device))
-    _check(st, name)
-    return ws, (code, T, B, Hq, Hk, Dh, page_size, max_q, max_kv, window)
-
-
 def mhc_paged_attn_plan(cu_q, kv_lens, dtype, T: int, Hq: int, Hk: int, Dh: int, page_size: int,
                         max_q: int, max_kv: int, window: int = 0):
     """Splits a batch over the GPU once, for every mhc_paged_attn call of the
     same sizes (the layers of one step).  Calls that share a plan share its
     workspace: they must not overlap.  After a call that timed out the batch has
     to be planned again."""
-    return PagedAttnPlan(*_attn_plan("mhc_paged_attn_plan", cu_q, kv_lens, dtype, T, Hq, Hk, Dh, page_size, max_q,
-                                     max_kv, window))
-
-
-def mhc_tree_attn_plan(cu_q, kv_lens, dtype, T: int, Hq: int, Hk: int, Dh: int, page_size: int,
-                       max_q: int, max_kv: int, window: int = 0):
-    """mhc_paged_attn_plan for mhc_tree_attn (whatever the trees are)."""
-    return TreeAttnPlan(*_attn_plan("mhc_tree_attn_plan", cu_q, kv_lens, dtype, T, Hq, Hk, Dh, page_size, max_q,
-                                    max_kv, window))
-
-
-def _planned(plan, q, k_cache, page_table, cu_q, kv_lens, max_q, max_kv, window):
-    """A plan's workspace and its own bounds, which the call's must not contradict."""
-    ws, sizes = plan
-    max_q, max_kv, window = (a if b is None else b for a, b in zip(sizes[7:], (max_q, max_kv, window)))
-    code = MHC_BF16 if q.dtype == torch.bfloat16 else MHC_F32
-    want = (code, q.shape[0], page_table.shape[0], q.shape[1], k_cache.shape[2], q.shape[2], k_cache.shape[1],
-            max_q, max_kv, window)
-    if want != sizes or cu_q is not None or kv_lens is not None:
-        raise ValueError(f"the plan has its own lengths and sizes: {sizes}, not {want}")
-    return ws, max_q, max_kv, window
+    B = kv_lens.numel()
+    for t, name, n in ((cu_q, "cu_q", B + 1), (kv_lens, "kv_lens", B)):
+        if t.dtype != torch.int32:
+            raise TypeError(f"{name} must be {torch.int32}, got {t.dtype}")
+        if t.numel() != n:
+            raise ValueError(f"{name} must have {n} entries, got {t.numel()}")
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"activations must be bfloat16 or float32, got {dtype}")
+    code = MHC_BF16 if dtype == torch.bfloat16 else MHC_F32
+    need = int(lib().mhc_paged_attn_workspace_bytes(code, T, B, Hq, Hk, Dh, page_size, max_q))
+    ws = _empty((max(need, 16),), dtype=torch.uint8, device=cu_q.device)
+    st = lib().mhc_paged_attn_plan(code, _ptr(cu_q), _ptr(kv_lens), T, B, Hq, Hk, Dh, page_size, max_q, max_kv,
+                                   window, _ptr(ws), need, _stream(cu_q.device))
+    _check(st, "mhc_paged_attn_plan")
+    return PagedAttnPlan(ws, (code, T, B, Hq, Hk, Dh, page_size, max_q, max_kv, window))
 
 
 def mhc_paged_attn(q, k_cache, v_cache, page_table, cu_q=None, kv_lens=None, max_q: int = None,
@@ -612,9 +586,13 @@ def mhc_paged_attn(q, k_cache, v_cache, page_table, cu_q=None, kv_lens=None, max
     as they are.  Returns o and lse [T, Hq]."""
     ws = None
     if plan is not None:
-        if isinstance(plan, TreeAttnPlan):
-            raise TypeError("mhc_paged_attn takes a plan of mhc_paged_attn_plan")
-        ws, max_q, max_kv, window = _planned(plan, q, k_cache, page_table, cu_q, kv_lens, max_q, max_kv, window)
+        ws, sizes = plan
+        max_q, max_kv, window = (a if b is None else b for a, b in zip(sizes[7:], (max_q, max_kv, window)))
+        code = MHC_BF16 if q.dtype == torch.bfloat16 else MHC_F32
+        want = (code, q.shape[0], page_table.shape[0], q.shape[1], k_cache.shape[2], q.shape[2], k_cache.shape[1],
+                max_q, max_kv, window)
+        if want != sizes or cu_q is not None or kv_lens is not None:
+            raise ValueError(f"the plan has its own lengths and sizes: {sizes}, not {want}")
     st, o, lse = (_calls_module or _calls()).paged_attn(
         _allocator(), q, k_cache, v_cache, page_table, cu_q, kv_lens, max_q, max_kv, scale, window or 0, softcap, ws, out)
     if st:
@@ -622,22 +600,16 @@ def mhc_paged_attn(q, k_cache, v_cache, page_table, cu_q=None, kv_lens=None, max
     return PagedAttnOut(o, lse)
 
 
-def mhc_tree_attn(q, k_cache, v_cache, page_table, tree, cu_q=None, kv_lens=None, max_q: int = None,
-                  max_kv: int = None, scale: float = None, window: int = None, softcap: float = 0.0,
-                  plan=None, out=None):
+def mhc_tree_attn(q, k_cache, v_cache, page_table, tree, cu_q, kv_lens, max_q: int = None, max_kv: int = None,
+                  scale: float = None, window: int = None, softcap: float = 0.0, out=None):
     """Attention of trees of drafted tokens: as mhc_paged_attn, but of the new
     tokens of its sequence row t sees those whose bits tree[t] has (int32 words;
     bit i % 32 of word i // 32: the i-th new token), and all cached tokens before
-    them.  ``window`` counts a row's nodes and the context behind them.
-    ``plan``: from mhc_tree_attn_plan.  Returns o and lse [T, Hq]."""
-    ws = None
-    if plan is not None:
-        if not isinstance(plan, TreeAttnPlan):
-            raise TypeError("mhc_tree_attn takes a plan of mhc_tree_attn_plan")
-        ws, max_q, max_kv, window = _planned(plan, q, k_cache, page_table, cu_q, kv_lens, max_q, max_kv, window)
+    them.  ``window`` counts a row's nodes and the context behind them.  There is no
+    plan: each call splits the batch by itself.  Returns o and lse [T, Hq]."""
     st, o, lse = (_calls_module or _calls()).tree_attn(
-        _allocator(), q, k_cache, v_cache, page_table, cu_q, kv_lens, max_q, max_kv, scale, window or 0, softcap, ws, out,
-        tree)
+        _allocator(), q, k_cache, v_cache, page_table, cu_q, kv_lens, max_q, max_kv, scale, window or 0, softcap, None,
+        out, tree)
     if st:
         _check(st, "mhc_tree_attn")
     return PagedAttnOut(o, lse)

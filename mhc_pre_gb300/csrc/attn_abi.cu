@@ -393,12 +393,11 @@ static mhc_status check_tree(int64_t max_q, const int32_t* tree, int64_t tree_st
     return check_plain(tree, 4);
 }
 
-static mhc_status plan_call(mhc_dtype dt, const int32_t* cu_q, const int32_t* kv_lens, int64_t T, int B, int Hq, int Hk,
-                            int Dh, int page_size, int64_t max_q, int64_t max_kv, int window, bool tree,
-                            void* workspace, size_t ws_bytes, cudaStream_t stream) {
+mhc_status mhc_paged_attn_plan(mhc_dtype dt, const int32_t* cu_q, const int32_t* kv_lens, int64_t T, int B, int Hq,
+                               int Hk, int Dh, int page_size, int64_t max_q, int64_t max_kv, int window,
+                               void* workspace, size_t ws_bytes, cudaStream_t stream) {
     mhc_status st = check_attn(dt, T, B, Hq, Hk, Dh, page_size, max_q, max_kv, window);
     if (st != MHC_OK) return st;
-    if (tree && max_q > mhc::TREE_MOST) return MHC_ERR_UNSUPPORTED;
     if (T == 0 || B == 0) return MHC_OK;
     const void* ptrs[] = {workspace};
     if ((st = check_ptrs(ptrs, 1)) != MHC_OK) return st;
@@ -406,22 +405,7 @@ static mhc_status plan_call(mhc_dtype dt, const int32_t* cu_q, const int32_t* kv
     const mhc::AttnPlan plan = mhc::attn_plan_sizes(dt == MHC_BF16, T, B, Hq, Hk, Dh, page_size, max_q);
     if (!counters_fit(plan, Hk)) return MHC_ERR_UNSUPPORTED;
     if (ws_bytes < plan.total) return MHC_ERR_INVALID_ARG;
-    return from_cuda(mhc::launch_attn_plan(plan, cu_q, kv_lens, T, B, Hq, Hk, window, max_q, max_kv, tree, workspace,
-                                           stream));
-}
-
-mhc_status mhc_paged_attn_plan(mhc_dtype dt, const int32_t* cu_q, const int32_t* kv_lens, int64_t T, int B, int Hq,
-                               int Hk, int Dh, int page_size, int64_t max_q, int64_t max_kv, int window,
-                               void* workspace, size_t ws_bytes, cudaStream_t stream) {
-    return plan_call(dt, cu_q, kv_lens, T, B, Hq, Hk, Dh, page_size, max_q, max_kv, window, false, workspace, ws_bytes,
-                     stream);
-}
-
-mhc_status mhc_tree_attn_plan(mhc_dtype dt, const int32_t* cu_q, const int32_t* kv_lens, int64_t T, int B, int Hq,
-                              int Hk, int Dh, int page_size, int64_t max_q, int64_t max_kv, int window,
-                              void* workspace, size_t ws_bytes, cudaStream_t stream) {
-    return plan_call(dt, cu_q, kv_lens, T, B, Hq, Hk, Dh, page_size, max_q, max_kv, window, true, workspace, ws_bytes,
-                     stream);
+    return from_cuda(mhc::launch_attn_plan(plan, cu_q, kv_lens, T, B, Hq, Hk, window, max_q, max_kv, workspace, stream));
 }
 
 static mhc_status attn_call(mhc_dtype dt, const void* q, int64_t q_stride, const void* k_cache, int64_t k_page_stride,
@@ -450,9 +434,11 @@ static mhc_status attn_call(mhc_dtype dt, const void* q, int64_t q_stride, const
     const mhc::AttnPlan plan = mhc::attn_plan_sizes(dt == MHC_BF16, T, B, Hq, Hk, Dh, page_size, max_q);
     if (!counters_fit(plan, Hk)) return MHC_ERR_UNSUPPORTED;
     if (ws_bytes < plan.total) return MHC_ERR_INVALID_ARG;
-    if (cu_q != nullptr) {
-        st = plan_call(dt, cu_q, kv_lens, T, B, Hq, Hk, Dh, page_size, max_q, max_kv, window, trees, workspace, ws_bytes,
-                       stream);
+    if (trees) {
+        if ((st = check_plain(cu_q, 4)) != MHC_OK || (st = check_plain(kv_lens, 4)) != MHC_OK) return st;
+    } else if (cu_q != nullptr) {
+        st = mhc_paged_attn_plan(dt, cu_q, kv_lens, T, B, Hq, Hk, Dh, page_size, max_q, max_kv, window, workspace,
+                                 ws_bytes, stream);
         if (st != MHC_OK) return st;
     }
     mhc::AttnParams p = {};
@@ -464,6 +450,8 @@ static mhc_status attn_call(mhc_dtype dt, const void* q, int64_t q_stride, const
     p.page_table = page_table;
     p.tree = reinterpret_cast<const uint32_t*>(tree);
     p.tree_stride = tree_stride;
+    p.cu_q = cu_q;
+    p.kv_lens = kv_lens;
     p.ws = static_cast<unsigned char*>(workspace);
     p.q_stride = q_stride;
     p.table_stride = table_stride;

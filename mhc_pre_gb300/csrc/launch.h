@@ -160,8 +160,7 @@ struct AttnPlan;
 struct AttnParams;
 AttnPlan attn_plan_sizes(bool bf16, int64_t T, int B, int Hq, int Hk, int Dh, int page_size, int64_t max_q);
 cudaError_t launch_attn_plan(const AttnPlan& plan, const int32_t* cu_q, const int32_t* kv_lens, int64_t T, int B,
-                             int Hq, int Hk, int window, int64_t max_q, int64_t max_kv, bool tree, void* ws,
-                             cudaStream_t s);
+                             int Hq, int Hk, int window, int64_t max_q, int64_t max_kv, void* ws, cudaStream_t s);
 cudaError_t launch_paged_attn(bool bf16, const AttnParams& p, cudaStream_t s);
 cudaError_t launch_tree_attn(bool bf16, const AttnParams& p, cudaStream_t s);   // p.tree: trees of drafted tokens
 

@@ -25,7 +25,6 @@ namespace attn {
 
 constexpr int PLAN_THREADS = 512;   // also at least PLAN_CTAS
 constexpr int PLAN_NEAR = 256;      // whole tiles kept there for the borders (12 KB)
-constexpr int SMALL_TILE = 8;       // tiles below 1/8 of a CTA's share are not split
 constexpr int PLAN_CTAS = 512;      // most CTAs of a launch
 constexpr int PLAN_TILES = 2048;    // tile starts kept in shared memory for the CTAs' search
 
@@ -34,7 +33,7 @@ struct PlanParams {
     unsigned char* ws;
     int64_t T;
     int64_t max_kv;
-    int B, Hq, Hk, G, window, max_q, tree;
+    int B, Hq, Hk, G, window, max_q;
     AttnPlan plan;
 };
 
@@ -126,9 +125,9 @@ attn_plan_kernel(const PlanParams p) {
                 t.kvlen = s_kvlen[lo];
                 t.row0 = (i - tile_base[lo]) * TR;
                 const int last = min(t.row0 + TR, t.qlen * p.G) - 1;
-                int lo_k, hi_k;
-                if (p.tree) attn_tile_keys<true>(t, 0, 0, p.window, lo_k, hi_k);
-                else attn_tile_keys<false>(t, t.row0 / p.G, last / p.G, p.window, lo_k, hi_k);
+                int lo_k, hi_k, unused;
+                attn_token_keys(t, t.row0 / p.G, p.window, lo_k, unused);
+                attn_token_keys(t, last / p.G, p.window, unused, hi_k);
                 // rows that see nothing still get their zeros written: one masked block
                 t.blk0 = hi_k > lo_k ? lo_k / BN : 0;
                 t.nblk = hi_k > lo_k ? (hi_k + BN - 1) / BN - t.blk0 : 1;
@@ -165,7 +164,6 @@ attn_plan_kernel(const PlanParams p) {
         h->block_keys = BN;
         h->window = p.window;
         h->lead = p.plan.lead;
-        h->tree = p.tree;
         h->spent = 0;
     }
     AttnStart* starts = reinterpret_cast<AttnStart*>(p.ws + p.plan.start_off);
@@ -186,7 +184,7 @@ attn_plan_kernel(const PlanParams p) {
         s.tile = lo;
         s.head = static_cast<int>(in / cost);
         s.unit = static_cast<int>(in - static_cast<int64_t>(s.head) * cost);
-        if (s.unit > 0 && cost * SMALL_TILE <= per) {
+        if (s.unit > 0 && cost * ATTN_SMALL_TILE <= per) {
             if (2 * s.unit < cost) {
                 u -= s.unit;
             } else {
@@ -248,8 +246,7 @@ AttnPlan attn_plan_sizes(bool bf16, int64_t T, int B, int Hq, int Hk, int Dh, in
 }
 
 cudaError_t launch_attn_plan(const AttnPlan& plan, const int32_t* cu_q, const int32_t* kv_lens, int64_t T, int B,
-                             int Hq, int Hk, int window, int64_t max_q, int64_t max_kv, bool tree, void* ws,
-                             cudaStream_t s) {
+                             int Hq, int Hk, int window, int64_t max_q, int64_t max_kv, void* ws, cudaStream_t s) {
     g_error_word.may_be_set();
     attn::PlanParams p;
     p.cu_q = cu_q;
@@ -263,7 +260,6 @@ cudaError_t launch_attn_plan(const AttnPlan& plan, const int32_t* cu_q, const in
     p.G = Hq / Hk;
     p.window = window;
     p.max_q = static_cast<int>(max_q);
-    p.tree = tree ? 1 : 0;
     p.plan = plan;
     attn::attn_plan_kernel<<<1, attn::PLAN_THREADS, 0, s>>>(p);
     return cudaGetLastError();

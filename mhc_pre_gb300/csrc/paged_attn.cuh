@@ -33,6 +33,9 @@ constexpr unsigned ATTN_ERR_TIMEOUT = 1u, ATTN_ERR_RANGE = 2u;
 // Most new tokens of a sequence that is a tree.
 constexpr int TREE_MOST = 1024;
 
+// Tiles below 1/8 of a CTA's share are not split.
+constexpr int ATTN_SMALL_TILE = 8;
+
 // Join counters of a tile and key head: each warp's rows are joined by
 // themselves.
 constexpr int JOINS = 8;
@@ -57,7 +60,6 @@ struct AttnHead {       // start of the plan
     int ntiles;
     int ncta;
     int Hq, Hk, B, tile_rows, block_keys, window, lead;
-    int tree;           // of trees of drafted tokens: its tiles see other keys
     int spent;          // a wait ran out in a call with this plan: parts of its tiles never
                         // came, and their join counters stand where the next call would
                         // take them for its own
@@ -81,6 +83,7 @@ struct AttnParams {
     float* lse;                    // may be null
     const int32_t* page_table;     // [B, table_stride]
     const uint32_t* tree;          // [T, tree_stride]: bit i of a row, the sequence's i-th new token is seen
+    const int32_t *cu_q, *kv_lens; // of trees only, which have no plan
     unsigned char* ws;
     int64_t q_stride, table_stride, num_pages, tree_stride;
     int64_t k_page_stride, k_slot_stride, k_head_stride;
@@ -118,13 +121,12 @@ __device__ __forceinline__ int* attn_counts(const AttnParams& p) {
 // Whether the plan in the workspace is the one that this call's sizes ask for (a
 // larger max_q would overrun the parts, a larger max_kv the page table) and its
 // counters are at zero.
-template <bool TREE>
 __device__ __forceinline__ bool attn_plan_agrees(const AttnParams& p) {
     const AttnHead* h = attn_head(p);
     return h->T == p.T && h->max_q == p.max_q && h->max_kv == p.max_kv && h->Hq == p.Hq && h->Hk == p.Hk &&
            h->B == p.B && h->tile_rows == p.plan.tile_rows && h->block_keys == p.plan.block_keys &&
            h->window == p.window && h->ncta == p.plan.ncta && h->lead == p.plan.lead && h->ntiles >= 0 &&
-           h->ntiles <= p.plan.max_tiles && h->per_cta > 0 && h->spent == 0 && h->tree == (TREE ? 1 : 0);
+           h->ntiles <= p.plan.max_tiles && h->per_cta > 0 && h->spent == 0;
 }
 __device__ __forceinline__ void attn_plan_spent(const AttnParams& p) { reinterpret_cast<AttnHead*>(p.ws)->spent = 1; }
 
@@ -197,6 +199,172 @@ struct AttnNode {
     }
 };
 
+// A sequence of drafted tokens as tiles, all alike: they see the same keys.
+struct TreeSeq {
+    int64_t q0;
+    int qlen, kvlen, blk0, nblk, tiles;   // no tiles: no new tokens, or numbers that do not fit the call
+    bool fits;
+    __device__ __forceinline__ int64_t units(const AttnParams& p) const {
+        return static_cast<int64_t>(tiles) * p.Hk * (nblk + p.plan.lead);
+    }
+    __device__ __forceinline__ AttnTile tile(const AttnParams& p, int seq, int i, int64_t start) const {
+        AttnTile t = {};
+        t.start = start;
+        t.q0 = q0;
+        t.seq = seq;
+        t.qlen = qlen;
+        t.kvlen = kvlen;
+        t.row0 = i * p.plan.tile_rows;
+        t.blk0 = blk0;
+        t.nblk = nblk;
+        return t;
+    }
+};
+__device__ __forceinline__ TreeSeq tree_seq(const AttnParams& p, int b) {
+    const int q0 = p.cu_q[b], qlen = p.cu_q[b + 1] - q0, kvlen = p.kv_lens[b];
+    TreeSeq s;
+    s.fits = q0 >= 0 && qlen >= 0 && qlen <= p.max_q && q0 + static_cast<int64_t>(qlen) <= p.T && kvlen >= 0 &&
+             kvlen <= p.max_kv;
+    s.q0 = q0;
+    s.qlen = s.fits ? qlen : 0;
+    s.kvlen = kvlen;
+    s.tiles = (s.qlen * p.G + p.plan.tile_rows - 1) / p.plan.tile_rows;
+    int lo, hi;
+    attn_tree_keys(s, p.window, lo, hi);
+    // rows that see nothing still get their zeros written: one masked block
+    s.blk0 = hi > lo ? lo / p.plan.block_keys : 0;
+    s.nblk = hi > lo ? (hi + p.plan.block_keys - 1) / p.plan.block_keys - s.blk0 : 1;
+    return s;
+}
+// The tile after `t`: of its sequence, or the first of the next that has any
+// (seq = B: there is none).
+__device__ __forceinline__ void tree_next_tile(const AttnParams& p, AttnTile& t) {
+    t.start += static_cast<int64_t>(p.Hk) * (t.nblk + p.plan.lead);
+    t.row0 += p.plan.tile_rows;
+    if (t.row0 < t.qlen * p.G) return;
+    for (int b = t.seq + 1; b < p.B; ++b) {
+        const TreeSeq s = tree_seq(p, b);
+        if (s.tiles == 0) continue;
+        t = s.tile(p, b, 0, t.start);
+        return;
+    }
+    t.seq = p.B;
+}
+
+// What the CTAs of a launch leave for the joins, and how a CTA finds its share: in
+// place of a plan, each CTA sums up the units of all sequences (a scan of a few
+// numbers each) and finds its two borders among them.  The sums cost it less than
+// reading a plan would, and there is no launch before it.
+struct TreeShare {
+    AttnStart start;
+    int64_t per, sums[32];
+};
+// The border at unit u of a batch of `units`, moved to the nearer end of a tile (of
+// one key head) that is not to be split; u lies in sequence b, whose first unit is
+// `base`.
+__device__ __forceinline__ AttnStart tree_border(const AttnParams& p, const TreeSeq& s, int b, int64_t base, int64_t u,
+                                                 int64_t units, int64_t per) {
+    const int cost = s.nblk + p.plan.lead;
+    const int64_t in = u - base, row = static_cast<int64_t>(p.Hk) * cost;
+    const int tile = static_cast<int>(in / row);
+    const int left = static_cast<int>(in - tile * row);
+    AttnStart a = {};
+    a.head = left / cost;
+    a.unit = left - a.head * cost;
+    a.t = s.tile(p, b, tile, base + tile * row);
+    a.begin = u;
+    if (a.unit > 0 && static_cast<int64_t>(cost) * ATTN_SMALL_TILE <= per) {
+        if (2 * a.unit < cost) {
+            a.begin -= a.unit;
+        } else {
+            a.begin += cost - a.unit;
+            if (++a.head == p.Hk) {
+                a.head = 0;
+                if (a.begin < units) tree_next_tile(p, a.t);
+            }
+        }
+        a.unit = 0;
+    }
+    return a;
+}
+// All threads of CTA `cta`: its share, into shared memory and the workspace.
+template <int THREADS>
+__device__ __forceinline__ void tree_share(const AttnParams& p, int cta, TreeShare& out, unsigned* error_word) {
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    // Inclusive sum over the block; `total` is the block's.
+    auto scan = [&](int64_t v, int64_t& total) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += y;
+        }
+        __syncthreads();
+        if (lane == 31) out.sums[w] = v;
+        __syncthreads();
+        int64_t before = 0;
+        total = 0;
+#pragma unroll
+        for (int i = 0; i < THREADS / 32; ++i) {
+            const int64_t s = out.sums[i];
+            if (i < w) before += s;
+            total += s;
+        }
+        return before + v;
+    };
+    TreeSeq s = {};
+    int64_t mine = 0, units = 0, upto = 0;
+    const bool once = p.B <= THREADS;
+    for (int b0 = 0; b0 < p.B; b0 += THREADS) {
+        const int b = b0 + tid;
+        mine = 0;
+        if (b < p.B) {
+            s = tree_seq(p, b);
+            if (!s.fits && cta == 0) atomicOr(error_word, ATTN_ERR_RANGE);
+            mine = s.units(p);
+        }
+        int64_t sum;
+        upto = units + scan(mine, sum);
+        units += sum;
+    }
+    int64_t per = (units + p.plan.ncta - 1) / p.plan.ncta;
+    if (per < 1) per = 1;
+    const int64_t u0 = min(cta * per, units), u1 = cta + 1 < p.plan.ncta ? min(u0 + per, units) : units;
+    if (tid == 0) {
+        out.per = per;
+        out.start = AttnStart{};
+        out.start.begin = out.start.end = units;
+    }
+    int64_t done = 0;
+    for (int b0 = 0; b0 < p.B; b0 += THREADS) {
+        const int b = b0 + tid;
+        if (!once) {
+            mine = 0;
+            if (b < p.B) {
+                s = tree_seq(p, b);
+                mine = s.units(p);
+            }
+            int64_t sum;
+            upto = done + scan(mine, sum);
+            done += sum;
+        }
+        __syncthreads();
+        // the end first, in its own field, which the start's thread does not touch
+        if (u1 < units && upto - mine <= u1 && u1 < upto) out.start.end = tree_border(p, s, b, upto - mine, u1, units, per).begin;
+        if (u0 < units && upto - mine <= u0 && u0 < upto) {
+            const AttnStart a = tree_border(p, s, b, upto - mine, u0, units, per);
+            out.start.begin = a.begin;
+            out.start.head = a.head;
+            out.start.unit = a.unit;
+            out.start.t = a.t;
+        }
+    }
+    __syncthreads();
+    if (tid == 0) {
+        reinterpret_cast<AttnStart*>(p.ws + p.plan.start_off)[cta] = out.start;
+        if (cta == 0) reinterpret_cast<AttnHead*>(p.ws)->per_cta = per;
+    }
+}
+
 // A CTA's pieces one after the other.
 struct AttnPiece {
     int64_t q0;
@@ -212,9 +380,10 @@ struct AttnWalk {
     int tile, head, unit;
     AttnTile t;
     __device__ __forceinline__ bool begin(const AttnParams& p, int cta) {
-        const AttnHead* h = attn_head(p);
-        const AttnStart s = attn_starts(p)[cta];
-        per = h->per_cta;
+        return begin(attn_starts(p)[cta], attn_head(p)->per_cta);
+    }
+    __device__ __forceinline__ bool begin(const AttnStart& s, int64_t per_cta) {
+        per = per_cta;
         at = s.begin;
         end = s.end;
         tile = s.tile;
@@ -244,7 +413,7 @@ struct AttnWalk {
                                  p.window, out.lo, out.hi);
             out.cnt = (t.cnt + head) * JOINS;
             out.slot = 2 * cta + (b0 > 0 ? 0 : 1);
-            if (!out.whole) {
+            if (!TREE && !out.whole) {   // who joins a tile's parts
                 const int64_t u0 = t.start + static_cast<int64_t>(head) * cost + lead, u1 = u0 + t.nblk - 1;
                 if (u1 >> 31 == 0) {   // the 64-bit division is a long subroutine
                     out.first_cta = static_cast<int>(static_cast<uint32_t>(u0) / static_cast<uint32_t>(per));
@@ -261,7 +430,10 @@ struct AttnWalk {
                 if (++head == p.Hk) {
                     head = 0;
                     ++tile;
-                    if (at < end) t = attn_tiles(p)[tile];
+                    if (at < end) {
+                        if (TREE) tree_next_tile(p, t);
+                        else t = attn_tiles(p)[tile];
+                    }
                 }
             }
             if (b1 > b0) return true;

@@ -334,15 +334,24 @@ attn_cc_kernel(const AttnParams p) {
     const int cta = blockIdx.x;
     if (TREE) ptx::griddep_launch_dependents();
     ptx::griddep_wait();
-    if (!attn_plan_agrees<TREE>(p)) {
-        if (threadIdx.x == 0) atomicOr(&g_attn_error, ATTN_ERR_RANGE);
-        return;
-    }
     AttnWalk walk;
-    if (!walk.begin(p, cta)) return;
+    if constexpr (TREE) {
+        __shared__ TreeShare share;
+        tree_share<TY * 16>(p, cta, share, &g_attn_error);
+        if (!walk.begin(share.start, share.per)) return;
+    } else {
+        if (!attn_plan_agrees(p)) {
+            if (threadIdx.x == 0) atomicOr(&g_attn_error, ATTN_ERR_RANGE);
+            return;
+        }
+        if (!walk.begin(p, cta)) return;
+    }
     AttnPiece pc;
     while (walk.next<TREE>(p, cta, pc)) {
-        if (RPT > 1 && pc.qlen * p.G - pc.row0 <= TY) cc_piece<TA, DP, TY, 1, TREE>(p, pc, Qs, Ps, Ks, Vs, &s_last, s_drafted);
+        const int rows = pc.qlen * p.G - pc.row0;
+        if (RPT > 1 && rows <= TY) cc_piece<TA, DP, TY, 1, TREE>(p, pc, Qs, Ps, Ks, Vs, &s_last, s_drafted);
+        else if (TREE && RPT > 2 && rows <= 2 * TY) cc_piece<TA, DP, TY, 2, TREE>(p, pc, Qs, Ps, Ks, Vs, &s_last, s_drafted);
+        else if (TREE && RPT > 3 && rows <= 3 * TY) cc_piece<TA, DP, TY, 3, TREE>(p, pc, Qs, Ps, Ks, Vs, &s_last, s_drafted);
         else cc_piece<TA, DP, TY, RPT, TREE>(p, pc, Qs, Ps, Ks, Vs, &s_last, s_drafted);
         __syncthreads();
     }

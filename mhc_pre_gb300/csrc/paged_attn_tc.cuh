@@ -119,7 +119,8 @@ template <int DP> struct Cfg {
     static constexpr int ML = MISC + 16;                               // lane 1's maxima and sums
     static constexpr int PIECE = ML + 2 * ROWS * 4;
     static constexpr int SEEN = PIECE + PIECES * PIECE_BYTES;
-    static constexpr int TOTAL = SEEN + PIECES * static_cast<int>(sizeof(TreeSeen));
+    static constexpr int SHARE = SEEN + PIECES * static_cast<int>(sizeof(TreeSeen));
+    static constexpr int TOTAL = SHARE + static_cast<int>(sizeof(TreeShare));
     static constexpr int SMEM = 232448;                                // all that a block may have
     static_assert(TOTAL <= SMEM, "shared memory of one SM");
 };
@@ -329,6 +330,14 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
         const int lo_most = same(__reduce_max_sync(FULL, lo)), hi_least = same(__reduce_min_sync(FULL, hi));
         const int lo_least = same(__reduce_min_sync(FULL, valid ? lo : 0x7fffffff));
         const int hi_most = same(TREE ? pc.hi : __reduce_max_sync(FULL, valid ? hi : 0));
+        const Seen<TREE> see = {lo, hi, lo_least, lo_most, hi_least, hi_most, node};
+        // a tree's bits of the lane's last block, usually the only one that needs any, come with the queries
+        uint32_t last_bits[4] = {FULL, FULL, FULL, FULL};
+        if (TREE && active && mine > 0) {
+            const int k0 = (blk + (pair ? mine - 1 : 2 * (mine - 1) + L)) * KEYS;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) last_bits[c] = see.bits(k0 + 32 * c);
+        }
         float m = -INFINITY, l = 0.0f;
         if (lent) {
             ok = wait_warp(bar(C::B_XE + w4), par_x, abort_flag);
@@ -339,10 +348,8 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
         for (int i = 0; ok && i < mine; ++i) {
             const int k0 = (blk + (pair ? i : 2 * i + L)) * KEYS;
             const bool partial = k0 < lo_most || k0 + KEYS > hi_least;
-            const Seen<TREE> see = {lo, hi, lo_least, lo_most, hi_least, hi_most, node};
-            // a tree's bits are on their way while the scores are being formed
-            uint32_t tree_bits[4] = {FULL, FULL, FULL, FULL};
-            if (TREE && active && partial) {
+            uint32_t tree_bits[4] = {last_bits[0], last_bits[1], last_bits[2], last_bits[3]};
+            if (TREE && active && partial && i + 1 < mine) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tree_bits[c] = see.bits(k0 + 32 * c);
             }
@@ -714,13 +721,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
         if (tid == 0 && ptx::forced_wait_runs_out(sbase, 100000ull)) {
             atomicOr(&g_attn_tc_error, ATTN_ERR_TIMEOUT);
             ptx::griddep_wait();   // the plan is written
-            attn_plan_spent(p);
+            if (!TREE) attn_plan_spent(p);
         }
         __syncthreads();
         return;
     }
     if ((sbase & 1023u) != 0) {   // the swizzle needs it; dynamic shared memory starts there without static arrays
         if (tid == 0) atomicOr(&g_attn_tc_error, ATTN_ERR_TIMEOUT);
+        if (TREE && tid == 0) reinterpret_cast<AttnStart*>(p.ws + p.plan.start_off)[cta] = AttnStart{};   // nothing to join
         return;
     }
     if (tid == 0) {
@@ -764,9 +772,16 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
     ptx::griddep_wait();   // the plan, the queries and the cache are written
 
     AttnWalk walk;
-    const bool begun = walk.begin(p, cta), agrees = attn_plan_agrees<TREE>(p);   // one round of loads
-    if (!agrees && tid == 0) atomicOr(&g_attn_tc_error, ATTN_ERR_RANGE);
-    const bool work = agrees && begun;
+    bool work;
+    if constexpr (TREE) {
+        TreeShare& share = *reinterpret_cast<TreeShare*>(smem + C::SHARE);
+        tree_share<NTHREADS>(p, cta, share, &g_attn_tc_error);
+        work = walk.begin(share.start, share.per);
+    } else {
+        const bool begun = walk.begin(p, cta), agrees = attn_plan_agrees(p);   // one round of loads
+        if (!agrees && tid == 0) atomicOr(&g_attn_tc_error, ATTN_ERR_RANGE);
+        work = agrees && begun;
+    }
     if (warp >= LOAD_WARP) {
         ptx::regs_dec<OTHER_REGS>();
         Pieces<DP> pieces(smem, sbase, abort_flag);
@@ -893,10 +908,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
                                                                             : pc.nb) {
                     const int k0 = (pc.blk + j) * KEYS;
                     const bool listed = TREE && j >= tail;
+                    uint4 seen = make_uint4(FULL, FULL, FULL, FULL);
                     if (listed) {
-                        const uint32_t blank = pieces.seen(ok).blank;
+                        const TreeSeen& list = pieces.seen(ok);
                         if (!ok) break;
-                        if (!(blank >> (j - tail) & 1u)) continue;
+                        if (!(list.blank >> (j - tail) & 1u)) continue;
+                        seen = *reinterpret_cast<const uint4*>(list.keys[j - tail]);
                     } else if (!partly_seen(k0, tlo, thi)) {
                         continue;
                     }
@@ -914,11 +931,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
                         const int c = lane % LPR;
 #pragma unroll
                         for (int w = 0; w < 4; ++w) {
-                            const uint32_t seen = pieces.seen(ok).keys[j - tail][w];
-                            if (seen == FULL) continue;
+                            const uint32_t bits = w == 0 ? seen.x : w == 1 ? seen.y : w == 2 ? seen.z : seen.w;
+                            if (bits == FULL) continue;
 #pragma unroll
                             for (int r = lane / LPR; r < 32; r += 32 / LPR)
-                                if (!(seen >> r & 1u))
+                                if (!(bits >> r & 1u))
                                     *reinterpret_cast<uint4*>(rows + (c >> 3) * SUB + (32 * w + r) * 128 + (c & 7) * 16) =
                                         make_uint4(0u, 0u, 0u, 0u);
                         }
@@ -1081,7 +1098,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
     }
     __syncthreads();
     if (*abort_flag) {
-        if (tid == 0) attn_plan_spent(p);
+        if (!TREE && tid == 0) attn_plan_spent(p);
         // let copies already issued land before the shared memory goes away
         const uint64_t t0 = ptx::globaltimer();
         while (ptx::globaltimer() - t0 < 20000ull) {

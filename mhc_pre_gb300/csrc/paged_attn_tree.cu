@@ -5,8 +5,8 @@
 // taken), in any order.  Node i sees every cached token before the new ones, and
 // of the new ones those whose bits its row of the mask has:
 //   z_ij = scale <q_i, k_j> over those keys,  o_i = sum_j softmax(z_i)_j v_j.
-// All nodes read the same context, so the tiles, the plan and the kernels are
-// those of a causal chunk; only the blocks with drafted tokens differ: there a
+// All nodes read the same context, so the tiles and the kernels are those of a
+// causal chunk (with each CTA finding its own share: tree_share); only the blocks with drafted tokens differ: there a
 // row's bits take the place of the diagonal, 32 keys to a word, and values that no
 // row of a tile sees are zeroed like those past a sequence's end.
 //
@@ -76,7 +76,6 @@ __global__ void __launch_bounds__(JOIN_THREADS)
 tree_join_kernel(const AttnParams p) {
     constexpr int N = DP / 32;
     ptx::griddep_wait();
-    if (!attn_plan_agrees<true>(p)) return;   // the kernel before has said so
     const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (c + 1 >= p.plan.ncta) return;
     const AttnStart s = attn_starts(p)[c + 1];   // where this CTA's share ends
@@ -163,7 +162,8 @@ cudaError_t launch_tree_attn(bool bf16, const AttnParams& p, cudaStream_t s) {
         g_error_word.may_be_set();
         e = bf16 ? attn::launch_cc_dp<__nv_bfloat16, true>(p, s) : attn::launch_cc_dp<float, true>(p, s);
     }
-    if (e != cudaSuccess) return e;
+    // (a forced timeout leaves no shares to join)
+    if (e != cudaSuccess || p.force_timeout != 0u) return e;
     return bf16 ? attn::launch_tree_join<__nv_bfloat16>(p, s) : attn::launch_tree_join<float>(p, s);
 }
 

@@ -650,7 +650,7 @@ PyObject* paged_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return arguments(n, 14) ? attn(a, nullptr) : nullptr;
     END_HANDLE_TH_ERRORS
 }
-// The same, and the mask as the last argument.
+// The same without a planned workspace, and the mask as the last argument.
 PyObject* tree_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     return arguments(n, 15) ? attn(a, a[14]) : nullptr;

@@ -198,28 +198,24 @@ def test_masks_that_are_parts_of_wider_ones(dtype):
     assert torch.equal(r.o, want.o) and torch.equal(r.lse, want.lse)
 
 
+def test_many_sequences():
+    """More sequences than a CTA has threads, which each find their share: some
+    with nothing, some with numbers that do not fit."""
+    rng = np.random.default_rng(0)
+    lens = [(int(n), int(n + m)) for n, m in zip(rng.integers(0, 4, 1500), rng.integers(0, 40, 1500))]
+    for dtype in ("bf16", "f32"):
+        c = Trees(lens, 2, 1, 64, 16, dtype, "tree")
+        c.check(c.run())
+        c.kv[700] = -3
+        c.check(c.run(), only=[0, 1, 2, 699, 701, 1498, 1499], error=B.MHC_ERR_RANGE)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_a_plan_serves_many_trees(dtype):
-    c = Trees([(13, 3000), (40, 900), (0, 5), (1, 1)], 10, 2, 64, 64, dtype, "tree")
-    plan = B.mhc_tree_attn_plan(c.cu, c.kv, DT[dtype], c.T, 10, 2, 64, 64, c.most, c.table.shape[1] * 64)
-    for kind in ("tree", "any"):
-        d = Trees(c.lens, 10, 2, 64, 64, dtype, kind)
-        want = d.run()
-        r = B.mhc_tree_attn(d.q, d.k, d.v, d.table, d.tree, plan=plan)
-        assert torch.equal(r.o, want.o) and torch.equal(r.lse, want.lse)
-    with pytest.raises(ValueError):
-        B.mhc_tree_attn(c.q, c.k, c.v, c.table, c.tree, plan=plan, window=64)
-    with pytest.raises(TypeError):
-        B.mhc_paged_attn(c.q, c.k, c.v, c.table, plan=plan)
-    causal = B.mhc_paged_attn_plan(c.cu, c.kv, DT[dtype], c.T, 10, 2, 64, 64, c.most, c.table.shape[1] * 64)
-    with pytest.raises(TypeError):
-        B.mhc_tree_attn(c.q, c.k, c.v, c.table, c.tree, plan=causal)
-    # the same workspace handed over as the other kind: the device says so and computes nothing
-    out = torch.full(c.q.shape, 9.0, dtype=c.q.dtype, device=c.q.device)
-    B.mhc_tree_attn(c.q, c.k, c.v, c.table, c.tree, plan=B.TreeAttnPlan(*causal), out=out)
-    assert B.get_last_device_error() == B.MHC_ERR_RANGE and bool((out == 9.0).all())
-    B.mhc_paged_attn(c.q, c.k, c.v, c.table, plan=B.PagedAttnPlan(*plan), out=out)
-    assert B.get_last_device_error() == B.MHC_ERR_RANGE and bool((out == 9.0).all())
+@pytest.mark.parametrize("n", [1, 12, 25, 26, 50, 51, 90])
+def test_short_contexts_in_great_number(n, dtype):
+    """Tiles far smaller than a CTA's share, whole and with borders moved."""
+    c = Trees([(n, n + 3 * (i % 50)) for i in range(120)], 5, 1, 64, 16, dtype, "tree")
+    c.check(c.run())
 
 
 def test_padding_rows_stay_and_out_is_taken():

@@ -21,7 +21,8 @@ def _call(L, **o):                                        # noqa: F811
 @pytest.mark.parametrize("bad,status", BAD_HEADS + [
     (dict(q=None), INV), (dict(tree=None), INV), (dict(tree=A + 2), MIS), (dict(trs=0), INV), (dict(mq=33), INV),
     (dict(mq=1025, trs=33), UNS), (dict(trs=(1 << 36) + 1), UNS), (dict(pt=None), INV), (dict(o=None), INV),
-    (dict(ws=None), INV), (dict(n=100), INV), (dict(cu=None), INV), (dict(scale=0.0), INV),
+    (dict(ws=None), INV), (dict(n=100), INV), (dict(cu=None), INV), (dict(kv=None), INV),
+    (dict(cu=None, kv=None), INV), (dict(kv=A + 2), MIS), (dict(scale=0.0), INV),
     (dict(cap=float("nan")), INV), (dict(window=-1), INV), (dict(mkv=65), INV), (dict(mkv=1 << 31), UNS)])
 def test_refusals(L, bad, status):                        # noqa: F811
     assert _call(L, **bad) == status
@@ -30,18 +31,6 @@ def test_refusals(L, bad, status):                        # noqa: F811
 def test_of_nothing(L):                                   # noqa: F811
     assert _call(L, T=0, q=None, tree=None) == OK
     assert _call(L, B=0, pt=None) == OK
-
-
-def test_plan_refusals(L):                                # noqa: F811
-    def plan(**o):
-        a = dict(dt=B.MHC_BF16, cu=A, kv=A, T=4, B=2, Hq=8, Hk=2, Dh=64, ps=16, mq=4, mkv=64, window=0, ws=A,
-                 n=1 << 30)
-        a.update(o)
-        return L.mhc_tree_attn_plan(*a.values(), None)
-    for bad, status in BAD_HEADS + [(dict(cu=None), INV), (dict(ws=None), INV), (dict(n=10), INV),
-                                    (dict(ws=A + 4), MIS), (dict(mq=1025), UNS)]:
-        assert plan(**bad) == status, bad
-    assert plan(T=0, cu=None) == OK
 
 
 def test_binding_refuses_what_it_cannot_pass_on(L):       # noqa: F811
