@@ -33,8 +33,12 @@ constexpr unsigned ATTN_ERR_TIMEOUT = 1u, ATTN_ERR_RANGE = 2u;
 // Most new tokens of a sequence that is a tree.
 constexpr int TREE_MOST = 1024;
 
-// Tiles below 1/8 of a CTA's share are not split.
-constexpr int ATTN_SMALL_TILE = 8;
+// Tiles below 1/8 of a CTA's share are not split.  Of trees, whose parts have many
+// rows to write and join, those below 1/3, and a tile's fixed cost counts as 3 units:
+// 64 sequences of 8 drafted and 1000 cached tokens take 60 us, 70 with 1/4 or 1/6
+// (47 and 60 with heads of 64); fixed costs of 1, 2 and 5 are 0 to 6 % slower or
+// faster, case by case.
+constexpr int ATTN_SMALL_TILE = 8, TREE_SMALL_TILE = 3, TREE_LEAD = 3;
 
 // Join counters of a tile and key head: each warp's rows are joined by
 // themselves.
@@ -190,12 +194,16 @@ struct AttnNode {
             lo = max(0, min(ctx, ctx - p.window + max(path, 1)));
         }
     }
-    // Which of the 32 keys from g that lie at ctx or later it sees (bits of keys before ctx are 0).
-    __device__ __forceinline__ uint32_t drafted(int g) const {
-        const int from = g - ctx;
-        if (from <= -32) return 0u;
-        if (from < 0) return word(0) << -from;
-        return __funnelshift_r(word(from >> 5), word((from >> 5) + 1), from & 31);
+    // Which of the 32 N keys from g that lie at ctx or later it sees (bits of keys
+    // before ctx are 0).  The words come in one round of loads.
+    template <int N>
+    __device__ __forceinline__ void drafted(int g, uint32_t (&out)[N]) const {
+        const int from = g - ctx, w0 = from >> 5;   // rounded down: the first word may be one before the first
+        uint32_t w[N + 1];
+#pragma unroll
+        for (int i = 0; i <= N; ++i) w[i] = word(w0 + i);
+#pragma unroll
+        for (int i = 0; i < N; ++i) out[i] = __funnelshift_r(w[i], w[i + 1], from & 31);
     }
 };
 
@@ -251,6 +259,12 @@ __device__ __forceinline__ void tree_next_tile(const AttnParams& p, AttnTile& t)
     t.seq = p.B;
 }
 
+// a / b for a >= 0, b > 0 with a quotient of 32 bits: the 64-bit division is a long subroutine.
+__device__ __forceinline__ int tree_divide(int64_t a, int64_t b) {
+    if (((a | b) >> 31) == 0) return static_cast<int>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
+    return static_cast<int>(a / b);
+}
+
 // What the CTAs of a launch leave for the joins, and how a CTA finds its share: in
 // place of a plan, each CTA sums up the units of all sequences (a scan of a few
 // numbers each) and finds its two borders among them.  The sums cost it less than
@@ -266,14 +280,14 @@ __device__ __forceinline__ AttnStart tree_border(const AttnParams& p, const Tree
                                                  int64_t units, int64_t per) {
     const int cost = s.nblk + p.plan.lead;
     const int64_t in = u - base, row = static_cast<int64_t>(p.Hk) * cost;
-    const int tile = static_cast<int>(in / row);
+    const int tile = tree_divide(in, row);
     const int left = static_cast<int>(in - tile * row);
     AttnStart a = {};
     a.head = left / cost;
     a.unit = left - a.head * cost;
     a.t = s.tile(p, b, tile, base + tile * row);
     a.begin = u;
-    if (a.unit > 0 && static_cast<int64_t>(cost) * ATTN_SMALL_TILE <= per) {
+    if (a.unit > 0 && static_cast<int64_t>(cost) * TREE_SMALL_TILE <= per) {
         if (2 * a.unit < cost) {
             a.begin -= a.unit;
         } else {
@@ -288,8 +302,9 @@ __device__ __forceinline__ AttnStart tree_border(const AttnParams& p, const Tree
     return a;
 }
 // All threads of CTA `cta`: its share, into shared memory and the workspace.
+// `least`: units that a CTA has at least.
 template <int THREADS>
-__device__ __forceinline__ void tree_share(const AttnParams& p, int cta, TreeShare& out, unsigned* error_word) {
+__device__ __forceinline__ void tree_share(const AttnParams& p, int cta, int least, TreeShare& out, unsigned* error_word) {
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     // Inclusive sum over the block; `total` is the block's.
     auto scan = [&](int64_t v, int64_t& total) {
@@ -326,8 +341,9 @@ __device__ __forceinline__ void tree_share(const AttnParams& p, int cta, TreeSha
         upto = units + scan(mine, sum);
         units += sum;
     }
-    int64_t per = (units + p.plan.ncta - 1) / p.plan.ncta;
-    if (per < 1) per = 1;
+    int64_t per = units >> 31 == 0 ? static_cast<int64_t>(tree_divide(units + p.plan.ncta - 1, p.plan.ncta))
+                                   : (units + p.plan.ncta - 1) / p.plan.ncta;
+    if (per < least) per = least;
     const int64_t u0 = min(cta * per, units), u1 = cta + 1 < p.plan.ncta ? min(u0 + per, units) : units;
     if (tid == 0) {
         out.per = per;

@@ -200,8 +200,7 @@ __device__ __forceinline__ void cc_piece(const AttnParams& p, const AttnPiece& p
                 n.words = p.tree + (pc.q0 + attn_token(p, pc.row0 + ty + TY * a)) * p.tree_stride;
                 n.ctx = pc.kvlen - pc.qlen;
                 n.nodes = n.ctx >= 0 ? pc.qlen : 0;
-                node[0] = n.drafted(k0);
-                node[1] = n.drafted(k0 + 32);
+                n.drafted(k0, node);
             }
 #pragma unroll
             for (int j = 0; j < CC_KPT; ++j) {
@@ -337,7 +336,7 @@ attn_cc_kernel(const AttnParams p) {
     AttnWalk walk;
     if constexpr (TREE) {
         __shared__ TreeShare share;
-        tree_share<TY * 16>(p, cta, share, &g_attn_error);
+        tree_share<TY * 16>(p, cta, 1, share, &g_attn_error);
         if (!walk.begin(share.start, share.per)) return;
     } else {
         if (!attn_plan_agrees(p)) {

@@ -257,6 +257,15 @@ __device__ __forceinline__ void mask32(uint32_t* u, uint32_t seen, uint32_t with
 }
 
 // The keys [lo, hi) that a row sees, and the bounds of its warp's rows.
+// Trees of drafted tokens (TREE): every row of a tile sees the context, and of the
+// drafted tokens those whose bits it has; the walking warp lists ahead which of
+// them some row sees, and the blanking warp zeroes the others.  Tried and not kept:
+// the bits of a piece's last block loaded at its start (B64 below 69 -> 71 us), the
+// queries' copies in another warp than the keys' (69 -> 75), both lanes' sums read
+// from tensor memory at once (69 -> 74: registers), blocks brought into L2 ahead of
+// the ring (25 tokens over 8192 keys, 32 sequences: 188 -> 244).  B64: 64 sequences
+// of 8 drafted and 1000 cached tokens.
+//
 // A tree's row sees the keys [lo, node.ctx) and some of those up to hi, the
 // sequence's last; hi_least and hi_most are then the least ctx and the last key.
 template <bool TREE> struct Seen {
@@ -268,14 +277,18 @@ template <bool TREE> struct Seen {
     __device__ __forceinline__ bool all(int g) const { return g >= lo_most && g + 32 <= hi_least; }
     __device__ __forceinline__ uint32_t bits(int g) const {
         const int from = max(lo - g, 0), to = min(hi - g, 32);
-        if (TREE) {
-            // keys from ctx on by their bits, the others by lo
-            const uint32_t low = from < 32 ? FULL << from : 0u;
-            const int later = node.ctx - g;
-            if (later >= 32) return low;
-            return later > 0 ? (low & ~(FULL << later)) | node.drafted(g) : node.drafted(g);
-        }
         return from < to ? (FULL << from) & (FULL >> (32 - to)) : 0u;
+    }
+    // The same of the 128 keys from k0, of a tree: keys from ctx on by their bits, the others by lo.
+    __device__ __forceinline__ void tree_bits(int k0, uint32_t (&out)[4]) const {
+        node.drafted(k0, out);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int g = k0 + 32 * c, from = max(lo - g, 0), later = node.ctx - g;
+            const uint32_t low = from < 32 ? FULL << from : 0u;
+            if (later >= 32) out[c] = low;
+            else if (later > 0) out[c] |= low & ~(FULL << later);
+        }
     }
 };
 template <bool V> struct Flag { static constexpr bool value = V; };
@@ -331,13 +344,6 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
         const int lo_least = same(__reduce_min_sync(FULL, valid ? lo : 0x7fffffff));
         const int hi_most = same(TREE ? pc.hi : __reduce_max_sync(FULL, valid ? hi : 0));
         const Seen<TREE> see = {lo, hi, lo_least, lo_most, hi_least, hi_most, node};
-        // a tree's bits of the lane's last block, usually the only one that needs any, come with the queries
-        uint32_t last_bits[4] = {FULL, FULL, FULL, FULL};
-        if (TREE && active && mine > 0) {
-            const int k0 = (blk + (pair ? mine - 1 : 2 * (mine - 1) + L)) * KEYS;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) last_bits[c] = see.bits(k0 + 32 * c);
-        }
         float m = -INFINITY, l = 0.0f;
         if (lent) {
             ok = wait_warp(bar(C::B_XE + w4), par_x, abort_flag);
@@ -348,11 +354,9 @@ __device__ __forceinline__ void softmax_lanes(const AttnParams& p, unsigned char
         for (int i = 0; ok && i < mine; ++i) {
             const int k0 = (blk + (pair ? i : 2 * i + L)) * KEYS;
             const bool partial = k0 < lo_most || k0 + KEYS > hi_least;
-            uint32_t tree_bits[4] = {last_bits[0], last_bits[1], last_bits[2], last_bits[3]};
-            if (TREE && active && partial && i + 1 < mine) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tree_bits[c] = see.bits(k0 + 32 * c);
-            }
+            // a tree's bits come while the scores are being formed
+            uint32_t tree_bits[4] = {FULL, FULL, FULL, FULL};
+            if (TREE && active && partial) see.tree_bits(k0, tree_bits);
             auto bits = [&](int c) {
                 if (!TREE) return see.bits(k0 + 32 * c);
                 return c < 2 ? (c == 0 ? tree_bits[0] : tree_bits[1]) : (c == 2 ? tree_bits[2] : tree_bits[3]);
@@ -686,8 +690,10 @@ __device__ __forceinline__ void tree_seen(const AttnParams& p, const AttnPiece& 
             n.words = p.tree + (pc.q0 + t) * p.tree_stride;
             n.ctx = ctx;
             n.nodes = ctx >= 0 ? pc.qlen : 0;
+            uint32_t bits[4];
+            n.drafted(k0, bits);
 #pragma unroll
-            for (int w = 0; w < 4; ++w) seen[w] |= n.drafted(k0 + 32 * w);
+            for (int w = 0; w < 4; ++w) seen[w] |= bits[w];
         }
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
@@ -775,7 +781,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
     bool work;
     if constexpr (TREE) {
         TreeShare& share = *reinterpret_cast<TreeShare*>(smem + C::SHARE);
-        tree_share<NTHREADS>(p, cta, share, &g_attn_tc_error);
+        tree_share<NTHREADS>(p, cta, 2, share, &g_attn_tc_error);   // a block for each lane
         work = walk.begin(share.start, share.per);
     } else {
         const bool begun = walk.begin(p, cta), agrees = attn_plan_agrees(p);   // one round of loads

@@ -25,7 +25,12 @@ cudaError_t read_and_clear_attn_tree_error(unsigned* word) { return g_error_word
 
 namespace attn {
 
-constexpr int JOIN_THREADS = 128, JOIN_WARPS = JOIN_THREADS / 32, JOIN_SPLIT = 16, JOIN_AHEAD = 8;
+// Rows that a warp has on their way together, parts of each, blocks of a tile.  Of
+// 1 and 2 rows with 4, 8 and 16 parts and 4 to 32 blocks these are within 3 % of the
+// best for 11 batches of all kinds; 8 parts or more cost registers, and with them
+// blocks of an SM (2 rows, 8 parts: 104 -> 111 us for 32 sequences of up to 8192),
+// 4 blocks of a tile leave too little in flight (37 -> 87 us in the worst case).
+constexpr int JOIN_THREADS = 128, JOIN_WARPS = JOIN_THREADS / 32, JOIN_ROWS = 2, JOIN_AHEAD = 4, JOIN_SPLIT = 16;
 
 // N consecutive floats of a part.
 template <int N> struct Floats {
@@ -67,79 +72,100 @@ template <int N> struct Floats {
 };
 
 // Block (c, y): of the tile and head whose first part is CTA c's (a CTA has at
-// most one such, its last piece), a share of the rows, a warp for each.  Lane j
-// takes the maximum and the sum of the j-th part, so that all weights come from
-// one round of loads; then the lanes have DP/32 values of the row each and the
-// parts are added in their order, JOIN_AHEAD of them on their way together.
+// most one such, its last piece), a share of the rows, JOIN_ROWS at a time for a
+// warp.  Lane j takes the maximum and the sum of the j-th part, so that all weights
+// come from one round of loads; then the lanes have DP/32 values of each row and
+// the parts are added in their order, JOIN_AHEAD of them on their way together.
 template <typename TA, int DP>
-__global__ void __launch_bounds__(JOIN_THREADS)
+__global__ void __launch_bounds__(JOIN_THREADS, DP <= 128 ? 8 : 4)
 tree_join_kernel(const AttnParams p) {
-    constexpr int N = DP / 32;
+    constexpr int N = DP / 32, R = JOIN_ROWS;
     ptx::griddep_wait();
     const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (c + 1 >= p.plan.ncta) return;
-    const AttnStart s = attn_starts(p)[c + 1];   // where this CTA's share ends
-    const int cost = s.t.nblk + p.plan.lead;
+    const AttnStart& s = attn_starts(p)[c + 1];   // where this CTA's share ends
     if (s.begin >= s.end || s.unit <= p.plan.lead) return;   // no tile goes on there
     const int64_t per = attn_head(p)->per_cta;
-    const int64_t u0 = s.t.start + static_cast<int64_t>(s.head) * cost + p.plan.lead;
-    const int first = static_cast<int>(u0 / per), last = static_cast<int>((u0 + s.t.nblk - 1) / per);
+    const int64_t u0 = s.t.start + static_cast<int64_t>(s.head) * (s.t.nblk + p.plan.lead) + p.plan.lead;
+    const int first = tree_divide(u0, per), last = tree_divide(u0 + s.t.nblk - 1, per);
     if (first != c || last == first) return;
     const int rows = min(p.plan.tile_rows, s.t.qlen * p.G - s.t.row0), sr = p.plan.slot_rows;
     auto part = [&](int j) { return attn_slot(p, 2 * j + (j == first ? 1 : 0)); };
-    for (int row = blockIdx.y * JOIN_WARPS + warp; row < rows; row += gridDim.y * JOIN_WARPS) {
-        float M = -INFINITY, l = 0.0f;
-        Floats<N> a;
+    for (int r0 = (blockIdx.y * JOIN_WARPS + warp) * R; r0 < rows; r0 += gridDim.y * JOIN_WARPS * R) {
+        float M[R], l[R];
+        Floats<N> a[R];
 #pragma unroll
-        for (int i = 0; i < N; ++i) a.v[i] = 0.0f;
+        for (int i = 0; i < R; ++i) {
+            M[i] = -INFINITY;
+            l[i] = 0.0f;
+#pragma unroll
+            for (int e = 0; e < N; ++e) a[i].v[e] = 0.0f;
+        }
         for (int c0 = first; c0 <= last; c0 += 32) {
             const int n = min(32, last - c0 + 1);
-            const float* stat = part(c0 + min(lane, n - 1)) + static_cast<int64_t>(sr) * DP + row;
-            float w = lane < n ? __ldcg(stat) : -INFINITY;
-            const float pl = lane < n ? __ldcg(stat + sr) : 0.0f;
-            Floats<N> x[JOIN_AHEAD];
+            const float* stat = part(c0 + min(lane, n - 1)) + static_cast<int64_t>(sr) * DP;
+            float w[R], pl[R];
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int row = min(r0 + i, rows - 1);
+                w[i] = lane < n ? __ldcg(stat + row) : -INFINITY;
+                pl[i] = lane < n ? __ldcg(stat + sr + row) : 0.0f;
+            }
+            Floats<N> x[JOIN_AHEAD][R];
             auto fetch = [&](int j0) {
 #pragma unroll
-                for (int u = 0; u < JOIN_AHEAD; ++u)
-                    x[u].load(part(c0 + min(j0 + u, n - 1)) + static_cast<int64_t>(row) * DP + lane * N);
+                for (int u = 0; u < JOIN_AHEAD; ++u) {
+                    const float* base = part(c0 + min(j0 + u, n - 1)) + lane * N;
+#pragma unroll
+                    for (int i = 0; i < R; ++i) x[u][i].load(base + static_cast<int64_t>(min(r0 + i, rows - 1)) * DP);
+                }
             };
             fetch(0);   // on their way with the weights
-            float top = w;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            top = fmaxf(top, M);
-            const float base = top == -INFINITY ? 0.0f : top, keep = ex2(M - base);
-            w = ex2(w - base);
-            l = fmaf(l, keep, warp_sum(pl * w));
-            M = top;
+            for (int i = 0; i < R; ++i) {
+                float top = w[i];
 #pragma unroll
-            for (int i = 0; i < N; ++i) a.v[i] *= keep;
+                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                top = fmaxf(top, M[i]);
+                const float base = top == -INFINITY ? 0.0f : top, keep = ex2(M[i] - base);
+                w[i] = ex2(w[i] - base);
+                l[i] = fmaf(l[i], keep, warp_sum(pl[i] * w[i]));
+                M[i] = top;
+#pragma unroll
+                for (int e = 0; e < N; ++e) a[i].v[e] *= keep;
+            }
             for (int j0 = 0; j0 < n; j0 += JOIN_AHEAD) {
                 if (j0 > 0) fetch(j0);
 #pragma unroll
-                for (int u = 0; u < JOIN_AHEAD; ++u) {
-                    const float f = __shfl_sync(0xffffffffu, w, min(j0 + u, 31));
-                    if (j0 + u < n)
+                for (int u = 0; u < JOIN_AHEAD; ++u)
 #pragma unroll
-                        for (int i = 0; i < N; ++i) a.v[i] = fmaf(x[u].v[i], f, a.v[i]);
-                }
+                    for (int i = 0; i < R; ++i) {
+                        const float f = __shfl_sync(0xffffffffu, w[i], min(j0 + u, 31));
+                        if (j0 + u < n)
+#pragma unroll
+                            for (int e = 0; e < N; ++e) a[i].v[e] = fmaf(x[u][i].v[e], f, a[i].v[e]);
+                    }
             }
         }
-        const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-        const int r = s.t.row0 + row, tok = attn_token(p, r);
-        const int64_t out = (s.t.q0 + tok) * p.Hq + s.head * p.G + (r - tok * p.G);
 #pragma unroll
-        for (int i = 0; i < N; ++i) a.v[i] *= inv;
-        if (lane * N < p.Dh) a.store(static_cast<TA*>(p.o) + out * p.Dh + lane * N);   // heads are multiples of 8
-        if (lane == 0 && p.lse != nullptr) p.lse[out] = attn_lse(M, l);
+        for (int i = 0; i < R; ++i) {
+            if (r0 + i >= rows) break;
+            const float inv = l[i] != 0.0f ? 1.0f / l[i] : 0.0f;
+            const int r = s.t.row0 + r0 + i, tok = attn_token(p, r);
+            const int64_t out = (s.t.q0 + tok) * p.Hq + s.head * p.G + (r - tok * p.G);
+#pragma unroll
+            for (int e = 0; e < N; ++e) a[i].v[e] *= inv;
+            if (lane * N < p.Dh) a[i].store(static_cast<TA*>(p.o) + out * p.Dh + lane * N);   // heads are multiples of 8
+            if (lane == 0 && p.lse != nullptr) p.lse[out] = attn_lse(M[i], l[i]);
+        }
     }
 }
 
 template <typename TA>
 cudaError_t launch_tree_join(const AttnParams& p, cudaStream_t s) {
-    const int most = (p.plan.slot_rows + JOIN_WARPS - 1) / JOIN_WARPS;
+    if (p.plan.ncta < 2) return cudaSuccess;
+    const int most = (p.plan.slot_rows + JOIN_WARPS * JOIN_ROWS - 1) / (JOIN_WARPS * JOIN_ROWS);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.plan.ncta), static_cast<unsigned>(most < JOIN_SPLIT ? most : JOIN_SPLIT));
+    cfg.gridDim = dim3(static_cast<unsigned>(p.plan.ncta - 1), static_cast<unsigned>(most < JOIN_SPLIT ? most : JOIN_SPLIT));
     cfg.blockDim = dim3(JOIN_THREADS);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
