@@ -483,7 +483,7 @@ static mhc_status attn_call(mhc_dtype dt, const void* q, int64_t q_stride, const
     p.softcap = softcap;
     p.force_timeout = mhc::forced_timeout();
     p.plan = plan;
-    if (trees) p.plan.lead = mhc::TREE_LEAD;
+    if (trees) p.plan.lead = plan.block_keys == 128 ? mhc::TREE_LEAD : mhc::TREE_LEAD_CC;
     return from_cuda(trees ? mhc::launch_tree_attn(dt == MHC_BF16, p, stream)
                            : mhc::launch_paged_attn(dt == MHC_BF16, p, stream));
 }

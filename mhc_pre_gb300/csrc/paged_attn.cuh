@@ -37,8 +37,9 @@ constexpr int TREE_MOST = 1024;
 // rows to write and join, those below 1/3, and a tile's fixed cost counts as 3 units:
 // 64 sequences of 8 drafted and 1000 cached tokens take 60 us, 70 with 1/4 or 1/6
 // (47 and 60 with heads of 64); fixed costs of 1, 2 and 5 are 0 to 6 % slower or
-// faster, case by case.
-constexpr int ATTN_SMALL_TILE = 8, TREE_SMALL_TILE = 3, TREE_LEAD = 3;
+// faster, case by case.  On the CUDA cores, where a block takes much longer, 1 unit:
+// 4 sequences of 30 and 2000 in float32 119 us, 123, 134 and 134 with 0, 2 and 3.
+constexpr int ATTN_SMALL_TILE = 8, TREE_SMALL_TILE = 3, TREE_LEAD = 3, TREE_LEAD_CC = 1;
 
 // Join counters of a tile and key head: each warp's rows are joined by
 // themselves.

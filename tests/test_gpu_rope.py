@@ -53,7 +53,9 @@ def _check(got, x, R, dtype):
 
 
 SHAPES = [(1, 40, 8, 128, 128), (5, 4, 4, 64, 32), (131, 6, 2, 96, 48), (33, 3, 1, 256, 256), (64, 1, 1, 24, 16),
-          (1700, 40, 8, 128, 64), (6500, 2, 1, 64, 64), (400, 64, 8, 256, 256), (24500, 2, 1, 64, 32)]
+          (1700, 40, 8, 128, 64), (6500, 2, 1, 64, 64), (400, 64, 8, 256, 256), (24500, 2, 1, 64, 32),
+          (5000, 40, 8, 128, 128), (5000, 12, 4, 96, 96), (4900, 6, 3, 96, 48), (5100, 2, 2, 256, 256),
+          (9001, 3, 3, 24, 16), (5000, 33, 3, 40, 32)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -80,11 +82,15 @@ def test_forward_backward_append(T, Hq, Hk, dh, rot, adjacent, dtype):
         want = torch.zeros_like(c).flatten(0, 1)
         want[slots[keep]] = src[keep]
         assert torch.equal(c.flatten(0, 1), want)
+    # caches with the heads outside
+    outside = [torch.zeros(pages, Hk, 16, dh, dtype=q.dtype, device=q.device).transpose(1, 2) for _ in range(2)]
+    B.mhc_rope_append(q, k, v, *outside, slots, **kw)
+    assert all(torch.equal(a, b) for a, b in zip(outside, caches))
     assert B.get_last_device_error() == B.MHC_OK
 
 
 @pytest.mark.parametrize("adjacent", [False, True])
-@pytest.mark.parametrize("T", [3, 1700])
+@pytest.mark.parametrize("T", [3, 1700, 5000])
 def test_the_backward_is_the_transpose(T, adjacent):
     """<g, R x> = <R^T g, x>, and its change with x: the operator is linear, so a
     difference of any step is the gradient.  Sums of N products of size 1.6 in
