@@ -436,7 +436,7 @@ CALLS_PATH = os.path.join(os.path.dirname(LIB_PATH), "_attn_calls.so")
 CALLS_ENTRIES = ("mhc_qk_norm_rope", "mhc_qk_norm_rope_bwd", "mhc_qk_norm_rope_bwd_workspace_bytes",
                  "mhc_qk_norm_rope_append", "mhc_paged_attn", "mhc_paged_attn_workspace_bytes",
                  "mhc_rope", "mhc_rope_bwd", "mhc_rope_append", "mhc_tree_attn",
-                 "mhc_paged_step", "mhc_cache_keep")
+                 "mhc_paged_step", "mhc_cache_keep", "mhc_rope_table")
 _calls_module = None
 
 
@@ -505,15 +505,16 @@ def mhc_rope_table(n: int, rot: int, base: float = 10000.0, factor: float = 1.0,
     trained one; ``original`` 0 slows every pair down by it, a trained length
     only the pairs that make fewer than ``high`` turns over it (all of it below
     ``low`` turns).  ``device``: a CUDA device (default: the current one)."""
-    dev = torch.device("cuda" if device is None else device)
-    if dev.type != "cuda":
-        raise ValueError("the mHC library takes CUDA tensors only")
-    if n < 0 or rot < 0:
-        raise ValueError(f"a table of {n} positions and {rot} values")
-    out = _empty((n, rot), dtype=torch.float32, device=dev)
-    with torch.cuda.device(out.device):
-        st = lib().mhc_rope_table(n, rot, base, factor, original, low, high, amplitude, _ptr(out), _stream(out.device))
-    _check(st, "mhc_rope_table")
+    index = -1
+    if device is not None:
+        dev = torch.device(device)
+        if dev.type != "cuda":
+            raise ValueError("the mHC library takes CUDA tensors only")
+        index = -1 if dev.index is None else dev.index
+    st, out = (_calls_module or _calls()).rope_table(_allocator(), index, n, rot, base, factor, original, low, high,
+                                                     amplitude)
+    if st:
+        _check(st, "mhc_rope_table")
     return out
 
 

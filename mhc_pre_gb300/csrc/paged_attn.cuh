@@ -282,10 +282,10 @@ __device__ __forceinline__ AttnStart tree_border(const AttnParams& p, const Tree
     const int cost = s.nblk + p.plan.lead;
     const int64_t in = u - base, row = static_cast<int64_t>(p.Hk) * cost;
     const int tile = tree_divide(in, row);
-    const int left = static_cast<int>(in - tile * row);
+    const int64_t left = in - tile * row;
     AttnStart a = {};
-    a.head = left / cost;
-    a.unit = left - a.head * cost;
+    a.head = tree_divide(left, cost);
+    a.unit = static_cast<int>(left - static_cast<int64_t>(a.head) * cost);
     a.t = s.tile(p, b, tile, base + tile * row);
     a.begin = u;
     if (a.unit > 0 && static_cast<int64_t>(cost) * TREE_SMALL_TILE <= per) {

@@ -13,7 +13,6 @@
 #include <stdint.h>
 
 #include "launch.h"
-#include "mhc_common.cuh"
 #include "paged_attn.cuh"
 
 namespace mhc {
@@ -27,70 +26,77 @@ cudaError_t read_and_clear_keep_error(unsigned* word) { return g_error_word.read
 namespace keep {
 
 constexpr int THREADS = 128, HELD = 8;   // 16-byte pieces of a thread: 16 KB of a block in flight
+constexpr int ROWS = THREADS;            // of a path, looked up together
 
 __global__ void __launch_bounds__(THREADS)
 keep_kernel(const __grid_constant__ KeepParams p) {
+    __shared__ int64_t from[ROWS], to[ROWS];   // byte offsets in the cache, -1: a page outside it
     const int b = static_cast<int>(blockIdx.x), cache = static_cast<int>(blockIdx.y), tid = threadIdx.x;
     const bool values = cache >= p.layers;
+    const int32_t* path = p.path + b * p.path_stride;
+    // the path's first entries are on their way before its length is known
+    int mine = tid < p.max_keep ? path[tid] : 0, before = tid > 0 && tid < p.max_keep ? path[tid - 1] : -1;
     const int n = p.cu_q[b + 1] - p.cu_q[b], m = p.kv_lens[b], c = p.keep[b];
     if (c == 0) return;   // nothing moves, its length stays
-    const int32_t* path = p.path + b * p.path_stride;
     bool bad = c < 0 || c > p.max_keep || n < 0 || m < n || m > p.max_kv || c > n;
-    int moved = 0;        // path entries of this thread that do not stay
     if (!bad)
         for (int d = tid; d < c; d += THREADS) {
-            const int at = path[d], before = d > 0 ? path[d - 1] : -1;
-            bad = bad || at <= before || at >= n;
-            moved += at != d;
+            const int at = d == tid ? mine : path[d], prev = d == tid ? before : path[d - 1];
+            bad = bad || at <= prev || at >= n;
         }
-    __shared__ int s_moved;
-    if (tid == 0) s_moved = 0;
     if (__syncthreads_or(bad)) {
         if (tid == 0 && cache == 0) atomicOr(&g_keep_error, ATTN_ERR_RANGE);
         return;
     }
-    if (moved > 0) atomicAdd(&s_moved, moved);
-    __syncthreads();
-    // once an entry has moved all later ones have
-    const int first = c - s_moved, ctx = m - n;
+    const int ctx = m - n;
     if (p.lens != nullptr && cache == 0 && tid == 0) p.lens[b] = ctx + c;
+    // once an entry has moved all later ones have: the first ones stay
+    int first = 0;
+    for (int d0 = 0; d0 < c; d0 += THREADS) first += __syncthreads_count(d0 + tid < c && (d0 == 0 ? mine : path[d0 + tid]) == d0 + tid);
     char* base = static_cast<char*>(values ? p.v[cache - p.layers] : p.k[cache]);
     const int64_t page_bytes = values ? p.v_page : p.k_page, slot_bytes = values ? p.v_slot : p.k_slot;
     const int64_t head_bytes = values ? p.v_head : p.k_head;
     const int32_t* table = p.table + b * p.table_stride;
-    // a token's row in the cache, null for a page number outside it
-    auto row = [&](int token) -> char* {
+    auto place = [&](int token) -> int64_t {
         const int pg = p.page_shift >= 0 ? token >> p.page_shift : token / p.page;
         const int page = __ldg(table + pg);
-        if (page < 0 || page >= p.num_pages) return nullptr;
-        return base + page * page_bytes + (token - pg * p.page) * slot_bytes;
+        if (page < 0 || page >= p.num_pages) {
+            atomicOr(&g_keep_error, ATTN_ERR_RANGE);
+            return -1;
+        }
+        return page * page_bytes + (token - pg * p.page) * slot_bytes;
     };
-    const int per = p.row_pieces;   // pieces of a token
-    const int64_t total = static_cast<int64_t>(c - first) * per;
-    for (int64_t i0 = 0; i0 < total; i0 += THREADS * HELD) {
-        uint4 held[HELD];
-        char* to[HELD];
-#pragma unroll
-        for (int u = 0; u < HELD; ++u) {
-            const int64_t i = i0 + u * THREADS + tid;
-            to[u] = nullptr;
-            if (i < total) {
-                const int d = first + static_cast<int>(i / per), piece = static_cast<int>(i % per);
-                const char* from = row(ctx + path[d]);
-                char* goal = row(ctx + d);
-                const int64_t in = (piece / p.head_pieces) * head_bytes + (piece % p.head_pieces) * 16;
-                if (from != nullptr && goal != nullptr) {
-                    held[u] = *reinterpret_cast<const uint4*>(from + in);
-                    to[u] = goal + in;
-                } else {
-                    atomicOr(&g_keep_error, ATTN_ERR_RANGE);
-                }
-            }
+    const uint32_t per = static_cast<uint32_t>(p.row_pieces), head = static_cast<uint32_t>(p.head_pieces);
+    for (int d0 = first; d0 < c; d0 += ROWS) {
+        const int rows = min(ROWS, c - d0);
+        if (tid < rows) {
+            const int64_t f = place(ctx + path[d0 + tid]), t = place(ctx + d0 + tid);
+            from[tid] = t >= 0 ? f : -1;
+            to[tid] = t;
         }
         __syncthreads();
+        const uint32_t total = static_cast<uint32_t>(rows) * per;
+        for (uint32_t i0 = 0; i0 < total; i0 += THREADS * HELD) {
+            uint4 held[HELD];
+            char* goal[HELD];
 #pragma unroll
-        for (int u = 0; u < HELD; ++u)
-            if (to[u] != nullptr) *reinterpret_cast<uint4*>(to[u]) = held[u];
+            for (int u = 0; u < HELD; ++u) {
+                const uint32_t i = i0 + u * THREADS + tid;
+                goal[u] = nullptr;
+                if (i < total) {
+                    const uint32_t d = i / per, piece = i - d * per, h = piece / head;
+                    const int64_t f = from[d], in = h * head_bytes + (piece - h * head) * 16u;
+                    if (f >= 0) {
+                        held[u] = *reinterpret_cast<const uint4*>(base + f + in);
+                        goal[u] = base + to[d] + in;
+                    }
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < HELD; ++u)
+                if (goal[u] != nullptr) *reinterpret_cast<uint4*>(goal[u]) = held[u];
+        }
     }
 }
 

@@ -25,7 +25,6 @@
 #include <atomic>
 
 #include "launch.h"
-#include "mhc_common.cuh"
 #include "paged_attn.cuh"
 #include "tc_ptx.cuh"
 
@@ -39,10 +38,9 @@ cudaError_t read_and_clear_step_error(unsigned* word) { return g_error_word.read
 
 namespace step {
 
-constexpr int THREADS = 1024, WARPS = THREADS / 32;
-
 // Inclusive sums over the block of three values each; `carry` is added to and
 // becomes the sums so far.
+template <int WARPS>
 __device__ __forceinline__ void scan3(int64_t (&v)[3], int64_t (&carry)[3], int64_t (*warp_sums)[3]) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
 #pragma unroll
@@ -59,18 +57,17 @@ __device__ __forceinline__ void scan3(int64_t (&v)[3], int64_t (&carry)[3], int6
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-        int64_t s = warp_sums[lane][i];   // WARPS is 32
+        int64_t s = lane < WARPS ? warp_sums[lane][i] : 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
+        for (int o = 1; o < WARPS; o <<= 1) {
             const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
             if (lane >= o) s += y;
         }
         const int64_t before = __shfl_sync(0xffffffffu, s, w > 0 ? w - 1 : 0);
         v[i] += carry[i] + (w > 0 ? before : 0);
-        carry[i] += __shfl_sync(0xffffffffu, s, 31);
+        carry[i] += __shfl_sync(0xffffffffu, s, WARPS - 1);
     }
 }
-static_assert(WARPS == 32, "scan3");
 
 // The last of entries [0, n) that is at most x; entry 0 is.
 __device__ __forceinline__ int last_at_most(const int* a, int n, int x) {
@@ -87,71 +84,65 @@ __device__ __forceinline__ int last_at_most(const int* a, int n, int x) {
     return lo;
 }
 
-// What a sequence asks for, from its own numbers alone.
-struct Ask {
-    int64_t rows, need;   // tokens of the step, pages that it has not got
-    int back;             // pages that it gives back
-    bool over, good;      // it ends; its numbers fit
-};
-__device__ __forceinline__ Ask ask_of(const StepParams& p, int b) {
-    const int n = p.new_lens[b], m = p.lens[b], h = p.held[b];
-    Ask a;
-    a.over = n == -1;
-    a.good = h >= 0 && h <= p.width;
-    if (!a.over)
-        a.good = a.good && n >= 0 && m >= 0 && static_cast<int64_t>(h) * p.page >= m &&
-                 static_cast<int64_t>(m) + n <= p.width * p.page && static_cast<int64_t>(m) + n <= p.max_len;
-    a.rows = n > 0 ? min(static_cast<int64_t>(n), p.T + 1) : 0;
-    a.need = a.good && !a.over ? max(int64_t(0), (static_cast<int64_t>(m) + n + p.page - 1) / p.page - h) : 0;
-    a.back = a.good && a.over ? h : 0;
-    return a;
-}
+// Five numbers of each sequence in shared memory.
+constexpr int NUMBERS = 5;
+constexpr int BAD = -1, OVER = -2;   // in place of its cached tokens: its numbers do not fit, it ends
 
+template <int THREADS>
 __global__ void __launch_bounds__(THREADS)
 step_kernel(const StepParams p) {
     extern __shared__ int smem[];
     int* cu = smem;                    // [B + 1] first rows (more than T: does not fit the call)
     int* upto = cu + p.B + 1;          // [B + 1] missing pages of the sequences before
     int* back = upto + p.B + 1;        // [B + 1] pages given back by the sequences before
-    __shared__ int64_t warp_sums[WARPS][3];
-    __shared__ int s_rows, s_take;
+    int* cached = back + p.B + 1;      // [B] tokens, BAD or OVER
+    int* holds = cached + p.B + 1;     // [B] pages
+    __shared__ int64_t warp_sums[THREADS / 32][3];
     const int tid = threadIdx.x, rank = static_cast<int>(blockIdx.x), ctas = static_cast<int>(gridDim.x);
-    if (tid == 0) {
-        cu[0] = upto[0] = back[0] = 0;
-        s_rows = s_take = 0;
-    }
     const int raw = *p.free_count;
+    if (tid == 0) cu[0] = upto[0] = back[0] = 0;
     int64_t carry[3] = {0, 0, 0};
     for (int b0 = 0; b0 < p.B; b0 += THREADS) {
         const int b = b0 + tid;
-        int64_t v[3] = {0, 0, 0};
+        int64_t v[3] = {0, 0, 0};      // rows, missing pages, pages given back
         if (b < p.B) {
-            const Ask a = ask_of(p, b);
-            if (!a.good && rank == 0) atomicOr(&g_step_error, ATTN_ERR_RANGE);
-            v[0] = a.rows;
-            v[1] = a.need;
-            v[2] = a.back;
+            const int n = p.new_lens[b], m = p.lens[b], h = p.held[b];
+            const bool over = n == -1;
+            bool good = h >= 0 && h <= p.width;
+            if (!over) {
+                const int64_t all = static_cast<int64_t>(m) + n;
+                good = good && n >= 0 && m >= 0 && static_cast<int64_t>(h) * p.page >= m && all <= p.width * p.page &&
+                       all <= p.max_len;
+            }
+            if (!good && rank == 0) atomicOr(&g_step_error, ATTN_ERR_RANGE);
+            v[0] = n > 0 ? min(static_cast<int64_t>(n), p.T + 1) : 0;
+            if (good && !over) {       // m + n is below 2^31 - 256
+                const uint32_t last = static_cast<uint32_t>(m + n) + static_cast<uint32_t>(p.page - 1);
+                const int pages = static_cast<int>(p.page_shift >= 0 ? last >> p.page_shift : last / static_cast<uint32_t>(p.page));
+                v[1] = max(0, pages - h);
+            }
+            v[2] = good && over ? h : 0;
+            cached[b] = !good ? BAD : over ? OVER : m;
+            holds[b] = h;
         }
-        scan3(v, carry, warp_sums);
+        scan3<THREADS / 32>(v, carry, warp_sums);
         if (b < p.B) {
             cu[b + 1] = static_cast<int>(min(v[0], p.T + 1));
             upto[b + 1] = static_cast<int>(v[1]);
             back[b + 1] = static_cast<int>(v[2]);
-            if (v[0] <= p.T) atomicMax(&s_rows, static_cast<int>(v[0]));
-            else if (rank == 0) atomicOr(&g_step_error, ATTN_ERR_RANGE);
         }
     }
     __syncthreads();
+    // All three sums rise, so what fits is found by bisection: sequences whose rows
+    // fit, their rows, the pages that those of them take which get what they miss.
     const int count = max(0, min(raw, p.cap));
     const int avail = static_cast<int>(min(static_cast<int64_t>(count) + back[p.B], static_cast<int64_t>(p.cap)));
-    if (rank == 0 && tid == 0 && (raw != count || static_cast<int64_t>(count) + back[p.B] > p.cap))
+    const int fit = cu[p.B] <= p.T ? p.B : last_at_most(cu, p.B + 1, static_cast<int>(p.T));
+    const int rows = cu[fit];
+    const int take = upto[fit] <= avail ? upto[fit] : upto[last_at_most(upto, fit + 1, avail)];
+    if (rank == 0 && tid == 0 && (raw != count || static_cast<int64_t>(count) + back[p.B] > p.cap || fit < p.B))
         atomicOr(&g_step_error, ATTN_ERR_RANGE);
-    // Sequences whose rows fit and whose pages are there; of those that miss pages they are the first.
-    auto served = [&](int b) { return cu[b + 1] <= p.T && (upto[b + 1] == upto[b] || upto[b + 1] <= avail); };
-    for (int b = tid; b < p.B; b += THREADS)
-        if (upto[b + 1] > upto[b] && served(b)) atomicMax(&s_take, upto[b + 1]);
-    __syncthreads();
-    const int rows = s_rows, take = s_take;
+    auto served = [&](int b) { return b < fit && (upto[b + 1] == upto[b] || upto[b + 1] <= avail); };
     // the i-th page that came back, the k-th from the top of the list with those on it
     auto returned = [&](int i) {
         const int b = last_at_most(back, p.B + 1, i);
@@ -171,17 +162,18 @@ step_kernel(const StepParams p) {
         uint32_t bits = 0u;
         if (t < rows) {
             const int b = last_at_most(cu, p.B + 1, static_cast<int>(t));
-            const int i = static_cast<int>(t) - cu[b], m = p.lens[b], h = p.held[b];
-            const bool good = ask_of(p, b).good;
+            const int i = static_cast<int>(t) - cu[b], m = cached[b], h = holds[b];
+            const bool good = m >= 0;   // (one that ends has no rows)
             pos = good ? m + i : 0;
-            if (good && served(b)) {
+            int page = 0, in = 0;
+            const bool room = good && served(b);
+            if (room) {   // on its way while the tree is climbed
                 const int at = p.page_shift >= 0 ? pos >> p.page_shift : pos / p.page;
-                const int page = at < h ? p.table[b * p.table_stride + at] : page_from_top(upto[b] + at - h);
-                if (page >= 0) slot = static_cast<int64_t>(page) * p.page + (pos - at * p.page);
-                else atomicOr(&g_step_error, ATTN_ERR_RANGE);
+                in = pos - at * p.page;
+                page = at < h ? p.table[b * p.table_stride + at] : page_from_top(upto[b] + at - h);
             }
             if (words != nullptr) {
-                // up the tree: numbers fall, so the words are finished from the last to the first
+                // numbers fall on the way up, so the words are finished from the last to the first
                 const int32_t* parents = p.parents + cu[b];
                 for (int node = i; node >= 0; ++path) {
                     if (node < 32 * p.words) {
@@ -202,6 +194,10 @@ step_kernel(const StepParams p) {
                 }
                 pos = good ? m + path - 1 : 0;
             }
+            if (room) {
+                if (page >= 0) slot = static_cast<int64_t>(page) * p.page + in;
+                else atomicOr(&g_step_error, ATTN_ERR_RANGE);
+            }
         }
         if (words != nullptr)
             for (; w >= 0; --w) {
@@ -214,51 +210,50 @@ step_kernel(const StepParams p) {
     // the missing pages into the table; those that came back and stay, onto the list
     for (int64_t k = me; k < take; k += all) {
         const int b = last_at_most(upto, p.B + 1, static_cast<int>(k));
-        p.table[b * p.table_stride + p.held[b] + (k - upto[b])] = page_from_top(static_cast<int>(k));
+        p.table[b * p.table_stride + holds[b] + (k - upto[b])] = page_from_top(static_cast<int>(k));
     }
     for (int64_t i = me; i < avail - take - count; i += all) p.free_pages[count + i] = returned(static_cast<int>(i));
-    for (int64_t b = me; b < p.B; b += all) {
-        const Ask a = ask_of(p, static_cast<int>(b));
-        p.cu_q[b + 1] = cu[b + 1] <= p.T ? cu[b + 1] : rows;
-        p.kv_lens[b] = a.over || !a.good ? 0 : p.lens[b] + (served(static_cast<int>(b)) ? p.new_lens[b] : 0);
-        if (b == 0) p.cu_q[0] = 0;
+    for (int64_t i = me; i < p.B; i += all) {
+        const int b = static_cast<int>(i), m = cached[b];
+        p.cu_q[b + 1] = b < fit ? cu[b + 1] : rows;
+        // a sequence without room has no new tokens; one with room its rows (of numbers that fit)
+        p.kv_lens[b] = m < 0 ? 0 : m + (served(b) ? cu[b + 1] - cu[b] : 0);
     }
-    if (p.B == 0 && me == 0) p.cu_q[0] = 0;
+    if (me == 0) p.cu_q[0] = 0;
     // every CTA has read held and the list's length
-    __syncwarp();
-    ptx::cluster_sync();
+    if (ctas > 1) {
+        __syncwarp();
+        ptx::cluster_sync();
+    } else {
+        __syncthreads();
+    }
     if (rank == 0) {
         for (int b = tid; b < p.B; b += THREADS) {
-            const Ask a = ask_of(p, b);
-            if (a.back > 0) p.held[b] = 0;
-            else if (upto[b + 1] > upto[b] && served(b)) p.held[b] += upto[b + 1] - upto[b];
+            if (back[b + 1] > back[b]) p.held[b] = 0;
+            else if (upto[b + 1] > upto[b] && served(b)) p.held[b] = holds[b] + upto[b + 1] - upto[b];
         }
         if (tid == 0) *p.free_count = avail - take;
     }
 }
 
-}  // namespace step
-
-cudaError_t launch_paged_step(const StepParams& p, cudaStream_t s) {
-    g_error_word.may_be_set();
+template <int THREADS>
+cudaError_t launch(const StepParams& p, unsigned ctas, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};   // devices whose kernel has its shared memory and clusters allowed
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
     if (bit == 0 || !(done.load() & bit)) {
-        e = cudaFuncSetAttribute(step::step_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 3 * (STEP_SEQUENCES + 1) * static_cast<int>(sizeof(int)));
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(step::step_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        e = cudaFuncSetAttribute(step_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 NUMBERS * (STEP_SEQUENCES + 1) * static_cast<int>(sizeof(int)));
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(step_kernel<THREADS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
         done.fetch_or(bit);
     }
-    unsigned ctas = 1;
-    while (ctas < 16 && static_cast<int64_t>(ctas) * step::THREADS < p.T) ctas *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(step::THREADS);
-    cfg.dynamicSmemBytes = 3u * static_cast<size_t>(p.B + 1) * sizeof(int);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = static_cast<size_t>(NUMBERS) * static_cast<size_t>(p.B + 1) * sizeof(int);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -266,8 +261,20 @@ cudaError_t launch_paged_step(const StepParams& p, cudaStream_t s) {
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, step::step_kernel, p);
+    cfg.numAttrs = ctas > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, step_kernel<THREADS>, p);
+}
+
+}  // namespace step
+
+// One CTA of 256 threads where that is a thread for each token and sequence, else
+// 1024 threads in as many CTAs as the tokens fill, up to 16.
+cudaError_t launch_paged_step(const StepParams& p, cudaStream_t s) {
+    g_error_word.may_be_set();
+    if (p.T <= 256 && p.B <= 256) return step::launch<256>(p, 1, s);
+    unsigned ctas = 1;
+    while (ctas < 16 && static_cast<int64_t>(ctas) * 1024 < p.T) ctas *= 2;
+    return step::launch<1024>(p, ctas, s);
 }
 
 }  // namespace mhc

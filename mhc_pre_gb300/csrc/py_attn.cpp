@@ -15,6 +15,7 @@
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <initializer_list>
@@ -48,6 +49,7 @@ struct Library {
     decltype(&mhc_tree_attn) tree_attn;
     decltype(&mhc_paged_step) paged_step;
     decltype(&mhc_cache_keep) cache_keep;
+    decltype(&mhc_rope_table) rope_table;
 };
 Library lib = {};
 constexpr int ENTRIES = sizeof(Library) / sizeof(void*);
@@ -497,6 +499,53 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+bool to_double(PyObject* o, double* out) {
+    *out = PyFloat_AsDouble(o);
+    return *out != -1.0 || !PyErr_Occurred();
+}
+
+// (empty, device, n, rot, base, factor, original, low, high, amplitude) -> (status, table); device: its
+// index, or -1 for the current one
+PyObject* rope_table(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!arguments(n, 10)) return nullptr;
+    int64_t shape[2];
+    int device;
+    double v[5];
+    float amplitude;
+    if (!to_int(a[1], &device) || !to_i64(a[2], &shape[0]) || !to_i64(a[3], &shape[1]) || !to_float(a[9], &amplitude))
+        return nullptr;
+    for (int i = 0; i < 5; ++i)
+        if (!to_double(a[4 + i], &v[i])) return nullptr;
+    if (shape[0] < 0 || shape[1] < 0) {
+        PyErr_Format(PyExc_ValueError, "a table of %lld positions and %lld values", static_cast<long long>(shape[0]),
+                     static_cast<long long>(shape[1]));
+        return nullptr;
+    }
+    c10::cuda::OptionalCUDAGuard guard;
+    if (device >= 0) guard.set_index(static_cast<c10::DeviceIndex>(device));
+    else device = c10::cuda::current_device();
+    Ref table;
+    if (a[0] == Py_None) {
+        table.reset(THPVariable_Wrap(at::empty(c10::IntArrayRef(shape, 2),
+                                               at::TensorOptions().dtype(ScalarType::Float).device(c10::kCUDA, static_cast<c10::DeviceIndex>(device)))));
+    } else {
+        Ref torch(PyImport_ImportModule("torch"));
+        if (!torch) return nullptr;
+        Ref kind(PyObject_GetAttrString(torch.get(), "float32")), dims(Py_BuildValue("LL", static_cast<long long>(shape[0]), static_cast<long long>(shape[1])));
+        Ref where(PyUnicode_FromFormat("cuda:%d", device));
+        if (!kind || !dims || !where) return nullptr;
+        PyObject* args[3] = {dims.get(), kind.get(), where.get()};
+        table.reset(PyObject_Vectorcall(a[0], args, 3, nullptr));
+    }
+    const at::Tensor* t;
+    if (!table || !tensor_of(table.get(), "a new tensor", &t)) return nullptr;
+    const int st = lib.rope_table(shape[0], clip(shape[1]), v[0], v[1], v[2], v[3], v[4], amplitude,
+                                  static_cast<float*>(t->data_ptr()), stream_of(table.get()));
+    return Py_BuildValue("iO", st, table.get());
+    END_HANDLE_TH_ERRORS
+}
+
 // (empty, q, k, v, k_cache, v_cache, slots, positions, cos_sin, flags) -> (status, q_out)
 PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -804,6 +853,7 @@ PyObject* cache_keep(PyObject*, PyObject* const* a, Py_ssize_t n) {
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(bind), FAST(qk_norm_rope), FAST(qk_norm_rope_bwd), FAST(qk_norm_rope_append), FAST(paged_attn),
                          FAST(rope), FAST(rope_append), FAST(tree_attn), FAST(paged_step), FAST(cache_keep),
+                         FAST(rope_table),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_attn_calls", "Marshalling of the attention sublayer's calls.", -1,
                       methods, nullptr, nullptr, nullptr, nullptr};

@@ -151,6 +151,10 @@ def test_the_most_sequences():
     rng = np.random.default_rng(6)
     s = Server(8192, 64, 4, 3000, rng, most=200)
     s.step([1] * 8192)
+    s = Server(8192, 64, 4, 3000, rng, most=200)
+    new = [int(n) for n in rng.integers(0, 5, 8192)]
+    s.step(new, parents=[p for n in new for p in random_parents(rng, n)], words=1)
+    assert B.get_last_device_error() == B.MHC_OK
     with pytest.raises(B.MhcError):
         Server(8193, 64, 4, 10, rng, most=200).step([1] * 8193)
 

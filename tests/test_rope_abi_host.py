@@ -67,6 +67,8 @@ def test_binding_refuses_what_it_cannot_pass_on(L):       # noqa: F811
         B.mhc_rope(q.half(), k.half(), pos, cs)
     with pytest.raises(ValueError):
         B.mhc_rope_table(4, 64, device="cpu")
+    with pytest.raises(ValueError):
+        B.mhc_rope_table(-4, 64)
 
 
 def test_oracle_table():
