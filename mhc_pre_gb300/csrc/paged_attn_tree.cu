@@ -25,63 +25,62 @@ cudaError_t read_and_clear_attn_tree_error(unsigned* word) { return g_error_word
 
 namespace attn {
 
-// Rows that a warp has on their way together, parts of each, blocks of a tile.  Of
-// 1 and 2 rows with 4, 8 and 16 parts and 4 to 32 blocks these are within 3 % of the
-// best for 11 batches of all kinds; 8 parts or more cost registers, and with them
-// blocks of an SM (2 rows, 8 parts: 104 -> 111 us for 32 sequences of up to 8192),
-// 4 blocks of a tile leave too little in flight (37 -> 87 us in the worst case).
-constexpr int JOIN_THREADS = 128, JOIN_WARPS = JOIN_THREADS / 32, JOIN_ROWS = 2, JOIN_AHEAD = 4, JOIN_SPLIT = 16;
+// Lanes of a row, rows that a warp has side by side, parts on their way together,
+// blocks of a tile.
+constexpr int JOIN_THREADS = 128, JOIN_WARPS = JOIN_THREADS / 32, JOIN_LANES = 16, JOIN_ROWS = 32 / JOIN_LANES;
+constexpr int JOIN_AHEAD = 4, JOIN_SPLIT = 16;
 
-// N consecutive floats of a part.
+// N consecutive floats of a part, a multiple of 4.
 template <int N> struct Floats {
     float v[N];
     __device__ __forceinline__ void load(const float* p) {
-        if constexpr (N == 2) {
-            const float2 x = __ldcg(reinterpret_cast<const float2*>(p));
-            v[0] = x.x;
-            v[1] = x.y;
-        } else {
 #pragma unroll
-            for (int i = 0; i < N; i += 4) {
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(p + i));
-                v[i] = x.x;
-                v[i + 1] = x.y;
-                v[i + 2] = x.z;
-                v[i + 3] = x.w;
-            }
+        for (int i = 0; i < N; i += 4) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(p + i));
+            v[i] = x.x;
+            v[i + 1] = x.y;
+            v[i + 2] = x.z;
+            v[i + 3] = x.w;
         }
     }
-    __device__ __forceinline__ void store(float* p) const {
-        if constexpr (N == 2) *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
-        else
+    // From value `at` of a head of Dh, a multiple of 8, whose rest is not there.
+    __device__ __forceinline__ void store(float* head, int at, int Dh) const {
 #pragma unroll
-            for (int i = 0; i < N; i += 4)
-                *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        for (int i = 0; i < N; i += 4)
+            if (at + i < Dh) *reinterpret_cast<float4*>(head + at + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
     }
-    __device__ __forceinline__ void store(__nv_bfloat16* p) const {
+    __device__ __forceinline__ void store(__nv_bfloat16* head, int at, int Dh) const {
         uint32_t u[N / 2];
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
             const __nv_bfloat162 x = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
             u[i] = *reinterpret_cast<const uint32_t*>(&x);
         }
-        if constexpr (N == 2) *reinterpret_cast<uint32_t*>(p) = u[0];
-        else if constexpr (N == 4) *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
-        else *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+        if constexpr (N == 4) {
+            if (at < Dh) *reinterpret_cast<uint2*>(head + at) = make_uint2(u[0], u[1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; i += 8)
+                if (at + i < Dh)
+                    *reinterpret_cast<uint4*>(head + at + i) = make_uint4(u[i / 2], u[i / 2 + 1], u[i / 2 + 2], u[i / 2 + 3]);
+        }
     }
 };
 
 // Block (c, y): of the tile and head whose first part is CTA c's (a CTA has at
-// most one such, its last piece), a share of the rows, JOIN_ROWS at a time for a
-// warp.  Lane j takes the maximum and the sum of the j-th part, so that all weights
-// come from one round of loads; then the lanes have DP/32 values of each row and
+// most one such, its last piece), a share of the rows, two at a time for a warp.
+// Lane j of a row takes the maximum and the sum of its j-th part, so that all weights
+// come from one round of loads; then the lanes have DP/16 values of the row each and
 // the parts are added in their order, JOIN_AHEAD of them on their way together.
+// Bound by instructions as much as by reads: 16 sequences of 25 drafted and 8192 cached
+// tokens took 12 us at half the issue rate with a row for all 32 lanes.
 template <typename TA, int DP>
 __global__ void __launch_bounds__(JOIN_THREADS, DP <= 128 ? 8 : 4)
 tree_join_kernel(const AttnParams p) {
-    constexpr int N = DP / 32, R = JOIN_ROWS;
+    constexpr int N = DP / JOIN_LANES;
     ptx::griddep_wait();
     const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int sub = lane % JOIN_LANES, side = lane / JOIN_LANES;
     const AttnStart& s = attn_starts(p)[c + 1];   // where this CTA's share ends
     if (s.begin >= s.end || s.unit <= p.plan.lead) return;   // no tile goes on there
     const int64_t per = attn_head(p)->per_cta;
@@ -89,74 +88,61 @@ tree_join_kernel(const AttnParams p) {
     const int first = tree_divide(u0, per), last = tree_divide(u0 + s.t.nblk - 1, per);
     if (first != c || last == first) return;
     const int rows = min(p.plan.tile_rows, s.t.qlen * p.G - s.t.row0), sr = p.plan.slot_rows;
+    // the tile's parts, from the second on two slots apart
     auto part = [&](int j) { return attn_slot(p, 2 * j + (j == first ? 1 : 0)); };
-    for (int r0 = (blockIdx.y * JOIN_WARPS + warp) * R; r0 < rows; r0 += gridDim.y * JOIN_WARPS * R) {
-        float M[R], l[R];
-        Floats<N> a[R];
+    for (int r0 = (blockIdx.y * JOIN_WARPS + warp) * JOIN_ROWS; r0 < rows; r0 += gridDim.y * JOIN_WARPS * JOIN_ROWS) {
+        const int row = min(r0 + side, rows - 1);
+        const int stat = sr * DP + row, mine = row * DP + sub * N;   // in a part: below 2^31
+        float M = -INFINITY, l = 0.0f;
+        Floats<N> a;
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            M[i] = -INFINITY;
-            l[i] = 0.0f;
-#pragma unroll
-            for (int e = 0; e < N; ++e) a[i].v[e] = 0.0f;
-        }
-        for (int c0 = first; c0 <= last; c0 += 32) {
-            const int n = min(32, last - c0 + 1);
-            const float* stat = part(c0 + min(lane, n - 1)) + static_cast<int64_t>(sr) * DP;
-            float w[R], pl[R];
-#pragma unroll
-            for (int i = 0; i < R; ++i) {
-                const int row = min(r0 + i, rows - 1);
-                w[i] = lane < n ? __ldcg(stat + row) : -INFINITY;
-                pl[i] = lane < n ? __ldcg(stat + sr + row) : 0.0f;
-            }
-            Floats<N> x[JOIN_AHEAD][R];
+        for (int e = 0; e < N; ++e) a.v[e] = 0.0f;
+        for (int c0 = first; c0 <= last; c0 += JOIN_LANES) {
+            const int n = min(JOIN_LANES, last - c0 + 1);
+            const float* st = part(c0 + min(sub, n - 1)) + stat;
+            float w = sub < n ? __ldcg(st) : -INFINITY;
+            const float pl = sub < n ? __ldcg(st + sr) : 0.0f;
+            Floats<N> x[JOIN_AHEAD];
             auto fetch = [&](int j0) {
 #pragma unroll
-                for (int u = 0; u < JOIN_AHEAD; ++u) {
-                    const float* base = part(c0 + min(j0 + u, n - 1)) + lane * N;
-#pragma unroll
-                    for (int i = 0; i < R; ++i) x[u][i].load(base + static_cast<int64_t>(min(r0 + i, rows - 1)) * DP);
-                }
+                for (int u = 0; u < JOIN_AHEAD; ++u)
+                    if (j0 + u < n) x[u].load(part(c0 + j0 + u) + mine);
             };
             fetch(0);   // on their way with the weights
+            float top = w;
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-                float top = w[i];
+            for (int o = JOIN_LANES / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            top = fmaxf(top, M);
+            const float base = top == -INFINITY ? 0.0f : top, keep = ex2(M - base);
+            w = ex2(w - base);
+            float sum = pl * w;
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                top = fmaxf(top, M[i]);
-                const float base = top == -INFINITY ? 0.0f : top, keep = ex2(M[i] - base);
-                w[i] = ex2(w[i] - base);
-                l[i] = fmaf(l[i], keep, warp_sum(pl[i] * w[i]));
-                M[i] = top;
+            for (int o = JOIN_LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            l = fmaf(l, keep, sum);
+            M = top;
+            if (c0 > first) {
 #pragma unroll
-                for (int e = 0; e < N; ++e) a[i].v[e] *= keep;
+                for (int e = 0; e < N; ++e) a.v[e] *= keep;
             }
             for (int j0 = 0; j0 < n; j0 += JOIN_AHEAD) {
                 if (j0 > 0) fetch(j0);
 #pragma unroll
                 for (int u = 0; u < JOIN_AHEAD; ++u)
+                    if (j0 + u < n) {
+                        const float f = __shfl_sync(0xffffffffu, w, j0 + u, JOIN_LANES);
 #pragma unroll
-                    for (int i = 0; i < R; ++i) {
-                        const float f = __shfl_sync(0xffffffffu, w[i], min(j0 + u, 31));
-                        if (j0 + u < n)
-#pragma unroll
-                            for (int e = 0; e < N; ++e) a[i].v[e] = fmaf(x[u][i].v[e], f, a[i].v[e]);
+                        for (int e = 0; e < N; ++e) a.v[e] = fmaf(x[u].v[e], f, a.v[e]);
                     }
             }
         }
+        if (r0 + side >= rows) continue;
+        const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+        const int r = s.t.row0 + row, tok = attn_token(p, r);
+        const int64_t out = (s.t.q0 + tok) * p.Hq + s.head * p.G + (r - tok * p.G);
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            if (r0 + i >= rows) break;
-            const float inv = l[i] != 0.0f ? 1.0f / l[i] : 0.0f;
-            const int r = s.t.row0 + r0 + i, tok = attn_token(p, r);
-            const int64_t out = (s.t.q0 + tok) * p.Hq + s.head * p.G + (r - tok * p.G);
-#pragma unroll
-            for (int e = 0; e < N; ++e) a[i].v[e] *= inv;
-            if (lane * N < p.Dh) a[i].store(static_cast<TA*>(p.o) + out * p.Dh + lane * N);   // heads are multiples of 8
-            if (lane == 0 && p.lse != nullptr) p.lse[out] = attn_lse(M[i], l[i]);
-        }
+        for (int e = 0; e < N; ++e) a.v[e] *= inv;
+        a.store(static_cast<TA*>(p.o) + out * p.Dh, sub * N, p.Dh);
+        if (sub == 0 && p.lse != nullptr) p.lse[out] = attn_lse(M, l);
     }
 }
 
