@@ -1,5 +1,5 @@
 // attn_abi.cu -- the extern "C" entry points of the attention sublayer:
-// validation and dispatch only (qk_norm_rope.cu and paged_attn.cu compute).
+// validation and dispatch only (the qk_norm_rope and paged_attn files compute).
 // Nothing here allocates memory or synchronises the host.
 #include <math.h>
 

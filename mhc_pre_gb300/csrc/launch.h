@@ -113,8 +113,8 @@ inline int sm_count() {
 }
 
 // ---------------------------------------------------------------------------
-// The attention sublayer between mhc_pre and mhc_post (qk_norm_rope.cu,
-// paged_attn.cu, paged_attn_tc.cu).
+// The attention sublayer between mhc_pre and mhc_post (the qk_norm_rope and
+// paged_attn files).
 // ---------------------------------------------------------------------------
 
 // Per-head RMSNorm and rotation.  Strides are in elements; `v`, `slots` and

@@ -1,5 +1,5 @@
 // paged_attn.cu -- attention of a chunk of new tokens over a paged cache: the
-// plan kernel, the CUDA-core kernel, and the choice of kernel.
+// plan kernel, and the choice of kernel.
 //
 //   z[i, j] = scale <q_i, k_j>,  z = softcap tanh(z / softcap) when capped,
 //   keys j <= kvlen - qlen + i, and j > kvlen - qlen + i - window,

