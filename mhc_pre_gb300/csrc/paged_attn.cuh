@@ -267,12 +267,13 @@ __device__ __forceinline__ int tree_divide(int64_t a, int64_t b) {
 }
 
 // What the CTAs of a launch leave for the joins, and how a CTA finds its share: in
-// place of a plan, each CTA sums up the units of all sequences (a scan of a few
-// numbers each) and finds its two borders among them.  The sums cost it less than
-// reading a plan would, and there is no launch before it.
+// place of a plan, each CTA sums up the units and the tiles of all sequences and finds
+// its two borders among them.  That takes a microsecond more than reading a plan, and
+// a launch of five less.
 struct TreeShare {
     AttnStart start;
-    int64_t per, sums[32];
+    int64_t per, sums[32][2];
+    int most[32];
 };
 // The border at unit u of a batch of `units`, moved to the nearer end of a tile (of
 // one key head) that is not to be split; u lies in sequence b, whose first unit is
@@ -302,73 +303,122 @@ __device__ __forceinline__ AttnStart tree_border(const AttnParams& p, const Tree
     }
     return a;
 }
+// The border before the sequence's i-th tile and head.
+__device__ __forceinline__ AttnStart tree_border_whole(const AttnParams& p, const TreeSeq& s, int b, int64_t base, int i) {
+    const int cost = s.nblk + p.plan.lead, tile = i / p.Hk;
+    const int64_t start = base + static_cast<int64_t>(tile) * p.Hk * cost;
+    AttnStart a = {};
+    a.head = i - tile * p.Hk;
+    a.t = s.tile(p, b, tile, start);
+    a.begin = start + static_cast<int64_t>(a.head) * cost;
+    return a;
+}
 // All threads of CTA `cta`: its share, into shared memory and the workspace.
-// `least`: units that a CTA has at least.
+// `least`: units that a CTA has at least; `join`: what splitting tiles costs a call,
+// in units: where whole tiles dealt out by their number take no more than that above
+// an even share, none is split.
 template <int THREADS>
-__device__ __forceinline__ void tree_share(const AttnParams& p, int cta, int least, TreeShare& out, unsigned* error_word) {
+__device__ __forceinline__ void tree_share(const AttnParams& p, int cta, int least, int join, TreeShare& out,
+                                           unsigned* error_word) {
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-    // Inclusive sum over the block; `total` is the block's.
-    auto scan = [&](int64_t v, int64_t& total) {
+    struct Two {
+        int64_t units, tiles;   // tiles: of a key head each
+    };
+    // Inclusive sums over the block; `total` has the block's.
+    auto scan = [&](Two v, Two& total) {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v += y;
+            const int64_t y = __shfl_up_sync(0xffffffffu, v.units, o), z = __shfl_up_sync(0xffffffffu, v.tiles, o);
+            if (lane >= o) {
+                v.units += y;
+                v.tiles += z;
+            }
         }
         __syncthreads();
-        if (lane == 31) out.sums[w] = v;
+        if (lane == 31) {
+            out.sums[w][0] = v.units;
+            out.sums[w][1] = v.tiles;
+        }
         __syncthreads();
-        int64_t before = 0;
-        total = 0;
+        Two before = {0, 0};
+        total = {0, 0};
 #pragma unroll
         for (int i = 0; i < THREADS / 32; ++i) {
-            const int64_t s = out.sums[i];
-            if (i < w) before += s;
-            total += s;
+            const int64_t a = out.sums[i][0], b = out.sums[i][1];
+            if (i < w) {
+                before.units += a;
+                before.tiles += b;
+            }
+            total.units += a;
+            total.tiles += b;
         }
-        return before + v;
+        return Two{before.units + v.units, before.tiles + v.tiles};
     };
     TreeSeq s = {};
-    int64_t mine = 0, units = 0, upto = 0;
+    Two mine = {0, 0}, all = {0, 0}, upto = {0, 0};
+    int most = 0;               // units of the largest tile
     const bool once = p.B <= THREADS;
     for (int b0 = 0; b0 < p.B; b0 += THREADS) {
         const int b = b0 + tid;
-        mine = 0;
+        mine = {0, 0};
         if (b < p.B) {
             s = tree_seq(p, b);
             if (!s.fits && cta == 0) atomicOr(error_word, ATTN_ERR_RANGE);
-            mine = s.units(p);
+            mine = {s.units(p), static_cast<int64_t>(s.tiles) * p.Hk};
+            if (s.tiles > 0) most = max(most, s.nblk + p.plan.lead);
         }
-        int64_t sum;
-        upto = units + scan(mine, sum);
-        units += sum;
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 0) out.most[w] = most;   // (the scan's barriers are behind it)
+        Two sum;
+        const Two here = scan(mine, sum);
+        upto = {all.units + here.units, all.tiles + here.tiles};
+        all.units += sum.units;
+        all.tiles += sum.tiles;
     }
-    int64_t per = units >> 31 == 0 ? static_cast<int64_t>(tree_divide(units + p.plan.ncta - 1, p.plan.ncta))
-                                   : (units + p.plan.ncta - 1) / p.plan.ncta;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) most = max(most, p.B > 0 ? out.most[i] : 0);
+    const int ncta = p.plan.ncta;
+    int64_t per = all.units >> 31 == 0 ? static_cast<int64_t>(tree_divide(all.units + ncta - 1, ncta))
+                                       : (all.units + ncta - 1) / ncta;
     if (per < least) per = least;
-    const int64_t u0 = min(cta * per, units), u1 = cta + 1 < p.plan.ncta ? min(u0 + per, units) : units;
+    // (more than 31 bits of them only if sequences overlap)
+    const int n = all.tiles >> 31 == 0 ? static_cast<int>(all.tiles) : 0, deal = n / ncta, rest = n - deal * ncta;
+    const bool whole = n > 0 && static_cast<int64_t>(deal + (rest > 0 ? 1 : 0)) * most <= per + join;
+    // in units, or in tiles: the first `rest` CTAs have one more
+    const int64_t u0 = whole ? static_cast<int64_t>(cta) * deal + min(cta, rest) : min(cta * per, all.units);
+    const int64_t end = whole ? all.tiles : all.units;
+    const int64_t u1 = cta + 1 == ncta ? end : whole ? u0 + deal + (cta < rest ? 1 : 0) : min(u0 + per, all.units);
     if (tid == 0) {
         out.per = per;
         out.start = AttnStart{};
-        out.start.begin = out.start.end = units;
+        out.start.begin = out.start.end = all.units;
     }
-    int64_t done = 0;
+    Two done = {0, 0};
     for (int b0 = 0; b0 < p.B; b0 += THREADS) {
         const int b = b0 + tid;
         if (!once) {
-            mine = 0;
+            mine = {0, 0};
             if (b < p.B) {
                 s = tree_seq(p, b);
-                mine = s.units(p);
+                mine = {s.units(p), static_cast<int64_t>(s.tiles) * p.Hk};
             }
-            int64_t sum;
-            upto = done + scan(mine, sum);
-            done += sum;
+            Two sum;
+            const Two here = scan(mine, sum);
+            upto = {done.units + here.units, done.tiles + here.tiles};
+            done.units += sum.units;
+            done.tiles += sum.tiles;
         }
         __syncthreads();
+        const int64_t hi = whole ? upto.tiles : upto.units, lo = hi - (whole ? mine.tiles : mine.units);
+        const int64_t base = upto.units - mine.units;
+        auto border = [&](int64_t u) {
+            return whole ? tree_border_whole(p, s, b, base, static_cast<int>(u - lo))
+                         : tree_border(p, s, b, base, u, all.units, per);
+        };
         // the end first, in its own field, which the start's thread does not touch
-        if (u1 < units && upto - mine <= u1 && u1 < upto) out.start.end = tree_border(p, s, b, upto - mine, u1, units, per).begin;
-        if (u0 < units && upto - mine <= u0 && u0 < upto) {
-            const AttnStart a = tree_border(p, s, b, upto - mine, u0, units, per);
+        if (u1 < end && lo <= u1 && u1 < hi) out.start.end = border(u1).begin;
+        if (u0 < end && lo <= u0 && u0 < hi) {
+            const AttnStart a = border(u0);
             out.start.begin = a.begin;
             out.start.head = a.head;
             out.start.unit = a.unit;

@@ -336,7 +336,7 @@ attn_cc_kernel(const AttnParams p) {
     AttnWalk walk;
     if constexpr (TREE) {
         __shared__ TreeShare share;
-        tree_share<TY * 16>(p, cta, 1, share, &g_attn_error);
+        tree_share<TY * 16>(p, cta, 1, 0, share, &g_attn_error);   // a block takes longer than the joins
         if (!walk.begin(share.start, share.per)) return;
     } else {
         if (!attn_plan_agrees(p)) {

@@ -96,6 +96,13 @@ constexpr int NO_CAP = 0, LOW_CAP = 1, HIGH_CAP = 2, FAR_CAP = 3;
 constexpr float LOW_MOST = 75.0f, LOW_SPAN = 90.0f;
 constexpr uint32_t FULL = 0xffffffffu;
 
+// What parts of tiles and their joins cost a call of trees, some 6 us, in blocks: of
+// two lanes' rows, of heads of 64 and of 128.  Whole tiles where they take no more than
+// that longer: 16 sequences of 16 drafted and 1000 cached tokens 27.7 -> 21.3 us, 16 of
+// 100 58.5 -> 44.8, 20 of 5 and 400 (16 heads of 64) 28.9 -> 24.3, 32 of 16 with a window
+// of 500 38.6 -> 29.0.  Half of these numbers loses the second of the four, 1.5 times
+// them costs 8 of 16 and 2048 24.0 -> 26.5.
+constexpr int JOIN_PAIR = 4, JOIN_64 = 12, JOIN_128 = 7;
 constexpr int PIECES = 4;                    // pieces handed out and not done with
 constexpr int PIECE_BYTES = 64;
 static_assert(sizeof(AttnPiece) <= PIECE_BYTES, "see Cfg::TOTAL");
@@ -782,7 +789,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
     bool work;
     if constexpr (TREE) {
         TreeShare& share = *reinterpret_cast<TreeShare*>(smem + C::SHARE);
-        tree_share<NTHREADS>(p, cta, 2, share, &g_attn_tc_error);   // a block for each lane
+        const int join = p.max_q * p.G > p.plan.lane_rows ? JOIN_PAIR : DP == 64 ? JOIN_64 : JOIN_128;
+        tree_share<NTHREADS>(p, cta, 2, join, share, &g_attn_tc_error);   // a block for each lane
         work = walk.begin(share.start, share.per);
     } else {
         const bool begun = walk.begin(p, cta), agrees = attn_plan_agrees(p);   // one round of loads
