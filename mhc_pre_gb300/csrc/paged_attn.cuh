@@ -208,14 +208,13 @@ struct AttnNode {
     }
 };
 
-// A sequence of drafted tokens as tiles, all alike: they see the same keys.
+// A sequence of drafted tokens as tiles.  They see the same keys, so they have the
+// same blocks; the last one may have fewer rows than the others, and its blocks then
+// take less time.
 struct TreeSeq {
     int64_t q0;
     int qlen, kvlen, blk0, nblk, tiles;   // no tiles: no new tokens, or numbers that do not fit the call
     bool fits;
-    __device__ __forceinline__ int64_t units(const AttnParams& p) const {
-        return static_cast<int64_t>(tiles) * p.Hk * (nblk + p.plan.lead);
-    }
     __device__ __forceinline__ AttnTile tile(const AttnParams& p, int seq, int i, int64_t start) const {
         AttnTile t = {};
         t.start = start;
@@ -267,153 +266,192 @@ __device__ __forceinline__ int tree_divide(int64_t a, int64_t b) {
 }
 
 // What the CTAs of a launch leave for the joins, and how a CTA finds its share: in
-// place of a plan, each CTA sums up the units and the tiles of all sequences and finds
-// its two borders among them.  That takes a microsecond more than reading a plan, and
-// a launch of five less.
+// place of a plan, each CTA sums up the units, the weights and the tiles of all
+// sequences and finds its two borders among them.  That takes a microsecond more than
+// reading a plan, and a launch of five less.
 struct TreeShare {
     AttnStart start;
-    int64_t per, sums[32][2];
-    int most[32];
+    int64_t sums[16][3];   // of a warp each
+    int most[16], kinds[16];
 };
-// The border at unit u of a batch of `units`, moved to the nearer end of a tile (of
-// one key head) that is not to be split; u lies in sequence b, whose first unit is
-// `base`.
-__device__ __forceinline__ AttnStart tree_border(const AttnParams& p, const TreeSeq& s, int b, int64_t base, int64_t u,
-                                                 int64_t units, int64_t per) {
-    const int cost = s.nblk + p.plan.lead;
-    const int64_t in = u - base, row = static_cast<int64_t>(p.Hk) * cost;
-    const int tile = tree_divide(in, row);
-    const int64_t left = in - tile * row;
-    AttnStart a = {};
-    a.head = tree_divide(left, cost);
-    a.unit = static_cast<int>(left - static_cast<int64_t>(a.head) * cost);
-    a.t = s.tile(p, b, tile, base + tile * row);
-    a.begin = u;
-    if (a.unit > 0 && static_cast<int64_t>(cost) * TREE_SMALL_TILE <= per) {
-        if (2 * a.unit < cost) {
-            a.begin -= a.unit;
-        } else {
-            a.begin += cost - a.unit;
-            if (++a.head == p.Hk) {
-                a.head = 0;
-                if (a.begin < units) tree_next_tile(p, a.t);
-            }
-        }
-        a.unit = 0;
+// How shares are cut.
+struct TreeCut {
+    int least;          // weight of a CTA's share, at least: a block or more, so that none in a tile is empty
+    int join;           // what splitting tiles costs a call, in weight
+    int full, part;     // weight of a block: of a tile of more rows than one lane holds, of fewer
+};
+struct TreeSums {
+    int64_t units, weight, tiles;   // tiles: of a key head each
+};
+// The tiles' weights.
+struct TreeWeights {
+    int lead, full, last;   // of the fixed cost; of a tile (of a key head), all but the last and the last one
+    int block;              // of a block of the last one
+    __device__ __forceinline__ TreeWeights(const AttnParams& p, const TreeSeq& s, const TreeCut& cut) {
+        block = s.qlen * p.G - (s.tiles - 1) * p.plan.tile_rows <= p.plan.lane_rows ? cut.part : cut.full;
+        lead = p.plan.lead * cut.part;
+        full = lead + s.nblk * cut.full;
+        last = lead + s.nblk * block;
     }
-    return a;
+};
+__device__ __forceinline__ TreeSums tree_sums(const AttnParams& p, const TreeSeq& s, const TreeWeights& w) {
+    if (s.tiles == 0) return {0, 0, 0};
+    const int64_t t = static_cast<int64_t>(s.tiles) * p.Hk;
+    return {t * (s.nblk + p.plan.lead), static_cast<int64_t>(p.Hk) * (static_cast<int64_t>(s.tiles - 1) * w.full + w.last), t};
 }
-// The border before the sequence's i-th tile and head.
-__device__ __forceinline__ AttnStart tree_border_whole(const AttnParams& p, const TreeSeq& s, int b, int64_t base, int i) {
+// The border before the sequence's i-th tile and head (of its last: behind it), whose
+// first unit is `base` units.
+__device__ __forceinline__ AttnStart tree_border_whole(const AttnParams& p, const TreeSeq& s, int b, int64_t base, int i,
+                                                       int64_t units) {
     const int cost = s.nblk + p.plan.lead, tile = i / p.Hk;
     const int64_t start = base + static_cast<int64_t>(tile) * p.Hk * cost;
     AttnStart a = {};
     a.head = i - tile * p.Hk;
-    a.t = s.tile(p, b, tile, start);
     a.begin = start + static_cast<int64_t>(a.head) * cost;
+    a.t = s.tile(p, b, tile, start);
+    if (tile == s.tiles && a.begin < units) {   // the next sequence's first one
+        a.t = s.tile(p, b, tile - 1, start - static_cast<int64_t>(p.Hk) * cost);
+        tree_next_tile(p, a.t);
+    }
     return a;
 }
-// All threads of CTA `cta`: its share, into shared memory and the workspace.
-// `least`: units that a CTA has at least; `join`: what splitting tiles costs a call,
-// in units: where whole tiles dealt out by their number take no more than that above
-// an even share, none is split.
+// The border at weight `in` of a sequence, moved to the nearer end of a tile that is
+// not to be split (`per`: a CTA's share of the weight), else between two blocks.
+__device__ __forceinline__ AttnStart tree_border(const AttnParams& p, const TreeSeq& s, const TreeWeights& w,
+                                                 const TreeCut& cut, int b, int64_t base, int64_t in, int64_t per,
+                                                 int64_t units) {
+    const int64_t before = static_cast<int64_t>(s.tiles - 1) * p.Hk * w.full;   // of all tiles but the last
+    const bool last = in >= before;
+    const int64_t cost = last ? w.last : w.full, block = last ? w.block : cut.full;
+    const int i = last ? (s.tiles - 1) * p.Hk + tree_divide(in - before, cost) : tree_divide(in, cost);
+    const int off = static_cast<int>(last ? in - before - static_cast<int64_t>(i - (s.tiles - 1) * p.Hk) * cost
+                                          : in - static_cast<int64_t>(i) * cost);
+    const bool small = cost * TREE_SMALL_TILE <= per;
+    AttnStart a = tree_border_whole(p, s, b, base, small && 2 * off >= cost ? i + 1 : i, units);
+    if (!small) {
+        a.unit = off < w.lead ? off / cut.part : p.plan.lead + (off - w.lead) / static_cast<int>(block);
+        a.begin += a.unit;
+    }
+    return a;
+}
+// All threads of CTA `cta`: its share, into shared memory and the workspace.  Where
+// whole tiles dealt out by their number take no more than cut.join above an even
+// share, none is split.
 template <int THREADS>
-__device__ __forceinline__ void tree_share(const AttnParams& p, int cta, int least, int join, TreeShare& out,
+__device__ __forceinline__ void tree_share(const AttnParams& p, int cta, const TreeCut& cut, TreeShare& out,
                                            unsigned* error_word) {
+    static_assert(THREADS <= 512, "TreeShare has 16 warps");
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-    struct Two {
-        int64_t units, tiles;   // tiles: of a key head each
-    };
     // Inclusive sums over the block; `total` has the block's.
-    auto scan = [&](Two v, Two& total) {
+    auto scan = [&](TreeSums v, TreeSums& total) {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, v.units, o), z = __shfl_up_sync(0xffffffffu, v.tiles, o);
+            const int64_t x = __shfl_up_sync(0xffffffffu, v.units, o), y = __shfl_up_sync(0xffffffffu, v.weight, o);
+            const int64_t z = __shfl_up_sync(0xffffffffu, v.tiles, o);
             if (lane >= o) {
-                v.units += y;
+                v.units += x;
+                v.weight += y;
                 v.tiles += z;
             }
         }
         __syncthreads();
         if (lane == 31) {
             out.sums[w][0] = v.units;
-            out.sums[w][1] = v.tiles;
+            out.sums[w][1] = v.weight;
+            out.sums[w][2] = v.tiles;
         }
         __syncthreads();
-        Two before = {0, 0};
-        total = {0, 0};
+        total = {0, 0, 0};
 #pragma unroll
         for (int i = 0; i < THREADS / 32; ++i) {
-            const int64_t a = out.sums[i][0], b = out.sums[i][1];
-            if (i < w) {
-                before.units += a;
-                before.tiles += b;
+            if (i == w) {
+                v.units += total.units;
+                v.weight += total.weight;
+                v.tiles += total.tiles;
             }
-            total.units += a;
-            total.tiles += b;
+            total.units += out.sums[i][0];
+            total.weight += out.sums[i][1];
+            total.tiles += out.sums[i][2];
         }
-        return Two{before.units + v.units, before.tiles + v.tiles};
+        return v;
     };
     TreeSeq s = {};
-    Two mine = {0, 0}, all = {0, 0}, upto = {0, 0};
-    int most = 0;               // units of the largest tile
+    TreeSums mine = {0, 0, 0}, all = {0, 0, 0}, upto = {0, 0, 0};
+    int most = 0;               // weight of the heaviest tile
+    int kinds = 0;              // of blocks: 1, of tiles of fewer rows; 2, of more
     const bool once = p.B <= THREADS;
     for (int b0 = 0; b0 < p.B; b0 += THREADS) {
         const int b = b0 + tid;
-        mine = {0, 0};
+        mine = {0, 0, 0};
         if (b < p.B) {
             s = tree_seq(p, b);
             if (!s.fits && cta == 0) atomicOr(error_word, ATTN_ERR_RANGE);
-            mine = {s.units(p), static_cast<int64_t>(s.tiles) * p.Hk};
-            if (s.tiles > 0) most = max(most, s.nblk + p.plan.lead);
+            const TreeWeights tw(p, s, cut);
+            mine = tree_sums(p, s, tw);
+            if (s.tiles > 0) {
+                most = max(most, s.tiles > 1 ? tw.full : tw.last);
+                kinds |= (s.tiles > 1 || tw.block == cut.full ? 2 : 0) | (tw.block == cut.part ? 1 : 0);
+            }
         }
         most = __reduce_max_sync(0xffffffffu, most);
-        if (lane == 0) out.most[w] = most;   // (the scan's barriers are behind it)
-        Two sum;
-        const Two here = scan(mine, sum);
-        upto = {all.units + here.units, all.tiles + here.tiles};
+        kinds = __reduce_or_sync(0xffffffffu, kinds);
+        if (lane == 0) {   // (the scan's barriers are behind it)
+            out.most[w] = most;
+            out.kinds[w] = kinds;
+        }
+        TreeSums sum;
+        const TreeSums here = scan(mine, sum);
+        upto = {all.units + here.units, all.weight + here.weight, all.tiles + here.tiles};
         all.units += sum.units;
+        all.weight += sum.weight;
         all.tiles += sum.tiles;
     }
 #pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) most = max(most, p.B > 0 ? out.most[i] : 0);
+    for (int i = 0; i < THREADS / 32; ++i) {
+        most = max(most, p.B > 0 ? out.most[i] : 0);
+        kinds |= p.B > 0 ? out.kinds[i] : 0;
+    }
     const int ncta = p.plan.ncta;
-    int64_t per = all.units >> 31 == 0 ? static_cast<int64_t>(tree_divide(all.units + ncta - 1, ncta))
-                                       : (all.units + ncta - 1) / ncta;
-    if (per < least) per = least;
+    // where all blocks weigh the same a multiple of that, so that borders leave no remainders
+    const int grain = kinds == 1 ? cut.part : kinds == 2 ? cut.full : 1;
+    const int64_t even = static_cast<int64_t>(ncta) * grain;
+    int64_t per = all.weight >> 31 == 0 ? static_cast<int64_t>(tree_divide(all.weight + even - 1, even))
+                                        : (all.weight + even - 1) / even;
+    per *= grain;
+    if (per < cut.least) per = cut.least;
     // (more than 31 bits of them only if sequences overlap)
     const int n = all.tiles >> 31 == 0 ? static_cast<int>(all.tiles) : 0, deal = n / ncta, rest = n - deal * ncta;
-    const bool whole = n > 0 && static_cast<int64_t>(deal + (rest > 0 ? 1 : 0)) * most <= per + join;
-    // in units, or in tiles: the first `rest` CTAs have one more
-    const int64_t u0 = whole ? static_cast<int64_t>(cta) * deal + min(cta, rest) : min(cta * per, all.units);
-    const int64_t end = whole ? all.tiles : all.units;
-    const int64_t u1 = cta + 1 == ncta ? end : whole ? u0 + deal + (cta < rest ? 1 : 0) : min(u0 + per, all.units);
+    const bool whole = n > 0 && static_cast<int64_t>(deal + (rest > 0 ? 1 : 0)) * most <= per + cut.join;
+    // in weight, or in tiles: the first `rest` CTAs have one more
+    const int64_t end = whole ? all.tiles : all.weight;
+    const int64_t u0 = whole ? static_cast<int64_t>(cta) * deal + min(cta, rest) : min(cta * per, end);
+    const int64_t u1 = cta + 1 == ncta ? end : whole ? u0 + deal + (cta < rest ? 1 : 0) : min(u0 + per, end);
     if (tid == 0) {
-        out.per = per;
         out.start = AttnStart{};
         out.start.begin = out.start.end = all.units;
     }
-    Two done = {0, 0};
+    TreeSums done = {0, 0, 0};
     for (int b0 = 0; b0 < p.B; b0 += THREADS) {
         const int b = b0 + tid;
         if (!once) {
-            mine = {0, 0};
+            mine = {0, 0, 0};
             if (b < p.B) {
                 s = tree_seq(p, b);
-                mine = {s.units(p), static_cast<int64_t>(s.tiles) * p.Hk};
+                mine = tree_sums(p, s, TreeWeights(p, s, cut));
             }
-            Two sum;
-            const Two here = scan(mine, sum);
-            upto = {done.units + here.units, done.tiles + here.tiles};
+            TreeSums sum;
+            const TreeSums here = scan(mine, sum);
+            upto = {done.units + here.units, done.weight + here.weight, done.tiles + here.tiles};
             done.units += sum.units;
+            done.weight += sum.weight;
             done.tiles += sum.tiles;
         }
         __syncthreads();
-        const int64_t hi = whole ? upto.tiles : upto.units, lo = hi - (whole ? mine.tiles : mine.units);
+        const int64_t hi = whole ? upto.tiles : upto.weight, lo = hi - (whole ? mine.tiles : mine.weight);
         const int64_t base = upto.units - mine.units;
         auto border = [&](int64_t u) {
-            return whole ? tree_border_whole(p, s, b, base, static_cast<int>(u - lo))
-                         : tree_border(p, s, b, base, u, all.units, per);
+            return whole ? tree_border_whole(p, s, b, base, static_cast<int>(u - lo), all.units)
+                         : tree_border(p, s, TreeWeights(p, s, cut), cut, b, base, u - lo, per, all.units);
         };
         // the end first, in its own field, which the start's thread does not touch
         if (u1 < end && lo <= u1 && u1 < hi) out.start.end = border(u1).begin;
@@ -426,10 +464,7 @@ __device__ __forceinline__ void tree_share(const AttnParams& p, int cta, int lea
         }
     }
     __syncthreads();
-    if (tid == 0) {
-        reinterpret_cast<AttnStart*>(p.ws + p.plan.start_off)[cta] = out.start;
-        if (cta == 0) reinterpret_cast<AttnHead*>(p.ws)->per_cta = per;
-    }
+    if (tid == 0) reinterpret_cast<AttnStart*>(p.ws + p.plan.start_off)[cta] = out.start;
 }
 
 // A CTA's pieces one after the other.
@@ -449,7 +484,7 @@ struct AttnWalk {
     __device__ __forceinline__ bool begin(const AttnParams& p, int cta) {
         return begin(attn_starts(p)[cta], attn_head(p)->per_cta);
     }
-    __device__ __forceinline__ bool begin(const AttnStart& s, int64_t per_cta) {
+    __device__ __forceinline__ bool begin(const AttnStart& s, int64_t per_cta = 0) {   // (of trees it is not asked for)
         per = per_cta;
         at = s.begin;
         end = s.end;

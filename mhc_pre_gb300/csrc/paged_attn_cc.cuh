@@ -336,8 +336,9 @@ attn_cc_kernel(const AttnParams p) {
     AttnWalk walk;
     if constexpr (TREE) {
         __shared__ TreeShare share;
-        tree_share<TY * 16>(p, cta, 1, 0, share, &g_attn_error);   // a block takes longer than the joins
-        if (!walk.begin(share.start, share.per)) return;
+        // a block of 64 keys takes longer than the joins, and about as long with fewer rows
+        tree_share<TY * 16>(p, cta, {1, 0, 1, 1}, share, &g_attn_error);
+        if (!walk.begin(share.start)) return;
     } else {
         if (!attn_plan_agrees(p)) {
             if (threadIdx.x == 0) atomicOr(&g_attn_error, ATTN_ERR_RANGE);

@@ -103,6 +103,12 @@ constexpr uint32_t FULL = 0xffffffffu;
 // of 500 38.6 -> 29.0.  Half of these numbers loses the second of the four, 1.5 times
 // them costs 8 of 16 and 2048 24.0 -> 26.5.
 constexpr int JOIN_PAIR = 4, JOIN_64 = 12, JOIN_128 = 7;
+// What a block weighs in a CTA's share, of a tile for both lanes and of one for one lane:
+// the second is bound by memory, the first by the products too. 4 sequences of 64 and
+// 65536 (tiles of 250 and 70 rows) take 333 us, 363, 343 and 338 with 1 to 1, 5 to 4
+// and 3 to 2; 32 of 16 to 32 and up to 8192 96, 98, 96 and 99.
+constexpr int FULL_BLOCK = 4, PART_BLOCK = 3;
+static_assert(2 * PART_BLOCK >= FULL_BLOCK, "the least share has a block");
 constexpr int PIECES = 4;                    // pieces handed out and not done with
 constexpr int PIECE_BYTES = 64;
 static_assert(sizeof(AttnPiece) <= PIECE_BYTES, "see Cfg::TOTAL");
@@ -789,9 +795,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
     bool work;
     if constexpr (TREE) {
         TreeShare& share = *reinterpret_cast<TreeShare*>(smem + C::SHARE);
-        const int join = p.max_q * p.G > p.plan.lane_rows ? JOIN_PAIR : DP == 64 ? JOIN_64 : JOIN_128;
-        tree_share<NTHREADS>(p, cta, 2, join, share, &g_attn_tc_error);   // a block for each lane
-        work = walk.begin(share.start, share.per);
+        const TreeCut cut = {2 * PART_BLOCK, PART_BLOCK * (p.max_q * p.G > p.plan.lane_rows ? JOIN_PAIR : DP == 64 ? JOIN_64 : JOIN_128),
+                             FULL_BLOCK, PART_BLOCK};
+        tree_share<NTHREADS>(p, cta, cut, share, &g_attn_tc_error);
+        work = walk.begin(share.start);
     } else {
         const bool begun = walk.begin(p, cta), agrees = attn_plan_agrees(p);   // one round of loads
         if (!agrees && tid == 0) atomicOr(&g_attn_tc_error, ATTN_ERR_RANGE);

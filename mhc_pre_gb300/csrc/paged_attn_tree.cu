@@ -18,9 +18,10 @@
 // 16 lanes for each row.
 //
 // Figures, 40 + 8 heads of 128 in bf16 on one GB300: 32 sequences of 16 to 32 drafted
-// tokens on up to 8192 cached ones 99 us, 25 on 8192 each 185 us (5.9 TB/s), 4 of 64 on
-// 65536 360 us (their 320 rows of a key head are two tiles, which read the context
-// twice), one of 13 on 777 15 us.  float32, 20 + 4 heads, 8 of 11 on 3200: 115 us.
+// tokens on up to 8192 cached ones 96 us, 25 on 8192 each 187 us (5.8 TB/s), 4 of 64 on
+// 65536 333 us (their 320 rows of a key head are two tiles, which read the context
+// twice, at 6.4 TB/s), one of 13 on 777 16 us.  float32, 20 + 4 heads, 8 of 11 on 3200:
+// 115 us.
 #include "paged_attn_cc.cuh"
 
 namespace mhc {
@@ -88,12 +89,24 @@ tree_join_kernel(const AttnParams p) {
     ptx::griddep_wait();
     const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int sub = lane % JOIN_LANES, side = lane / JOIN_LANES;
-    const AttnStart& s = attn_starts(p)[c + 1];   // where this CTA's share ends
+    const AttnStart* starts = attn_starts(p);
+    const AttnStart& s = starts[c + 1];   // where this CTA's share ends
     if (s.begin >= s.end || s.unit <= p.plan.lead) return;   // no tile goes on there
-    const int64_t per = attn_head(p)->per_cta;
     const int64_t u0 = s.t.start + static_cast<int64_t>(s.head) * (s.t.nblk + p.plan.lead) + p.plan.lead;
-    const int first = tree_divide(u0, per), last = tree_divide(u0 + s.t.nblk - 1, per);
-    if (first != c || last == first) return;
+    const int first = c;
+    if (starts[c].begin > u0) return;     // it began before
+    // the CTA in whose share the tile's last block is; all between have blocks of it
+    int last = c + 1;
+    while (true) {
+        const int j = last + lane;
+        const unsigned ends = __ballot_sync(0xffffffffu, j >= p.plan.ncta || starts[min(j, p.plan.ncta - 1)].end >= u0 + s.t.nblk);
+        if (ends != 0u) {
+            last += __ffs(ends) - 1;
+            break;
+        }
+        last += 32;
+    }
+    last = min(last, p.plan.ncta - 1);
     const int rows = min(p.plan.tile_rows, s.t.qlen * p.G - s.t.row0), sr = p.plan.slot_rows;
     // the tile's parts, from the second on two slots apart
     auto part = [&](int j) { return attn_slot(p, 2 * j + (j == first ? 1 : 0)); };
