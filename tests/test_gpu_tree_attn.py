@@ -201,6 +201,17 @@ def test_masks_that_are_parts_of_wider_ones(dtype):
     assert torch.equal(r.o, want.o) and torch.equal(r.lse, want.lse)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens", [[(70, 6000), (10, 5000), (30, 3000), (1, 7000), (0, 9)], [(101, 900), (26, 2500)],
+                                  [(51, 4000), (25, 60), (25, 70), (26, 80)] * 3, [(120, 5000)]])
+def test_tiles_of_all_kinds_split_at_any_block(lens, dtype):
+    """Tiles of one lane's rows, of both and several of a sequence, whose blocks weigh
+    differently in the CTAs' shares."""
+    for dh in (64, 128):
+        c = Trees(lens, 5, 1, dh, 64, dtype, "any")
+        c.check(c.run())
+
+
 def test_many_sequences():
     """More sequences than a CTA has threads, which each find their share: some
     with nothing, some with numbers that do not fit."""
