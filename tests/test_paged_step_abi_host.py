@@ -51,6 +51,16 @@ def test_keep_refusals(L, bad, status):                   # noqa: F811
     assert _keep(L, **bad) == status
 
 
+def test_keep_refuses_lengths_that_it_reads(L):           # noqa: F811
+    """Blocks read kv_lens (and the others) while lens is written."""
+    far = {k: A + 4096 * i for i, k in enumerate(("table", "cu", "kv", "path", "keep"), 1)}
+    for k, at in far.items():
+        for lens in (at, at - 4):
+            assert _keep(L, **{**far, "lens": lens}) == INV, k
+    assert _keep(L, **far, lens=far["table"] + 4 * 7) == INV     # its second row's last page
+    assert _keep(L, **far, lens=far["path"] + 4 * 5) == INV
+
+
 def test_keep_of_nothing(L):                              # noqa: F811
     for none in (dict(B=0, cu=None), dict(layers=0, k=None), dict(most=0, path=None)):
         assert _keep(L, **none) == OK
