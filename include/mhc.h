@@ -676,7 +676,8 @@ mhc_status mhc_tree_attn(mhc_dtype dt, const void* q, int64_t q_stride, const vo
  * MHC_ERR_RANGE: sequences whose rows would pass T (they and all later ones get
  * none: cu_q stays), whose numbers do not fit (lengths below 0, or past held pages
  * or the table; they get slots -1, positions 0 and kv_lens 0), parents that are not
- * below their node (as -1), nodes past tree_words * 32 (without a bit), a list's
+ * below their node (as -1), nodes past tree_words * 32 (without a bit; of their
+ * paths the last 1024 nodes count), a list's
  * length outside its tensor, more pages coming back than it has room for (those
  * are lost).  At most 8192 sequences, 2^30 entries of the table.
  */
@@ -693,7 +694,9 @@ mhc_status mhc_paged_step(const int32_t* new_lens, const int32_t* lens, int B, i
  * last of its m = kv_lens[b] cached ones, and keeps keep[b] of them: nodes
  * path[b, 0] < path[b, 1] < ... of 0 .. n - 1 go to the places m - n, m - n + 1,
  * ...; then lens[b] = m - n + keep[b].  keep[b] = 0 moves nothing and leaves
- * lens[b] as it is.  Places behind the kept tokens hold what is left there.
+ * lens[b] as it is (as it must be for a sequence that mhc_paged_step gave no room:
+ * its drafted tokens are not in the cache).  Places behind the kept tokens hold what
+ * is left there.
  *
  *   k_caches, v_caches   host arrays of `layers` device pointers, each a cache as
  *                        in mhc_qk_norm_rope_append, all keys (and all values)
@@ -702,7 +705,7 @@ mhc_status mhc_paged_step(const int32_t* new_lens, const int32_t* lens, int B, i
  *                                         ceil(max_kv / page_size)
  *   cu_q [B+1], kv_lens [B], keep [B] int32
  *   path [B, *]          int32            path_stride between rows, >= max_keep
- *   lens [B]             int32   out      or null
+ *   lens [B]             int32   out      or null; none of the inputs' memory
  * MHC_ERR_RANGE: a sequence whose numbers do not fit (a path that does not rise
  * or leaves the drafted tokens, keep past max_keep or n, m outside n .. max_kv) is
  * left as it is; a row on a page outside the cache is not moved.

@@ -641,7 +641,8 @@ def mhc_cache_keep(k_caches, v_caches, page_table, cu_q, kv_lens, path, keep, le
     Hk, Dh], or a sequence of one for each layer) the accepted path path[b, :keep[b]]
     of each sequence's new tokens, rising numbers, moves behind its context, in
     place.  ``lens`` [B], when given, becomes the context and the kept tokens (as
-    it was where keep[b] is 0)."""
+    it was where keep[b] is 0, as for sequences that got no room in the step); it
+    is not kv_lens."""
     st = (_calls_module or _calls()).cache_keep(k_caches, v_caches, page_table, cu_q, kv_lens, path, keep, lens, max_kv)
     if st:
         _check(st, "mhc_cache_keep")

@@ -178,7 +178,9 @@ step_kernel(const StepParams p) {
             if (words != nullptr) {
                 // numbers fall on the way up, so the words are finished from the last to the first
                 const int32_t* parents = p.parents + cu[b];
-                for (int node = i; node >= 0; ++path) {
+                // (a path of more than 1024 is of a node past the words, and is cut off: the
+                // climbs of a chain of all rows would take minutes)
+                for (int node = i; node >= 0 && path < TREE_MOST; ++path) {
                     if (node < 32 * p.words) {
                         for (; w > node >> 5; --w) {
                             words[w] = static_cast<int32_t>(bits);

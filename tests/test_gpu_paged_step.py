@@ -107,6 +107,21 @@ def test_trees(B_, n, words, deep):
     assert B.get_last_device_error() == B.MHC_OK
 
 
+def test_paths_longer_than_any_tree_are_cut_off():
+    """A chain of thousands of rows: each climbs at most 1024 nodes."""
+    n, m = 5000, 37
+    dev = _dev()
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)       # noqa: E731
+    r = B.mhc_paged_step(i32([n]), i32([m]), torch.zeros(1, 400, dtype=torch.int32, device=dev), i32([400]), i32([0]),
+                         i32([0]), 16, n, parents=torch.arange(-1, n - 1, dtype=torch.int32, device=dev))
+    assert B.get_last_device_error() == B.MHC_ERR_RANGE
+    assert r.positions.tolist() == [m + min(i, 1023) for i in range(n)]
+    got = r.tree.cpu().numpy().view(np.uint32)
+    bits = (got[:, :, None] >> np.arange(32, dtype=np.uint32) & 1).reshape(n, 1024).astype(bool)
+    i, j = np.arange(n)[:, None], np.arange(1024)[None]
+    assert (bits == ((j <= i) & (j > i - 1024))).all()
+
+
 def test_pages_given_back_are_used_in_the_same_step():
     """The list alone would not do: the top of the list is what has come back."""
     rng = np.random.default_rng(3)
