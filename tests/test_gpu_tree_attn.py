@@ -225,6 +225,29 @@ def test_many_sequences():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("at", [[0, 1, 2], [0, 17, 18, 146, 147, 400, 1183], [1999], [127, 128, 129, 255, 256, 385], [],
+                                list(range(3, 2000, 97)), [0, 1, 33, 1998]])
+def test_sequences_far_apart_among_idle_ones(at, dtype):
+    """Most of a large batch has no new tokens in this step; the same with the idle
+    ones taken out."""
+    rng = np.random.default_rng(len(at))
+    lens = [(0, int(m)) for m in rng.integers(0, 30, 2000)]
+    for b in at:
+        n = int(rng.integers(1, 30))
+        lens[b] = (n, n + int(rng.integers(0, 900)))
+    c = Trees(lens, 5, 1, 64, 16, dtype, "tree") if at else Trees([(0, 9)] * 2000, 5, 1, 64, 16, dtype)
+    kw = dict(max_q=30, max_kv=c.table.shape[1] * 16)
+    if not at:
+        c.tree = c.tree[:0].reshape(0, 1)
+    r = B.mhc_tree_attn(c.q, c.k, c.v, c.table, c.tree, c.cu, c.kv, **kw)
+    c.check(r)
+    here = torch.tensor(at, dtype=torch.long, device=c.q.device)
+    cu = torch.cat([c.cu[:1], c.cu[1:][here]])
+    s = B.mhc_tree_attn(c.q, c.k, c.v, c.table[here], c.tree, cu, c.kv[here], **kw)
+    assert torch.equal(r.o, s.o) and torch.equal(r.lse, s.lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("n", [1, 12, 25, 26, 50, 51, 90])
 def test_short_contexts_in_great_number(n, dtype):
     """Tiles far smaller than a CTA's share, whole and with borders moved."""
