@@ -93,6 +93,17 @@ def test_layers(layers):
     c.check()
 
 
+@pytest.mark.parametrize("sequences,layers", [(3000, 3), (4097, 1), (9000, 7), (700, 67), (8192, 9)])
+def test_many_sequences_of_which_few_keep_something(sequences, layers):
+    """Blocks that take several caches, the last one fewer."""
+    lens = [(0, 2)] * sequences
+    for b in range(5, sequences, 397):
+        lens[b] = (20, 30 + b % 40)
+    c = Case(lens, 2, 8, 16, "bf16", layers=layers)
+    c.run()
+    c.check()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_caches_with_the_heads_outside(dtype):
     c = Case(LENS["batch"], 4, 64, 16, dtype, layers=2, order="head")
