@@ -177,6 +177,26 @@ def test_nothing_is_written_outside(T, Hq, Hk, dh, rot, dtype, monkeypatch):
     assert all(torch.equal(a, b) for a, b in zip(plain, got))
 
 
+@pytest.mark.parametrize("T,Hq,Hk", [(420000, 40, 8), (66000, 256, 8)])
+def test_tensors_past_32_bits(T, Hq, Hk):
+    """More than 2^31 values: the last tokens as in a call of their own."""
+    q, k, v, pos, cs = _inputs(5, Hq, Hk, 128, 64, "bf16")
+    Q, K = (torch.zeros(T, h, 128, dtype=torch.bfloat16, device=q.device) for h in (Hq, Hk))
+    P = torch.zeros(T, dtype=torch.int32, device=q.device)
+    Q[-5:], K[-5:], P[-5:] = q, k, pos
+    for f in (B.mhc_rope, B.mhc_rope_bwd):
+        r, want = f(Q, K, P, cs), f(q, k, pos, cs)
+        assert torch.equal(r.q[-5:], want.q) and torch.equal(r.k[-5:], want.k)
+        assert not bool(r.q[:1000].any()) and not bool(r.q[T // 2:T // 2 + 1000].any())
+    cache = torch.zeros(2, 16, Hk, 128, dtype=torch.bfloat16, device=q.device)
+    slots = torch.full((T,), -1, dtype=torch.int64, device=q.device)
+    slots[-5:] = torch.arange(5)
+    got = B.mhc_rope_append(Q, K, K, cache, cache.clone(), slots, P, cs)
+    want = B.mhc_rope(q, k, pos, cs)
+    assert torch.equal(got[-5:], want.q) and torch.equal(cache[0, :5], want.k)
+    assert B.get_last_device_error() == B.MHC_OK
+
+
 def test_another_stream_and_a_graph():
     q, k, v, pos, cs = _inputs(50, 6, 2, 64, 64, "bf16")
     want = B.mhc_rope(q, k, pos, cs)
