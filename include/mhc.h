@@ -672,7 +672,9 @@ mhc_status mhc_tree_attn(mhc_dtype dt, const void* q, int64_t q_stride, const vo
  *   parents [T]          int32            or null: no trees
  *   tree_words                            words of a row of `tree`, 1 to 32
  * outputs: cu_q [B+1], kv_lens [B], positions [T] int32, slots [T] int64,
- *   tree [T, tree_words] int32 (null without parents).  No output may be an input.
+ *   tree [T, tree_words] int32 (null without parents).  Nothing that is written may
+ *   lie in the memory of another argument (kv_lens is not lens, say): such a call is
+ *   refused with MHC_ERR_INVALID_ARG.  new_lens, lens and parents may be the same.
  * MHC_ERR_RANGE: sequences whose rows would pass T (they and all later ones get
  * none: cu_q stays), whose numbers do not fit (lengths below 0, or past held pages
  * or the table; they get slots -1, positions 0 and kv_lens 0), parents that are not

@@ -91,6 +91,22 @@ bool overlap(const void* a, int64_t a_count, const void* b, int64_t b_count) {
     return x < y + static_cast<uintptr_t>(b_count) * 4 && y < x + static_cast<uintptr_t>(a_count) * 4;
 }
 
+// 32-bit numbers in memory: rows of `width`, `stride` apart.
+struct Numbers {
+    const void* p;
+    int64_t rows, width, stride;
+};
+// Whether rows and a run (one row) have any in common; what lies between rows is theirs only.
+bool meet(const Numbers& a, const Numbers& run) {
+    if (a.p == nullptr || run.p == nullptr || a.rows == 0 || a.width == 0 || run.width == 0) return false;
+    const int64_t from = (static_cast<int64_t>(reinterpret_cast<uintptr_t>(run.p)) -
+                          static_cast<int64_t>(reinterpret_cast<uintptr_t>(a.p))) / 4, to = from + run.width;
+    int64_t r = a.rows > 1 && from > 0 ? from / a.stride : 0;   // the last row that begins at `from` or before
+    if (r >= a.rows) r = a.rows - 1;
+    if (from < r * a.stride + a.width && r * a.stride < to) return true;
+    return r + 1 < a.rows && (r + 1) * a.stride < to;
+}
+
 // The page size as a shift, -1 where it is none.
 int shift_of(int page_size) {
     for (int i = 0; i < 21; ++i)
@@ -543,6 +559,19 @@ mhc_status mhc_paged_step(const int32_t* new_lens, const int32_t* lens, int B, i
         if (tree_words <= 0) return MHC_ERR_INVALID_ARG;
         if (tree_words > mhc::TREE_MOST / 32) return MHC_ERR_UNSUPPORTED;
         if ((st = check_plain(parents, 4)) != MHC_OK || (st = check_plain(tree, 4)) != MHC_OK) return st;
+    }
+    // blocks read the inputs, and what is brought up to date, while outputs are written
+    const int64_t words = T > 0 && tree != nullptr ? T * tree_words : 0;
+    const Numbers table = {page_table, B, table_width, table_stride};
+    const Numbers runs[] = {{held, 1, B, 0},     {free_pages, 1, free_capacity, 0}, {free_count, 1, 1, 0},
+                            {cu_q, 1, B + 1, 0}, {kv_lens, 1, B, 0},                {positions, 1, T, 0},
+                            {slots, 1, 2 * T, 0}, {tree, 1, words, 0},              {new_lens, 1, B, 0},
+                            {lens, 1, B, 0},     {parents, 1, T, 0}};
+    constexpr int WRITTEN = 8, RUNS = 11;   // the last ones are only read, and may be the same
+    for (int i = 0; i < RUNS; ++i) {
+        if (meet(table, runs[i])) return MHC_ERR_INVALID_ARG;
+        for (int j = 0; j < i && j < WRITTEN; ++j)
+            if (meet(runs[i], runs[j])) return MHC_ERR_INVALID_ARG;
     }
     mhc::StepParams p = {};
     p.new_lens = new_lens;

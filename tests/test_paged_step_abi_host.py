@@ -28,6 +28,46 @@ def test_step_refusals(L, bad, status):                   # noqa: F811
     assert L.mhc_paged_step(*a.values(), None) == status
 
 
+STEP_INPUTS, STEP_OUTPUTS = ("new", "lens", "parents"), ("table", "held", "free", "count", "cu", "kv", "pos", "slots", "tree")
+
+
+def _step_apart(**o):
+    """Arguments of a step whose tensors lie 64 KB apart: 4 sequences, a table of 4 rows
+    of 8 entries 12 apart, 9 tokens, 10 free pages."""
+    a = dict(new=0, lens=0, B=4, table=0, stride=12, width=8, held=0, free=0, cap=10, count=0, page=16, T=9, parents=0,
+             words=2, cu=0, kv=0, pos=0, slots=0, tree=0)
+    for i, k in enumerate(STEP_INPUTS + STEP_OUTPUTS):
+        a[k] = A + 65536 * i
+    a.update(o)
+    return a
+
+
+@pytest.mark.parametrize("out", STEP_OUTPUTS)
+def test_step_refuses_outputs_in_the_memory_of_others(L, out):        # noqa: F811
+    """Blocks read the inputs while outputs are written (lengths that are to advance in
+    place, kv_lens = lens, among them)."""
+    size = dict(new=16, lens=16, parents=36, table=4 * (3 * 12 + 8), held=16, free=40, count=4, cu=20, kv=16, pos=36,
+                slots=72, tree=72)
+    a = _step_apart()
+    for other in STEP_INPUTS + STEP_OUTPUTS:
+        if other == out:
+            continue
+        last = size[other] - 4 if out != "slots" else (size[other] - 1) // 8 * 8
+        for at in (a[other], a[other] + last):                         # its first and its last entry
+            assert L.mhc_paged_step(*_step_apart(**{out: at}).values(), None) == INV, (other, at - a[other])
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are not memory: nothing may be launched")
+def test_step_takes_outputs_beside_and_between_others(L):             # noqa: F811
+    """Behind an input's last entry, in the gaps of a table's rows, and inputs that are
+    one tensor: past the checks, at the launch (which needs a GPU)."""
+    a = _step_apart()
+    for o in ({}, dict(kv=a["lens"] + 16), dict(kv=a["lens"] - 16), dict(new=a["lens"]), dict(held=a["table"] + 32),
+              dict(held=a["table"] + 4 * 44), dict(table=a["held"] - 32), dict(count=a["table"] + 4 * (12 + 11)),
+              dict(slots=a["pos"] + 40), dict(parents=None, tree=None, words=0)):
+        assert L.mhc_paged_step(*_step_apart(**o).values(), None) == B.MHC_ERR_CUDA, o
+
+
 def _pointers(*p):
     return (ctypes.c_void_p * len(p))(*p)
 
