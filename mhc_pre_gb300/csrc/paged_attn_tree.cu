@@ -190,12 +190,12 @@ cudaError_t launch_tree_attn(bool bf16, const AttnParams& p, cudaStream_t s) {
     cudaError_t e;
     if (attn_tc_supports(bf16, p.Hq, p.Hk, p.Dh, p.page_size)) {
         e = launch_tree_attn_tc(p, s);
-    } else {
+        if (p.force_timeout != 0u) return e;   // a forced timeout leaves no shares to join
+    } else {   // (nothing waits here: the hook has nothing to run out)
         g_error_word.may_be_set();
         e = bf16 ? attn::launch_cc_dp<__nv_bfloat16, true>(p, s) : attn::launch_cc_dp<float, true>(p, s);
     }
-    // (a forced timeout leaves no shares to join)
-    if (e != cudaSuccess || p.force_timeout != 0u) return e;
+    if (e != cudaSuccess) return e;
     return bf16 ? attn::launch_tree_join<__nv_bfloat16>(p, s) : attn::launch_tree_join<float>(p, s);
 }
 

@@ -311,6 +311,22 @@ def test_forced_timeout_is_reported():
     assert torch.equal(got.o, want.o)
 
 
+@pytest.mark.parametrize("dtype,dh,page", [("f32", 64, 64), ("bf16", 136, 64), ("bf16", 64, 48)])
+def test_the_timeout_hook_leaves_kernels_without_waits_alone(dtype, dh, page):
+    """On the CUDA cores nothing waits, so nothing runs out: whole tiles and split
+    ones get their rows, and there is nothing to report."""
+    c = Trees([(20, 3000), (3, 40)], 4, 2, dh, page, dtype)
+    want = c.run()
+    L = B.lib()
+    try:
+        assert L.mhc_test_force_timeout(1) == B.MHC_OK
+        got = c.run(out=torch.full_like(c.q, float("nan")))
+        assert B.get_last_device_error() == B.MHC_OK
+    finally:
+        assert L.mhc_test_force_timeout(0) == B.MHC_OK
+    assert torch.equal(got.o, want.o) and torch.equal(got.lse, want.lse)
+
+
 def test_another_stream_and_a_graph():
     c = Trees([(7, 700), (20, 300)], 10, 2, 128, 64, "bf16")
     want = c.run()
