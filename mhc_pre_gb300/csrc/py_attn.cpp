@@ -15,6 +15,7 @@
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
+#include <algorithm>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -626,7 +627,8 @@ PyObject* attn(PyObject* const* a, PyObject* mask) {
         tree = static_cast<int32_t*>(m->data_ptr());
         tree_stride = T > 1 ? m->stride(0) : stree[1];
     }
-    if (a[7] == Py_None) max_q = T;
+    // by default all tokens may be one sequence's; a tree's are no more than its mask has bits for
+    if (a[7] == Py_None) max_q = mask == nullptr ? T : std::min({T, std::max(32 * stree[1], int64_t(1)), int64_t(1024)});
     else if (!to_i64(a[7], &max_q)) return nullptr;
     if (mask != nullptr && 32 * stree[1] < max_q) {
         PyErr_Format(PyExc_ValueError, "tree has bits for %lld tokens a sequence, max_q is %lld",

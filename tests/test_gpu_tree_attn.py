@@ -255,6 +255,30 @@ def test_short_contexts_in_great_number(n, dtype):
     c.check(c.run())
 
 
+def _without_max_q(c):
+    return B.mhc_tree_attn(c.q, c.k, c.v, c.table, c.tree, c.cu, c.kv, window=c.window)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,words", [([(20, 120)] * 32, 1), ([(20, 60)] * 60, 2), ([(20, 60)] * 60, 60),
+                                        ([(1024, 1100), (1024, 1024), (9, 40)], 32), ([(3, 30)], 4), ([(32, 32)], 1)])
+def test_the_default_most_new_tokens(lens, words, dtype):
+    """Without max_q a sequence may have as many as the mask has bits for, at most
+    1024, whatever the batch's rows are."""
+    c = Trees(lens, 2, 1, 64, 64, dtype, "tree", words=words)
+    c.check(_without_max_q(c))
+
+
+def test_the_default_most_new_tokens_is_held_to():
+    """A sequence with more of them than the mask's bits is left out and reported."""
+    c = Trees([(9, 40), (33, 100), (32, 50)], 2, 1, 64, 64, "bf16", "tree", words=2)
+    c.tree = c.tree[:, :1].contiguous()
+    c.check(_without_max_q(c), only=[0, 2], error=B.MHC_ERR_RANGE)
+    c.tree = c.tree[:, :0]
+    with pytest.raises(ValueError):
+        _without_max_q(c)
+
+
 def test_padding_rows_stay_and_out_is_taken():
     c = Trees([(2, 50), (3, 90)], 4, 2, 64, 16, "bf16")
     q, tree = torch.cat([c.q, c.q[:4]]), torch.cat([c.tree, c.tree[:4]])
