@@ -105,7 +105,8 @@ struct AttnParams {
 // (one read instead of two on the way to the first queries and keys).
 struct alignas(16) AttnStart {
     int64_t begin, end;     // the CTA's units
-    int tile, head, unit, pad;
+    int tile, head, unit;
+    int after;              // of trees, while it is looked for: `t` is the last tile before it
     AttnTile t;
 };
 static_assert(sizeof(AttnStart) == 80, "AttnStart is read as five 16-byte words");
@@ -245,10 +246,9 @@ __device__ __forceinline__ TreeSeq tree_seq(const AttnParams& p, int b) {
     return s;
 }
 // The tile after `t`: of its sequence, or the first of the next that has any
-// (seq = B: there is none).  WARP: all lanes of a warp call it, and look through
-// the sequences without new tokens together (8 of 11 new tokens on 3200 keys among 8184
+// (seq = B: there is none).  All lanes of a warp call it, and look through the
+// sequences without new tokens together (8 of 11 new tokens on 3200 keys among 8184
 // without, float32: 126 us, one after the other 535).
-template <bool WARP>
 __device__ __forceinline__ void tree_next_tile(const AttnParams& p, AttnTile& t) {
     t.start += static_cast<int64_t>(p.Hk) * (t.nblk + p.plan.lead);
     t.row0 += p.plan.tile_rows;
@@ -260,13 +260,12 @@ __device__ __forceinline__ void tree_next_tile(const AttnParams& p, AttnTile& t)
             t = s.tile(p, b, 0, t.start);
             return;
         }
+        // on to the next one with rows, whether they fit the call or not
         ++b;
-        if (WARP) {   // on to the next one with rows, whether they fit the call or not
-            unsigned found = 0u;
-            for (; found == 0u && b < p.B; b += found != 0u ? __ffs(found) - 1 : 32) {
-                const int at = b + static_cast<int>(threadIdx.x & 31);
-                found = __ballot_sync(0xffffffffu, at < p.B && p.cu_q[at] != p.cu_q[at + 1]);
-            }
+        unsigned found = 0u;
+        for (; found == 0u && b < p.B; b += found != 0u ? __ffs(found) - 1 : 32) {
+            const int at = b + static_cast<int>(threadIdx.x & 31);
+            found = __ballot_sync(0xffffffffu, at < p.B && p.cu_q[at] != p.cu_q[at + 1]);
         }
     }
     t.seq = p.B;
@@ -312,8 +311,8 @@ __device__ __forceinline__ TreeSums tree_sums(const AttnParams& p, const TreeSeq
     const int64_t t = static_cast<int64_t>(s.tiles) * p.Hk;
     return {t * (s.nblk + p.plan.lead), static_cast<int64_t>(p.Hk) * (static_cast<int64_t>(s.tiles - 1) * w.full + w.last), t};
 }
-// The border before the sequence's i-th tile and head (of its last: behind it), whose
-// first unit is `base` units.
+// The border before the sequence's i-th tile and head (behind its last where there is
+// no such one), whose first unit is `base` units.
 __device__ __forceinline__ AttnStart tree_border_whole(const AttnParams& p, const TreeSeq& s, int b, int64_t base, int i,
                                                        int64_t units) {
     const int cost = s.nblk + p.plan.lead, tile = i / p.Hk;
@@ -323,8 +322,9 @@ __device__ __forceinline__ AttnStart tree_border_whole(const AttnParams& p, cons
     a.begin = start + static_cast<int64_t>(a.head) * cost;
     a.t = s.tile(p, b, tile, start);
     if (tile == s.tiles && a.begin < units) {   // the next sequence's first one
-        a.t = s.tile(p, b, tile - 1, start - static_cast<int64_t>(p.Hk) * cost);
-        tree_next_tile<false>(p, a.t);
+        const TreeSeq next = tree_seq(p, b + 1);
+        a.after = next.tiles == 0;              // far: looked for by a warp
+        a.t = a.after ? s.tile(p, b, tile - 1, start - static_cast<int64_t>(p.Hk) * cost) : next.tile(p, b + 1, 0, start);
     }
     return a;
 }
@@ -438,6 +438,7 @@ __device__ __forceinline__ void tree_share(const AttnParams& p, int cta, const T
                 out.start.begin = a.begin;
                 out.start.head = a.head;
                 out.start.unit = a.unit;
+                out.start.after = a.after;
                 out.start.t = a.t;
             }
             lo = hi;
@@ -445,6 +446,15 @@ __device__ __forceinline__ void tree_share(const AttnParams& p, int cta, const T
         }
     }
     __syncthreads();
+    if (out.start.after != 0) {   // (past 7400 sequences without new tokens: 2200 us by one thread, 20 by a warp)
+        if (w == 0) {
+            AttnTile t = out.start.t;
+            tree_next_tile(p, t);
+            __syncwarp();
+            if (lane == 0) out.start.t = t;
+        }
+        __syncthreads();
+    }
     if (tid == 0) reinterpret_cast<AttnStart*>(p.ws + p.plan.start_off)[cta] = out.start;
 }
 
@@ -514,7 +524,7 @@ struct AttnWalk {
                     head = 0;
                     ++tile;
                     if (at < end) {
-                        if (TREE) tree_next_tile<true>(p, t);
+                        if (TREE) tree_next_tile(p, t);
                         else t = attn_tiles(p)[tile];
                     }
                 }

@@ -248,6 +248,26 @@ def test_sequences_far_apart_among_idle_ones(at, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("first,idle,last", [(598, 7400, 20), (229, 7400, 20), (598, 1, 20), (200, 7900, 1)])
+def test_shares_that_begin_behind_idle_sequences(first, idle, last, dtype):
+    """Short trees, then a run of sequences without new tokens, then more trees.  With 152
+    SMs a share of 598 (bf16) or 229 (float32) of them begins behind the run.  The same
+    with the idle ones taken out."""
+    rng = np.random.default_rng(0)
+    new = np.concatenate([rng.integers(1, 9, first), np.zeros(idle, int), rng.integers(1, 9, last)])
+    context = np.where(new > 0, rng.integers(0, 200, len(new)), 5)
+    c = Trees([(int(n), int(n + m)) for n, m in zip(new, context)], 10, 2, 128, 64, dtype, "tree")
+    r = B.mhc_tree_attn(c.q, c.k, c.v, c.table, c.tree, c.cu, c.kv, max_q=9)
+    here = torch.tensor(np.flatnonzero(new), device=c.q.device)
+    cu = torch.cat([c.cu[:1], c.cu[1:][here]])
+    s = B.mhc_tree_attn(c.q, c.k, c.v, c.table[here], c.tree, cu, c.kv[here], max_q=9)
+    assert torch.equal(r.o, s.o) and torch.equal(r.lse, s.lse)
+    if first < 300:
+        c.check(r)
+    assert B.get_last_device_error() == B.MHC_OK
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("n", [1, 12, 25, 26, 50, 51, 90])
 def test_short_contexts_in_great_number(n, dtype):
     """Tiles far smaller than a CTA's share, whole and with borders moved."""
