@@ -503,9 +503,16 @@ mhc_status mhc_qk_norm_rope_append(mhc_dtype dt, const void* q, int64_t q_stride
  * make more than `high` turns over it keep their frequency, those that make
  * fewer than `low` are slowed down, and the ones between are blended.  Scaling
  * the base is the caller's: base factor^(rot / (rot - 2)).
- * Angles are right to p f_j 2^-51 for every position (frequencies are computed in
- * double and multiplied by positions in 64-bit integers), values to 3 2^-24 times
- * the amplitude.
+ * The blend is linear in a pair's turns.  Models whose blend is linear in the pair's
+ * number instead, or that have a factor of their own for each pair, have other
+ * frequencies (by up to 65 % for base 10000, factor 16, 1 to 32 turns over 8192):
+ * their tables are not made here; the rotations take a table from anywhere.
+ * Frequencies are computed in double and multiplied by positions in 64-bit integers,
+ * so the angle of position p is off by at most
+ *   p max(1, 1 / factor) (2^-49 + 2^-50 high / (high - low))
+ * radians (the second term only where high > 0 and original > 0) for every pair: a
+ * slow pair's angle has fewer right digits than a fast one's.  Values are right to
+ * 3 2^-24 times the amplitude beside that.
  *
  *   base >= 1, factor > 0, original >= 0, low < high, all finite
  *   rot  int             multiple of 16, 16 <= rot <= 256

@@ -10,6 +10,9 @@ amplitude with what the fractions of a turn leave out; frequencies in double
 move the angle by 2^-51 of it.
 """
 
+import math
+from decimal import Decimal, localcontext
+
 import numpy as np
 import pytest
 import torch
@@ -240,6 +243,40 @@ def test_far_positions():
     for first in (0, 1 << 20, (1 << 24) - 5, n - 100):
         ref, angles = A.rope_table(100, 16, base=3.0, factor=1.5, first=first)
         assert np.all(np.abs(f64(got[first:first + 100]) - ref) <= 3 * U + np.tile(angles, 2) * 2.0 ** -51)
+
+
+PI = Decimal("3.14159265358979323846264338327950288419716939937510582097494")
+
+
+def _table_row(p, rot, base, factor=1.0, original=0.0, low=1.0, high=32.0):
+    """Row p in 60 digits."""
+    with localcontext() as digits:
+        digits.prec = 60
+        c, s = [], []
+        for j in range(rot // 2):
+            e = Decimal(base) ** (Decimal(-2 * j) / rot)
+            g = min(Decimal(1), max(Decimal(0), (Decimal(original) * e / (2 * PI) - Decimal(low)) /
+                                    (Decimal(high) - Decimal(low))))
+            a = float(p * e * (g + (1 - g) / Decimal(factor)) % (2 * PI))
+            c.append(math.cos(a))
+            s.append(math.sin(a))
+    return np.array(c + s)
+
+
+@pytest.mark.parametrize("rot,scaling", [
+    (16, dict(base=1e6, factor=16.0, original=8192.0)), (16, dict(base=1e4)), (96, dict(base=1e6, factor=16.0, original=8192.0)),
+    (32, dict(base=5e5, factor=8.0, original=8192.0, low=1.0, high=4.0)), (16, dict(base=1e9, factor=0.25)),
+    (64, dict(base=1e4, factor=40.0, original=4096.0, low=3.0, high=3.5))])
+def test_slow_pairs_at_far_positions(rot, scaling):
+    """The angles' bound as include/mhc.h states it, and 2^-50 for the rows themselves,
+    whose angles below 8 are rounded to double."""
+    _dev()
+    n = (1 << 24) * 16 // rot + 77
+    got = B.mhc_rope_table(n, rot, **scaling)
+    low, high = scaling.get("low", 1.0), scaling.get("high", 32.0)
+    per = max(1.0, 1.0 / scaling.get("factor", 1.0)) * (2.0 ** -49 + 2.0 ** -50 * high / (high - low))
+    for p in (1, 4097, 131071, n // 3, n // 2 + 1, n - 2, n - 1):
+        assert np.all(np.abs(f64(got[p]) - _table_row(p, rot, **scaling)) <= 3 * U + p * per + 2.0 ** -50)
 
 
 def test_scaled_table_serves_the_normalising_rotation():
