@@ -561,7 +561,7 @@ mhc_status mhc_rope_append(mhc_dtype dt, const void* q, int64_t q_stride, const 
  *   o_i = sum_j exp(z_ij) v_j / sum_j exp(z_ij),   lse_i = log sum_j exp(z_ij).
  * A row that sees no key (m < n) gets o = 0 and lse = -inf.  Sums and softmax
  * statistics are float32; on the tensor cores the exponentials of a block are
- * rounded to bf16 for their product with the values (relative 2^-9 each).
+ * rounded to bf16 for their product with the values (by at most 2^-8 of each).
  * There a capped score is right to 2^-20 of a softcap of up to 256, and to a
  * relative 2^-18 of the score with a larger one.
  *
@@ -621,6 +621,9 @@ size_t mhc_paged_attn_workspace_bytes(mhc_dtype dt, int64_t T, int B, int Hq, in
  * last window - max(1, how many these are) tokens of the context.
  * A row that sees no key gets o = 0 and lse = -inf; so does every row of a
  * sequence with m < n, whose drafted tokens are not all cached.
+ * In bf16 on the tensor cores the exponentials are rounded as there: o is off by at
+ * most 2^-8 (sum_j p_j |v_j| + |o|) beside float32 sums, with p_j the probabilities;
+ * lse, and all of float32, is not touched by it.
  *
  *   tree [T, *]          int32            tree_stride words between rows, at
  *                                         least ceil(max_q / 32); bits past a

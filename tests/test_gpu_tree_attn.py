@@ -432,3 +432,22 @@ def test_empty_calls():
     k = torch.zeros(2, 16, 2, 64, dtype=torch.bfloat16, device=dev)
     i = lambda *s: torch.zeros(*s, dtype=torch.int32, device=dev)       # noqa: E731
     assert B.mhc_tree_attn(q, k, k, i(1, 1), i(0, 1), i(2), i(1)).o.shape == (0, 4, 64)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,Hq,Hk,dh", [([(13, 777)], 10, 2, 128), ([(21, 3000), (60, 900), (1, 5000)], 5, 1, 64)])
+def test_nothing_depends_on_what_the_memory_held(lens, Hq, Hk, dh, dtype, monkeypatch):
+    """Workspace and outputs of any contents: the same bits."""
+    c = Trees(lens, Hq, Hk, dh, 64, dtype, "tree")
+    got = []
+    for value in (0, 255, 127):
+        def filled(shape, dtype, device, value=value):
+            t = torch.empty(shape, dtype=dtype, device=device)
+            t.view(-1).view(torch.uint8).fill_(value)
+            return t
+        monkeypatch.setattr(B, "_empty", filled)
+        got.append(c.run())
+    monkeypatch.undo()
+    for r in got[1:]:
+        assert torch.equal(got[0].o, r.o) and torch.equal(got[0].lse, r.lse)
+    c.check(got[0])
