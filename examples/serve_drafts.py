@@ -56,12 +56,13 @@ class DraftServer:
         i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)       # noqa: E731
         s = B.mhc_paged_step(i32(counts), self.lens, self.table, self.held, self.free, self.count, self.page, T,
                              parents=None if parents is None else i32(parents), width=-(-n // 32))
-        plan, lay = None, self.layers[0]
-        if parents is None:
-            plan = B.mhc_paged_attn_plan(s.cu_q, s.kv_lens, torch.bfloat16, T, lay.Hq, lay.Hk, lay.Dh, self.page, n,
-                                         self.max_kv, lay.window)
+        plans, lay = {}, self.layers[0]
+        if parents is None:      # one for all layers with the same window
+            for window in {layer.window for layer in self.layers}:
+                plans[window] = B.mhc_paged_attn_plan(s.cu_q, s.kv_lens, torch.bfloat16, T, lay.Hq, lay.Hk, lay.Dh,
+                                                      self.page, n, self.max_kv, window)
         for layer, k, v in zip(self.layers, self.k, self.v):
-            x = self.layer(layer, x, k, v, s, n, plan)
+            x = self.layer(layer, x, k, v, s, n, plans.get(layer.window))
         if paths is None:
             self.lens = s.kv_lens
         else:

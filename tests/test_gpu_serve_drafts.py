@@ -46,6 +46,19 @@ def test_kept_paths_match_whole_streams(drafts, Hq, Hk, Dh, window, page, most):
         assert float((a.float() - b.float()).abs().max()) <= 8 * 2.0 ** -8 * float(b.float().abs().max())
 
 
+@pytest.mark.parametrize("windows", [(0, 3), (5, 0, 5), (40, 2)])
+def test_layers_of_different_windows(drafts, windows):
+    """Prompts through several layers at once and through each of them alone: the same bits."""
+    layers = [drafts.ServedLayer(D=1024, Hq=8, Hk=2, Dh=64, window=w, max_pos=64, seed=i) for i, w in enumerate(windows)]
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(33, 4, 1024, generator=g, device="cuda").bfloat16()
+    y = drafts.DraftServer(layers, 2, 64, 16).step(x, [24, 9])
+    for layer in layers:
+        x = drafts.DraftServer([layer], 2, 64, 16).step(x, [24, 9])
+    assert torch.equal(x, y)
+    assert B.get_last_device_error() == B.MHC_OK
+
+
 def test_keys_of_kept_paths_are_those_of_whole_streams(drafts):
     """The caches, token by token: in one layer keys and values depend on the token
     and its position alone.  The projections of other batch sizes may round
