@@ -52,6 +52,11 @@ class DraftServer:
         """x [T, 4, D]: the streams of counts[b] new tokens of each sequence, nodes
         of the trees `parents` if given.  All of them are kept, or `paths[b]` of each.
         Returns the states after the last layer."""
+        if parents is not None:
+            deepest = max(depths(parents, counts), default=0)
+            for layer in self.layers:    # the masks have all ancestors, also those that a window hides
+                if 0 < layer.window < deepest:
+                    raise ValueError(f"a path of {deepest} drafted tokens is longer than a layer's window of {layer.window}")
         dev, T, n = x.device, x.shape[0], max(counts)
         i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)       # noqa: E731
         s = B.mhc_paged_step(i32(counts), self.lens, self.table, self.held, self.free, self.count, self.page, T,
@@ -83,6 +88,16 @@ class DraftServer:
             o = B.mhc_tree_attn(q, k_cache, v_cache, self.table, s.tree, s.cu_q, s.kv_lens, max_q=most,
                                 max_kv=self.max_kv, window=layer.window).o
         return B.mhc_post(x, o.view(T, h) @ layer.w_out, f.H_post, f.H_res)
+
+
+def depths(parents, counts):
+    """How many nodes the path of each node has, of trees laid end to end."""
+    out = []
+    for n in counts:
+        first = len(out)
+        for p in parents[first:first + n]:
+            out.append(1 if p < 0 else out[first + p] + 1)
+    return out
 
 
 def draft(rng, left: int, most: int):

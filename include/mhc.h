@@ -618,7 +618,10 @@ size_t mhc_paged_attn_workspace_bytes(mhc_dtype dt, int64_t T, int B, int Hq, in
  * sees: bit i % 32 of word i / 32 for the i-th one (itself and its ancestors,
  * usually; any mask is taken).  Node t sees the m - n cached tokens before the
  * new ones (its context) and those.  With a window, it sees its nodes and the
- * last window - max(1, how many these are) tokens of the context.
+ * last window - max(1, how many these are) tokens of the context: the window of
+ * mhc_paged_attn where a node has at most `window` bits.  A node's bits count
+ * whatever the window is: of a path that is longer, the mask has to leave out the
+ * ancestors that lie `window` or more back (those of mhc_paged_step have all of them).
  * A row that sees no key gets o = 0 and lse = -inf; so does every row of a
  * sequence with m < n, whose drafted tokens are not all cached.
  * In bf16 on the tensor cores the exponentials are rounded as there: o is off by at
@@ -670,7 +673,8 @@ mhc_status mhc_tree_attn(mhc_dtype dt, const void* q, int64_t q_stride, const vo
  * Positions are the places in the sequence, or with trees lens[b] + the number of
  * the node's ancestors.  Parent parents[t] of row t is a number among its
  * sequence's new tokens, below its own, or -1 (it follows the context); row t of
- * `tree` gets the bits of the node and its ancestors, as mhc_tree_attn takes them.
+ * `tree` gets the bits of the node and all its ancestors, as mhc_tree_attn takes them
+ * (layers with a window shorter than a path need their early ones taken out).
  *
  *   new_lens, lens [B]   int32
  *   page_table [B, *]    int32   in/out   table_width entries a row, table_stride apart

@@ -606,7 +606,9 @@ def mhc_tree_attn(q, k_cache, v_cache, page_table, tree, cu_q, kv_lens, max_q: i
     """Attention of trees of drafted tokens: as mhc_paged_attn, but of the new
     tokens of its sequence row t sees those whose bits tree[t] has (int32 words;
     bit i % 32 of word i // 32: the i-th new token), and all cached tokens before
-    them.  ``window`` counts a row's nodes and the context behind them.  There is no
+    them.  ``window`` counts a row's nodes and the context behind them; all bits of a
+    row are seen whatever it is, so a mask for paths longer than the window leaves out
+    the ancestors that it hides (mhc_paged_step's has all of them).  There is no
     plan: each call splits the batch by itself.  ``max_q`` bounds the new tokens of a
     sequence (default: the bits of a row of ``tree``, at most 1024; a bound near
     the most that there are makes smaller tiles).  Returns o and lse [T, Hq]."""

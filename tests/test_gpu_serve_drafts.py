@@ -59,6 +59,25 @@ def test_layers_of_different_windows(drafts, windows):
     assert B.get_last_device_error() == B.MHC_OK
 
 
+def test_paths_longer_than_a_window_are_refused(drafts):
+    """The step's masks have all ancestors of a node, also those that the window hides;
+    a path as long as the window is served."""
+    assert drafts.depths([-1, 0, 1, -1, -1, 0, 0, 2], [3, 1, 4]) == [1, 2, 3, 1, 1, 2, 2, 3]
+    layers = [drafts.ServedLayer(D=1024, Hq=8, Hk=2, Dh=64, window=w, max_pos=64) for w in (0, 3)]
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn(24, 4, 1024, generator=g, device="cuda").bfloat16()
+    whole = drafts.DraftServer(layers, 1, 64, 16).step(x, [24])
+    server = drafts.DraftServer(layers, 1, 64, 16)
+    server.step(x[:20], [20])
+    lens = server.lens.clone()
+    with pytest.raises(ValueError):
+        server.step(x[20:], [4], [-1, 0, 1, 2], [[0, 1, 2, 3]])
+    assert torch.equal(server.lens, lens)
+    y = server.step(x[20:23], [3], [-1, 0, 1], [[0, 1, 2]])
+    assert B.get_last_device_error() == B.MHC_OK
+    assert float((y.float() - whole[20:23].float()).abs().max()) <= 8 * 2.0 ** -8 * float(whole.float().abs().max())
+
+
 def test_keys_of_kept_paths_are_those_of_whole_streams(drafts):
     """The caches, token by token: in one layer keys and values depend on the token
     and its position alone.  The projections of other batch sizes may round

@@ -180,6 +180,19 @@ def test_chains_are_causal(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("window", [1, 7, 20, 45, 130])
+def test_chains_with_a_window_are_causal(window, dtype):
+    """A chain longer than the window, with the ancestors that it hides taken out of the
+    mask: the same keys as a chunk's."""
+    c = Trees([(20, 300), (1, 129), (70, 70), (90, 400)], 10, 2, 64, 16, dtype, "chain", window=window)
+    c.masks = [m & np.triu(np.ones_like(m), 1 - window) for m in c.masks]
+    c.tree = pack(c.masks, c.tree.shape[1], False).to(c.q.device)
+    s = B.mhc_paged_attn(c.q, c.k, c.v, c.table, c.cu, c.kv, max_q=c.most, window=window)
+    c.check(c.run())
+    c.check(s)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_long_contexts_are_split_and_repeat(dtype):
     c = Trees([(21, 9000), (40, 4097)], 5, 1, 128, 64, dtype, "tree")
     r = c.run()
