@@ -722,6 +722,7 @@ mhc_status mhc_paged_step(const int32_t* new_lens, const int32_t* lens, int B, i
  *   cu_q [B+1], kv_lens [B], keep [B] int32
  *   path [B, *]          int32            path_stride between rows, >= max_keep
  *   lens [B]             int32   out      or null; none of the inputs' memory
+ * No sequences, no layers or max_keep = 0: a no-op, lens stays as it is too.
  * MHC_ERR_RANGE: a sequence whose numbers do not fit (a path that does not rise
  * or leaves the drafted tokens, keep past max_keep or n, m outside n .. max_kv) is
  * left as it is; a row on a page outside the cache is not moved.
