@@ -170,7 +170,7 @@ cudaError_t launch_paged_attn_tc(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_tree_attn_tc(const AttnParams& p, cudaStream_t s);
 
 // The tables of a step's new tokens (paged_attn_step.cu).
-constexpr int STEP_SEQUENCES = 8192;   // at most: three numbers of each are in shared memory
+constexpr int STEP_SEQUENCES = 8192;   // at most: five numbers of each are in shared memory
 struct StepParams {
     const int32_t *new_lens, *lens, *parents;   // parents may be null (no trees)
     int32_t *table, *held, *free_pages, *free_count;

@@ -5,9 +5,10 @@
 // For sequence b with context c = m - n and accepted nodes path[0] < path[1] <
 // ...: token c + path[d] -> place c + d.  path[d] >= d, so a row moves to a lower
 // place or stays, and a row that is read for d is never the goal of an earlier
-// one.  A block (one sequence in one cache) therefore takes as many 16-byte
-// pieces as its threads hold in registers, in the order of d: all are read, then
-// all are written, and the next ones need no more than that.
+// one.  A block (one sequence in one cache, or in up to four, one after the other)
+// therefore takes as many 16-byte pieces as its threads hold in registers, in the
+// order of d: all are read, then all are written, and the next ones need no more
+// than that.
 // Bound by memory behind two dependent reads (the path, the page number): 7 of 32
 // tokens of 48 sequences in 16 layers, 44 MB read and written, take 10.9 us (4.1
 // TB/s), one sequence in one layer 3.7.  Rows looked up together in shared memory:
@@ -30,7 +31,7 @@ namespace keep {
 
 constexpr int THREADS = 128, HELD = 8;   // 16-byte pieces of a thread: 16 KB of a block in flight
 constexpr int ROWS = THREADS;            // of a path, looked up together
-constexpr int BLOCKS = 8192;             // from these on a block has more than one cache
+constexpr int BLOCKS = 8192;             // a block has two caches from twice as many sequences and caches on, ...
 
 __global__ void __launch_bounds__(THREADS)
 keep_kernel(const __grid_constant__ KeepParams p) {
@@ -111,7 +112,7 @@ keep_kernel(const __grid_constant__ KeepParams p) {
 
 // A block for each sequence and cache; where those are many, most of them may find
 // only that nothing moves, at 0.5 ns each, and a block has up to 4 caches one after the
-// other. 48 sequences that keep rows among 512, 2048 and 8192, in 16 layers: 14.5, 22
+// other: two from 16384 sequences and caches on, 4 from 32768. 48 sequences that keep rows among 512, 2048 and 8192, in 16 layers: 14.5, 22
 // and 45 us, with a block each 16, 38 and 136 (up to 8 caches: 14.5, 28 and 39).  256 that
 // all do in 32 layers: 82, with a block each 86.
 cudaError_t launch_cache_keep(const KeepParams& p, int B, cudaStream_t s) {

@@ -115,7 +115,7 @@ constexpr int JOIN_PAIR = 4, JOIN_64 = 12, JOIN_128 = 7;
 // What a block weighs in a CTA's share, of a tile for both lanes and of one for one lane:
 // the second is bound by memory, the first by the products too. 4 sequences of 64 and
 // 65536 (tiles of 250 and 70 rows) take 333 us, 363, 343 and 338 with 1 to 1, 5 to 4
-// and 3 to 2; 32 of 16 to 32 and up to 8192 96, 98, 96 and 99.
+// and 3 to 2 (in short runs); 32 of 16 to 32 and up to 8192 96, 98, 96 and 99.
 constexpr int FULL_BLOCK = 4, PART_BLOCK = 3;
 static_assert(2 * PART_BLOCK >= FULL_BLOCK, "the least share has a block");
 constexpr int PIECES = 4;                    // pieces handed out and not done with
@@ -924,7 +924,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
         } else if (work && warp == BLANK_WARP) {
             // ---------------------------------------------------- blanks ---
             // Value rows that no row of the tile sees become zeros before
-            // their product.  Only a tile's first and last block can have some.
+            // their product.  Of causal rows only a tile's first and last block can have
+            // some, of trees the first one and those with drafted tokens.
             uint32_t n = 0, par_a = 0;   // ring stages used by earlier pieces
             while (ok) {
                 const AttnPiece pc = pieces.get(ok);

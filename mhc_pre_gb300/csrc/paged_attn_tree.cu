@@ -19,8 +19,9 @@
 //
 // Figures, 40 + 8 heads of 128 in bf16 on one GB300: 32 sequences of 16 to 32 drafted
 // tokens on up to 8192 cached ones 96 us, 25 on 8192 each 187 us (5.8 TB/s), 4 of 64 on
-// 65536 333 us (their 320 rows of a key head are two tiles, which read the context
-// twice, at 6.4 TB/s), one of 13 on 777 16 us.  float32, 20 + 4 heads, 8 of 11 on 3200:
+// 65536 330 to 338 us (their 320 rows of a key head are two tiles, which read the context
+// twice, at 6.4 TB/s; 350 to 372 after thousands of calls in a row, when the power cap has
+// brought the SM clock down to 1.7 GHz), one of 13 on 777 16 us.  float32, 20 + 4 heads, 8 of 11 on 3200:
 // 115 us.
 #include "paged_attn_cc.cuh"
 

@@ -7,7 +7,9 @@
 // qk_norm_rope_fwd.cuh with NORM off.  Bound by memory: 32768 tokens of 40 + 8 heads
 // of 128 in bf16 take 130 us (6.2 TB/s, 0.93 of the measured copy rate; 144 in those
 // kernels, which store 8 bytes a lane), with neighbouring pairs 133, into the cache
-// 164; 64 tokens 3.2 us, a chain of three reads.  A table of 131072 x 128 takes 11.8 us
+// 164; in float32, whose rows leave room for 4 warps' stages only and so go through
+// qk_norm_rope_fwd.cuh, 252 and 302 (0.95 and 0.93).  64 tokens 3.2 us: a position, then
+// its angles, and the launch.  A table of 131072 x 128 takes 11.8 us
 // (5.7 TB/s).
 #include <math.h>
 

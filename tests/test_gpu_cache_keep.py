@@ -104,6 +104,16 @@ def test_many_sequences_of_which_few_keep_something(sequences, layers):
     c.check()
 
 
+@pytest.mark.parametrize("sequences,layers", [(8191, 1), (8192, 1), (8193, 1), (4096, 2), (8191, 2), (8192, 2)])
+def test_either_side_of_a_second_and_a_fourth_cache_of_a_block(sequences, layers):
+    lens = [(0, 2)] * sequences
+    for b in range(0, sequences, 511):
+        lens[b] = (20, 30 + b % 40)
+    c = Case(lens, 2, 8, 16, "bf16", layers=layers)
+    c.run()
+    c.check()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_caches_with_the_heads_outside(dtype):
     c = Case(LENS["batch"], 4, 64, 16, dtype, layers=2, order="head")
