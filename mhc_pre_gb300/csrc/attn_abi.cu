@@ -85,12 +85,6 @@ mhc_status check_attn(mhc_dtype dt, int64_t T, int B, int Hq, int Hk, int Dh, in
     return MHC_OK;
 }
 
-// Whether runs of 32-bit numbers have any in common.
-bool overlap(const void* a, int64_t a_count, const void* b, int64_t b_count) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + static_cast<uintptr_t>(b_count) * 4 && y < x + static_cast<uintptr_t>(a_count) * 4;
-}
-
 // 32-bit numbers in memory: rows of `width`, `stride` apart.
 struct Numbers {
     const void* p;
@@ -621,10 +615,11 @@ mhc_status mhc_cache_keep(mhc_dtype dt, void* const* k_caches, int64_t k_page_st
     for (const void* n : numbers)
         if ((st = check_plain(n, 4)) != MHC_OK) return st;
     if (lens != nullptr && (st = check_plain(lens, 4)) != MHC_OK) return st;
-    const int64_t pages = (max_kv + page_size - 1) / page_size, last = B - 1;   // of a row, last row
-    const int64_t counts[] = {last * table_stride + pages, int64_t(B) + 1, B, last * path_stride + max_keep, B};
-    for (int i = 0; i < 5; ++i)   // blocks of other caches read them while `lens` is written
-        if (lens != nullptr && overlap(lens, B, numbers[i], counts[i])) return MHC_ERR_INVALID_ARG;
+    const Numbers read[] = {{page_table, B, (max_kv + page_size - 1) / page_size, table_stride},
+                            {cu_q, 1, int64_t(B) + 1, 0}, {kv_lens, 1, B, 0}, {path, B, max_keep, path_stride},
+                            {keep, 1, B, 0}};
+    for (const Numbers& r : read)   // blocks of other caches read them while `lens` is written
+        if (meet(r, {lens, 1, B, 0})) return MHC_ERR_INVALID_ARG;
     const int64_t e = dt == MHC_BF16 ? 2 : 4;
     mhc::KeepParams p = {};
     p.table = page_table;

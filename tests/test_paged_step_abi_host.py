@@ -101,6 +101,16 @@ def test_keep_refuses_lengths_that_it_reads(L):           # noqa: F811
     assert _keep(L, **far, lens=far["path"] + 4 * 5) == INV
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are not memory: nothing may be launched")
+def test_keep_takes_lengths_beside_and_between_what_it_reads(L):      # noqa: F811
+    """In the gaps of a table's or a path's rows, and behind their last entries."""
+    far = {k: A + 4096 * i for i, k in enumerate(("table", "cu", "kv", "path", "keep"), 1)}
+    for lens in (far["table"] + 16, far["table"] + 48, far["path"] + 12, far["cu"] + 12, far["kv"] - 8, far["keep"] + 8):
+        assert _keep(L, **far, ts=8, ps=6, lens=lens) == B.MHC_ERR_CUDA, lens
+    for lens in (far["table"] + 12, far["table"] + 28, far["table"] + 44, far["path"] + 20, far["path"] + 32):
+        assert _keep(L, **far, ts=8, ps=6, lens=lens) == INV, lens
+
+
 def test_keep_of_nothing(L):                              # noqa: F811
     for none in (dict(B=0, cu=None), dict(layers=0, k=None), dict(most=0, path=None)):
         assert _keep(L, **none) == OK
